@@ -9,7 +9,9 @@ is missing, every call raises.
 
 Entry points carry the C names (``kda_workspace_bytes``, ``kda_fwd``,
 ``kda_bwd``, ``gdn_workspace_bytes``, ``gdn_fwd``, ``gdn_bwd``,
-``gdr_status_string``).  Outputs and workspaces are allocated with torch when
+``gdr_status_string``); the operators around the recurrence (``sconv_*``,
+``ssm_*``, ``kda_step``, ``gdn_step``, ``norm_*``) live in ``ops.py`` and are
+reached from here too.  Outputs and workspaces are allocated with torch when
 the caller does not pass them.
 """
 from __future__ import annotations
@@ -52,6 +54,18 @@ EXPORTED = (
     "gdr_set_slice_chunks",
     "gdr_walk_slices",
     "gdr_segment_plan",
+    "sconv_fwd",
+    "sconv_workspace_bytes",
+    "sconv_bwd",
+    "sconv_step",
+    "ssm_workspace_bytes",
+    "ssm_fwd",
+    "ssm_step",
+    "kda_step",
+    "gdn_step",
+    "norm_fwd",
+    "norm_workspace_bytes",
+    "norm_bwd",
 )
 
 _lock = threading.Lock()
@@ -90,6 +104,23 @@ _SIGS = {
                  SZ, P], ctypes.c_int),
     "gdn_bwd": ([P, P, P, P, P, P, PI32, I32, I64, I32, I32, F32, ctypes.c_int, P, P, P, P, SZ, P, P, P, P, P, P,
                  P, SZ, P], ctypes.c_int),
+    "sconv_workspace_bytes": ([I64, I32, I32, PSZ], ctypes.c_int),
+    "sconv_fwd": ([I32, P, I64, P, P, I32, P, P, I32, I64, I32, I32, I32, P, P, P, P], ctypes.c_int),
+    "sconv_bwd": ([I32, P, I64, P, P, I32, P, P, I32, I64, I32, I32, I32, P, P, I64, P, P, P, P, P, P, SZ, P],
+                  ctypes.c_int),
+    "sconv_step": ([I32, P, I64, P, P, I32, P, P, I32, I32, I32, I32, I32, P, P], ctypes.c_int),
+    "ssm_workspace_bytes": ([I64, I32, I32, I32, I32, I32, P, PSZ], ctypes.c_int),
+    "ssm_fwd": ([P, I64, P, I32, I64, P, P, I64, P, I64, P, P, I32, P, P, I32, I64, I32, I32, I32, I32, P, P, P, P, SZ,
+                 P], ctypes.c_int),
+    "ssm_step": ([P, I64, P, I32, I64, P, P, I64, P, I64, P, P, I32, P, P, I32, I32, I32, I32, I32, I32, P, P],
+                 ctypes.c_int),
+    "kda_step": ([P, P, P, P, P, P, P, I32, I32, I32, F32, I32, P, P], ctypes.c_int),
+    "gdn_step": ([P, P, P, P, P, P, P, I32, I32, I32, I32, F32, I32, P, P], ctypes.c_int),
+    "norm_workspace_bytes": ([I32, PSZ], ctypes.c_int),
+    "norm_fwd": ([I32, I64, I32, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, F32, P, P, I32, F32, P, P, P],
+                 ctypes.c_int),
+    "norm_bwd": ([I32, I64, I32, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, F32, P, P, I32, F32, P, I64, I64, P,
+                  I64, I64, P, P, P, P, P, P, SZ, P], ctypes.c_int),
 }
 
 
@@ -388,3 +419,18 @@ def gdr_selftest_wait(limit_ns: int, stream=None):
     """Enqueue a kernel whose bounded wait on a barrier that nothing completes
     runs out after limit_ns; gdr_check_device() then raises GDR_DEVICE_TIMEOUT."""
     _check(load().gdr_selftest_wait(int(limit_ns), _stream(stream)), "gdr_selftest_wait")
+
+
+# The operators around the recurrence (torch is needed from here on; the host-side
+# functions above work without it).
+_OPS = ("sconv_workspace_bytes", "sconv_fwd", "sconv_bwd", "sconv_step", "ssm_workspace_bytes", "ssm_fwd", "ssm_step",
+        "kda_step", "gdn_step", "norm_workspace_bytes", "norm_fwd", "norm_bwd")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -17,6 +17,7 @@
 #include "../../include/gdr.h"
 #include "gdr_common.cuh"
 #include "gdr_kernels.h"
+#include "gdr_runtime.h"
 #include "gdr_tc.cuh"
 
 namespace gdr {
@@ -204,7 +205,6 @@ constexpr int kNoSplit = 1 << 30;
 constexpr double kWalkStepNs = 7700.0, kChunkHeadNs = 50000.0;
 std::atomic<int> g_seg_chunks{0};  // gdr_set_segment_chunks: 0 = choose
 
-int sm_count();
 int slice_chunks();
 
 int segment_chunks(int32_t N, const int32_t* cu, int32_t HV) {
@@ -335,6 +335,8 @@ Layout make_layout(int64_t T, int64_t NC, int32_t N, int32_t Hqk, int32_t HV, bo
   return L;
 }
 
+}  // namespace
+
 // Validates cu_seqlens_host and counts chunks.
 gdr_status plan_host(int64_t T, int32_t N, const int32_t* cu, int64_t* NC) {
   if (N < 0 || T < 0) return GDR_INVALID_ARG;
@@ -349,6 +351,8 @@ gdr_status plan_host(int64_t T, int32_t N, const int32_t* cu, int64_t* NC) {
   *NC = nc;
   return GDR_OK;
 }
+
+namespace {
 
 uint64_t hash_cu(const int32_t* cu, int32_t N) {
   uint64_t h = 1469598103934665603ull;
@@ -409,6 +413,8 @@ SavedHeader header_of(const Stamp& s) {
   return h;
 }
 
+}  // namespace
+
 gdr_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GDR_CUDA_ERROR;
@@ -425,6 +431,8 @@ int sm_count() {
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   return n > 0 ? n : 152;
 }
+
+namespace {
 
 bool aligned(const void* p) { return ((uintptr_t)p % kAlign) == 0; }
 // Tensors the kernels copy in 16-byte pieces (q, k, v, g, dout) or store in
@@ -496,6 +504,8 @@ static __device__ int g_device_error;
 std::mutex g_err_mu;
 int* g_err_ptr[64] = {};
 
+}  // namespace
+
 int* device_error_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
@@ -508,6 +518,7 @@ int* device_error_ptr() {
   return g_err_ptr[dev];
 }
 
+namespace {
 
 // ---------------------------------------------------------------------------
 // Opt-in per-kernel timing for benchmarks: while enabled, every launch is
@@ -537,25 +548,25 @@ std::atomic<uint64_t> g_launches{0};
 // document groups one after another): per-kernel timing without overlap.
 std::atomic<bool> g_serial{false};
 
-struct ProfScope {
-  cudaStream_t st;
-  bool on;
-  ProfScope(const char* name, cudaStream_t s, double units = 0) : st(s), on(false) {
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on) return;
-    ProfRec r{name, nullptr, nullptr, units};
-    if (cudaEventCreate(&r.a) != cudaSuccess || cudaEventCreate(&r.b) != cudaSuccess) return;
-    cudaEventRecord(r.a, st);
-    g_prof.push_back(r);
-    on = true;
-  }
-  ~ProfScope() {
-    if (!on) return;
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    cudaEventRecord(g_prof.back().b, st);
-  }
-};
+}  // namespace
+
+ProfScope::ProfScope(const char* name, cudaStream_t s, double units) : st(s), on(false) {
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  if (!g_prof_on) return;
+  ProfRec r{name, nullptr, nullptr, units};
+  if (cudaEventCreate(&r.a) != cudaSuccess || cudaEventCreate(&r.b) != cudaSuccess) return;
+  cudaEventRecord(r.a, st);
+  g_prof.push_back(r);
+  on = true;
+}
+ProfScope::~ProfScope() {
+  if (!on) return;
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  cudaEventRecord(g_prof.back().b, st);
+}
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Streams the backward's document groups run on (per device, created once,

@@ -1,0 +1,517 @@
+// gdr_sconv.cu -- the short causal depthwise convolution in front of the
+// recurrences, over packed documents:
+//   z[t][c] = bias[c] + sum_{j<W} w[c][j] xx[t - (W-1) + j][c],  out = z or silu(z)
+// where xx is x inside the document and, before its first token, the W - 1
+// rows of the document's start state (or zero).  Backward:
+//   dz = dout act'(z),  dxx[t] = sum_j w[c][j] dz[t + (W-1) - j]  (same document),
+//   dw[c][j] = sum_t dz[t] xx[t - (W-1) + j],  dbias = sum_t dz[t].
+#include "gdr_ops.cuh"
+#include "gdr_runtime.h"
+
+namespace gdr {
+namespace {
+
+struct ConvArgs {
+  const void *x, *weight, *bias;
+  int wf32;             // weight and bias in FP32 (else in the type of x)
+  int64_t ldx;          // row stride of x (elements)
+  const int* cu;
+  int N, T, C;
+  int silu;
+  const void* s0;       // [N][W-1][C] or null
+  void *out, *st;       // [T][C]; [N][W-1][C] or null
+  int tile;             // tokens per tile
+  int cblocks;          // blocks along the channels; block b works on tile b / cblocks
+};
+
+// One thread owns V adjacent channels and walks the tokens of one tile with
+// the last W - 1 inputs in registers, so each input is read once (and W - 1
+// rows again at a tile's start).  Bound by HBM: 2 reads or writes an element.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(128) k_sconv_fwd(ConvArgs a) {
+  constexpr int K = W - 1;
+  const int c = ((int)(blockIdx.x % a.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / a.cblocks;
+  if (c >= a.C) return;
+  const T* x = static_cast<const T*>(a.x) + c;
+  const T* s0 = a.s0 ? static_cast<const T*>(a.s0) + c : nullptr;
+  T* out = static_cast<T*>(a.out) + c;
+  T* st = a.st ? static_cast<T*>(a.st) + c : nullptr;
+  float w[W][V], b[V], win[K][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    b[v] = a.bias ? load_param<T>(a.bias, a.wf32, c + v) : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][v] = load_param<T>(a.weight, a.wf32, (int64_t)(c + v) * W + j);
+  }
+  const int t0 = tile_id * a.tile, t1 = min(a.T, t0 + a.tile);
+  auto start_window = [&](int d) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (s0) {
+        vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + k) * a.C), win[k]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[k][v] = 0.f;
+      }
+    }
+  };
+  auto end_state = [&](int d) {
+    if (!st) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) vstore<T, V>(st + ((int64_t)d * K + k) * a.C, win[k]);
+  };
+  // The document the tile starts in; the empty documents at a position belong
+  // to the tile that ends the token before them (position 0: to the first).
+  int d = 0, t = t0;
+  if (t0 == 0) {
+    while (d < a.N && a.cu[d + 1] == 0) {
+      start_window(d);
+      end_state(d);
+      ++d;
+    }
+  } else {
+    d = doc_of(a.cu, a.N, t0);
+  }
+  while (t < t1) {
+    const int ds = a.cu[d], de = a.cu[d + 1], e = min(de, t1);
+    if (t == ds) {
+      start_window(d);
+    } else {  // mid-document: the rows before the tile, the first ones from the start state
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int p = t - K + k;
+        if (p >= ds) {
+          vunpack<T, V>(vload<T, V>(x + (int64_t)p * a.ldx), win[k]);
+        } else if (s0) {
+          vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + (p - ds + K)) * a.C), win[k]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) win[k][v] = 0.f;
+        }
+      }
+    }
+    auto token = [&](const Vec<T, V>& raw) {
+      float xv[V], y[V];
+      vunpack<T, V>(raw, xv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float z = b[v];
+#pragma unroll
+        for (int k = 0; k < K; ++k) z = fmaf(w[k][v], win[k][v], z);
+        z = fmaf(w[K][v], xv[v], z);
+        y[v] = a.silu ? silu_f(z) : z;
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) win[k][v] = win[k + 1][v];
+        win[K - 1][v] = xv[v];
+      }
+      vstore<T, V>(out + (int64_t)t * a.C, y);
+    };
+    constexpr int U = 8;  // rows in flight
+    while (t + U <= e) {
+      Vec<T, V> raw[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) raw[i] = vload<T, V>(x + (int64_t)(t + i) * a.ldx);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        token(raw[i]);
+        ++t;
+      }
+    }
+    for (; t < e; ++t) token(vload<T, V>(x + (int64_t)t * a.ldx));
+    if (t == de) {
+      end_state(d);
+      ++d;
+      while (d < a.N && a.cu[d + 1] == de) {
+        start_window(d);
+        end_state(d);
+        ++d;
+      }
+    }
+  }
+}
+
+struct ConvBwdArgs {
+  ConvArgs f;
+  const void* dout;
+  int64_t ldo;
+  const void* dst;  // [N][W-1][C] or null
+  void *dx, *ds0;   // [T][C]; [N][W-1][C] or null
+  float* part;      // [tiles][W + 1][C]: each tile's dw rows and dbias
+};
+
+// One thread owns V channels of one tile and walks it in token order: dz of
+// token t completes dxx of row t - (W-1), whose partial sums are kept in W - 1
+// registers a channel; dw and dbias accumulate in registers and leave as one
+// partial row per tile.  The tile's last rows need dz of the W - 1 tokens after
+// it, which are recomputed.  Bound by HBM: x and dout read, dx written.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(128) k_sconv_bwd(ConvBwdArgs a) {
+  constexpr int K = W - 1;
+  const ConvArgs& f = a.f;
+  const int c = ((int)(blockIdx.x % f.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / f.cblocks;
+  if (c >= f.C) return;
+  const T* x = static_cast<const T*>(f.x) + c;
+  const T* dout = static_cast<const T*>(a.dout) + c;
+  const T* s0 = f.s0 ? static_cast<const T*>(f.s0) + c : nullptr;
+  const T* dst = a.dst ? static_cast<const T*>(a.dst) + c : nullptr;
+  T* dx = static_cast<T*>(a.dx) + c;
+  T* ds0 = a.ds0 ? static_cast<T*>(a.ds0) + c : nullptr;
+  float w[W][V], b[V], win[K][V], acc[K][V], dw[W][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    b[v] = f.bias ? load_param<T>(f.bias, f.wf32, c + v) : 0.f;
+    db[v] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      w[j][v] = load_param<T>(f.weight, f.wf32, (int64_t)(c + v) * W + j);
+      dw[j][v] = 0.f;
+    }
+  }
+  const int t0 = tile_id * f.tile, t1 = min(f.T, t0 + f.tile);
+  // Row K - 1 - (number of rows after it) of an empty document's start state
+  // is its end state.
+  auto empty_doc = [&](int d) {
+    if (!ds0) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float g[V];
+      if (dst) {
+        vunpack<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = 0.f;
+      }
+      vstore<T, V>(ds0 + ((int64_t)d * K + k) * f.C, g);
+    }
+  };
+  int d = 0, t = t0;
+  if (t0 == 0) {
+    while (d < f.N && f.cu[d + 1] == 0) empty_doc(d++);
+  } else {
+    d = doc_of(f.cu, f.N, t0);
+  }
+  while (t < t1) {
+    const int ds = f.cu[d], de = f.cu[d + 1];
+    const bool fresh = t == ds;  // this tile owns the document's start-state rows
+    const int e = min(de, t1);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int p = t - K + k;
+      if (p >= ds) {
+        vunpack<T, V>(vload<T, V>(x + (int64_t)p * f.ldx), win[k]);
+      } else if (s0) {
+        vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + (p - ds + K)) * f.C), win[k]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[k][v] = 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
+    }
+    const int own0 = fresh ? ds - K : t;  // rows [own0, t1) of this document are written here
+    // dxx of row p is complete.
+    auto emit = [&](int p, const float (&g)[V]) {
+      if (p < own0 || p >= t1) return;
+      if (p >= ds) {
+        vstore<T, V>(dx + (int64_t)p * f.C, g);
+      } else if (ds0) {
+        vstore<T, V>(ds0 + ((int64_t)d * K + (p - ds + K)) * f.C, g);
+      }
+    };
+    auto token = [&](int tt, const Vec<T, V>& rx, const Vec<T, V>& rg, bool mine) {
+      float xv[V], g[V], done[V];
+      vunpack<T, V>(rx, xv);
+      vunpack<T, V>(rg, g);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float z = b[v];
+#pragma unroll
+        for (int k = 0; k < K; ++k) z = fmaf(w[k][v], win[k][v], z);
+        z = fmaf(w[K][v], xv[v], z);
+        float dz = g[v];
+        if (f.silu) {
+          const float s = sigmoid_f(z);
+          dz *= fmaf(silu_f(z), 1.f - s, s);
+        }
+        if (mine) {
+          db[v] += dz;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dw[k][v] = fmaf(dz, win[k][v], dw[k][v]);
+          dw[K][v] = fmaf(dz, xv[v], dw[K][v]);
+        }
+        // acc[k]: row tt - K + k
+        done[v] = fmaf(w[0][v], dz, acc[0][v]);
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) acc[k][v] = fmaf(w[k + 1][v], dz, acc[k + 1][v]);
+        acc[K - 1][v] = w[K][v] * dz;
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) win[k][v] = win[k + 1][v];
+        win[K - 1][v] = xv[v];
+      }
+      emit(tt - K, done);
+    };
+    constexpr int U = 4;  // rows in flight
+    while (t + U <= e) {
+      Vec<T, V> rx[U], rg[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        rx[i] = vload<T, V>(x + (int64_t)(t + i) * f.ldx);
+        rg[i] = vload<T, V>(dout + (int64_t)(t + i) * a.ldo);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        token(t, rx[i], rg[i], true);
+        ++t;
+      }
+    }
+    for (; t < e; ++t)
+      token(t, vload<T, V>(x + (int64_t)t * f.ldx), vload<T, V>(dout + (int64_t)t * a.ldo), true);
+    // The tokens after the tile that the tile's last rows feed.
+    int tt = e;
+    for (; tt < min(de, e + K); ++tt)
+      token(tt, vload<T, V>(x + (int64_t)tt * f.ldx), vload<T, V>(dout + (int64_t)tt * a.ldo), false);
+    if (tt == de) {  // the document's last rows: the end state's gradient joins
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (dst) {
+          float g[V];
+          vunpack<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[k][v] += g[v];
+        }
+        emit(de - K + k, acc[k]);
+      }
+    }
+    if (e == de) {
+      ++d;
+      while (d < f.N && f.cu[d + 1] == de) empty_doc(d++);
+    }
+  }
+  float* part = a.part + (int64_t)tile_id * (W + 1) * f.C + c;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[(int64_t)j * f.C + v] = dw[j][v];
+    part[(int64_t)W * f.C + v] = db[v];
+  }
+}
+
+// dw[c][j] and dbias[c]: the tiles' partial rows summed in a fixed order.
+__global__ void __launch_bounds__(256) k_sconv_wgrad(const float* __restrict__ part, int tiles, int C, int W,
+                                                     float* dw, float* db) {
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
+  float sum = 0.f;
+  if (c < C)
+    for (int i = row; i < tiles; i += 8) sum += part[((int64_t)i * (W + 1) + j) * C + c];
+  s[row][lane] = sum;
+  __syncthreads();
+  if (row == 0 && c < C) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += s[i][lane];
+    if (j < W) dw[(int64_t)c * W + j] = sum;
+    else if (db) db[c] = sum;
+  }
+}
+
+struct ConvStepArgs {
+  const void *x, *weight, *bias;
+  int wf32;
+  int64_t ldx;
+  void* state;        // [S][W-1][C]
+  const int* slots;   // [B] or null
+  int B, S, C;
+  int silu;
+  void* out;          // [B][C]
+};
+
+// One token of each sequence: the state's rows move up by one and x becomes
+// its last.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(128) k_sconv_step(ConvStepArgs a) {
+  constexpr int K = W - 1;
+  const int c = (blockIdx.x * 128 + threadIdx.x) * V;
+  if (c >= a.C) return;
+  for (int i = blockIdx.y; i < a.B; i += gridDim.y) {
+    const int slot = a.slots ? a.slots[i] : i;
+    T* out = static_cast<T*>(a.out) + (int64_t)i * a.C + c;
+    float y[V];
+    if (slot < 0 || slot >= a.S) {  // an inactive row
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = 0.f;
+      vstore<T, V>(out, y);
+      continue;
+    }
+    T* st = static_cast<T*>(a.state) + (int64_t)slot * K * a.C + c;
+    Vec<T, V> win[W];
+#pragma unroll
+    for (int k = 0; k < K; ++k) win[k] = vload<T, V>(st + (int64_t)k * a.C);
+    win[K] = vload<T, V>(static_cast<const T*>(a.x) + (int64_t)i * a.ldx + c);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float z = a.bias ? load_param<T>(a.bias, a.wf32, c + v) : 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        z = fmaf(load_param<T>(a.weight, a.wf32, (int64_t)(c + v) * W + j), to_f<T>(win[j].e[v]), z);
+      y[v] = a.silu ? silu_f(z) : z;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) *reinterpret_cast<Vec<T, V>*>(st + (int64_t)k * a.C) = win[k + 1];
+    vstore<T, V>(out, y);
+  }
+}
+
+// Tokens a thread walks: long enough that the rows read again at a tile's
+// start stay a small share, short enough that the grid fills the GPU.
+int tile_tokens(int64_t T, int64_t vec_channels) {
+  const int64_t blocks = (vec_channels + 127) / 128;
+  int64_t tile = (T * blocks + 152 * 16 - 1) / (152 * 16);
+  tile = (tile + 7) / 8 * 8;
+  if (tile < 16) tile = 16;
+  if (tile > 256) tile = 256;
+  return (int)tile;
+}
+// The partial rows a backward leaves do not depend on alignment, so that the
+// workspace does not either: its tile is that of single-channel threads.
+int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, (C + 3) / 4); }
+
+size_t elem(int dtype) { return dtype == GDR_DTYPE_F32 ? 4 : 2; }
+bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// Runs f(type tag, vector width, taps) for the run-time type, alignment and W.
+template <typename T, int V, typename F>
+cudaError_t with_taps(int W, F f) {
+  if (W == 2) return f(T(), std::integral_constant<int, V>(), std::integral_constant<int, 2>());
+  if (W == 3) return f(T(), std::integral_constant<int, V>(), std::integral_constant<int, 3>());
+  return f(T(), std::integral_constant<int, V>(), std::integral_constant<int, 4>());
+}
+template <int BYTES, typename F>
+cudaError_t dispatch(int dtype, bool vec, int W, F f) {
+  switch (dtype) {
+    case GDR_DTYPE_BF16:
+      return vec ? with_taps<__nv_bfloat16, BYTES / 2>(W, f) : with_taps<__nv_bfloat16, 1>(W, f);
+    case GDR_DTYPE_F16: return vec ? with_taps<__half, BYTES / 2>(W, f) : with_taps<__half, 1>(W, f);
+    default: return vec ? with_taps<float, BYTES / 4>(W, f) : with_taps<float, 1>(W, f);
+  }
+}
+
+gdr_status conv_check(int dtype, int wdtype, int64_t T, int64_t ldx, int32_t C, int32_t W, const void* x,
+                      const void* weight) {
+  if (dtype < 0 || dtype > GDR_DTYPE_F32 || (wdtype != dtype && wdtype != GDR_DTYPE_F32)) return GDR_INVALID_ARG;
+  if (C <= 0 || W < 2 || W > 4 || T < 0 || (T > 1 && ldx < C)) return GDR_INVALID_ARG;
+  if (T > 0 && (!x || !weight)) return GDR_INVALID_ARG;
+  return GDR_OK;
+}
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+gdr_status sconv_workspace_bytes(int64_t T, int32_t C, int32_t W, size_t* scratch_bytes) {
+  if (!scratch_bytes || T < 0 || T > INT32_MAX || C <= 0 || W < 2 || W > 4) return GDR_INVALID_ARG;
+  const int tile = bwd_tile_tokens(T, C);
+  const int64_t tiles = T > 0 ? (T + tile - 1) / tile : 1;
+  *scratch_bytes = (size_t)tiles * (W + 1) * C * sizeof(float);
+  return GDR_OK;
+}
+
+gdr_status sconv_fwd(int dtype, const void* x, int64_t ldx, const void* weight, const void* bias, int wdtype,
+                     const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T, int32_t C,
+                     int32_t W, int silu, const void* s0, void* out, void* st, cudaStream_t stream) {
+  gdr_status rc = conv_check(dtype, wdtype, T, ldx, C, W, x, weight);
+  if (rc != GDR_OK) return rc;
+  int64_t nc = 0;
+  if ((rc = plan_host(T, N, cu_seqlens_host, &nc)) != GDR_OK) return rc;
+  if (N == 0 || (T == 0 && !st)) return GDR_OK;
+  if (!cu_seqlens || !weight || (T > 0 && !out)) return GDR_INVALID_ARG;
+  if ((rc = check_device()) != GDR_OK) return rc;
+  ConvArgs a{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, cu_seqlens, N, (int)T, C, silu, s0, out, st, 0, 0};
+  const int V = 16 / (int)elem(dtype);
+  const bool vec = C % V == 0 && ldx % V == 0 && on16(x) && on16(out) && on16(s0) && on16(st);
+  const int nv = vec ? C / V : C;
+  a.tile = tile_tokens(T, nv);
+  a.cblocks = (nv + 127) / 128;
+  const int64_t grid = (T > 0 ? (T + a.tile - 1) / a.tile : 1) * a.cblocks;
+  if (grid > INT32_MAX) return GDR_INVALID_ARG;
+  ProfScope ps("sconv_fwd", stream, (double)T * C);
+  const cudaError_t e = dispatch<16>(dtype, vec, W, [&](auto t, auto v, auto w) {
+    k_sconv_fwd<decltype(t), decltype(v)::value, decltype(w)::value><<<(unsigned)grid, 128, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}
+
+gdr_status sconv_bwd(int dtype, const void* x, int64_t ldx, const void* weight, const void* bias, int wdtype,
+                     const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T, int32_t C,
+                     int32_t W, int silu, const void* s0, const void* dout, int64_t lddout, const void* dst, void* dx,
+                     float* dweight, float* dbias, void* ds0, void* scratch, size_t scratch_bytes,
+                     cudaStream_t stream) {
+  gdr_status rc = conv_check(dtype, wdtype, T, ldx, C, W, x, weight);
+  if (rc != GDR_OK) return rc;
+  int64_t nc = 0;
+  if ((rc = plan_host(T, N, cu_seqlens_host, &nc)) != GDR_OK) return rc;
+  if (!weight || !dweight || !scratch || !cu_seqlens) return GDR_INVALID_ARG;
+  if (T > 0 && (!dout || !dx || (T > 1 && lddout < C))) return GDR_INVALID_ARG;
+  size_t need = 0;
+  sconv_workspace_bytes(T, C, W, &need);
+  if (((uintptr_t)scratch & 255) != 0) return GDR_INVALID_ARG;
+  if (scratch_bytes < need) return GDR_WORKSPACE_TOO_SMALL;
+  if ((rc = check_device()) != GDR_OK) return rc;
+  ConvBwdArgs a{};
+  a.f = ConvArgs{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, cu_seqlens, N, (int)T, C, silu, s0, nullptr, nullptr,
+                 0, 0};
+  a.dout = dout;
+  a.ldo = lddout;
+  a.dst = dst;
+  a.dx = dx;
+  a.ds0 = ds0;
+  a.part = static_cast<float*>(scratch);
+  const int V = dtype == GDR_DTYPE_F32 ? 2 : 4;  // 8 bytes a thread: the sums kept in registers are W of them a channel
+  const uintptr_t all = (uintptr_t)x | (uintptr_t)s0 | (uintptr_t)dout | (uintptr_t)dst | (uintptr_t)dx | (uintptr_t)ds0;
+  const bool vec = C % V == 0 && ldx % V == 0 && lddout % V == 0 && (all & 7) == 0;
+  const int nv = vec ? C / V : C;
+  a.f.tile = bwd_tile_tokens(T, C);
+  a.f.cblocks = (nv + 127) / 128;
+  const int64_t tiles = T > 0 ? (T + a.f.tile - 1) / a.f.tile : 1, grid = tiles * a.f.cblocks;
+  if (grid > INT32_MAX) return GDR_INVALID_ARG;
+  {
+    ProfScope ps("sconv_bwd", stream, (double)T * C);
+    const cudaError_t e = dispatch<8>(dtype, vec, W, [&](auto t, auto v, auto w) {
+      k_sconv_bwd<decltype(t), decltype(v)::value, decltype(w)::value><<<(unsigned)grid, 128, 0, stream>>>(a);
+      return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return GDR_CUDA_ERROR;
+  }
+  ProfScope ps("sconv_wgrad", stream);
+  k_sconv_wgrad<<<dim3((C + 31) / 32, W + 1), 256, 0, stream>>>(a.part, (int)tiles, C, W, dweight, dbias);
+  return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}
+
+gdr_status sconv_step(int dtype, const void* x, int64_t ldx, const void* weight, const void* bias, int wdtype,
+                      void* state, const int32_t* slots, int32_t B, int32_t S, int32_t C, int32_t W, int silu,
+                      void* out, cudaStream_t stream) {
+  gdr_status rc = conv_check(dtype, wdtype, B, ldx, C, W, x, weight);
+  if (rc != GDR_OK) return rc;
+  if (S < 0 || (!slots && B > S)) return GDR_INVALID_ARG;
+  if (B == 0) return GDR_OK;
+  if (!out || (S > 0 && !state)) return GDR_INVALID_ARG;
+  if ((rc = check_device()) != GDR_OK) return rc;
+  ConvStepArgs a{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, state, slots, B, S, C, silu, out};
+  const int V = dtype == GDR_DTYPE_F32 ? 2 : 4;
+  const uintptr_t all = (uintptr_t)x | (uintptr_t)state | (uintptr_t)out;
+  const bool vec = C % V == 0 && ldx % V == 0 && (all & 7) == 0;
+  const int nv = vec ? C / V : C;
+  ProfScope ps("sconv_step", stream, (double)B * C);
+  const cudaError_t e = dispatch<8>(dtype, vec, W, [&](auto t, auto v, auto w) {
+    k_sconv_step<decltype(t), decltype(v)::value, decltype(w)::value>
+        <<<dim3((nv + 127) / 128, B < 65535 ? B : 65535), 128, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}
+
+}  // extern "C"

@@ -1,0 +1,284 @@
+// gdr_ssm.cu -- the selective state space scan with a scalar decay a head, for
+// packed prompts and for single tokens.  Per (document, head), state S [N][P]:
+//   dt' = softplus(dt + dt_bias) (or dt + dt_bias),  S_t = exp(dt' A) S_{t-1} + dt' B_t x_t^T,
+//   out_t = S_t^T C_t + D x_t
+// head h reads B and C of group h / (H / G).
+#include "gdr_ops.cuh"
+#include "gdr_runtime.h"
+
+namespace gdr {
+namespace {
+
+struct SsmArgs {
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const void* dt;
+  int dt_f32;
+  int64_t lddt;
+  const float* A;
+  const __nv_bfloat16 *B, *C;
+  int64_t ldb, ldc;
+  const float *D, *dt_bias;  // [H] or null
+  int softplus;
+  const int* cu;
+  int N, T, H, P, G, NS;  // documents, tokens, heads, head dim, groups, state size
+  const float* h0;        // [N][H][NS][P] or null
+  __nv_bfloat16* out;     // [T][H][P]
+  float* ht;              // [N][H][NS][P] or null
+  // step
+  float* state;           // [S][H][NS][P]
+  const int* slots;
+  int S;
+};
+
+// log(1 + e^x) without overflow and without losing small e^x.
+__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+__device__ __forceinline__ float load_dt(const SsmArgs& a, int64_t t, int h) {
+  float v = a.dt_f32 ? static_cast<const float*>(a.dt)[t * a.lddt + h]
+                     : to_f(static_cast<const __nv_bfloat16*>(a.dt)[t * a.lddt + h]);
+  if (a.dt_bias) v += a.dt_bias[h];
+  return a.softplus ? softplus_f(v) : v;
+}
+
+// Token by token: one block per (document, head, 32 columns of the state), the
+// state in registers (warp w holds rows w, w + 8, ...), tokens staged through
+// shared memory in tiles of 16.
+constexpr int kSeqTok = 16;
+__global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
+  __shared__ float sx[kSeqTok][32], sb[kSeqTok][GDR_SSM_MAX_N], sc[kSeqTok][GDR_SSM_MAX_N];
+  __shared__ float sdt[kSeqTok], sda[kSeqTok], sy[kSeqTok][32];
+  constexpr int R = GDR_SSM_MAX_N / 8;
+  const int slices = (a.P + 31) / 32;
+  const int p0 = (blockIdx.x % slices) * 32, h = (blockIdx.x / slices) % a.H, d = blockIdx.x / slices / a.H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p = p0 + lane, grp = h / (a.H / a.G);
+  const bool on = p < a.P;
+  const int t0 = a.cu[d], t1 = a.cu[d + 1];
+  float s[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int n = warp + 8 * i;
+    s[i] = a.h0 && on && n < a.NS ? a.h0[(((int64_t)d * a.H + h) * a.NS + n) * a.P + p] : 0.f;
+  }
+  for (int t = t0; t < t1; t += kSeqTok) {
+    const int len = min(kSeqTok, t1 - t);
+    for (int i = threadIdx.x; i < len * 32; i += 256) {
+      const int j = i >> 5, l = i & 31;
+      sx[j][l] = p0 + l < a.P ? to_f(a.x[(int64_t)(t + j) * a.ldx + h * a.P + p0 + l]) : 0.f;
+      sy[j][l] = 0.f;
+    }
+    for (int i = threadIdx.x; i < len * a.NS; i += 256) {
+      const int j = i / a.NS, n = i - j * a.NS;
+      sb[j][n] = to_f(a.B[(int64_t)(t + j) * a.ldb + grp * a.NS + n]);
+      sc[j][n] = to_f(a.C[(int64_t)(t + j) * a.ldc + grp * a.NS + n]);
+    }
+    if (threadIdx.x < len) {
+      const float dt = load_dt(a, t + threadIdx.x, h);
+      sdt[threadIdx.x] = dt;
+      sda[threadIdx.x] = expf(dt * a.A[h]);
+    }
+    __syncthreads();
+    for (int j = 0; j < len; ++j) {
+      const float xd = sx[j][lane] * sdt[j], da = sda[j];
+      float y = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int n = warp + 8 * i;
+        if (n < a.NS) {
+          s[i] = fmaf(da, s[i], sb[j][n] * xd);
+          y = fmaf(sc[j][n], s[i], y);
+        }
+      }
+      // the warps' partial sums, in turn (a fixed order)
+      for (int w = 0; w < 8; ++w) {
+        if (w == warp) sy[j][lane] += y;
+        __syncthreads();
+      }
+    }
+    for (int i = threadIdx.x; i < len * 32; i += 256) {
+      const int j = i >> 5, l = i & 31;
+      if (p0 + l < a.P)
+        a.out[((int64_t)(t + j) * a.H + h) * a.P + p0 + l] =
+            from_f<__nv_bfloat16>(fmaf(a.D ? a.D[h] : 0.f, sx[j][l], sy[j][l]));
+    }
+    __syncthreads();
+  }
+  if (a.ht && on) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int n = warp + 8 * i;
+      if (n < a.NS) a.ht[(((int64_t)d * a.H + h) * a.NS + n) * a.P + p] = s[i];
+    }
+  }
+}
+
+// One token of each sequence: one block per (sequence, head), each state row
+// read, updated, multiplied by C and written in one pass.  256 threads cover
+// P / V columns times the rows; the rows' partial sums meet in shared memory.
+// Bound by HBM: 8 bytes a state element.
+template <int V>
+__global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
+  __shared__ float sb[GDR_SSM_MAX_N], sc[GDR_SSM_MAX_N];
+  __shared__ float red[256 * V];
+  const int h = blockIdx.x % a.H, b = blockIdx.x / a.H, grp = h / (a.H / a.G);
+  const int cols = (a.P + V - 1) / V, rows = 256 / cols;  // column groups, rows at a time
+  const int c = threadIdx.x % cols, r = threadIdx.x / cols;
+  const int slot = a.slots ? a.slots[b] : b;
+  __nv_bfloat16* out = a.out + ((int64_t)b * a.H + h) * a.P;
+  if (slot < 0 || slot >= a.S) {  // an inactive row
+    for (int p = threadIdx.x; p < a.P; p += 256) out[p] = from_f<__nv_bfloat16>(0.f);
+    return;
+  }
+  for (int n = threadIdx.x; n < a.NS; n += 256) {
+    sb[n] = to_f(a.B[(int64_t)b * a.ldb + grp * a.NS + n]);
+    sc[n] = to_f(a.C[(int64_t)b * a.ldc + grp * a.NS + n]);
+  }
+  const float dt = load_dt(a, b, h), da = expf(dt * a.A[h]);
+  __syncthreads();
+  float* S = a.state + ((int64_t)slot * a.H + h) * a.NS * a.P + c * V;
+  float xd[V], y[V];
+  const bool on = r < rows;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    xd[v] = to_f(a.x[(int64_t)b * a.ldx + h * a.P + c * V + v]) * dt;
+    y[v] = 0.f;
+  }
+  if (on) {
+    for (int n = r; n < a.NS; n += rows) {
+      float s[V];
+      vunpack<float, V>(vload<float, V>(S + (int64_t)n * a.P), s);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[v] = fmaf(da, s[v], sb[n] * xd[v]);
+        y[v] = fmaf(sc[n], s[v], y[v]);
+      }
+      vstore<float, V>(S + (int64_t)n * a.P, s);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) red[(r * cols + c) * V + v] = y[v];
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < a.P; p += 256) {
+    float sum = 0.f;
+    for (int i = 0; i < rows; ++i) sum += red[i * cols * V + p];
+    const float x = to_f(a.x[(int64_t)b * a.ldx + h * a.P + p]);
+    out[p] = from_f<__nv_bfloat16>(fmaf(a.D ? a.D[h] : 0.f, x, sum));
+  }
+}
+
+gdr_status ssm_check(const SsmArgs& a, int64_t T) {
+  if (a.H <= 0 || a.G <= 0 || a.H % a.G != 0 || a.P <= 0 || a.P > GDR_SSM_MAX_P || a.NS <= 0 ||
+      a.NS > GDR_SSM_MAX_N || T < 0)
+    return GDR_INVALID_ARG;
+  if (T > 0 && (!a.x || !a.dt || !a.A || !a.B || !a.C || !a.out)) return GDR_INVALID_ARG;
+  if (T > 1 && (a.ldx < (int64_t)a.H * a.P || a.ldb < (int64_t)a.G * a.NS || a.ldc < (int64_t)a.G * a.NS ||
+                a.lddt < a.H))
+    return GDR_INVALID_ARG;
+  return GDR_OK;
+}
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+gdr_status ssm_workspace_bytes(int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, int32_t N,
+                               const int32_t* cu_seqlens_host, size_t* scratch_bytes) {
+  int64_t nc = 0;
+  if (!scratch_bytes || H <= 0 || G <= 0 || H % G != 0 || P <= 0 || P > GDR_SSM_MAX_P || NS <= 0 ||
+      NS > GDR_SSM_MAX_N)
+    return GDR_INVALID_ARG;
+  const gdr_status rc = plan_host(T, N, cu_seqlens_host, &nc);
+  if (rc != GDR_OK) return rc;
+  *scratch_bytes = 0;
+  return GDR_OK;
+}
+
+gdr_status ssm_fwd(const gdr_bf16* x, int64_t ldx, const void* dt, int dt_dtype, int64_t lddt, const float* A,
+                   const gdr_bf16* B, int64_t ldb, const gdr_bf16* C, int64_t ldc, const float* D,
+                   const float* dt_bias, int softplus, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                   int32_t N, int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, const float* h0, gdr_bf16* out,
+                   float* ht, void* scratch, size_t scratch_bytes, cudaStream_t stream) {
+  int64_t nc = 0;
+  gdr_status rc = plan_host(T, N, cu_seqlens_host, &nc);
+  if (rc != GDR_OK) return rc;
+  if (dt_dtype != GDR_DTYPE_BF16 && dt_dtype != GDR_DTYPE_F32) return GDR_INVALID_ARG;
+  SsmArgs a{};
+  a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  a.ldx = ldx;
+  a.dt = dt;
+  a.dt_f32 = dt_dtype == GDR_DTYPE_F32;
+  a.lddt = lddt;
+  a.A = A;
+  a.B = reinterpret_cast<const __nv_bfloat16*>(B);
+  a.C = reinterpret_cast<const __nv_bfloat16*>(C);
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.D = D;
+  a.dt_bias = dt_bias;
+  a.softplus = softplus;
+  a.cu = cu_seqlens;
+  a.N = N;
+  a.T = (int)T;
+  a.H = H;
+  a.P = P;
+  a.G = G;
+  a.NS = NS;
+  a.h0 = h0;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.ht = ht;
+  if ((rc = ssm_check(a, T)) != GDR_OK) return rc;
+  if (N == 0) return GDR_OK;
+  if (!cu_seqlens) return GDR_INVALID_ARG;
+  (void)scratch;
+  (void)scratch_bytes;
+  const int64_t grid = (int64_t)N * H * ((P + 31) / 32);
+  if (grid > INT32_MAX) return GDR_INVALID_ARG;
+  if ((rc = check_device()) != GDR_OK) return rc;
+  ProfScope ps("ssm_scan", stream, (double)T * H);
+  k_ssm_seq<<<(unsigned)grid, 256, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}
+
+gdr_status ssm_step(const gdr_bf16* x, int64_t ldx, const void* dt, int dt_dtype, int64_t lddt, const float* A,
+                    const gdr_bf16* B, int64_t ldb, const gdr_bf16* C, int64_t ldc, const float* D,
+                    const float* dt_bias, int softplus, float* state, const int32_t* slots, int32_t NB, int32_t S,
+                    int32_t H, int32_t P, int32_t G, int32_t NS, gdr_bf16* out, cudaStream_t stream) {
+  if (dt_dtype != GDR_DTYPE_BF16 && dt_dtype != GDR_DTYPE_F32) return GDR_INVALID_ARG;
+  SsmArgs a{};
+  a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  a.ldx = ldx;
+  a.dt = dt;
+  a.dt_f32 = dt_dtype == GDR_DTYPE_F32;
+  a.lddt = lddt;
+  a.A = A;
+  a.B = reinterpret_cast<const __nv_bfloat16*>(B);
+  a.C = reinterpret_cast<const __nv_bfloat16*>(C);
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.D = D;
+  a.dt_bias = dt_bias;
+  a.softplus = softplus;
+  a.H = H;
+  a.P = P;
+  a.G = G;
+  a.NS = NS;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.state = state;
+  a.slots = slots;
+  a.S = S;
+  gdr_status rc = ssm_check(a, NB);
+  if (rc != GDR_OK) return rc;
+  if (S < 0 || (!slots && NB > S) || (S > 0 && !state)) return GDR_INVALID_ARG;
+  if (NB == 0) return GDR_OK;
+  if ((int64_t)NB * H > INT32_MAX) return GDR_INVALID_ARG;
+  if ((rc = check_device()) != GDR_OK) return rc;
+  ProfScope ps("ssm_step", stream, (double)NB * H);
+  if (P % 4 == 0 && ((uintptr_t)state & 15) == 0) k_ssm_step<4><<<NB * H, 256, 0, stream>>>(a);
+  else k_ssm_step<1><<<NB * H, 256, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}
+
+}  // extern "C"

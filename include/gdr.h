@@ -259,7 +259,10 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * into buf; it returns GDR_INVALID_ARG if buf_bytes is too small.  Kernel
  * names: plan, check, l2norm, prep, walk_fwd_sum, merge_fwd, walk_fwd, walk_bwd_sum,
  * merge_bwd, walk_bwd, grad_state, grad, group_reduce (the _sum and merge
- * launches run only for split packs, l2norm only with qk_l2norm). */
+ * launches run only for split packs, l2norm only with qk_l2norm); the
+ * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
+ * sconv_step, ssm_scan, ssm_step, kda_step, gdn_step, norm_fwd, norm_bwd,
+ * norm_wgrad. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
 
@@ -328,6 +331,132 @@ int gdr_set_slice_chunks(int chunks);
  * GDR_INVALID_ARG for null pointers, nchunks < 0, a direction other than 0
  * or 1, or a cap too small for the plan. */
 gdr_status gdr_walk_slices(int32_t nchunks, int32_t direction, int32_t* bounds, int32_t cap, int32_t* n_slices);
+
+/* ===========================================================================
+ * Operators around the recurrence: the short causal convolution in front of
+ * it, the selective state space scan beside it, the norms after it and before
+ * the next block, and the single-token forms that serve a model.
+ *
+ * Conventions as above, and:
+ *   - Element types (gdr_dtype): the activations of sconv_* and norm_* are
+ *     BF16, FP16 or FP32; their weights and biases have the activations' type
+ *     or FP32 (wdtype).  All arithmetic, statistics and weight gradients are
+ *     FP32; each output is rounded once.
+ *   - Strides (ld*, *s0, *s1) count elements; the innermost dimensions are
+ *     dense, so that slices of a wider projection can be passed as they are.
+ *     Any alignment of at least the element size is accepted; rows on 16-byte
+ *     boundaries are read in 16-byte pieces.
+ *   - Single-token forms work on a pool of S states, updated in place: row b
+ *     of the batch uses state slots[b] (slots null: state b, B <= S).  A slot
+ *     outside [0, S) makes the row inactive: its output is zero and no state
+ *     is touched.  Two rows of one call must not share a slot.
+ *   - Results are deterministic (no floating-point atomics). */
+typedef int gdr_dtype;
+#define GDR_DTYPE_BF16 0
+#define GDR_DTYPE_F16 1
+#define GDR_DTYPE_F32 2
+
+/* Short causal depthwise convolution over packed documents, W = 2, 3 or 4
+ * taps, one filter a channel:
+ *     z[t][c] = bias[c] + sum_{j<W} weight[c][j] xx[t - (W-1) + j][c],
+ *     out = z, or z sigmoid(z) when silu is non-zero,
+ * where xx is x inside the document and, before its first token, the W - 1
+ * rows of its start state s0[doc] (oldest first; null: zero).  x [T][C] with
+ * rows ldx apart; weight [C][W]; bias [C] or null; s0, st [N][W-1][C];
+ * out [T][C].  st, when non-null, gets the last W - 1 rows of xx of every
+ * document (an empty document's start state). */
+gdr_status sconv_fwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
+                     gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
+                     int32_t C, int32_t W, int silu, const void* s0, void* out, void* st, cudaStream_t stream);
+
+/* Bytes of scratch that sconv_bwd needs (host only). */
+gdr_status sconv_workspace_bytes(int64_t T, int32_t C, int32_t W, size_t* scratch_bytes);
+
+/* Gradients of sconv_fwd: dout [T][C] with rows lddout apart, dst [N][W-1][C]
+ * or null (zero).  Writes dx [T][C], dweight [C][W] FP32 and, when non-null,
+ * dbias [C] FP32 and ds0 [N][W-1][C]. */
+gdr_status sconv_bwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
+                     gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
+                     int32_t C, int32_t W, int silu, const void* s0, const void* dout, int64_t lddout, const void* dst,
+                     void* dx, float* dweight, float* dbias, void* ds0, void* scratch, size_t scratch_bytes,
+                     cudaStream_t stream);
+
+/* One token of each of B sequences through the convolution: x [B][C] (rows
+ * ldx apart), state [S][W-1][C] updated in place, out [B][C]. */
+gdr_status sconv_step(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
+                      gdr_dtype wdtype, void* state, const int32_t* slots, int32_t B, int32_t S, int32_t C, int32_t W,
+                      int silu, void* out, cudaStream_t stream);
+
+/* Selective state space scan, one scalar decay a head, over packed documents:
+ *     dt'_t = softplus(dt_t + dt_bias)  (softplus = 0: dt_t + dt_bias),
+ *     S_t = exp(dt'_t A) S_{t-1} + dt'_t B_t x_t^T      (S [NS][P]),
+ *     out_t = S_t^T C_t + D x_t,
+ * S starting from h0[doc] (null: zero).  x [T][H][P], B, C [T][G][NS] BF16 and
+ * dt [T][H] BF16 or FP32 (dt_dtype), their tokens ldx, ldb, ldc, lddt apart;
+ * head h reads group h / (H / G) of B and C; A, D, dt_bias [H] FP32 (D,
+ * dt_bias null: zero).  Writes out [T][H][P] BF16 and, when non-null, the end
+ * states ht [N][H][NS][P] FP32.  1 <= P <= GDR_SSM_MAX_P, 1 <= NS <=
+ * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay). */
+#define GDR_SSM_MAX_P 256
+#define GDR_SSM_MAX_N 256
+gdr_status ssm_workspace_bytes(int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, int32_t N,
+                               const int32_t* cu_seqlens_host, size_t* scratch_bytes);
+gdr_status ssm_fwd(const gdr_bf16* x, int64_t ldx, const void* dt, gdr_dtype dt_dtype, int64_t lddt, const float* A,
+                   const gdr_bf16* B, int64_t ldb, const gdr_bf16* C, int64_t ldc, const float* D,
+                   const float* dt_bias, int softplus, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                   int32_t N, int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, const float* h0, gdr_bf16* out,
+                   float* ht, void* scratch, size_t scratch_bytes, cudaStream_t stream);
+
+/* One token of each of NB sequences through the scan: state [S][H][NS][P]
+ * FP32 updated in place, the other arguments as for ssm_fwd with T = NB. */
+gdr_status ssm_step(const gdr_bf16* x, int64_t ldx, const void* dt, gdr_dtype dt_dtype, int64_t lddt, const float* A,
+                    const gdr_bf16* B, int64_t ldb, const gdr_bf16* C, int64_t ldc, const float* D,
+                    const float* dt_bias, int softplus, float* state, const int32_t* slots, int32_t NB, int32_t S,
+                    int32_t H, int32_t P, int32_t G, int32_t NS, gdr_bf16* out, cudaStream_t stream);
+
+/* One token of each of B sequences through the gated delta rule (the
+ * recurrence at the top of this file), state [S][HV][128][128] FP32 (S[k][v],
+ * 16-byte aligned) updated in place: a forward's ht can be served as it is.
+ * q, k [B][Hqk][128], v, out [B][HV][128]; gates as in kda_fwd / gdn_fwd, any
+ * finite or -inf log-decay. */
+gdr_status kda_step(const gdr_bf16* q, const gdr_bf16* k, const gdr_bf16* v, const float* g, const gdr_bf16* beta,
+                    float* state, const int32_t* slots, int32_t B, int32_t S, int32_t H, float scale, int qk_l2norm,
+                    gdr_bf16* out, cudaStream_t stream);
+gdr_status gdn_step(const gdr_bf16* q, const gdr_bf16* k, const gdr_bf16* v, const float* g, const float* beta,
+                    float* state, const int32_t* slots, int32_t B, int32_t S, int32_t Hqk, int32_t HV, float scale,
+                    int qk_l2norm, gdr_bf16* out, cudaStream_t stream);
+
+/* The norms around a block, fused with its gate, residual scale and residual,
+ * on rows of D elements (1 <= D <= GDR_NORM_MAX_D):
+ *     u = x, or x (mean x^2 + eps)^(-1/2) post_weight   (post_weight non-null)
+ *     u = u act(gate)                                   (gate non-null)
+ *     h = residual + res_scale u, or u                  (residual null)
+ *     y = h (mean h^2 + eps)^(-1/2) weight              (y, weight non-null)
+ * act: GDR_ACT_SILU (z sigmoid(z)) or GDR_ACT_SIGMOID.  Rows are indexed by
+ * (R0, R1), the input's row strides are (*s0, *s1); h and y are dense
+ * [R0][R1][D], each written when non-null; y is formed from the unrounded h.
+ * At least one of residual, post_weight, weight is given. */
+#define GDR_ACT_SILU 0
+#define GDR_ACT_SIGMOID 1
+#define GDR_NORM_MAX_D 16384
+gdr_status norm_fwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
+                    const void* gate, int64_t gs0, int64_t gs1, int act, const void* residual, int64_t rs0,
+                    int64_t rs1, float res_scale, const void* post_weight, const void* weight, gdr_dtype wdtype,
+                    float eps, void* h, void* y, cudaStream_t stream);
+
+/* Bytes of scratch that norm_bwd needs (host only). */
+gdr_status norm_workspace_bytes(int32_t D, size_t* scratch_bytes);
+
+/* Gradients of norm_fwd from dh and dy, the gradients with respect to h and y
+ * (either may be null: zero; dy needs weight).  Writes, each when non-null,
+ * dx, dgate, dresidual (dense rows, the activations' type) and dweight,
+ * dpost_weight [D] FP32. */
+gdr_status norm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
+                    const void* gate, int64_t gs0, int64_t gs1, int act, const void* residual, int64_t rs0,
+                    int64_t rs1, float res_scale, const void* post_weight, const void* weight, gdr_dtype wdtype,
+                    float eps, const void* dh, int64_t dhs0, int64_t dhs1, const void* dy, int64_t dys0, int64_t dys1,
+                    void* dx, void* dgate, void* dresidual, float* dweight, float* dpost_weight, void* scratch,
+                    size_t scratch_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
