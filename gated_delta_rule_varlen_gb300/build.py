@@ -14,8 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libgdr.so")
-SOURCES = ["gdr_fwd.cu", "gdr_walk.cu", "gdr_bwd.cu", "gdr_api.cu", "gdr_sconv.cu", "gdr_ssm.cu", "gdr_step.cu",
-           "gdr_norm_fwd.cu", "gdr_norm_bwd.cu"]
+SOURCES = ["gdr_fwd.cu", "gdr_walk.cu", "gdr_bwd.cu", "gdr_api.cu", "gdr_sconv.cu", "gdr_ssm.cu", "gdr_ssm_tc.cu",
+           "gdr_step.cu", "gdr_norm_fwd.cu", "gdr_norm_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -3,43 +3,10 @@
 //   dt' = softplus(dt + dt_bias) (or dt + dt_bias),  S_t = exp(dt' A) S_{t-1} + dt' B_t x_t^T,
 //   out_t = S_t^T C_t + D x_t
 // head h reads B and C of group h / (H / G).
-#include "gdr_ops.cuh"
-#include "gdr_runtime.h"
+#include "gdr_ssm.cuh"
 
 namespace gdr {
 namespace {
-
-struct SsmArgs {
-  const __nv_bfloat16* x;
-  int64_t ldx;
-  const void* dt;
-  int dt_f32;
-  int64_t lddt;
-  const float* A;
-  const __nv_bfloat16 *B, *C;
-  int64_t ldb, ldc;
-  const float *D, *dt_bias;  // [H] or null
-  int softplus;
-  const int* cu;
-  int N, T, H, P, G, NS;  // documents, tokens, heads, head dim, groups, state size
-  const float* h0;        // [N][H][NS][P] or null
-  __nv_bfloat16* out;     // [T][H][P]
-  float* ht;              // [N][H][NS][P] or null
-  // step
-  float* state;           // [S][H][NS][P]
-  const int* slots;
-  int S;
-};
-
-// log(1 + e^x) without overflow and without losing small e^x.
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
-__device__ __forceinline__ float load_dt(const SsmArgs& a, int64_t t, int h) {
-  float v = a.dt_f32 ? static_cast<const float*>(a.dt)[t * a.lddt + h]
-                     : to_f(static_cast<const __nv_bfloat16*>(a.dt)[t * a.lddt + h]);
-  if (a.dt_bias) v += a.dt_bias[h];
-  return a.softplus ? softplus_f(v) : v;
-}
 
 // Token by token: one block per (document, head, 32 columns of the state), the
 // state in registers (warp w holds rows w, w + 8, ...), tokens staged through
@@ -192,7 +159,7 @@ gdr_status ssm_workspace_bytes(int64_t T, int32_t H, int32_t P, int32_t G, int32
     return GDR_INVALID_ARG;
   const gdr_status rc = plan_host(T, N, cu_seqlens_host, &nc);
   if (rc != GDR_OK) return rc;
-  *scratch_bytes = 0;
+  *scratch_bytes = N > 0 && ssm_tc_shape(P, NS) ? ssm_tc_plan(H, P, NS, N, cu_seqlens_host).scratch : 0;
   return GDR_OK;
 }
 
@@ -232,12 +199,20 @@ gdr_status ssm_fwd(const gdr_bf16* x, int64_t ldx, const void* dt, int dt_dtype,
   if ((rc = ssm_check(a, T)) != GDR_OK) return rc;
   if (N == 0) return GDR_OK;
   if (!cu_seqlens) return GDR_INVALID_ARG;
-  (void)scratch;
-  (void)scratch_bytes;
+  // The chunked kernels need rows that TMA can address; others go token by token.
+  const bool tc = ssm_tc_shape(P, NS) && ssm_tc_layout(a);
+  if (tc) {
+    const SsmPlan plan = ssm_tc_plan(H, P, NS, N, cu_seqlens_host);
+    if (plan.nseg * H * ((P + 63) / 64) > INT32_MAX) return GDR_INVALID_ARG;
+    if (plan.scratch > 0 && (!scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
+    if (scratch_bytes < plan.scratch) return GDR_WORKSPACE_TOO_SMALL;
+    if ((rc = check_device()) != GDR_OK) return rc;
+    return launch_ssm_tc(a, plan, scratch, stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  }
   const int64_t grid = (int64_t)N * H * ((P + 31) / 32);
   if (grid > INT32_MAX) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
-  ProfScope ps("ssm_scan", stream, (double)T * H);
+  ProfScope ps("ssm_seq", stream, (double)T * H);
   k_ssm_seq<<<(unsigned)grid, 256, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
 }

@@ -1,0 +1,54 @@
+// gdr_ssm.cuh -- arguments and pieces that the selective scan's kernels share.
+#pragma once
+#include <cuda.h>
+#include "gdr_ops.cuh"
+#include "gdr_runtime.h"
+
+namespace gdr {
+
+struct SsmArgs {
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const void* dt;
+  int dt_f32;
+  int64_t lddt;
+  const float* A;
+  const __nv_bfloat16 *B, *C;
+  int64_t ldb, ldc;
+  const float *D, *dt_bias;  // [H] or null
+  int softplus;
+  const int* cu;
+  int N, T, H, P, G, NS;  // documents, tokens, heads, head dim, groups, state size
+  const float* h0;        // [N][H][NS][P] or null
+  __nv_bfloat16* out;     // [T][H][P]
+  float* ht;              // [N][H][NS][P] or null
+  // step
+  float* state;           // [S][H][NS][P]
+  const int* slots;
+  int S;
+};
+
+// log(1 + e^x) without overflow and without losing small e^x.
+__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+__device__ __forceinline__ float load_dt(const SsmArgs& a, int64_t t, int h) {
+  float v = a.dt_f32 ? static_cast<const float*>(a.dt)[t * a.lddt + h]
+                     : to_f(static_cast<const __nv_bfloat16*>(a.dt)[t * a.lddt + h]);
+  if (a.dt_bias) v += a.dt_bias[h];
+  return a.softplus ? softplus_f(v) : v;
+}
+
+// The chunked scan on the tensor cores (gdr_ssm_tc.cu): whether these
+// arguments can take it, how it cuts the documents, its scratch and its launch.
+struct SsmPlan {
+  int lseg;          // chunks of a segment at most
+  int64_t nseg;      // segments of all documents (an empty document has one)
+  bool split;        // some document has several
+  size_t scratch;    // bytes
+};
+bool ssm_tc_shape(int P, int NS);
+bool ssm_tc_layout(const SsmArgs& a);
+SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu_host);
+cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, cudaStream_t st);
+
+}  // namespace gdr
