@@ -28,8 +28,25 @@ struct SsmArgs {
   int S;
 };
 
-// log(1 + e^x) without overflow and without losing small e^x.
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// log(1 + e^x) = max(x, 0) + log(1 + y) with y = e^-|x| in (0, 1], and log(1 + y)
+// = 2 atanh(t), t = y / (2 + y) <= 1/3, by its series 2 t (1 + t^2/3 + t^4/5 +
+// ...), whose first seven terms leave less than 2^-26; small y keep their
+// relative accuracy.  The exponent's product with log2(e) carries its rounding
+// error along (as the factor 1 + err ln 2).
+__device__ __forceinline__ float softplus_f(float x) {
+  const float z = fminf(fabsf(x), 1e4f), e = -z * LOG2E;  // e^-1e4 is 0 (and inf stays out of the products)
+  const float err = fmaf(-z, LOG2E, -e) - z * 1.92596299e-8f;  // log2(e) - LOG2E
+  const float y = ex2(e) * fmaf(err, 0.69314718f, 1.f);
+  const float t = __fdividef(y, 2.f + y), t2 = t * t;
+  float s = fmaf(t2, 1.f / 13.f, 1.f / 11.f);
+  s = fmaf(t2, s, 1.f / 9.f);
+  s = fmaf(t2, s, 1.f / 7.f);
+  s = fmaf(t2, s, 1.f / 5.f);
+  s = fmaf(t2, s, 1.f / 3.f);
+  s = fmaf(t2, s, 1.f);
+  const float v = fmaxf(x, 0.f) + 2.f * t * s;
+  return x != x ? x : v;
+}
 
 __device__ __forceinline__ float load_dt(const SsmArgs& a, int64_t t, int h) {
   float v = a.dt_f32 ? static_cast<const float*>(a.dt)[t * a.lddt + h]

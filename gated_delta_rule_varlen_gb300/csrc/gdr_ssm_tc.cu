@@ -92,18 +92,26 @@ __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int wan
   return Seg{0, 0, 1, 0, 0, 0};
 }
 
-// Bounded wait that also gives up once another role of the block has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  if (tc::mbar_try(bar, parity)) return true;
-  const uint64_t t0 = tc::global_ns();
-  while (!tc::mbar_try(bar, parity)) {
-    if (*abort) return false;
-    if (tc::global_ns() - t0 > 2000000000ull) {
+// Waits of the blocks' roles.  Each gives up after kTries tries of at most a
+// microsecond, or once another role has, and returns false; the block then
+// reports the timeout as it ends.  Few instructions: the roles run straight
+// through long loops that share the instruction cache.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (int tries = 0; !try_phase(bar, parity); ++tries)
+    if (tries > kTries || *abort) {
       *abort = 1;
-      atomicExch(err, 10);
       return false;
     }
-  }
   return true;
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -115,86 +123,217 @@ constexpr uint32_t kIdescTransposeA = 1u << 15;
 // Byte of the 16-byte piece c (8 BF16) of row r of a 128-byte-swizzled block.
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Two FP32 numbers as BF16 pairs: hi rounded to nearest, lo the rest rounded
-// (off by at most 2^-18 of the number).
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+// Pairs of FP32 operations as one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The two BF16 of a word as a pair of FP32.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(bf_lo(w), bf_hi(w)); }
+
+// A pair of FP32 numbers as BF16 pairs: hi rounded to nearest, lo the rest
+// rounded (off by at most 2^-18 of the number).
+__device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(v, a, b);
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   hi = *reinterpret_cast<const uint32_t*>(&h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf_lo(hi), b - bf_hi(hi));
+  unpack2(fma2(widen2(hi), pack2(-1.f, -1.f), v), a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a, b);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// Inclusive warp scan.
-__device__ __forceinline__ float scan_up(float v, int lane) {
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, v, m);
-    if (lane >= m) v += u;
-  }
-  return v;
+// Shared-memory matrix descriptors of 128-byte-swizzled tiles share their upper
+// word (8-row groups 1024 bytes apart, descriptor version 1, the swizzle); the
+// lower word is the address in 16-byte units and, for MN-major tiles, the
+// distance of the 64-element blocks along MN.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(const void* tile) { return tc::smem_u32(tile) >> 4 | (BLK / 16) << 16; }
+
+// MMAs and commits that a whole warp walks through together and one elected
+// thread performs (the same one each time).  Measured: 36 clocks an MMA of 64
+// columns from TMEM and 53 from shared memory, its read time; picked by a
+// comparison of the lane instead, 72 for either.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
 }
-__device__ __forceinline__ float scan_down(float v, int lane) {
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const float u = __shfl_down_sync(0xffffffffu, v, m);
-    if (lane + m < 32) v += u;
-  }
-  return v;
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+// The same values, known to be the same on every lane: what is computed from
+// them (loop bounds, operand addresses) can live in uniform registers.
+__device__ __forceinline__ Seg uniform(const Seg& s) {
+  Seg u;
+  u.doc = __shfl_sync(0xffffffffu, s.doc, 0);
+  u.idx = __shfl_sync(0xffffffffu, s.idx, 0);
+  u.nseg = __shfl_sync(0xffffffffu, s.nseg, 0);
+  u.tok0 = __shfl_sync(0xffffffffu, s.tok0, 0);
+  u.len = __shfl_sync(0xffffffffu, s.len, 0);
+  u.first = __shfl_sync(0xffffffffu, s.first, 0);
+  return u;
+}
+// One arrival for the warp, after all its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
+}
+// The wait of a whole warp: the same answer on every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (int tries = 0; !__all_sync(0xffffffffu, try_phase(bar, parity)); ++tries)
+    if (__any_sync(0xffffffffu, tries > kTries || *abort)) {
+      *abort = 1;
+      return false;
+    }
+  return true;
+}
+// tcgen05.wait::ld with the loaded registers as operands: nothing that reads
+// them can be scheduled before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+// Eight consecutive TMEM columns of the warp's lanes to registers (complete
+// after wait_ld).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) {
+  return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// Eight consecutive TMEM columns of the warp's lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
-// Lane l loads the raw dt of tokens 4 l .. 4 l + 3 (zero past `len`: no step at all).
-__device__ __forceinline__ void load_gates(const SsmArgs& a, int h, int tok0, int len, float (&dt)[4]) {
+// Exclusive sums over the lanes before and after this one.
+__device__ __forceinline__ void scan_both(float v, int lane, float& before, float& after) {
+  float up = v, down = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, m), d = __shfl_down_sync(0xffffffffu, down, m);
+    if (lane >= m) up += u;
+    if (lane + m < 32) down += d;
+  }
+  up = __shfl_up_sync(0xffffffffu, up, 1);
+  down = __shfl_down_sync(0xffffffffu, down, 1);
+  before = lane == 0 ? 0.f : up;
+  after = lane == 31 ? 0.f : down;
+}
+
+// Lane l loads the raw dt of tokens 4 l .. 4 l + 3 (of `len`, which may be none).
+__device__ __forceinline__ void load_raw(const SsmArgs& a, int h, int tok0, int len, float (&dt)[4]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = 4 * lane + i;
-    dt[i] = j < len ? load_dt(a, tok0 + j, h) : 0.f;
+    dt[i] = 0.f;
+    if (j < len) {
+      const int64_t at = (int64_t)(tok0 + j) * a.lddt + h;
+      dt[i] = a.dt_f32 ? static_cast<const float*>(a.dt)[at] : to_f(static_cast<const __nv_bfloat16*>(a.dt)[at]);
+    }
   }
 }
+__device__ __forceinline__ float activate(const SsmArgs& a, float v) { return a.softplus ? softplus_f(v) : v; }
 
-// Row j of a tile block to zero.
-__device__ __forceinline__ void clear_row(unsigned char* tile, int j) {
+// Pieces [c0, c0 + n) of row j of a tile block to zero.
+template <int N>
+__device__ __forceinline__ void clear_pieces(unsigned char* tile, int j, int c0) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + j * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+  for (int c = 0; c < N; ++c) *reinterpret_cast<uint4*>(tile + piece(j, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// xw rows: w_j x_j of token row j as hi and lo blocks.
-__device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* hi, unsigned char* lo, int j, float w) {
+// w_j x_j of token row j, pieces [c0, c0 + n), as hi and lo blocks.
+template <int N>
+__device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* hi, unsigned char* lo, int j, int c0,
+                                         float w) {
+  const uint64_t ww = pack2(w, w);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint4 v = *reinterpret_cast<const uint4*>(x + piece(j, c));
+  for (int c = 0; c < N; ++c) {
+    const uint32_t at = piece(j, c0 + c);
+    const uint4 v = *reinterpret_cast<const uint4*>(x + at);
     uint4 h, l;
-    split2(bf_lo(v.x) * w, bf_hi(v.x) * w, h.x, l.x);
-    split2(bf_lo(v.y) * w, bf_hi(v.y) * w, h.y, l.y);
-    split2(bf_lo(v.z) * w, bf_hi(v.z) * w, h.z, l.z);
-    split2(bf_lo(v.w) * w, bf_hi(v.w) * w, h.w, l.w);
-    *reinterpret_cast<uint4*>(hi + piece(j, c)) = h;
-    *reinterpret_cast<uint4*>(lo + piece(j, c)) = l;
+    split2(mul2(widen2(v.x), ww), h.x, l.x);
+    split2(mul2(widen2(v.y), ww), h.y, l.y);
+    split2(mul2(widen2(v.z), ww), h.z, l.z);
+    split2(mul2(widen2(v.w), ww), h.w, l.w);
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
   }
 }
 
 // ---------------------------------------------------------------------------
-// The walk: one block per (segment, head, 64 columns of the state).
-//   warp 0: TMA;  warp 1: MMA issue, TMEM;  warp 2: gates
-//   warps 4-7: M from CB;  warps 8-11: w x, the state;  warps 12-15: outputs
-// Every role runs through the chunks on its own; barriers hand buffers over.
+// The walk: one block per (segment, head, 64 columns of the state).  One warp
+// for TMA, one for MMA issue, one for the gates, and six groups of four warps:
+//   groups 0, 1: M from CB (16 of each 32 columns each)
+//   groups 2, 3: the state (32 columns each)
+//   groups 4, 5: w x and the outputs (32 columns each)
+// Every role runs through the chunks on its own; barriers hand the buffers
+// over.  Per chunk the MMA warp issues U, Yo, Yd and the next chunk's CB.  An MMA
+// of 64 columns takes as long to issue as one of 128, and reads A as often: the
+// hi and lo operands of U and Yo sit side by side as one of 128 columns.
 // ---------------------------------------------------------------------------
-constexpr int WALK_THREADS = 512;
-constexpr uint32_t T_CB = 0, T_YO = 128, T_YD = 192, T_U = 256, T_MH = 320, T_ML = 384;
+constexpr int WALK_THREADS = 28 * 32;
+// TMEM columns: CB (16 of them a step of 16 K, over which M's hi and lo are
+// written, 8 columns each), Yo and U (hi products, lo products), Yd.
+constexpr uint32_t T_CB = 0, T_YO = 128, T_U = 256, T_YD = 384;
 
 struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
   unsigned char xw[2][BLK];  // hi, lo
   unsigned char S[2][BLK];   // hi, lo
-  // One chunk's gates.  gc is read until the chunk's outputs leave, the others
+  // One chunk's gates.  gc and gam are read until the chunk's end, the others
   // only up to M and w x: single buffers (shared memory is full).
   float gc[2][Q];  // prefix sums of dt A log2(e)
   float dt[Q];
   float colf[Q];   // dt_j 2^(gc[end of j's 32-block] - gc_j)
   float w[Q];      // dt_j 2^(sum after j)
-  float gam;       // 2^gc[last]
-  uint64_t full[2], empty[2], gates[2], w_full;
-  uint64_t cb_full, m_full, xw_full, u_full, s_full, y_full, y_empty, done;
+  float gam[2];    // 2^gc[last]
+  // by the chunk's parity where a role may wait a chunk apart from the others
+  uint64_t full[2], empty[2], gates[2], m_full[2], xw_full[2];
+  uint64_t w_full, cb_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done;
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -204,10 +343,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   extern __shared__ __align__(1024) unsigned char ssm_smem[];  // tiles are swizzled in 1024-byte atoms
   WalkSmem& s = *reinterpret_cast<WalkSmem*>(ssm_smem);
   const SsmArgs& a = ta.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per = a.H * ta.pblocks;
   const int hp = blockIdx.x % per, h = hp / ta.pblocks, p0 = (hp % ta.pblocks) * PT, sid = blockIdx.x / per;
-  const int grp = h / (a.H / a.G);
   const int nblk = a.NS > 64 ? 2 : 1, ksteps = (a.NS + 15) / 16;
   if (warp == 0) {
     const Seg sg = find_segment(a.cu, a.N, ta.lseg, sid);
@@ -216,17 +355,19 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       s.abort = 0;
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&s.full[i], 1);
-        tc::mbar_init(&s.empty[i], 1 + 128);
-        tc::mbar_init(&s.gates[i], 32);
+        tc::mbar_init(&s.empty[i], 1 + 8);
+        tc::mbar_init(&s.gates[i], 1);
+        tc::mbar_init(&s.m_full[i], 8);
+        tc::mbar_init(&s.xw_full[i], 8);
       }
-      tc::mbar_init(&s.w_full, 32);
+      tc::mbar_init(&s.w_full, 1);
       tc::mbar_init(&s.cb_full, 1);
-      tc::mbar_init(&s.m_full, 128);
-      tc::mbar_init(&s.xw_full, 128);
       tc::mbar_init(&s.u_full, 1);
-      tc::mbar_init(&s.s_full, 128);
+      tc::mbar_init(&s.u_empty, 8);
+      tc::mbar_init(&s.s_full, 8);
+      tc::mbar_init(&s.yo_full, 1);
       tc::mbar_init(&s.y_full, 1);
-      tc::mbar_init(&s.y_empty, 128);
+      tc::mbar_init(&s.y_empty, 8);
       tc::mbar_init(&s.done, 1);
       tc::mbar_fence_init();
     }
@@ -238,19 +379,22 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const Seg sg = s.seg;
-  const uint32_t tmem = s.tmem;
+  const Seg sg = uniform(s.seg);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
   const int nch = (sg.len + Q - 1) / Q;
-  const bool last_seg = sg.idx == sg.nseg - 1;
   volatile int* ab = &s.abort;
-  int* err = ta.err;
+  const int quad = warp & 3, r = 32 * quad + lane;         // TMEM lanes of the warp; row of the thread
+  const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
+  const int group = (warp >> 2) - 1, half = group & 1;
 
   if (warp == 0) {
     if (lane == 0) {
+      const int grp = h / (a.H / a.G);
       int issued = 0;
+#pragma unroll 1
       for (int c = 0; c < nch; ++c) {
         const int b = c & 1;
-        if (c >= 2 && !wait_or_abort(&s.empty[b], ((c >> 1) - 1) & 1, ab, err)) break;
+        if (c >= 2 && !wait_or_abort(&s.empty[b], ((c >> 1) - 1) & 1, ab)) break;
         const int row = sg.tok0 + c * Q;
         tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + 2 * nblk) * BLK));
         for (int k = 0; k < nblk; ++k) {
@@ -265,290 +409,307 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
-      constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
-      constexpr uint32_t i_u = i_yo | kIdescTransposeA;
-      bool ok = true;
-      auto cb = [&](int c) {  // CB = C B^T
-        const int b = c & 1;
-        ok = ok && wait_or_abort(&s.full[b], (c >> 1) & 1, ab, err);
-        if (!ok) return;
-        tc::tc_fence_after();
-        const uint64_t dc = tc::desc_k_sw128(s.C[b]), db = tc::desc_k_sw128(s.B[b]);
-        for (int k = 0; k < ksteps; ++k)
-          tc::mma_bf16(tmem + T_CB, tc::kstep32(dc, k, Q), tc::kstep32(db, k, Q), i_cb, k > 0);
-        tc::mma_commit(&s.cb_full);
-      };
-      if (nch > 0) cb(0);
-      for (int c = 0; c < nch && ok; ++c) {
-        const int b = c & 1;
-        // U = B^T (w x): the previous U has been read once w x of this chunk is there
-        ok = ok && wait_or_abort(&s.xw_full, c & 1, ab, err);
-        if (!ok) break;
-        tc::tc_fence_after();
+    constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
+    constexpr uint32_t i_yd = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    constexpr uint32_t i_yo = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB;
+    constexpr uint32_t i_u = i_yo | kIdescTransposeA;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]), d_w = desc_lo(s.xw[0]),
+                   d_s = desc_lo(s.S[0]);
+    // in 16-byte units: a stage of B or C, a block, a step of 16 K rows (MN-major)
+    constexpr uint32_t stage2 = 2 * BLK / 16, stage1 = BLK / 16, step = 2048 / 16;
+    // and of 16 K elements (K-major: 32 bytes, four of them a block)
+    auto kmaj = [](int k) { return (uint32_t)((k >> 2) * (BLK / 16) + (k & 3) * 2); };
+    bool ok = true;
+    auto cb = [&](int c) {  // CB = C B^T
+      const uint32_t b = c & 1;
+      ok = warp_wait(&s.full[b], (c >> 1) & 1, ab);
+      if (!ok) return;
+      tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t da = tc::desc_mn_sw128(s.B[b] + k * 2048, BLK, 1024);
-          tc::mma_bf16(tmem + T_U, da, tc::desc_mn_sw128(s.xw[0] + k * 2048, BLK, 1024), i_u, k > 0);
-          tc::mma_bf16(tmem + T_U, da, tc::desc_mn_sw128(s.xw[1] + k * 2048, BLK, 1024), i_u, 1);
-        }
-        tc::mma_commit(&s.u_full);
-        // Yo = C S0
-        ok = ok && wait_or_abort(&s.s_full, c & 1, ab, err);
-        if (c > 0) ok = ok && wait_or_abort(&s.y_empty, (c - 1) & 1, ab, err);
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint64_t dc = tc::desc_k_sw128(s.C[b]);
-        for (int k = 0; k < ksteps; ++k) {
-          tc::mma_bf16(tmem + T_YO, tc::kstep32(dc, k, Q), tc::desc_mn_sw128(s.S[0] + k * 2048, BLK, 1024), i_yo, k > 0);
-          tc::mma_bf16(tmem + T_YO, tc::kstep32(dc, k, Q), tc::desc_mn_sw128(s.S[1] + k * 2048, BLK, 1024), i_yo, 1);
-        }
-        // Yd = M x
-        ok = ok && wait_or_abort(&s.m_full, c & 1, ab, err);
-        if (!ok) break;
-        tc::tc_fence_after();
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps)
+          mma_ss(tmem + T_CB, d_c + b * stage2 + kmaj(k), d_b + b * stage2 + kmaj(k), i_cb, k > 0);
+      commit(&s.cb_full);
+    };
+    if (nch > 0) cb(0);
+#pragma unroll 1
+    for (int c = 0; c < nch && ok; ++c) {
+      const uint32_t b = c & 1;
+      // U = B^T (w x)
+      ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t dx = tc::desc_mn_sw128(s.X[b] + k * 2048, BLK, 1024);
-          tc::mma_f16_ta(tmem + T_YD, tmem + T_MH + 8 * k, dx, i_yo, k > 0);
-          tc::mma_f16_ta(tmem + T_YD, tmem + T_ML + 8 * k, dx, i_yo, 1);
-        }
-        tc::mma_commit(&s.y_full);
-        tc::mma_commit(&s.empty[b]);
-        if (c + 1 < nch) cb(c + 1);
+      for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
+      commit(&s.u_full);
+      // Yo = C S0
+      ok = warp_wait(&s.s_full, c & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
+      commit(&s.yo_full);
+      // Yd = M x
+      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
+        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, 1);
       }
-      // no MMA is in flight when the block ends
-      if (nch > 0) {
-        tc::mma_commit(&s.done);
-        tc::mbar_wait(&s.done, 0);
-      }
+      commit(&s.y_full);
+      commit(&s.empty[b]);
+      if (c + 1 < nch) cb(c + 1);
+    }
+    // no MMA is in flight when the block ends
+    if (nch > 0) {
+      commit(&s.done);
+      tc::mbar_wait(&s.done, 0);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    float dt[4], nx[4];
-    if (nch > 0) load_gates(a, h, sg.tok0, min(Q, sg.len), nx);
-    const float A = a.A[h] * LOG2E;
-    for (int c = 0; c < nch; ++c) {
+  } else if (warp < 4) {
+    // gates of the even (warp 2) and the odd chunks (warp 3)
+    float raw[4];
+    load_raw(a, h, sg.tok0 + (warp - 2) * Q, sg.len - (warp - 2) * Q, raw);
+    const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+#pragma unroll 1
+    for (int c = warp - 2; c < nch; c += 2) {
       const int b = c & 1;
+      float dt[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dt[i] = nx[i];
-      if (c + 1 < nch) load_gates(a, h, sg.tok0 + (c + 1) * Q, min(Q, sg.len - (c + 1) * Q), nx);
-      float g[4], r[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
+      for (int i = 0; i < 4; ++i) dt[i] = 4 * lane + i < sg.len - c * Q ? activate(a, raw[i] + bias) : 0.f;
+      load_raw(a, h, sg.tok0 + (c + 2) * Q, sg.len - (c + 2) * Q, raw);
+      float g[4], r4[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
       float run = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         run = fmaf(dt[i], A, run);
         g[i] = run;
       }
-      float before = __shfl_up_sync(0xffffffffu, scan_up(run, lane), 1);
-      float after = __shfl_down_sync(0xffffffffu, scan_down(run, lane), 1);
-      if (lane == 0) before = 0.f;
-      if (lane == 31) after = 0.f;
+      float before, after;
+      scan_both(run, lane, before, after);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] += before;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
-        r[i] = after;
+        r4[i] = after;
         after = fmaf(dt[i], A, after);
       }
       const float blk_end = __shfl_sync(0xffffffffu, g[3], lane | 7);
-      const float4 w = make_float4(dt[0] * exp2f(r[0]), dt[1] * exp2f(r[1]), dt[2] * exp2f(r[2]), dt[3] * exp2f(r[3]));
-      const float4 cf = make_float4(dt[0] * exp2f(blk_end - g[0]), dt[1] * exp2f(blk_end - g[1]),
-                                    dt[2] * exp2f(blk_end - g[2]), dt[3] * exp2f(blk_end - g[3]));
-      bool ok = c == 0 || wait_or_abort(&s.xw_full, (c - 1) & 1, ab, err);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      const float4 w = make_float4(dt[0] * ex2(r4[0]), dt[1] * ex2(r4[1]), dt[2] * ex2(r4[2]), dt[3] * ex2(r4[3]));
+      const float4 cf = make_float4(dt[0] * ex2(blk_end - g[0]), dt[1] * ex2(blk_end - g[1]),
+                                    dt[2] * ex2(blk_end - g[2]), dt[3] * ex2(blk_end - g[3]));
+      bool ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
+      if (!ok) break;
       *reinterpret_cast<float4*>(&s.w[4 * lane]) = w;
-      if (lane == 31) s.gam = exp2f(g[3]);
-      arrive(&s.w_full);
-      ok = c == 0 || wait_or_abort(&s.m_full, (c - 1) & 1, ab, err);
-      if (c >= 2) ok = ok && wait_or_abort(&s.empty[b], ((c >> 1) - 1) & 1, ab, err);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      warp_arrive(&s.w_full);
+      ok = c == 0 || warp_wait(&s.m_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
+      if (c >= 2) ok = ok && warp_wait(&s.empty[b], ((c >> 1) - 1) & 1, ab);
+      if (!ok) break;
+      if (lane == 31) s.gam[b] = ex2(g[3]);
       *reinterpret_cast<float4*>(&s.gc[b][4 * lane]) = make_float4(g[0], g[1], g[2], g[3]);
       *reinterpret_cast<float4*>(&s.dt[4 * lane]) = make_float4(dt[0], dt[1], dt[2], dt[3]);
       *reinterpret_cast<float4*>(&s.colf[4 * lane]) = cf;
-      arrive(&s.gates[b]);
+      warp_arrive(&s.gates[b]);
     }
-  } else if (warp >= 4 && warp < 8) {
-    // M: thread = row i; column blocks b < w by factors, b == w directly, b > w zero
-    const int w = warp - 4, i = 32 * w + lane;
-    const uint32_t row = tmem + ((uint32_t)(32 * w) << 16);
-    {
-      uint32_t z[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) z[q] = 0u;
-      for (int b = w + 1; b < 4; ++b) {
-        tc::tmem_st16(row + T_MH + 16 * b, z);
-        tc::tmem_st16(row + T_ML + 16 * b, z);
-      }
-      tc::tmem_wait_st();
-    }
+  } else if (group == 0 || group == 1) {
+    // M: thread = row r; column blocks b < quad by factors, b == quad directly, b > quad zero
+    const int j0 = 16 * half;
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
-      bool ok = wait_or_abort(&s.gates[st], (c >> 1) & 1, ab, err) && wait_or_abort(&s.cb_full, c & 1, ab, err);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      bool ok = warp_wait(&s.gates[st], (c >> 1) & 1, ab) && warp_wait(&s.cb_full, c & 1, ab);
+      if (!ok) break;
       tc::tc_fence_after();
       const float* gc = s.gc[st];
-      const float gi = gc[i];
-      for (int b = 0; b <= w; ++b) {
-        uint32_t v[32], hi[16], lo[16];
-        tc::tmem_ld32(row + T_CB + 32 * b, v);
-        const float rf = ex2(gi - gc[32 * b + 31]);
-        tc::tmem_wait_ld();
-        if (b < w) {
+      const float gi = gc[r];
+#pragma unroll 1
+      for (int b = 0; b <= quad; ++b) {
+        uint32_t v[16], hi[8], lo[8];
+        tc::tmem_ld16(trow + T_CB + 32 * b + j0, v);
+        if (b < quad) {
+          const float rf = ex2(gi - gc[32 * b + 31]);
+          const uint64_t rr = pack2(rf, rf);
+          wait_ld(v);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 cf = *reinterpret_cast<const float4*>(&s.colf[32 * b + j]);
-            split2(__uint_as_float(v[j]) * (cf.x * rf), __uint_as_float(v[j + 1]) * (cf.y * rf), hi[j / 2], lo[j / 2]);
-            split2(__uint_as_float(v[j + 2]) * (cf.z * rf), __uint_as_float(v[j + 3]) * (cf.w * rf), hi[j / 2 + 1],
+          for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 cf = *reinterpret_cast<const ulonglong2*>(&s.colf[32 * b + j0 + j]);
+            split2(mul2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), mul2(cf.x, rr)), hi[j / 2], lo[j / 2]);
+            split2(mul2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), mul2(cf.y, rr)), hi[j / 2 + 1],
                    lo[j / 2 + 1]);
           }
         } else {
+          float f[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 gj = *reinterpret_cast<const float2*>(&gc[32 * b + j]);
-            const float2 dj = *reinterpret_cast<const float2*>(&s.dt[32 * b + j]);
-            const float m0 = j <= lane ? __uint_as_float(v[j]) * (dj.x * ex2(gi - gj.x)) : 0.f;
-            const float m1 = j + 1 <= lane ? __uint_as_float(v[j + 1]) * (dj.y * ex2(gi - gj.y)) : 0.f;
-            split2(m0, m1, hi[j / 2], lo[j / 2]);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 gj = *reinterpret_cast<const float4*>(&gc[32 * b + j0 + j]);
+            const float4 dj = *reinterpret_cast<const float4*>(&s.dt[32 * b + j0 + j]);
+            f[j] = dj.x * ex2(gi - gj.x);
+            f[j + 1] = dj.y * ex2(gi - gj.y);
+            f[j + 2] = dj.z * ex2(gi - gj.z);
+            f[j + 3] = dj.w * ex2(gi - gj.w);
+          }
+          wait_ld(v);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float m0 = j0 + j <= lane ? __uint_as_float(v[j]) * f[j] : 0.f;
+            const float m1 = j0 + j + 1 <= lane ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f;
+            split2(pack2(m0, m1), hi[j / 2], lo[j / 2]);
           }
         }
-        // the previous chunk's Yd has read M
-        if (b == 0 && c > 0) {
-          ok = wait_or_abort(&s.y_full, (c - 1) & 1, ab, err);
-          tc::tc_fence_after();
-        }
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc::tmem_st16(row + T_MH + 16 * b, hi);
-        tc::tmem_st16(row + T_ML + 16 * b, lo);
+        // over the columns just read
+        tmem_st8(trow + T_CB + 32 * b + j0, hi);
+        tmem_st8(trow + T_CB + 32 * b + j0 + 8, lo);
       }
-      if (!ok) break;
+#pragma unroll 1
+      for (int b = quad + 1; b < 4; ++b) {
+        const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        tmem_st8(trow + T_CB + 32 * b + j0, z);
+        tmem_st8(trow + T_CB + 32 * b + j0 + 8, z);
+      }
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      arrive(&s.m_full);
+      warp_arrive(&s.m_full[st]);
     }
-  } else if (warp >= 8 && warp < 12) {
-    // w x of token row j, and state row n (both 32 (warp - 8) + lane)
-    const int j = tid - 256, n = j;
-    const uint32_t row = tmem + ((uint32_t)(32 * (warp - 8)) << 16);
-    float S[PT];
+  } else if (group == 2 || group == 3) {
+    // state row n = r, columns p0 + 32 half + [0, 32)
+    const int pc = p0 + 32 * half;
+    uint64_t S[16];
     const float* start = nullptr;
-    if (sg.idx > 0) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + n) * a.P + p0;
-    else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + n) * a.P + p0;
+    if (sg.idx > 0) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
+    else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
-    for (int p = 0; p < PT; p += 4) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (start && n < a.NS && p0 + p < a.P) v = *reinterpret_cast<const float4*>(start + p);
-      S[p] = v.x;
-      S[p + 1] = v.y;
-      S[p + 2] = v.z;
-      S[p + 3] = v.w;
+    for (int q = 0; q < 16; q += 2) {
+      ulonglong2 v = make_ulonglong2(0, 0);
+      if (start && r < a.NS && pc + 2 * q < a.P) v = *reinterpret_cast<const ulonglong2*>(start + 2 * q);
+      S[q] = v.x;
+      S[q + 1] = v.y;
     }
     float gam = 0.f;
     bool ok = true;
     auto advance = [&](int c) {  // S = gam S + U of chunk c
-      ok = ok && wait_or_abort(&s.u_full, c & 1, ab, err);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(&s.u_full, c & 1, ab);
       if (!ok) return;
       tc::tc_fence_after();
+      const uint64_t gg = pack2(gam, gam), one = pack2(1.f, 1.f);
 #pragma unroll
-      for (int p = 0; p < PT; p += 32) {
-        uint32_t u[32];
-        tc::tmem_ld32(row + T_U + p, u);
-        tc::tmem_wait_ld();
+      for (int p = 0; p < 32; p += 8) {
+        uint32_t u[8], v[8];
+        tmem_ld8(trow + T_U + 32 * half + p, u);
+        tmem_ld8(trow + T_U + PT + 32 * half + p, v);
+        wait_ld(u);
+        wait_ld(v);
 #pragma unroll
-        for (int q = 0; q < 32; ++q) S[p + q] = fmaf(gam, S[p + q], __uint_as_float(u[q]));
+        for (int q = 0; q < 4; ++q)
+          S[p / 2 + q] = fma2(gg, S[p / 2 + q], fma2(one, pair_of(u + 2 * q), pair_of(v + 2 * q)));
       }
       tc::tc_fence_before();
+      warp_arrive(&s.u_empty);
     };
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
-      const int b = c & 1, len = min(Q, sg.len - c * Q);
+      const int b = c & 1;
       if (c > 0) advance(c - 1);
-      ok = ok && wait_or_abort(&s.full[b], (c >> 1) & 1, ab, err);
-      ok = ok && wait_or_abort(&s.w_full, c & 1, ab, err);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (j >= len) {
-        clear_row(s.X[b], j);
-        for (int k = 0; k < nblk; ++k) clear_row(s.B[b] + k * BLK, j);
-      }
-      gam = s.gam;
-      build_xw(s.X[b], s.xw[0], s.xw[1], j, s.w[j]);
-      tc::fence_proxy_async();
-      arrive(&s.xw_full);
-      // S0 as operand, once the previous chunk's Yo has read the old one
-      if (c > 0) ok = wait_or_abort(&s.y_full, (c - 1) & 1, ab, err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      uint4 hi[4], lo[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint4 hi, lo;
-        split2(S[8 * q], S[8 * q + 1], hi.x, lo.x);
-        split2(S[8 * q + 2], S[8 * q + 3], hi.y, lo.y);
-        split2(S[8 * q + 4], S[8 * q + 5], hi.z, lo.z);
-        split2(S[8 * q + 6], S[8 * q + 7], hi.w, lo.w);
-        *reinterpret_cast<uint4*>(s.S[0] + piece(n, q)) = hi;
-        *reinterpret_cast<uint4*>(s.S[1] + piece(n, q)) = lo;
+      for (int q = 0; q < 4; ++q) {
+        split2(S[4 * q], hi[q].x, lo[q].x);
+        split2(S[4 * q + 1], hi[q].y, lo[q].y);
+        split2(S[4 * q + 2], hi[q].z, lo[q].z);
+        split2(S[4 * q + 3], hi[q].w, lo[q].w);
+      }
+      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab);
+      // the previous chunk's Yo has read the operand
+      if (c > 0) ok = ok && warp_wait(&s.yo_full, (c - 1) & 1, ab);
+      if (!ok) break;
+      gam = s.gam[b];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        *reinterpret_cast<uint4*>(s.S[0] + piece(r, 4 * half + q)) = hi[q];
+        *reinterpret_cast<uint4*>(s.S[1] + piece(r, 4 * half + q)) = lo[q];
       }
       tc::fence_proxy_async();
-      arrive(&s.s_full);
+      warp_arrive(&s.s_full);
     }
     if (ok && nch > 0) advance(nch - 1);
-    if (ok && last_seg && a.ht && n < a.NS) {
-      float* to = a.ht + (((int64_t)sg.doc * a.H + h) * a.NS + n) * a.P + p0;
+    if (ok && sg.idx == sg.nseg - 1 && a.ht && r < a.NS) {
+      float* to = a.ht + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
-      for (int p = 0; p < PT; p += 4)
-        if (p0 + p < a.P) *reinterpret_cast<float4*>(to + p) = make_float4(S[p], S[p + 1], S[p + 2], S[p + 3]);
+      for (int q = 0; q < 16; q += 2)
+        if (pc + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
     }
-  } else if (warp >= 12) {
-    // outputs of token row i
-    const int w = warp - 12, i = 32 * w + lane;
-    const uint32_t row = tmem + ((uint32_t)(32 * w) << 16);
+  } else if (group == 4 || group == 5) {
+    // w x and the outputs of token row r, columns p0 + 32 half + [0, 32)
+    const int pc = p0 + 32 * half;
     const float D = a.D ? a.D[h] : 0.f;
-    for (int c = 0; c < nch; ++c) {
-      const int b = c & 1, len = min(Q, sg.len - c * Q);
-      bool ok = wait_or_abort(&s.full[b], (c >> 1) & 1, ab, err);
-      ok = ok && wait_or_abort(&s.gates[b], (c >> 1) & 1, ab, err);
-      ok = ok && wait_or_abort(&s.y_full, c & 1, ab, err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc::tc_fence_after();
-      const float e = ex2(s.gc[b][i]);
-      __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + i) * a.H + h) * a.P + p0;
-#pragma unroll
-      for (int p = 0; p < PT; p += 32) {
-        uint32_t yo[32], yd[32];
-        tc::tmem_ld32(row + T_YO + p, yo);
-        tc::tmem_ld32(row + T_YD + p, yd);
-        tc::tmem_wait_ld();
-        if (p + 32 == PT) {
-          tc::tc_fence_before();
-          arrive(&s.y_empty);
-        }
-#pragma unroll
-        for (int q = 0; q < 32; q += 8) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(s.X[b] + piece(i, (p + q) / 8));
-          const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int k = q + 2 * z;
-            const float y0 = fmaf(D, bf_lo(xs[z]), fmaf(e, __uint_as_float(yo[k]), __uint_as_float(yd[k])));
-            const float y1 = fmaf(D, bf_hi(xs[z]), fmaf(e, __uint_as_float(yo[k + 1]), __uint_as_float(yd[k + 1])));
-            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
-            o[z] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          if (i < len && p0 + p + q < a.P)
-            *reinterpret_cast<uint4*>(out + p + q) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+    const uint64_t DD = pack2(D, D);
+    bool ok = true;
+    auto make_xw = [&](int c) {
+      const int b = c & 1, len = sg.len - c * Q;
+      ok = warp_wait(&s.full[b], (c >> 1) & 1, ab) && warp_wait(&s.w_full, c & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.u_full, (c - 1) & 1, ab);  // the previous U has read the operand
+      if (!ok) return;
+      if (r >= len) {
+        clear_pieces<4>(s.X[b], r, 4 * half);
+        if (half < nblk) clear_pieces<8>(s.B[b] + half * BLK, r, 0);
       }
-      arrive(&s.empty[b]);
+      build_xw<4>(s.X[b], s.xw[0], s.xw[1], r, 4 * half, s.w[r]);
+      tc::fence_proxy_async();
+      warp_arrive(&s.xw_full[b]);
+    };
+    if (nch > 0) make_xw(0);
+#pragma unroll 1
+    for (int c = 0; c < nch && ok; ++c) {
+      const int b = c & 1, len = sg.len - c * Q;
+      if (c + 1 < nch) make_xw(c + 1);
+      ok = ok && warp_wait(&s.gates[b], (c >> 1) & 1, ab) && warp_wait(&s.y_full, c & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const float e = ex2(s.gc[b][r]);
+      const uint64_t ee = pack2(e, e);
+      uint4 o[4];
+#pragma unroll
+      for (int p = 0; p < 32; p += 8) {
+        uint32_t yh[8], yl[8], yd[8];
+        tmem_ld8(trow + T_YO + 32 * half + p, yh);
+        tmem_ld8(trow + T_YO + PT + 32 * half + p, yl);
+        tmem_ld8(trow + T_YD + 32 * half + p, yd);
+        const uint4 xv = *reinterpret_cast<const uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
+        wait_ld(yh);
+        wait_ld(yl);
+        wait_ld(yd);
+        uint32_t y[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          float y0, y1;
+          uint64_t v = fma2(ee, pair_of(yl + 2 * z), pair_of(yd + 2 * z));
+          v = fma2(ee, pair_of(yh + 2 * z), v);
+          unpack2(fma2(DD, widen2(xs[z]), v), y0, y1);
+          const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
+          y[z] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        o[p / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      tc::tc_fence_before();
+      warp_arrive(&s.y_empty);
+      if (lane == 0) arrive(&s.empty[b]);
+      if (r < len) {
+        __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (pc + 8 * q < a.P) *reinterpret_cast<uint4*>(out + 8 * q) = o[q];
+      }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s.abort) atomicExch(ta.err, 10);
   if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
 
@@ -574,7 +735,8 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   extern __shared__ __align__(1024) unsigned char ssm_smem[];
   SumSmem& s = *reinterpret_cast<SumSmem*>(ssm_smem);
   const SsmArgs& a = ta.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per = a.H * ta.pblocks;
   const int hp = blockIdx.x % per, h = hp / ta.pblocks, p0 = (hp % ta.pblocks) * PT, sid = blockIdx.x / per;
   const int grp = h / (a.H / a.G);
@@ -587,8 +749,8 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&s.full[i], 1);
         tc::mbar_init(&s.empty[i], 1);
-        tc::mbar_init(&s.gates[i], 32);
-        tc::mbar_init(&s.xw_full[i], 128);
+        tc::mbar_init(&s.gates[i], 1);
+        tc::mbar_init(&s.xw_full[i], 4);
       }
       tc::mbar_init(&s.done, 1);
       tc::mbar_fence_init();
@@ -598,7 +760,7 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   const Seg sg = s.seg;
   if (sg.idx == sg.nseg - 1) return;  // no segment starts from this one's end
   if (warp == 1) {
-    tc::tmem_alloc(&s.tmem, 64);
+    tc::tmem_alloc(&s.tmem, 128);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
@@ -607,14 +769,14 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   const uint32_t tmem = s.tmem;
   const int nch = sg.len / Q;  // a segment that is not its document's last holds whole chunks
   volatile int* ab = &s.abort;
-  int* err = ta.err;
 
   if (warp == 0) {
     if (lane == 0) {
       int issued = 0;
+#pragma unroll 1
       for (int k = 0; k < nch; ++k) {
         const int b = k & 1, row = sg.tok0 + (nch - 1 - k) * Q;
-        if (k >= 2 && !wait_or_abort(&s.empty[b], ((k >> 1) - 1) & 1, ab, err)) break;
+        if (k >= 2 && !wait_or_abort(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
         tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + nblk) * BLK));
         for (int q = 0; q < nblk; ++q) tc::tma_load_3d(s.B[b] + q * BLK, &ta.b_map, 64 * q, grp, row, &s.full[b]);
         tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.full[b]);
@@ -624,62 +786,62 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t i_u = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB | kIdescTransposeA;
-      for (int k = 0; k < nch; ++k) {
-        const int b = k & 1;
-        if (!wait_or_abort(&s.xw_full[b], (k >> 1) & 1, ab, err)) break;
-        tc::tc_fence_after();
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0][0]);
+    constexpr uint32_t stage2 = 2 * BLK / 16, step = 2048 / 16;
+#pragma unroll 1
+    for (int k = 0; k < nch; ++k) {
+      const uint32_t b = k & 1;
+      if (!warp_wait(&s.xw_full[b], (k >> 1) & 1, ab)) break;
+      tc::tc_fence_after();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint64_t da = tc::desc_mn_sw128(s.B[b] + q * 2048, BLK, 1024);
-          tc::mma_bf16(tmem, da, tc::desc_mn_sw128(s.xw[b][0] + q * 2048, BLK, 1024), i_u, k + q > 0);
-          tc::mma_bf16(tmem, da, tc::desc_mn_sw128(s.xw[b][1] + q * 2048, BLK, 1024), i_u, 1);
-        }
-        tc::mma_commit(&s.empty[b]);
-      }
-      tc::mma_commit(&s.done);
-      tc::mbar_wait(&s.done, 0);
+      for (int q = 0; q < 8; ++q)
+        mma_ss(tmem, d_b + b * stage2 + q * step, d_w + b * stage2 + q * step, i_u, k + q > 0);
+      commit(&s.empty[b]);
     }
+    commit(&s.done);
+    tc::mbar_wait(&s.done, 0);
     __syncwarp();
   } else if (warp == 2) {
     const float A = a.A[h] * LOG2E;
-    float tail = 0.f, dt[4], nx[4];  // the gates after this chunk
-    if (nch > 0) load_gates(a, h, sg.tok0 + (nch - 1) * Q, Q, nx);
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    float tail = 0.f, dt[4], raw[4];  // tail: the gates after this chunk
+    if (nch > 0) load_raw(a, h, sg.tok0 + (nch - 1) * Q, Q, raw);
+#pragma unroll 1
     for (int k = 0; k < nch; ++k) {
       const int b = k & 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dt[i] = nx[i];
-      if (k + 1 < nch) load_gates(a, h, sg.tok0 + (nch - 2 - k) * Q, Q, nx);
-      const bool ok = k < 2 || wait_or_abort(&s.empty[b], ((k >> 1) - 1) & 1, ab, err);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      for (int i = 0; i < 4; ++i) dt[i] = activate(a, raw[i] + bias);
+      if (k + 1 < nch) load_raw(a, h, sg.tok0 + (nch - 2 - k) * Q, Q, raw);
+      if (k >= 2 && !warp_wait(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
       const float run = ((dt[0] + dt[1]) + (dt[2] + dt[3])) * A;
-      const float inc = scan_down(run, lane);
-      float after = __shfl_down_sync(0xffffffffu, inc, 1);
-      after = (lane == 31 ? 0.f : after) + tail;
+      float before, after;
+      scan_both(run, lane, before, after);
+      const float inc = __shfl_sync(0xffffffffu, run + after, 0);
+      after += tail;
       float4 v;
-      v.w = dt[3] * exp2f(after);
+      v.w = dt[3] * ex2(after);
       after = fmaf(dt[3], A, after);
-      v.z = dt[2] * exp2f(after);
+      v.z = dt[2] * ex2(after);
       after = fmaf(dt[2], A, after);
-      v.y = dt[1] * exp2f(after);
+      v.y = dt[1] * ex2(after);
       after = fmaf(dt[1], A, after);
-      v.x = dt[0] * exp2f(after);
+      v.x = dt[0] * ex2(after);
       *reinterpret_cast<float4*>(&s.w[b][4 * lane]) = v;
-      tail += __shfl_sync(0xffffffffu, inc, 0);
-      arrive(&s.gates[b]);
+      tail += inc;
+      warp_arrive(&s.gates[b]);
     }
     if (lane == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
   } else if (warp >= 4) {
     const int g = (warp - 4) >> 2, j = (tid - 128) & 127;
+#pragma unroll 1
     for (int k = g; k < nch; k += 2) {
-      bool ok = wait_or_abort(&s.full[g], (k >> 1) & 1, ab, err);
-      ok = ok && wait_or_abort(&s.gates[g], (k >> 1) & 1, ab, err);
-      if (k >= 2) ok = ok && wait_or_abort(&s.empty[g], ((k >> 1) - 1) & 1, ab, err);
+      bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab) && warp_wait(&s.gates[g], (k >> 1) & 1, ab);
+      if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
       if (!ok) break;
-      build_xw(s.X[g], s.xw[g][0], s.xw[g][1], j, s.w[g][j]);
+      build_xw<8>(s.X[g], s.xw[g][0], s.xw[g][1], j, 0, s.w[g][j]);
       tc::fence_proxy_async();
-      arrive(&s.xw_full[g]);
+      warp_arrive(&s.xw_full[g]);
     }
   }
   __syncthreads();
@@ -689,20 +851,25 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     const uint32_t row = tmem + ((uint32_t)(32 * (warp - 4)) << 16);
     float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + n) * a.P + p0;
 #pragma unroll
-    for (int p = 0; p < PT; p += 32) {
-      uint32_t u[32];
-      tc::tmem_ld32(row + p, u);
-      tc::tmem_wait_ld();
+    for (int p = 0; p < PT; p += 16) {
+      uint32_t u[16], v[16];
+      tc::tmem_ld16(row + p, u);
+      tc::tmem_ld16(row + PT + p, v);
+      wait_ld(u);
+      wait_ld(v);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) + __uint_as_float(v[q]));
       if (n < a.NS) {
 #pragma unroll
-        for (int q = 0; q < 32; q += 4)
+        for (int q = 0; q < 16; q += 4)
           if (p0 + p + q < a.P) *reinterpret_cast<uint4*>(to + p + q) = make_uint4(u[q], u[q + 1], u[q + 2], u[q + 3]);
       }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 1) tc::tmem_dealloc(tmem, 64);
+  if (tid == 0 && s.abort) atomicExch(ta.err, 10);
+  if (warp == 1) tc::tmem_dealloc(tmem, 128);
 }
 
 // The start states of split documents' segments, in place of the segments' own
