@@ -13,10 +13,8 @@
 // few 1e-6, and the outputs' error stays that of their own rounding).  The state
 // itself stays in FP32 registers.
 //
-// exp(G_i - G_j) is formed per 32-column block of M: for rows below the block
-// as exp(G_i - G_r) exp(G_r - G_j) with r the block's last token (both factors
-// at most 1, so neither overflows, and one that underflows belongs to a product
-// that does), inside the diagonal block directly.
+// exp(G_i - G_j) is formed from the difference, at most 1 on and below the
+// diagonal; what is above is dropped by selection.
 //
 // A chunk's tiles land by TMA; rows past the document's end are cleared, since
 // they hold another document's values (a NaN there would pass through a zero
@@ -305,35 +303,35 @@ __device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* 
 }
 
 // ---------------------------------------------------------------------------
-// The walk: one block per (segment, head, 64 columns of the state).  One warp
-// for TMA, one for MMA issue, one for the gates, and six groups of four warps:
-//   groups 0, 1: M from CB (16 of each 32 columns each)
+// The walk: one block per (segment, head, 64 columns of the state).
+//   warp 0: TMA, and the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
+//   warps 2, 3: the gates of the even and the odd chunks
+//   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
 //   groups 2, 3: the state (32 columns each)
 //   groups 4, 5: w x and the outputs (32 columns each)
 // Every role runs through the chunks on its own; barriers hand the buffers
-// over.  Per chunk the MMA warp issues U, Yo, Yd and the next chunk's CB.  An MMA
-// of 64 columns takes as long to issue as one of 128, and reads A as often: the
-// hi and lo operands of U and Yo sit side by side as one of 128 columns.
+// over.  CB (and M, written over it) has two buffers, so that M of one chunk
+// follows M of the last without waiting for their products.  An MMA of 64
+// columns with both operands in shared memory reads A as often as one of 128:
+// U's hi and lo operands sit side by side as one of 128 columns.
 // ---------------------------------------------------------------------------
 constexpr int WALK_THREADS = 28 * 32;
-// TMEM columns: CB (16 of them a step of 16 K, over which M's hi and lo are
-// written, 8 columns each), Yo and U (hi products, lo products), Yd.
-constexpr uint32_t T_CB = 0, T_YO = 128, T_U = 256, T_YD = 384;
+// TMEM columns: CB twice (16 of them a step of 16 K, over which M's hi and lo
+// are written, 8 columns each), U (hi products, lo products), Yo, Yd.
+constexpr uint32_t T_CB = 0, T_U = 256, T_YO = 384, T_YD = 448;
 
 struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
   unsigned char xw[2][BLK];  // hi, lo
   unsigned char S[2][BLK];   // hi, lo
-  // One chunk's gates.  gc and gam are read until the chunk's end, the others
-  // only up to M and w x: single buffers (shared memory is full).
+  // A chunk's gates.
   float gc[2][Q];  // prefix sums of dt A log2(e)
-  float dt[Q];
-  float colf[Q];   // dt_j 2^(gc[end of j's 32-block] - gc_j)
+  float dt[2][Q];
   float w[Q];      // dt_j 2^(sum after j)
   float gam[2];    // 2^gc[last]
-  // by the chunk's parity where a role may wait a chunk apart from the others
-  uint64_t full[2], empty[2], gates[2], m_full[2], xw_full[2];
-  uint64_t w_full, cb_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done;
+  // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], gates[2], xw_full[2], cb_full[2], m_full[2];
+  uint64_t w_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -354,21 +352,23 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       s.seg = sg;
       s.abort = 0;
       for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&s.full[i], 1);
-        tc::mbar_init(&s.empty[i], 1 + 8);
+        tc::mbar_init(&s.bc_full[i], 1);
+        tc::mbar_init(&s.bc_empty[i], 2);
+        tc::mbar_init(&s.x_full[i], 1);
+        tc::mbar_init(&s.x_empty[i], 1 + 8);
         tc::mbar_init(&s.gates[i], 1);
-        tc::mbar_init(&s.m_full[i], 8);
         tc::mbar_init(&s.xw_full[i], 8);
+        tc::mbar_init(&s.cb_full[i], 1);
+        tc::mbar_init(&s.m_full[i], 8);
+        tc::mbar_init(&s.done[i], 1);
       }
       tc::mbar_init(&s.w_full, 1);
-      tc::mbar_init(&s.cb_full, 1);
       tc::mbar_init(&s.u_full, 1);
       tc::mbar_init(&s.u_empty, 8);
       tc::mbar_init(&s.s_full, 8);
       tc::mbar_init(&s.yo_full, 1);
-      tc::mbar_init(&s.y_full, 1);
+      tc::mbar_init(&s.y_full, 2);
       tc::mbar_init(&s.y_empty, 8);
-      tc::mbar_init(&s.done, 1);
       tc::mbar_fence_init();
     }
   }
@@ -386,54 +386,50 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   const int quad = warp & 3, r = 32 * quad + lane;         // TMEM lanes of the warp; row of the thread
   const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
   const int group = (warp >> 2) - 1, half = group & 1;
+  // descriptor address units (16 bytes): a stage of B or C, a block, a step of
+  // 16 K rows (MN-major); a step of 16 K elements (K-major: 32 bytes, four a block)
+  constexpr uint32_t stage2 = 2 * BLK / 16, stage1 = BLK / 16, step = 2048 / 16;
+  auto kmaj = [](int k) { return (uint32_t)((k >> 2) * (BLK / 16) + (k & 3) * 2); };
 
   if (warp == 0) {
-    if (lane == 0) {
-      const int grp = h / (a.H / a.G);
-      int issued = 0;
+    constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S[0]);
+    const int grp = h / (a.H / a.G);
+    int bc_issued = 0, x_issued = 0;
+    auto load_bc = [&](int c) {
+      const int b = c & 1, row = sg.tok0 + c * Q;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
 #pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
-        const int b = c & 1;
-        if (c >= 2 && !wait_or_abort(&s.empty[b], ((c >> 1) - 1) & 1, ab)) break;
-        const int row = sg.tok0 + c * Q;
-        tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + 2 * nblk) * BLK));
         for (int k = 0; k < nblk; ++k) {
-          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.full[b]);
-          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.full[b]);
+          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
+          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
         }
-        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.full[b]);
-        issued = c + 1;
       }
-      // no copy is in flight when the block ends
-      for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&s.full[c & 1], (c >> 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
-    constexpr uint32_t i_yd = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
-    constexpr uint32_t i_yo = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB;
-    constexpr uint32_t i_u = i_yo | kIdescTransposeA;
-    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]), d_w = desc_lo(s.xw[0]),
-                   d_s = desc_lo(s.S[0]);
-    // in 16-byte units: a stage of B or C, a block, a step of 16 K rows (MN-major)
-    constexpr uint32_t stage2 = 2 * BLK / 16, stage1 = BLK / 16, step = 2048 / 16;
-    // and of 16 K elements (K-major: 32 bytes, four of them a block)
-    auto kmaj = [](int k) { return (uint32_t)((k >> 2) * (BLK / 16) + (k & 3) * 2); };
-    bool ok = true;
-    auto cb = [&](int c) {  // CB = C B^T
-      const uint32_t b = c & 1;
-      ok = warp_wait(&s.full[b], (c >> 1) & 1, ab);
-      if (!ok) return;
-      tc::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < ksteps)
-          mma_ss(tmem + T_CB, d_c + b * stage2 + kmaj(k), d_b + b * stage2 + kmaj(k), i_cb, k > 0);
-      commit(&s.cb_full);
+      __syncwarp();
+      bc_issued = c + 1;
     };
-    if (nch > 0) cb(0);
+    auto load_x = [&](int c) {
+      const int b = c & 1;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
+        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, sg.tok0 + c * Q, &s.x_full[b]);
+      }
+      __syncwarp();
+      x_issued = c + 1;
+    };
+    if (nch > 0) {
+      load_x(0);
+      load_bc(0);
+    }
+    if (nch > 1) {
+      load_x(1);
+      load_bc(1);
+    }
+    bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < nch && ok; ++c) {
+    for (int c = 0; c < nch; ++c) {
       const uint32_t b = c & 1;
       // U = B^T (w x)
       ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
@@ -443,6 +439,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
       commit(&s.u_full);
+      if (c > 0 && c + 1 < nch) {
+        ok = warp_wait(&s.bc_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
+        if (!ok) break;
+        load_bc(c + 1);
+      }
       // Yo = C S0
       ok = warp_wait(&s.s_full, c & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
@@ -450,29 +451,69 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
+        if (k < ksteps) {
+          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
+          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + stage1 + k * step, i_yo, 1);
+        }
       commit(&s.yo_full);
+      commit(&s.y_full);
+      commit(&s.bc_empty[b]);
+      if (c > 0 && c + 1 < nch) {
+        ok = warp_wait(&s.x_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
+        if (!ok) break;
+        load_x(c + 1);
+      }
+    }
+    // no MMA and no copy is in flight when the block ends
+    if (nch > 0) {
+      commit(&s.done[0]);
+      tc::mbar_wait(&s.done[0], 0);
+    }
+#pragma unroll 1
+    for (int c = max(0, bc_issued - 2); c < bc_issued; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
+#pragma unroll 1
+    for (int c = max(0, x_issued - 2); c < x_issued; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
+    constexpr uint32_t i_yd = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]);
+    bool ok = true;
+#pragma unroll 1
+    for (int c = -1; c < nch; ++c) {
+      const uint32_t b = c & 1, n = b ^ 1;
+      if (c + 1 < nch) {  // CB = C B^T of the next chunk, once Yd has read the M in its columns
+        ok = warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
+        if (c > 0) ok = ok && warp_wait(&s.y_full, (c - 1) & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ksteps)
+            mma_ss(tmem + T_CB + 128 * n, d_c + n * stage2 + kmaj(k), d_b + n * stage2 + kmaj(k), i_cb, k > 0);
+        commit(&s.cb_full[n]);
+        commit(&s.bc_empty[n]);
+      }
+      if (c < 0) continue;
       // Yd = M x
-      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab);
+      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab) && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
-        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, 1);
+        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
+        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, 1);
       }
       commit(&s.y_full);
-      commit(&s.empty[b]);
-      if (c + 1 < nch) cb(c + 1);
+      commit(&s.x_empty[b]);
     }
-    // no MMA is in flight when the block ends
     if (nch > 0) {
-      commit(&s.done);
-      tc::mbar_wait(&s.done, 0);
+      commit(&s.done[1]);
+      tc::mbar_wait(&s.done[1], 0);
     }
     __syncwarp();
   } else if (warp < 4) {
-    // gates of the even (warp 2) and the odd chunks (warp 3)
     float raw[4];
     load_raw(a, h, sg.tok0 + (warp - 2) * Q, sg.len - (warp - 2) * Q, raw);
     const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -496,80 +537,62 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       for (int i = 0; i < 4; ++i) g[i] += before;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
-        r4[i] = after;
+        r4[i] = dt[i] * ex2(after);
         after = fmaf(dt[i], A, after);
       }
-      const float blk_end = __shfl_sync(0xffffffffu, g[3], lane | 7);
-      const float4 w = make_float4(dt[0] * ex2(r4[0]), dt[1] * ex2(r4[1]), dt[2] * ex2(r4[2]), dt[3] * ex2(r4[3]));
-      const float4 cf = make_float4(dt[0] * ex2(blk_end - g[0]), dt[1] * ex2(blk_end - g[1]),
-                                    dt[2] * ex2(blk_end - g[2]), dt[3] * ex2(blk_end - g[3]));
-      bool ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
-      if (!ok) break;
-      *reinterpret_cast<float4*>(&s.w[4 * lane]) = w;
-      warp_arrive(&s.w_full);
-      ok = c == 0 || warp_wait(&s.m_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
-      if (c >= 2) ok = ok && warp_wait(&s.empty[b], ((c >> 1) - 1) & 1, ab);
+      bool ok = c < 2 || warp_wait(&s.x_empty[b], ((c >> 1) - 1) & 1, ab);
       if (!ok) break;
       if (lane == 31) s.gam[b] = ex2(g[3]);
       *reinterpret_cast<float4*>(&s.gc[b][4 * lane]) = make_float4(g[0], g[1], g[2], g[3]);
-      *reinterpret_cast<float4*>(&s.dt[4 * lane]) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-      *reinterpret_cast<float4*>(&s.colf[4 * lane]) = cf;
+      *reinterpret_cast<float4*>(&s.dt[b][4 * lane]) = make_float4(dt[0], dt[1], dt[2], dt[3]);
       warp_arrive(&s.gates[b]);
+      ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
+      if (!ok) break;
+      *reinterpret_cast<float4*>(&s.w[4 * lane]) = make_float4(r4[0], r4[1], r4[2], r4[3]);
+      warp_arrive(&s.w_full);
     }
   } else if (group == 0 || group == 1) {
-    // M: thread = row r; column blocks b < quad by factors, b == quad directly, b > quad zero
+    // M: thread = row r; zero above the diagonal
     const int j0 = 16 * half;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
-      bool ok = warp_wait(&s.gates[st], (c >> 1) & 1, ab) && warp_wait(&s.cb_full, c & 1, ab);
+      bool ok = warp_wait(&s.gates[st], (c >> 1) & 1, ab) && warp_wait(&s.cb_full[st], (c >> 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
-      const float* gc = s.gc[st];
-      const float gi = gc[r];
+      const float gi = s.gc[st][r];
+      const uint32_t cb = trow + T_CB + 128 * st + j0;
 #pragma unroll 1
-      for (int b = 0; b <= quad; ++b) {
-        uint32_t v[16], hi[8], lo[8];
-        tc::tmem_ld16(trow + T_CB + 32 * b + j0, v);
-        if (b < quad) {
-          const float rf = ex2(gi - gc[32 * b + 31]);
-          const uint64_t rr = pack2(rf, rf);
-          wait_ld(v);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const ulonglong2 cf = *reinterpret_cast<const ulonglong2*>(&s.colf[32 * b + j0 + j]);
-            split2(mul2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), mul2(cf.x, rr)), hi[j / 2], lo[j / 2]);
-            split2(mul2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), mul2(cf.y, rr)), hi[j / 2 + 1],
-                   lo[j / 2 + 1]);
-          }
-        } else {
+      for (int b = 0; b < 4; ++b) {
+        uint32_t hi[8], lo[8];
+        if (b <= quad) {
+          uint32_t v[16];
+          tc::tmem_ld16(cb + 32 * b, v);
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const float4 gj = *reinterpret_cast<const float4*>(&gc[32 * b + j0 + j]);
-            const float4 dj = *reinterpret_cast<const float4*>(&s.dt[32 * b + j0 + j]);
+            const float4 gj = *reinterpret_cast<const float4*>(&s.gc[st][32 * b + j0 + j]);
+            const float4 dj = *reinterpret_cast<const float4*>(&s.dt[st][32 * b + j0 + j]);
             f[j] = dj.x * ex2(gi - gj.x);
             f[j + 1] = dj.y * ex2(gi - gj.y);
             f[j + 2] = dj.z * ex2(gi - gj.z);
             f[j + 3] = dj.w * ex2(gi - gj.w);
           }
           wait_ld(v);
+          const int last = b < quad ? 32 : lane - j0;  // the last column kept
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            const float m0 = j0 + j <= lane ? __uint_as_float(v[j]) * f[j] : 0.f;
-            const float m1 = j0 + j + 1 <= lane ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f;
+            const float m0 = j <= last ? __uint_as_float(v[j]) * f[j] : 0.f;
+            const float m1 = j + 1 <= last ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f;
             split2(pack2(m0, m1), hi[j / 2], lo[j / 2]);
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
         }
         // over the columns just read
-        tmem_st8(trow + T_CB + 32 * b + j0, hi);
-        tmem_st8(trow + T_CB + 32 * b + j0 + 8, lo);
-      }
-#pragma unroll 1
-      for (int b = quad + 1; b < 4; ++b) {
-        const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        tmem_st8(trow + T_CB + 32 * b + j0, z);
-        tmem_st8(trow + T_CB + 32 * b + j0 + 8, z);
+        tmem_st8(cb + 32 * b, hi);
+        tmem_st8(cb + 32 * b + 8, lo);
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
@@ -611,10 +634,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       warp_arrive(&s.u_empty);
     };
 #pragma unroll 1
-    for (int c = 0; c < nch; ++c) {
+    for (int c = 0; c <= nch; ++c) {
       const int b = c & 1;
       if (c > 0) advance(c - 1);
-      if (!ok) break;
+      if (!ok || c == nch) break;
       uint4 hi[4], lo[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -636,38 +659,37 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::fence_proxy_async();
       warp_arrive(&s.s_full);
     }
-    if (ok && nch > 0) advance(nch - 1);
     if (ok && sg.idx == sg.nseg - 1 && a.ht && r < a.NS) {
       float* to = a.ht + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
       for (int q = 0; q < 16; q += 2)
         if (pc + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
     }
-  } else if (group == 4 || group == 5) {
+  } else {
     // w x and the outputs of token row r, columns p0 + 32 half + [0, 32)
     const int pc = p0 + 32 * half;
     const float D = a.D ? a.D[h] : 0.f;
     const uint64_t DD = pack2(D, D);
     bool ok = true;
-    auto make_xw = [&](int c) {
-      const int b = c & 1, len = sg.len - c * Q;
-      ok = warp_wait(&s.full[b], (c >> 1) & 1, ab) && warp_wait(&s.w_full, c & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.u_full, (c - 1) & 1, ab);  // the previous U has read the operand
-      if (!ok) return;
-      if (r >= len) {
-        clear_pieces<4>(s.X[b], r, 4 * half);
-        if (half < nblk) clear_pieces<8>(s.B[b] + half * BLK, r, 0);
-      }
-      build_xw<4>(s.X[b], s.xw[0], s.xw[1], r, 4 * half, s.w[r]);
-      tc::fence_proxy_async();
-      warp_arrive(&s.xw_full[b]);
-    };
-    if (nch > 0) make_xw(0);
 #pragma unroll 1
-    for (int c = 0; c < nch && ok; ++c) {
+    for (int c = -1; c < nch; ++c) {
+      if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
+        const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
+        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab) &&
+             warp_wait(&s.w_full, (c + 1) & 1, ab);
+        if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
+        if (!ok) break;
+        if (r >= len) {
+          clear_pieces<4>(s.X[n], r, 4 * half);
+          if (half < nblk) clear_pieces<8>(s.B[n] + half * BLK, r, 0);
+        }
+        build_xw<4>(s.X[n], s.xw[0], s.xw[1], r, 4 * half, s.w[r]);
+        tc::fence_proxy_async();
+        warp_arrive(&s.xw_full[n]);
+      }
+      if (c < 0) continue;
       const int b = c & 1, len = sg.len - c * Q;
-      if (c + 1 < nch) make_xw(c + 1);
-      ok = ok && warp_wait(&s.gates[b], (c >> 1) & 1, ab) && warp_wait(&s.y_full, c & 1, ab);
+      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab) && warp_wait(&s.y_full, c & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
       const float e = ex2(s.gc[b][r]);
@@ -675,21 +697,18 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       uint4 o[4];
 #pragma unroll
       for (int p = 0; p < 32; p += 8) {
-        uint32_t yh[8], yl[8], yd[8];
-        tmem_ld8(trow + T_YO + 32 * half + p, yh);
-        tmem_ld8(trow + T_YO + PT + 32 * half + p, yl);
+        uint32_t yo[8], yd[8];
+        tmem_ld8(trow + T_YO + 32 * half + p, yo);
         tmem_ld8(trow + T_YD + 32 * half + p, yd);
         const uint4 xv = *reinterpret_cast<const uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
         const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-        wait_ld(yh);
-        wait_ld(yl);
+        wait_ld(yo);
         wait_ld(yd);
         uint32_t y[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           float y0, y1;
-          uint64_t v = fma2(ee, pair_of(yl + 2 * z), pair_of(yd + 2 * z));
-          v = fma2(ee, pair_of(yh + 2 * z), v);
+          const uint64_t v = fma2(ee, pair_of(yo + 2 * z), pair_of(yd + 2 * z));
           unpack2(fma2(DD, widen2(xs[z]), v), y0, y1);
           const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
           y[z] = *reinterpret_cast<const uint32_t*>(&t);
@@ -698,7 +717,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       }
       tc::tc_fence_before();
       warp_arrive(&s.y_empty);
-      if (lane == 0) arrive(&s.empty[b]);
+      if (lane == 0) arrive(&s.x_empty[b]);
       if (r < len) {
         __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
 #pragma unroll

@@ -1,0 +1,1065 @@
+// gdr_ssm_tc.cu -- the selective state space scan of prompts on the tensor
+// cores, in chunks of Q = 128 tokens that restart at each document.
+//
+// Inside a chunk with start state S0 [N][P], gates a_t = dt_t A, prefix sums
+// G_i = sum_{k<=i} a_k:
+//   out_i = exp(G_i) C_i S0 + sum_{j<=i} M_ij x_j + D x_i,
+//           M_ij = (C_i . B_j) exp(G_i - G_j) dt_j
+//   S_end = exp(G_last) S0 + B^T (w x),  w_j = dt_j exp(sum_{k>j} a_k)
+// Four products of 128-row tiles (tcgen05, FP32 accumulators in TMEM):
+//   CB = C B^T,  Yo = C S0,  Yd = M x,  U = B^T (w x).
+// x, B and C are BF16 and enter exactly; what is formed in FP32 (M, S0, w x)
+// enters as a pair of BF16 numbers hi + lo (17 bits: FP32 end states within a
+// few 1e-6, and the outputs' error stays that of their own rounding).  The state
+// itself stays in FP32 registers.
+//
+// exp(G_i - G_j) dt_j is formed as one exponential 2^(g_i - (g_j - log2 dt_j)),
+// whose exponent is at most log2 dt_j on and below the diagonal.
+//
+// A chunk's tiles land by TMA; rows past the document's end are cleared, since
+// they hold another document's values (a NaN there would pass through a zero
+// weight).  Within a document a non-finite value reaches the outputs of its
+// whole chunk.
+#include <algorithm>
+#include <cudaTypedefs.h>
+
+#include "gdr_ssm.cuh"
+#include "gdr_tc.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int Q = 128;        // tokens of a chunk
+constexpr int PT = 64;        // columns of the state that a block works on
+constexpr int BLK = Q * 128;  // bytes of a tile block: 128 rows of 64 BF16
+
+struct TcArgs {
+  CUtensorMap x_map, b_map, c_map;
+  SsmArgs a;
+  int pblocks;      // ceil(P / 64)
+  int lseg;         // chunks of a segment at most
+  float* seg;       // [segments][H][NS][P]: start states of split documents' segments
+  float* gsum;      // [segments][H]: log2 decay over each segment
+  int* err;
+};
+
+// The segment `idx` of document `doc`, its chunks [c0, c1) and tokens.
+struct Seg {
+  int doc, idx, nseg, tok0, len;  // first token and tokens of the segment
+  int first;                      // the document's first segment
+};
+
+// Finds segment `want` by a scan over the documents (one warp).
+__device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int want) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int d0 = 0; d0 < N; d0 += 32) {
+    const int d = d0 + lane;
+    int n = 0, start = 0, len = 0;
+    if (d < N) {
+      start = cu[d];
+      len = cu[d + 1] - start;
+      const int ch = (len + Q - 1) / Q;
+      n = ch == 0 ? 1 : (ch + lseg - 1) / lseg;
+    }
+    int pre = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, pre, m);
+      if (lane >= m) pre += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, pre, 31);
+    if (want < base + total) {
+      const unsigned hit = __ballot_sync(0xffffffffu, want < base + pre);
+      const int l = __ffs(hit) - 1;
+      Seg s;
+      s.doc = d0 + l;
+      s.nseg = __shfl_sync(0xffffffffu, n, l);
+      s.first = base + __shfl_sync(0xffffffffu, pre, l) - s.nseg;
+      s.idx = want - s.first;
+      const int dl = __shfl_sync(0xffffffffu, len, l), ds = __shfl_sync(0xffffffffu, start, l);
+      const int ch = (dl + Q - 1) / Q, per = ch / s.nseg, extra = ch % s.nseg;
+      // the first `extra` segments have one chunk more
+      const int c0 = s.idx * per + min(s.idx, extra), c1 = c0 + per + (s.idx < extra ? 1 : 0);
+      s.tok0 = ds + c0 * Q;
+      s.len = min(dl, c1 * Q) - c0 * Q;
+      return s;
+    }
+    base += total;
+  }
+  return Seg{0, 0, 1, 0, 0, 0};
+}
+
+// Waits of the blocks' roles.  Each gives up after kTries tries of at most a
+// microsecond, or once another role has, and returns false; the block then
+// reports the timeout as it ends.  Few instructions: the roles run straight
+// through long loops that share the instruction cache.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (int tries = 0; !try_phase(bar, parity); ++tries)
+    if (tries > kTries || *abort) {
+      *abort = 1;
+      return false;
+    }
+  return true;
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+constexpr uint32_t kIdescTransposeA = 1u << 15;
+
+// Byte of the 16-byte piece c (8 BF16) of row r of a 128-byte-swizzled block.
+__device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Pairs of FP32 operations as one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The two BF16 of a word as a pair of FP32.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(bf_lo(w), bf_hi(w)); }
+
+// A pair of FP32 numbers as BF16 pairs: hi rounded to nearest, lo the rest
+// rounded (off by at most 2^-18 of the number).
+__device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  unpack2(fma2(widen2(hi), pack2(-1.f, -1.f), v), a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a, b);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Shared-memory matrix descriptors of 128-byte-swizzled tiles share their upper
+// word (8-row groups 1024 bytes apart, descriptor version 1, the swizzle); the
+// lower word is the address in 16-byte units and, for MN-major tiles, the
+// distance of the 64-element blocks along MN.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(const void* tile) { return tc::smem_u32(tile) >> 4 | (BLK / 16) << 16; }
+
+// MMAs and commits that a whole warp walks through together and one elected
+// thread performs (the same one each time).  Measured: 36 clocks an MMA of 64
+// columns from TMEM and 53 from shared memory, its read time; picked by a
+// comparison of the lane instead, 72 for either.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+// The same values, known to be the same on every lane: what is computed from
+// them (loop bounds, operand addresses) can live in uniform registers.
+__device__ __forceinline__ Seg uniform(const Seg& s) {
+  Seg u;
+  u.doc = __shfl_sync(0xffffffffu, s.doc, 0);
+  u.idx = __shfl_sync(0xffffffffu, s.idx, 0);
+  u.nseg = __shfl_sync(0xffffffffu, s.nseg, 0);
+  u.tok0 = __shfl_sync(0xffffffffu, s.tok0, 0);
+  u.len = __shfl_sync(0xffffffffu, s.len, 0);
+  u.first = __shfl_sync(0xffffffffu, s.first, 0);
+  return u;
+}
+// One arrival for the warp, after all its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
+}
+// The wait of a whole warp: the same answer on every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (int tries = 0; !__all_sync(0xffffffffu, try_phase(bar, parity)); ++tries)
+    if (__any_sync(0xffffffffu, tries > kTries || *abort)) {
+      *abort = 1;
+      return false;
+    }
+  return true;
+}
+// tcgen05.wait::ld with the loaded registers as operands: nothing that reads
+// them can be scheduled before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+// Eight consecutive TMEM columns of the warp's lanes to registers (complete
+// after wait_ld).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) {
+  return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// Eight consecutive TMEM columns of the warp's lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Exclusive sums over the lanes before and after this one.
+__device__ __forceinline__ void scan_both(float v, int lane, float& before, float& after) {
+  float up = v, down = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, m), d = __shfl_down_sync(0xffffffffu, down, m);
+    if (lane >= m) up += u;
+    if (lane + m < 32) down += d;
+  }
+  up = __shfl_up_sync(0xffffffffu, up, 1);
+  down = __shfl_down_sync(0xffffffffu, down, 1);
+  before = lane == 0 ? 0.f : up;
+  after = lane == 31 ? 0.f : down;
+}
+
+// Lane l loads the raw dt of tokens 4 l .. 4 l + 3 (of `len`, which may be none).
+__device__ __forceinline__ void load_raw(const SsmArgs& a, int h, int tok0, int len, float (&dt)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = 4 * lane + i;
+    dt[i] = 0.f;
+    if (j < len) {
+      const int64_t at = (int64_t)(tok0 + j) * a.lddt + h;
+      dt[i] = a.dt_f32 ? static_cast<const float*>(a.dt)[at] : to_f(static_cast<const __nv_bfloat16*>(a.dt)[at]);
+    }
+  }
+}
+__device__ __forceinline__ float activate(const SsmArgs& a, float v) { return a.softplus ? softplus_f(v) : v; }
+
+// Pieces [c0, c0 + n) of row j of a tile block to zero.
+template <int N>
+__device__ __forceinline__ void clear_pieces(unsigned char* tile, int j, int c0) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) *reinterpret_cast<uint4*>(tile + piece(j, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// w_j x_j of token row j, pieces [c0, c0 + n), as hi and lo blocks.
+template <int N>
+__device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* hi, unsigned char* lo, int j, int c0,
+                                         float w) {
+  const uint64_t ww = pack2(w, w);
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const uint32_t at = piece(j, c0 + c);
+    const uint4 v = *reinterpret_cast<const uint4*>(x + at);
+    uint4 h, l;
+    split2(mul2(widen2(v.x), ww), h.x, l.x);
+    split2(mul2(widen2(v.y), ww), h.y, l.y);
+    split2(mul2(widen2(v.z), ww), h.z, l.z);
+    split2(mul2(widen2(v.w), ww), h.w, l.w);
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The walk: one block per (segment, head, 64 columns of the state).
+//   warp 0: TMA, and the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
+//   warps 2, 3: the gates of the even and the odd chunks
+//   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
+//   groups 2, 3: the state (32 columns each)
+//   groups 4, 5: w x and the outputs (32 columns each)
+// Every role runs through the chunks on its own; barriers hand the buffers
+// over.  CB (and M, written over it) has two buffers, so that M of one chunk
+// follows M of the last without waiting for their products.  An MMA of 64
+// columns with both operands in shared memory reads A as often as one of 128:
+// U's hi and lo operands sit side by side as one of 128 columns.
+// ---------------------------------------------------------------------------
+constexpr int WALK_THREADS = 28 * 32;
+// TMEM columns: CB twice (16 of them a step of 16 K, over which M's hi and lo
+// are written, 8 columns each), U (hi products, lo products), Yo, Yd.
+constexpr uint32_t T_CB = 0, T_U = 256, T_YO = 384, T_YD = 448;
+
+struct WalkSmem {
+  unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
+  unsigned char xw[2][BLK];  // hi, lo
+  unsigned char S[2][BLK];   // hi, lo
+  // A chunk's gates.
+  float gc[2][Q];  // prefix sums of dt A log2(e)
+  float gd[2][Q];  // gc - log2(dt): dt_j 2^(gc_i - gc_j) = 2^(gc_i - gd_j)
+  float w[Q];      // dt_j 2^(sum after j)
+  float gam[2];    // 2^gc[last]
+  // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], gates[2], xw_full[2], cb_full[2];
+  uint64_t w_full, m_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
+  uint32_t tmem;
+  int abort;
+  Seg seg;
+};
+
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_constant__ TcArgs ta) {
+  extern __shared__ __align__(1024) unsigned char ssm_smem[];  // tiles are swizzled in 1024-byte atoms
+  WalkSmem& s = *reinterpret_cast<WalkSmem*>(ssm_smem);
+  const SsmArgs& a = ta.a;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int per = a.H * ta.pblocks;
+  const int hp = blockIdx.x % per, h = hp / ta.pblocks, p0 = (hp % ta.pblocks) * PT, sid = blockIdx.x / per;
+  const int nblk = a.NS > 64 ? 2 : 1, ksteps = (a.NS + 15) / 16;
+  if (warp == 0) {
+    const Seg sg = find_segment(a.cu, a.N, ta.lseg, sid);
+    if (lane == 0) {
+      s.seg = sg;
+      s.abort = 0;
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&s.bc_full[i], 1);
+        tc::mbar_init(&s.bc_empty[i], 2);
+        tc::mbar_init(&s.x_full[i], 1);
+        tc::mbar_init(&s.x_empty[i], 1 + 8);
+        tc::mbar_init(&s.gates[i], 1);
+        tc::mbar_init(&s.xw_full[i], 8);
+        tc::mbar_init(&s.cb_full[i], 1);
+        tc::mbar_init(&s.done[i], 1);
+      }
+      tc::mbar_init(&s.w_full, 1);
+      tc::mbar_init(&s.m_full, 8);
+      tc::mbar_init(&s.u_full, 1);
+      tc::mbar_init(&s.u_empty, 8);
+      tc::mbar_init(&s.s_full, 8);
+      tc::mbar_init(&s.yo_full, 1);
+      tc::mbar_init(&s.y_full, 2);
+      tc::mbar_init(&s.y_empty, 8);
+      tc::mbar_fence_init();
+    }
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&s.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const Seg sg = uniform(s.seg);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+  const int nch = (sg.len + Q - 1) / Q;
+  volatile int* ab = &s.abort;
+  const int quad = warp & 3, r = 32 * quad + lane;         // TMEM lanes of the warp; row of the thread
+  const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
+  const int group = (warp >> 2) - 1, half = group & 1;
+  // descriptor address units (16 bytes): a stage of B or C, a block, a step of
+  // 16 K rows (MN-major); a step of 16 K elements (K-major: 32 bytes, four a block)
+  constexpr uint32_t stage2 = 2 * BLK / 16, stage1 = BLK / 16, step = 2048 / 16;
+  auto kmaj = [](int k) { return (uint32_t)((k >> 2) * (BLK / 16) + (k & 3) * 2); };
+
+  if (warp == 0) {
+    constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S[0]);
+    const int grp = h / (a.H / a.G);
+    int bc_issued = 0, x_issued = 0;
+    auto load_bc = [&](int c) {
+      const int b = c & 1, row = sg.tok0 + c * Q;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
+#pragma unroll 1
+        for (int k = 0; k < nblk; ++k) {
+          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
+          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
+        }
+      }
+      __syncwarp();
+      bc_issued = c + 1;
+    };
+    auto load_x = [&](int c) {
+      const int b = c & 1;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
+        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, sg.tok0 + c * Q, &s.x_full[b]);
+      }
+      __syncwarp();
+      x_issued = c + 1;
+    };
+    if (nch > 0) {
+      load_x(0);
+      load_bc(0);
+    }
+    if (nch > 1) {
+      load_x(1);
+      load_bc(1);
+    }
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      const uint32_t b = c & 1;
+      // U = B^T (w x)
+      ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
+      commit(&s.u_full);
+      if (c > 0 && c + 1 < nch) {
+        ok = warp_wait(&s.bc_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
+        if (!ok) break;
+        load_bc(c + 1);
+      }
+      // Yo = C S0
+      ok = warp_wait(&s.s_full, c & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps) {
+          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
+          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + stage1 + k * step, i_yo, 1);
+        }
+      commit(&s.yo_full);
+      commit(&s.y_full);
+      commit(&s.bc_empty[b]);
+      if (c > 0 && c + 1 < nch) {
+        ok = warp_wait(&s.x_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
+        if (!ok) break;
+        load_x(c + 1);
+      }
+    }
+    // no MMA and no copy is in flight when the block ends
+    if (nch > 0) {
+      commit(&s.done[0]);
+      tc::mbar_wait(&s.done[0], 0);
+    }
+#pragma unroll 1
+    for (int c = max(0, bc_issued - 2); c < bc_issued; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
+#pragma unroll 1
+    for (int c = max(0, x_issued - 2); c < x_issued; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
+    __syncwarp();
+  } else if (warp == 1 && ta.lseg == -5) {
+ return;
+ } else if (false) {
+    constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
+    constexpr uint32_t i_yd = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]);
+    bool ok = true;
+#pragma unroll 1
+    for (int c = -1; c < nch; ++c) {
+      const uint32_t b = c & 1, n = b ^ 1;
+      if (c + 1 < nch) {  // CB = C B^T of the next chunk, once Yd has read the M in its columns
+        ok = warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
+        if (c > 0) ok = ok && warp_wait(&s.y_full, (c - 1) & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ksteps)
+            mma_ss(tmem + T_CB + 128 * n, d_c + n * stage2 + kmaj(k), d_b + n * stage2 + kmaj(k), i_cb, k > 0);
+        commit(&s.cb_full[n]);
+        commit(&s.bc_empty[n]);
+      }
+      if (c < 0) continue;
+      // Yd = M x
+      ok = warp_wait(&s.m_full, c & 1, ab) && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
+        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, 1);
+      }
+      commit(&s.y_full);
+      commit(&s.x_empty[b]);
+    }
+    if (nch > 0) {
+      commit(&s.done[1]);
+      tc::mbar_wait(&s.done[1], 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    float raw[4];
+    load_raw(a, h, sg.tok0 + (warp - 2) * Q, sg.len - (warp - 2) * Q, raw);
+    const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+#pragma unroll 1
+    for (int c = warp - 2; c < nch; c += 2) {
+      const int b = c & 1;
+      float dt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dt[i] = 4 * lane + i < sg.len - c * Q ? activate(a, raw[i] + bias) : 0.f;
+      load_raw(a, h, sg.tok0 + (c + 2) * Q, sg.len - (c + 2) * Q, raw);
+      float g[4], r4[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
+      float run = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        run = fmaf(dt[i], A, run);
+        g[i] = run;
+      }
+      float before, after;
+      scan_both(run, lane, before, after);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] += before;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        r4[i] = dt[i] * ex2(after);
+        after = fmaf(dt[i], A, after);
+      }
+      bool ok = c < 2 || warp_wait(&s.x_empty[b], ((c >> 1) - 1) & 1, ab);
+      if (!ok) break;
+      if (lane == 31) s.gam[b] = ex2(g[3]);
+      *reinterpret_cast<float4*>(&s.gc[b][4 * lane]) = make_float4(g[0], g[1], g[2], g[3]);
+      *reinterpret_cast<float4*>(&s.gd[b][4 * lane]) =
+          make_float4(g[0] - __log2f(dt[0]), g[1] - __log2f(dt[1]), g[2] - __log2f(dt[2]), g[3] - __log2f(dt[3]));
+      warp_arrive(&s.gates[b]);
+      ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
+      if (!ok) break;
+      *reinterpret_cast<float4*>(&s.w[4 * lane]) = make_float4(r4[0], r4[1], r4[2], r4[3]);
+      warp_arrive(&s.w_full);
+    }
+  } else if (group == 0 || group == 1) {
+    // M: thread = row r; zero above the diagonal
+    const int j0 = 16 * half;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1;
+      bool ok = warp_wait(&s.gates[st], (c >> 1) & 1, ab) && warp_wait(&s.cb_full[st], (c >> 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const float gi = s.gc[st][r];
+      const uint32_t cb = trow + T_CB + 128 * st + j0;
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        uint32_t hi[8], lo[8];
+        if (b <= quad) {
+          uint32_t v[16];
+          tc::tmem_ld16(cb + 32 * b, v);
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 gj = *reinterpret_cast<const float4*>(&s.gd[st][32 * b + j0 + j]);
+            f[j] = ex2(gi - gj.x);
+            f[j + 1] = ex2(gi - gj.y);
+            f[j + 2] = ex2(gi - gj.z);
+            f[j + 3] = ex2(gi - gj.w);
+          }
+          wait_ld(v);
+          const int last = b < quad ? 32 : lane - j0;  // the last column kept
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float m0 = j <= last ? __uint_as_float(v[j]) * f[j] : 0.f;
+            const float m1 = j + 1 <= last ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f;
+            split2(pack2(m0, m1), hi[j / 2], lo[j / 2]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
+        }
+        // over the columns just read
+        tmem_st8(cb + 32 * b, hi);
+        tmem_st8(cb + 32 * b + 8, lo);
+      }
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      warp_arrive(&s.m_full);
+    }
+  } else if (group == 2 || group == 3) {
+    // state row n = r, columns p0 + 32 half + [0, 32)
+    const int pc = p0 + 32 * half;
+    uint64_t S[16];
+    const float* start = nullptr;
+    if (sg.idx > 0) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
+    else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
+#pragma unroll
+    for (int q = 0; q < 16; q += 2) {
+      ulonglong2 v = make_ulonglong2(0, 0);
+      if (start && r < a.NS && pc + 2 * q < a.P) v = *reinterpret_cast<const ulonglong2*>(start + 2 * q);
+      S[q] = v.x;
+      S[q + 1] = v.y;
+    }
+    float gam = 0.f;
+    bool ok = true;
+    auto advance = [&](int c) {  // S = gam S + U of chunk c
+      ok = warp_wait(&s.u_full, c & 1, ab);
+      if (!ok) return;
+      tc::tc_fence_after();
+      const uint64_t gg = pack2(gam, gam), one = pack2(1.f, 1.f);
+#pragma unroll
+      for (int p = 0; p < 32; p += 8) {
+        uint32_t u[8], v[8];
+        tmem_ld8(trow + T_U + 32 * half + p, u);
+        tmem_ld8(trow + T_U + PT + 32 * half + p, v);
+        wait_ld(u);
+        wait_ld(v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          S[p / 2 + q] = fma2(gg, S[p / 2 + q], fma2(one, pair_of(u + 2 * q), pair_of(v + 2 * q)));
+      }
+      tc::tc_fence_before();
+      warp_arrive(&s.u_empty);
+    };
+#pragma unroll 1
+    for (int c = 0; c <= nch; ++c) {
+      const int b = c & 1;
+      if (c > 0) advance(c - 1);
+      if (!ok || c == nch) break;
+      uint4 hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        split2(S[4 * q], hi[q].x, lo[q].x);
+        split2(S[4 * q + 1], hi[q].y, lo[q].y);
+        split2(S[4 * q + 2], hi[q].z, lo[q].z);
+        split2(S[4 * q + 3], hi[q].w, lo[q].w);
+      }
+      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab);
+      // the previous chunk's Yo has read the operand
+      if (c > 0) ok = ok && warp_wait(&s.yo_full, (c - 1) & 1, ab);
+      if (!ok) break;
+      gam = s.gam[b];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        *reinterpret_cast<uint4*>(s.S[0] + piece(r, 4 * half + q)) = hi[q];
+        *reinterpret_cast<uint4*>(s.S[1] + piece(r, 4 * half + q)) = lo[q];
+      }
+      tc::fence_proxy_async();
+      warp_arrive(&s.s_full);
+    }
+    if (ok && sg.idx == sg.nseg - 1 && a.ht && r < a.NS) {
+      float* to = a.ht + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
+#pragma unroll
+      for (int q = 0; q < 16; q += 2)
+        if (pc + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
+    }
+  } else {
+    // w x and the outputs of token row r, columns p0 + 32 half + [0, 32)
+    const int pc = p0 + 32 * half;
+    const float D = a.D ? a.D[h] : 0.f;
+    const uint64_t DD = pack2(D, D);
+    bool ok = true;
+#pragma unroll 1
+    for (int c = -1; c < nch; ++c) {
+      if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
+        const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
+        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab) &&
+             warp_wait(&s.w_full, (c + 1) & 1, ab);
+        if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
+        if (!ok) break;
+        if (r >= len) {
+          clear_pieces<4>(s.X[n], r, 4 * half);
+          if (half < nblk) clear_pieces<8>(s.B[n] + half * BLK, r, 0);
+        }
+        build_xw<4>(s.X[n], s.xw[0], s.xw[1], r, 4 * half, s.w[r]);
+        tc::fence_proxy_async();
+        warp_arrive(&s.xw_full[n]);
+      }
+      if (c < 0) continue;
+      const int b = c & 1, len = sg.len - c * Q;
+      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab) && warp_wait(&s.y_full, c & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const float e = ex2(s.gc[b][r]);
+      const uint64_t ee = pack2(e, e);
+      uint4 o[4];
+#pragma unroll
+      for (int p = 0; p < 32; p += 8) {
+        uint32_t yo[8], yd[8];
+        tmem_ld8(trow + T_YO + 32 * half + p, yo);
+        tmem_ld8(trow + T_YD + 32 * half + p, yd);
+        const uint4 xv = *reinterpret_cast<const uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
+        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
+        wait_ld(yo);
+        wait_ld(yd);
+        uint32_t y[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          float y0, y1;
+          const uint64_t v = fma2(ee, pair_of(yo + 2 * z), pair_of(yd + 2 * z));
+          unpack2(fma2(DD, widen2(xs[z]), v), y0, y1);
+          const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
+          y[z] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        o[p / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      tc::tc_fence_before();
+      warp_arrive(&s.y_empty);
+      if (lane == 0) arrive(&s.x_empty[b]);
+      if (r < len) {
+        __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (pc + 8 * q < a.P) *reinterpret_cast<uint4*>(out + 8 * q) = o[q];
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s.abort) atomicExch(ta.err, 10);
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Summary of a segment (split documents only): its end state from a zero start,
+//   U = B^T (w x) with w_j = dt_j exp(sum of the gates after j in the segment),
+// accumulated in TMEM over its chunks, last chunk first, and its total decay.
+//   warp 0: TMA;  warp 1: MMA;  warp 2: gates;  warps 4-7 / 8-11: w x of the
+//   even / odd steps
+// ---------------------------------------------------------------------------
+constexpr int SUM_THREADS = 384;
+struct SumSmem {
+  unsigned char B[2][2 * BLK], X[2][BLK];
+  unsigned char xw[2][2][BLK];  // step parity; hi, lo
+  float w[2][Q];
+  uint64_t full[2], empty[2], gates[2], xw_full[2], done;
+  uint32_t tmem;
+  int abort;
+  Seg seg;
+};
+
+__global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constant__ TcArgs ta) {
+  extern __shared__ __align__(1024) unsigned char ssm_smem[];
+  SumSmem& s = *reinterpret_cast<SumSmem*>(ssm_smem);
+  const SsmArgs& a = ta.a;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int per = a.H * ta.pblocks;
+  const int hp = blockIdx.x % per, h = hp / ta.pblocks, p0 = (hp % ta.pblocks) * PT, sid = blockIdx.x / per;
+  const int grp = h / (a.H / a.G);
+  const int nblk = a.NS > 64 ? 2 : 1;
+  if (warp == 0) {
+    const Seg sg = find_segment(a.cu, a.N, ta.lseg, sid);
+    if (lane == 0) {
+      s.seg = sg;
+      s.abort = 0;
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&s.full[i], 1);
+        tc::mbar_init(&s.empty[i], 1);
+        tc::mbar_init(&s.gates[i], 1);
+        tc::mbar_init(&s.xw_full[i], 4);
+      }
+      tc::mbar_init(&s.done, 1);
+      tc::mbar_fence_init();
+    }
+  }
+  __syncthreads();
+  const Seg sg = s.seg;
+  if (sg.idx == sg.nseg - 1) return;  // no segment starts from this one's end
+  if (warp == 1) {
+    tc::tmem_alloc(&s.tmem, 128);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  const int nch = sg.len / Q;  // a segment that is not its document's last holds whole chunks
+  volatile int* ab = &s.abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+#pragma unroll 1
+      for (int k = 0; k < nch; ++k) {
+        const int b = k & 1, row = sg.tok0 + (nch - 1 - k) * Q;
+        if (k >= 2 && !wait_or_abort(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
+        tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + nblk) * BLK));
+        for (int q = 0; q < nblk; ++q) tc::tma_load_3d(s.B[b] + q * BLK, &ta.b_map, 64 * q, grp, row, &s.full[b]);
+        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.full[b]);
+        issued = k + 1;
+      }
+      for (int k = max(0, issued - 2); k < issued; ++k) tc::mbar_wait(&s.full[k & 1], (k >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0][0]);
+    constexpr uint32_t stage2 = 2 * BLK / 16, step = 2048 / 16;
+#pragma unroll 1
+    for (int k = 0; k < nch; ++k) {
+      const uint32_t b = k & 1;
+      if (!warp_wait(&s.xw_full[b], (k >> 1) & 1, ab)) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        mma_ss(tmem, d_b + b * stage2 + q * step, d_w + b * stage2 + q * step, i_u, k + q > 0);
+      commit(&s.empty[b]);
+    }
+    commit(&s.done);
+    tc::mbar_wait(&s.done, 0);
+    __syncwarp();
+  } else if (warp == 2) {
+    const float A = a.A[h] * LOG2E;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    float tail = 0.f, dt[4], raw[4];  // tail: the gates after this chunk
+    if (nch > 0) load_raw(a, h, sg.tok0 + (nch - 1) * Q, Q, raw);
+#pragma unroll 1
+    for (int k = 0; k < nch; ++k) {
+      const int b = k & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dt[i] = activate(a, raw[i] + bias);
+      if (k + 1 < nch) load_raw(a, h, sg.tok0 + (nch - 2 - k) * Q, Q, raw);
+      if (k >= 2 && !warp_wait(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
+      const float run = ((dt[0] + dt[1]) + (dt[2] + dt[3])) * A;
+      float before, after;
+      scan_both(run, lane, before, after);
+      const float inc = __shfl_sync(0xffffffffu, run + after, 0);
+      after += tail;
+      float4 v;
+      v.w = dt[3] * ex2(after);
+      after = fmaf(dt[3], A, after);
+      v.z = dt[2] * ex2(after);
+      after = fmaf(dt[2], A, after);
+      v.y = dt[1] * ex2(after);
+      after = fmaf(dt[1], A, after);
+      v.x = dt[0] * ex2(after);
+      *reinterpret_cast<float4*>(&s.w[b][4 * lane]) = v;
+      tail += inc;
+      warp_arrive(&s.gates[b]);
+    }
+    if (lane == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
+  } else if (warp >= 4) {
+    const int g = (warp - 4) >> 2, j = (tid - 128) & 127;
+#pragma unroll 1
+    for (int k = g; k < nch; k += 2) {
+      bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab) && warp_wait(&s.gates[g], (k >> 1) & 1, ab);
+      if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
+      if (!ok) break;
+      build_xw<8>(s.X[g], s.xw[g][0], s.xw[g][1], j, 0, s.w[g][j]);
+      tc::fence_proxy_async();
+      warp_arrive(&s.xw_full[g]);
+    }
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp >= 4 && warp < 8 && !s.abort) {
+    const int n = tid - 128;
+    const uint32_t row = tmem + ((uint32_t)(32 * (warp - 4)) << 16);
+    float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + n) * a.P + p0;
+#pragma unroll
+    for (int p = 0; p < PT; p += 16) {
+      uint32_t u[16], v[16];
+      tc::tmem_ld16(row + p, u);
+      tc::tmem_ld16(row + PT + p, v);
+      wait_ld(u);
+      wait_ld(v);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) + __uint_as_float(v[q]));
+      if (n < a.NS) {
+#pragma unroll
+        for (int q = 0; q < 16; q += 4)
+          if (p0 + p + q < a.P) *reinterpret_cast<uint4*>(to + p + q) = make_uint4(u[q], u[q + 1], u[q + 2], u[q + 3]);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s.abort) atomicExch(ta.err, 10);
+  if (warp == 1) tc::tmem_dealloc(tmem, 128);
+}
+
+// The start states of split documents' segments, in place of the segments' own
+// end states: S[s + 1] = 2^gsum[s] S[s] + U[s].  One thread per state element.
+__global__ void __launch_bounds__(256) k_ssm_merge(const __grid_constant__ TcArgs ta) {
+  const SsmArgs& a = ta.a;
+  const int64_t elems = (int64_t)a.NS * a.P;
+  const int eblocks = (int)((elems + 1023) / 1024);
+  const int e0 = (blockIdx.x % eblocks) * 1024 + threadIdx.x * 4, h = (blockIdx.x / eblocks) % a.H;
+  const int d = blockIdx.x / eblocks / a.H;
+  // the document's first segment: the segments of the documents before it
+  int before = 0;
+  for (int i = threadIdx.x; i < d; i += 256) {
+    const int ch = (a.cu[i + 1] - a.cu[i] + Q - 1) / Q;
+    before += ch == 0 ? 1 : (ch + ta.lseg - 1) / ta.lseg;
+  }
+  __shared__ int sums[8];
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) before += __shfl_xor_sync(0xffffffffu, before, m);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) before += sums[i];
+  const int ch = (a.cu[d + 1] - a.cu[d] + Q - 1) / Q, nseg = ch == 0 ? 1 : (ch + ta.lseg - 1) / ta.lseg;
+  if (nseg == 1 || e0 >= elems) return;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.h0) S = *reinterpret_cast<const float4*>(a.h0 + ((int64_t)d * a.H + h) * elems + e0);
+  const int64_t step = (int64_t)a.H * elems;
+  float* at = ta.seg + ((int64_t)before * a.H + h) * elems + e0;
+  const float* gs = ta.gsum + (int64_t)before * a.H + h;
+  for (int s0 = 0; s0 < nseg; s0 += 8) {
+    float4 u[8];
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i < nseg - 1) {
+        u[i] = *reinterpret_cast<const float4*>(at + (s0 + i) * step);
+        g[i] = exp2f(gs[(int64_t)(s0 + i) * a.H]);
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i < nseg) {
+        *reinterpret_cast<float4*>(at + (s0 + i) * step) = S;
+        if (s0 + i < nseg - 1) {
+          S.x = fmaf(g[i], S.x, u[i].x);
+          S.y = fmaf(g[i], S.y, u[i].y);
+          S.z = fmaf(g[i], S.z, u[i].z);
+          S.w = fmaf(g[i], S.w, u[i].w);
+        }
+      }
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// [T][heads][dim] BF16, tokens ld elements apart, one head at a time: boxes of
+// 64 elements x 1 head x 128 tokens, 128-byte swizzle, zero fill outside.
+bool token_map(CUtensorMap* map, const void* base, uint64_t T, uint64_t heads, uint64_t dim, uint64_t ld) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {dim, heads, T};
+  cuuint64_t strides[2] = {dim * 2, ld * 2};
+  cuuint32_t box[3] = {64, 1, Q};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+bool ssm_tc_shape(int P, int NS) { return P % 8 == 0 && NS % 8 == 0 && NS <= 128; }
+
+bool ssm_tc_layout(const SsmArgs& a) {
+  const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.B | (uintptr_t)a.C | (uintptr_t)a.out | (uintptr_t)a.h0 |
+                        (uintptr_t)a.ht;
+  if ((all & 15) != 0) return false;
+  return a.T <= 1 || (a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0);
+}
+
+// Whole documents while they keep the SMs evenly busy; else the segment length
+// with the least estimated time, in chunk steps of one block: kStart steps to
+// start a block, kSum for a summary's step.
+SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
+  constexpr double kStart = 3.0, kSum = 0.4;
+  const int64_t items = (int64_t)H * ((P + 63) / 64);
+  const double sms = 152.0;
+  int64_t nc = 0, most = 0;
+  for (int i = 0; i < N; ++i) {
+    const int64_t ch = (cu[i + 1] - (int64_t)cu[i] + Q - 1) / Q;
+    nc += ch;
+    most = std::max(most, ch);
+  }
+  SsmPlan best{(int)std::max<int64_t>(most, 1), N, false, 0};
+  double cost = std::max((double)(nc + kStart * N) * items / sms, most + kStart);
+  // pieces of the longest document
+  for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
+    const int64_t L = (most + k - 1) / k;
+    int64_t nseg = 0, again = 0;
+    for (int i = 0; i < N; ++i) {
+      const int64_t ch = (cu[i + 1] - (int64_t)cu[i] + Q - 1) / Q;
+      const int64_t n = ch == 0 ? 1 : (ch + L - 1) / L;
+      nseg += n;
+      if (n > 1) again += ch - ch / n;
+    }
+    const double waves = (double)nseg * items / sms;
+    const double walk = std::max((nc + kStart * nseg) * items / sms, (double)(L + kStart) * (int64_t)(waves + 0.999));
+    const double sum = std::max(kSum * again * items / sms, kSum * L) + 2 * kStart;
+    if (walk + sum < 0.95 * cost) {
+      cost = walk + sum;
+      best.lseg = (int)L;
+      best.nseg = nseg;
+      best.split = true;
+    }
+  }
+  if (best.split)
+    best.scratch = up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
+  return best;
+}
+
+cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, cudaStream_t st) {
+  TcArgs t{};
+  t.a = a;
+  t.pblocks = (a.P + 63) / 64;
+  t.lseg = plan.lseg;
+  t.err = device_error_ptr();
+  if (!t.err) return cudaErrorUnknown;
+  if (a.T > 0) {
+    const uint64_t one = 8;  // a single token's stride is never used
+    if (!token_map(&t.x_map, a.x, a.T, a.H, a.P, a.T > 1 ? a.ldx : (uint64_t)a.H * a.P * one) ||
+        !token_map(&t.b_map, a.B, a.T, a.G, a.NS, a.T > 1 ? a.ldb : (uint64_t)a.G * a.NS * one) ||
+        !token_map(&t.c_map, a.C, a.T, a.G, a.NS, a.T > 1 ? a.ldc : (uint64_t)a.G * a.NS * one))
+      return cudaErrorInvalidValue;
+  }
+  const unsigned grid = (unsigned)(plan.nseg * a.H * t.pblocks);
+  constexpr int sm_walk = (int)sizeof(WalkSmem), sm_sum = (int)sizeof(SumSmem);
+  static_assert(sm_walk <= 232448 && sm_sum <= 232448, "227 KB of shared memory a block");
+  if (plan.split) {
+    t.seg = static_cast<float*>(scratch);
+    t.gsum = reinterpret_cast<float*>(static_cast<char*>(scratch) +
+                                      up256((size_t)plan.nseg * a.H * a.NS * a.P * sizeof(float)));
+    cudaFuncSetAttribute(k_ssm_sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_sum);
+    {
+      ProfScope ps("ssm_sum", st, (double)a.T * a.H);
+      k_ssm_sum<<<grid, SUM_THREADS, sm_sum, st>>>(t);
+    }
+    if (cudaError_t e = cudaGetLastError()) return e;
+    ProfScope ps("ssm_merge", st);
+    const unsigned mb = (unsigned)(((int64_t)a.NS * a.P + 1023) / 1024) * a.H * a.N;
+    k_ssm_merge<<<mb, 256, 0, st>>>(t);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  cudaFuncSetAttribute(k_ssm_walk, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_walk);
+  ProfScope ps("ssm_walk", st, (double)a.T * a.H);
+  k_ssm_walk<<<grid, WALK_THREADS, sm_walk, st>>>(t);
+  return cudaGetLastError();
+}
+
+}  // namespace gdr
