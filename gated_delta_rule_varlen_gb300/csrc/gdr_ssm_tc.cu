@@ -304,8 +304,8 @@ __device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* 
 
 // ---------------------------------------------------------------------------
 // The walk: one block per (segment, head, 64 columns of the state).
-//   warp 0: TMA, and the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
-//   warps 2, 3: the gates of the even and the odd chunks
+//   warp 0: the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
+//   warp 2: TMA;  warp 3: the gates
 //   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
 //   groups 2, 3: the state (32 columns each)
 //   groups 4, 5: w x and the outputs (32 columns each)
@@ -395,38 +395,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
     constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
     const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S[0]);
-    const int grp = h / (a.H / a.G);
-    int bc_issued = 0, x_issued = 0;
-    auto load_bc = [&](int c) {
-      const int b = c & 1, row = sg.tok0 + c * Q;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
-#pragma unroll 1
-        for (int k = 0; k < nblk; ++k) {
-          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
-          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
-        }
-      }
-      __syncwarp();
-      bc_issued = c + 1;
-    };
-    auto load_x = [&](int c) {
-      const int b = c & 1;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
-        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, sg.tok0 + c * Q, &s.x_full[b]);
-      }
-      __syncwarp();
-      x_issued = c + 1;
-    };
-    if (nch > 0) {
-      load_x(0);
-      load_bc(0);
-    }
-    if (nch > 1) {
-      load_x(1);
-      load_bc(1);
-    }
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
@@ -439,11 +407,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
       commit(&s.u_full);
-      if (c > 0 && c + 1 < nch) {
-        ok = warp_wait(&s.bc_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
-        if (!ok) break;
-        load_bc(c + 1);
-      }
       // Yo = C S0
       ok = warp_wait(&s.s_full, c & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
@@ -458,21 +421,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       commit(&s.yo_full);
       commit(&s.y_full);
       commit(&s.bc_empty[b]);
-      if (c > 0 && c + 1 < nch) {
-        ok = warp_wait(&s.x_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
-        if (!ok) break;
-        load_x(c + 1);
-      }
     }
-    // no MMA and no copy is in flight when the block ends
+    // no MMA is in flight when the block ends
     if (nch > 0) {
       commit(&s.done[0]);
       tc::mbar_wait(&s.done[0], 0);
     }
-#pragma unroll 1
-    for (int c = max(0, bc_issued - 2); c < bc_issued; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
-#pragma unroll 1
-    for (int c = max(0, x_issued - 2); c < x_issued; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
@@ -513,17 +467,44 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::mbar_wait(&s.done[1], 0);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    if (lane == 0) {
+      const int grp = h / (a.H / a.G);
+      int bc = 0, x = 0;  // chunks asked for
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        const int b = c & 1, row = sg.tok0 + c * Q;
+        if (c >= 2 && !wait_or_abort(&s.bc_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
+#pragma unroll 1
+        for (int k = 0; k < nblk; ++k) {
+          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
+          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
+        }
+        bc = c + 1;
+        if (c >= 2 && !wait_or_abort(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
+        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.x_full[b]);
+        x = c + 1;
+      }
+      // no copy is in flight when the block ends
+#pragma unroll 1
+      for (int c = max(0, bc - 2); c < bc; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
+#pragma unroll 1
+      for (int c = max(0, x - 2); c < x; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
     float raw[4];
-    load_raw(a, h, sg.tok0 + (warp - 2) * Q, sg.len - (warp - 2) * Q, raw);
+    load_raw(a, h, sg.tok0, sg.len, raw);
     const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
 #pragma unroll 1
-    for (int c = warp - 2; c < nch; c += 2) {
+    for (int c = 0; c < nch; ++c) {
       const int b = c & 1;
       float dt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) dt[i] = 4 * lane + i < sg.len - c * Q ? activate(a, raw[i] + bias) : 0.f;
-      load_raw(a, h, sg.tok0 + (c + 2) * Q, sg.len - (c + 2) * Q, raw);
+      load_raw(a, h, sg.tok0 + (c + 1) * Q, sg.len - (c + 1) * Q, raw);
       float g[4], r4[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
       float run = 0.f;
 #pragma unroll
@@ -675,9 +656,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = -1; c < nch; ++c) {
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
-        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab) &&
-             warp_wait(&s.w_full, (c + 1) & 1, ab);
+        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.w_full, (c + 1) & 1, ab);
         if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
+        if (len < Q) ok = ok && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
         if (!ok) break;
         if (r >= len) {
           clear_pieces<4>(s.X[n], r, 4 * half);

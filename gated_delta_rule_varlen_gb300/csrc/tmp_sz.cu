@@ -13,8 +13,8 @@
 // few 1e-6, and the outputs' error stays that of their own rounding).  The state
 // itself stays in FP32 registers.
 //
-// exp(G_i - G_j) dt_j is formed as one exponential 2^(g_i - (g_j - log2 dt_j)),
-// whose exponent is at most log2 dt_j on and below the diagonal.
+// exp(G_i - G_j) is formed from the difference, at most 1 on and below the
+// diagonal; what is above is dropped by selection.
 //
 // A chunk's tiles land by TMA; rows past the document's end are cleared, since
 // they hold another document's values (a NaN there would pass through a zero
@@ -304,8 +304,8 @@ __device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* 
 
 // ---------------------------------------------------------------------------
 // The walk: one block per (segment, head, 64 columns of the state).
-//   warp 0: TMA, and the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
-//   warps 2, 3: the gates of the even and the odd chunks
+//   warp 0: the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
+//   warp 2: TMA;  warp 3: the gates
 //   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
 //   groups 2, 3: the state (32 columns each)
 //   groups 4, 5: w x and the outputs (32 columns each)
@@ -326,12 +326,12 @@ struct WalkSmem {
   unsigned char S[2][BLK];   // hi, lo
   // A chunk's gates.
   float gc[2][Q];  // prefix sums of dt A log2(e)
-  float gd[2][Q];  // gc - log2(dt): dt_j 2^(gc_i - gc_j) = 2^(gc_i - gd_j)
+  float dt[2][Q];
   float w[Q];      // dt_j 2^(sum after j)
   float gam[2];    // 2^gc[last]
   // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
-  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], gates[2], xw_full[2], cb_full[2];
-  uint64_t w_full, m_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], gates[2], xw_full[2], cb_full[2], m_full[2];
+  uint64_t w_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -359,10 +359,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         tc::mbar_init(&s.gates[i], 1);
         tc::mbar_init(&s.xw_full[i], 8);
         tc::mbar_init(&s.cb_full[i], 1);
+        tc::mbar_init(&s.m_full[i], 8);
         tc::mbar_init(&s.done[i], 1);
       }
       tc::mbar_init(&s.w_full, 1);
-      tc::mbar_init(&s.m_full, 8);
       tc::mbar_init(&s.u_full, 1);
       tc::mbar_init(&s.u_empty, 8);
       tc::mbar_init(&s.s_full, 8);
@@ -395,38 +395,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
     constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
     const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S[0]);
-    const int grp = h / (a.H / a.G);
-    int bc_issued = 0, x_issued = 0;
-    auto load_bc = [&](int c) {
-      const int b = c & 1, row = sg.tok0 + c * Q;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
-#pragma unroll 1
-        for (int k = 0; k < nblk; ++k) {
-          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
-          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
-        }
-      }
-      __syncwarp();
-      bc_issued = c + 1;
-    };
-    auto load_x = [&](int c) {
-      const int b = c & 1;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
-        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, sg.tok0 + c * Q, &s.x_full[b]);
-      }
-      __syncwarp();
-      x_issued = c + 1;
-    };
-    if (nch > 0) {
-      load_x(0);
-      load_bc(0);
-    }
-    if (nch > 1) {
-      load_x(1);
-      load_bc(1);
-    }
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
@@ -439,11 +407,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
       commit(&s.u_full);
-      if (c > 0 && c + 1 < nch) {
-        ok = warp_wait(&s.bc_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
-        if (!ok) break;
-        load_bc(c + 1);
-      }
       // Yo = C S0
       ok = warp_wait(&s.s_full, c & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
@@ -458,21 +421,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       commit(&s.yo_full);
       commit(&s.y_full);
       commit(&s.bc_empty[b]);
-      if (c > 0 && c + 1 < nch) {
-        ok = warp_wait(&s.x_empty[b ^ 1], ((c - 1) >> 1) & 1, ab);
-        if (!ok) break;
-        load_x(c + 1);
-      }
     }
-    // no MMA and no copy is in flight when the block ends
+    // no MMA is in flight when the block ends
     if (nch > 0) {
       commit(&s.done[0]);
       tc::mbar_wait(&s.done[0], 0);
     }
-#pragma unroll 1
-    for (int c = max(0, bc_issued - 2); c < bc_issued; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
-#pragma unroll 1
-    for (int c = max(0, x_issued - 2); c < x_issued; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
     __syncwarp();
   } else if (warp == 1 && ta.lseg == -5) {
  return;
@@ -498,7 +452,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       }
       if (c < 0) continue;
       // Yd = M x
-      ok = warp_wait(&s.m_full, c & 1, ab) && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab) && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
@@ -515,17 +469,44 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::mbar_wait(&s.done[1], 0);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    if (lane == 0) {
+      const int grp = h / (a.H / a.G);
+      int bc = 0, x = 0;  // chunks asked for
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        const int b = c & 1, row = sg.tok0 + c * Q;
+        if (c >= 2 && !wait_or_abort(&s.bc_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
+#pragma unroll 1
+        for (int k = 0; k < nblk; ++k) {
+          tc::tma_load_3d(s.C[b] + k * BLK, &ta.c_map, 64 * k, grp, row, &s.bc_full[b]);
+          tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
+        }
+        bc = c + 1;
+        if (c >= 2 && !wait_or_abort(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
+        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.x_full[b]);
+        x = c + 1;
+      }
+      // no copy is in flight when the block ends
+#pragma unroll 1
+      for (int c = max(0, bc - 2); c < bc; ++c) tc::mbar_wait(&s.bc_full[c & 1], (c >> 1) & 1);
+#pragma unroll 1
+      for (int c = max(0, x - 2); c < x; ++c) tc::mbar_wait(&s.x_full[c & 1], (c >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
     float raw[4];
-    load_raw(a, h, sg.tok0 + (warp - 2) * Q, sg.len - (warp - 2) * Q, raw);
+    load_raw(a, h, sg.tok0, sg.len, raw);
     const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
 #pragma unroll 1
-    for (int c = warp - 2; c < nch; c += 2) {
+    for (int c = 0; c < nch; ++c) {
       const int b = c & 1;
       float dt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) dt[i] = 4 * lane + i < sg.len - c * Q ? activate(a, raw[i] + bias) : 0.f;
-      load_raw(a, h, sg.tok0 + (c + 2) * Q, sg.len - (c + 2) * Q, raw);
+      load_raw(a, h, sg.tok0 + (c + 1) * Q, sg.len - (c + 1) * Q, raw);
       float g[4], r4[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
       float run = 0.f;
 #pragma unroll
@@ -546,8 +527,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       if (!ok) break;
       if (lane == 31) s.gam[b] = ex2(g[3]);
       *reinterpret_cast<float4*>(&s.gc[b][4 * lane]) = make_float4(g[0], g[1], g[2], g[3]);
-      *reinterpret_cast<float4*>(&s.gd[b][4 * lane]) =
-          make_float4(g[0] - __log2f(dt[0]), g[1] - __log2f(dt[1]), g[2] - __log2f(dt[2]), g[3] - __log2f(dt[3]));
+      *reinterpret_cast<float4*>(&s.dt[b][4 * lane]) = make_float4(dt[0], dt[1], dt[2], dt[3]);
       warp_arrive(&s.gates[b]);
       ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
       if (!ok) break;
@@ -574,11 +554,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const float4 gj = *reinterpret_cast<const float4*>(&s.gd[st][32 * b + j0 + j]);
-            f[j] = ex2(gi - gj.x);
-            f[j + 1] = ex2(gi - gj.y);
-            f[j + 2] = ex2(gi - gj.z);
-            f[j + 3] = ex2(gi - gj.w);
+            const float4 gj = *reinterpret_cast<const float4*>(&s.gc[st][32 * b + j0 + j]);
+            const float4 dj = *reinterpret_cast<const float4*>(&s.dt[st][32 * b + j0 + j]);
+            f[j] = dj.x * ex2(gi - gj.x);
+            f[j + 1] = dj.y * ex2(gi - gj.y);
+            f[j + 2] = dj.z * ex2(gi - gj.z);
+            f[j + 3] = dj.w * ex2(gi - gj.w);
           }
           wait_ld(v);
           const int last = b < quad ? 32 : lane - j0;  // the last column kept
@@ -598,7 +579,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      warp_arrive(&s.m_full);
+      warp_arrive(&s.m_full[st]);
     }
   } else if (group == 2 || group == 3) {
     // state row n = r, columns p0 + 32 half + [0, 32)
@@ -677,9 +658,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = -1; c < nch; ++c) {
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
-        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab) &&
-             warp_wait(&s.w_full, (c + 1) & 1, ab);
+        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.w_full, (c + 1) & 1, ab);
         if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
+        if (len < Q) ok = ok && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
         if (!ok) break;
         if (r >= len) {
           clear_pieces<4>(s.X[n], r, 4 * half);
