@@ -8,10 +8,14 @@
 //   S_end = exp(G_last) S0 + B^T (w x),  w_j = dt_j exp(sum_{k>j} a_k)
 // Four products of 128-row tiles (tcgen05, FP32 accumulators in TMEM):
 //   CB = C B^T,  Yo = C S0,  Yd = M x,  U = B^T (w x).
-// x, B and C are BF16 and enter exactly; what is formed in FP32 (M, S0, w x)
-// enters as a pair of BF16 numbers hi + lo (17 bits: FP32 end states within a
-// few 1e-6, and the outputs' error stays that of their own rounding).  The state
-// itself stays in FP32 registers.
+// x, B and C are BF16 and enter exactly.  w x enters U as a pair of BF16 numbers
+// hi + lo (17 bits), so that the FP32 state, kept in registers from chunk to
+// chunk, stays within a few 1e-6.  M and S0, which only outputs depend on, enter
+// as BF16 like x, B and C themselves: each term of an output's sums is rounded
+// once, to the precision the output is rounded to, and the sums are FP32.  (As
+// pairs they took 1.4 times the chunk's MMA time and half as many instructions
+// again, for outputs 1.66e-3 instead of 1.7e-3 off, of which their own rounding is
+// 1.66e-3.)
 //
 // exp(G_i - G_j) is formed from the difference, at most 1 on and below the
 // diagonal; what is above is dropped by selection.
@@ -34,8 +38,9 @@ constexpr int PT = 64;        // columns of the state that a block works on
 constexpr int BLK = Q * 128;  // bytes of a tile block: 128 rows of 64 BF16
 
 struct TcArgs {
-  CUtensorMap x_map, b_map, c_map;
+  CUtensorMap x_map, b_map, c_map, out_map;
   SsmArgs a;
+  const float* gates;  // [chunks][H][3][Q], written by k_ssm_gates (Gates)
   int pblocks;      // ceil(P / 64)
   int lseg;         // chunks of a segment at most
   float* seg;       // [segments][H][NS][P]: start states of split documents' segments
@@ -46,46 +51,69 @@ struct TcArgs {
 // The segment `idx` of document `doc`, its chunks [c0, c1) and tokens.
 struct Seg {
   int doc, idx, nseg, tok0, len;  // first token and tokens of the segment
-  int first;                      // the document's first segment
+  int chunk0;                     // its first chunk; an empty document counts as one
 };
+
+// A chunk's gates of one head (a_t = dt_t A log2 e):
+//   ss[j]   sum of the a after token j: 2^(ss_j - ss_i) is the decay from j to i,
+//           and dt_j 2^ss_j = w_j keeps its accuracy, since ss is summed from the end
+//   dt[j]   activated (zero past the document's end)
+//   colf[j] dt_j 2^(ss_j - ss[end of j's 32 tokens])
+struct Gates {
+  const float* p;
+  __device__ __forceinline__ const float* ss() const { return p; }
+  __device__ __forceinline__ const float* dt() const { return p + Q; }
+  __device__ __forceinline__ const float* colf() const { return p + 2 * Q; }
+  // the chunk's whole decay (log2)
+  __device__ __forceinline__ float total(float A) const { return fmaf(*dt(), A, *ss()); }
+};
+__device__ __forceinline__ Gates gates_of(const TcArgs& t, int chunk, int h) {
+  return Gates{t.gates + ((int64_t)chunk * t.a.H + h) * (3 * Q)};
+}
 
 // Finds segment `want` by a scan over the documents (one warp).
 __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int want) {
   const int lane = threadIdx.x & 31;
-  int base = 0;
+  int base = 0, cbase = 0;
+#pragma unroll 1
   for (int d0 = 0; d0 < N; d0 += 32) {
     const int d = d0 + lane;
-    int n = 0, start = 0, len = 0;
+    int n = 0, start = 0, len = 0, nc = 0;
     if (d < N) {
       start = cu[d];
       len = cu[d + 1] - start;
       const int ch = (len + Q - 1) / Q;
       n = ch == 0 ? 1 : (ch + lseg - 1) / lseg;
+      nc = ch == 0 ? 1 : ch;
     }
-    int pre = n;
+    int pre = n, cpre = nc;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, pre, m);
-      if (lane >= m) pre += v;
+      const int v = __shfl_up_sync(0xffffffffu, pre, m), w = __shfl_up_sync(0xffffffffu, cpre, m);
+      if (lane >= m) {
+        pre += v;
+        cpre += w;
+      }
     }
-    const int total = __shfl_sync(0xffffffffu, pre, 31);
+    const int total = __shfl_sync(0xffffffffu, pre, 31), ctotal = __shfl_sync(0xffffffffu, cpre, 31);
     if (want < base + total) {
       const unsigned hit = __ballot_sync(0xffffffffu, want < base + pre);
       const int l = __ffs(hit) - 1;
       Seg s;
       s.doc = d0 + l;
       s.nseg = __shfl_sync(0xffffffffu, n, l);
-      s.first = base + __shfl_sync(0xffffffffu, pre, l) - s.nseg;
-      s.idx = want - s.first;
+      s.idx = want - (base + __shfl_sync(0xffffffffu, pre, l) - s.nseg);
       const int dl = __shfl_sync(0xffffffffu, len, l), ds = __shfl_sync(0xffffffffu, start, l);
       const int ch = (dl + Q - 1) / Q, per = ch / s.nseg, extra = ch % s.nseg;
       // the first `extra` segments have one chunk more
       const int c0 = s.idx * per + min(s.idx, extra), c1 = c0 + per + (s.idx < extra ? 1 : 0);
       s.tok0 = ds + c0 * Q;
       s.len = min(dl, c1 * Q) - c0 * Q;
+      s.chunk0 = cbase + __shfl_sync(0xffffffffu, cpre - nc, l) + c0;
       return s;
     }
     base += total;
+    cbase += ctotal;
   }
   return Seg{0, 0, 1, 0, 0, 0};
 }
@@ -143,6 +171,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // The two BF16 of a word as a pair of FP32.
 __device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(bf_lo(w), bf_hi(w)); }
 
+// A pair of FP32 numbers rounded to BF16.
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // A pair of FP32 numbers as BF16 pairs: hi rounded to nearest, lo the rest
 // rounded (off by at most 2^-18 of the number).
 __device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
@@ -197,7 +232,7 @@ __device__ __forceinline__ Seg uniform(const Seg& s) {
   u.nseg = __shfl_sync(0xffffffffu, s.nseg, 0);
   u.tok0 = __shfl_sync(0xffffffffu, s.tok0, 0);
   u.len = __shfl_sync(0xffffffffu, s.len, 0);
-  u.first = __shfl_sync(0xffffffffu, s.first, 0);
+  u.chunk0 = __shfl_sync(0xffffffffu, s.chunk0, 0);
   return u;
 }
 // One arrival for the warp, after all its lanes' work.
@@ -246,35 +281,71 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
-// Exclusive sums over the lanes before and after this one.
-__device__ __forceinline__ void scan_both(float v, int lane, float& before, float& after) {
-  float up = v, down = v;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, up, m), d = __shfl_down_sync(0xffffffffu, down, m);
-    if (lane >= m) up += u;
-    if (lane + m < 32) down += d;
+// ---------------------------------------------------------------------------
+// The gates of every chunk: one block per (chunk, 32 heads).  dt is read with
+// the heads on the lanes (its rows are tokens), then each warp scans whole
+// heads, four tokens a lane.
+// ---------------------------------------------------------------------------
+constexpr int GATE_WARPS = 16;
+__global__ void __launch_bounds__(GATE_WARPS * 32) k_ssm_gates(const int* __restrict__ cu, SsmArgs a, float* gates) {
+  __shared__ float sdt[Q][33];
+  __shared__ Seg sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (warp == 0) {
+    const Seg sg = find_segment(cu, a.N, 1, blockIdx.x);
+    if (lane == 0) sh = sg;
   }
-  up = __shfl_up_sync(0xffffffffu, up, 1);
-  down = __shfl_down_sync(0xffffffffu, down, 1);
-  before = lane == 0 ? 0.f : up;
-  after = lane == 31 ? 0.f : down;
-}
-
-// Lane l loads the raw dt of tokens 4 l .. 4 l + 3 (of `len`, which may be none).
-__device__ __forceinline__ void load_raw(const SsmArgs& a, int h, int tok0, int len, float (&dt)[4]) {
-  const int lane = threadIdx.x & 31;
+  __syncthreads();
+  const Seg sg = sh;
+  const int h0 = blockIdx.y * 32, h = h0 + lane;
+  const float bias = h < a.H && a.dt_bias ? a.dt_bias[h] : 0.f;
+  float v[Q / GATE_WARPS];  // all rows asked for before the first is used
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = 4 * lane + i;
-    dt[i] = 0.f;
-    if (j < len) {
-      const int64_t at = (int64_t)(tok0 + j) * a.lddt + h;
-      dt[i] = a.dt_f32 ? static_cast<const float*>(a.dt)[at] : to_f(static_cast<const __nv_bfloat16*>(a.dt)[at]);
+  for (int i = 0; i < Q / GATE_WARPS; ++i) {
+    const int j = warp + GATE_WARPS * i;
+    v[i] = 0.f;
+    if (j < sg.len && h < a.H) {
+      const int64_t at = (int64_t)(sg.tok0 + j) * a.lddt + h;
+      v[i] = a.dt_f32 ? static_cast<const float*>(a.dt)[at] : to_f(static_cast<const __nv_bfloat16*>(a.dt)[at]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < Q / GATE_WARPS; ++i) {
+    const int j = warp + GATE_WARPS * i;
+    const float x = v[i] + bias;
+    sdt[j][lane] = j >= sg.len ? 0.f : a.softplus ? softplus_f(x) : x;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = warp; k < 32 && h0 + k < a.H; k += GATE_WARPS) {
+    const float A = a.A[h0 + k] * LOG2E;
+    float dt[4], ss[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dt[i] = sdt[4 * lane + i][k];
+    float run = 0.f;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      ss[i] = run;
+      run = fmaf(dt[i], A, run);
+    }
+    float after = run;  // inclusive sums from the last lane down
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const float v = __shfl_down_sync(0xffffffffu, after, m);
+      if (lane + m < 32) after += v;
+    }
+    after = __shfl_down_sync(0xffffffffu, after, 1);
+    if (lane == 31) after = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss[i] += after;
+    const float end = __shfl_sync(0xffffffffu, ss[3], lane | 7);
+    float* to = gates + ((int64_t)blockIdx.x * a.H + h0 + k) * (3 * Q) + 4 * lane;
+    *reinterpret_cast<float4*>(to) = make_float4(ss[0], ss[1], ss[2], ss[3]);
+    *reinterpret_cast<float4*>(to + Q) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+    *reinterpret_cast<float4*>(to + 2 * Q) = make_float4(dt[0] * ex2(ss[0] - end), dt[1] * ex2(ss[1] - end),
+                                                         dt[2] * ex2(ss[2] - end), dt[3] * ex2(ss[3] - end));
+  }
 }
-__device__ __forceinline__ float activate(const SsmArgs& a, float v) { return a.softplus ? softplus_f(v) : v; }
 
 // Pieces [c0, c0 + n) of row j of a tile block to zero.
 template <int N>
@@ -305,7 +376,7 @@ __device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* 
 // ---------------------------------------------------------------------------
 // The walk: one block per (segment, head, 64 columns of the state).
 //   warp 0: the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
-//   warp 2: TMA;  warp 3: the gates
+//   warp 2: TMA loads;  warp 3: TMA stores of the outputs
 //   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
 //   groups 2, 3: the state (32 columns each)
 //   groups 4, 5: w x and the outputs (32 columns each)
@@ -316,22 +387,18 @@ __device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* 
 // U's hi and lo operands sit side by side as one of 128 columns.
 // ---------------------------------------------------------------------------
 constexpr int WALK_THREADS = 28 * 32;
-// TMEM columns: CB twice (16 of them a step of 16 K, over which M's hi and lo
-// are written, 8 columns each), U (hi products, lo products), Yo, Yd.
+// TMEM columns: CB twice (16 of them a step of 16 K, over the first 8 of which M
+// is written), U (hi products, lo products), Yo, Yd.
 constexpr uint32_t T_CB = 0, T_U = 256, T_YO = 384, T_YD = 448;
 
 struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
   unsigned char xw[2][BLK];  // hi, lo
-  unsigned char S[2][BLK];   // hi, lo
-  // A chunk's gates.
-  float gc[2][Q];  // prefix sums of dt A log2(e)
-  float dt[2][Q];
-  float w[Q];      // dt_j 2^(sum after j)
-  float gam[2];    // 2^gc[last]
+  unsigned char S[BLK];      // S0 in BF16
+  float gates[2][3 * Q];     // ss, dt, colf (Gates)
   // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
-  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], gates[2], xw_full[2], cb_full[2], m_full[2];
-  uint64_t w_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], cb_full[2], m_full[2], staged[2];
+  uint64_t u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -355,14 +422,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         tc::mbar_init(&s.bc_full[i], 1);
         tc::mbar_init(&s.bc_empty[i], 2);
         tc::mbar_init(&s.x_full[i], 1);
-        tc::mbar_init(&s.x_empty[i], 1 + 8);
-        tc::mbar_init(&s.gates[i], 1);
+        tc::mbar_init(&s.x_empty[i], 2);
+        tc::mbar_init(&s.staged[i], 8);
         tc::mbar_init(&s.xw_full[i], 8);
         tc::mbar_init(&s.cb_full[i], 1);
         tc::mbar_init(&s.m_full[i], 8);
         tc::mbar_init(&s.done[i], 1);
       }
-      tc::mbar_init(&s.w_full, 1);
       tc::mbar_init(&s.u_full, 1);
       tc::mbar_init(&s.u_empty, 8);
       tc::mbar_init(&s.s_full, 8);
@@ -386,6 +452,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   const int quad = warp & 3, r = 32 * quad + lane;         // TMEM lanes of the warp; row of the thread
   const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
   const int group = (warp >> 2) - 1, half = group & 1;
+  const float A = a.A[h] * LOG2E;
   // descriptor address units (16 bytes): a stage of B or C, a block, a step of
   // 16 K rows (MN-major); a step of 16 K elements (K-major: 32 bytes, four a block)
   constexpr uint32_t stage2 = 2 * BLK / 16, stage1 = BLK / 16, step = 2048 / 16;
@@ -394,7 +461,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   if (warp == 0) {
     constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
     constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
-    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S[0]);
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S);
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
@@ -414,10 +481,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < ksteps) {
-          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
-          mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + stage1 + k * step, i_yo, 1);
-        }
+        if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
       commit(&s.yo_full);
       commit(&s.y_full);
       commit(&s.bc_empty[b]);
@@ -455,10 +519,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 8; ++k)
         mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
-        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, 1);
-      }
       commit(&s.y_full);
       commit(&s.x_empty[b]);
     }
@@ -483,8 +545,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         }
         bc = c + 1;
         if (c >= 2 && !wait_or_abort(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
-        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)BLK);
+        tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)(BLK + sizeof(s.gates[0])));
         tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.x_full[b]);
+        tc::bulk_load(s.gates[b], gates_of(ta, sg.chunk0 + c, h).p, sizeof(s.gates[0]), &s.x_full[b]);
         x = c + 1;
       }
       // no copy is in flight when the block ends
@@ -495,85 +558,80 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     }
     __syncwarp();
   } else if (warp == 3) {
-    float raw[4];
-    load_raw(a, h, sg.tok0, sg.len, raw);
-    const float A = a.A[h] * LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < nch; ++c) {
+    for (int c = 0; c < nch && ok; ++c) {
       const int b = c & 1;
-      float dt[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dt[i] = 4 * lane + i < sg.len - c * Q ? activate(a, raw[i] + bias) : 0.f;
-      load_raw(a, h, sg.tok0 + (c + 1) * Q, sg.len - (c + 1) * Q, raw);
-      float g[4], r4[4];  // inclusive prefix; exclusive suffix (summed from the end, where it is small)
-      float run = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        run = fmaf(dt[i], A, run);
-        g[i] = run;
+      ok = warp_wait(&s.staged[b], (c >> 1) & 1, ab);
+      if (ok && lane == 0) {
+        if (sg.len - c * Q >= Q) {  // a whole chunk; a partial one was stored row by row
+          asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
+                           reinterpret_cast<uint64_t>(&ta.out_map)),
+                       "r"(p0), "r"(h), "r"(sg.tok0 + c * Q), "r"(tc::smem_u32(s.X[b]))
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        }
+        arrive(&s.x_empty[b]);
       }
-      float before, after;
-      scan_both(run, lane, before, after);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] += before;
-#pragma unroll
-      for (int i = 3; i >= 0; --i) {
-        r4[i] = dt[i] * ex2(after);
-        after = fmaf(dt[i], A, after);
-      }
-      bool ok = c < 2 || warp_wait(&s.x_empty[b], ((c >> 1) - 1) & 1, ab);
-      if (!ok) break;
-      if (lane == 31) s.gam[b] = ex2(g[3]);
-      *reinterpret_cast<float4*>(&s.gc[b][4 * lane]) = make_float4(g[0], g[1], g[2], g[3]);
-      *reinterpret_cast<float4*>(&s.dt[b][4 * lane]) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-      warp_arrive(&s.gates[b]);
-      ok = c == 0 || warp_wait(&s.xw_full[b ^ 1], ((c - 1) >> 1) & 1, ab);
-      if (!ok) break;
-      *reinterpret_cast<float4*>(&s.w[4 * lane]) = make_float4(r4[0], r4[1], r4[2], r4[3]);
-      warp_arrive(&s.w_full);
+      __syncwarp();
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    __syncwarp();
   } else if (group == 0 || group == 1) {
-    // M: thread = row r; zero above the diagonal
+    // M: thread = row r; column blocks b < quad by factors 2^(ss[end of b] - ss_r)
+    // colf_j, both at most 1; b == quad from the difference; zero above the diagonal
     const int j0 = 16 * half;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
-      bool ok = warp_wait(&s.gates[st], (c >> 1) & 1, ab) && warp_wait(&s.cb_full[st], (c >> 1) & 1, ab);
-      if (!ok) break;
+      const Gates g{s.gates[st]};
+      if (!warp_wait(&s.x_full[st], (c >> 1) & 1, ab) || !warp_wait(&s.cb_full[st], (c >> 1) & 1, ab)) break;
       tc::tc_fence_after();
-      const float gi = s.gc[st][r];
+      const float sr = g.ss()[r];
       const uint32_t cb = trow + T_CB + 128 * st + j0;
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
-        uint32_t hi[8], lo[8];
-        if (b <= quad) {
-          uint32_t v[16];
+        uint32_t v[16], m[8];
+        if (b < quad) {
+          tc::tmem_ld16(cb + 32 * b, v);
+          const float rf = ex2(g.ss()[32 * b + 31] - sr);
+          const uint64_t rr = pack2(rf, rf);
+          ulonglong2 cf[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            cf[j] = *reinterpret_cast<const ulonglong2*>(g.colf() + 32 * b + j0 + 4 * j);
+            cf[j].x = mul2(cf[j].x, rr);
+            cf[j].y = mul2(cf[j].y, rr);
+          }
+          wait_ld(v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            m[2 * j] = round2(mul2(pair_of(v + 4 * j), cf[j].x));
+            m[2 * j + 1] = round2(mul2(pair_of(v + 4 * j + 2), cf[j].y));
+          }
+        } else if (b == quad) {
           tc::tmem_ld16(cb + 32 * b, v);
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const float4 gj = *reinterpret_cast<const float4*>(&s.gc[st][32 * b + j0 + j]);
-            const float4 dj = *reinterpret_cast<const float4*>(&s.dt[st][32 * b + j0 + j]);
-            f[j] = dj.x * ex2(gi - gj.x);
-            f[j + 1] = dj.y * ex2(gi - gj.y);
-            f[j + 2] = dj.z * ex2(gi - gj.z);
-            f[j + 3] = dj.w * ex2(gi - gj.w);
+            const float4 sj = *reinterpret_cast<const float4*>(g.ss() + 32 * b + j0 + j);
+            const float4 dj = *reinterpret_cast<const float4*>(g.dt() + 32 * b + j0 + j);
+            f[j] = dj.x * ex2(sj.x - sr);
+            f[j + 1] = dj.y * ex2(sj.y - sr);
+            f[j + 2] = dj.z * ex2(sj.z - sr);
+            f[j + 3] = dj.w * ex2(sj.w - sr);
           }
           wait_ld(v);
-          const int last = b < quad ? 32 : lane - j0;  // the last column kept
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float m0 = j <= last ? __uint_as_float(v[j]) * f[j] : 0.f;
-            const float m1 = j + 1 <= last ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f;
-            split2(pack2(m0, m1), hi[j / 2], lo[j / 2]);
-          }
+          for (int j = 0; j < 16; j += 2)
+            m[j / 2] = round2(pack2(j0 + j <= lane ? __uint_as_float(v[j]) * f[j] : 0.f,
+                                    j0 + j + 1 <= lane ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f));
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
+          for (int j = 0; j < 8; ++j) m[j] = 0u;
         }
-        // over the columns just read
-        tmem_st8(cb + 32 * b, hi);
-        tmem_st8(cb + 32 * b + 8, lo);
+        tmem_st8(cb + 32 * b, m);  // over columns just read
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
@@ -616,27 +674,19 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     };
 #pragma unroll 1
     for (int c = 0; c <= nch; ++c) {
-      const int b = c & 1;
       if (c > 0) advance(c - 1);
       if (!ok || c == nch) break;
-      uint4 hi[4], lo[4];
+      uint4 v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        split2(S[4 * q], hi[q].x, lo[q].x);
-        split2(S[4 * q + 1], hi[q].y, lo[q].y);
-        split2(S[4 * q + 2], hi[q].z, lo[q].z);
-        split2(S[4 * q + 3], hi[q].w, lo[q].w);
-      }
-      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab);
+      for (int q = 0; q < 4; ++q)
+        v[q] = make_uint4(round2(S[4 * q]), round2(S[4 * q + 1]), round2(S[4 * q + 2]), round2(S[4 * q + 3]));
+      ok = warp_wait(&s.x_full[c & 1], (c >> 1) & 1, ab);
       // the previous chunk's Yo has read the operand
       if (c > 0) ok = ok && warp_wait(&s.yo_full, (c - 1) & 1, ab);
       if (!ok) break;
-      gam = s.gam[b];
+      gam = ex2(Gates{s.gates[c & 1]}.total(A));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        *reinterpret_cast<uint4*>(s.S[0] + piece(r, 4 * half + q)) = hi[q];
-        *reinterpret_cast<uint4*>(s.S[1] + piece(r, 4 * half + q)) = lo[q];
-      }
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(s.S + piece(r, 4 * half + q)) = v[q];
       tc::fence_proxy_async();
       warp_arrive(&s.s_full);
     }
@@ -656,7 +706,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = -1; c < nch; ++c) {
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
-        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab) && warp_wait(&s.w_full, (c + 1) & 1, ab);
+        const Gates g{s.gates[n]};
+        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab);
         if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
         if (len < Q) ok = ok && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
         if (!ok) break;
@@ -664,24 +715,26 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           clear_pieces<4>(s.X[n], r, 4 * half);
           if (half < nblk) clear_pieces<8>(s.B[n] + half * BLK, r, 0);
         }
-        build_xw<4>(s.X[n], s.xw[0], s.xw[1], r, 4 * half, s.w[r]);
+        build_xw<4>(s.X[n], s.xw[0], s.xw[1], r, 4 * half, g.dt()[r] * ex2(g.ss()[r]));
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[n]);
       }
       if (c < 0) continue;
       const int b = c & 1, len = sg.len - c * Q;
-      ok = warp_wait(&s.gates[b], (c >> 1) & 1, ab) && warp_wait(&s.y_full, c & 1, ab);
+      const Gates g{s.gates[b]};
+      const float e = ex2(g.total(A) - g.ss()[r]);  // the decay from the chunk's start
+      const uint64_t ee = pack2(e, e);
+      __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
+      ok = warp_wait(&s.y_full, c & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
-      const float e = ex2(s.gc[b][r]);
-      const uint64_t ee = pack2(e, e);
-      uint4 o[4];
 #pragma unroll
       for (int p = 0; p < 32; p += 8) {
         uint32_t yo[8], yd[8];
         tmem_ld8(trow + T_YO + 32 * half + p, yo);
         tmem_ld8(trow + T_YD + 32 * half + p, yd);
-        const uint4 xv = *reinterpret_cast<const uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
+        uint4* at = reinterpret_cast<uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
+        const uint4 xv = *at;
         const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
         wait_ld(yo);
         wait_ld(yd);
@@ -694,17 +747,15 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
           y[z] = *reinterpret_cast<const uint32_t*>(&t);
         }
-        o[p / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+        // a whole chunk's outputs take the place of x and leave by TMA
+        const uint4 yv = make_uint4(y[0], y[1], y[2], y[3]);
+        if (len >= Q) *at = yv;
+        else if (r < len && pc + p < a.P) *reinterpret_cast<uint4*>(out + p) = yv;
       }
       tc::tc_fence_before();
       warp_arrive(&s.y_empty);
-      if (lane == 0) arrive(&s.x_empty[b]);
-      if (r < len) {
-        __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (pc + 8 * q < a.P) *reinterpret_cast<uint4*>(out + 8 * q) = o[q];
-      }
+      tc::fence_proxy_async();
+      warp_arrive(&s.staged[b]);
     }
   }
   tc::tc_fence_before();
@@ -717,15 +768,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 // Summary of a segment (split documents only): its end state from a zero start,
 //   U = B^T (w x) with w_j = dt_j exp(sum of the gates after j in the segment),
 // accumulated in TMEM over its chunks, last chunk first, and its total decay.
-//   warp 0: TMA;  warp 1: MMA;  warp 2: gates;  warps 4-7 / 8-11: w x of the
-//   even / odd steps
+//   warp 0: TMA;  warp 1: MMA;  warps 4-7 / 8-11: w x of the even / odd steps
 // ---------------------------------------------------------------------------
 constexpr int SUM_THREADS = 384;
 struct SumSmem {
   unsigned char B[2][2 * BLK], X[2][BLK];
   unsigned char xw[2][2][BLK];  // step parity; hi, lo
-  float w[2][Q];
-  uint64_t full[2], empty[2], gates[2], xw_full[2], done;
+  uint64_t full[2], empty[2], xw_full[2], done;
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -749,7 +798,6 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&s.full[i], 1);
         tc::mbar_init(&s.empty[i], 1);
-        tc::mbar_init(&s.gates[i], 1);
         tc::mbar_init(&s.xw_full[i], 4);
       }
       tc::mbar_init(&s.done, 1);
@@ -802,47 +850,25 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     commit(&s.done);
     tc::mbar_wait(&s.done, 0);
     __syncwarp();
-  } else if (warp == 2) {
-    const float A = a.A[h] * LOG2E;
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-    float tail = 0.f, dt[4], raw[4];  // tail: the gates after this chunk
-    if (nch > 0) load_raw(a, h, sg.tok0 + (nch - 1) * Q, Q, raw);
-#pragma unroll 1
-    for (int k = 0; k < nch; ++k) {
-      const int b = k & 1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dt[i] = activate(a, raw[i] + bias);
-      if (k + 1 < nch) load_raw(a, h, sg.tok0 + (nch - 2 - k) * Q, Q, raw);
-      if (k >= 2 && !warp_wait(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
-      const float run = ((dt[0] + dt[1]) + (dt[2] + dt[3])) * A;
-      float before, after;
-      scan_both(run, lane, before, after);
-      const float inc = __shfl_sync(0xffffffffu, run + after, 0);
-      after += tail;
-      float4 v;
-      v.w = dt[3] * ex2(after);
-      after = fmaf(dt[3], A, after);
-      v.z = dt[2] * ex2(after);
-      after = fmaf(dt[2], A, after);
-      v.y = dt[1] * ex2(after);
-      after = fmaf(dt[1], A, after);
-      v.x = dt[0] * ex2(after);
-      *reinterpret_cast<float4*>(&s.w[b][4 * lane]) = v;
-      tail += inc;
-      warp_arrive(&s.gates[b]);
-    }
-    if (lane == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
   } else if (warp >= 4) {
     const int g = (warp - 4) >> 2, j = (tid - 128) & 127;
+    const float A = a.A[h] * LOG2E;
+    float tail = 0.f;  // the gates after this chunk
 #pragma unroll 1
-    for (int k = g; k < nch; k += 2) {
-      bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab) && warp_wait(&s.gates[g], (k >> 1) & 1, ab);
-      if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
-      if (!ok) break;
-      build_xw<8>(s.X[g], s.xw[g][0], s.xw[g][1], j, 0, s.w[g][j]);
-      tc::fence_proxy_async();
-      warp_arrive(&s.xw_full[g]);
+    for (int k = 0; k < nch; ++k) {
+      const Gates ga = gates_of(ta, sg.chunk0 + nch - 1 - k, h);
+      if ((k & 1) == g) {
+        const float w = __ldg(ga.dt() + j) * ex2(__ldg(ga.ss() + j) + tail);
+        bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab);
+        if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
+        if (!ok) break;
+        build_xw<8>(s.X[g], s.xw[g][0], s.xw[g][1], j, 0, w);
+        tc::fence_proxy_async();
+        warp_arrive(&s.xw_full[g]);
+      }
+      tail += ga.total(A);
     }
+    if (tid == 128 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
   }
   __syncthreads();
   tc::tc_fence_after();
@@ -971,12 +997,14 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
   const int64_t items = (int64_t)H * ((P + 63) / 64);
   const double sms = 152.0;
   int64_t nc = 0, most = 0;
+  int64_t gate_chunks = 0;
   for (int i = 0; i < N; ++i) {
     const int64_t ch = (cu[i + 1] - (int64_t)cu[i] + Q - 1) / Q;
     nc += ch;
+    gate_chunks += std::max<int64_t>(ch, 1);
     most = std::max(most, ch);
   }
-  SsmPlan best{(int)std::max<int64_t>(most, 1), N, false, 0};
+  SsmPlan best{(int)std::max<int64_t>(most, 1), N, 0, false, 0};
   double cost = std::max((double)(nc + kStart * N) * items / sms, most + kStart);
   // pieces of the longest document
   for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
@@ -998,8 +1026,10 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
       best.split = true;
     }
   }
+  best.chunks = gate_chunks;
+  best.scratch = up256((size_t)gate_chunks * H * 3 * Q * sizeof(float));
   if (best.split)
-    best.scratch = up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
+    best.scratch += up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
   return best;
 }
 
@@ -1014,16 +1044,23 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
     const uint64_t one = 8;  // a single token's stride is never used
     if (!token_map(&t.x_map, a.x, a.T, a.H, a.P, a.T > 1 ? a.ldx : (uint64_t)a.H * a.P * one) ||
         !token_map(&t.b_map, a.B, a.T, a.G, a.NS, a.T > 1 ? a.ldb : (uint64_t)a.G * a.NS * one) ||
-        !token_map(&t.c_map, a.C, a.T, a.G, a.NS, a.T > 1 ? a.ldc : (uint64_t)a.G * a.NS * one))
+        !token_map(&t.c_map, a.C, a.T, a.G, a.NS, a.T > 1 ? a.ldc : (uint64_t)a.G * a.NS * one) ||
+        !token_map(&t.out_map, a.out, a.T, a.H, a.P, a.T > 1 ? (uint64_t)a.H * a.P : (uint64_t)a.H * a.P * one))
       return cudaErrorInvalidValue;
   }
+  t.gates = static_cast<const float*>(scratch);
+  {
+    ProfScope ps("ssm_gates", st, (double)a.T * a.H);
+    k_ssm_gates<<<dim3((unsigned)plan.chunks, (a.H + 31) / 32), GATE_WARPS * 32, 0, st>>>(a.cu, a, static_cast<float*>(scratch));
+  }
+  if (cudaError_t e = cudaGetLastError()) return e;
+  char* rest = static_cast<char*>(scratch) + up256((size_t)plan.chunks * a.H * 3 * Q * sizeof(float));
   const unsigned grid = (unsigned)(plan.nseg * a.H * t.pblocks);
   constexpr int sm_walk = (int)sizeof(WalkSmem), sm_sum = (int)sizeof(SumSmem);
   static_assert(sm_walk <= 232448 && sm_sum <= 232448, "227 KB of shared memory a block");
   if (plan.split) {
-    t.seg = static_cast<float*>(scratch);
-    t.gsum = reinterpret_cast<float*>(static_cast<char*>(scratch) +
-                                      up256((size_t)plan.nseg * a.H * a.NS * a.P * sizeof(float)));
+    t.seg = reinterpret_cast<float*>(rest);
+    t.gsum = reinterpret_cast<float*>(rest + up256((size_t)plan.nseg * a.H * a.NS * a.P * sizeof(float)));
     cudaFuncSetAttribute(k_ssm_sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_sum);
     {
       ProfScope ps("ssm_sum", st, (double)a.T * a.H);

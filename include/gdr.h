@@ -261,7 +261,7 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * merge_bwd, walk_bwd, grad_state, grad, group_reduce (the _sum and merge
  * launches run only for split packs, l2norm only with qk_l2norm); the
  * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
- * sconv_step, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
+ * sconv_step, ssm_gates, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
  * gdn_step, norm_fwd, norm_bwd, norm_wgrad. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
