@@ -36,11 +36,12 @@ namespace {
 constexpr int Q = 128;        // tokens of a chunk
 constexpr int PT = 64;        // columns of the state that a block works on
 constexpr int BLK = Q * 128;  // bytes of a tile block: 128 rows of 64 BF16
+constexpr int GATES = 2 * Q + 96;  // floats of a chunk's gates
 
 struct TcArgs {
   CUtensorMap x_map, b_map, c_map, out_map;
   SsmArgs a;
-  const float* gates;  // [chunks][H][3][Q], written by k_ssm_gates (Gates)
+  const float* gates;  // [chunks][H][GATES], written by k_ssm_gates (Gates)
   int pblocks;      // ceil(P / 64)
   int lseg;         // chunks of a segment at most
   float* seg;       // [segments][H][NS][P]: start states of split documents' segments
@@ -58,7 +59,7 @@ struct Seg {
 //   ss[j]   sum of the a after token j: 2^(ss_j - ss_i) is the decay from j to i,
 //           and dt_j 2^ss_j = w_j keeps its accuracy, since ss is summed from the end
 //   dt[j]   activated (zero past the document's end)
-//   colf[j] dt_j 2^(ss_j - ss[end of j's 32 tokens])
+//   colf[j] dt_j 2^(ss_j - ss[end of j's 32 tokens]), j < 96
 struct Gates {
   const float* p;
   __device__ __forceinline__ const float* ss() const { return p; }
@@ -68,7 +69,7 @@ struct Gates {
   __device__ __forceinline__ float total(float A) const { return fmaf(*dt(), A, *ss()); }
 };
 __device__ __forceinline__ Gates gates_of(const TcArgs& t, int chunk, int h) {
-  return Gates{t.gates + ((int64_t)chunk * t.a.H + h) * (3 * Q)};
+  return Gates{t.gates + ((int64_t)chunk * t.a.H + h) * GATES};
 }
 
 // Finds segment `want` by a scan over the documents (one warp).
@@ -339,10 +340,11 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) k_ssm_gates(const int* __rest
 #pragma unroll
     for (int i = 0; i < 4; ++i) ss[i] += after;
     const float end = __shfl_sync(0xffffffffu, ss[3], lane | 7);
-    float* to = gates + ((int64_t)blockIdx.x * a.H + h0 + k) * (3 * Q) + 4 * lane;
+    float* to = gates + ((int64_t)blockIdx.x * a.H + h0 + k) * GATES + 4 * lane;
     *reinterpret_cast<float4*>(to) = make_float4(ss[0], ss[1], ss[2], ss[3]);
     *reinterpret_cast<float4*>(to + Q) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-    *reinterpret_cast<float4*>(to + 2 * Q) = make_float4(dt[0] * ex2(ss[0] - end), dt[1] * ex2(ss[1] - end),
+    if (lane < 24)
+      *reinterpret_cast<float4*>(to + 2 * Q) = make_float4(dt[0] * ex2(ss[0] - end), dt[1] * ex2(ss[1] - end),
                                                          dt[2] * ex2(ss[2] - end), dt[3] * ex2(ss[3] - end));
   }
 }
@@ -354,20 +356,19 @@ __device__ __forceinline__ void clear_pieces(unsigned char* tile, int j, int c0)
   for (int c = 0; c < N; ++c) *reinterpret_cast<uint4*>(tile + piece(j, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// w_j x_j of token row j, pieces [c0, c0 + n), as hi and lo blocks.
+// w_j times the pieces [c0, c0 + N) of token row j (in `x`), as hi and lo blocks.
 template <int N>
-__device__ __forceinline__ void build_xw(const unsigned char* x, unsigned char* hi, unsigned char* lo, int j, int c0,
+__device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* hi, unsigned char* lo, int j, int c0,
                                          float w) {
   const uint64_t ww = pack2(w, w);
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const uint32_t at = piece(j, c0 + c);
-    const uint4 v = *reinterpret_cast<const uint4*>(x + at);
     uint4 h, l;
-    split2(mul2(widen2(v.x), ww), h.x, l.x);
-    split2(mul2(widen2(v.y), ww), h.y, l.y);
-    split2(mul2(widen2(v.z), ww), h.z, l.z);
-    split2(mul2(widen2(v.w), ww), h.w, l.w);
+    split2(mul2(widen2(x[c].x), ww), h.x, l.x);
+    split2(mul2(widen2(x[c].y), ww), h.y, l.y);
+    split2(mul2(widen2(x[c].z), ww), h.z, l.z);
+    split2(mul2(widen2(x[c].w), ww), h.w, l.w);
     *reinterpret_cast<uint4*>(hi + at) = h;
     *reinterpret_cast<uint4*>(lo + at) = l;
   }
@@ -395,10 +396,11 @@ struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
   unsigned char xw[2][BLK];  // hi, lo
   unsigned char S[BLK];      // S0 in BF16
-  float gates[2][3 * Q];     // ss, dt, colf (Gates)
+  unsigned char Y[BLK];      // outputs on their way out
+  float gates[2][GATES];
   // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
-  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], cb_full[2], m_full[2], staged[2];
-  uint64_t u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], cb_full[2], m_full[2];
+  uint64_t u_full, u_empty, s_full, yo_full, y_full, y_empty, staged, y_free, done[2];
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -422,8 +424,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         tc::mbar_init(&s.bc_full[i], 1);
         tc::mbar_init(&s.bc_empty[i], 2);
         tc::mbar_init(&s.x_full[i], 1);
-        tc::mbar_init(&s.x_empty[i], 2);
-        tc::mbar_init(&s.staged[i], 8);
+        tc::mbar_init(&s.x_empty[i], 1 + 8 + 8);
         tc::mbar_init(&s.xw_full[i], 8);
         tc::mbar_init(&s.cb_full[i], 1);
         tc::mbar_init(&s.m_full[i], 8);
@@ -435,6 +436,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::mbar_init(&s.yo_full, 1);
       tc::mbar_init(&s.y_full, 2);
       tc::mbar_init(&s.y_empty, 8);
+      tc::mbar_init(&s.staged, 8);
+      tc::mbar_init(&s.y_free, 1);
       tc::mbar_fence_init();
     }
   }
@@ -561,18 +564,17 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch && ok; ++c) {
-      const int b = c & 1;
-      ok = warp_wait(&s.staged[b], (c >> 1) & 1, ab);
+      ok = warp_wait(&s.staged, c & 1, ab);
       if (ok && lane == 0) {
         if (sg.len - c * Q >= Q) {  // a whole chunk; a partial one was stored row by row
           asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
                            reinterpret_cast<uint64_t>(&ta.out_map)),
-                       "r"(p0), "r"(h), "r"(sg.tok0 + c * Q), "r"(tc::smem_u32(s.X[b]))
+                       "r"(p0), "r"(h), "r"(sg.tok0 + c * Q), "r"(tc::smem_u32(s.Y))
                        : "memory");
           asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         }
-        arrive(&s.x_empty[b]);
+        arrive(&s.y_free);
       }
       __syncwarp();
     }
@@ -685,6 +687,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       if (c > 0) ok = ok && warp_wait(&s.yo_full, (c - 1) & 1, ab);
       if (!ok) break;
       gam = ex2(Gates{s.gates[c & 1]}.total(A));
+      warp_arrive(&s.x_empty[c & 1]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(s.S + piece(r, 4 * half + q)) = v[q];
       tc::fence_proxy_async();
@@ -697,13 +700,44 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         if (pc + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
     }
   } else {
-    // w x and the outputs of token row r, columns p0 + 32 half + [0, 32)
+    // w x and the outputs of token row r, columns p0 + 32 half + [0, 32); x and the
+    // decay from the chunk's start stay in registers from the one to the other
     const int pc = p0 + 32 * half;
     const float D = a.D ? a.D[h] : 0.f;
     const uint64_t DD = pack2(D, D);
     bool ok = true;
+    uint4 x[4];
+    uint64_t ee = 0;
 #pragma unroll 1
     for (int c = -1; c < nch; ++c) {
+      if (c >= 0) {
+        const int len = sg.len - c * Q;
+        __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
+        ok = warp_wait(&s.y_full, c & 1, ab);
+        if (c > 0) ok = ok && warp_wait(&s.y_free, (c - 1) & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t yo[8], yd[8], y[4];
+          tmem_ld8(trow + T_YO + 32 * half + 8 * p, yo);
+          tmem_ld8(trow + T_YD + 32 * half + 8 * p, yd);
+          const uint32_t xs[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+          wait_ld(yo);
+          wait_ld(yd);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            y[z] = round2(fma2(DD, widen2(xs[z]), fma2(ee, pair_of(yo + 2 * z), pair_of(yd + 2 * z))));
+          // a whole chunk's outputs leave by TMA
+          const uint4 yv = make_uint4(y[0], y[1], y[2], y[3]);
+          if (len >= Q) *reinterpret_cast<uint4*>(s.Y + piece(r, 4 * half + p)) = yv;
+          else if (r < len && pc + 8 * p < a.P) *reinterpret_cast<uint4*>(out + 8 * p) = yv;
+        }
+        tc::tc_fence_before();
+        warp_arrive(&s.y_empty);
+        tc::fence_proxy_async();
+        warp_arrive(&s.staged);
+      }
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
         const Gates g{s.gates[n]};
@@ -715,47 +749,15 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           clear_pieces<4>(s.X[n], r, 4 * half);
           if (half < nblk) clear_pieces<8>(s.B[n] + half * BLK, r, 0);
         }
-        build_xw<4>(s.X[n], s.xw[0], s.xw[1], r, 4 * half, g.dt()[r] * ex2(g.ss()[r]));
+#pragma unroll
+        for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const uint4*>(s.X[n] + piece(r, 4 * half + p));
+        const float ss = g.ss()[r], w = g.dt()[r] * ex2(ss), e = ex2(g.total(A) - ss);
+        ee = pack2(e, e);
+        build_xw<4>(x, s.xw[0], s.xw[1], r, 4 * half, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[n]);
+        if (lane == 0) arrive(&s.x_empty[n]);
       }
-      if (c < 0) continue;
-      const int b = c & 1, len = sg.len - c * Q;
-      const Gates g{s.gates[b]};
-      const float e = ex2(g.total(A) - g.ss()[r]);  // the decay from the chunk's start
-      const uint64_t ee = pack2(e, e);
-      __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
-      ok = warp_wait(&s.y_full, c & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
-#pragma unroll
-      for (int p = 0; p < 32; p += 8) {
-        uint32_t yo[8], yd[8];
-        tmem_ld8(trow + T_YO + 32 * half + p, yo);
-        tmem_ld8(trow + T_YD + 32 * half + p, yd);
-        uint4* at = reinterpret_cast<uint4*>(s.X[b] + piece(r, 4 * half + p / 8));
-        const uint4 xv = *at;
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-        wait_ld(yo);
-        wait_ld(yd);
-        uint32_t y[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          float y0, y1;
-          const uint64_t v = fma2(ee, pair_of(yo + 2 * z), pair_of(yd + 2 * z));
-          unpack2(fma2(DD, widen2(xs[z]), v), y0, y1);
-          const __nv_bfloat162 t = __floats2bfloat162_rn(y0, y1);
-          y[z] = *reinterpret_cast<const uint32_t*>(&t);
-        }
-        // a whole chunk's outputs take the place of x and leave by TMA
-        const uint4 yv = make_uint4(y[0], y[1], y[2], y[3]);
-        if (len >= Q) *at = yv;
-        else if (r < len && pc + p < a.P) *reinterpret_cast<uint4*>(out + p) = yv;
-      }
-      tc::tc_fence_before();
-      warp_arrive(&s.y_empty);
-      tc::fence_proxy_async();
-      warp_arrive(&s.staged[b]);
     }
   }
   tc::tc_fence_before();
@@ -862,7 +864,10 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
         bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab);
         if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
         if (!ok) break;
-        build_xw<8>(s.X[g], s.xw[g][0], s.xw[g][1], j, 0, w);
+        uint4 x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[g] + piece(j, c));
+        build_xw<8>(x, s.xw[g][0], s.xw[g][1], j, 0, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[g]);
       }
@@ -1027,7 +1032,7 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
     }
   }
   best.chunks = gate_chunks;
-  best.scratch = up256((size_t)gate_chunks * H * 3 * Q * sizeof(float));
+  best.scratch = up256((size_t)gate_chunks * H * GATES * sizeof(float));
   if (best.split)
     best.scratch += up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
   return best;
@@ -1054,7 +1059,7 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
     k_ssm_gates<<<dim3((unsigned)plan.chunks, (a.H + 31) / 32), GATE_WARPS * 32, 0, st>>>(a.cu, a, static_cast<float*>(scratch));
   }
   if (cudaError_t e = cudaGetLastError()) return e;
-  char* rest = static_cast<char*>(scratch) + up256((size_t)plan.chunks * a.H * 3 * Q * sizeof(float));
+  char* rest = static_cast<char*>(scratch) + up256((size_t)plan.chunks * a.H * GATES * sizeof(float));
   const unsigned grid = (unsigned)(plan.nseg * a.H * t.pblocks);
   constexpr int sm_walk = (int)sizeof(WalkSmem), sm_sum = (int)sizeof(SumSmem);
   static_assert(sm_walk <= 232448 && sm_sum <= 232448, "227 KB of shared memory a block");
