@@ -469,16 +469,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const uint32_t b = c & 1;
-      // U = B^T (w x)
-      ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
-      commit(&s.u_full);
       // Yo = C S0
-      ok = warp_wait(&s.s_full, c & 1, ab);
+      ok = warp_wait(&s.s_full, c & 1, ab) && warp_wait(&s.bc_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
@@ -487,6 +479,14 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
       commit(&s.yo_full);
       commit(&s.y_full);
+      // U = B^T (w x)
+      ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mma_ss(tmem + T_U, d_b + b * stage2 + k * step, d_w + k * step, i_u, k > 0);
+      commit(&s.u_full);
       commit(&s.bc_empty[b]);
     }
     // no MMA is in flight when the block ends
@@ -517,7 +517,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       }
       if (c < 0) continue;
       // Yd = M x
-      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab) && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
+      // (M waited for x; the rows past the end are cleared with w x)
+      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab);
+      if (sg.len - c * Q < Q) ok = ok && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
