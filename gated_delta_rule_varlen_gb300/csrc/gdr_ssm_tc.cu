@@ -771,14 +771,17 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 // ---------------------------------------------------------------------------
 // Summary of a segment (split documents only): its end state from a zero start,
 //   U = B^T (w x) with w_j = dt_j exp(sum of the gates after j in the segment),
-// accumulated in TMEM over its chunks, last chunk first, and its total decay.
+// over its chunks, last chunk first, and its total decay.
 //   warp 0: TMA;  warp 1: MMA;  warps 4-7 / 8-11: w x of the even / odd steps
+// The tensor cores' FP32 accumulation truncates, a bias that grows with the
+// number of products: after kBatch chunks warps 4-7 add the sums up in registers,
+// while the other of two accumulators takes over.
 // ---------------------------------------------------------------------------
-constexpr int SUM_THREADS = 384;
+constexpr int SUM_THREADS = 384, SUM_STAGES = 3, kBatch = 4;
 struct SumSmem {
-  unsigned char B[2][2 * BLK], X[2][BLK];
+  unsigned char B[SUM_STAGES][2 * BLK], X[SUM_STAGES][BLK];
   unsigned char xw[2][2][BLK];  // step parity; hi, lo
-  uint64_t full[2], empty[2], xw_full[2], done;
+  uint64_t full[SUM_STAGES], empty[SUM_STAGES], xw_full[2], xw_empty[2], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -799,26 +802,31 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     if (lane == 0) {
       s.seg = sg;
       s.abort = 0;
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < SUM_STAGES; ++i) {
         tc::mbar_init(&s.full[i], 1);
         tc::mbar_init(&s.empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&s.xw_full[i], 4);
+        tc::mbar_init(&s.xw_empty[i], 1);
+        tc::mbar_init(&s.acc_full[i], 1);
+        tc::mbar_init(&s.acc_empty[i], 4);
       }
       tc::mbar_init(&s.done, 1);
       tc::mbar_fence_init();
     }
   }
   __syncthreads();
-  const Seg sg = s.seg;
+  const Seg sg = uniform(s.seg);
   if (sg.idx == sg.nseg - 1) return;  // no segment starts from this one's end
   if (warp == 1) {
-    tc::tmem_alloc(&s.tmem, 128);
+    tc::tmem_alloc(&s.tmem, 256);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
   const int nch = sg.len / Q;  // a segment that is not its document's last holds whole chunks
   volatile int* ab = &s.abort;
 
@@ -826,83 +834,123 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     if (lane == 0) {
       int issued = 0;
 #pragma unroll 1
-      for (int k = 0; k < nch; ++k) {
-        const int b = k & 1, row = sg.tok0 + (nch - 1 - k) * Q;
-        if (k >= 2 && !wait_or_abort(&s.empty[b], ((k >> 1) - 1) & 1, ab)) break;
+      for (int k = 0, b = 0, ph = 1; k < nch; ++k) {
+        const int row = sg.tok0 + (nch - 1 - k) * Q;
+        if (k >= SUM_STAGES && !wait_or_abort(&s.empty[b], ph, ab)) break;
         tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + nblk) * BLK));
+#pragma unroll 1
         for (int q = 0; q < nblk; ++q) tc::tma_load_3d(s.B[b] + q * BLK, &ta.b_map, 64 * q, grp, row, &s.full[b]);
         tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.full[b]);
         issued = k + 1;
+        if (++b == SUM_STAGES) {
+          b = 0;
+          ph ^= 1;
+        }
       }
-      for (int k = max(0, issued - 2); k < issued; ++k) tc::mbar_wait(&s.full[k & 1], (k >> 1) & 1);
+      // no copy is in flight when the block ends
+#pragma unroll 1
+      for (int k = max(0, issued - SUM_STAGES); k < issued; ++k)
+        tc::mbar_wait(&s.full[k % SUM_STAGES], (k / SUM_STAGES) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
     const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0][0]);
     constexpr uint32_t stage2 = 2 * BLK / 16, step = 2048 / 16;
+    uint32_t b = 0;
 #pragma unroll 1
     for (int k = 0; k < nch; ++k) {
-      const uint32_t b = k & 1;
-      if (!warp_wait(&s.xw_full[b], (k >> 1) & 1, ab)) break;
+      const uint32_t w = k & 1;
+      const int batch = k / kBatch, first = k % kBatch == 0;
+      const uint32_t acc = (batch & 1) * 128;
+      bool ok = warp_wait(&s.xw_full[w], (k >> 1) & 1, ab);  // (whose warps waited for B and x)
+      if (first && batch >= 2) ok = ok && warp_wait(&s.acc_empty[batch & 1], ((batch >> 1) - 1) & 1, ab);
+      if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        mma_ss(tmem, d_b + b * stage2 + q * step, d_w + b * stage2 + q * step, i_u, k + q > 0);
+        mma_ss(tmem + acc, d_b + b * stage2 + q * step, d_w + w * stage2 + q * step, i_u, !first || q > 0);
       commit(&s.empty[b]);
+      commit(&s.xw_empty[w]);
+      if (k % kBatch == kBatch - 1 || k == nch - 1) commit(&s.acc_full[batch & 1]);
+      b = b == SUM_STAGES - 1 ? 0 : b + 1;
     }
     commit(&s.done);
     tc::mbar_wait(&s.done, 0);
     __syncwarp();
   } else if (warp >= 4) {
     const int g = (warp - 4) >> 2, j = (tid - 128) & 127;
+    const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float A = a.A[h] * LOG2E;
+    const uint64_t one = pack2(1.f, 1.f);
     float tail = 0.f;  // the gates after this chunk
+    uint64_t S[PT / 2];  // state row j (warps 4-7)
+#pragma unroll
+    for (int q = 0; q < PT / 2; ++q) S[q] = 0;
+    auto drain = [&](int batch) {
+      if (!warp_wait(&s.acc_full[batch & 1], (batch >> 1) & 1, ab)) return false;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < PT; p += 8) {
+        uint32_t u[8], v[8];
+        tmem_ld8(trow + (batch & 1) * 128 + p, u);
+        tmem_ld8(trow + (batch & 1) * 128 + PT + p, v);
+        wait_ld(u);
+        wait_ld(v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          S[p / 2 + q] = fma2(one, fma2(one, pair_of(u + 2 * q), pair_of(v + 2 * q)), S[p / 2 + q]);
+      }
+      tc::tc_fence_before();
+      warp_arrive(&s.acc_empty[batch & 1]);
+      return true;
+    };
+    bool ok = true;
+    int drained = 0;
 #pragma unroll 1
-    for (int k = 0; k < nch; ++k) {
+    for (int k = 0, b = 0, ph = 0; k < nch; ++k) {
       const Gates ga = gates_of(ta, sg.chunk0 + nch - 1 - k, h);
       if ((k & 1) == g) {
-        const float w = __ldg(ga.dt() + j) * ex2(__ldg(ga.ss() + j) + tail);
-        bool ok = warp_wait(&s.full[g], (k >> 1) & 1, ab);
-        if (k >= 2) ok = ok && warp_wait(&s.empty[g], ((k >> 1) - 1) & 1, ab);
+        const float w = ga.dt()[j] * ex2(ga.ss()[j] + tail);
+        // (in this order: chunk k - 2 is done, so that chunk k - 3, which had this
+        // stage before, is known to have landed)
+        ok = k < 2 || warp_wait(&s.xw_empty[g], ((k >> 1) - 1) & 1, ab);
+        ok = ok && warp_wait(&s.full[b], ph, ab);
         if (!ok) break;
         uint4 x[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[g] + piece(j, c));
+        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[b] + piece(j, c));
         build_xw<8>(x, s.xw[g][0], s.xw[g][1], j, 0, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[g]);
       }
       tail += ga.total(A);
-    }
-    if (tid == 128 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
-  }
-  __syncthreads();
-  tc::tc_fence_after();
-  if (warp >= 4 && warp < 8 && !s.abort) {
-    const int n = tid - 128;
-    const uint32_t row = tmem + ((uint32_t)(32 * (warp - 4)) << 16);
-    float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + n) * a.P + p0;
-#pragma unroll
-    for (int p = 0; p < PT; p += 16) {
-      uint32_t u[16], v[16];
-      tc::tmem_ld16(row + p, u);
-      tc::tmem_ld16(row + PT + p, v);
-      wait_ld(u);
-      wait_ld(v);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) + __uint_as_float(v[q]));
-      if (n < a.NS) {
-#pragma unroll
-        for (int q = 0; q < 16; q += 4)
-          if (p0 + p + q < a.P) *reinterpret_cast<uint4*>(to + p + q) = make_uint4(u[q], u[q + 1], u[q + 2], u[q + 3]);
+      if (++b == SUM_STAGES) {
+        b = 0;
+        ph ^= 1;
       }
+      // a batch behind: its last product has had time to finish
+      if (g == 0 && k % kBatch == kBatch - 1 && k >= 2 * kBatch - 1) {
+        ok = drain(drained++);
+        if (!ok) break;
+      }
+    }
+    if (g == 0) {
+#pragma unroll 1
+      while (ok && drained * kBatch < nch) ok = drain(drained++);
+      if (ok && j < a.NS) {
+        float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + j) * a.P + p0;
+#pragma unroll
+        for (int q = 0; q < PT / 2; q += 2)
+          if (p0 + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
+      }
+      if (j == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && s.abort) atomicExch(ta.err, 10);
-  if (warp == 1) tc::tmem_dealloc(tmem, 128);
+  if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
 // The start states of split documents' segments, in place of the segments' own
