@@ -8,9 +8,9 @@
 //   S_end = exp(G_last) S0 + B^T (w x),  w_j = dt_j exp(sum_{k>j} a_k)
 // Four products of 128-row tiles (tcgen05, FP32 accumulators in TMEM):
 //   CB = C B^T,  Yo = C S0,  Yd = M x,  U = B^T (w x).
-// x, B and C are BF16 and enter exactly.  w x enters U as a pair of BF16 numbers
-// hi + lo (17 bits), so that the FP32 state, kept in registers from chunk to
-// chunk, stays within a few 1e-6.  M and S0, which only outputs depend on, enter
+// x, B and C are BF16 and enter exactly.  w x enters U as the sum of three BF16
+// numbers (24 bits), so that the state, kept in FP32 registers from chunk to
+// chunk, is that of FP32 arithmetic.  M and S0, which only outputs depend on, enter
 // as BF16 like x, B and C themselves: each term of an output's sums is rounded
 // once, to the precision the output is rounded to, and the sums are FP32.  (As
 // pairs they took 1.4 times the chunk's MMA time and half as many instructions
@@ -179,16 +179,14 @@ __device__ __forceinline__ uint32_t round2(uint64_t v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// A pair of FP32 numbers as BF16 pairs: hi rounded to nearest, lo the rest
-// rounded (off by at most 2^-18 of the number).
-__device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
-  float a, b;
-  unpack2(v, a, b);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  unpack2(fma2(widen2(hi), pack2(-1.f, -1.f), v), a, b);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(a, b);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+// A pair of FP32 numbers as three BF16 pairs, each the rest of the ones before it
+// rounded: all 24 bits.
+__device__ __forceinline__ void split3(uint64_t v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const uint64_t minus = pack2(-1.f, -1.f);
+  hi = round2(v);
+  v = fma2(widen2(hi), minus, v);
+  mid = round2(v);
+  lo = round2(fma2(widen2(mid), minus, v));
 }
 
 // Shared-memory matrix descriptors of 128-byte-swizzled tiles share their upper
@@ -356,21 +354,21 @@ __device__ __forceinline__ void clear_pieces(unsigned char* tile, int j, int c0)
   for (int c = 0; c < N; ++c) *reinterpret_cast<uint4*>(tile + piece(j, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// w_j times the pieces [c0, c0 + N) of token row j (in `x`), as hi and lo blocks.
+// w_j times the pieces [c0, c0 + N) of token row j (in `x`), as three blocks.
 template <int N>
-__device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* hi, unsigned char* lo, int j, int c0,
-                                         float w) {
+__device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char (*xw)[BLK], int j, int c0, float w) {
   const uint64_t ww = pack2(w, w);
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const uint32_t at = piece(j, c0 + c);
-    uint4 h, l;
-    split2(mul2(widen2(x[c].x), ww), h.x, l.x);
-    split2(mul2(widen2(x[c].y), ww), h.y, l.y);
-    split2(mul2(widen2(x[c].z), ww), h.z, l.z);
-    split2(mul2(widen2(x[c].w), ww), h.w, l.w);
-    *reinterpret_cast<uint4*>(hi + at) = h;
-    *reinterpret_cast<uint4*>(lo + at) = l;
+    uint4 h, m, l;
+    split3(mul2(widen2(x[c].x), ww), h.x, m.x, l.x);
+    split3(mul2(widen2(x[c].y), ww), h.y, m.y, l.y);
+    split3(mul2(widen2(x[c].z), ww), h.z, m.z, l.z);
+    split3(mul2(widen2(x[c].w), ww), h.w, m.w, l.w);
+    *reinterpret_cast<uint4*>(xw[0] + at) = h;
+    *reinterpret_cast<uint4*>(xw[1] + at) = m;
+    *reinterpret_cast<uint4*>(xw[2] + at) = l;
   }
 }
 
@@ -382,25 +380,23 @@ __device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* hi,
 //   groups 2, 3: the state (32 columns each)
 //   groups 4, 5: w x and the outputs (32 columns each)
 // Every role runs through the chunks on its own; barriers hand the buffers
-// over.  CB (and M, written over it) has two buffers, so that M of one chunk
-// follows M of the last without waiting for their products.  An MMA of 64
-// columns with both operands in shared memory reads A as often as one of 128:
-// U's hi and lo operands sit side by side as one of 128 columns.
+// over.  An MMA of 64 columns with both operands in shared memory takes as long
+// as one of 96 (it waits for A): the three operands of U sit side by side as one
+// of 192 columns.
 // ---------------------------------------------------------------------------
 constexpr int WALK_THREADS = 28 * 32;
-// TMEM columns: CB twice (16 of them a step of 16 K, over the first 8 of which M
-// is written), U (hi products, lo products), Yo, Yd.
-constexpr uint32_t T_CB = 0, T_U = 256, T_YO = 384, T_YD = 448;
+// TMEM columns: CB (16 of them a step of 16 K, over the first 8 of which M is
+// written), U (the three terms' products), Yo, Yd.
+constexpr uint32_t T_CB = 0, T_U = 128, T_YO = 320, T_YD = 384;
 
 struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
-  unsigned char xw[2][BLK];  // hi, lo
+  unsigned char xw[3][BLK];  // w x in three terms
   unsigned char S[BLK];      // S0 in BF16
-  unsigned char Y[BLK];      // outputs on their way out
   float gates[2][GATES];
   // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
-  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], cb_full[2], m_full[2];
-  uint64_t u_full, u_empty, s_full, yo_full, y_full, y_empty, staged, y_free, done[2];
+  uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], staged[2];
+  uint64_t cb_full, m_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -424,10 +420,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         tc::mbar_init(&s.bc_full[i], 1);
         tc::mbar_init(&s.bc_empty[i], 2);
         tc::mbar_init(&s.x_full[i], 1);
-        tc::mbar_init(&s.x_empty[i], 1 + 8 + 8);
+        tc::mbar_init(&s.x_empty[i], 1 + 8 + 1);
+        tc::mbar_init(&s.staged[i], 8);
         tc::mbar_init(&s.xw_full[i], 8);
-        tc::mbar_init(&s.cb_full[i], 1);
-        tc::mbar_init(&s.m_full[i], 8);
         tc::mbar_init(&s.done[i], 1);
       }
       tc::mbar_init(&s.u_full, 1);
@@ -436,8 +431,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::mbar_init(&s.yo_full, 1);
       tc::mbar_init(&s.y_full, 2);
       tc::mbar_init(&s.y_empty, 8);
-      tc::mbar_init(&s.staged, 8);
-      tc::mbar_init(&s.y_free, 1);
+      tc::mbar_init(&s.cb_full, 1);
+      tc::mbar_init(&s.m_full, 8);
       tc::mbar_fence_init();
     }
   }
@@ -463,7 +458,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 
   if (warp == 0) {
     constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
-    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 3 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
     const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]), d_s = desc_lo(s.S);
     bool ok = true;
 #pragma unroll 1
@@ -501,31 +496,27 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]);
     bool ok = true;
 #pragma unroll 1
-    for (int c = -1; c < nch; ++c) {
-      const uint32_t b = c & 1, n = b ^ 1;
-      if (c + 1 < nch) {  // CB = C B^T of the next chunk, once Yd has read the M in its columns
-        ok = warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
-        if (c > 0) ok = ok && warp_wait(&s.y_full, (c - 1) & 1, ab);
-        if (!ok) break;
-        tc::tc_fence_after();
+    for (int c = 0; c < nch; ++c) {
+      const uint32_t b = c & 1;
+      // CB = C B^T, once Yd has read the M in its columns
+      ok = warp_wait(&s.bc_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.y_full, (c - 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ksteps)
-            mma_ss(tmem + T_CB + 128 * n, d_c + n * stage2 + kmaj(k), d_b + n * stage2 + kmaj(k), i_cb, k > 0);
-        commit(&s.cb_full[n]);
-        commit(&s.bc_empty[n]);
-      }
-      if (c < 0) continue;
-      // Yd = M x
-      // (M waited for x; the rows past the end are cleared with w x)
-      ok = warp_wait(&s.m_full[b], (c >> 1) & 1, ab);
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps) mma_ss(tmem + T_CB, d_c + b * stage2 + kmaj(k), d_b + b * stage2 + kmaj(k), i_cb, k > 0);
+      commit(&s.cb_full);
+      commit(&s.bc_empty[b]);
+      // Yd = M x (M waited for x; the rows past the end are cleared with w x)
+      ok = warp_wait(&s.m_full, c & 1, ab);
       if (sg.len - c * Q < Q) ok = ok && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        mma_ts(tmem + T_YD, tmem + T_CB + 128 * b + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
+        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
       commit(&s.y_full);
       commit(&s.x_empty[b]);
     }
@@ -566,17 +557,18 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch && ok; ++c) {
-      ok = warp_wait(&s.staged, c & 1, ab);
+      const int b = c & 1;
+      ok = warp_wait(&s.staged[b], (c >> 1) & 1, ab);
       if (ok && lane == 0) {
         if (sg.len - c * Q >= Q) {  // a whole chunk; a partial one was stored row by row
           asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
                            reinterpret_cast<uint64_t>(&ta.out_map)),
-                       "r"(p0), "r"(h), "r"(sg.tok0 + c * Q), "r"(tc::smem_u32(s.Y))
+                       "r"(p0), "r"(h), "r"(sg.tok0 + c * Q), "r"(tc::smem_u32(s.X[b]))
                        : "memory");
           asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         }
-        arrive(&s.y_free);
+        arrive(&s.x_empty[b]);
       }
       __syncwarp();
     }
@@ -590,10 +582,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
       const Gates g{s.gates[st]};
-      if (!warp_wait(&s.x_full[st], (c >> 1) & 1, ab) || !warp_wait(&s.cb_full[st], (c >> 1) & 1, ab)) break;
+      if (!warp_wait(&s.x_full[st], (c >> 1) & 1, ab) || !warp_wait(&s.cb_full, c & 1, ab)) break;
       tc::tc_fence_after();
       const float sr = g.ss()[r];
-      const uint32_t cb = trow + T_CB + 128 * st + j0;
+      const uint32_t cb = trow + T_CB + j0;
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t v[16], m[8];
@@ -639,7 +631,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      warp_arrive(&s.m_full[st]);
+      warp_arrive(&s.m_full);
     }
   } else if (group == 2 || group == 3) {
     // state row n = r, columns p0 + 32 half + [0, 32)
@@ -664,14 +656,17 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       const uint64_t gg = pack2(gam, gam), one = pack2(1.f, 1.f);
 #pragma unroll
       for (int p = 0; p < 32; p += 8) {
-        uint32_t u[8], v[8];
+        uint32_t u[8], v[8], w[8];
         tmem_ld8(trow + T_U + 32 * half + p, u);
         tmem_ld8(trow + T_U + PT + 32 * half + p, v);
+        tmem_ld8(trow + T_U + 2 * PT + 32 * half + p, w);
         wait_ld(u);
         wait_ld(v);
+        wait_ld(w);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          S[p / 2 + q] = fma2(gg, S[p / 2 + q], fma2(one, pair_of(u + 2 * q), pair_of(v + 2 * q)));
+          S[p / 2 + q] = fma2(gg, S[p / 2 + q],
+                              fma2(one, pair_of(u + 2 * q), fma2(one, pair_of(v + 2 * q), pair_of(w + 2 * q))));
       }
       tc::tc_fence_before();
       warp_arrive(&s.u_empty);
@@ -716,7 +711,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         const int len = sg.len - c * Q;
         __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
         ok = warp_wait(&s.y_full, c & 1, ab);
-        if (c > 0) ok = ok && warp_wait(&s.y_free, (c - 1) & 1, ab);
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
@@ -730,15 +724,15 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
           for (int z = 0; z < 4; ++z)
             y[z] = round2(fma2(DD, widen2(xs[z]), fma2(ee, pair_of(yo + 2 * z), pair_of(yd + 2 * z))));
-          // a whole chunk's outputs leave by TMA
+          // a whole chunk's outputs take the place of x and leave by TMA
           const uint4 yv = make_uint4(y[0], y[1], y[2], y[3]);
-          if (len >= Q) *reinterpret_cast<uint4*>(s.Y + piece(r, 4 * half + p)) = yv;
+          if (len >= Q) *reinterpret_cast<uint4*>(s.X[c & 1] + piece(r, 4 * half + p)) = yv;
           else if (r < len && pc + 8 * p < a.P) *reinterpret_cast<uint4*>(out + 8 * p) = yv;
         }
         tc::tc_fence_before();
         warp_arrive(&s.y_empty);
         tc::fence_proxy_async();
-        warp_arrive(&s.staged);
+        warp_arrive(&s.staged[c & 1]);
       }
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
@@ -755,10 +749,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const uint4*>(s.X[n] + piece(r, 4 * half + p));
         const float ss = g.ss()[r], w = g.dt()[r] * ex2(ss), e = ex2(g.total(A) - ss);
         ee = pack2(e, e);
-        build_xw<4>(x, s.xw[0], s.xw[1], r, 4 * half, w);
+        build_xw<4>(x, s.xw, r, 4 * half, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[n]);
-        if (lane == 0) arrive(&s.x_empty[n]);
       }
     }
   }
@@ -777,10 +770,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 // number of products: after kBatch chunks warps 4-7 add the sums up in registers,
 // while the other of two accumulators takes over.
 // ---------------------------------------------------------------------------
-constexpr int SUM_THREADS = 384, SUM_STAGES = 3, kBatch = 4;
+constexpr int SUM_THREADS = 384, SUM_STAGES = 2, kBatch = 4;
 struct SumSmem {
   unsigned char B[SUM_STAGES][2 * BLK], X[SUM_STAGES][BLK];
-  unsigned char xw[2][2][BLK];  // step parity; hi, lo
+  unsigned char xw[2][3][BLK];  // step parity; w x in three terms
   uint64_t full[SUM_STAGES], empty[SUM_STAGES], xw_full[2], xw_empty[2], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
@@ -820,7 +813,7 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   const Seg sg = uniform(s.seg);
   if (sg.idx == sg.nseg - 1) return;  // no segment starts from this one's end
   if (warp == 1) {
-    tc::tmem_alloc(&s.tmem, 256);
+    tc::tmem_alloc(&s.tmem, 512);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
@@ -854,22 +847,22 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     }
     __syncwarp();
   } else if (warp == 1) {
-    constexpr uint32_t i_u = tc::idesc_bf16(128, 2 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
+    constexpr uint32_t i_u = tc::idesc_bf16(128, 3 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
     const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0][0]);
-    constexpr uint32_t stage2 = 2 * BLK / 16, step = 2048 / 16;
+    constexpr uint32_t stage2 = 2 * BLK / 16, stage3 = 3 * BLK / 16, step = 2048 / 16;
     uint32_t b = 0;
 #pragma unroll 1
     for (int k = 0; k < nch; ++k) {
       const uint32_t w = k & 1;
       const int batch = k / kBatch, first = k % kBatch == 0;
-      const uint32_t acc = (batch & 1) * 128;
+      const uint32_t acc = (batch & 1) * 256;
       bool ok = warp_wait(&s.xw_full[w], (k >> 1) & 1, ab);  // (whose warps waited for B and x)
       if (first && batch >= 2) ok = ok && warp_wait(&s.acc_empty[batch & 1], ((batch >> 1) - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        mma_ss(tmem + acc, d_b + b * stage2 + q * step, d_w + w * stage2 + q * step, i_u, !first || q > 0);
+        mma_ss(tmem + acc, d_b + b * stage2 + q * step, d_w + w * stage3 + q * step, i_u, !first || q > 0);
       commit(&s.empty[b]);
       commit(&s.xw_empty[w]);
       if (k % kBatch == kBatch - 1 || k == nch - 1) commit(&s.acc_full[batch & 1]);
@@ -892,14 +885,17 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       tc::tc_fence_after();
 #pragma unroll
       for (int p = 0; p < PT; p += 8) {
-        uint32_t u[8], v[8];
-        tmem_ld8(trow + (batch & 1) * 128 + p, u);
-        tmem_ld8(trow + (batch & 1) * 128 + PT + p, v);
+        uint32_t u[8], v[8], w[8];
+        tmem_ld8(trow + (batch & 1) * 256 + p, u);
+        tmem_ld8(trow + (batch & 1) * 256 + PT + p, v);
+        tmem_ld8(trow + (batch & 1) * 256 + 2 * PT + p, w);
         wait_ld(u);
         wait_ld(v);
+        wait_ld(w);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          S[p / 2 + q] = fma2(one, fma2(one, pair_of(u + 2 * q), pair_of(v + 2 * q)), S[p / 2 + q]);
+          S[p / 2 + q] =
+              fma2(one, fma2(one, pair_of(u + 2 * q), fma2(one, pair_of(v + 2 * q), pair_of(w + 2 * q))), S[p / 2 + q]);
       }
       tc::tc_fence_before();
       warp_arrive(&s.acc_empty[batch & 1]);
@@ -912,15 +908,13 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       const Gates ga = gates_of(ta, sg.chunk0 + nch - 1 - k, h);
       if ((k & 1) == g) {
         const float w = ga.dt()[j] * ex2(ga.ss()[j] + tail);
-        // (in this order: chunk k - 2 is done, so that chunk k - 3, which had this
-        // stage before, is known to have landed)
         ok = k < 2 || warp_wait(&s.xw_empty[g], ((k >> 1) - 1) & 1, ab);
         ok = ok && warp_wait(&s.full[b], ph, ab);
         if (!ok) break;
         uint4 x[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[b] + piece(j, c));
-        build_xw<8>(x, s.xw[g][0], s.xw[g][1], j, 0, w);
+        build_xw<8>(x, s.xw[g], j, 0, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[g]);
       }
@@ -950,7 +944,7 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && s.abort) atomicExch(ta.err, 10);
-  if (warp == 1) tc::tmem_dealloc(tmem, 256);
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
 
 // The start states of split documents' segments, in place of the segments' own
