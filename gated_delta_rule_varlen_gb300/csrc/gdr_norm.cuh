@@ -8,6 +8,8 @@
 // shuffles (and across warps through shared memory) in a fixed order.
 #pragma once
 #include "gdr_ops.cuh"
+#include <algorithm>
+
 #include "gdr_runtime.h"
 
 namespace gdr {
@@ -23,6 +25,7 @@ struct NormArgs {
   RowTensor x, gate, res;  // gate.p, res.p null when absent
   const void *w_post, *w;  // [D] or null
   int wf32;
+  int wvec;                // the weights can be read like the rows
   int sigmoid;             // act: 0 silu, 1 sigmoid
   float alpha, eps;
   void *h, *y;             // outputs, dense [rows][D], or null
@@ -32,17 +35,33 @@ struct NormArgs {
   float* part;             // [blocks][2][D]: partial dw, dw_post
 };
 
-// What a call needs decides the path: the smallest power-of-two group of
-// threads that holds the row, NV vectors of V elements each.
+// The threads of a row: TPR of them with NV vectors of V elements each.
 struct NormShape {
   int V, TPR, NV;
 };
 
-cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, int blocks, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int blocks, cudaStream_t st);
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, cudaStream_t st);
+// *blocks: how many blocks ran (and left a partial row each)
+cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* blocks, cudaStream_t st);
+
+// Most blocks of an SM that a backward is launched with, by threads of a block.
+constexpr int norm_blocks_per_sm(int threads) { return threads <= 128 ? 8 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1; }
 
 // Threads in a block of a shape: 128 for the shapes of up to a warp a row.
 constexpr int norm_threads(int TPR) { return TPR < 128 ? 128 : TPR; }
+
+// As many blocks as the GPU holds at a time (each goes through its share of the
+// rows), or fewer where there are fewer rows.
+template <typename K>
+int norm_grid(K kernel, int threads, size_t smem, int64_t groups, int occ_limit, int* occ_cache) {
+  if (*occ_cache == 0) {
+    int occ = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess || occ < 1) occ = 1;
+    *occ_cache = occ;
+  }
+  const int64_t most = (int64_t)152 * std::min(*occ_cache, occ_limit);
+  return (int)std::min<int64_t>(groups, most);
+}
 
 template <int TPR>
 struct RowGroup {
@@ -50,7 +69,20 @@ struct RowGroup {
   static constexpr int GROUPS = THREADS / TPR;  // rows a block works on at a time
   static constexpr int WARPS = TPR > 32 ? TPR / 32 : 1;
 
-  // Sums of a and b over the row's threads, on every thread of the row.
+  // Sum of a over the row's threads, on every thread of the row.
+  static __device__ __forceinline__ void sum(float& a, float2* sm) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int m = W / 2; m >= 1; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+    if constexpr (TPR > 32) {
+      const int warp = threadIdx.x >> 5;
+      if ((threadIdx.x & 31) == 0) sm[warp].x = a;
+      __syncthreads();
+      a = 0.f;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) a += sm[i].x;
+    }
+  }
   static __device__ __forceinline__ void sum2(float& a, float& b, float2* sm) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
@@ -59,7 +91,6 @@ struct RowGroup {
       b += __shfl_xor_sync(0xffffffffu, b, m);
     }
     if constexpr (TPR > 32) {
-      // two buffers in turn, so that one barrier per sum is enough
       const int warp = threadIdx.x >> 5;
       if ((threadIdx.x & 31) == 0) sm[warp] = make_float2(a, b);
       __syncthreads();
@@ -75,10 +106,64 @@ struct RowGroup {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ const T* row_ptr(const RowTensor& t, int64_t r, int R1) {
-  const int64_t i = r / R1;
-  return static_cast<const T*>(t.p) + i * t.s0 + (r - i * R1) * t.s1;
+// A row index as its two leading indices, advanced by a fixed number of rows
+// without a division.
+struct RowIndex {
+  int64_t r, i0;  // row; outer index
+  int i1, R1;     // inner index
+  int64_t step, step0;
+  int step1;
+  __device__ __forceinline__ RowIndex(int64_t first, int64_t step_, int R1_) : r(first), R1(R1_), step(step_) {
+    i0 = first / R1;
+    i1 = (int)(first - i0 * R1);
+    step0 = step / R1;
+    step1 = (int)(step - step0 * R1);
+  }
+  __device__ __forceinline__ void next() {
+    r += step;
+    i0 += step0;
+    i1 += step1;
+    if (i1 >= R1) {
+      i1 -= R1;
+      ++i0;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ const T* of(const RowTensor& t) const {
+    return static_cast<const T*>(t.p) + i0 * t.s0 + i1 * t.s1;
+  }
+};
+
+// V elements of a weight from c on, in pairs.
+template <typename T, int V>
+__device__ __forceinline__ void load_weight(const NormArgs& a, const void* p, int c, uint64_t (&f)[pairs_of<V>]) {
+  if (V > 1 && a.wvec) {
+    if (a.wf32) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + c + 4 * i));
+        f[2 * i] = v.x;
+        f[V > 1 ? 2 * i + 1 : 0] = v.y;
+      }
+    } else {
+      to_pairs<T, V>(vload<T, V>(static_cast<const T*>(p) + c), f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < pairs_of<V>; ++i)
+      f[i] = pack2(load_param<T>(p, a.wf32, c + 2 * i), 2 * i + 1 < V ? load_param<T>(p, a.wf32, c + 2 * i + 1) : 0.f);
+  }
 }
+
+// sigmoid(z) and z sigmoid(z) of a pair; the latter closes at z = -inf (where
+// the product would be 0 inf).
+__device__ __forceinline__ void gate_of(uint64_t z, uint64_t& sg, uint64_t& act, bool sigmoid) {
+  float a, b;
+  unpack2(z, a, b);
+  const float sa = sigmoid_f(a), sb = sigmoid_f(b);
+  sg = pack2(sa, sb);
+  act = sigmoid ? sg : pack2(a == -INFINITY ? 0.f : a * sa, b == -INFINITY ? 0.f : b * sb);
+}
+__device__ __forceinline__ uint64_t both(float a) { return pack2(a, a); }
 
 }  // namespace gdr

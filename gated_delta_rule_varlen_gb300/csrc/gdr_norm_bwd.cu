@@ -15,154 +15,229 @@ namespace gdr {
 namespace {
 
 // Bound by HBM.  A block keeps its columns' weight gradients in registers over
-// all its rows and leaves one partial row; k_norm_wgrad adds those.
+// all its rows and leaves one partial row; k_norm_wgrad adds those.  Threads of
+// few columns keep the weights in registers too.
 template <typename T, int V, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads(TPR)) k_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : 1)
+    k_norm_bwd(NormArgs a) {
   using G = RowGroup<TPR>;
+  constexpr int P = pairs_of<V>;
+  constexpr bool KEEP = NV * V <= 16;
   __shared__ float2 sm[3][G::WARPS];
   extern __shared__ float sred[];  // [GROUPS][D] when a block works on several rows
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float inv_d = 1.f / (float)a.D;
-  float dw[NV][V], dwp[NV][V];
+  const uint64_t one = both(1.f), minus = both(-1.f);
+  uint64_t dw[NV][P], dwp[NV][P];
+  uint64_t wk[KEEP ? NV : 1][P], pk[KEEP ? NV : 1][P];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    zero_pairs<V>(dw[i]);
+    zero_pairs<V>(dwp[i]);
+  }
+  if constexpr (KEEP) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) dw[i][v] = dwp[i][v] = 0.f;
-  for (int64_t base = (int64_t)blockIdx.x * G::GROUPS; base < a.rows; base += (int64_t)gridDim.x * G::GROUPS) {
-    const int64_t r = base + grp;
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+      if (c < a.D) {
+        if (a.w) load_weight<T, V>(a, a.w, c, wk[i]);
+        if (a.w_post) load_weight<T, V>(a, a.w_post, c, pk[i]);
+      }
+    }
+  }
+  // weight vector i of this thread
+  auto weight = [&](const uint64_t (&kept)[KEEP ? NV : 1][P], const void* p, int i, uint64_t (&f)[P]) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int q = 0; q < P; ++q) f[q] = kept[i][q];
+    } else {
+      load_weight<T, V>(a, p, (i * TPR + lane) * V, f);
+    }
+  };
+  RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
+#pragma unroll 1
+  for (; row.r - grp < a.rows; row.next()) {
+    const int64_t r = row.r;
     const bool live = r < a.rows;
     Vec<T, V> xr[NV], zr[NV], rr[NV], hr[NV], yr[NV];
-    if (live) {
-      const T* xp = row_ptr<T>(a.x, r, a.R1);
-      const T* zp = a.gate.p ? row_ptr<T>(a.gate, r, a.R1) : nullptr;
-      const T* rp = a.res.p ? row_ptr<T>(a.res, r, a.R1) : nullptr;
-      const T* hp = a.dh.p ? row_ptr<T>(a.dh, r, a.R1) : nullptr;
-      const T* yp = a.dy.p ? row_ptr<T>(a.dy, r, a.R1) : nullptr;
+    auto fetch = [&](const RowTensor& t, Vec<T, V> (&to)[NV]) {
+      if (!t.p || !live) return;
+      const T* p = row.template of<T>(t);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
-        if (c < a.D) {
-          xr[i] = vload<T, V>(xp + c);
-          if (zp) zr[i] = vload<T, V>(zp + c);
-          if (rp) rr[i] = vload<T, V>(rp + c);
-          if (hp) hr[i] = vload<T, V>(hp + c);
-          if (yp) yr[i] = vload<T, V>(yp + c);
-        }
+        if (c < a.D) to[i] = vload<T, V>(p + c);
       }
-    }
+    };
+    auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
+      if (!to || !live) return;
+      T* p = static_cast<T*>(to) + r * a.D;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * V;
+        if (c < a.D) store_pairs<T, V>(p + c, f[i]);
+      }
+    };
+    auto on = [&](int i) { return live && (i * TPR + lane) * V < a.D; };
+    fetch(a.x, xr);
+    fetch(a.gate, zr);
+    if (a.dy.p) fetch(a.res, rr);
+    fetch(a.dh, hr);
+    fetch(a.dy, yr);
     // r1
-    float r1 = 1.f, s = 0.f, s2 = 0.f;
+    float r1 = 1.f;
     if (a.w_post) {
+      uint64_t s2 = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (live && (i * TPR + lane) * V < a.D) {
+        if (on(i)) {
+          uint64_t x[P];
+          to_pairs<T, V>(xr[i], x);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float x = to_f<T>(xr[i].e[v]);
-            s = fmaf(x, x, s);
-          }
+          for (int q = 0; q < P; ++q) s2 = fma2(x[q], x[q], s2);
         }
-      G::sum2(s, s2, sm[0]);
+      float s = sum_of(s2);
+      G::sum(s, sm[0]);
       r1 = rsqrtf(fmaf(s, inv_d, a.eps));
     }
-    // h, its mean square and mean(dy w h)
-    float h[NV][V];
-    float r2 = 0.f, c2 = 0.f;
-    s = 0.f;
-    s2 = 0.f;
+    const uint64_t rr1 = both(r1);
+    // du starts as dH: dh and, through the second norm, dy
+    uint64_t du[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * V;
-      const bool on = live && c < a.D;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[i][v] = 0.f;
-        if (!on || !a.dy.p) continue;
-        float u = to_f<T>(xr[i].e[v]);
-        if (a.w_post) u *= r1 * load_param<T>(a.w_post, a.wf32, c + v);
-        if (a.gate.p) {
-          const float z = to_f<T>(zr[i].e[v]);
-          u *= a.sigmoid ? sigmoid_f(z) : silu_f(z);
-        }
-        if (a.res.p) u = fmaf(a.alpha, u, to_f<T>(rr[i].e[v]));
-        h[i][v] = u;
-        s = fmaf(u, u, s);
-        s2 = fmaf(to_f<T>(yr[i].e[v]) * load_param<T>(a.w, a.wf32, c + v), u, s2);
-      }
+      if (on(i) && a.dh.p) to_pairs<T, V>(hr[i], du[i]);
+      else zero_pairs<V>(du[i]);
     }
     if (a.dy.p) {
-      G::sum2(s, s2, sm[1]);
-      r2 = rsqrtf(fmaf(s, inv_d, a.eps));
-      c2 = s2 * r2 * inv_d;  // mean(dn hn)
-    }
-    // dH, dresidual, dgate, du; mean(dm xn)
-    s = 0.f;
-    s2 = 0.f;
-    float du[NV][V];
+      uint64_t h[NV][P], s2 = 0, t2 = 0;
+      const uint64_t alpha = both(a.alpha);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * V;
-      const bool on = live && c < a.D;
-      float dH[V], dz[V];
+      for (int i = 0; i < NV; ++i) {
+        zero_pairs<V>(h[i]);
+        if (on(i)) {
+          uint64_t f[P], y[P];
+          to_pairs<T, V>(xr[i], h[i]);
+          if (a.w_post) {
+            weight(pk, a.w_post, i, f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        du[i][v] = 0.f;
-        dH[v] = 0.f;
-        dz[v] = 0.f;
-        if (!on) continue;
-        float g = a.dh.p ? to_f<T>(hr[i].e[v]) : 0.f;
-        if (a.dy.p) {
-          const float dy = to_f<T>(yr[i].e[v]), hn = h[i][v] * r2;
-          dw[i][v] = fmaf(dy, hn, dw[i][v]);
-          const float dn = dy * load_param<T>(a.w, a.wf32, c + v);
-          g += r2 * (a.D > 1 ? dn - hn * c2 : dn * a.eps * r2 * r2);
+            for (int q = 0; q < P; ++q) h[i][q] = mul2(h[i][q], mul2(rr1, f[q]));
+          }
+          if (a.gate.p) {
+            uint64_t sg, act;
+            to_pairs<T, V>(zr[i], f);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+              gate_of(f[q], sg, act, a.sigmoid);
+              h[i][q] = mul2(h[i][q], act);
+            }
+          }
+          if (a.res.p) {
+            to_pairs<T, V>(rr[i], f);
+#pragma unroll
+            for (int q = 0; q < P; ++q) h[i][q] = fma2(alpha, h[i][q], f[q]);
+          }
+          weight(wk, a.w, i, f);
+          to_pairs<T, V>(yr[i], y);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            s2 = fma2(h[i][q], h[i][q], s2);
+            t2 = fma2(mul2(y[q], f[q]), h[i][q], t2);
+          }
         }
-        dH[v] = g;
-        g *= a.alpha;
-        const float x = to_f<T>(xr[i].e[v]), wp = a.w_post ? load_param<T>(a.w_post, a.wf32, c + v) : 1.f;
-        if (a.gate.p) {
-          const float z = to_f<T>(zr[i].e[v]), sg = sigmoid_f(z);
-          const float act = a.sigmoid ? sg : silu_f(z);
-          const float dact = a.sigmoid ? sg * (1.f - sg) : fmaf(act, 1.f - sg, sg);
-          dz[v] = g * (x * r1 * wp) * dact;
-          g *= act;
-        }
-        if (a.w_post) {
-          dwp[i][v] = fmaf(g, x * r1, dwp[i][v]);
-          g *= wp;
-          s = fmaf(g, x, s);
-        }
-        du[i][v] = g;
       }
-      if (on) {
-        if (a.dres) vstore<T, V>(static_cast<T*>(a.dres) + r * a.D + c, dH);
-        if (a.dgate) vstore<T, V>(static_cast<T*>(a.dgate) + r * a.D + c, dz);
-      }
+      float s = sum_of(s2), t = sum_of(t2);
+      G::sum2(s, t, sm[1]);
+      const float r2 = rsqrtf(fmaf(s, inv_d, a.eps));
+      const float c2 = t * r2 * inv_d;  // mean(dn hn)
+      // du += r2 (dn - hn c2); a single column: r2 dn eps r2^2
+      const uint64_t pa = both(a.D > 1 ? r2 : r2 * a.eps * r2 * r2), pb = both(a.D > 1 ? -r2 * r2 * c2 : 0.f);
+      const uint64_t rr2 = both(r2);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          uint64_t f[P], y[P];
+          weight(wk, a.w, i, f);
+          to_pairs<T, V>(yr[i], y);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            dw[i][q] = fma2(y[q], mul2(h[i][q], rr2), dw[i][q]);
+            du[i][q] = fma2(pa, mul2(y[q], f[q]), fma2(pb, h[i][q], du[i][q]));
+          }
+        }
     }
-    if (a.w_post) {
-      G::sum2(s, s2, sm[2]);
-      const float c1 = s * r1 * inv_d;  // mean(dm xn)
+    put(a.dres, du);
+    if (a.res.p) {
+      const uint64_t alpha = both(a.alpha);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float xn = live && (i * TPR + lane) * V < a.D ? to_f<T>(xr[i].e[v]) * r1 : 0.f;
-          du[i][v] = r1 * (a.D > 1 ? du[i][v] - xn * c1 : du[i][v] * a.eps * r1 * r1);
+        for (int q = 0; q < P; ++q) du[i][q] = mul2(alpha, du[i][q]);
+    }
+    if (a.gate.p) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          uint64_t z[P], n[P], p[P], sg, act;
+          to_pairs<T, V>(zr[i], z);
+          to_pairs<T, V>(xr[i], n);
+          if (a.w_post) {
+            weight(pk, a.w_post, i, p);
+#pragma unroll
+            for (int q = 0; q < P; ++q) n[q] = mul2(n[q], mul2(rr1, p[q]));
+          }
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            gate_of(z[q], sg, act, a.sigmoid);
+            // silu: sg + act (1 - sg); sigmoid: sg (1 - sg)
+            const uint64_t rest = fma2(minus, sg, one);
+            const uint64_t dact = a.sigmoid ? mul2(sg, rest) : fma2(act, rest, sg);
+            n[q] = mul2(mul2(du[i][q], n[q]), dact);
+            du[i][q] = mul2(du[i][q], act);
+          }
+          if (a.dgate) store_pairs<T, V>(static_cast<T*>(a.dgate) + r * a.D + (i * TPR + lane) * V, n);
         }
     }
-    if (a.dx && live) {
-      T* dxp = static_cast<T*>(a.dx) + r * a.D;
+    if (a.w_post) {
+      uint64_t s2 = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) vstore<T, V>(dxp + c, du[i]);
-      }
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          uint64_t x[P], p[P];
+          to_pairs<T, V>(xr[i], x);
+          weight(pk, a.w_post, i, p);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            x[q] = mul2(x[q], rr1);
+            dwp[i][q] = fma2(du[i][q], x[q], dwp[i][q]);
+            du[i][q] = mul2(du[i][q], p[q]);
+            s2 = fma2(du[i][q], x[q], s2);
+          }
+        }
+      float s = sum_of(s2);
+      G::sum(s, sm[2]);
+      const float c1 = s * inv_d;  // mean(dm xn)
+      // dx = r1 (dm - xn c1); a single column: r1 dm eps r1^2
+      const uint64_t pa = both(a.D > 1 ? r1 : r1 * a.eps * r1 * r1), pb = both(a.D > 1 ? -r1 * r1 * c1 : 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          uint64_t x[P];
+          to_pairs<T, V>(xr[i], x);
+#pragma unroll
+          for (int q = 0; q < P; ++q) du[i][q] = fma2(pa, du[i][q], mul2(pb, x[q]));
+        }
     }
+    put(a.dx, du);
     // rows that run one sum only would meet its buffer again
     if (TPR > 32 && !a.w_post) __syncthreads();
   }
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
-  auto leave = [&](float (&g)[NV][V], float* to) {
+  auto leave = [&](const uint64_t (&gp)[NV][P], float* to) {
+    float g[NV][V + 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < P; ++q) unpack2(gp[i][q], g[i][2 * q], g[i][2 * q + 1]);
     if constexpr (G::GROUPS == 1) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -195,36 +270,43 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_bwd(NormArgs a) {
 }
 
 // dw and dw_post: the blocks' partial rows added in a fixed order.
-__global__ void __launch_bounds__(512) k_norm_wgrad(const float* __restrict__ part, int blocks, int D, float* dw,
-                                                    float* dwp) {
+__global__ void __launch_bounds__(1024) k_norm_wgrad(const float* __restrict__ part, int blocks, int D, float* dw,
+                                                     float* dwp) {
   float* to = blockIdx.y == 0 ? dw : dwp;
   if (!to) return;
-  __shared__ float s[16][33];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
-  if (c < D)
-    for (int i = row; i < blocks; i += 16) sum += part[((int64_t)i * 2 + blockIdx.y) * D + c];
+  if (c < D) {
+#pragma unroll 8
+    for (int i = row; i < blocks; i += 32) sum += part[((int64_t)i * 2 + blockIdx.y) * D + c];
+  }
   s[row][lane] = sum;
   __syncthreads();
   if (row == 0 && c < D) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) sum += s[i][lane];
+    for (int i = 1; i < 32; ++i) sum += s[i][lane];
     to[c] = sum;
   }
 }
 
 template <typename T, int VT>
-cudaError_t launch_t(const NormArgs& a, const NormShape& s, int blocks, cudaStream_t st) {
-#define GDR_NORM_CASE(v, tpr, nv)                                                                       \
-  if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                         \
-    const size_t sm = RowGroup<tpr>::GROUPS > 1 ? (size_t)RowGroup<tpr>::GROUPS * a.D * sizeof(float) : 0; \
-    k_norm_bwd<T, v, tpr, nv><<<blocks, norm_threads(tpr), sm, st>>>(a);                                \
-    return cudaGetLastError();                                                                          \
+cudaError_t launch_t(const NormArgs& a, const NormShape& s, int* blocks, cudaStream_t st) {
+#define GDR_NORM_CASE(v, tpr, nv)                                                                              \
+  if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                                \
+    constexpr int groups = RowGroup<tpr>::GROUPS, threads = norm_threads(tpr);                                 \
+    const size_t sm = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;                                   \
+    static int occ = 0;                                                                                        \
+    *blocks = norm_grid(k_norm_bwd<T, v, tpr, nv>, threads, sm, (a.rows + groups - 1) / groups,                \
+                        norm_blocks_per_sm(threads), &occ);                                                    \
+    k_norm_bwd<T, v, tpr, nv><<<*blocks, threads, sm, st>>>(a);                                                \
+    return cudaGetLastError();                                                                                 \
   }
   GDR_NORM_CASE(VT, 8, 1)
   GDR_NORM_CASE(VT, 16, 1)
   GDR_NORM_CASE(VT, 32, 1)
+  GDR_NORM_CASE(VT, 32, 2)
   GDR_NORM_CASE(VT, 128, 1)
   GDR_NORM_CASE(VT, 256, 1)
   GDR_NORM_CASE(VT, 512, 1)
@@ -240,7 +322,7 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, int blocks, cudaStre
 
 }  // namespace
 
-cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int blocks, cudaStream_t st) {
+cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* blocks, cudaStream_t st) {
   switch (dtype) {
     case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, blocks, st);
     case GDR_DTYPE_F16: return launch_t<__half, 8>(a, s, blocks, st);
@@ -250,9 +332,9 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, in
 
 namespace {
 
-// Most blocks of a backward on rows of D elements (norm_blocks over the shapes
-// that such rows take): the partial rows its workspace has to hold.
-int max_norm_blocks(int D) { return D <= 1024 ? 152 * 8 : D <= 2048 ? 152 * 4 : 152 * 2; }
+// Most blocks of a backward on rows of D elements, over the shapes that such
+// rows take: the partial rows its workspace has to hold.
+int max_norm_blocks(int D) { return 152 * norm_blocks_per_sm(D <= 1024 ? 128 : D <= 2048 ? 256 : 512); }
 
 // Whether rows of D elements at these addresses and strides can be read in
 // 16-byte pieces.
@@ -261,31 +343,28 @@ bool rows16(const RowTensor& t, int V) {
 }
 
 // The threads that hold a row: 16-byte pieces where all rows allow them, else
-// single elements.
-NormShape norm_shape(int D, int dtype, bool vec) {
+// single elements.  Up to 512 columns of BF16 a backward's row stays within a
+// warp, and up to 1024 a forward's, whose threads hold less beside it (no barrier
+// a row); longer rows take one piece a thread in the backward and two in the
+// forward, more where a block would not hold them.
+NormShape norm_shape(int D, int dtype, bool vec, bool bwd) {
   const int V = dtype == GDR_DTYPE_F32 ? 4 : 8;
   if (vec && D % V == 0) {
     const int n = D / V;
     if (n <= 8) return {V, 8, 1};
     if (n <= 16) return {V, 16, 1};
     if (n <= 32) return {V, 32, 1};
-    if (n <= 128) return {V, 128, 1};
-    if (n <= 256) return {V, 256, 1};
-    if (n <= 512) return {V, 512, 1};
+    if (n <= 64) return {V, 32, 2};
+    if (n <= 128) return bwd ? NormShape{V, 128, 1} : NormShape{V, 32, 4};
+    if (n <= 256) return bwd ? NormShape{V, 256, 1} : NormShape{V, 128, 2};
+    if (n <= 512) return bwd ? NormShape{V, 512, 1} : NormShape{V, 256, 2};
     if (n <= 1024) return {V, 512, 2};
-    if (n <= 2048) return {V, 1024, 2};
+    if (n <= 2048) return bwd ? NormShape{V, 1024, 2} : NormShape{V, 512, 4};
     return {V, 1024, 4};
   }
   if (D <= 256) return {1, 32, 8};
   if (D <= 2048) return {1, 256, 8};
   return {1, 1024, 16};
-}
-
-int norm_blocks(int64_t rows, int TPR) {
-  const int threads = norm_threads(TPR);
-  const int64_t need = (rows + threads / TPR - 1) / (threads / TPR);
-  const int64_t most = 152 * (1024 / threads);
-  return (int)(need < most ? need : most);
 }
 
 gdr_status norm_check(int dtype, int wdtype, int64_t R0, int32_t R1, int32_t D, const void* x, const void* residual,
@@ -330,6 +409,7 @@ gdr_status norm_fwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   a.w_post = post_weight;
   a.w = weight;
   a.wf32 = wdtype == GDR_DTYPE_F32;
+  a.wvec = (((uintptr_t)post_weight | (uintptr_t)weight) & 15) == 0;
   a.sigmoid = act == GDR_ACT_SIGMOID;
   a.alpha = residual ? res_scale : 1.f;
   a.eps = eps;
@@ -338,9 +418,9 @@ gdr_status norm_fwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   const int V = dtype == GDR_DTYPE_F32 ? 4 : 8;
   const bool vec = rows16(a.x, V) && rows16(a.gate, V) && rows16(a.res, V) &&
                    (((uintptr_t)h | (uintptr_t)y) & 15) == 0;
-  const NormShape s = norm_shape(D, dtype, vec);
+  const NormShape s = norm_shape(D, dtype, vec, false);
   ProfScope ps("norm_fwd", stream, (double)a.rows * D);
-  return launch_norm_fwd(a, dtype, s, norm_blocks(a.rows, s.TPR), stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  return launch_norm_fwd(a, dtype, s, stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
 }
 
 gdr_status norm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
@@ -369,6 +449,7 @@ gdr_status norm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   a.w_post = post_weight;
   a.w = weight;
   a.wf32 = wdtype == GDR_DTYPE_F32;
+  a.wvec = (((uintptr_t)post_weight | (uintptr_t)weight) & 15) == 0;
   a.sigmoid = act == GDR_ACT_SIGMOID;
   a.alpha = residual ? res_scale : 1.f;
   a.eps = eps;
@@ -381,15 +462,15 @@ gdr_status norm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   const int V = dtype == GDR_DTYPE_F32 ? 4 : 8;
   const bool vec = rows16(a.x, V) && rows16(a.gate, V) && rows16(a.res, V) && rows16(a.dh, V) && rows16(a.dy, V) &&
                    (((uintptr_t)dx | (uintptr_t)dgate | (uintptr_t)dresidual) & 15) == 0;
-  const NormShape s = norm_shape(D, dtype, vec);
-  const int blocks = norm_blocks(a.rows, s.TPR);
-  if (blocks > 0) {
+  const NormShape s = norm_shape(D, dtype, vec, true);
+  int blocks = 0;
+  if (a.rows > 0) {
     ProfScope ps("norm_bwd", stream, (double)a.rows * D);
-    if (launch_norm_bwd(a, dtype, s, blocks, stream) != cudaSuccess) return GDR_CUDA_ERROR;
+    if (launch_norm_bwd(a, dtype, s, &blocks, stream) != cudaSuccess) return GDR_CUDA_ERROR;
   }
   if (dweight || dpost_weight) {
     ProfScope ps("norm_wgrad", stream);
-    k_norm_wgrad<<<dim3((D + 31) / 32, 2), 512, 0, stream>>>(a.part, blocks, D, dweight, dpost_weight);
+    k_norm_wgrad<<<dim3((D + 31) / 32, 2), 1024, 0, stream>>>(a.part, blocks, D, dweight, dpost_weight);
     if (cudaGetLastError() != cudaSuccess) return GDR_CUDA_ERROR;
   }
   return GDR_OK;

@@ -6,91 +6,120 @@ namespace {
 
 // Bound by HBM: each input read and each output written once.  Rows are dealt
 // to the blocks in turn; rows past the end keep their threads in the barriers.
+// Threads of few columns keep their weights in registers over all their rows.
+// Arithmetic in pairs of columns, so that its instructions fit beside the loads.
 template <typename T, int V, int TPR, int NV>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
   using G = RowGroup<TPR>;
+  constexpr int P = pairs_of<V>;
+  constexpr bool KEEP = NV * V <= 16;
   __shared__ float2 sm[2][G::WARPS];
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float inv_d = 1.f / (float)a.D;
-  for (int64_t base = (int64_t)blockIdx.x * G::GROUPS; base < a.rows; base += (int64_t)gridDim.x * G::GROUPS) {
-    const int64_t r = base + grp;
-    const bool live = r < a.rows;
+  uint64_t wk[KEEP ? NV : 1][P], pk[KEEP ? NV : 1][P];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+      if (c < a.D) {
+        if (a.w) load_weight<T, V>(a, a.w, c, wk[i]);
+        if (a.w_post) load_weight<T, V>(a, a.w_post, c, pk[i]);
+      }
+    }
+  }
+  RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
+#pragma unroll 1
+  for (; row.r - grp < a.rows; row.next()) {
+    const bool live = row.r < a.rows;
     Vec<T, V> xr[NV], zr[NV], rr[NV];
-    if (live) {
-      const T* xp = row_ptr<T>(a.x, r, a.R1);
-      const T* zp = a.gate.p ? row_ptr<T>(a.gate, r, a.R1) : nullptr;
-      const T* rp = a.res.p ? row_ptr<T>(a.res, r, a.R1) : nullptr;
+    auto fetch = [&](const RowTensor& t, Vec<T, V> (&to)[NV]) {
+      if (!t.p || !live) return;
+      const T* p = row.template of<T>(t);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
-        if (c < a.D) {
-          xr[i] = vload<T, V>(xp + c);
-          if (zp) zr[i] = vload<T, V>(zp + c);
-          if (rp) rr[i] = vload<T, V>(rp + c);
-        }
+        if (c < a.D) to[i] = vload<T, V>(p + c);
       }
-    }
-    float u[NV][V];
-    float ss = 0.f, dummy = 0.f;
+    };
+    auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
+      if (!to || !live) return;
+      T* p = static_cast<T*>(to) + row.r * a.D;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * V;
+        if (c < a.D) store_pairs<T, V>(p + c, f[i]);
+      }
+    };
+    auto mean_square = [&](const uint64_t (&f)[NV][P], float2* buf) {
+      uint64_t s = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int q = 0; q < P; ++q) s = fma2(f[i][q], f[i][q], s);
+      float ss = sum_of(s);
+      G::sum(ss, buf);
+      return fmaf(ss, inv_d, a.eps);
+    };
+    fetch(a.x, xr);
+    fetch(a.gate, zr);
+    fetch(a.res, rr);
+    uint64_t u[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool on = live && (i * TPR + lane) * V < a.D;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        u[i][v] = on ? to_f<T>(xr[i].e[v]) : 0.f;
-        ss = fmaf(u[i][v], u[i][v], ss);
-      }
+      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(xr[i], u[i]);
+      else zero_pairs<V>(u[i]);
     }
     if (a.w_post) {
-      G::sum2(ss, dummy, sm[0]);
-      const float r1 = rsqrtf(fmaf(ss, inv_d, a.eps));
+      const uint64_t r1 = both(rsqrtf(mean_square(u, sm[0])));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
         if (c < a.D) {
+          uint64_t w[P];
+          if constexpr (!KEEP) load_weight<T, V>(a, a.w_post, c, w);
 #pragma unroll
-          for (int v = 0; v < V; ++v) u[i][v] *= r1 * load_param<T>(a.w_post, a.wf32, c + v);
+          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r1, KEEP ? pk[KEEP ? i : 0][q] : w[q]));
         }
       }
     }
-    ss = 0.f;
+    if (a.gate.p && live) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool on = live && (i * TPR + lane) * V < a.D;
+      for (int i = 0; i < NV; ++i)
+        if ((i * TPR + lane) * V < a.D) {
+          uint64_t z[P], sg, act;
+          to_pairs<T, V>(zr[i], z);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (a.gate.p && on) {
-          const float z = to_f<T>(zr[i].e[v]);
-          u[i][v] *= a.sigmoid ? sigmoid_f(z) : silu_f(z);
+          for (int q = 0; q < P; ++q) {
+            gate_of(z[q], sg, act, a.sigmoid);
+            u[i][q] = mul2(u[i][q], act);
+          }
         }
-        if (a.res.p && on) u[i][v] = fmaf(a.alpha, u[i][v], to_f<T>(rr[i].e[v]));
-        ss = fmaf(u[i][v], u[i][v], ss);
-      }
     }
-    if (a.h && live) {
-      T* hp = static_cast<T*>(a.h) + r * a.D;
+    if (a.res.p && live) {
+      const uint64_t alpha = both(a.alpha);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((i * TPR + lane) * V < a.D) {
+          uint64_t r[P];
+          to_pairs<T, V>(rr[i], r);
+#pragma unroll
+          for (int q = 0; q < P; ++q) u[i][q] = fma2(alpha, u[i][q], r[q]);
+        }
+    }
+    put(a.h, u);
+    if (a.y) {
+      const uint64_t r2 = both(rsqrtf(mean_square(u, sm[1])));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
-        if (c < a.D) vstore<T, V>(hp + c, u[i]);
-      }
-    }
-    if (a.y) {
-      G::sum2(ss, dummy, sm[1]);
-      const float r2 = rsqrtf(fmaf(ss, inv_d, a.eps));
-      if (live) {
-        T* yp = static_cast<T*>(a.y) + r * a.D;
+        if (c < a.D) {
+          uint64_t w[P];
+          if constexpr (!KEEP) load_weight<T, V>(a, a.w, c, w);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (i * TPR + lane) * V;
-          if (c < a.D) {
-            float y[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[v] = u[i][v] * r2 * load_param<T>(a.w, a.wf32, c + v);
-            vstore<T, V>(yp + c, y);
-          }
+          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r2, KEEP ? wk[KEEP ? i : 0][q] : w[q]));
         }
       }
+      put(a.y, u);
     }
     // a row that runs only one of the two sums would meet its own buffer again
     if (TPR > 32 && !(a.w_post && a.y)) __syncthreads();
@@ -98,20 +127,24 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
 }
 
 template <typename T, int VT>
-cudaError_t launch_t(const NormArgs& a, const NormShape& s, int blocks, cudaStream_t st) {
-#define GDR_NORM_CASE(v, tpr, nv)                                             \
-  if (s.V == v && s.TPR == tpr && s.NV == nv) {                               \
-    k_norm_fwd<T, v, tpr, nv><<<blocks, norm_threads(tpr), 0, st>>>(a);       \
-    return cudaGetLastError();                                                \
+cudaError_t launch_t(const NormArgs& a, const NormShape& s, cudaStream_t st) {
+#define GDR_NORM_CASE(v, tpr, nv)                                                                              \
+  if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                                \
+    constexpr int groups = RowGroup<tpr>::GROUPS, threads = norm_threads(tpr);                                 \
+    static int occ = 0;                                                                                        \
+    const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv>, threads, 0, (a.rows + groups - 1) / groups, 32, &occ); \
+    k_norm_fwd<T, v, tpr, nv><<<blocks, threads, 0, st>>>(a);                                                  \
+    return cudaGetLastError();                                                                                 \
   }
   GDR_NORM_CASE(VT, 8, 1)
   GDR_NORM_CASE(VT, 16, 1)
   GDR_NORM_CASE(VT, 32, 1)
-  GDR_NORM_CASE(VT, 128, 1)
-  GDR_NORM_CASE(VT, 256, 1)
-  GDR_NORM_CASE(VT, 512, 1)
+  GDR_NORM_CASE(VT, 32, 2)
+  GDR_NORM_CASE(VT, 32, 4)
+  GDR_NORM_CASE(VT, 128, 2)
+  GDR_NORM_CASE(VT, 256, 2)
   GDR_NORM_CASE(VT, 512, 2)
-  GDR_NORM_CASE(VT, 1024, 2)
+  GDR_NORM_CASE(VT, 512, 4)
   GDR_NORM_CASE(VT, 1024, 4)
   GDR_NORM_CASE(1, 32, 8)
   GDR_NORM_CASE(1, 256, 8)
@@ -122,11 +155,11 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, int blocks, cudaStre
 
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, int blocks, cudaStream_t st) {
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, cudaStream_t st) {
   switch (dtype) {
-    case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, blocks, st);
-    case GDR_DTYPE_F16: return launch_t<__half, 8>(a, s, blocks, st);
-    default: return launch_t<float, 4>(a, s, blocks, st);
+    case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, st);
+    case GDR_DTYPE_F16: return launch_t<__half, 8>(a, s, st);
+    default: return launch_t<float, 4>(a, s, st);
   }
 }
 

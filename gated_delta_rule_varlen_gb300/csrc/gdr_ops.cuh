@@ -33,11 +33,71 @@ __device__ __forceinline__ void vstore(T* p, const float (&f)[V]) {
   *reinterpret_cast<Vec<T, V>*>(p) = v;
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + __expf(-z)); }
-// z sigmoid(z): 0 for z = -inf, where the product would be 0 * inf.
-__device__ __forceinline__ float silu_f(float z) {
-  const float e = __expf(-z);
-  return e == INFINITY ? 0.f : z / (1.f + e);
+// Pairs of FP32 operations as one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 1 / (1 + e^-z) from the approximate base-2 exponential and reciprocal (about
+// 3e-7 relative; 0 at -inf, 1 at inf).
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z * -LOG2E)));
+  return r;
+}
+
+// V elements as pairs (a single one: the pair's low half, beside zero).
+template <int V>
+constexpr int pairs_of = (V + 1) / 2;
+template <typename T, int V>
+__device__ __forceinline__ void to_pairs(const Vec<T, V>& v, uint64_t (&f)[pairs_of<V>]) {
+  if constexpr (V == 1) {
+    f[0] = pack2(to_f<T>(v.e[0]), 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = pack2(to_f<T>(v.e[2 * i]), to_f<T>(v.e[2 * i + 1]));
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t (&f)[pairs_of<V>]) {
+  float o[V + 1];
+#pragma unroll
+  for (int i = 0; i < pairs_of<V>; ++i) unpack2(f[i], o[2 * i], o[2 * i + 1]);
+  Vec<T, V> v;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v.e[i] = from_f<T>(o[i]);
+  *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+template <int V>
+__device__ __forceinline__ void zero_pairs(uint64_t (&f)[pairs_of<V>]) {
+#pragma unroll
+  for (int i = 0; i < pairs_of<V>; ++i) f[i] = 0;
+}
+// The sum of a pair.
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
 }
 
 // Parameter element (weights and biases come in the activations' type or FP32).

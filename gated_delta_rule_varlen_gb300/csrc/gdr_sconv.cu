@@ -24,48 +24,62 @@ struct ConvArgs {
   int cblocks;          // blocks along the channels; block b works on tile b / cblocks
 };
 
+// The filters of V channels from c on, one pair vector a tap, and their biases.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_filters(const ConvArgs& a, int c, uint64_t (&w)[W][pairs_of<V>],
+                                             uint64_t (&b)[pairs_of<V>]) {
+  auto at = [&](const void* p, int64_t i) { return load_param<T>(p, a.wf32, i); };
+#pragma unroll
+  for (int i = 0; i < pairs_of<V>; ++i) {
+    const bool two = 2 * i + 1 < V;
+    b[i] = a.bias ? pack2(at(a.bias, c + 2 * i), two ? at(a.bias, c + 2 * i + 1) : 0.f) : 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      w[j][i] = pack2(at(a.weight, (int64_t)(c + 2 * i) * W + j),
+                      two ? at(a.weight, (int64_t)(c + 2 * i + 1) * W + j) : 0.f);
+  }
+}
+// The W - 1 rows before token t of document d, which starts at ds.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_window(const ConvArgs& a, const T* x, const T* s0, int d, int ds, int t,
+                                            uint64_t (&win)[W - 1][pairs_of<V>]) {
+  constexpr int K = W - 1;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int p = t - K + k;
+    if (p >= ds) to_pairs<T, V>(vload<T, V>(x + (int64_t)p * a.ldx), win[k]);
+    else if (s0) to_pairs<T, V>(vload<T, V>(s0 + ((int64_t)d * K + (p - ds + K)) * a.C), win[k]);
+    else zero_pairs<V>(win[k]);
+  }
+}
+
 // One thread owns V adjacent channels and walks the tokens of one tile with
 // the last W - 1 inputs in registers, so each input is read once (and W - 1
-// rows again at a tile's start).  Bound by HBM: 2 reads or writes an element.
+// rows again at a tile's start).  Arithmetic in pairs of channels: the kernel is
+// bound by HBM (2 accesses an element) only while its instructions fit beside.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128) k_sconv_fwd(ConvArgs a) {
-  constexpr int K = W - 1;
+__global__ void __launch_bounds__(128, 4) k_sconv_fwd(ConvArgs a) {
+  constexpr int K = W - 1, P = pairs_of<V>;
   const int c = ((int)(blockIdx.x % a.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / a.cblocks;
   if (c >= a.C) return;
   const T* x = static_cast<const T*>(a.x) + c;
   const T* s0 = a.s0 ? static_cast<const T*>(a.s0) + c : nullptr;
   T* out = static_cast<T*>(a.out) + c;
   T* st = a.st ? static_cast<T*>(a.st) + c : nullptr;
-  float w[W][V], b[V], win[K][V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    b[v] = a.bias ? load_param<T>(a.bias, a.wf32, c + v) : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][v] = load_param<T>(a.weight, a.wf32, (int64_t)(c + v) * W + j);
-  }
+  uint64_t w[W][P], b[P], win[K][P];
+  load_filters<T, V, W>(a, c, w, b);
   const int t0 = tile_id * a.tile, t1 = min(a.T, t0 + a.tile);
-  auto start_window = [&](int d) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (s0) {
-        vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + k) * a.C), win[k]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[k][v] = 0.f;
-      }
-    }
-  };
   auto end_state = [&](int d) {
     if (!st) return;
 #pragma unroll
-    for (int k = 0; k < K; ++k) vstore<T, V>(st + ((int64_t)d * K + k) * a.C, win[k]);
+    for (int k = 0; k < K; ++k) store_pairs<T, V>(st + ((int64_t)d * K + k) * a.C, win[k]);
   };
   // The document the tile starts in; the empty documents at a position belong
   // to the tile that ends the token before them (position 0: to the first).
   int d = 0, t = t0;
   if (t0 == 0) {
     while (d < a.N && a.cu[d + 1] == 0) {
-      start_window(d);
+      load_window<T, V, W>(a, x, s0, d, 0, 0, win);
       end_state(d);
       ++d;
     }
@@ -74,39 +88,29 @@ __global__ void __launch_bounds__(128) k_sconv_fwd(ConvArgs a) {
   }
   while (t < t1) {
     const int ds = a.cu[d], de = a.cu[d + 1], e = min(de, t1);
-    if (t == ds) {
-      start_window(d);
-    } else {  // mid-document: the rows before the tile, the first ones from the start state
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int p = t - K + k;
-        if (p >= ds) {
-          vunpack<T, V>(vload<T, V>(x + (int64_t)p * a.ldx), win[k]);
-        } else if (s0) {
-          vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + (p - ds + K)) * a.C), win[k]);
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) win[k][v] = 0.f;
-        }
-      }
-    }
+    load_window<T, V, W>(a, x, s0, d, ds, t, win);
     auto token = [&](const Vec<T, V>& raw) {
-      float xv[V], y[V];
-      vunpack<T, V>(raw, xv);
+      uint64_t xv[P], y[P];
+      to_pairs<T, V>(raw, xv);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float z = b[v];
+      for (int i = 0; i < P; ++i) {
+        uint64_t z = b[i];
 #pragma unroll
-        for (int k = 0; k < K; ++k) z = fmaf(w[k][v], win[k][v], z);
-        z = fmaf(w[K][v], xv[v], z);
-        y[v] = a.silu ? silu_f(z) : z;
+        for (int k = 0; k < K; ++k) z = fma2(w[k][i], win[k][i], z);
+        z = fma2(w[K][i], xv[i], z);
+        if (a.silu) {
+          float z0, z1;
+          unpack2(z, z0, z1);
+          z = mul2(z, pack2(sigmoid_f(z0), V > 1 ? sigmoid_f(z1) : 0.f));
+        }
+        y[i] = z;
 #pragma unroll
-        for (int k = 0; k + 1 < K; ++k) win[k][v] = win[k + 1][v];
-        win[K - 1][v] = xv[v];
+        for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
+        win[K - 1][i] = xv[i];
       }
-      vstore<T, V>(out + (int64_t)t * a.C, y);
+      store_pairs<T, V>(out + (int64_t)t * a.C, y);
     };
-    constexpr int U = 8;  // rows in flight
+    constexpr int U = 6;  // rows in flight
     while (t + U <= e) {
       Vec<T, V> raw[U];
 #pragma unroll
@@ -117,12 +121,13 @@ __global__ void __launch_bounds__(128) k_sconv_fwd(ConvArgs a) {
         ++t;
       }
     }
+#pragma unroll 1
     for (; t < e; ++t) token(vload<T, V>(x + (int64_t)t * a.ldx));
     if (t == de) {
       end_state(d);
       ++d;
       while (d < a.N && a.cu[d + 1] == de) {
-        start_window(d);
+        load_window<T, V, W>(a, x, s0, d, de, de, win);
         end_state(d);
         ++d;
       }
@@ -145,8 +150,8 @@ struct ConvBwdArgs {
 // partial row per tile.  The tile's last rows need dz of the W - 1 tokens after
 // it, which are recomputed.  Bound by HBM: x and dout read, dx written.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128) k_sconv_bwd(ConvBwdArgs a) {
-  constexpr int K = W - 1;
+__global__ void __launch_bounds__(128, 4) k_sconv_bwd(ConvBwdArgs a) {
+  constexpr int K = W - 1, P = pairs_of<V>;
   const ConvArgs& f = a.f;
   const int c = ((int)(blockIdx.x % f.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / f.cblocks;
   if (c >= f.C) return;
@@ -156,32 +161,22 @@ __global__ void __launch_bounds__(128) k_sconv_bwd(ConvBwdArgs a) {
   const T* dst = a.dst ? static_cast<const T*>(a.dst) + c : nullptr;
   T* dx = static_cast<T*>(a.dx) + c;
   T* ds0 = a.ds0 ? static_cast<T*>(a.ds0) + c : nullptr;
-  float w[W][V], b[V], win[K][V], acc[K][V], dw[W][V], db[V];
+  const uint64_t one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f);
+  uint64_t w[W][P], b[P], win[K][P], acc[K][P], dw[W][P], db[P];
+  load_filters<T, V, W>(f, c, w, b);
+  zero_pairs<V>(db);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    b[v] = f.bias ? load_param<T>(f.bias, f.wf32, c + v) : 0.f;
-    db[v] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      w[j][v] = load_param<T>(f.weight, f.wf32, (int64_t)(c + v) * W + j);
-      dw[j][v] = 0.f;
-    }
-  }
+  for (int j = 0; j < W; ++j) zero_pairs<V>(dw[j]);
   const int t0 = tile_id * f.tile, t1 = min(f.T, t0 + f.tile);
-  // Row K - 1 - (number of rows after it) of an empty document's start state
-  // is its end state.
+  // The start state of an empty document is its end state.
   auto empty_doc = [&](int d) {
     if (!ds0) return;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float g[V];
-      if (dst) {
-        vunpack<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) g[v] = 0.f;
-      }
-      vstore<T, V>(ds0 + ((int64_t)d * K + k) * f.C, g);
+      uint64_t g[P];
+      if (dst) to_pairs<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
+      else zero_pairs<V>(g);
+      store_pairs<T, V>(ds0 + ((int64_t)d * K + k) * f.C, g);
     }
   };
   int d = 0, t = t0;
@@ -194,90 +189,97 @@ __global__ void __launch_bounds__(128) k_sconv_bwd(ConvBwdArgs a) {
     const int ds = f.cu[d], de = f.cu[d + 1];
     const bool fresh = t == ds;  // this tile owns the document's start-state rows
     const int e = min(de, t1);
+    load_window<T, V, W>(f, x, s0, d, ds, t, win);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int p = t - K + k;
-      if (p >= ds) {
-        vunpack<T, V>(vload<T, V>(x + (int64_t)p * f.ldx), win[k]);
-      } else if (s0) {
-        vunpack<T, V>(vload<T, V>(s0 + ((int64_t)d * K + (p - ds + K)) * f.C), win[k]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[k][v] = 0.f;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
-    }
+    for (int k = 0; k < K; ++k) zero_pairs<V>(acc[k]);
     const int own0 = fresh ? ds - K : t;  // rows [own0, t1) of this document are written here
     // dxx of row p is complete.
-    auto emit = [&](int p, const float (&g)[V]) {
+    auto emit = [&](int p, const uint64_t (&g)[P]) {
       if (p < own0 || p >= t1) return;
-      if (p >= ds) {
-        vstore<T, V>(dx + (int64_t)p * f.C, g);
-      } else if (ds0) {
-        vstore<T, V>(ds0 + ((int64_t)d * K + (p - ds + K)) * f.C, g);
-      }
+      if (p >= ds) store_pairs<T, V>(dx + (int64_t)p * f.C, g);
+      else if (ds0) store_pairs<T, V>(ds0 + ((int64_t)d * K + (p - ds + K)) * f.C, g);
     };
-    auto token = [&](int tt, const Vec<T, V>& rx, const Vec<T, V>& rg, bool mine) {
-      float xv[V], g[V], done[V];
-      vunpack<T, V>(rx, xv);
-      vunpack<T, V>(rg, g);
+    // Token tt: its dz, added to dw and dbias where the token is this tile's;
+    // `done` gets dxx of row tt - K.
+    auto token = [&](const Vec<T, V>& rx, const Vec<T, V>& rg, bool mine, uint64_t (&done)[P]) {
+      uint64_t xv[P], g[P];
+      to_pairs<T, V>(rx, xv);
+      to_pairs<T, V>(rg, g);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float z = b[v];
-#pragma unroll
-        for (int k = 0; k < K; ++k) z = fmaf(w[k][v], win[k][v], z);
-        z = fmaf(w[K][v], xv[v], z);
-        float dz = g[v];
+      for (int i = 0; i < P; ++i) {
+        uint64_t dz = g[i];
         if (f.silu) {
-          const float s = sigmoid_f(z);
-          dz *= fmaf(silu_f(z), 1.f - s, s);
+          uint64_t z = b[i];
+#pragma unroll
+          for (int k = 0; k < K; ++k) z = fma2(w[k][i], win[k][i], z);
+          z = fma2(w[K][i], xv[i], z);
+          float z0, z1;
+          unpack2(z, z0, z1);
+          const uint64_t s = pack2(sigmoid_f(z0), V > 1 ? sigmoid_f(z1) : 0.f);
+          // s + z s (1 - s)
+          dz = mul2(dz, fma2(mul2(z, s), fma2(minus, s, one), s));
         }
         if (mine) {
-          db[v] += dz;
+          db[i] = add2(db[i], dz);
 #pragma unroll
-          for (int k = 0; k < K; ++k) dw[k][v] = fmaf(dz, win[k][v], dw[k][v]);
-          dw[K][v] = fmaf(dz, xv[v], dw[K][v]);
+          for (int k = 0; k < K; ++k) dw[k][i] = fma2(dz, win[k][i], dw[k][i]);
+          dw[K][i] = fma2(dz, xv[i], dw[K][i]);
         }
         // acc[k]: row tt - K + k
-        done[v] = fmaf(w[0][v], dz, acc[0][v]);
+        done[i] = fma2(w[0][i], dz, acc[0][i]);
 #pragma unroll
-        for (int k = 0; k + 1 < K; ++k) acc[k][v] = fmaf(w[k + 1][v], dz, acc[k + 1][v]);
-        acc[K - 1][v] = w[K][v] * dz;
+        for (int k = 0; k + 1 < K; ++k) acc[k][i] = fma2(w[k + 1][i], dz, acc[k + 1][i]);
+        acc[K - 1][i] = mul2(w[K][i], dz);
 #pragma unroll
-        for (int k = 0; k + 1 < K; ++k) win[k][v] = win[k + 1][v];
-        win[K - 1][v] = xv[v];
+        for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
+        win[K - 1][i] = xv[i];
       }
-      emit(tt - K, done);
     };
+    auto rows = [&](int tt, Vec<T, V>& rx, Vec<T, V>& rg) {
+      rx = vload<T, V>(x + (int64_t)tt * f.ldx);
+      rg = vload<T, V>(dout + (int64_t)tt * a.ldo);
+    };
+    // the first K tokens, whose rows may be the start state's or another tile's
+#pragma unroll 1
+    for (int head = min(e, t + K); t < head; ++t) {
+      Vec<T, V> rx, rg;
+      uint64_t done[P];
+      rows(t, rx, rg);
+      token(rx, rg, true, done);
+      emit(t - K, done);
+    }
     constexpr int U = 4;  // rows in flight
     while (t + U <= e) {
       Vec<T, V> rx[U], rg[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        rx[i] = vload<T, V>(x + (int64_t)(t + i) * f.ldx);
-        rg[i] = vload<T, V>(dout + (int64_t)(t + i) * a.ldo);
-      }
+      for (int i = 0; i < U; ++i) rows(t + i, rx[i], rg[i]);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        token(t, rx[i], rg[i], true);
-        ++t;
+        uint64_t done[P];
+        token(rx[i], rg[i], true, done);
+        store_pairs<T, V>(dx + (int64_t)(t + i - K) * f.C, done);
       }
+      t += U;
     }
-    for (; t < e; ++t)
-      token(t, vload<T, V>(x + (int64_t)t * f.ldx), vload<T, V>(dout + (int64_t)t * a.ldo), true);
-    // The tokens after the tile that the tile's last rows feed.
-    int tt = e;
-    for (; tt < min(de, e + K); ++tt)
-      token(tt, vload<T, V>(x + (int64_t)tt * f.ldx), vload<T, V>(dout + (int64_t)tt * a.ldo), false);
-    if (tt == de) {  // the document's last rows: the end state's gradient joins
+    // the rest, and the tokens after the tile that the tile's last rows feed
+    const int tail = min(de, e + K);
+#pragma unroll 1
+    for (int tt = t; tt < tail; ++tt) {
+      Vec<T, V> rx, rg;
+      uint64_t done[P];
+      rows(tt, rx, rg);
+      token(rx, rg, tt < e, done);
+      emit(tt - K, done);
+    }
+    t = e;
+    if (tail == de) {  // the document's last rows: the end state's gradient joins
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (dst) {
-          float g[V];
-          vunpack<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
+          uint64_t g[P];
+          to_pairs<T, V>(vload<T, V>(dst + ((int64_t)d * K + k) * f.C), g);
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[k][v] += g[v];
+          for (int i = 0; i < P; ++i) acc[k][i] = add2(acc[k][i], g[i]);
         }
         emit(de - K + k, acc[k]);
       }
@@ -289,27 +291,31 @@ __global__ void __launch_bounds__(128) k_sconv_bwd(ConvBwdArgs a) {
   }
   float* part = a.part + (int64_t)tile_id * (W + 1) * f.C + c;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+  for (int j = 0; j <= W; ++j) {
+    float o[V + 1];
 #pragma unroll
-    for (int j = 0; j < W; ++j) part[(int64_t)j * f.C + v] = dw[j][v];
-    part[(int64_t)W * f.C + v] = db[v];
+    for (int i = 0; i < P; ++i) unpack2(j < W ? dw[j < W ? j : 0][i] : db[i], o[2 * i], o[2 * i + 1]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[(int64_t)j * f.C + v] = o[v];
   }
 }
 
 // dw[c][j] and dbias[c]: the tiles' partial rows summed in a fixed order.
-__global__ void __launch_bounds__(256) k_sconv_wgrad(const float* __restrict__ part, int tiles, int C, int W,
+__global__ void __launch_bounds__(512) k_sconv_wgrad(const float* __restrict__ part, int tiles, int C, int W,
                                                      float* dw, float* db) {
-  __shared__ float s[8][33];
+  __shared__ float s[16][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
   float sum = 0.f;
-  if (c < C)
-    for (int i = row; i < tiles; i += 8) sum += part[((int64_t)i * (W + 1) + j) * C + c];
+  if (c < C) {
+#pragma unroll 8
+    for (int i = row; i < tiles; i += 16) sum += part[((int64_t)i * (W + 1) + j) * C + c];
+  }
   s[row][lane] = sum;
   __syncthreads();
   if (row == 0 && c < C) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += s[i][lane];
+    for (int i = 1; i < 16; ++i) sum += s[i][lane];
     if (j < W) dw[(int64_t)c * W + j] = sum;
     else if (db) db[c] = sum;
   }
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(128) k_sconv_step(ConvStepArgs a) {
 #pragma unroll
       for (int j = 0; j < W; ++j)
         z = fmaf(load_param<T>(a.weight, a.wf32, (int64_t)(c + v) * W + j), to_f<T>(win[j].e[v]), z);
-      y[v] = a.silu ? silu_f(z) : z;
+      y[v] = a.silu ? z * sigmoid_f(z) : z;
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) *reinterpret_cast<Vec<T, V>*>(st + (int64_t)k * a.C) = win[k + 1];
@@ -362,19 +368,22 @@ __global__ void __launch_bounds__(128) k_sconv_step(ConvStepArgs a) {
   }
 }
 
-// Tokens a thread walks: long enough that the rows read again at a tile's
-// start stay a small share, short enough that the grid fills the GPU.
-int tile_tokens(int64_t T, int64_t vec_channels) {
-  const int64_t blocks = (vec_channels + 127) / 128;
-  int64_t tile = (T * blocks + 152 * 16 - 1) / (152 * 16);
-  tile = (tile + 7) / 8 * 8;
+// Tokens a thread walks: about `most`, so that the rows read again at a tile's
+// ends stay a small share, and such that the blocks fill whole waves of `wave`
+// blocks (what the GPU holds at a time); short tiles only where there is too
+// little to fill one.
+int tile_tokens(int64_t T, int64_t cblocks, int wave, int most) {
+  int64_t waves = (T * cblocks + (int64_t)wave * most - 1) / ((int64_t)wave * most);
+  if (waves < 1) waves = 1;
+  int64_t tiles = wave * waves / cblocks;
+  if (tiles < 1) tiles = 1;
+  int64_t tile = (T + tiles - 1) / tiles;
   if (tile < 16) tile = 16;
-  if (tile > 256) tile = 256;
   return (int)tile;
 }
 // The partial rows a backward leaves do not depend on alignment, so that the
-// workspace does not either: its tile is that of single-channel threads.
-int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, (C + 3) / 4); }
+// workspace does not either: its tile is that of threads of eight bytes of BF16.
+int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, ((C + 3) / 4 + 127) / 128, 152 * 4, 256); }
 
 size_t elem(int dtype) { return dtype == GDR_DTYPE_F32 ? 4 : 2; }
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -433,8 +442,8 @@ gdr_status sconv_fwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   const int V = 16 / (int)elem(dtype);
   const bool vec = C % V == 0 && ldx % V == 0 && on16(x) && on16(out) && on16(s0) && on16(st);
   const int nv = vec ? C / V : C;
-  a.tile = tile_tokens(T, nv);
   a.cblocks = (nv + 127) / 128;
+  a.tile = tile_tokens(T, a.cblocks, 152 * 4, 128);
   const int64_t grid = (T > 0 ? (T + a.tile - 1) / a.tile : 1) * a.cblocks;
   if (grid > INT32_MAX) return GDR_INVALID_ARG;
   ProfScope ps("sconv_fwd", stream, (double)T * C);
@@ -487,7 +496,7 @@ gdr_status sconv_bwd(int dtype, const void* x, int64_t ldx, const void* weight, 
     if (e != cudaSuccess) return GDR_CUDA_ERROR;
   }
   ProfScope ps("sconv_wgrad", stream);
-  k_sconv_wgrad<<<dim3((C + 31) / 32, W + 1), 256, 0, stream>>>(a.part, (int)tiles, C, W, dweight, dbias);
+  k_sconv_wgrad<<<dim3((C + 31) / 32, W + 1), 512, 0, stream>>>(a.part, (int)tiles, C, W, dweight, dbias);
   return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
 }
 
