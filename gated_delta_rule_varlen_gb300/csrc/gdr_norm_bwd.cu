@@ -16,8 +16,8 @@ namespace {
 
 // Bound by HBM.  A block keeps its columns' weight gradients in registers over
 // all its rows and leaves one partial row; k_norm_wgrad adds those.  Threads of
-// few columns keep the weights in registers too.
-template <typename T, int V, int TPR, int NV>
+// few columns keep the weights in registers too.  OUT: as in the forward.
+template <typename T, int V, int TPR, int NV, bool OUT>
 __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : 1)
     k_norm_bwd(NormArgs a) {
   using G = RowGroup<TPR>;
@@ -28,11 +28,12 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const float inv_d = 1.f / (float)a.D;
   const uint64_t one = both(1.f), minus = both(-1.f);
-  uint64_t dw[NV][P], dwp[NV][P];
+  const bool has_res = !OUT && a.res.p, has_dy = !OUT && a.dy.p;
+  uint64_t dw[OUT ? 1 : NV][P], dwp[NV][P];
   uint64_t wk[KEEP ? NV : 1][P], pk[KEEP ? NV : 1][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    zero_pairs<V>(dw[i]);
+    zero_pairs<V>(dw[OUT ? 0 : i]);
     zero_pairs<V>(dwp[i]);
   }
   if constexpr (KEEP) {
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * V;
       if (c < a.D) {
-        if (a.w) load_weight<T, V>(a, a.w, c, wk[i]);
+        if (!OUT && a.w) load_weight<T, V>(a, a.w, c, wk[i]);
         if (a.w_post) load_weight<T, V>(a, a.w_post, c, pk[i]);
       }
     }
@@ -55,20 +56,43 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     }
   };
   RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
-#pragma unroll 1
-  for (; row.r - grp < a.rows; row.next()) {
-    const int64_t r = row.r;
-    const bool live = r < a.rows;
-    Vec<T, V> xr[NV], zr[NV], rr[NV], hr[NV], yr[NV];
-    auto fetch = [&](const RowTensor& t, Vec<T, V> (&to)[NV]) {
-      if (!t.p || !live) return;
-      const T* p = row.template of<T>(t);
+  struct Raw {
+    Vec<T, V> x[NV], z[NV], h[NV], r[OUT ? 1 : NV], y[OUT ? 1 : NV];
+  };
+  auto ask = [&](const RowIndex& at, Raw& raw) {
+    if (at.r >= a.rows) return;
+    auto fetch = [&](const RowTensor& t, auto& to) {
+      const T* p = at.template of<T>(t);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
         if (c < a.D) to[i] = vload<T, V>(p + c);
       }
     };
+    fetch(a.x, raw.x);
+    if (a.gate.p) fetch(a.gate, raw.z);
+    if (a.dh.p) fetch(a.dh, raw.h);
+    if constexpr (!OUT) {
+      if (has_dy) {
+        fetch(a.dy, raw.y);
+        if (has_res) fetch(a.res, raw.r);
+      }
+    }
+  };
+  constexpr bool AHEAD = OUT && TPR <= 32;
+  Raw raw, next;
+  if (AHEAD) ask(row, raw);
+#pragma unroll 1
+  for (; row.r - grp < a.rows; row.next()) {
+    const int64_t r = row.r;
+    const bool live = r < a.rows;
+    if (AHEAD) {
+      RowIndex after = row;
+      after.next();
+      ask(after, next);
+    } else {
+      ask(row, raw);
+    }
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
       T* p = static_cast<T*>(to) + r * a.D;
@@ -79,11 +103,6 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       }
     };
     auto on = [&](int i) { return live && (i * TPR + lane) * V < a.D; };
-    fetch(a.x, xr);
-    fetch(a.gate, zr);
-    if (a.dy.p) fetch(a.res, rr);
-    fetch(a.dh, hr);
-    fetch(a.dy, yr);
     // r1
     float r1 = 1.f;
     if (a.w_post) {
@@ -92,7 +111,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P];
-          to_pairs<T, V>(xr[i], x);
+          to_pairs<T, V>(raw.x[i], x);
 #pragma unroll
           for (int q = 0; q < P; ++q) s2 = fma2(x[q], x[q], s2);
         }
@@ -105,10 +124,10 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     uint64_t du[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (on(i) && a.dh.p) to_pairs<T, V>(hr[i], du[i]);
+      if (on(i) && a.dh.p) to_pairs<T, V>(raw.h[i], du[i]);
       else zero_pairs<V>(du[i]);
     }
-    if (a.dy.p) {
+    if (has_dy) {
       uint64_t h[NV][P], s2 = 0, t2 = 0;
       const uint64_t alpha = both(a.alpha);
 #pragma unroll
@@ -116,7 +135,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
         zero_pairs<V>(h[i]);
         if (on(i)) {
           uint64_t f[P], y[P];
-          to_pairs<T, V>(xr[i], h[i]);
+          to_pairs<T, V>(raw.x[i], h[i]);
           if (a.w_post) {
             weight(pk, a.w_post, i, f);
 #pragma unroll
@@ -124,20 +143,20 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
           }
           if (a.gate.p) {
             uint64_t sg, act;
-            to_pairs<T, V>(zr[i], f);
+            to_pairs<T, V>(raw.z[i], f);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
               gate_of(f[q], sg, act, a.sigmoid);
               h[i][q] = mul2(h[i][q], act);
             }
           }
-          if (a.res.p) {
-            to_pairs<T, V>(rr[i], f);
+          if (has_res) {
+            to_pairs<T, V>(raw.r[OUT ? 0 : i], f);
 #pragma unroll
             for (int q = 0; q < P; ++q) h[i][q] = fma2(alpha, h[i][q], f[q]);
           }
           weight(wk, a.w, i, f);
-          to_pairs<T, V>(yr[i], y);
+          to_pairs<T, V>(raw.y[OUT ? 0 : i], y);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             s2 = fma2(h[i][q], h[i][q], s2);
@@ -157,16 +176,16 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
         if (on(i)) {
           uint64_t f[P], y[P];
           weight(wk, a.w, i, f);
-          to_pairs<T, V>(yr[i], y);
+          to_pairs<T, V>(raw.y[OUT ? 0 : i], y);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            dw[i][q] = fma2(y[q], mul2(h[i][q], rr2), dw[i][q]);
+            dw[OUT ? 0 : i][q] = fma2(y[q], mul2(h[i][q], rr2), dw[OUT ? 0 : i][q]);
             du[i][q] = fma2(pa, mul2(y[q], f[q]), fma2(pb, h[i][q], du[i][q]));
           }
         }
     }
-    put(a.dres, du);
-    if (a.res.p) {
+    if (!OUT) put(a.dres, du);
+    if (has_res) {
       const uint64_t alpha = both(a.alpha);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -178,8 +197,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t z[P], n[P], p[P], sg, act;
-          to_pairs<T, V>(zr[i], z);
-          to_pairs<T, V>(xr[i], n);
+          to_pairs<T, V>(raw.z[i], z);
+          to_pairs<T, V>(raw.x[i], n);
           if (a.w_post) {
             weight(pk, a.w_post, i, p);
 #pragma unroll
@@ -203,7 +222,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P], p[P];
-          to_pairs<T, V>(xr[i], x);
+          to_pairs<T, V>(raw.x[i], x);
           weight(pk, a.w_post, i, p);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
@@ -222,7 +241,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P];
-          to_pairs<T, V>(xr[i], x);
+          to_pairs<T, V>(raw.x[i], x);
 #pragma unroll
           for (int q = 0; q < P; ++q) du[i][q] = fma2(pa, du[i][q], mul2(pb, x[q]));
         }
@@ -230,6 +249,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     put(a.dx, du);
     // rows that run one sum only would meet its buffer again
     if (TPR > 32 && !a.w_post) __syncthreads();
+    if (AHEAD) raw = next;
   }
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
   auto leave = [&](const uint64_t (&gp)[NV][P], float* to) {
@@ -265,7 +285,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       }
     }
   };
-  if (a.w) leave(dw, part);
+  if constexpr (!OUT)
+    if (a.w) leave(dw, part);
   if (a.w_post) leave(dwp, part + a.D);
 }
 
@@ -297,15 +318,21 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, int* blocks, cudaStr
   if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                                \
     constexpr int groups = RowGroup<tpr>::GROUPS, threads = norm_threads(tpr);                                 \
     const size_t sm = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;                                   \
-    static int occ = 0;                                                                                        \
-    *blocks = norm_grid(k_norm_bwd<T, v, tpr, nv>, threads, sm, (a.rows + groups - 1) / groups,                \
-                        norm_blocks_per_sm(threads), &occ);                                                    \
-    k_norm_bwd<T, v, tpr, nv><<<*blocks, threads, sm, st>>>(a);                                                \
+    const int64_t work = (a.rows + groups - 1) / groups;                                                       \
+    constexpr int most = norm_blocks_per_sm(threads);                                                          \
+    static int occ = 0, occ_out = 0;                                                                           \
+    if (a.res.p || a.w) {                                                                                      \
+      *blocks = norm_grid(k_norm_bwd<T, v, tpr, nv, false>, threads, sm, work, most, &occ);                    \
+      k_norm_bwd<T, v, tpr, nv, false><<<*blocks, threads, sm, st>>>(a);                                       \
+    } else {                                                                                                   \
+      *blocks = norm_grid(k_norm_bwd<T, v, tpr, nv, true>, threads, sm, work, most, &occ_out);                 \
+      k_norm_bwd<T, v, tpr, nv, true><<<*blocks, threads, sm, st>>>(a);                                        \
+    }                                                                                                          \
     return cudaGetLastError();                                                                                 \
   }
   GDR_NORM_CASE(VT, 8, 1)
-  GDR_NORM_CASE(VT, 16, 1)
-  GDR_NORM_CASE(VT, 32, 1)
+  GDR_NORM_CASE(VT, 8, 2)
+  GDR_NORM_CASE(VT, 16, 2)
   GDR_NORM_CASE(VT, 32, 2)
   GDR_NORM_CASE(VT, 128, 1)
   GDR_NORM_CASE(VT, 256, 1)
@@ -352,8 +379,8 @@ NormShape norm_shape(int D, int dtype, bool vec, bool bwd) {
   if (vec && D % V == 0) {
     const int n = D / V;
     if (n <= 8) return {V, 8, 1};
-    if (n <= 16) return {V, 16, 1};
-    if (n <= 32) return {V, 32, 1};
+    if (n <= 16) return {V, 8, 2};
+    if (n <= 32) return {V, 16, 2};
     if (n <= 64) return {V, 32, 2};
     if (n <= 128) return bwd ? NormShape{V, 128, 1} : NormShape{V, 32, 4};
     if (n <= 256) return bwd ? NormShape{V, 256, 1} : NormShape{V, 128, 2};

@@ -8,7 +8,9 @@ namespace {
 // to the blocks in turn; rows past the end keep their threads in the barriers.
 // Threads of few columns keep their weights in registers over all their rows.
 // Arithmetic in pairs of columns, so that its instructions fit beside the loads.
-template <typename T, int V, int TPR, int NV>
+// OUT: the norm of a block's output alone (and its gate), without the residual
+// and the second norm: fewer registers; its rows are asked for one ahead.
+template <typename T, int V, int TPR, int NV, bool OUT>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
   using G = RowGroup<TPR>;
   constexpr int P = pairs_of<V>;
@@ -22,25 +24,44 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * V;
       if (c < a.D) {
-        if (a.w) load_weight<T, V>(a, a.w, c, wk[i]);
+        if (!OUT && a.w) load_weight<T, V>(a, a.w, c, wk[i]);
         if (a.w_post) load_weight<T, V>(a, a.w_post, c, pk[i]);
       }
     }
   }
+  const bool has_res = !OUT && a.res.p, has_y = !OUT && a.y;
   RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
+  struct Raw {
+    Vec<T, V> x[NV], z[NV], r[OUT ? 1 : NV];
+  };
+  auto ask = [&](const RowIndex& at, Raw& raw) {
+    if (at.r >= a.rows) return;
+    const T* xp = at.template of<T>(a.x);
+    const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
+    const T* rp = has_res ? at.template of<T>(a.res) : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+      if (c < a.D) {
+        raw.x[i] = vload<T, V>(xp + c);
+        if (zp) raw.z[i] = vload<T, V>(zp + c);
+        if (rp) raw.r[OUT ? 0 : i] = vload<T, V>(rp + c);
+      }
+    }
+  };
+  constexpr bool AHEAD = OUT && TPR <= 32;
+  Raw raw, next;
+  if (AHEAD) ask(row, raw);
 #pragma unroll 1
   for (; row.r - grp < a.rows; row.next()) {
     const bool live = row.r < a.rows;
-    Vec<T, V> xr[NV], zr[NV], rr[NV];
-    auto fetch = [&](const RowTensor& t, Vec<T, V> (&to)[NV]) {
-      if (!t.p || !live) return;
-      const T* p = row.template of<T>(t);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) to[i] = vload<T, V>(p + c);
-      }
-    };
+    if (AHEAD) {
+      RowIndex after = row;
+      after.next();
+      ask(after, next);
+    } else {
+      ask(row, raw);
+    }
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
       T* p = static_cast<T*>(to) + row.r * a.D;
@@ -60,13 +81,10 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       G::sum(ss, buf);
       return fmaf(ss, inv_d, a.eps);
     };
-    fetch(a.x, xr);
-    fetch(a.gate, zr);
-    fetch(a.res, rr);
     uint64_t u[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(xr[i], u[i]);
+      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(raw.x[i], u[i]);
       else zero_pairs<V>(u[i]);
     }
     if (a.w_post) {
@@ -87,7 +105,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       for (int i = 0; i < NV; ++i)
         if ((i * TPR + lane) * V < a.D) {
           uint64_t z[P], sg, act;
-          to_pairs<T, V>(zr[i], z);
+          to_pairs<T, V>(raw.z[i], z);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             gate_of(z[q], sg, act, a.sigmoid);
@@ -95,19 +113,19 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
           }
         }
     }
-    if (a.res.p && live) {
+    if (has_res && live) {
       const uint64_t alpha = both(a.alpha);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((i * TPR + lane) * V < a.D) {
           uint64_t r[P];
-          to_pairs<T, V>(rr[i], r);
+          to_pairs<T, V>(raw.r[OUT ? 0 : i], r);
 #pragma unroll
           for (int q = 0; q < P; ++q) u[i][q] = fma2(alpha, u[i][q], r[q]);
         }
     }
     put(a.h, u);
-    if (a.y) {
+    if (has_y) {
       const uint64_t r2 = both(rsqrtf(mean_square(u, sm[1])));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -122,7 +140,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       put(a.y, u);
     }
     // a row that runs only one of the two sums would meet its own buffer again
-    if (TPR > 32 && !(a.w_post && a.y)) __syncthreads();
+    if (TPR > 32 && !(a.w_post && has_y)) __syncthreads();
+    if (AHEAD) raw = next;
   }
 }
 
@@ -131,14 +150,20 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 #define GDR_NORM_CASE(v, tpr, nv)                                                                              \
   if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                                \
     constexpr int groups = RowGroup<tpr>::GROUPS, threads = norm_threads(tpr);                                 \
-    static int occ = 0;                                                                                        \
-    const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv>, threads, 0, (a.rows + groups - 1) / groups, 32, &occ); \
-    k_norm_fwd<T, v, tpr, nv><<<blocks, threads, 0, st>>>(a);                                                  \
+    const int64_t work = (a.rows + groups - 1) / groups;                                                       \
+    static int occ = 0, occ_out = 0;                                                                           \
+    if (a.res.p || a.w) {                                                                                      \
+      const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv, false>, threads, 0, work, 32, &occ);              \
+      k_norm_fwd<T, v, tpr, nv, false><<<blocks, threads, 0, st>>>(a);                                         \
+    } else {                                                                                                   \
+      const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv, true>, threads, 0, work, 32, &occ_out);           \
+      k_norm_fwd<T, v, tpr, nv, true><<<blocks, threads, 0, st>>>(a);                                          \
+    }                                                                                                          \
     return cudaGetLastError();                                                                                 \
   }
   GDR_NORM_CASE(VT, 8, 1)
-  GDR_NORM_CASE(VT, 16, 1)
-  GDR_NORM_CASE(VT, 32, 1)
+  GDR_NORM_CASE(VT, 8, 2)
+  GDR_NORM_CASE(VT, 16, 2)
   GDR_NORM_CASE(VT, 32, 2)
   GDR_NORM_CASE(VT, 32, 4)
   GDR_NORM_CASE(VT, 128, 2)

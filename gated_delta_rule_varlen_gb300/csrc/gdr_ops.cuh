@@ -100,6 +100,29 @@ __device__ __forceinline__ float sum_of(uint64_t v) {
   return a + b;
 }
 
+// A ring of DEP vectors of V elements a thread in shared memory, filled by
+// asynchronous copies: rows of a walk asked for DEP steps ahead without holding
+// registers.  Each thread reads its own copies only, so that its own waits order
+// them.  Every step of the walk takes one push (of nothing past the end).
+template <typename T, int V, int DEP, int THREADS>
+struct RowRing {
+  using Item = Vec<T, V>;
+  static_assert(sizeof(Item) == 4 || sizeof(Item) == 8 || sizeof(Item) == 16, "cp.async sizes");
+  Item* base;  // [DEP][THREADS], at this thread's element
+  __device__ __forceinline__ explicit RowRing(void* smem) : base(static_cast<Item*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ void push(int slot, const T* src, bool live) {
+    if (live) {
+      const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(base + slot * THREADS));
+      if constexpr (sizeof(Item) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(d), "l"(src), "n"((int)sizeof(Item))
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ Item at(int slot) const { return base[slot * THREADS]; }
+};
+
 // Parameter element (weights and biases come in the activations' type or FP32).
 template <typename T>
 __device__ __forceinline__ float load_param(const void* p, bool f32, int64_t i) {

@@ -53,13 +53,18 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const T* x, const
   }
 }
 
+// Rows of the walks asked for ahead (8 or 16 bytes each a thread).
+constexpr int kDepth = 8;
+
 // One thread owns V adjacent channels and walks the tokens of one tile with
 // the last W - 1 inputs in registers, so each input is read once (and W - 1
 // rows again at a tile's start).  Arithmetic in pairs of channels: the kernel is
 // bound by HBM (2 accesses an element) only while its instructions fit beside.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128, 4) k_sconv_fwd(ConvArgs a) {
+__global__ void __launch_bounds__(128, 5) k_sconv_fwd(ConvArgs a) {
   constexpr int K = W - 1, P = pairs_of<V>;
+  __shared__ Vec<T, V> rows_ahead[V > 1 ? kDepth * 128 : 1];
+  RowRing<T, (V > 1 ? V : 4), kDepth, 128> ring(rows_ahead);
   const int c = ((int)(blockIdx.x % a.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / a.cblocks;
   if (c >= a.C) return;
   const T* x = static_cast<const T*>(a.x) + c;
@@ -110,19 +115,36 @@ __global__ void __launch_bounds__(128, 4) k_sconv_fwd(ConvArgs a) {
       }
       store_pairs<T, V>(out + (int64_t)t * a.C, y);
     };
-    constexpr int U = 6;  // rows in flight
-    while (t + U <= e) {
-      Vec<T, V> raw[U];
+    if constexpr (V > 1) {
+      const T* ahead = x + (int64_t)t * a.ldx;
+      int tp = t;  // the next row to ask for
 #pragma unroll
-      for (int i = 0; i < U; ++i) raw[i] = vload<T, V>(x + (int64_t)(t + i) * a.ldx);
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        token(raw[i]);
-        ++t;
+      for (int i = 0; i < kDepth; ++i) {
+        ring.push(i, ahead, tp < e);
+        cp_async_commit();
+        ahead += a.ldx;
+        ++tp;
       }
-    }
 #pragma unroll 1
-    for (; t < e; ++t) token(vload<T, V>(x + (int64_t)t * a.ldx));
+      while (t < e) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+          if (t < e) {
+            cp_async_wait<kDepth - 1>();
+            token(ring.at(i));
+            ring.push(i, ahead, tp < e);
+            cp_async_commit();
+            ahead += a.ldx;
+            ++tp;
+            ++t;
+          }
+        }
+      }
+      cp_async_wait<0>();
+    } else {
+#pragma unroll 1
+      for (; t < e; ++t) token(vload<T, V>(x + (int64_t)t * a.ldx));
+    }
     if (t == de) {
       end_state(d);
       ++d;
@@ -150,8 +172,10 @@ struct ConvBwdArgs {
 // partial row per tile.  The tile's last rows need dz of the W - 1 tokens after
 // it, which are recomputed.  Bound by HBM: x and dout read, dx written.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128, 4) k_sconv_bwd(ConvBwdArgs a) {
+__global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
   constexpr int K = W - 1, P = pairs_of<V>;
+  __shared__ Vec<T, V> rows_ahead[2][V > 1 ? kDepth * 128 : 1];
+  RowRing<T, (V > 1 ? V : 4), kDepth, 128> rx_ring(rows_ahead[0]), rg_ring(rows_ahead[1]);
   const ConvArgs& f = a.f;
   const int c = ((int)(blockIdx.x % f.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / f.cblocks;
   if (c >= f.C) return;
@@ -248,18 +272,36 @@ __global__ void __launch_bounds__(128, 4) k_sconv_bwd(ConvBwdArgs a) {
       token(rx, rg, true, done);
       emit(t - K, done);
     }
-    constexpr int U = 4;  // rows in flight
-    while (t + U <= e) {
-      Vec<T, V> rx[U], rg[U];
+    if constexpr (V > 1) {
+      const T *ax = x + (int64_t)t * f.ldx, *ag = dout + (int64_t)t * a.ldo;
+      int tp = t;
+      auto ask = [&](int i) {
+        rx_ring.push(i, ax, tp < e);
+        rg_ring.push(i, ag, tp < e);
+        cp_async_commit();
+        ax += f.ldx;
+        ag += a.ldo;
+        ++tp;
+      };
 #pragma unroll
-      for (int i = 0; i < U; ++i) rows(t + i, rx[i], rg[i]);
+      for (int i = 0; i < kDepth; ++i) ask(i);
+      T* to = dx + (int64_t)(t - K) * f.C;
+#pragma unroll 1
+      while (t < e) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        uint64_t done[P];
-        token(rx[i], rg[i], true, done);
-        store_pairs<T, V>(dx + (int64_t)(t + i - K) * f.C, done);
+        for (int i = 0; i < kDepth; ++i) {
+          if (t < e) {
+            cp_async_wait<kDepth - 1>();
+            uint64_t done[P];
+            token(rx_ring.at(i), rg_ring.at(i), true, done);
+            ask(i);
+            store_pairs<T, V>(to, done);
+            to += f.C;
+            ++t;
+          }
+        }
       }
-      t += U;
+      cp_async_wait<0>();
     }
     // the rest, and the tokens after the tile that the tile's last rows feed
     const int tail = min(de, e + K);
@@ -383,7 +425,7 @@ int tile_tokens(int64_t T, int64_t cblocks, int wave, int most) {
 }
 // The partial rows a backward leaves do not depend on alignment, so that the
 // workspace does not either: its tile is that of threads of eight bytes of BF16.
-int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, ((C + 3) / 4 + 127) / 128, 152 * 4, 256); }
+int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, ((C + 3) / 4 + 127) / 128, 152 * 5, 256); }
 
 size_t elem(int dtype) { return dtype == GDR_DTYPE_F32 ? 4 : 2; }
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -443,7 +485,7 @@ gdr_status sconv_fwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   const bool vec = C % V == 0 && ldx % V == 0 && on16(x) && on16(out) && on16(s0) && on16(st);
   const int nv = vec ? C / V : C;
   a.cblocks = (nv + 127) / 128;
-  a.tile = tile_tokens(T, a.cblocks, 152 * 4, 128);
+  a.tile = tile_tokens(T, a.cblocks, 152 * 5, 128);
   const int64_t grid = (T > 0 ? (T + a.tile - 1) / a.tile : 1) * a.cblocks;
   if (grid > INT32_MAX) return GDR_INVALID_ARG;
   ProfScope ps("sconv_fwd", stream, (double)T * C);
