@@ -134,6 +134,17 @@ struct RowIndex {
   }
 };
 
+// The rows a thread works on next, asked for DEPTH rows ahead: ITEMS vectors of
+// the thread a row, in shared memory (gdr_ops.cuh: RowRing).
+template <typename T, int V, int ITEMS, int DEPTH, int THREADS>
+struct RowsAhead {
+  static constexpr int BYTES = DEPTH * ITEMS * THREADS * (int)sizeof(Vec<T, V>);
+  RowRing<T, V, DEPTH * ITEMS, THREADS> ring;
+  __device__ __forceinline__ explicit RowsAhead(void* smem) : ring(smem) {}
+  __device__ __forceinline__ void ask(int slot, int item, const T* src) { ring.push(slot * ITEMS + item, src, true); }
+  __device__ __forceinline__ Vec<T, V> get(int slot, int item) const { return ring.at(slot * ITEMS + item); }
+};
+
 // V elements of a weight from c on, in pairs.
 template <typename T, int V>
 __device__ __forceinline__ void load_weight(const NormArgs& a, const void* p, int c, uint64_t (&f)[pairs_of<V>]) {

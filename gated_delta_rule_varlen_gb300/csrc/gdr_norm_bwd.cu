@@ -18,7 +18,7 @@ namespace {
 // all its rows and leaves one partial row; k_norm_wgrad adds those.  Threads of
 // few columns keep the weights in registers too.  OUT: as in the forward.
 template <typename T, int V, int TPR, int NV, bool OUT>
-__global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : 1)
+__global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : OUT && TPR <= 32 ? 4 : 1)
     k_norm_bwd(NormArgs a) {
   using G = RowGroup<TPR>;
   constexpr int P = pairs_of<V>;
@@ -79,20 +79,60 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       }
     }
   };
-  constexpr bool AHEAD = OUT && TPR <= 32;
-  Raw raw, next;
-  if (AHEAD) ask(row, raw);
+  // Rows are asked for ahead where two at least fit 40 KB a block: with the row in
+  // work alone too few bytes are in flight.
+  constexpr int ITEMS = (OUT ? 3 : 5) * NV, SLOT = ITEMS * G::THREADS * 16;
+  constexpr int DEPTH = SLOT > 20480 ? 1 : SLOT * 4 <= 40960 ? 4 : 40960 / SLOT;
+  constexpr bool AHEAD = V > 1 && DEPTH >= 2;
+  using Ahead = RowsAhead<T, (V > 1 ? V : 4), ITEMS, DEPTH, G::THREADS>;
+  __shared__ __align__(16) unsigned char ahead[AHEAD ? Ahead::BYTES : 16];
+  Ahead rows(ahead);
+  auto ask_ahead = [&](const RowIndex& at, int slot) {
+    if constexpr (AHEAD) {
+      if (at.r < a.rows) {
+        const T* xp = at.template of<T>(a.x);
+        const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
+        const T* hp = a.dh.p ? at.template of<T>(a.dh) : nullptr;
+        const T* yp = has_dy ? at.template of<T>(a.dy) : nullptr;
+        const T* rp = has_dy && has_res ? at.template of<T>(a.res) : nullptr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * V;
+          if (c < a.D) {
+            rows.ask(slot, i, xp + c);
+            if (zp) rows.ask(slot, NV + i, zp + c);
+            if (hp) rows.ask(slot, 2 * NV + i, hp + c);
+            if constexpr (!OUT) {
+              if (yp) rows.ask(slot, 3 * NV + i, yp + c);
+              if (rp) rows.ask(slot, 4 * NV + i, rp + c);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  Raw raw;
+  RowIndex far = row;
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      ask_ahead(far, i);
+      far.next();
+    }
+  }
+  int slot = 0;
 #pragma unroll 1
   for (; row.r - grp < a.rows; row.next()) {
     const int64_t r = row.r;
     const bool live = r < a.rows;
-    if (AHEAD) {
-      RowIndex after = row;
-      after.next();
-      ask(after, next);
-    } else {
-      ask(row, raw);
-    }
+    if constexpr (AHEAD) cp_async_wait<DEPTH - 1>();
+    else ask(row, raw);
+    // the row's vectors: from shared memory whenever they are used, or registers
+    auto vec = [&](int item, const Vec<T, V>& held) {
+      if constexpr (AHEAD) return rows.get(slot, item);
+      else return held;
+    };
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
       T* p = static_cast<T*>(to) + r * a.D;
@@ -111,7 +151,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P];
-          to_pairs<T, V>(raw.x[i], x);
+          to_pairs<T, V>(vec(i, raw.x[i]), x);
 #pragma unroll
           for (int q = 0; q < P; ++q) s2 = fma2(x[q], x[q], s2);
         }
@@ -124,7 +164,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     uint64_t du[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (on(i) && a.dh.p) to_pairs<T, V>(raw.h[i], du[i]);
+      if (on(i) && a.dh.p) to_pairs<T, V>(vec(2 * NV + i, raw.h[i]), du[i]);
       else zero_pairs<V>(du[i]);
     }
     if (has_dy) {
@@ -135,7 +175,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
         zero_pairs<V>(h[i]);
         if (on(i)) {
           uint64_t f[P], y[P];
-          to_pairs<T, V>(raw.x[i], h[i]);
+          to_pairs<T, V>(vec(i, raw.x[i]), h[i]);
           if (a.w_post) {
             weight(pk, a.w_post, i, f);
 #pragma unroll
@@ -143,7 +183,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
           }
           if (a.gate.p) {
             uint64_t sg, act;
-            to_pairs<T, V>(raw.z[i], f);
+            to_pairs<T, V>(vec(NV + i, raw.z[i]), f);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
               gate_of(f[q], sg, act, a.sigmoid);
@@ -151,12 +191,12 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
             }
           }
           if (has_res) {
-            to_pairs<T, V>(raw.r[OUT ? 0 : i], f);
+            to_pairs<T, V>(vec(4 * NV + i, raw.r[OUT ? 0 : i]), f);
 #pragma unroll
             for (int q = 0; q < P; ++q) h[i][q] = fma2(alpha, h[i][q], f[q]);
           }
           weight(wk, a.w, i, f);
-          to_pairs<T, V>(raw.y[OUT ? 0 : i], y);
+          to_pairs<T, V>(vec(3 * NV + i, raw.y[OUT ? 0 : i]), y);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             s2 = fma2(h[i][q], h[i][q], s2);
@@ -176,7 +216,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
         if (on(i)) {
           uint64_t f[P], y[P];
           weight(wk, a.w, i, f);
-          to_pairs<T, V>(raw.y[OUT ? 0 : i], y);
+          to_pairs<T, V>(vec(3 * NV + i, raw.y[OUT ? 0 : i]), y);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             dw[OUT ? 0 : i][q] = fma2(y[q], mul2(h[i][q], rr2), dw[OUT ? 0 : i][q]);
@@ -197,8 +237,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t z[P], n[P], p[P], sg, act;
-          to_pairs<T, V>(raw.z[i], z);
-          to_pairs<T, V>(raw.x[i], n);
+          to_pairs<T, V>(vec(NV + i, raw.z[i]), z);
+          to_pairs<T, V>(vec(i, raw.x[i]), n);
           if (a.w_post) {
             weight(pk, a.w_post, i, p);
 #pragma unroll
@@ -222,7 +262,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P], p[P];
-          to_pairs<T, V>(raw.x[i], x);
+          to_pairs<T, V>(vec(i, raw.x[i]), x);
           weight(pk, a.w_post, i, p);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
@@ -241,7 +281,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       for (int i = 0; i < NV; ++i)
         if (on(i)) {
           uint64_t x[P];
-          to_pairs<T, V>(raw.x[i], x);
+          to_pairs<T, V>(vec(i, raw.x[i]), x);
 #pragma unroll
           for (int q = 0; q < P; ++q) du[i][q] = fma2(pa, du[i][q], mul2(pb, x[q]));
         }
@@ -249,7 +289,11 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     put(a.dx, du);
     // rows that run one sum only would meet its buffer again
     if (TPR > 32 && !a.w_post) __syncthreads();
-    if (AHEAD) raw = next;
+    if constexpr (AHEAD) {  // (what was read from the slot has been used)
+      ask_ahead(far, slot);
+      far.next();
+      slot = slot == DEPTH - 1 ? 0 : slot + 1;
+    }
   }
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
   auto leave = [&](const uint64_t (&gp)[NV][P], float* to) {

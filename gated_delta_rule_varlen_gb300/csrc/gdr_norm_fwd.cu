@@ -9,7 +9,7 @@ namespace {
 // Threads of few columns keep their weights in registers over all their rows.
 // Arithmetic in pairs of columns, so that its instructions fit beside the loads.
 // OUT: the norm of a block's output alone (and its gate), without the residual
-// and the second norm: fewer registers; its rows are asked for one ahead.
+// and the second norm: fewer registers.
 template <typename T, int V, int TPR, int NV, bool OUT>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
   using G = RowGroup<TPR>;
@@ -49,19 +49,54 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       }
     }
   };
-  constexpr bool AHEAD = OUT && TPR <= 32;
-  Raw raw, next;
-  if (AHEAD) ask(row, raw);
+  // Rows are asked for ahead where two at least fit 40 KB a block: with the row in
+  // work alone too few bytes are in flight.
+  constexpr int ITEMS = (OUT ? 2 : 3) * NV, SLOT = ITEMS * G::THREADS * 16;
+  constexpr int DEPTH = SLOT > 20480 ? 1 : SLOT * 4 <= 40960 ? 4 : 40960 / SLOT;
+  constexpr bool AHEAD = V > 1 && DEPTH >= 2;
+  using Ahead = RowsAhead<T, (V > 1 ? V : 4), ITEMS, DEPTH, G::THREADS>;
+  __shared__ __align__(16) unsigned char ahead[AHEAD ? Ahead::BYTES : 16];
+  Ahead rows(ahead);
+  auto ask_ahead = [&](const RowIndex& at, int slot) {
+    if constexpr (AHEAD) {
+      if (at.r < a.rows) {
+        const T* xp = at.template of<T>(a.x);
+        const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
+        const T* rp = has_res ? at.template of<T>(a.res) : nullptr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * V;
+          if (c < a.D) {
+            rows.ask(slot, i, xp + c);
+            if (zp) rows.ask(slot, NV + i, zp + c);
+            if constexpr (!OUT)
+              if (rp) rows.ask(slot, 2 * NV + i, rp + c);
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  Raw raw;
+  RowIndex far = row;
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      ask_ahead(far, i);
+      far.next();
+    }
+  }
+  int slot = 0;
 #pragma unroll 1
   for (; row.r - grp < a.rows; row.next()) {
     const bool live = row.r < a.rows;
-    if (AHEAD) {
-      RowIndex after = row;
-      after.next();
-      ask(after, next);
-    } else {
-      ask(row, raw);
-    }
+    if constexpr (AHEAD) cp_async_wait<DEPTH - 1>();
+    else ask(row, raw);
+    // the row's vectors: from shared memory whenever they are used, or registers
+    auto vec = [&](int item, const Vec<T, V>& held) {
+      if constexpr (AHEAD) return rows.get(slot, item);
+      else return held;
+    };
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
       T* p = static_cast<T*>(to) + row.r * a.D;
@@ -84,7 +119,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
     uint64_t u[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(raw.x[i], u[i]);
+      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(vec(i, raw.x[i]), u[i]);
       else zero_pairs<V>(u[i]);
     }
     if (a.w_post) {
@@ -105,7 +140,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       for (int i = 0; i < NV; ++i)
         if ((i * TPR + lane) * V < a.D) {
           uint64_t z[P], sg, act;
-          to_pairs<T, V>(raw.z[i], z);
+          to_pairs<T, V>(vec(NV + i, raw.z[i]), z);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             gate_of(z[q], sg, act, a.sigmoid);
@@ -119,7 +154,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       for (int i = 0; i < NV; ++i)
         if ((i * TPR + lane) * V < a.D) {
           uint64_t r[P];
-          to_pairs<T, V>(raw.r[OUT ? 0 : i], r);
+          to_pairs<T, V>(vec(2 * NV + i, raw.r[OUT ? 0 : i]), r);
 #pragma unroll
           for (int q = 0; q < P; ++q) u[i][q] = fma2(alpha, u[i][q], r[q]);
         }
@@ -141,7 +176,11 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
     }
     // a row that runs only one of the two sums would meet its own buffer again
     if (TPR > 32 && !(a.w_post && has_y)) __syncthreads();
-    if (AHEAD) raw = next;
+    if constexpr (AHEAD) {  // (what was read from the slot has been used)
+      ask_ahead(far, slot);
+      far.next();
+      slot = slot == DEPTH - 1 ? 0 : slot + 1;
+    }
   }
 }
 
