@@ -106,31 +106,34 @@ struct RowGroup {
   }
 };
 
-// A row index as its two leading indices, advanced by a fixed number of rows
-// without a division.
-struct RowIndex {
-  int64_t r, i0;  // row; outer index
-  int i1, R1;     // inner index
-  int64_t step, step0;
-  int step1;
-  __device__ __forceinline__ RowIndex(int64_t first, int64_t step_, int R1_) : r(first), R1(R1_), step(step_) {
-    i0 = first / R1;
-    i1 = (int)(first - i0 * R1);
-    step0 = step / R1;
-    step1 = (int)(step - step0 * R1);
+// The rows of a thread, every `step`-th one, in up to K tensors: their addresses
+// advance by one sum, and another where the inner index wraps, without a
+// multiplication or division a row.
+template <typename T, int K>
+struct Cursor {
+  int64_t r, step;   // row
+  int i1, step1, R1; // inner index
+  const T* p[K];     // the tensors' rows
+  int64_t by[K], wrap[K];
+  __device__ __forceinline__ Cursor(int64_t first, int64_t step_, int R1_) : r(first), step(step_), R1(R1_) {
+    i1 = (int)(first % R1);
+    step1 = (int)(step % R1);
+  }
+  __device__ __forceinline__ void add(int k, const RowTensor& t) {
+    p[k] = static_cast<const T*>(t.p) + (r / R1) * t.s0 + i1 * t.s1;
+    by[k] = (step / R1) * t.s0 + step1 * t.s1;
+    wrap[k] = t.s0 - R1 * t.s1;
   }
   __device__ __forceinline__ void next() {
     r += step;
-    i0 += step0;
     i1 += step1;
-    if (i1 >= R1) {
-      i1 -= R1;
-      ++i0;
+    const bool over = i1 >= R1;
+    if (over) i1 -= R1;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      p[k] += by[k];
+      if (over) p[k] += wrap[k];
     }
-  }
-  template <typename T>
-  __device__ __forceinline__ const T* of(const RowTensor& t) const {
-    return static_cast<const T*>(t.p) + i0 * t.s0 + i1 * t.s1;
   }
 };
 

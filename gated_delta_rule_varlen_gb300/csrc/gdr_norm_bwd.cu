@@ -18,7 +18,7 @@ namespace {
 // all its rows and leaves one partial row; k_norm_wgrad adds those.  Threads of
 // few columns keep the weights in registers too.  OUT: as in the forward.
 template <typename T, int V, int TPR, int NV, bool OUT>
-__global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : OUT && TPR <= 32 ? 4 : 1)
+__global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ? 5 : TPR == 256 ? 2 : 1) : NV * V == 16 ? (TPR <= 32 && OUT ? 4 : TPR <= 128 ? 3 : 1) : 1)
     k_norm_bwd(NormArgs a) {
   using G = RowGroup<TPR>;
   constexpr int P = pairs_of<V>;
@@ -55,82 +55,77 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
       load_weight<T, V>(a, p, (i * TPR + lane) * V, f);
     }
   };
-  RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
-  struct Raw {
-    Vec<T, V> x[NV], z[NV], h[NV], r[OUT ? 1 : NV], y[OUT ? 1 : NV];
-  };
-  auto ask = [&](const RowIndex& at, Raw& raw) {
-    if (at.r >= a.rows) return;
-    auto fetch = [&](const RowTensor& t, auto& to) {
-      const T* p = at.template of<T>(t);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) to[i] = vload<T, V>(p + c);
-      }
-    };
-    fetch(a.x, raw.x);
-    if (a.gate.p) fetch(a.gate, raw.z);
-    if (a.dh.p) fetch(a.dh, raw.h);
-    if constexpr (!OUT) {
-      if (has_dy) {
-        fetch(a.dy, raw.y);
-        if (has_res) fetch(a.res, raw.r);
-      }
-    }
-  };
   // Rows are asked for ahead where two at least fit 40 KB a block: with the row in
   // work alone too few bytes are in flight.
   constexpr int ITEMS = (OUT ? 3 : 5) * NV, SLOT = ITEMS * G::THREADS * 16;
   constexpr int DEPTH = SLOT > 20480 ? 1 : SLOT * 4 <= 40960 ? 4 : 40960 / SLOT;
   constexpr bool AHEAD = V > 1 && DEPTH >= 2;
   using Ahead = RowsAhead<T, (V > 1 ? V : 4), ITEMS, DEPTH, G::THREADS>;
-  __shared__ __align__(16) unsigned char ahead[AHEAD ? Ahead::BYTES : 16];
-  Ahead rows(ahead);
-  auto ask_ahead = [&](const RowIndex& at, int slot) {
+  __shared__ __align__(16) unsigned char ahead_rows[AHEAD ? Ahead::BYTES : 16];
+  Ahead ahead(ahead_rows);
+  const int64_t first = (int64_t)blockIdx.x * G::GROUPS + grp, step = (int64_t)gridDim.x * G::GROUPS;
+  Cursor<T, OUT ? 3 : 5> in(first, step, a.R1);  // the next row to ask for
+  in.add(0, a.x);
+  in.add(1, a.gate);
+  in.add(2, a.dh);
+  if constexpr (!OUT) {
+    in.add(3, a.dy);
+    in.add(4, a.res);
+  }
+  struct Raw {
+    Vec<T, V> x[NV], z[NV], h[NV], r[OUT ? 1 : NV], y[OUT ? 1 : NV];
+  };
+  Raw raw;
+  auto ask = [&](int slot) {
     if constexpr (AHEAD) {
-      if (at.r < a.rows) {
-        const T* xp = at.template of<T>(a.x);
-        const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
-        const T* hp = a.dh.p ? at.template of<T>(a.dh) : nullptr;
-        const T* yp = has_dy ? at.template of<T>(a.dy) : nullptr;
-        const T* rp = has_dy && has_res ? at.template of<T>(a.res) : nullptr;
+      if (in.r < a.rows) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = (i * TPR + lane) * V;
           if (c < a.D) {
-            rows.ask(slot, i, xp + c);
-            if (zp) rows.ask(slot, NV + i, zp + c);
-            if (hp) rows.ask(slot, 2 * NV + i, hp + c);
+            ahead.ask(slot, i, in.p[0] + c);
+            if (a.gate.p) ahead.ask(slot, NV + i, in.p[1] + c);
+            if (a.dh.p) ahead.ask(slot, 2 * NV + i, in.p[2] + c);
             if constexpr (!OUT) {
-              if (yp) rows.ask(slot, 3 * NV + i, yp + c);
-              if (rp) rows.ask(slot, 4 * NV + i, rp + c);
+              if (has_dy) ahead.ask(slot, 3 * NV + i, in.p[3] + c);
+              if (has_dy && has_res) ahead.ask(slot, 4 * NV + i, in.p[4] + c);
             }
           }
         }
       }
       cp_async_commit();
+    } else if (in.r < a.rows) {
+      auto fetch = [&](bool given, int k, auto& to) {
+        if (!given) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * V;
+          if (c < a.D) to[i] = vload<T, V>(in.p[k] + c);
+        }
+      };
+      fetch(true, 0, raw.x);
+      fetch(a.gate.p, 1, raw.z);
+      fetch(a.dh.p, 2, raw.h);
+      if constexpr (!OUT) {
+        fetch(has_dy, 3, raw.y);
+        fetch(has_dy && has_res, 4, raw.r);
+      }
     }
+    in.next();
   };
-  Raw raw;
-  RowIndex far = row;
   if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-      ask_ahead(far, i);
-      far.next();
-    }
+    for (int i = 0; i < DEPTH; ++i) ask(i);
   }
   int slot = 0;
 #pragma unroll 1
-  for (; row.r - grp < a.rows; row.next()) {
-    const int64_t r = row.r;
+  for (int64_t r = first; r - grp < a.rows; r += step) {
     const bool live = r < a.rows;
     if constexpr (AHEAD) cp_async_wait<DEPTH - 1>();
-    else ask(row, raw);
+    else ask(0);
     // the row's vectors: from shared memory whenever they are used, or registers
     auto vec = [&](int item, const Vec<T, V>& held) {
-      if constexpr (AHEAD) return rows.get(slot, item);
+      if constexpr (AHEAD) return ahead.get(slot, item);
       else return held;
     };
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
@@ -290,8 +285,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), NV * V <= 8 ? (TPR <= 128 ?
     // rows that run one sum only would meet its buffer again
     if (TPR > 32 && !a.w_post) __syncthreads();
     if constexpr (AHEAD) {  // (what was read from the slot has been used)
-      ask_ahead(far, slot);
-      far.next();
+      ask(slot);
       slot = slot == DEPTH - 1 ? 0 : slot + 1;
     }
   }
@@ -379,8 +373,8 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, int* blocks, cudaStr
   GDR_NORM_CASE(VT, 16, 2)
   GDR_NORM_CASE(VT, 32, 2)
   GDR_NORM_CASE(VT, 128, 1)
-  GDR_NORM_CASE(VT, 256, 1)
-  GDR_NORM_CASE(VT, 512, 1)
+  GDR_NORM_CASE(VT, 128, 2)
+  GDR_NORM_CASE(VT, 256, 2)
   GDR_NORM_CASE(VT, 512, 2)
   GDR_NORM_CASE(VT, 1024, 2)
   GDR_NORM_CASE(VT, 1024, 4)
@@ -405,7 +399,7 @@ namespace {
 
 // Most blocks of a backward on rows of D elements, over the shapes that such
 // rows take: the partial rows its workspace has to hold.
-int max_norm_blocks(int D) { return 152 * norm_blocks_per_sm(D <= 1024 ? 128 : D <= 2048 ? 256 : 512); }
+int max_norm_blocks(int D) { return 152 * norm_blocks_per_sm(D <= 2048 ? 128 : 256); }
 
 // Whether rows of D elements at these addresses and strides can be read in
 // 16-byte pieces.
@@ -414,10 +408,9 @@ bool rows16(const RowTensor& t, int V) {
 }
 
 // The threads that hold a row: 16-byte pieces where all rows allow them, else
-// single elements.  Up to 512 columns of BF16 a backward's row stays within a
-// warp, and up to 1024 a forward's, whose threads hold less beside it (no barrier
-// a row); longer rows take one piece a thread in the backward and two in the
-// forward, more where a block would not hold them.
+// single elements.  Two pieces a thread (what a row costs beside its elements is
+// then shared by 16 of BF16) while the row's group has 128 threads at least, or
+// less than a warp's; within a warp there is no barrier a row.
 NormShape norm_shape(int D, int dtype, bool vec, bool bwd) {
   const int V = dtype == GDR_DTYPE_F32 ? 4 : 8;
   if (vec && D % V == 0) {
@@ -427,8 +420,8 @@ NormShape norm_shape(int D, int dtype, bool vec, bool bwd) {
     if (n <= 32) return {V, 16, 2};
     if (n <= 64) return {V, 32, 2};
     if (n <= 128) return bwd ? NormShape{V, 128, 1} : NormShape{V, 32, 4};
-    if (n <= 256) return bwd ? NormShape{V, 256, 1} : NormShape{V, 128, 2};
-    if (n <= 512) return bwd ? NormShape{V, 512, 1} : NormShape{V, 256, 2};
+    if (n <= 256) return {V, 128, 2};
+    if (n <= 512) return {V, 256, 2};
     if (n <= 1024) return {V, 512, 2};
     if (n <= 2048) return bwd ? NormShape{V, 1024, 2} : NormShape{V, 512, 4};
     return {V, 1024, 4};

@@ -30,76 +30,71 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
     }
   }
   const bool has_res = !OUT && a.res.p, has_y = !OUT && a.y;
-  RowIndex row((int64_t)blockIdx.x * G::GROUPS + grp, (int64_t)gridDim.x * G::GROUPS, a.R1);
-  struct Raw {
-    Vec<T, V> x[NV], z[NV], r[OUT ? 1 : NV];
-  };
-  auto ask = [&](const RowIndex& at, Raw& raw) {
-    if (at.r >= a.rows) return;
-    const T* xp = at.template of<T>(a.x);
-    const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
-    const T* rp = has_res ? at.template of<T>(a.res) : nullptr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * V;
-      if (c < a.D) {
-        raw.x[i] = vload<T, V>(xp + c);
-        if (zp) raw.z[i] = vload<T, V>(zp + c);
-        if (rp) raw.r[OUT ? 0 : i] = vload<T, V>(rp + c);
-      }
-    }
-  };
   // Rows are asked for ahead where two at least fit 40 KB a block: with the row in
   // work alone too few bytes are in flight.
   constexpr int ITEMS = (OUT ? 2 : 3) * NV, SLOT = ITEMS * G::THREADS * 16;
   constexpr int DEPTH = SLOT > 20480 ? 1 : SLOT * 4 <= 40960 ? 4 : 40960 / SLOT;
   constexpr bool AHEAD = V > 1 && DEPTH >= 2;
   using Ahead = RowsAhead<T, (V > 1 ? V : 4), ITEMS, DEPTH, G::THREADS>;
-  __shared__ __align__(16) unsigned char ahead[AHEAD ? Ahead::BYTES : 16];
-  Ahead rows(ahead);
-  auto ask_ahead = [&](const RowIndex& at, int slot) {
+  __shared__ __align__(16) unsigned char ahead_rows[AHEAD ? Ahead::BYTES : 16];
+  Ahead ahead(ahead_rows);
+  const int64_t first = (int64_t)blockIdx.x * G::GROUPS + grp, step = (int64_t)gridDim.x * G::GROUPS;
+  Cursor<T, OUT ? 2 : 3> in(first, step, a.R1);  // the next row to ask for
+  in.add(0, a.x);
+  in.add(1, a.gate);
+  if constexpr (!OUT) in.add(2, a.res);
+  struct Raw {
+    Vec<T, V> x[NV], z[NV], r[OUT ? 1 : NV];
+  };
+  Raw raw;
+  auto ask = [&](int slot) {
     if constexpr (AHEAD) {
-      if (at.r < a.rows) {
-        const T* xp = at.template of<T>(a.x);
-        const T* zp = a.gate.p ? at.template of<T>(a.gate) : nullptr;
-        const T* rp = has_res ? at.template of<T>(a.res) : nullptr;
+      if (in.r < a.rows) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = (i * TPR + lane) * V;
           if (c < a.D) {
-            rows.ask(slot, i, xp + c);
-            if (zp) rows.ask(slot, NV + i, zp + c);
+            ahead.ask(slot, i, in.p[0] + c);
+            if (a.gate.p) ahead.ask(slot, NV + i, in.p[1] + c);
             if constexpr (!OUT)
-              if (rp) rows.ask(slot, 2 * NV + i, rp + c);
+              if (has_res) ahead.ask(slot, 2 * NV + i, in.p[2] + c);
           }
         }
       }
       cp_async_commit();
+    } else if (in.r < a.rows) {
+      auto fetch = [&](bool given, int k, auto& to) {
+        if (!given) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * V;
+          if (c < a.D) to[i] = vload<T, V>(in.p[k] + c);
+        }
+      };
+      fetch(true, 0, raw.x);
+      fetch(a.gate.p, 1, raw.z);
+      if constexpr (!OUT) fetch(has_res, 2, raw.r);
     }
+    in.next();
   };
-  Raw raw;
-  RowIndex far = row;
   if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-      ask_ahead(far, i);
-      far.next();
-    }
+    for (int i = 0; i < DEPTH; ++i) ask(i);
   }
   int slot = 0;
 #pragma unroll 1
-  for (; row.r - grp < a.rows; row.next()) {
-    const bool live = row.r < a.rows;
+  for (int64_t r = first; r - grp < a.rows; r += step) {
+    const bool live = r < a.rows;
     if constexpr (AHEAD) cp_async_wait<DEPTH - 1>();
-    else ask(row, raw);
+    else ask(0);
     // the row's vectors: from shared memory whenever they are used, or registers
     auto vec = [&](int item, const Vec<T, V>& held) {
-      if constexpr (AHEAD) return rows.get(slot, item);
+      if constexpr (AHEAD) return ahead.get(slot, item);
       else return held;
     };
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
-      T* p = static_cast<T*>(to) + row.r * a.D;
+      T* p = static_cast<T*>(to) + r * a.D;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * V;
@@ -177,8 +172,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
     // a row that runs only one of the two sums would meet its own buffer again
     if (TPR > 32 && !(a.w_post && has_y)) __syncthreads();
     if constexpr (AHEAD) {  // (what was read from the slot has been used)
-      ask_ahead(far, slot);
-      far.next();
+      ask(slot);
       slot = slot == DEPTH - 1 ? 0 : slot + 1;
     }
   }
