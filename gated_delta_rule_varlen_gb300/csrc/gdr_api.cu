@@ -416,12 +416,15 @@ SavedHeader header_of(const Stamp& s) {
 }  // namespace
 
 gdr_status check_device() {
+  static std::atomic<int> known[64];  // 1: an sm_103
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GDR_CUDA_ERROR;
+  if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed) == 1) return GDR_OK;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return GDR_CUDA_ERROR;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return GDR_CUDA_ERROR;
   if (major != 10 || minor != 3) return GDR_UNSUPPORTED;
+  if (dev >= 0 && dev < 64) known[dev].store(1, std::memory_order_relaxed);
   return GDR_OK;
 }
 

@@ -104,22 +104,34 @@ __global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
   __syncthreads();
   float* S = a.state + ((int64_t)slot * a.H + h) * a.NS * a.P + c * V;
   float xd[V], y[V];
-  const bool on = r < rows;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     xd[v] = to_f(a.x[(int64_t)b * a.ldx + h * a.P + c * V + v]) * dt;
     y[v] = 0.f;
   }
-  if (on) {
-    for (int n = r; n < a.NS; n += rows) {
-      float s[V];
-      vunpack<float, V>(vload<float, V>(S + (int64_t)n * a.P), s);
+  if (r < rows) {
+    constexpr int U = 8;  // rows in flight a thread
+#pragma unroll 1
+    for (int n0 = r; n0 < a.NS; n0 += U * rows) {
+      float s[U][V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        s[v] = fmaf(da, s[v], sb[n] * xd[v]);
-        y[v] = fmaf(sc[n], s[v], y[v]);
+      for (int u = 0; u < U; ++u) {
+        const int n = n0 + u * rows;
+        if (n < a.NS) vunpack<float, V>(vload<float, V>(S + (int64_t)n * a.P), s[u]);
       }
-      vstore<float, V>(S + (int64_t)n * a.P, s);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int n = n0 + u * rows;
+        if (n < a.NS) {
+          const float bn = sb[n], cn = sc[n];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            s[u][v] = fmaf(da, s[u][v], bn * xd[v]);
+            y[v] = fmaf(cn, s[u][v], y[v]);
+          }
+          vstore<float, V>(S + (int64_t)n * a.P, s[u]);
+        }
+      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) red[(r * cols + c) * V + v] = y[v];

@@ -1036,6 +1036,10 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
   }
   SsmPlan best{(int)std::max<int64_t>(most, 1), N, 0, false, 0};
   double cost = std::max((double)(nc + kStart * N) * items / sms, most + kStart);
+  best.chunks = gate_chunks;
+  best.scratch = up256((size_t)gate_chunks * H * GATES * sizeof(float));
+  // (nothing to gain where whole documents come near to even work)
+  if (cost < 1.1 * nc * items / sms) return best;
   // pieces of the longest document
   for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
     const int64_t L = (most + k - 1) / k;
@@ -1056,8 +1060,6 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
       best.split = true;
     }
   }
-  best.chunks = gate_chunks;
-  best.scratch = up256((size_t)gate_chunks * H * GATES * sizeof(float));
   if (best.split)
     best.scratch += up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
   return best;
