@@ -96,43 +96,47 @@ __global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
     for (int p = threadIdx.x; p < a.P; p += 256) out[p] = from_f<__nv_bfloat16>(0.f);
     return;
   }
+  float* S = a.state + ((int64_t)slot * a.H + h) * a.NS * a.P + c * V;
+  constexpr int U = 8;  // rows in flight a thread
+  const int n_end = r < rows ? a.NS : 0;
+  Vec<float, V> s[U];
+  auto load = [&](int n0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (n0 + u * rows < n_end) s[u] = vload<float, V>(S + (int64_t)(n0 + u * rows) * a.P);
+  };
+  load(r);  // the state first: everything else is on its way meanwhile
   for (int n = threadIdx.x; n < a.NS; n += 256) {
     sb[n] = to_f(a.B[(int64_t)b * a.ldb + grp * a.NS + n]);
     sc[n] = to_f(a.C[(int64_t)b * a.ldc + grp * a.NS + n]);
   }
   const float dt = load_dt(a, b, h), da = expf(dt * a.A[h]);
-  __syncthreads();
-  float* S = a.state + ((int64_t)slot * a.H + h) * a.NS * a.P + c * V;
   float xd[V], y[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     xd[v] = to_f(a.x[(int64_t)b * a.ldx + h * a.P + c * V + v]) * dt;
     y[v] = 0.f;
   }
-  if (r < rows) {
-    constexpr int U = 8;  // rows in flight a thread
+  __syncthreads();
 #pragma unroll 1
-    for (int n0 = r; n0 < a.NS; n0 += U * rows) {
-      float s[U][V];
+  for (int n0 = r; n0 < n_end; n0 += U * rows) {
+    if (n0 != r) load(n0);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = n0 + u * rows;
-        if (n < a.NS) vunpack<float, V>(vload<float, V>(S + (int64_t)n * a.P), s[u]);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + u * rows;
+      if (n < n_end) {
+        const float bn = sb[n], cn = sc[n];
+        float t[V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = n0 + u * rows;
-        if (n < a.NS) {
-          const float bn = sb[n], cn = sc[n];
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            s[u][v] = fmaf(da, s[u][v], bn * xd[v]);
-            y[v] = fmaf(cn, s[u][v], y[v]);
-          }
-          vstore<float, V>(S + (int64_t)n * a.P, s[u]);
+        for (int v = 0; v < V; ++v) {
+          t[v] = fmaf(da, s[u].e[v], bn * xd[v]);
+          y[v] = fmaf(cn, t[v], y[v]);
         }
+        vstore<float, V>(S + (int64_t)n * a.P, t);
       }
     }
+  }
+  if (r < rows) {
 #pragma unroll
     for (int v = 0; v < V; ++v) red[(r * cols + c) * V + v] = y[v];
   }

@@ -27,6 +27,7 @@ _I32 = torch.int32
 _U8 = torch.uint8
 _NONE3 = (0, 0, 0)
 
+_new = torch.empty
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 _lib = None
@@ -74,9 +75,9 @@ def _dense(where, dev, name, t, dtype, shape):
 def _empty(like, stream, shape, dtype):
     """Allocated on the stream the call runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _new(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return _new(shape, dtype=dtype, device=like.device)
 
 
 def _raw(stream, dev):
@@ -212,10 +213,13 @@ def sconv_step(x, weight, bias, state, slots=None, silu=True, out=None, stream=N
     t, S = x.dtype, state.shape[0]
     if out is None:
         out = _empty(x, stream, (B, C), t)
+        op = out.data_ptr()
+    else:
+        op = _dense(where, dev, "out", out, t, (B, C))
     code = _library().sconv_step(dt, x.data_ptr(), _rows(where, "x", x), wp, bp, wdt,
                                  _dense(where, dev, "state", state, t, (S, W - 1, C)),
-                                 _dense(where, dev, "slots", slots, _I32, (B,)), B, S, C, W, 1 if silu else 0,
-                                 _dense(where, dev, "out", out, t, (B, C)), _raw(stream, dev))
+                                 _dense(where, dev, "slots", slots, _I32, (B,)), B, S, C, W, 1 if silu else 0, op,
+                                 _raw(stream, dev))
     if code:
         _check(code, where)
     return out
@@ -309,10 +313,13 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, softplus=True, slots=N
     T, H, P, G, NS, args = _ssm_args(where, dev, x, dt, A, B, C, D, dt_bias)
     if out is None:
         out = _empty(x, stream, (T, H, P), _BF16)
+        op = out.data_ptr()
+    else:
+        op = _dense(where, dev, "out", out, _BF16, (T, H, P))
     S = state.shape[0]
     code = _library().ssm_step(*args, 1 if softplus else 0, _dense(where, dev, "state", state, _F32, (S, H, NS, P)),
-                               _dense(where, dev, "slots", slots, _I32, (T,)), T, S, H, P, G, NS,
-                               _dense(where, dev, "out", out, _BF16, (T, H, P)), _raw(stream, dev))
+                               _dense(where, dev, "slots", slots, _I32, (T,)), T, S, H, P, G, NS, op,
+                               _raw(stream, dev))
     if code:
         _check(code, where)
     return out
@@ -335,12 +342,15 @@ def _delta_step(where, kda, q, k, v, g, beta, state, scale, slots, out, qk_l2nor
     vals = (B, HV, 128)
     if out is None:
         out = _empty(q, stream, vals, _BF16)
+        op = out.data_ptr()
+    else:
+        op = _dense(where, dev, "out", out, _BF16, vals)
     ptrs = (_dense(where, dev, "q", q, _BF16, heads), _dense(where, dev, "k", k, _BF16, heads),
             _dense(where, dev, "v", v, _BF16, vals), _dense(where, dev, "g", g, _F32, vals if kda else (B, HV)),
             _dense(where, dev, "beta", beta, _BF16 if kda else _F32, (B, HV)),
             _dense(where, dev, "state", state, _F32, (S, HV, 128, 128)),
             _dense(where, dev, "slots", slots, _I32, (B,)), B, S)
-    tail = (scale, 1 if qk_l2norm else 0, _dense(where, dev, "out", out, _BF16, vals), _raw(stream, dev))
+    tail = (scale, 1 if qk_l2norm else 0, op, _raw(stream, dev))
     code = _library().kda_step(*ptrs, HV, *tail) if kda else _library().gdn_step(*ptrs, Hqk, HV, *tail)
     if code:
         _check(code, where)
@@ -438,12 +448,18 @@ def norm_fwd(x, weight=None, post_weight=None, gate=None, act="silu", residual=N
     dev = _device(where, x)
     shape, _, args = _norm_args(where, dev, x, weight, post_weight, gate, act, residual, res_scale, eps)
     t = x.dtype
-    if h is None and (residual is not None or weight is None):
+    hp = yp = 0
+    if h is not None:
+        hp = _dense(where, dev, "h", h, t, shape)
+    elif residual is not None or weight is None:
         h = _empty(x, stream, shape, t)
-    if y is None and weight is not None:
+        hp = h.data_ptr()
+    if y is not None:
+        yp = _dense(where, dev, "y", y, t, shape)
+    elif weight is not None:
         y = _empty(x, stream, shape, t)
-    code = _library().norm_fwd(*args, _dense(where, dev, "h", h, t, shape), _dense(where, dev, "y", y, t, shape),
-                               _raw(stream, dev))
+        yp = y.data_ptr()
+    code = _library().norm_fwd(*args, hp, yp, _raw(stream, dev))
     if code:
         _check(code, where)
     return h, y
