@@ -8,31 +8,37 @@
 namespace gdr {
 namespace {
 
-// Token by token: one block per (document, head, 32 columns of the state), the
-// state in registers (warp w holds rows w, w + 8, ...), tokens staged through
-// shared memory in tiles of 16.
+// Token by token, for shapes and layouts that the chunked kernels do not take
+// (state sizes above 128, sizes or rows that TMA cannot address): one block per
+// (document, head, 32 columns of the state), a warp four of them with the state's
+// rows on its lanes, in registers; tokens staged through shared memory in tiles of
+// 16.  Bound by the chain of tokens: about 0.14 us each.
 constexpr int kSeqTok = 16;
 __global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
   __shared__ float sx[kSeqTok][32], sb[kSeqTok][GDR_SSM_MAX_N], sc[kSeqTok][GDR_SSM_MAX_N];
   __shared__ float sdt[kSeqTok], sda[kSeqTok], sy[kSeqTok][32];
-  constexpr int R = GDR_SSM_MAX_N / 8;
+  constexpr int R = GDR_SSM_MAX_N / 32;
   const int slices = (a.P + 31) / 32;
   const int p0 = (blockIdx.x % slices) * 32, h = (blockIdx.x / slices) % a.H, d = blockIdx.x / slices / a.H;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p = p0 + lane, grp = h / (a.H / a.G);
-  const bool on = p < a.P;
-  const int t0 = a.cu[d], t1 = a.cu[d + 1];
-  float s[R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = h / (a.H / a.G);
+  const int t0 = a.cu[d], t1 = a.cu[d + 1], pw = p0 + 4 * warp;  // the warp's first column
+  float s[R][4];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int n = warp + 8 * i;
-    s[i] = a.h0 && on && n < a.NS ? a.h0[(((int64_t)d * a.H + h) * a.NS + n) * a.P + p] : 0.f;
+    const int n = lane + 32 * i;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      s[i][q] = a.h0 && pw + q < a.P && n < a.NS ? a.h0[(((int64_t)d * a.H + h) * a.NS + n) * a.P + pw + q] : 0.f;
   }
+  // state rows past NS: B and C stay zero there
+  for (int i = threadIdx.x; i < kSeqTok * GDR_SSM_MAX_N; i += 256) (&sb[0][0])[i] = (&sc[0][0])[i] = 0.f;
+  const int rows = (a.NS + 31) / 32;
   for (int t = t0; t < t1; t += kSeqTok) {
     const int len = min(kSeqTok, t1 - t);
+    __syncthreads();
     for (int i = threadIdx.x; i < len * 32; i += 256) {
       const int j = i >> 5, l = i & 31;
       sx[j][l] = p0 + l < a.P ? to_f(a.x[(int64_t)(t + j) * a.ldx + h * a.P + p0 + l]) : 0.f;
-      sy[j][l] = 0.f;
     }
     for (int i = threadIdx.x; i < len * a.NS; i += 256) {
       const int j = i / a.NS, n = i - j * a.NS;
@@ -45,36 +51,45 @@ __global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
       sda[threadIdx.x] = expf(dt * a.A[h]);
     }
     __syncthreads();
+#pragma unroll 1
     for (int j = 0; j < len; ++j) {
-      const float xd = sx[j][lane] * sdt[j], da = sda[j];
-      float y = 0.f;
+      const float4 x = *reinterpret_cast<const float4*>(&sx[j][4 * warp]);
+      const float dt = sdt[j], da = sda[j], xd[4] = {x.x * dt, x.y * dt, x.z * dt, x.w * dt};
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int n = warp + 8 * i;
-        if (n < a.NS) {
-          s[i] = fmaf(da, s[i], sb[j][n] * xd);
-          y = fmaf(sc[j][n], s[i], y);
+      for (int i = 0; i < R; ++i)
+        if (i < rows) {
+          const float b = sb[j][lane + 32 * i], c = sc[j][lane + 32 * i];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            s[i][q] = fmaf(da, s[i][q], b * xd[q]);
+            y[q] = fmaf(c, s[i][q], y[q]);
+          }
         }
-      }
-      // the warps' partial sums, in turn (a fixed order)
-      for (int w = 0; w < 8; ++w) {
-        if (w == warp) sy[j][lane] += y;
-        __syncthreads();
-      }
+      // the four sums over the lanes: halves of the warp take two each, quarters one
+      const bool up = lane & 16, up2 = lane & 8;
+      float u = (up ? y[2] : y[0]) + __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 16);
+      float v = (up ? y[3] : y[1]) + __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 16);
+      float w = (up2 ? v : u) + __shfl_xor_sync(0xffffffffu, up2 ? u : v, 8);
+#pragma unroll
+      for (int m = 4; m >= 1; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
+      if ((lane & 7) == 0) sy[j][4 * warp + (lane >> 3)] = w;
     }
+    __syncthreads();
     for (int i = threadIdx.x; i < len * 32; i += 256) {
       const int j = i >> 5, l = i & 31;
       if (p0 + l < a.P)
         a.out[((int64_t)(t + j) * a.H + h) * a.P + p0 + l] =
             from_f<__nv_bfloat16>(fmaf(a.D ? a.D[h] : 0.f, sx[j][l], sy[j][l]));
     }
-    __syncthreads();
   }
-  if (a.ht && on) {
+  if (a.ht) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int n = warp + 8 * i;
-      if (n < a.NS) a.ht[(((int64_t)d * a.H + h) * a.NS + n) * a.P + p] = s[i];
+      const int n = lane + 32 * i;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n < a.NS && pw + q < a.P) a.ht[(((int64_t)d * a.H + h) * a.NS + n) * a.P + pw + q] = s[i][q];
     }
   }
 }
