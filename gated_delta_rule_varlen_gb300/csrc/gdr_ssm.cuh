@@ -66,7 +66,7 @@ struct SsmPlan {
 };
 bool ssm_tc_shape(int P, int NS);
 bool ssm_tc_layout(const SsmArgs& a);
-SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu_host);
+SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu_host);
 cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, cudaStream_t st);
 
 }  // namespace gdr

@@ -43,6 +43,7 @@ struct TcArgs {
   SsmArgs a;
   const float* gates;  // [chunks][H][GATES], written by k_ssm_gates (Gates)
   int pblocks;      // ceil(P / 64)
+  int pairs;        // summaries: two neighbours a block
   int lseg;         // chunks of a segment at most
   float* seg;       // [segments][H][NS][P]: start states of split documents' segments
   float* gsum;      // [segments][H]: log2 decay over each segment
@@ -335,9 +336,9 @@ __device__ __forceinline__ void clear_pieces(unsigned char* tile, int j, int c0)
   for (int c = 0; c < N; ++c) *reinterpret_cast<uint4*>(tile + piece(j, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// w_j times the pieces [c0, c0 + N) of token row j (in `x`), as three blocks.
+// w_j times the pieces [c0, c0 + N) of token row j (in `x`), as three blocks `stride` bytes apart.
 template <int N>
-__device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char (*xw)[BLK], int j, int c0, float w) {
+__device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* xw, int stride, int j, int c0, float w) {
   const uint64_t ww = pack2(w, w);
 #pragma unroll
   for (int c = 0; c < N; ++c) {
@@ -347,9 +348,9 @@ __device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char (*xw
     split3(mul2(widen2(x[c].y), ww), h.y, m.y, l.y);
     split3(mul2(widen2(x[c].z), ww), h.z, m.z, l.z);
     split3(mul2(widen2(x[c].w), ww), h.w, m.w, l.w);
-    *reinterpret_cast<uint4*>(xw[0] + at) = h;
-    *reinterpret_cast<uint4*>(xw[1] + at) = m;
-    *reinterpret_cast<uint4*>(xw[2] + at) = l;
+    *reinterpret_cast<uint4*>(xw + at) = h;
+    *reinterpret_cast<uint4*>(xw + stride + at) = m;
+    *reinterpret_cast<uint4*>(xw + 2 * stride + at) = l;
   }
 }
 
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const uint4*>(s.X[n] + piece(r, 4 * half + p));
         const float ss = g.ss()[r], w = g.dt()[r] * ex2(ss), e = ex2(g.total(A) - ss);
         ee = pack2(e, e);
-        build_xw<4>(x, s.xw, r, 4 * half, w);
+        build_xw<4>(x, s.xw[0], BLK, r, 4 * half, w);
         tc::fence_proxy_async();
         warp_arrive(&s.xw_full[n]);
       }
@@ -746,16 +747,24 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 // Summary of a segment (split documents only): its end state from a zero start,
 //   U = B^T (w x) with w_j = dt_j exp(sum of the gates after j in the segment),
 // over its chunks, last chunk first, and its total decay.
-//   warp 0: TMA;  warp 1: MMA;  warps 4-7 / 8-11: w x of the even / odd steps
+// A block takes two neighbours (head, 64 columns) of a group, or one where a group's
+// number of them is odd; two share the chunks of B.
+//   warps 0, 2: TMA of x and B;  warp 1: MMA;  warps 4-19: w x, eight for the first / second neighbour
+//   (for the even / odd chunks where there is one), four for each half of a chunk
+// w x goes in three BF16 terms; the first two have an accumulator each, the third
+// joins the second's.  Of two neighbours the same terms lie side by side, so that
+// one MMA of 256 columns and one of 128 read a piece of B twice, not four times:
+// shared memory's bandwidth bounds the kernel.
 // The tensor cores' FP32 accumulation truncates, a bias that grows with the
-// number of products: after kBatch chunks warps 4-7 add the sums up in registers,
+// number of products: after kBatch chunks the warps add the sums up in registers,
 // while the other of two accumulators takes over.
 // ---------------------------------------------------------------------------
-constexpr int SUM_THREADS = 384, SUM_STAGES = 2, kBatch = 4;
+constexpr int SUM_THREADS = 640, SUM_STAGES = 2, kBatch = 4, kAhead = 6;
 struct SumSmem {
-  unsigned char B[SUM_STAGES][2 * BLK], X[SUM_STAGES][BLK];
-  unsigned char xw[2][3][BLK];  // step parity; w x in three terms
-  uint64_t full[SUM_STAGES], empty[SUM_STAGES], xw_full[2], xw_empty[2], acc_full[2], acc_empty[2], done;
+  unsigned char B[SUM_STAGES][2 * BLK], X[SUM_STAGES][2][BLK];
+  unsigned char xw[6][BLK];  // [term][neighbour], or [chunk parity][term]
+  uint64_t x_full[SUM_STAGES], x_empty[SUM_STAGES], b_full[SUM_STAGES], b_empty[SUM_STAGES];
+  uint64_t xw_full[2][2], xw_empty[2][2], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -767,9 +776,9 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   const SsmArgs& a = ta.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int per = a.H * ta.pblocks;
-  const int hp = blockIdx.x % per, h = hp / ta.pblocks, p0 = (hp % ta.pblocks) * PT, sid = blockIdx.x / per;
-  const int grp = h / (a.H / a.G);
+  const int two = ta.pairs, per = two ? a.H * ta.pblocks / 2 : a.H * ta.pblocks;
+  const int item = (blockIdx.x % per) << two, sid = blockIdx.x / per;  // the first neighbour
+  const int grp = item / ta.pblocks / (a.H / a.G);
   const int nblk = a.NS > 64 ? 2 : 1;
   if (warp == 0) {
     const Seg sg = find_segment(a.cu, a.N, ta.lseg, sid);
@@ -777,14 +786,18 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       s.seg = sg;
       s.abort = 0;
       for (int i = 0; i < SUM_STAGES; ++i) {
-        tc::mbar_init(&s.full[i], 1);
-        tc::mbar_init(&s.empty[i], 1);
+        tc::mbar_init(&s.x_full[i], 1);
+        tc::mbar_init(&s.x_empty[i], 8 << two);
+        tc::mbar_init(&s.b_full[i], 1);
+        tc::mbar_init(&s.b_empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&s.xw_full[i], 4);
-        tc::mbar_init(&s.xw_empty[i], 1);
+        for (int n = 0; n < 2; ++n) {
+          tc::mbar_init(&s.xw_full[i][n], 4 << two);
+          tc::mbar_init(&s.xw_empty[i][n], 1);
+        }
         tc::mbar_init(&s.acc_full[i], 1);
-        tc::mbar_init(&s.acc_empty[i], 4);
+        tc::mbar_init(&s.acc_empty[i], 8 << two);
       }
       tc::mbar_init(&s.done, 1);
       tc::mbar_fence_init();
@@ -804,17 +817,28 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   const int nch = sg.len / Q;  // a segment that is not its document's last holds whole chunks
   volatile int* ab = &s.abort;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
+      const bool is_x = warp == 0;
+      uint64_t* full = is_x ? s.x_full : s.b_full;
+      uint64_t* empty = is_x ? s.x_empty : s.b_empty;
       int issued = 0;
 #pragma unroll 1
       for (int k = 0, b = 0, ph = 1; k < nch; ++k) {
         const int row = sg.tok0 + (nch - 1 - k) * Q;
-        if (k >= SUM_STAGES && !wait_or_abort(&s.empty[b], ph, ab)) break;
-        tc::mbar_arrive_expect_tx(&s.full[b], (uint32_t)((1 + nblk) * BLK));
+        if (k >= SUM_STAGES && !wait_or_abort(&empty[b], ph, ab)) break;
+        tc::mbar_arrive_expect_tx(&full[b], (uint32_t)((is_x ? 1 + two : nblk) * BLK));
+        if (is_x) {
 #pragma unroll 1
-        for (int q = 0; q < nblk; ++q) tc::tma_load_3d(s.B[b] + q * BLK, &ta.b_map, 64 * q, grp, row, &s.full[b]);
-        tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.full[b]);
+          for (int n = 0; n <= two; ++n) {
+            const int x = (item + n) % ta.pblocks * PT, y = (item + n) / ta.pblocks;
+            tc::tma_load_3d(s.X[b][n], &ta.x_map, x, y, row, &full[b]);
+            if (k + kAhead < nch) tc::tma_prefetch_3d(&ta.x_map, x, y, row - kAhead * Q);
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < nblk; ++q) tc::tma_load_3d(s.B[b] + q * BLK, &ta.b_map, 64 * q, grp, row, &full[b]);
+        }
         issued = k + 1;
         if (++b == SUM_STAGES) {
           b = 0;
@@ -824,59 +848,66 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       // no copy is in flight when the block ends
 #pragma unroll 1
       for (int k = max(0, issued - SUM_STAGES); k < issued; ++k)
-        tc::mbar_wait(&s.full[k % SUM_STAGES], (k / SUM_STAGES) & 1);
+        tc::mbar_wait(&full[k % SUM_STAGES], (k / SUM_STAGES) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    constexpr uint32_t i_u = tc::idesc_bf16(128, 3 * PT) | tc::kIdescTransposeB | kIdescTransposeA;
-    const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0][0]);
-    constexpr uint32_t stage2 = 2 * BLK / 16, stage3 = 3 * BLK / 16, step = 2048 / 16;
+    const uint32_t i_hi = tc::idesc_bf16(128, 2 * PT << two) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t i_lo = tc::idesc_bf16(128, PT << two) | tc::kIdescTransposeB | kIdescTransposeA;
+    const uint32_t d_b = desc_lo(s.B[0]), d_w = desc_lo(s.xw[0]);
+    constexpr uint32_t blk = BLK / 16, step = 2048 / 16;
+    const uint32_t lo = (2 << two) * blk, mid = PT << two;  // third terms; second terms' accumulators
     uint32_t b = 0;
+    bool ok = true;
 #pragma unroll 1
-    for (int k = 0; k < nch; ++k) {
-      const uint32_t w = k & 1;
+    for (int k = 0; k < nch && ok; ++k) {
       const int batch = k / kBatch, first = k % kBatch == 0;
-      const uint32_t acc = (batch & 1) * 256;
-      bool ok = warp_wait(&s.xw_full[w], (k >> 1) & 1, ab);  // (whose warps waited for B and x)
+      const uint32_t m = two ? 0 : k & 1, acc = tmem + (batch & 1) * 256;
+      const uint32_t bb = d_b + b * 2 * blk, ww = d_w + m * 3 * blk;
+      ok = warp_wait(&s.b_full[b], (k / SUM_STAGES) & 1, ab);
       if (first && batch >= 2) ok = ok && warp_wait(&s.acc_empty[batch & 1], ((batch >> 1) - 1) & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        mma_ss(tmem + acc, d_b + b * stage2 + q * step, d_w + w * stage3 + q * step, i_u, !first || q > 0);
-      commit(&s.empty[b]);
-      commit(&s.xw_empty[w]);
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && warp_wait(&s.xw_full[m][half], (two ? k : k >> 1) & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int q = 4 * half; q < 4 * half + 4; ++q) mma_ss(acc, bb + q * step, ww + q * step, i_hi, !first || q > 0);
+#pragma unroll
+        for (int q = 4 * half; q < 4 * half + 4; ++q) mma_ss(acc + mid, bb + q * step, ww + lo + q * step, i_lo, true);
+        commit(&s.xw_empty[m][half]);
+      }
       if (k % kBatch == kBatch - 1 || k == nch - 1) commit(&s.acc_full[batch & 1]);
+      commit(&s.b_empty[b]);
       b = b == SUM_STAGES - 1 ? 0 : b + 1;
     }
     commit(&s.done);
     tc::mbar_wait(&s.done, 0);
     __syncwarp();
   } else if (warp >= 4) {
-    const int g = (warp - 4) >> 2, j = (tid - 128) & 127;
+    // group g: half a chunk's rows, a row's 32 columns a thread; state row j's 32 columns
+    const int g = (warp - 4) >> 2, half = g & 1, j = (tid - 128) & 127, r = 64 * half + (j & 63), c0 = 4 * (j >> 6);
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int n = two ? g >> 1 : 0, h = (item + n) / ta.pblocks, p0 = (item + n) % ta.pblocks * PT;
+    const bool sums = two || g < 2;
     const float A = a.A[h] * LOG2E;
-    const uint64_t one = pack2(1.f, 1.f);
     float tail = 0.f;  // the gates after this chunk
-    uint64_t S[PT / 2];  // state row j (warps 4-7)
+    uint64_t S[PT / 4];
 #pragma unroll
-    for (int q = 0; q < PT / 2; ++q) S[q] = 0;
+    for (int q = 0; q < PT / 4; ++q) S[q] = 0;
     auto drain = [&](int batch) {
       if (!warp_wait(&s.acc_full[batch & 1], (batch >> 1) & 1, ab)) return false;
       tc::tc_fence_after();
 #pragma unroll
-      for (int p = 0; p < PT; p += 8) {
-        uint32_t u[8], v[8], w[8];
-        tmem_ld8(trow + (batch & 1) * 256 + p, u);
-        tmem_ld8(trow + (batch & 1) * 256 + PT + p, v);
-        tmem_ld8(trow + (batch & 1) * 256 + 2 * PT + p, w);
+      for (int p = 0; p < PT / 2; p += 8) {
+        uint32_t u[8], v[8];
+        tmem_ld8(trow + (batch & 1) * 256 + n * PT + PT / 2 * half + p, u);
+        tmem_ld8(trow + (batch & 1) * 256 + (PT << two) + n * PT + PT / 2 * half + p, v);
         wait_ld(u);
         wait_ld(v);
-        wait_ld(w);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          S[p / 2 + q] =
-              fma2(one, fma2(one, pair_of(u + 2 * q), fma2(one, pair_of(v + 2 * q), pair_of(w + 2 * q))), S[p / 2 + q]);
+          S[p / 2 + q] = add2(add2(pair_of(u + 2 * q), pair_of(v + 2 * q)), S[p / 2 + q]);
       }
       tc::tc_fence_before();
       warp_arrive(&s.acc_empty[batch & 1]);
@@ -884,42 +915,53 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
     };
     bool ok = true;
     int drained = 0;
+    float dt, ss, total;  // a chunk ahead
+    auto gates = [&](int k) {
+      const Gates ga = gates_of(ta, sg.chunk0 + nch - 1 - k, h);
+      dt = ga.dt()[r], ss = ga.ss()[r], total = ga.total(A);
+    };
+    gates(0);
 #pragma unroll 1
     for (int k = 0, b = 0, ph = 0; k < nch; ++k) {
-      const Gates ga = gates_of(ta, sg.chunk0 + nch - 1 - k, h);
-      if ((k & 1) == g) {
-        const float w = ga.dt()[j] * ex2(ga.ss()[j] + tail);
-        ok = k < 2 || warp_wait(&s.xw_empty[g], ((k >> 1) - 1) & 1, ab);
-        ok = ok && warp_wait(&s.full[b], ph, ab);
+      const float w = dt * ex2(ss + tail);
+      tail += total;
+      gates(min(k + 1, nch - 1));
+      if (two || (k & 1) == g >> 1) {
+        const int m = two ? 0 : k & 1, use = two ? k : k >> 1;
+        ok = warp_wait(&s.x_full[b], ph, ab);
         if (!ok) break;
-        uint4 x[8];
+        uint4 x[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[b] + piece(j, c));
-        build_xw<8>(x, s.xw[g], j, 0, w);
+        for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[b][n] + piece(r, c0 + c));
+        warp_arrive(&s.x_empty[b]);
+        ok = use < 1 || warp_wait(&s.xw_empty[m][half], (use - 1) & 1, ab);
+        if (!ok) break;
+        build_xw<4>(x, s.xw[3 * m + n], BLK << two, r, c0, w);
         tc::fence_proxy_async();
-        warp_arrive(&s.xw_full[g]);
+        warp_arrive(&s.xw_full[m][half]);
       }
-      tail += ga.total(A);
       if (++b == SUM_STAGES) {
         b = 0;
         ph ^= 1;
       }
       // a batch behind: its last product has had time to finish
-      if (g == 0 && k % kBatch == kBatch - 1 && k >= 2 * kBatch - 1) {
+      if (sums && k % kBatch == kBatch - 1 && k >= 2 * kBatch - 1) {
         ok = drain(drained++);
         if (!ok) break;
       }
     }
-    if (g == 0) {
+    if (sums) {
 #pragma unroll 1
       while (ok && drained * kBatch < nch) ok = drain(drained++);
       if (ok && j < a.NS) {
-        float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + j) * a.P + p0;
+        float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + j) * a.P;
 #pragma unroll
-        for (int q = 0; q < PT / 2; q += 2)
-          if (p0 + 2 * q < a.P) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(S[q], S[q + 1]);
+        for (int q = 0; q < PT / 4; q += 2) {
+          const int p = p0 + PT / 2 * half + 2 * q;
+          if (p < a.P) *reinterpret_cast<ulonglong2*>(to + p) = make_ulonglong2(S[q], S[q + 1]);
+        }
       }
-      if (j == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
+      if (j == 0 && half == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
     }
   }
   tc::tc_fence_before();
@@ -1019,11 +1061,16 @@ bool ssm_tc_layout(const SsmArgs& a) {
   return a.T <= 1 || (a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0);
 }
 
+// Whether the summaries' blocks take two neighbouring (head, 64 columns) of a group.
+static int ssm_pairs(int H, int P, int G) { return H / G * ((P + 63) / 64) % 2 == 0; }
+
 // Whole documents while they keep the SMs evenly busy; else the segment length
-// with the least estimated time, in chunk steps of one block: kStart steps to
-// start a block, kSum for a summary's step.
-SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
-  constexpr double kStart = 3.0, kSum = 0.4;
+// with the least estimated time, in chunk steps of one walking block: kStart steps
+// to start a block, kSum for a chunk of a summary (of one (head, 64 columns) or of
+// two).
+SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
+  const int pairs = ssm_pairs(H, P, G);
+  const double kStart = 3.0, kSum = pairs ? 0.8 : 0.55;
   const int64_t items = (int64_t)H * ((P + 63) / 64);
   const double sms = 152.0;
   int64_t nc = 0, most = 0;
@@ -1043,16 +1090,16 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int N, const int32_t* cu) {
   // pieces of the longest document
   for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
     const int64_t L = (most + k - 1) / k;
-    int64_t nseg = 0, again = 0;
+    int64_t nseg = 0, ends = 0;
     for (int i = 0; i < N; ++i) {
       const int64_t ch = (cu[i + 1] - (int64_t)cu[i] + Q - 1) / Q;
       const int64_t n = ch == 0 ? 1 : (ch + L - 1) / L;
       nseg += n;
-      if (n > 1) again += ch - ch / n;
+      ends += std::max<int64_t>(n, 1) - 1;
     }
     const double waves = (double)nseg * items / sms;
     const double walk = std::max((nc + kStart * nseg) * items / sms, (double)(L + kStart) * (int64_t)(waves + 0.999));
-    const double sum = std::max(kSum * again * items / sms, kSum * L) + 2 * kStart;
+    const double sum = kSum * L * (int64_t)((double)(ends * items >> pairs) / sms + 0.999) + 2 * kStart;
     if (walk + sum < 0.95 * cost) {
       cost = walk + sum;
       best.lseg = (int)L;
@@ -1088,6 +1135,7 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
   if (cudaError_t e = cudaGetLastError()) return e;
   char* rest = static_cast<char*>(scratch) + up256((size_t)plan.chunks * a.H * GATES * sizeof(float));
   const unsigned grid = (unsigned)(plan.nseg * a.H * t.pblocks);
+  t.pairs = ssm_pairs(a.H, a.P, a.G);
   constexpr int sm_walk = (int)sizeof(WalkSmem), sm_sum = (int)sizeof(SumSmem);
   static_assert(sm_walk <= 232448 && sm_sum <= 232448, "227 KB of shared memory a block");
   if (plan.split) {
@@ -1096,7 +1144,7 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
     cudaFuncSetAttribute(k_ssm_sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_sum);
     {
       ProfScope ps("ssm_sum", st, (double)a.T * a.H);
-      k_ssm_sum<<<grid, SUM_THREADS, sm_sum, st>>>(t);
+      k_ssm_sum<<<grid >> t.pairs, SUM_THREADS, sm_sum, st>>>(t);
     }
     if (cudaError_t e = cudaGetLastError()) return e;
     ProfScope ps("ssm_merge", st);

@@ -247,6 +247,37 @@ def test_ssm_prompt_equals_its_pieces(gdr, lengths, H, G):
         at += m
 
 
+@pytest.mark.parametrize("lengths,H,P,G,N", [
+    ([3000], 3, 64, 1, 96),        # an odd number of heads a group
+    ([40, 2900], 3, 128, 3, 64),   # one head a group, in two column blocks
+    ([2700], 2, 80, 2, 24),        # the second column block part empty, one block of state rows
+    ([2600, 1], 5, 72, 1, 128),
+])
+def test_ssm_prompt_in_segments(gdr, lengths, H, P, G, N):
+    g, T, n = gen(H * P + N + 1), sum(lengths), len(lengths)
+    x, dt, A, B, C, D, bias = scan_inputs(g, T, H, P, G, N, F32)
+    h0, cu, cuh = randn(g, n, H, N, P), *pack(lengths)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, cu, cuh, D=D, dt_bias=bias, h0=h0, ht=full((n, H, N, P), F32))
+    torch.cuda.synchronize()
+    gdr.gdr_check_device()
+    act = torch.nn.functional.softplus(dt.double() + bias.double())
+    ro, rh = ref.scan(x.double(), act, A.double(), B.double(), C.double(), D.double(), lengths, h0.double())
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
+def test_ssm_prompt_carries_nan(gdr):
+    # a NaN reaches every later token of its own document and head, across segments, and no other
+    g, P, N, H, lengths = gen(8), 64, 128, 2, [200, 3000]
+    x, dt, A, B, C, D, bias = scan_inputs(g, sum(lengths), H, P, 1, N, F32)
+    at = 200 + 131
+    x[at, 1, 7] = float("nan")
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *pack(lengths), D=D, dt_bias=bias)
+    assert torch.isnan(out[at:, 1, 7]).all() and torch.isnan(ht[1, 1, :, 7]).all()
+    assert torch.isfinite(out[:, 0]).all() and torch.isfinite(out[:200]).all() and torch.isfinite(ht[0]).all()
+    assert torch.isfinite(out[200:at // 128 * 128]).all()  # earlier tokens of the same chunk may see it
+
+
 @pytest.mark.parametrize("decay,dtv", [(0.0, 0.05), (-1e4, 1.0), (-16.0, 20.0), (-1e-3, 1e-3)])
 def test_ssm_prompt_extreme_decays(gdr, decay, dtv):
     # no decay at all, states that vanish within a token, and both ends between, without softplus
