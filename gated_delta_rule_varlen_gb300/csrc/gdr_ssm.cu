@@ -9,7 +9,8 @@ namespace gdr {
 namespace {
 
 // Token by token, for shapes and layouts that the chunked kernels do not take
-// (state sizes above 128, sizes or rows that TMA cannot address): one block per
+// (state sizes above 128, sizes or rows that TMA cannot address) and for packs of
+// short documents (short_documents()): one block per
 // (document, head, 32 columns of the state), a warp four of them with the state's
 // rows on its lanes, R a lane in registers; tokens staged through shared memory in
 // tiles of 32 and taken four at a time, so that their sums over the lanes overlap.
@@ -25,12 +26,18 @@ __global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = h / (a.H / a.G);
   const int t0 = a.cu[d], t1 = a.cu[d + 1], pw = p0 + 4 * warp;  // the warp's first column
   float s[R][4];
+  const int64_t state = (((int64_t)d * a.H + h) * a.NS + lane) * a.P + pw;
+  const bool quads = a.P % 4 == 0 && (((uintptr_t)a.h0 | (uintptr_t)a.ht) & 15) == 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int n = lane + 32 * i;
+    const float* from = a.h0 && lane + 32 * i < a.NS ? a.h0 + state + (int64_t)32 * i * a.P : nullptr;
+    if (quads) {
+      const float4 v = from && pw < a.P ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+      s[i][0] = v.x, s[i][1] = v.y, s[i][2] = v.z, s[i][3] = v.w;
+    } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      s[i][q] = a.h0 && pw + q < a.P && n < a.NS ? a.h0[(((int64_t)d * a.H + h) * a.NS + n) * a.P + pw + q] : 0.f;
+      for (int q = 0; q < 4; ++q) s[i][q] = from && pw + q < a.P ? from[q] : 0.f;
+    }
   }
   auto token = [&](int j) {
     const float4 x = *reinterpret_cast<const float4*>(&sx[j][4 * warp]);
@@ -99,10 +106,15 @@ __global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
   if (a.ht) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int n = lane + 32 * i;
+      if (lane + 32 * i >= a.NS) break;
+      float* to = a.ht + state + (int64_t)32 * i * a.P;
+      if (quads && pw < a.P) {
+        *reinterpret_cast<float4*>(to) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n < a.NS && pw + q < a.P) a.ht[(((int64_t)d * a.H + h) * a.NS + n) * a.P + pw + q] = s[i][q];
+        for (int q = 0; q < 4; ++q)
+          if (pw + q < a.P) to[q] = s[i][q];
+      }
     }
   }
 }
@@ -177,6 +189,18 @@ __global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
   }
 }
 
+// Whether the documents are short enough to go token by token.  The chunked
+// kernels work on 128 tokens whatever a document has; up to 32 tokens (a tile)
+// each the tokens one by one are faster: 64 documents of 64 heads x 128 x 64 states,
+// with h0 and ht, take 107, 186, 281, 397 us at 2, 16, 32, 48 tokens, in chunks
+// 256-260; of 8 heads x 64 x 64 17, 25, 33, 44 against 41; of 32 heads x 32 x 128 42, 88,
+// 145, 212 against 172-187.
+bool short_documents(int N, const int32_t* cu) {
+  for (int i = 0; i < N; ++i)
+    if (cu[i + 1] - cu[i] > kSeqTok) return false;
+  return true;
+}
+
 gdr_status ssm_check(const SsmArgs& a, int64_t T) {
   if (a.H <= 0 || a.G <= 0 || a.H % a.G != 0 || a.P <= 0 || a.P > GDR_SSM_MAX_P || a.NS <= 0 ||
       a.NS > GDR_SSM_MAX_N || T < 0)
@@ -244,14 +268,14 @@ gdr_status ssm_fwd(const gdr_bf16* x, int64_t ldx, const void* dt, int dt_dtype,
   if (N == 0) return GDR_OK;
   if (!cu_seqlens) return GDR_INVALID_ARG;
   // The chunked kernels need rows that TMA can address; others go token by token.
-  const bool tc = ssm_tc_shape(P, NS) && ssm_tc_layout(a);
-  if (tc) {
+  if (ssm_tc_shape(P, NS) && ssm_tc_layout(a)) {
     const SsmPlan plan = ssm_tc_plan(H, P, NS, G, N, cu_seqlens_host);
     if (plan.nseg * H * ((P + 63) / 64) > INT32_MAX) return GDR_INVALID_ARG;
     if (plan.scratch > 0 && (!scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
     if (scratch_bytes < plan.scratch) return GDR_WORKSPACE_TOO_SMALL;
     if ((rc = check_device()) != GDR_OK) return rc;
-    return launch_ssm_tc(a, plan, scratch, stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+    if (!short_documents(N, cu_seqlens_host))
+      return launch_ssm_tc(a, plan, scratch, stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
   }
   const int64_t grid = (int64_t)N * H * ((P + 31) / 32);
   if (grid > INT32_MAX) return GDR_INVALID_ARG;

@@ -266,6 +266,27 @@ def test_ssm_prompt_in_segments(gdr, lengths, H, P, G, N):
     check(ht, rh, "ht")
 
 
+@pytest.mark.parametrize("lengths,H,P,G,N,odd", [
+    ([32, 1, 0, 31, 4], 4, 64, 2, 128, False),    # every document short
+    ([33, 1, 0, 31, 4], 4, 64, 2, 128, False),    # one a token longer
+    ([2, 5], 2, 72, 1, 40, False),
+    ([7, 32, 3], 3, 66, 1, 33, False),
+    ([30, 9], 2, 44, 1, 200, True),
+])
+def test_ssm_prompt_short(gdr, lengths, H, P, G, N, odd):
+    g, T, n = gen(H + P * N), sum(lengths), len(lengths)
+    x, dt, A, B, C, D, bias = scan_inputs(g, T, H, P, G, N, F32, 0, odd)
+    h0, cu, cuh = randn(g, n, H, N, P), *pack(lengths)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, cu, cuh, D=D, dt_bias=bias, h0=h0, out=full((T, H, P), BF16),
+                          ht=full((n, H, N, P), F32))
+    torch.cuda.synchronize()
+    gdr.gdr_check_device()
+    act = torch.nn.functional.softplus(dt.double() + bias.double())
+    ro, rh = ref.scan(x.double(), act, A.double(), B.double(), C.double(), D.double(), lengths, h0.double())
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
 def test_ssm_prompt_carries_nan(gdr):
     # a NaN reaches every later token of its own document and head, across segments, and no other
     g, P, N, H, lengths = gen(8), 64, 128, 2, [200, 3000]
