@@ -3,9 +3,10 @@
 //   u = u act(z)                   with a gate z: act = silu or sigmoid
 //   h = residual + alpha u         or  u
 //   y = h r2 w,                    r2 = (mean h^2 + eps)^(-1/2)
-// Every step is optional.  A row (of D elements) is held in registers by TPR
-// threads from its one read to its one write; the means are FP32 sums by
-// shuffles (and across warps through shared memory) in a fixed order.
+// Every step is optional.  A row (of D elements) is held in registers from its
+// one read to its one write, by a few lanes of a warp, by a block, or, past 2048
+// elements of BF16, by a cluster of blocks; the means are FP32 sums by shuffles
+// (and across warps and blocks through shared memory) in a fixed order.
 #pragma once
 #include "gdr_ops.cuh"
 #include <algorithm>
@@ -32,76 +33,147 @@ struct NormArgs {
   // backward
   RowTensor dh, dy;        // or null
   void *dx, *dgate, *dres; // dense, or null
-  float* part;             // [blocks][2][D]: partial dw, dw_post
+  float* part;             // [row groups][2][D]: partial dw, dw_post
 };
 
-// The threads of a row: TPR of them with NV vectors of V elements each.
+// The threads of a row, with NV vectors of V elements each: TPR <= 32 lanes (a block
+// of 128 threads works on 128 / TPR rows at a time), a block of TPR threads, or
+// `cluster` > 0 blocks of 128.  shift: rows of any length whose pieces of 16 bytes
+// start before the row (norm_shape).
+constexpr int MAX_CLUSTER = 16;
 struct NormShape {
-  int V, TPR, NV;
+  int V, TPR, NV, cluster, shift;
 };
+constexpr int norm_threads(int TPR) { return TPR <= 32 ? 128 : TPR; }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, cudaStream_t st);
-// *blocks: how many blocks ran (and left a partial row each)
-cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* blocks, cudaStream_t st);
+// *parts: how many partial rows of weight gradients it left
+cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* parts, cudaStream_t st);
 
-// Most blocks of an SM that a backward is launched with, by threads of a block.
-constexpr int norm_blocks_per_sm(int threads) { return threads <= 128 ? 8 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1; }
+// Most blocks of an SM that a backward on rows of D elements is launched with.
+constexpr int norm_bwd_blocks(int D) { return D <= 2048 ? 8 : 3; }
 
-// Threads in a block of a shape: 128 for the shapes of up to a warp a row.
-constexpr int norm_threads(int TPR) { return TPR < 128 ? 128 : TPR; }
-
-// As many blocks as the GPU holds at a time (each goes through its share of the
-// rows), or fewer where there are fewer rows.
+// Launches as many row groups (blocks or clusters, each goes through its share of
+// the rows) as the GPU holds at a time, or fewer where there are fewer rows; a
+// shifted row keeps its place within 16 bytes from one of a thread's rows to the
+// next (the step between them is a multiple of V).  held: what the GPU holds, by
+// cluster, kept from call to call.
 template <typename K>
-int norm_grid(K kernel, int threads, size_t smem, int64_t groups, int occ_limit, int* occ_cache) {
-  if (*occ_cache == 0) {
-    int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess || occ < 1) occ = 1;
-    *occ_cache = occ;
+cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t smem, int limit,
+                        int (&held)[MAX_CLUSTER + 1], int* parts, cudaStream_t st) {
+  const int threads = norm_threads(s.TPR), groups = threads / s.TPR, size = s.cluster > 0 ? s.cluster : 1;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = s.cluster > 0 ? 1 : 0;
+  int& most = held[s.cluster];
+  if (most == 0) {
+    int n = 0;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    if (s.cluster > 0) {
+      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+      cfg.gridDim = dim3(152 / size * size);
+      if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) return e;
+      n = std::min(n, 152 * limit / size);
+    } else {
+      if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem)) return e;
+      n = 152 * std::min(n, limit);
+    }
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    most = n;
   }
-  const int64_t most = (int64_t)152 * std::min(*occ_cache, occ_limit);
-  return (int)std::min<int64_t>(groups, most);
+  int64_t n = std::min<int64_t>((a.rows + groups - 1) / groups, most);
+  if (s.shift && s.V > groups) {
+    const int64_t unit = s.V / groups;
+    n = std::max(unit, n / unit * unit);
+  }
+  *parts = (int)n;
+  cfg.gridDim = dim3((unsigned)(n * size));
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int TPR>
-struct RowGroup {
-  static constexpr int THREADS = norm_threads(TPR);
-  static constexpr int GROUPS = THREADS / TPR;  // rows a block works on at a time
-  static constexpr int WARPS = TPR > 32 ? TPR / 32 : 1;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// v to the place of `at` in block `rank` of the cluster.
+__device__ __forceinline__ void store_at_peer(float2* at, int rank, float2 v) {
+  asm volatile(
+      "{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.v2.f32 [p], {%2, %3};\n}\n" ::"r"(
+          (uint32_t)__cvta_generic_to_shared(at)),
+      "r"(rank), "f"(v.x), "f"(v.y)
+      : "memory");
+}
 
-  // Sum of a over the row's threads, on every thread of the row.
-  static __device__ __forceinline__ void sum(float& a, float2* sm) {
-    constexpr int W = TPR < 32 ? TPR : 32;
-#pragma unroll
-    for (int m = W / 2; m >= 1; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
-    if constexpr (TPR > 32) {
-      const int warp = threadIdx.x >> 5;
-      if ((threadIdx.x & 31) == 0) sm[warp].x = a;
-      __syncthreads();
-      a = 0.f;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) a += sm[i].x;
+// This thread's place: its rows are first, first + step, ...; in each it has the
+// vectors lane, lane + lanes, ...
+template <int TPR, bool CLUSTER>
+struct RowGroup {
+  static constexpr int THREADS = norm_threads(TPR), GROUPS = THREADS / TPR;  // rows a block works on at a time
+  static constexpr int WARPS = TPR > 32 ? TPR / 32 : 1, SUMS = CLUSTER ? WARPS * MAX_CLUSTER : WARPS;
+  int lanes = TPR, lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, rank = 0, cluster = 1;
+  int64_t first = (int64_t)blockIdx.x * GROUPS + grp, step = (int64_t)gridDim.x * GROUPS;
+
+  __device__ __forceinline__ RowGroup() {
+    if constexpr (CLUSTER) {
+      asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(rank));
+      asm("mov.u32 %0, %%cluster_nctaid.x;\n" : "=r"(cluster));
+      lanes = TPR * cluster;
+      lane = TPR * rank + (int)threadIdx.x;
+      first = blockIdx.x / cluster;
+      step = gridDim.x / cluster;
+      cluster_sync();  // the others' shared memory is there
     }
   }
-  static __device__ __forceinline__ void sum2(float& a, float& b, float2* sm) {
+  // All threads of the row.
+  __device__ __forceinline__ void sync() const {
+    if constexpr (CLUSTER) cluster_sync();
+    else if constexpr (TPR > 32) __syncthreads();
+  }
+  // Sums of N values over the row's threads, on every thread of the row.  Two calls
+  // in a row take different buffers: whoever writes one again has passed the
+  // other's barrier, which its readers reach after it.
+  template <int N>
+  __device__ __forceinline__ void sum(float (&a)[N], float2* sm) const {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
-    for (int m = W / 2; m >= 1; m >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, m);
-      b += __shfl_xor_sync(0xffffffffu, b, m);
-    }
-    if constexpr (TPR > 32) {
-      const int warp = threadIdx.x >> 5;
-      if ((threadIdx.x & 31) == 0) sm[warp] = make_float2(a, b);
-      __syncthreads();
-      a = 0.f;
-      b = 0.f;
+    for (int m = W / 2; m >= 1; m >>= 1)
 #pragma unroll
-      for (int i = 0; i < WARPS; ++i) {
-        const float2 v = sm[i];
-        a += v.x;
-        b += v.y;
+      for (int n = 0; n < N; ++n) a[n] += __shfl_xor_sync(0xffffffffu, a[n], m);
+    if constexpr (TPR > 32) {
+      const int warp = threadIdx.x >> 5, in_warp = threadIdx.x & 31;
+      const float2 own = make_float2(a[0], a[N - 1]);
+      if constexpr (CLUSTER) {
+        if (in_warp < cluster) store_at_peer(sm + rank * WARPS + warp, in_warp, own);
+        cluster_sync();
+      } else {
+        if (in_warp == 0) sm[warp] = own;
+        __syncthreads();
       }
+#pragma unroll
+      for (int n = 0; n < N; ++n) a[n] = 0.f;
+      if constexpr (CLUSTER) {
+#pragma unroll 1
+        for (int i = 0; i < cluster; ++i) add<N>(a, sm + i * WARPS);
+      } else {
+        add<N>(a, sm);
+      }
+    }
+  }
+
+ private:
+  template <int N>
+  static __device__ __forceinline__ void add(float (&a)[N], const float2* sm) {
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+      const float2 v = sm[i];
+      a[0] += v.x;
+      if (N == 2) a[N - 1] += v.y;
     }
   }
 };
@@ -138,20 +210,68 @@ struct Cursor {
 };
 
 // The rows a thread works on next, asked for DEPTH rows ahead: ITEMS vectors of
-// the thread a row, in shared memory (gdr_ops.cuh: RowRing).
-template <typename T, int V, int ITEMS, int DEPTH, int THREADS>
+// the thread a row, by asynchronous copies to shared memory, so that more bytes are
+// in flight than registers would hold.  A thread reads its own copies only.  The
+// threads' vectors lie side by side: with a thread's own together the gated norm's
+// training took 1.4 times as long.
+template <typename T, int V, int ITEMS, int DEPTH, int THREADS, bool WHOLE>
 struct RowsAhead {
-  static constexpr int BYTES = DEPTH * ITEMS * THREADS * (int)sizeof(Vec<T, V>);
-  RowRing<T, V, DEPTH * ITEMS, THREADS> ring;
-  __device__ __forceinline__ explicit RowsAhead(void* smem) : ring(smem) {}
-  __device__ __forceinline__ void ask(int slot, int item, const T* src) { ring.push(slot * ITEMS + item, src, true); }
-  __device__ __forceinline__ Vec<T, V> get(int slot, int item) const { return ring.at(slot * ITEMS + item); }
+  using Item = Vec<T, V>;
+  static constexpr int BYTES = ITEMS * DEPTH * THREADS * (int)sizeof(Item);
+  Item* base;
+  __device__ __forceinline__ explicit RowsAhead(void* smem) : base(static_cast<Item*>(smem) + threadIdx.x) {}
+  // The first `bytes` of a vector, zeros behind (WHOLE: all).
+  __device__ __forceinline__ void ask(int slot, int item, const T* src, int bytes) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(base + (slot * ITEMS + item) * THREADS));
+    if constexpr (sizeof(Item) != 16)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(d), "l"(src), "n"((int)sizeof(Item)) : "memory");
+    else if constexpr (WHOLE)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+  }
+  __device__ __forceinline__ Item get(int slot, int item) const { return base[(slot * ITEMS + item) * THREADS]; }
 };
+// Rows ahead of kernels whose threads take `bytes` each a row: as many as fit what
+// a block may take of shared memory, four at most.
+constexpr int rows_ahead(int threads, int bytes) {
+  const int room = threads <= 128 ? 40 << 10 : threads <= 256 ? 80 << 10 : threads <= 384 || (threads <= 512 && bytes <= 48) ? 100 << 10 : 200 << 10;
+  const int n = room / (threads * bytes);
+  return n < 4 ? n : 4;
+}
+
+// Vectors of a shifted row: elements before the row or past its end read as zero
+// and are not written.
+template <int V>
+__device__ __forceinline__ void clip_pairs(uint64_t (&f)[pairs_of<V>], int c, int D) {
+#pragma unroll
+  for (int i = 0; i < pairs_of<V>; ++i) {
+    float a, b;
+    unpack2(f[i], a, b);
+    const int k = c + 2 * i;
+    f[i] = pack2(k >= 0 && k < D ? a : 0.f, k + 1 >= 0 && k + 1 < D ? b : 0.f);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_clipped(T* row, int c, int D, const uint64_t (&f)[pairs_of<V>]) {
+#pragma unroll
+  for (int i = 0; i < pairs_of<V>; ++i) {
+    float a, b;
+    unpack2(f[i], a, b);
+    const int k = c + 2 * i;
+    if (k >= 0 && k < D) row[k] = from_f<T>(a);
+    if (k + 1 >= 0 && k + 1 < D) row[k + 1] = from_f<T>(b);
+  }
+}
 
 // V elements of a weight from c on, in pairs.
-template <typename T, int V>
+template <typename T, int V, bool SHIFT>
 __device__ __forceinline__ void load_weight(const NormArgs& a, const void* p, int c, uint64_t (&f)[pairs_of<V>]) {
-  if (V > 1 && a.wvec) {
+  if constexpr (SHIFT) {
+    auto at = [&](int k) { return k >= 0 && k < a.D ? load_param<T>(p, a.wf32, k) : 0.f; };
+#pragma unroll
+    for (int i = 0; i < pairs_of<V>; ++i) f[i] = pack2(at(c + 2 * i), at(c + 2 * i + 1));
+  } else if (V > 1 && a.wvec) {
     if (a.wf32) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {

@@ -10,36 +10,56 @@ namespace {
 // Arithmetic in pairs of columns, so that its instructions fit beside the loads.
 // OUT: the norm of a block's output alone (and its gate), without the residual
 // and the second norm: fewer registers.
-template <typename T, int V, int TPR, int NV, bool OUT>
+template <typename T, int V, int TPR, int NV, bool OUT, bool SHIFT>
+struct FwdRows {
+  static constexpr int ITEMS = (OUT ? 2 : 3) * NV, THREADS = norm_threads(TPR);
+  static constexpr int DEPTH = rows_ahead(THREADS, ITEMS * V * (int)sizeof(T));
+  static constexpr bool AHEAD = V * sizeof(T) >= 4 && DEPTH >= 1;  // (no copies of two bytes)
+  using Rows = RowsAhead<T, AHEAD ? V : 8, ITEMS, DEPTH, THREADS, !SHIFT>;
+};
+
+template <typename T, int V, int TPR, int NV, bool CLUSTER, bool OUT, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
-  using G = RowGroup<TPR>;
-  constexpr int P = pairs_of<V>;
-  constexpr bool KEEP = NV * V <= 16;
-  __shared__ float2 sm[2][G::WARPS];
-  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  using F = FwdRows<T, V, TPR, NV, OUT, SHIFT>;
+  using Rows = typename F::Rows;
+  constexpr bool AHEAD = F::AHEAD;
+  constexpr int P = pairs_of<V>, DEPTH = F::DEPTH;
+  __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
+  const RowGroup<TPR, CLUSTER> g;
+  // a shifted row's vectors start m elements before it, on 16 bytes
+  const int m = SHIFT ? (int)(g.first % V) * (a.D % V) % V : 0;
+  auto col = [&](int i) { return (i * g.lanes + g.lane) * V - m; };
+  auto whole = [&](int i) { return !SHIFT || (col(i) >= 0 && col(i) + V <= a.D); };
+  auto store = [&](T* row, int i, const uint64_t (&f)[P]) {
+    if (whole(i)) store_pairs<T, V>(row + col(i), f);
+    else store_clipped<T, V>(row, col(i), a.D, f);
+  };
   const float inv_d = 1.f / (float)a.D;
+  // The weights stay in registers, but for blocks that leave a thread 64 of them.
+  constexpr bool KEEP = TPR < 1024;
   uint64_t wk[KEEP ? NV : 1][P], pk[KEEP ? NV : 1][P];
   if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + lane) * V;
+      const int c = col(i);
       if (c < a.D) {
-        if (!OUT && a.w) load_weight<T, V>(a, a.w, c, wk[i]);
-        if (a.w_post) load_weight<T, V>(a, a.w_post, c, pk[i]);
+        if (!OUT && a.w) load_weight<T, V, SHIFT>(a, a.w, c, wk[i]);
+        if (a.w_post) load_weight<T, V, SHIFT>(a, a.w_post, c, pk[i]);
       }
     }
   }
+  auto weight = [&](const uint64_t (&kept)[KEEP ? NV : 1][P], const void* p, int i, uint64_t (&f)[P]) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int q = 0; q < P; ++q) f[q] = kept[i][q];
+    } else {
+      load_weight<T, V, SHIFT>(a, p, col(i), f);
+    }
+  };
   const bool has_res = !OUT && a.res.p, has_y = !OUT && a.y;
-  // Rows are asked for ahead where two at least fit 40 KB a block: with the row in
-  // work alone too few bytes are in flight.
-  constexpr int ITEMS = (OUT ? 2 : 3) * NV, SLOT = ITEMS * G::THREADS * 16;
-  constexpr int DEPTH = SLOT > 20480 ? 1 : SLOT * 4 <= 40960 ? 4 : 40960 / SLOT;
-  constexpr bool AHEAD = V > 1 && DEPTH >= 2;
-  using Ahead = RowsAhead<T, (V > 1 ? V : 4), ITEMS, DEPTH, G::THREADS>;
-  __shared__ __align__(16) unsigned char ahead_rows[AHEAD ? Ahead::BYTES : 16];
-  Ahead ahead(ahead_rows);
-  const int64_t first = (int64_t)blockIdx.x * G::GROUPS + grp, step = (int64_t)gridDim.x * G::GROUPS;
-  Cursor<T, OUT ? 2 : 3> in(first, step, a.R1);  // the next row to ask for
+  extern __shared__ __align__(16) unsigned char norm_smem[];
+  Rows ahead(norm_smem);
+  Cursor<T, OUT ? 2 : 3> in(g.first, g.step, a.R1);  // the next row to ask for
   in.add(0, a.x);
   in.add(1, a.gate);
   if constexpr (!OUT) in.add(2, a.res);
@@ -52,12 +72,13 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       if (in.r < a.rows) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (i * TPR + lane) * V;
+          const int c = col(i);
+          const int bytes = SHIFT ? min(V, a.D - c) * (int)sizeof(T) : V * (int)sizeof(T);
           if (c < a.D) {
-            ahead.ask(slot, i, in.p[0] + c);
-            if (a.gate.p) ahead.ask(slot, NV + i, in.p[1] + c);
+            ahead.ask(slot, i, in.p[0] + c, bytes);
+            if (a.gate.p) ahead.ask(slot, NV + i, in.p[1] + c, bytes);
             if constexpr (!OUT)
-              if (has_res) ahead.ask(slot, 2 * NV + i, in.p[2] + c);
+              if (has_res) ahead.ask(slot, 2 * NV + i, in.p[2] + c, bytes);
           }
         }
       }
@@ -67,7 +88,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
         if (!given) return;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (i * TPR + lane) * V;
+          const int c = col(i);
           if (c < a.D) to[i] = vload<T, V>(in.p[k] + c);
         }
       };
@@ -83,23 +104,22 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
   }
   int slot = 0;
 #pragma unroll 1
-  for (int64_t r = first; r - grp < a.rows; r += step) {
+  for (int64_t r = g.first; r - g.grp < a.rows; r += g.step) {
     const bool live = r < a.rows;
     if constexpr (AHEAD) cp_async_wait<DEPTH - 1>();
     else ask(0);
-    // the row's vectors: from shared memory whenever they are used, or registers
-    auto vec = [&](int item, const Vec<T, V>& held) {
-      if constexpr (AHEAD) return ahead.get(slot, item);
-      else return held;
+    // vector i of a tensor: from shared memory whenever it is used, or registers
+    auto get = [&](int k, int i, const Vec<T, V>& held, uint64_t (&f)[P]) {
+      if constexpr (AHEAD) to_pairs<T, V>(ahead.get(slot, k * NV + i), f);
+      else to_pairs<T, V>(held, f);
+      if (SHIFT && !whole(i)) clip_pairs<V>(f, col(i), a.D);
     };
     auto put = [&](void* to, const uint64_t (&f)[NV][P]) {
       if (!to || !live) return;
       T* p = static_cast<T*>(to) + r * a.D;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) store_pairs<T, V>(p + c, f[i]);
-      }
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.D) store(p, i, f[i]);
     };
     auto mean_square = [&](const uint64_t (&f)[NV][P], float2* buf) {
       uint64_t s = 0;
@@ -107,35 +127,34 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int q = 0; q < P; ++q) s = fma2(f[i][q], f[i][q], s);
-      float ss = sum_of(s);
-      G::sum(ss, buf);
-      return fmaf(ss, inv_d, a.eps);
+      float ss[1] = {sum_of(s)};
+      g.sum(ss, buf);
+      return fmaf(ss[0], inv_d, a.eps);
     };
     uint64_t u[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (live && (i * TPR + lane) * V < a.D) to_pairs<T, V>(vec(i, raw.x[i]), u[i]);
+      if (live && col(i) < a.D) get(0, i, raw.x[i], u[i]);
       else zero_pairs<V>(u[i]);
     }
     if (a.w_post) {
       const uint64_t r1 = both(rsqrtf(mean_square(u, sm[0])));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) {
+        if (col(i) < a.D) {
           uint64_t w[P];
-          if constexpr (!KEEP) load_weight<T, V>(a, a.w_post, c, w);
+          weight(pk, a.w_post, i, w);
 #pragma unroll
-          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r1, KEEP ? pk[KEEP ? i : 0][q] : w[q]));
+          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r1, w[q]));
         }
       }
     }
     if (a.gate.p && live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((i * TPR + lane) * V < a.D) {
+        if (col(i) < a.D) {
           uint64_t z[P], sg, act;
-          to_pairs<T, V>(vec(NV + i, raw.z[i]), z);
+          get(1, i, raw.z[i], z);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             gate_of(z[q], sg, act, a.sigmoid);
@@ -147,9 +166,9 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       const uint64_t alpha = both(a.alpha);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((i * TPR + lane) * V < a.D) {
+        if (col(i) < a.D) {
           uint64_t r[P];
-          to_pairs<T, V>(vec(2 * NV + i, raw.r[OUT ? 0 : i]), r);
+          get(2, i, raw.r[OUT ? 0 : i], r);
 #pragma unroll
           for (int q = 0; q < P; ++q) u[i][q] = fma2(alpha, u[i][q], r[q]);
         }
@@ -159,18 +178,17 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
       const uint64_t r2 = both(rsqrtf(mean_square(u, sm[1])));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < a.D) {
+        if (col(i) < a.D) {
           uint64_t w[P];
-          if constexpr (!KEEP) load_weight<T, V>(a, a.w, c, w);
+          weight(wk, a.w, i, w);
 #pragma unroll
-          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r2, KEEP ? wk[KEEP ? i : 0][q] : w[q]));
+          for (int q = 0; q < P; ++q) u[i][q] = mul2(u[i][q], mul2(r2, w[q]));
         }
       }
       put(a.y, u);
     }
     // a row that runs only one of the two sums would meet its own buffer again
-    if (TPR > 32 && !(a.w_post && has_y)) __syncthreads();
+    if (!(a.w_post && has_y)) g.sync();
     if constexpr (AHEAD) {  // (what was read from the slot has been used)
       ask(slot);
       slot = slot == DEPTH - 1 ? 0 : slot + 1;
@@ -178,35 +196,46 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
   }
 }
 
+template <typename T, int V, int TPR, int NV, bool CLUSTER, bool OUT, bool SHIFT>
+cudaError_t launch_one(const NormArgs& a, const NormShape& s, int* parts, cudaStream_t st) {
+  static int held[MAX_CLUSTER + 1];
+  using F = FwdRows<T, V, TPR, NV, OUT, SHIFT>;
+  const size_t smem = F::AHEAD ? F::Rows::BYTES : 0;
+  return norm_launch(k_norm_fwd<T, V, TPR, NV, CLUSTER, OUT, SHIFT>, a, s, smem, 32, held, parts, st);
+}
+
 template <typename T, int VT>
-cudaError_t launch_t(const NormArgs& a, const NormShape& s, cudaStream_t st) {
-#define GDR_NORM_CASE(v, tpr, nv)                                                                              \
-  if (s.V == v && s.TPR == tpr && s.NV == nv) {                                                                \
-    constexpr int groups = RowGroup<tpr>::GROUPS, threads = norm_threads(tpr);                                 \
-    const int64_t work = (a.rows + groups - 1) / groups;                                                       \
-    static int occ = 0, occ_out = 0;                                                                           \
-    if (a.res.p || a.w) {                                                                                      \
-      const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv, false>, threads, 0, work, 32, &occ);              \
-      k_norm_fwd<T, v, tpr, nv, false><<<blocks, threads, 0, st>>>(a);                                         \
-    } else {                                                                                                   \
-      const int blocks = norm_grid(k_norm_fwd<T, v, tpr, nv, true>, threads, 0, work, 32, &occ_out);           \
-      k_norm_fwd<T, v, tpr, nv, true><<<blocks, threads, 0, st>>>(a);                                          \
-    }                                                                                                          \
-    return cudaGetLastError();                                                                                 \
+cudaError_t launch_t(const NormArgs& a, const NormShape& s, int* parts, cudaStream_t st) {
+  constexpr int N = 8 / VT;  // vectors of 8 elements
+  const bool out = !a.res.p && !a.w;  // the norm of a block's output alone
+#define GDR_NORM_CASE(v, tpr, nv, cl, sh)                                                 \
+  if (s.V == v && s.TPR == tpr && s.NV == nv && (s.cluster > 0) == cl && s.shift == sh)   \
+    return out ? launch_one<T, v, tpr, nv, cl, true, sh>(a, s, parts, st)                 \
+               : launch_one<T, v, tpr, nv, cl, false, sh>(a, s, parts, st);
+#define GDR_NORM_CASES(tpr, nv, cl)     \
+  GDR_NORM_CASE(VT, tpr, nv, cl, false) \
+  GDR_NORM_CASE(VT, tpr, nv, cl, true)
+  GDR_NORM_CASES(2, 1, false)
+  GDR_NORM_CASES(4, 1, false)
+  GDR_NORM_CASES(8, 1, false)
+  GDR_NORM_CASES(8, 2, false)
+  GDR_NORM_CASES(16, 2, false)
+  GDR_NORM_CASES(32, 2, false)
+  GDR_NORM_CASES(64, 2, false)
+  GDR_NORM_CASES(96, 2, false)
+  GDR_NORM_CASES(128, 2, false)
+  if constexpr (VT == 4) {  // (of 16 bits 128 threads with two vectors hold as much)
+    GDR_NORM_CASES(256, N, false)
   }
-  GDR_NORM_CASE(VT, 8, 1)
-  GDR_NORM_CASE(VT, 8, 2)
-  GDR_NORM_CASE(VT, 16, 2)
-  GDR_NORM_CASE(VT, 32, 2)
-  GDR_NORM_CASE(VT, 32, 4)
-  GDR_NORM_CASE(VT, 128, 2)
-  GDR_NORM_CASE(VT, 256, 2)
-  GDR_NORM_CASE(VT, 512, 2)
-  GDR_NORM_CASE(VT, 512, 4)
-  GDR_NORM_CASE(VT, 1024, 4)
-  GDR_NORM_CASE(1, 32, 8)
-  GDR_NORM_CASE(1, 256, 8)
-  GDR_NORM_CASE(1, 1024, 16)
+  GDR_NORM_CASES(384, N, false)
+  GDR_NORM_CASES(512, N, false)
+  GDR_NORM_CASES(640, N, false)
+  GDR_NORM_CASES(768, N, false)
+  GDR_NORM_CASES(1024, N, false)
+  GDR_NORM_CASES(128, 2, true)
+  GDR_NORM_CASE(1, 32, 8, false, false)
+  GDR_NORM_CASE(1, 128, 8, true, false)
+#undef GDR_NORM_CASES
 #undef GDR_NORM_CASE
   return cudaErrorInvalidConfiguration;
 }
@@ -214,10 +243,11 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, cudaStream_t st) {
+  int parts = 0;
   switch (dtype) {
-    case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, st);
-    case GDR_DTYPE_F16: return launch_t<__half, 8>(a, s, st);
-    default: return launch_t<float, 4>(a, s, st);
+    case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, &parts, st);
+    case GDR_DTYPE_F16: return launch_t<__half, 8>(a, s, &parts, st);
+    default: return launch_t<float, 4>(a, s, &parts, st);
   }
 }
 

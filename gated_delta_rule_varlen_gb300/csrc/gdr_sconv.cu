@@ -142,8 +142,26 @@ __global__ void __launch_bounds__(128, 5) k_sconv_fwd(ConvArgs a) {
       }
       cp_async_wait<0>();
     } else {
+      Vec<T, V> next[kDepth];
+      auto fetch = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i)
+          if (from + i < e) next[i] = vload<T, V>(x + (int64_t)(from + i) * a.ldx);
+      };
+      fetch(t);
 #pragma unroll 1
-      for (; t < e; ++t) token(vload<T, V>(x + (int64_t)t * a.ldx));
+      while (t < e) {
+        Vec<T, V> now[kDepth];
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) now[i] = next[i];
+        fetch(t + kDepth);
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i)
+          if (t < e) {
+            token(now[i]);
+            ++t;
+          }
+      }
     }
     if (t == de) {
       end_state(d);
@@ -302,6 +320,33 @@ __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
         }
       }
       cp_async_wait<0>();
+    }
+    if constexpr (V == 1) {
+      constexpr int U = 4;
+      Vec<T, V> nx[U], ng[U];
+      auto fetch = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (from + i < e) rows(from + i, nx[i], ng[i]);
+      };
+      fetch(t);
+      T* to = dx + (int64_t)(t - K) * f.C;
+#pragma unroll 1
+      while (t < e) {
+        Vec<T, V> rx[U], rg[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) rx[i] = nx[i], rg[i] = ng[i];
+        fetch(t + U);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (t < e) {
+            uint64_t done[P];
+            token(rx[i], rg[i], true, done);
+            store_pairs<T, V>(to, done);
+            to += f.C;
+            ++t;
+          }
+      }
     }
     // the rest, and the tokens after the tile that the tile's last rows feed
     const int tail = min(de, e + K);

@@ -421,6 +421,15 @@ NORM = [
     ((0, 4, 128), BF16, True, "silu", False, False, False, False, 1.0),
     ((5000, 320), BF16, False, None, True, True, False, False, 1.0),
 ]
+# rows of every width class: lanes of a warp, one to four warps, clusters of two to nine blocks (sixteen of FP32);
+# lengths that are no whole number of 16-byte pieces, packed one after another or strided
+NORM += [((rows, D), dt, True, "silu" if D % 3 else None, True, True, False, False, 0.5) for rows, D, dt in (
+    (67, 3, BF16), (130, 17, F16), (41, 31, BF16), (35, 61, F32), (29, 127, BF16), (300, 249, BF16), (23, 511, F16),
+    (19, 520, BF16), (17, 1021, BF16), (700, 1032, BF16), (9, 1536, F32), (11, 2047, BF16), (21, 2056, BF16),
+    (10, 2050, F32), (13, 4097, BF16), (33, 5120, BF16), (3, 6144, F32), (5, 7168, F16), (9, 12289, BF16),
+    (2, 16381, F32), (4, 10246, F32))]
+NORM += [((43, 3, 77), BF16, True, "sigmoid", False, False, True, False, 1.0), ((1000, 5), F32, False, None, True, True, False, False, 1.0),
+         ((7, 3001), BF16, True, "silu", True, True, False, True, 0.5), ((5, 9001), F32, True, None, True, True, True, True, 0.5)]
 
 
 @pytest.mark.parametrize("shape,dtype,post,act,residual,pre,wf32,odd,alpha", NORM)
@@ -461,6 +470,24 @@ def test_norm_forward_and_gradients(gdr, shape, dtype, post, act, residual, pre,
     again = gdr.norm_bwd(x, **args, dh=dh, dy=dy)
     for k in rg:
         assert torch.equal(got[k], again[k]), k
+
+
+@pytest.mark.parametrize("D", [7, 129, 1021, 4099])
+def test_norm_rows_keep_to_themselves(gdr, D):
+    # rows whose pieces of 16 bytes reach into the rows beside them: a row of NaN and one of infinities stay alone
+    g = gen(D)
+    x, r, dy = (randn(g, 24, D, dtype=BF16) for _ in range(3))
+    w = (1 + 0.2 * randn(g, D)).to(BF16)
+    bad = x.clone()
+    bad[5], bad[18] = float("nan"), float("inf")
+    keep = [i for i in range(24) if i not in (5, 18)]
+    h, y = gdr.norm_fwd(x, weight=w, post_weight=w, residual=r)
+    h2, y2 = gdr.norm_fwd(bad, weight=w, post_weight=w, residual=r)
+    assert torch.equal(h[keep], h2[keep]) and torch.equal(y[keep], y2[keep])
+    a = gdr.norm_bwd(x, weight=w, post_weight=w, residual=r, dh=dy, dy=dy)
+    b = gdr.norm_bwd(bad, weight=w, post_weight=w, residual=r, dh=dy, dy=dy)
+    assert torch.equal(a["dx"][keep], b["dx"][keep]) and torch.equal(a["dresidual"][keep], b["dresidual"][keep])
+    assert torch.isnan(b["dx"][5]).all()
 
 
 def test_norm_gradients_by_differences(gdr):
