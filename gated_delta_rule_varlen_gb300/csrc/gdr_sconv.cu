@@ -531,6 +531,8 @@ gdr_status sconv_fwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   if ((rc = plan_host(T, N, cu_seqlens_host, &nc)) != GDR_OK) return rc;
   if (N == 0 || (T == 0 && !st)) return GDR_OK;
   if (!cu_seqlens || !weight || (T > 0 && !out)) return GDR_INVALID_ARG;
+  // other tiles read rows of x and s0 after a tile has written its own
+  if ((T > 0 && out == x) || (st && st == s0)) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
   ConvArgs a{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, cu_seqlens, N, (int)T, C, silu, s0, out, st, 0, 0};
   const int V = 16 / (int)elem(dtype);
@@ -563,6 +565,7 @@ gdr_status sconv_bwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   sconv_workspace_bytes(T, C, W, &need);
   if (((uintptr_t)scratch & 255) != 0) return GDR_INVALID_ARG;
   if (scratch_bytes < need) return GDR_WORKSPACE_TOO_SMALL;
+  if ((T > 0 && (dx == x || dx == dout)) || (ds0 && (ds0 == dst || ds0 == s0))) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
   ConvBwdArgs a{};
   a.f = ConvArgs{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, cu_seqlens, N, (int)T, C, silu, s0, nullptr, nullptr,

@@ -365,7 +365,8 @@ typedef int gdr_dtype;
  * rows ldx apart; weight [C][W]; bias [C] or null; s0, st [N][W-1][C];
  * out [T][C].  st, when non-null, gets the last W - 1 rows of xx of every
  * document (an empty document's start state).  out must not overlap x, nor st
- * s0.  Any C; where C or a row's place is no multiple of 16 bytes (8 in the
+ * s0; nor, in sconv_bwd, dx x or dout, nor ds0 s0 or dst (GDR_INVALID_ARG where
+ * they are the same).  Any C; where C or a row's place is no multiple of 16 bytes (8 in the
  * backward) a thread takes one channel, at a third to half of the rate. */
 gdr_status sconv_fwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
                      gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
@@ -407,6 +408,7 @@ gdr_status sconv_step(gdr_dtype dtype, const void* x, int64_t ldx, const void* w
  * tensor cores, long documents in several segments side by side; otherwise
  * token by token.  A value that is not finite reaches every later token of its
  * document and head, and in chunks the outputs of the chunk it is in.
+ * ht may be h0 (the states go on in place).
  * scratch: ssm_workspace_bytes bytes on a 256-byte boundary (0 for shapes that
  * never run in chunks). */
 #define GDR_SSM_MAX_P 256
@@ -450,7 +452,7 @@ gdr_status gdn_step(const gdr_bf16* q, const gdr_bf16* k, const gdr_bf16* v, con
  * At least one of residual, post_weight, weight is given.  Rows on 16-byte
  * boundaries, and dense tensors of any D that start on one, are read in 16-byte
  * pieces; strided rows of other places one element a time, at a quarter of the
- * rate. */
+ * rate.  h or y may be residual or x itself (the same rows). */
 #define GDR_ACT_SILU 0
 #define GDR_ACT_SIGMOID 1
 #define GDR_NORM_MAX_D 16384

@@ -53,6 +53,19 @@ def test_sconv_refusals(gdr):
     assert step(B=0) == gdr.GDR_OK
 
 
+def test_sconv_refuses_outputs_in_place(gdr):
+    lib, bad, c = gdr.load(), gdr.GDR_INVALID_ARG, (ctypes.c_int32 * 2)(0, 9)
+
+    def fwd(x=P(), out=P() + 4096, s0=None, st=None):
+        return lib.sconv_fwd(0, x, 64, P(), None, 0, P(), c, 1, 9, 64, 4, 1, s0, out, st, None)
+    assert fwd(out=P()) == bad and fwd(s0=P(), st=P()) == bad
+
+    def bwd(x=P(), dout=P() + 4096, dx=P() + 8192, s0=None, dst=None, ds0=None):
+        return lib.sconv_bwd(0, x, 64, P(), None, 0, P(), c, 1, 9, 64, 4, 1, s0, dout, 64, dst, dx, P(), None, ds0, P(),
+                             1 << 40, None)
+    assert bwd(dx=P()) == bad and bwd(dx=P() + 4096) == bad and bwd(dst=P(), ds0=P()) == bad and bwd(s0=P(), ds0=P()) == bad
+
+
 def test_ssm_refusals(gdr):
     lib, (k, c) = gdr.load(), cu(0, 5, 11)
     bad = gdr.GDR_INVALID_ARG

@@ -287,6 +287,28 @@ def test_ssm_prompt_short(gdr, lengths, H, P, G, N, odd):
     check(ht, rh, "ht")
 
 
+@pytest.mark.parametrize("lengths", [[3000], [200, 0, 129, 40], [20, 3, 0]])
+def test_ssm_prompt_states_in_place(gdr, lengths):
+    g, P, N, H, n = gen(12), 64, 128, 2, len(lengths)
+    x, dt, A, B, C, D, bias = scan_inputs(g, sum(lengths), H, P, 1, N, F32)
+    h0, cu = randn(g, n, H, N, P), pack(lengths)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *cu, D=D, dt_bias=bias, h0=h0)
+    pool = h0.clone()
+    out2, ht2 = gdr.ssm_fwd(x, dt, A, B, C, *cu, D=D, dt_bias=bias, h0=pool, ht=pool)
+    assert ht2 is pool and torch.equal(out, out2) and torch.equal(ht, pool)
+
+
+@pytest.mark.parametrize("D", [128, 1021, 2048, 5120, 9000])
+def test_norm_in_place(gdr, D):
+    g = gen(D)
+    x, r = randn(g, 50, D, dtype=BF16), randn(g, 50, D, dtype=BF16)
+    w = (1 + 0.2 * randn(g, D)).to(BF16)
+    h, y = gdr.norm_fwd(x, weight=w, post_weight=w, residual=r)
+    x2, r2 = x.clone(), r.clone()
+    gdr.norm_fwd(x2, weight=w, post_weight=w, residual=r2, h=r2, y=x2)
+    assert torch.equal(h, r2) and torch.equal(y, x2)
+
+
 def test_ssm_prompt_carries_nan(gdr):
     # a NaN reaches every later token of its own document and head, across segments, and no other
     g, P, N, H, lengths = gen(8), 64, 128, 2, [200, 3000]
