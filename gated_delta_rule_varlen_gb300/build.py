@@ -1,7 +1,10 @@
-"""Builds libgdr.so (the CUDA library behind include/gdr.h) in-tree for sm_103a.
+"""Builds libgdr.so (the CUDA library behind include/gdr.h) in-tree for sm_103a,
+and the operators' Python binding beside it.
 
-Each translation unit is compiled in parallel with nvcc, then linked as one
-shared library at gated_delta_rule_varlen_gb300/lib/libgdr.so.
+Each translation unit is compiled in parallel with nvcc (the binding with the
+host compiler), then linked as one shared library at
+gated_delta_rule_varlen_gb300/lib/libgdr.so; the binding, which depends on the
+PyTorch it was compiled against, carries that version in its name.
 """
 from __future__ import annotations
 
@@ -9,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -25,6 +29,24 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def binding_path() -> str:
+    import torch
+    return os.path.join(LIBDIR, f"_gdr_ops-{torch.__version__}.so")
+
+
+def _cxx(source: str, target: str):
+    """The compile and the link command of the binding."""
+    import torch
+    cxx = os.environ.get("CXX") or "g++"
+    home, cuda = os.path.dirname(torch.__file__), os.path.dirname(os.path.dirname(nvcc()))
+    obj = target[:-3] + ".o"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                f"-I{home}/include", f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}/include", "-c", source, "-o", obj]
+    link = [cxx, "-shared", obj, "-o", target + f".tmp{os.getpid()}", f"-L{home}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", f"-L{LIBDIR}", "-lgdr", "-Wl,-rpath,$ORIGIN"]
+    return obj, compile_, link
 
 
 def _stale(target: str, deps) -> bool:
@@ -48,20 +70,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding, source = binding_path(), os.path.join(CSRC, "gdr_binding.cpp")
+    bobj, compile_, link = _cxx(source, binding)
+    compiled = list(procs)
+    if force or _stale(bobj, [source, headers[-1]]):
+        compiled.append(("gdr_binding.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     errors = []
-    for src, p in procs:
+    for src, p in compiled:
         out, _ = p.communicate()
         if p.returncode != 0:
             errors.append(f"{src}:\n{out.decode(errors='replace')}")
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
     if force or procs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if force or _stale(binding, [bobj]):
+        subprocess.run(link, check=True)
+        os.replace(binding + f".tmp{os.getpid()}", binding)
     return LIB
 
 
