@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_bwd_min_blocks(TPR, V 
   constexpr bool AHEAD = F::AHEAD;
   constexpr int P = pairs_of<V>, DEPTH = F::DEPTH;
   __shared__ float2 sm[3][RowGroup<TPR, CLUSTER>::SUMS];
+  next_may_start();  // (the sum of the partial rows)
   const RowGroup<TPR, CLUSTER> g;
   // a shifted row's vectors start m elements before it, on 16 bytes
   const int m = SHIFT ? (int)(g.first % V) * (a.D % V) % V : 0;
@@ -342,6 +343,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_bwd_min_blocks(TPR, V 
 __global__ void __launch_bounds__(1024) k_norm_wgrad(const float* __restrict__ part, int blocks, int D, float* dw,
                                                      float* dwp) {
   float* to = blockIdx.y == 0 ? dw : dwp;
+  previous_ended();
   if (!to) return;
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
@@ -571,8 +573,8 @@ gdr_status norm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   }
   if (dweight || dpost_weight) {
     ProfScope ps("norm_wgrad", stream);
-    k_norm_wgrad<<<dim3((D + 31) / 32, 2), 1024, 0, stream>>>(a.part, parts, D, dweight, dpost_weight);
-    if (cudaGetLastError() != cudaSuccess) return GDR_CUDA_ERROR;
+    if (launch_early(k_norm_wgrad, dim3((D + 31) / 32, 2), 1024, 0, stream, a.part, parts, D, dweight, dpost_weight) != cudaSuccess)
+      return GDR_CUDA_ERROR;
   }
   return GDR_OK;
 }

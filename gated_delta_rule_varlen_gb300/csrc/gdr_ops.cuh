@@ -100,6 +100,27 @@ __device__ __forceinline__ float sum_of(uint64_t v) {
   return a + b;
 }
 
+// A launch whose blocks may start before the stream's previous kernel has ended, once
+// all of that kernel's blocks have called next_may_start(): what it does before
+// previous_ended() overlaps.  previous_ended() returns when the previous kernel has
+// ended and its writes are visible.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void previous_ended() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
 // A ring of DEP vectors of V elements a thread in shared memory, filled by
 // asynchronous copies: rows of a walk asked for DEP steps ahead without holding
 // registers.  Each thread reads its own copies only, so that its own waits order

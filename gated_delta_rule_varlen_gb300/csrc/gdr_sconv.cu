@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
       while (d < f.N && f.cu[d + 1] == de) empty_doc(d++);
     }
   }
+  next_may_start();  // (the sum of the partial rows)
   float* part = a.part + (int64_t)tile_id * (W + 1) * f.C + c;
 #pragma unroll
   for (int j = 0; j <= W; ++j) {
@@ -401,6 +402,7 @@ __global__ void __launch_bounds__(512) k_sconv_wgrad(const float* __restrict__ p
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
   float sum = 0.f;
+  previous_ended();
   if (c < C) {
 #pragma unroll 8
     for (int i = row; i < tiles; i += 16) sum += part[((int64_t)i * (W + 1) + j) * C + c];
@@ -593,8 +595,8 @@ gdr_status sconv_bwd(int dtype, const void* x, int64_t ldx, const void* weight, 
     if (e != cudaSuccess) return GDR_CUDA_ERROR;
   }
   ProfScope ps("sconv_wgrad", stream);
-  k_sconv_wgrad<<<dim3((C + 31) / 32, W + 1), 512, 0, stream>>>(a.part, (int)tiles, C, W, dweight, dbias);
-  return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  return launch_early(k_sconv_wgrad, dim3((C + 31) / 32, W + 1), 512, 0, stream, a.part, (int)tiles, C, W, dweight, dbias) ==
+                 cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
 }
 
 gdr_status sconv_step(int dtype, const void* x, int64_t ldx, const void* weight, const void* bias, int wdtype,

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) k_ssm_gates(const int* __rest
   __shared__ float sdt[Q][33];
   __shared__ Seg sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  next_may_start();
   if (warp == 0) {
     const Seg sg = find_segment(cu, a.N, 1, blockIdx.x);
     if (lane == 0) sh = sg;
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         if (c >= 2 && !wait_or_abort(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
         tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)(BLK + sizeof(s.gates[0])));
         tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.x_full[b]);
+        if (c == 0) previous_ended();  // the gates come from the kernel before
         tc::bulk_load(s.gates[b], gates_of(ta, sg.chunk0 + c, h).p, sizeof(s.gates[0]), &s.x_full[b]);
         x = c + 1;
       }
@@ -625,6 +627,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     const int pc = p0 + 32 * half;
     uint64_t S[16];
     const float* start = nullptr;
+    previous_ended();  // a segment's start state, too
     if (sg.idx > 0) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
     else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
@@ -812,6 +815,8 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
   }
   __syncthreads();
   const Seg sg = uniform(s.seg);
+  next_may_start();
+  previous_ended();
   if (sg.idx == sg.nseg - 1) return;  // no segment starts from this one's end
   if (warp == 1) {
     tc::tmem_alloc(&s.tmem, 512);
@@ -999,6 +1004,8 @@ __global__ void __launch_bounds__(256) k_ssm_merge(const __grid_constant__ TcArg
   before = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) before += sums[i];
+  next_may_start();
+  previous_ended();
   const int ch = (a.cu[d + 1] - a.cu[d] + Q - 1) / Q, nseg = ch == 0 ? 1 : (ch + ta.lseg - 1) / ta.lseg;
   if (nseg == 1 || e0 >= elems) return;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1153,18 +1160,15 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
     cudaFuncSetAttribute(k_ssm_sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_sum);
     {
       ProfScope ps("ssm_sum", st, (double)a.T * a.H);
-      k_ssm_sum<<<grid >> t.pairs, SUM_THREADS, sm_sum, st>>>(t);
+      if (cudaError_t e = launch_early(k_ssm_sum, dim3(grid >> t.pairs), SUM_THREADS, sm_sum, st, t)) return e;
     }
-    if (cudaError_t e = cudaGetLastError()) return e;
     ProfScope ps("ssm_merge", st);
     const unsigned mb = (unsigned)(((int64_t)a.NS * a.P + 1023) / 1024) * a.H * a.N;
-    k_ssm_merge<<<mb, 256, 0, st>>>(t);
-    if (cudaError_t e = cudaGetLastError()) return e;
+    if (cudaError_t e = launch_early(k_ssm_merge, dim3(mb), 256, 0, st, t)) return e;
   }
   cudaFuncSetAttribute(k_ssm_walk, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_walk);
   ProfScope ps("ssm_walk", st, (double)a.T * a.H);
-  k_ssm_walk<<<grid, WALK_THREADS, sm_walk, st>>>(t);
-  return cudaGetLastError();
+  return launch_early(k_ssm_walk, dim3(grid), WALK_THREADS, sm_walk, st, t);
 }
 
 }  // namespace gdr
