@@ -429,7 +429,7 @@ struct ConvStepArgs {
 };
 
 // One token of each sequence: the state's rows move up by one and x becomes
-// its last.  Bound by the launch: 12 us a call through Python, 6 of them on the GPU, one sequence or a few.
+// its last.  Bound by the launch: 4 us a call of one sequence or a few.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) k_sconv_step(ConvStepArgs a) {
   constexpr int K = W - 1;
