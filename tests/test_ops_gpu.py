@@ -635,3 +635,31 @@ def test_refusals(gdr):
             f()
             pytest.fail(f"call {i} was not refused")
     torch.cuda.synchronize()
+
+
+def test_binding_holds_nothing(gdr):
+    # references and device memory after calls, refused calls included, are what they were before
+    import sys
+    g = gen(14)
+    x, w, r = randn(g, 40, 64, dtype=BF16), randn(g, 64, 4, dtype=BF16), randn(g, 64, dtype=BF16)
+    cu, cuh = pack([30, 10])
+    bufs = {"dx": torch.empty_like(x)}
+
+    def calls():
+        out, st = gdr.sconv_fwd(x, w, None, cu, cuh, s0=None)
+        grads = gdr.sconv_bwd(x, w, None, cu, cuh, out, grads=bufs)
+        assert grads["dx"] is bufs["dx"] and grads["dbias"] is None and list(bufs) == ["dx"]
+        h, y = gdr.norm_fwd(x, weight=r, residual=out)
+        gdr.norm_bwd(x, weight=r, residual=out, dh=h, dy=y)
+        for bad in (lambda: gdr.sconv_fwd(x, w, None, cu, [0, 30, 41]), lambda: gdr.sconv_fwd(x, w, r[1:], cu, cuh),
+                    lambda: gdr.sconv_bwd(x, w, None, cu, cuh, out, grads={"dx": r}), lambda: gdr.norm_fwd(x, weight="r"),
+                    lambda: gdr.sconv_fwd(x, w, None, cu, cuh, out=x)):
+            with pytest.raises(ValueError):
+                bad()
+        gdr.sconv_fwd(x, w, None, cu, [0, 30, 40])  # any sequence of whole numbers
+    calls()
+    held = (x, w, r, cu, bufs["dx"])
+    before = [sys.getrefcount(t) for t in held], torch.cuda.memory_allocated()
+    for _ in range(50):
+        calls()
+    assert ([sys.getrefcount(t) for t in held], torch.cuda.memory_allocated()) == before
