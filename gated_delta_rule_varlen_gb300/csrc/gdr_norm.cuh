@@ -72,12 +72,17 @@ cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t 
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = s.cluster > 0 ? 1 : 0;
+  // (a device's own setting, so not kept from call to call)
+  if (smem > 40 << 10) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  }
+  if (s.cluster > 8) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+  }
   int& most = held[s.cluster];
   if (most == 0) {
     int n = 0;
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
     if (s.cluster > 0) {
-      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
       cfg.gridDim = dim3(152 / size * size);
       if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) return e;
       n = std::min(n, 152 * limit / size);
