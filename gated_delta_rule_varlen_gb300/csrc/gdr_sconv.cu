@@ -53,22 +53,27 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const T* x, const
   }
 }
 
-// Rows of the walks asked for ahead (8 or 16 bytes each a thread).
+// Rows of the walks asked for ahead: in shared memory (4 to 16 bytes each a thread),
+// or, single elements of 16 bits, which cannot be copied there, in registers.  (Of
+// single FP32 elements the forward keeps its rows in registers, too: 65536 x 4095
+// takes 391 us against 465; the backward, with two rings, 785 against 918.)
 constexpr int kDepth = 8;
+template <typename T, int V>
+constexpr bool kRing = V * sizeof(T) >= 4;
 
 // One thread owns V adjacent channels and walks the tokens of one tile with
 // the last W - 1 inputs in registers, so each input is read once (and W - 1
 // rows again at a tile's start).  Arithmetic in pairs of channels: the kernel is
 // bound by HBM (2 accesses an element) only while its instructions fit beside.
 // Measured (BF16, 4 taps, silu): 32768 tokens x 10240 channels 214 us = 92% of the copy
-// rate (one row at a time, without rows ahead, 261); channels in odd places, one a thread, 65536 x 8191
-// 791 us (two bytes cannot be copied ahead to shared memory; without rows ahead in
-// registers 1463), where 65536 x 8192 in pieces of 16 bytes takes 332.
+// rate (one row at a time, without rows ahead, 261); 65536 tokens in pieces of 16 bytes
+// (8192 channels) 331 us, in pairs of channels (8190) 489, one by one (8191) 792
+// (without rows ahead 1463).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128, 5) k_sconv_fwd(ConvArgs a) {
   constexpr int K = W - 1, P = pairs_of<V>;
   __shared__ Vec<T, V> rows_ahead[V > 1 ? kDepth * 128 : 1];
-  RowRing<T, (V > 1 ? V : 4), kDepth, 128> ring(rows_ahead);
+  RowRing<T, ((V > 1) ? V : 4), kDepth, 128> ring(rows_ahead);
   const int c = ((int)(blockIdx.x % a.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / a.cblocks;
   if (c >= a.C) return;
   const T* x = static_cast<const T*>(a.x) + c;
@@ -194,12 +199,12 @@ struct ConvBwdArgs {
 // partial row per tile.  The tile's last rows need dz of the W - 1 tokens after
 // it, which are recomputed.  Bound by HBM (x and dout read, dx written) and by
 // issue (66%): 32768 x 10240 in 396 us = 75% of the copy rate, 471 without rows ahead; 65536
-// tokens x 8192 channels 619 us, x 8191 1787 us.
+// tokens x 8192 channels 619 us, 8190 763, 8191 1790.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
   constexpr int K = W - 1, P = pairs_of<V>;
-  __shared__ Vec<T, V> rows_ahead[2][V > 1 ? kDepth * 128 : 1];
-  RowRing<T, (V > 1 ? V : 4), kDepth, 128> rx_ring(rows_ahead[0]), rg_ring(rows_ahead[1]);
+  __shared__ Vec<T, V> rows_ahead[2][kRing<T, V> ? kDepth * 128 : 1];
+  RowRing<T, (kRing<T, V> ? V : 4), kDepth, 128> rx_ring(rows_ahead[0]), rg_ring(rows_ahead[1]);
   const ConvArgs& f = a.f;
   const int c = ((int)(blockIdx.x % f.cblocks) * 128 + threadIdx.x) * V, tile_id = blockIdx.x / f.cblocks;
   if (c >= f.C) return;
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
       token(rx, rg, true, done);
       emit(t - K, done);
     }
-    if constexpr (V > 1) {
+    if constexpr (kRing<T, V>) {
       const T *ax = x + (int64_t)t * f.ldx, *ag = dout + (int64_t)t * a.ldo;
       int tp = t;
       auto ask = [&](int i) {
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
       }
       cp_async_wait<0>();
     }
-    if constexpr (V == 1) {
+    if constexpr (!kRing<T, V>) {
       constexpr int U = 4;
       Vec<T, V> nx[U], ng[U];
       auto fetch = [&](int from) {
@@ -482,7 +487,6 @@ int tile_tokens(int64_t T, int64_t cblocks, int wave, int most) {
 int bwd_tile_tokens(int64_t T, int64_t C) { return tile_tokens(T, ((C + 3) / 4 + 127) / 128, 152 * 5, 256); }
 
 size_t elem(int dtype) { return dtype == GDR_DTYPE_F32 ? 4 : 2; }
-bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Runs f(type tag, vector width, taps) for the run-time type, alignment and W.
 template <typename T, int V, typename F>
@@ -492,13 +496,25 @@ cudaError_t with_taps(int W, F f) {
   return f(T(), std::integral_constant<int, V>(), std::integral_constant<int, 4>());
 }
 template <int BYTES, typename F>
-cudaError_t dispatch(int dtype, bool vec, int W, F f) {
+cudaError_t dispatch(int dtype, int V, int W, F f) {
+  auto half = [&](auto t) {
+    using T = decltype(t);
+    return V > 2 ? with_taps<T, BYTES / 2>(W, f) : V == 2 ? with_taps<T, 2>(W, f) : with_taps<T, 1>(W, f);
+  };
   switch (dtype) {
-    case GDR_DTYPE_BF16:
-      return vec ? with_taps<__nv_bfloat16, BYTES / 2>(W, f) : with_taps<__nv_bfloat16, 1>(W, f);
-    case GDR_DTYPE_F16: return vec ? with_taps<__half, BYTES / 2>(W, f) : with_taps<__half, 1>(W, f);
-    default: return vec ? with_taps<float, BYTES / 4>(W, f) : with_taps<float, 1>(W, f);
+    case GDR_DTYPE_BF16: return half(__nv_bfloat16());
+    case GDR_DTYPE_F16: return half(__half());
+    default: return V > 1 ? with_taps<float, BYTES / 4>(W, f) : with_taps<float, 1>(W, f);
   }
+}
+// Channels a thread: BYTES of them where the channels, the rows' strides (or'ed into
+// `strides`) and the addresses (`all`) allow it, else, of 16 bits, pairs, else one.
+template <int BYTES>
+int width(int dtype, int64_t C, int64_t strides, uintptr_t all) {
+  const int e = (int)elem(dtype);
+  for (int V = BYTES / e; V > 1; V = e == 2 && V > 2 ? 2 : 1)
+    if (((C | strides) & (V - 1)) == 0 && (all & (uintptr_t)(V * e - 1)) == 0) return V;
+  return 1;
 }
 
 gdr_status conv_check(int dtype, int wdtype, int64_t T, int64_t ldx, int32_t C, int32_t W, const void* x,
@@ -537,15 +553,13 @@ gdr_status sconv_fwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   if ((T > 0 && out == x) || (st && st == s0)) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
   ConvArgs a{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, cu_seqlens, N, (int)T, C, silu, s0, out, st, 0, 0};
-  const int V = 16 / (int)elem(dtype);
-  const bool vec = C % V == 0 && ldx % V == 0 && on16(x) && on16(out) && on16(s0) && on16(st);
-  const int nv = vec ? C / V : C;
+  const int V = width<16>(dtype, C, ldx, (uintptr_t)x | (uintptr_t)out | (uintptr_t)s0 | (uintptr_t)st), nv = C / V;
   a.cblocks = (nv + 127) / 128;
   a.tile = tile_tokens(T, a.cblocks, 152 * 5, 128);
   const int64_t grid = (T > 0 ? (T + a.tile - 1) / a.tile : 1) * a.cblocks;
   if (grid > INT32_MAX) return GDR_INVALID_ARG;
   ProfScope ps("sconv_fwd", stream, (double)T * C);
-  const cudaError_t e = dispatch<16>(dtype, vec, W, [&](auto t, auto v, auto w) {
+  const cudaError_t e = dispatch<16>(dtype, V, W, [&](auto t, auto v, auto w) {
     k_sconv_fwd<decltype(t), decltype(v)::value, decltype(w)::value><<<(unsigned)grid, 128, 0, stream>>>(a);
     return cudaGetLastError();
   });
@@ -578,17 +592,16 @@ gdr_status sconv_bwd(int dtype, const void* x, int64_t ldx, const void* weight, 
   a.dx = dx;
   a.ds0 = ds0;
   a.part = static_cast<float*>(scratch);
-  const int V = dtype == GDR_DTYPE_F32 ? 2 : 4;  // 8 bytes a thread: the sums kept in registers are W of them a channel
   const uintptr_t all = (uintptr_t)x | (uintptr_t)s0 | (uintptr_t)dout | (uintptr_t)dst | (uintptr_t)dx | (uintptr_t)ds0;
-  const bool vec = C % V == 0 && ldx % V == 0 && lddout % V == 0 && (all & 7) == 0;
-  const int nv = vec ? C / V : C;
+  // 8 bytes a thread at most: the sums kept in registers are W of them a channel
+  const int V = width<8>(dtype, C, ldx | lddout, all), nv = C / V;
   a.f.tile = bwd_tile_tokens(T, C);
   a.f.cblocks = (nv + 127) / 128;
   const int64_t tiles = T > 0 ? (T + a.f.tile - 1) / a.f.tile : 1, grid = tiles * a.f.cblocks;
   if (grid > INT32_MAX) return GDR_INVALID_ARG;
   {
     ProfScope ps("sconv_bwd", stream, (double)T * C);
-    const cudaError_t e = dispatch<8>(dtype, vec, W, [&](auto t, auto v, auto w) {
+    const cudaError_t e = dispatch<8>(dtype, V, W, [&](auto t, auto v, auto w) {
       k_sconv_bwd<decltype(t), decltype(v)::value, decltype(w)::value><<<(unsigned)grid, 128, 0, stream>>>(a);
       return cudaGetLastError();
     });
@@ -609,12 +622,9 @@ gdr_status sconv_step(int dtype, const void* x, int64_t ldx, const void* weight,
   if (!out || (S > 0 && !state)) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
   ConvStepArgs a{x, weight, bias, wdtype == GDR_DTYPE_F32, ldx, state, slots, B, S, C, silu, out};
-  const int V = dtype == GDR_DTYPE_F32 ? 2 : 4;
-  const uintptr_t all = (uintptr_t)x | (uintptr_t)state | (uintptr_t)out;
-  const bool vec = C % V == 0 && ldx % V == 0 && (all & 7) == 0;
-  const int nv = vec ? C / V : C;
+  const int V = width<8>(dtype, C, ldx, (uintptr_t)x | (uintptr_t)state | (uintptr_t)out), nv = C / V;
   ProfScope ps("sconv_step", stream, (double)B * C);
-  const cudaError_t e = dispatch<8>(dtype, vec, W, [&](auto t, auto v, auto w) {
+  const cudaError_t e = dispatch<8>(dtype, V, W, [&](auto t, auto v, auto w) {
     k_sconv_step<decltype(t), decltype(v)::value, decltype(w)::value>
         <<<dim3((nv + 127) / 128, B < 65535 ? B : 65535), 128, 0, stream>>>(a);
     return cudaGetLastError();

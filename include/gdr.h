@@ -367,7 +367,8 @@ typedef int gdr_dtype;
  * document (an empty document's start state).  out must not overlap x, nor st
  * s0; nor, in sconv_bwd, dx x or dout, nor ds0 s0 or dst (GDR_INVALID_ARG where
  * they are the same).  Any C; where C or a row's place is no multiple of 16 bytes (8 in the
- * backward) a thread takes one channel, at a third to half of the rate. */
+ * backward) a thread takes two channels or one, at two thirds to a quarter of
+ * the rate. */
 gdr_status sconv_fwd(gdr_dtype dtype, const void* x, int64_t ldx, const void* weight, const void* bias,
                      gdr_dtype wdtype, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, int32_t N, int64_t T,
                      int32_t C, int32_t W, int silu, const void* s0, void* out, void* st, cudaStream_t stream);

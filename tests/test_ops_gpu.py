@@ -73,6 +73,11 @@ CONV = [
 ]
 
 
+# channels in pairs: counts and strides of no whole 8 or 16 bytes
+CONV += [([1, 33, 0, 7, 300], 1022, 4, BF16, True, True, True, 0, False, False), ([70, 5], 6, 3, F16, False, True, True, 2, False, True),
+         ([9, 140], 64, 2, BF16, True, False, True, 2, False, False), ([128, 64], 258, 4, F16, True, True, False, 0, False, False)]
+
+
 @pytest.mark.parametrize("lengths,C,W,dtype,bias,silu,states,pad,odd,wf32", CONV)
 def test_sconv_forward_and_gradients(gdr, lengths, C, W, dtype, bias, silu, states, pad, odd, wf32):
     g, T, n, K = gen(C + W), sum(lengths), len(lengths), W - 1
