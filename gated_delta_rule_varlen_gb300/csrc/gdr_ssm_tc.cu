@@ -11,11 +11,11 @@
 // x, B and C are BF16 and enter exactly.  w x enters U as the sum of three BF16
 // numbers (24 bits), so that the state, kept in FP32 registers from chunk to
 // chunk, is that of FP32 arithmetic.  M and S0, which only outputs depend on, enter
-// as BF16 like x, B and C themselves: each term of an output's sums is rounded
-// once, to the precision the output is rounded to, and the sums are FP32.  (As
-// pairs they took 1.4 times the chunk's MMA time and half as many instructions
-// again, for outputs 1.66e-3 instead of 1.7e-3 off, of which their own rounding is
-// 1.66e-3.)
+// as pairs of BF16 numbers: a term of an output's sums is off by at most 2^-17 of
+// itself, so that the output's own rounding (2^-9) is what is left of it unless
+// the terms cancel to some 2^-8 of their size.  (One BF16 number each is not
+// enough: the error is 2^-9 of |C| |S|, not of the output, 4e-2 of it where the state's
+// rows share a large part that C is orthogonal to.)
 //
 // exp(G_i - G_j) is formed from the difference, at most 1 on and below the
 // diagonal; what is above is dropped by selection.
@@ -161,6 +161,13 @@ __device__ __forceinline__ uint32_t round2(uint64_t v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// What rounding them leaves of a pair of FP32 numbers, rounded to BF16: the two
+// together hold 17 bits of each (the rest's sign is one).
+__device__ __forceinline__ uint32_t rest2(uint64_t v) { return round2(fma2(widen2(round2(v)), pack2(-1.f, -1.f), v)); }
+__device__ __forceinline__ void split2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  hi = round2(v);
+  lo = round2(fma2(widen2(hi), pack2(-1.f, -1.f), v));
+}
 // A pair of FP32 numbers as three BF16 pairs, each the rest of the ones before it
 // rounded: all 24 bits.
 __device__ __forceinline__ void split3(uint64_t v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
@@ -255,13 +262,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 __device__ __forceinline__ uint64_t pair_of(const uint32_t* r) {
   return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
-// Eight consecutive TMEM columns of the warp's lanes.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // The gates of every chunk: one block per (chunk, 32 heads).  dt is read with
 // the heads on the lanes (its rows are tokens), then each warp scans whole
@@ -357,7 +357,8 @@ __device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* xw,
 
 // ---------------------------------------------------------------------------
 // The walk: one block per (segment, head, 64 columns of the state).
-//   warp 0: the MMAs of U and Yo;  warp 1: the MMAs of CB and Yd
+//   warp 0: the MMAs of U and of Yo's first terms of S0;  warp 1: those of CB, Yd and
+//   Yo's second terms
 //   warp 2: TMA loads;  warp 3: TMA stores of the outputs
 //   groups 0, 1 (four warps each): M from CB (16 of each 32 columns each)
 //   groups 2, 3: the state (32 columns each)
@@ -366,25 +367,30 @@ __device__ __forceinline__ void build_xw(const uint4 (&x)[N], unsigned char* xw,
 // over.  An MMA of 64 columns with both operands in shared memory takes as long
 // as one of 96 (it waits for A): the three operands of U sit side by side as one
 // of 192 columns.
-// Bound by shared memory's 128 bytes a clock, beside issue: a chunk moves about 400 KB
-// through it (TMA writes 80, the MMAs' operands 220, the roles' own 100), 3125 of the
-// 4500 clk it takes.  One prompt of 32768 tokens of 64 heads x 64 columns x 128 rows in 29
-// chunks a segment: 278 us (as four roles of one warp each with every wait's failure
-// path in line 582).
+// S0's second terms take the place of the first once Yo has read those (there is no
+// room for both), while U's products run.  Yo's second products come before Yd, whose M
+// takes longer to form: after Yd 458 us for the prompt below, by warp 0 after U 447, so 439.
+// Bound by shared memory's 128 bytes a clock, beside issue: a chunk moves about 480 KB
+// through it (TMA writes 80, the MMAs' operands 285, the roles' own 115), 3750 of the
+// 5200 clk it takes.  One prompt of 32768 tokens of 64 heads x 64 columns x 128 rows in 29
+// chunks a segment: 320 us (278 with one BF16 number each of M and S0; as four roles of
+// one warp each with every wait's failure path in line 582).
 // ---------------------------------------------------------------------------
 constexpr int WALK_THREADS = 28 * 32;
-// TMEM columns: CB (16 of them a step of 16 K, over the first 8 of which M is
-// written), U (the three terms' products), Yo, Yd.
+// TMEM columns: CB (16 of them a step of 16 K, over which M is written: the first
+// terms of its pairs over 8, the second over the next 8), U (the three terms'
+// products), Yo, Yd.
 constexpr uint32_t T_CB = 0, T_U = 128, T_YO = 320, T_YD = 384;
 
 struct WalkSmem {
   unsigned char B[2][2 * BLK], C[2][2 * BLK], X[2][BLK];
   unsigned char xw[3][BLK];  // w x in three terms
-  unsigned char S[BLK];      // S0 in BF16
+  unsigned char S[BLK];      // S0: the first, then, once Yo has read them, the second terms of its pairs
   float gates[2][GATES];
   // [2]: by the chunk's parity, where a role may wait a chunk apart from the others
   uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], xw_full[2], staged[2];
   uint64_t cb_full, m_full, u_full, u_empty, s_full, yo_full, y_full, y_empty, done[2];
+  uint64_t s2_full, yo2_full;  // the second terms of S0
   uint32_t tmem;
   int abort;
   Seg seg;
@@ -417,7 +423,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       tc::mbar_init(&s.u_empty, 8);
       tc::mbar_init(&s.s_full, 8);
       tc::mbar_init(&s.yo_full, 1);
-      tc::mbar_init(&s.y_full, 2);
+      tc::mbar_init(&s.s2_full, 8);
+      tc::mbar_init(&s.yo2_full, 1);
+      tc::mbar_init(&s.y_full, 1);
       tc::mbar_init(&s.y_empty, 8);
       tc::mbar_init(&s.cb_full, 1);
       tc::mbar_init(&s.m_full, 8);
@@ -452,7 +460,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const uint32_t b = c & 1;
-      // Yo = C S0
+      // Yo = C S0, the first terms
       ok = warp_wait(&s.s_full, c & 1, ab) && warp_wait(&s.bc_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
@@ -461,7 +469,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       for (int k = 0; k < 8; ++k)
         if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
       commit(&s.yo_full);
-      commit(&s.y_full);
       // U = B^T (w x)
       ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
       if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
@@ -481,7 +488,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
   } else if (warp == 1) {
     constexpr uint32_t i_cb = tc::idesc_bf16(128, 128);
     constexpr uint32_t i_yd = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
-    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]);
+    constexpr uint32_t i_yo = tc::idesc_bf16(128, PT) | tc::kIdescTransposeB;
+    const uint32_t d_c = desc_lo(s.C[0]), d_b = desc_lo(s.B[0]), d_x = desc_lo(s.X[0]), d_s = desc_lo(s.S);
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
@@ -495,6 +503,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       for (int k = 0; k < 8; ++k)
         if (k < ksteps) mma_ss(tmem + T_CB, d_c + b * stage2 + kmaj(k), d_b + b * stage2 + kmaj(k), i_cb, k > 0);
       commit(&s.cb_full);
+      // Yo += C S0, the second terms (written once the first terms' products are there)
+      if (!warp_wait(&s.s2_full, c & 1, ab)) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, true);
+      commit(&s.yo2_full);
       commit(&s.bc_empty[b]);
       // Yd = M x (M waited for x; the rows past the end are cleared with w x)
       ok = warp_wait(&s.m_full, c & 1, ab);
@@ -505,7 +520,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         mma_ts(tmem + T_YD, tmem + T_CB + 16 * k, d_x + b * stage1 + k * step, i_yd, k > 0);
-      commit(&s.y_full);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mma_ts(tmem + T_YD, tmem + T_CB + 16 * k + 8, d_x + b * stage1 + k * step, i_yd, true);
+      commit(&s.y_full);  // (Yo's products came before)
       commit(&s.x_empty[b]);
     }
     if (nch > 0) {
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       const uint32_t cb = trow + T_CB + j0;
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
-        uint32_t v[16], m[8];
+        uint32_t v[16], m[16];  // first terms, second terms
         if (b < quad) {
           tc::tmem_ld16(cb + 32 * b, v);
           const float rf = ex2(g.ss()[32 * b + 31] - sr);
@@ -592,8 +610,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           wait_ld(v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            m[2 * j] = round2(mul2(pair_of(v + 4 * j), cf[j].x));
-            m[2 * j + 1] = round2(mul2(pair_of(v + 4 * j + 2), cf[j].y));
+            split2(mul2(pair_of(v + 4 * j), cf[j].x), m[2 * j], m[8 + 2 * j]);
+            split2(mul2(pair_of(v + 4 * j + 2), cf[j].y), m[2 * j + 1], m[8 + 2 * j + 1]);
           }
         } else if (b == quad) {
           tc::tmem_ld16(cb + 32 * b, v);
@@ -610,13 +628,14 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           wait_ld(v);
 #pragma unroll
           for (int j = 0; j < 16; j += 2)
-            m[j / 2] = round2(pack2(j0 + j <= lane ? __uint_as_float(v[j]) * f[j] : 0.f,
-                                    j0 + j + 1 <= lane ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f));
+            split2(pack2(j0 + j <= lane ? __uint_as_float(v[j]) * f[j] : 0.f,
+                         j0 + j + 1 <= lane ? __uint_as_float(v[j + 1]) * f[j + 1] : 0.f),
+                   m[j / 2], m[8 + j / 2]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m[j] = 0u;
+          for (int j = 0; j < 16; ++j) m[j] = 0u;
         }
-        tmem_st8(cb + 32 * b, m);  // over columns just read
+        tc::tmem_st16(cb + 32 * b, m);  // over columns just read
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
@@ -671,7 +690,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         v[q] = make_uint4(round2(S[4 * q]), round2(S[4 * q + 1]), round2(S[4 * q + 2]), round2(S[4 * q + 3]));
       ok = warp_wait(&s.x_full[c & 1], (c >> 1) & 1, ab);
       // the previous chunk's Yo has read the operand
-      if (c > 0) ok = ok && warp_wait(&s.yo_full, (c - 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait(&s.yo2_full, (c - 1) & 1, ab);
       if (!ok) break;
       gam = ex2(Gates{s.gates[c & 1]}.total(A));
       warp_arrive(&s.x_empty[c & 1]);
@@ -679,6 +698,15 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(s.S + piece(r, 4 * half + q)) = v[q];
       tc::fence_proxy_async();
       warp_arrive(&s.s_full);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = make_uint4(rest2(S[4 * q]), rest2(S[4 * q + 1]), rest2(S[4 * q + 2]), rest2(S[4 * q + 3]));
+      ok = warp_wait(&s.yo_full, c & 1, ab);
+      if (!ok) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(s.S + piece(r, 4 * half + q)) = v[q];
+      tc::fence_proxy_async();
+      warp_arrive(&s.s2_full);
     }
     if (ok && sg.idx == sg.nseg - 1 && a.ht && r < a.NS) {
       float* to = a.ht + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;

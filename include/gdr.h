@@ -402,13 +402,15 @@ gdr_status sconv_step(gdr_dtype dtype, const void* x, int64_t ldx, const void* w
  * dt_bias null: zero).  Writes out [T][H][P] BF16 and, when non-null, the end
  * states ht [N][H][NS][P] FP32.  1 <= P <= GDR_SSM_MAX_P, 1 <= NS <=
  * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay).  The state is kept in FP32
- * throughout; out is rounded once, its sums over at most 128 tokens and its
- * share of the state take their operands in BF16.
+ * throughout; out is rounded once.  In chunks (below) its sums over at most 128
+ * tokens and over the state's rows take their operands as pairs of BF16 numbers:
+ * each term is off by at most 2^-17 of itself.
  * With P and NS multiples of 8, NS <= 128, rows on 16-byte boundaries and a
  * document of more than 32 tokens the scan runs in chunks of 128 tokens on the
  * tensor cores, long documents in several segments side by side; otherwise
  * token by token.  A value that is not finite reaches every later token of its
- * document and head, and in chunks the outputs of the chunk it is in.
+ * document and head, and in chunks the outputs of the chunk it is in (where an
+ * infinity may come out as NaN).
  * ht may be h0 (the states go on in place).
  * scratch: ssm_workspace_bytes bytes on a 256-byte boundary (0 for shapes that
  * never run in chunks). */

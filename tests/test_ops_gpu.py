@@ -342,6 +342,40 @@ def test_ssm_prompt_extreme_decays(gdr, decay, dtv):
     check(ht, rh, "ht")
 
 
+@pytest.mark.parametrize("lengths,mean", [([32, 7], 3.0), ([512], 1.0), ([512], 3.0), ([300, 40, 129], 3.0), ([3000], 3.0)])
+def test_ssm_prompt_state_sums_that_cancel(gdr, lengths, mean):
+    # The state's rows share a large part that C is orthogonal to, so that an output is a small sum of large
+    # terms: an operand of the sum rounded to n bits is off by 2^-n of |C| |S|, some 30 times the output at a mean
+    # of 3. The bounds of the outputs' own type hold all the same, in chunks as token by token.
+    g, P, N, H, n, T = gen(31), 64, 128, 2, len(lengths), sum(lengths)
+    x, dt, A, B, C, _, bias = scan_inputs(g, T, H, P, 1, N, F32)
+    B = (mean + randn(g, T, 1, N)).to(BF16)
+    half = randn(g, T, 1, N // 2, dtype=BF16)
+    C = torch.cat([half, -half], -1)
+    h0 = 10 * mean + randn(g, n, H, N, P)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *pack(lengths), dt_bias=bias, h0=h0)
+    act = torch.nn.functional.softplus(dt.double() + bias.double())
+    ro, rh = ref.scan(x.double(), act, A.double(), B.double(), C.double(), None, lengths, h0.double())
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
+@pytest.mark.parametrize("lengths", [[32, 7], [512, 100], [3000]])
+def test_ssm_prompt_token_sums_that_cancel(gdr, lengths):
+    # x changes its sign from token to token under a slow decay: the sum over a chunk's tokens leaves a
+    # fraction of its terms
+    g, P, N, H, T = gen(32), 64, 128, 2, sum(lengths)
+    x, _, A, B, C, _, _ = scan_inputs(g, T, H, P, 1, N, F32)
+    sign = 1 - 2 * (torch.arange(T, device="cuda") % 2)
+    x = ((8 + 0.25 * randn(g, T, H, P)) * sign[:, None, None]).to(BF16)
+    B, C = ((1 + 0.05 * randn(g, T, 1, N)).to(BF16) for _ in range(2))
+    dt, A = torch.full((T, H), 0.0625, device="cuda"), torch.full_like(A, -0.01)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *pack(lengths), softplus=False)
+    ro, rh = ref.scan(x.double(), dt.double(), A.double(), B.double(), C.double(), None, lengths, None)
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
 @pytest.mark.parametrize("batch,H,P,G,N,dt_dtype,pad,odd", [
     (1, 16, 64, 1, 128, BF16, 0, False), (7, 6, 40, 2, 24, F32, 8, False), (5, 3, 33, 1, 17, BF16, 3, True),
     (2, 2, 256, 1, 256, F32, 0, False), (130, 8, 64, 8, 128, BF16, 64, False), (3, 1, 1, 1, 1, F32, 0, False)])
