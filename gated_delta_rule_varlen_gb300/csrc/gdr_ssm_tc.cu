@@ -647,7 +647,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     uint64_t S[16];
     const float* start = nullptr;
     previous_ended();  // a segment's start state, too
-    if (sg.idx > 0) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
+    // Of a split document every start state comes from k_ssm_merge, the first segment's too:
+    // ht may be h0, and the block of the last segment writes it whenever it is done.
+    if (sg.nseg > 1) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
     else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
     for (int q = 0; q < 16; q += 2) {

@@ -303,6 +303,27 @@ def test_ssm_prompt_states_in_place(gdr, lengths):
     assert ht2 is pool and torch.equal(out, out2) and torch.equal(ht, pool)
 
 
+@pytest.mark.parametrize("lengths,H,P,G,N,states", [
+    ([9000, 2500, 70], 3, 64, 1, 128, True), ([20000], 8, 64, 2, 64, True), ([5000, 0, 4999], 2, 80, 1, 96, True),
+    ([7000, 33], 4, 64, 1, 128, False)])
+def test_ssm_prompt_in_segments_in_place(gdr, lengths, H, P, G, N, states):
+    # a split document's first segment takes its start state from the merge, whatever its last segment has
+    # written over h0 by then: in place, out of place and without h0 but zeros, the same bits
+    g, n = gen(34), len(lengths)
+    x, dt, A, B, C, D, bias = scan_inputs(g, sum(lengths), H, P, G, N, F32)
+    h0, cu = 20 * randn(g, n, H, N, P) if states else torch.zeros(n, H, N, P, device="cuda"), pack(lengths)
+    assert gdr.ssm_workspace_bytes(sum(lengths), H, P, G, N, cu[1]) > 4 * 352 * H * sum(max(1, -(-m // 128)) for m in lengths) + 1024
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *cu, D=D, dt_bias=bias, h0=h0 if states else None)
+    for _ in range(5):
+        pool = h0.clone()
+        out2, ht2 = gdr.ssm_fwd(x, dt, A, B, C, *cu, D=D, dt_bias=bias, h0=pool, ht=pool)
+        assert ht2 is pool and torch.equal(out, out2) and torch.equal(ht, pool)
+    act = torch.nn.functional.softplus(dt.double() + bias.double())
+    ro, rh = ref.scan(x.double(), act, A.double(), B.double(), C.double(), D.double(), lengths, h0.double())
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
 @pytest.mark.parametrize("D", [128, 1021, 2048, 5120, 9000])
 def test_norm_in_place(gdr, D):
     g = gen(D)
