@@ -220,7 +220,7 @@ __device__ __forceinline__ uint32_t sw_elem(int r, int c, uint32_t block) {
 // One 4-byte asynchronous copy global -> shared.
 __device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(d), "l"(gmem));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(d), "l"(gmem) : "memory");
 }
 
 // A operand T diag(f) (rows i, tokens j; T lower triangular) as BF16 hi + lo
