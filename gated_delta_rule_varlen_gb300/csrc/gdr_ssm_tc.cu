@@ -56,7 +56,17 @@ struct Seg {
   int chunk0;                     // its first chunk; an empty document counts as one
 };
 
-// A chunk's gates of one head (a_t = dt_t A log2 e):
+// A token's gate dt A (log2).  Below -128 it is -128: ex2 of either is zero (it flushes
+// below 2^-126), while a chunk's prefix sums stay above -2^14, where the differences
+// that the decays between other tokens are formed from keep 2^-11; of sums that a
+// reset of -1e9 had entered nothing would be left.  (A NaN stays.)
+__device__ __forceinline__ float gate_log2(float dt, float A) {
+  float a;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(dt * A), "f"(-128.f));
+  return a;
+}
+
+// A chunk's gates of one head (a_t = gate_log2(dt_t, A log2 e)):
 //   ss[j]   sum of the a after token j: 2^(ss_j - ss_i) is the decay from j to i,
 //           and dt_j 2^ss_j = w_j keeps its accuracy, since ss is summed from the end
 //   dt[j]   activated (zero past the document's end)
@@ -66,7 +76,7 @@ struct Gates {
   __device__ __forceinline__ const float* ss() const { return p; }
   __device__ __forceinline__ const float* dt() const { return p + Q; }
   __device__ __forceinline__ const float* colf() const { return p + 2 * Q; }
-  // the chunk's whole decay (log2)
+  // the chunk's whole decay (log2; the first token's gate as it is: below -128 all of it is zero)
   __device__ __forceinline__ float total(float A) const { return fmaf(*dt(), A, *ss()); }
 };
 __device__ __forceinline__ Gates gates_of(const TcArgs& t, int chunk, int h) {
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) k_ssm_gates(const int* __rest
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
       ss[i] = run;
-      run = fmaf(dt[i], A, run);
+      run += gate_log2(dt[i], A);
     }
     float after = run;  // inclusive sums from the last lane down
 #pragma unroll

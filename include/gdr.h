@@ -401,7 +401,7 @@ gdr_status sconv_step(gdr_dtype dtype, const void* x, int64_t ldx, const void* w
  * head h reads group h / (H / G) of B and C; A, D, dt_bias [H] FP32 (D,
  * dt_bias null: zero).  Writes out [T][H][P] BF16 and, when non-null, the end
  * states ht [N][H][NS][P] FP32.  1 <= P <= GDR_SSM_MAX_P, 1 <= NS <=
- * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay).  The state is kept in FP32
+ * GDR_SSM_MAX_N.  Precondition: dt' A <= 0 (a decay, of any size).  The state is kept in FP32
  * throughout; out is rounded once.  In chunks (below) its sums over at most 128
  * tokens and over the state's rows take their operands as pairs of BF16 numbers:
  * each term is off by at most 2^-17 of itself.

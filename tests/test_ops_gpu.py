@@ -397,6 +397,23 @@ def test_ssm_prompt_token_sums_that_cancel(gdr, lengths):
     check(ht, rh, "ht")
 
 
+@pytest.mark.parametrize("decay,slow,reset", [(-64.0, 0.01, 1e3), (-1e4, 1e-4, 1e3), (-1.0, 0.02, 1e9)])
+def test_ssm_prompt_resets(gdr, decay, slow, reset):
+    # tokens whose decay leaves nothing of the state, among slow ones: the decays between the others keep theirs
+    g, lengths, H, P, N = gen(33), [300, 128, 20], 2, 64, 128
+    T = sum(lengths)
+    x, _, A, B, C, _, _ = scan_inputs(g, T, H, P, 1, N, F32)
+    dt = torch.where(rand(g, T, H) < 0.05, reset, slow) * (0.5 + rand(g, T, H))
+    x = torch.where(dt[:, :, None] > 0.5 * reset - 1, x / reset, x).to(BF16)  # (their terms as large as the others')
+    A = torch.full_like(A, decay)
+    out, ht = gdr.ssm_fwd(x, dt, A, B, C, *pack(lengths), softplus=False)
+    torch.cuda.synchronize()
+    gdr.gdr_check_device()
+    ro, rh = ref.scan(x.double(), dt.double(), A.double(), B.double(), C.double(), None, lengths, None)
+    check(out, ro, "out")
+    check(ht, rh, "ht")
+
+
 @pytest.mark.parametrize("batch,H,P,G,N,dt_dtype,pad,odd", [
     (1, 16, 64, 1, 128, BF16, 0, False), (7, 6, 40, 2, 24, F32, 8, False), (5, 3, 33, 1, 17, BF16, 3, True),
     (2, 2, 256, 1, 256, F32, 0, False), (130, 8, 64, 8, 128, BF16, 64, False), (3, 1, 1, 1, 1, F32, 0, False)])
