@@ -521,6 +521,7 @@ gdr_status conv_check(int dtype, int wdtype, int64_t T, int64_t ldx, int32_t C, 
                       const void* weight) {
   if (dtype < 0 || dtype > GDR_DTYPE_F32 || (wdtype != dtype && wdtype != GDR_DTYPE_F32)) return GDR_INVALID_ARG;
   if (C <= 0 || W < 2 || W > 4 || T < 0 || (T > 1 && ldx < C)) return GDR_INVALID_ARG;
+  if (T > GDR_OPS_MAX_T || C > GDR_OPS_MAX_T) return GDR_INVALID_ARG;  // a tile's or block's end stays an int
   if (T > 0 && (!x || !weight)) return GDR_INVALID_ARG;
   return GDR_OK;
 }
@@ -533,7 +534,7 @@ using namespace gdr;
 extern "C" {
 
 gdr_status sconv_workspace_bytes(int64_t T, int32_t C, int32_t W, size_t* scratch_bytes) {
-  if (!scratch_bytes || T < 0 || T > INT32_MAX || C <= 0 || W < 2 || W > 4) return GDR_INVALID_ARG;
+  if (!scratch_bytes || T < 0 || T > GDR_OPS_MAX_T || C <= 0 || C > GDR_OPS_MAX_T || W < 2 || W > 4) return GDR_INVALID_ARG;
   const int tile = bwd_tile_tokens(T, C);
   const int64_t tiles = T > 0 ? (T + tile - 1) / tile : 1;
   *scratch_bytes = (size_t)tiles * (W + 1) * C * sizeof(float);

@@ -207,6 +207,8 @@ gdr_status ssm_check(const SsmArgs& a, int64_t T) {
   if (a.H <= 0 || a.G <= 0 || a.H % a.G != 0 || a.P <= 0 || a.P > GDR_SSM_MAX_P || a.NS <= 0 ||
       a.NS > GDR_SSM_MAX_N || T < 0)
     return GDR_INVALID_ARG;
+  // a tile's end and a token's elements stay ints
+  if (T > GDR_OPS_MAX_T || (int64_t)a.H * a.P > INT32_MAX || (int64_t)a.G * a.NS > INT32_MAX) return GDR_INVALID_ARG;
   if (T > 0 && (!a.x || !a.dt || !a.A || !a.B || !a.C || !a.out)) return GDR_INVALID_ARG;
   if (T > 1 && (a.ldx < (int64_t)a.H * a.P || a.ldb < (int64_t)a.G * a.NS || a.ldc < (int64_t)a.G * a.NS ||
                 a.lddt < a.H))
@@ -224,6 +226,7 @@ extern "C" {
 gdr_status ssm_workspace_bytes(int64_t T, int32_t H, int32_t P, int32_t G, int32_t NS, int32_t N,
                                const int32_t* cu_seqlens_host, size_t* scratch_bytes) {
   int64_t nc = 0;
+  if (T > GDR_OPS_MAX_T) return GDR_INVALID_ARG;
   if (!scratch_bytes || H <= 0 || G <= 0 || H % G != 0 || P <= 0 || P > GDR_SSM_MAX_P || NS <= 0 ||
       NS > GDR_SSM_MAX_N)
     return GDR_INVALID_ARG;

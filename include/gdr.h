@@ -350,7 +350,10 @@ gdr_status gdr_walk_slices(int32_t nchunks, int32_t direction, int32_t* bounds, 
  *     of the batch uses state slots[b] (slots null: state b, B <= S).  A slot
  *     outside [0, S) makes the row inactive: its output is zero and no state
  *     is touched.  Two rows of one call must not share a slot.
+ *   - Tokens and, of the convolution, channels number at most GDR_OPS_MAX_T;
+ *     H P and G NS of the scan stay below 2^31.
  *   - Results are deterministic (no floating-point atomics). */
+#define GDR_OPS_MAX_T 2147418112 /* 2^31 - 2^16 */
 typedef int gdr_dtype;
 #define GDR_DTYPE_BF16 0
 #define GDR_DTYPE_F16 1

@@ -115,6 +115,31 @@ def test_norm_refusals(gdr):
     assert bwd(nbytes=64) == gdr.GDR_WORKSPACE_TOO_SMALL
 
 
+def test_sizes_at_the_end_of_32_bits(gdr):
+    # tile ends, channels and a token's elements are ints in the kernels: what would pass them is refused
+    lib, bad, most = gdr.load(), gdr.GDR_INVALID_ARG, 2**31 - 2**16
+    n = ctypes.c_size_t(0)
+    for T in (most + 1, 2**31 - 1):
+        k, c = cu(0, T)
+        assert lib.sconv_fwd(0, P(), 1, P(), None, 0, P(), c, 1, T, 1, 4, 1, None, P(2), None, None) == bad
+        assert lib.sconv_bwd(0, P(), 1, P(), None, 0, P(), c, 1, T, 1, 4, 1, None, P(2), 1, None, P(3), P(), None, None, P(),
+                             1 << 50, None) == bad
+        assert lib.sconv_step(0, P(), 1, P(), None, 0, P(), None, T, T, 1, 4, 1, P(2), None) == bad
+        assert lib.sconv_workspace_bytes(T, 1, 4, ctypes.byref(n)) == bad
+        assert lib.sconv_workspace_bytes(1, T, 4, ctypes.byref(n)) == bad
+        assert lib.ssm_workspace_bytes(T, 1, 1, 1, 1, 1, c, ctypes.byref(n)) == bad
+        assert lib.ssm_fwd(P(), 1, P(), 2, 1, P(), P(), 1, P(), 1, None, None, 1, P(), c, 1, T, 1, 1, 1, 1, None, P(2), None,
+                           P(), 1 << 50, None) == bad
+    k, c = cu(0, 4)
+    C = 2**31 - 500
+    assert lib.sconv_fwd(0, P(), C, P(), None, 0, P(), c, 1, 4, C, 4, 1, None, P(2), None, None) == bad
+    assert lib.sconv_step(0, P(), C, P(), None, 0, P(), None, 1, 1, C, 4, 1, P(2), None) == bad
+    H = 2**23  # of 256 columns
+    assert lib.ssm_step(P(), 2**31, P(), 2, H, P(), P(), 1, P(), 1, None, None, 1, P(), None, 1, 1, H, 256, 1, 1, P(2), None) == bad
+    assert lib.ssm_step(P(), H, P(), 2, H, P(), P(), 2**31, P(), 2**31, None, None, 1, P(), None, 1, 1, H, 1, H, 256, P(2),
+                        None) == bad
+
+
 def test_workspace_sizes(gdr):
     # partial rows of W + 1 sums a channel and tile; tiles of 256 tokens at most, 16 at least
     for T, C, W in ((0, 8, 2), (1, 37, 4), (1000, 64, 3), (32768, 10240, 4)):
