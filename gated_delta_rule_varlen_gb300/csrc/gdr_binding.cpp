@@ -113,6 +113,11 @@ struct Call {
     *bytes = (size_t)t.numel() * t.element_size();
     return t;
   }
+  // A size that the library takes as 32 bits.
+  int32_t size(const char* name, int64_t n) const {
+    if (n > INT32_MAX) fail(std::string(name) + " " + std::to_string(n) + " is past 2^31 - 1");
+    return (int32_t)n;
+  }
   void status(gdr_status code) const {
     if (code == GDR_OK) return;
     PyObject* r = PyObject_CallFunction(g_check, "is", (int)code, where);
@@ -217,7 +222,7 @@ struct Conv {
     if (x.dim() != 2) c.fail("x has shape " + str(x.sizes()) + ", expected [tokens, channels]");
     if (dt < 0) c.fail("x is " + str(type) + "; bfloat16, float16 and float32 are supported");
     T = x.size(0);
-    C = x.size(1);
+    C = c.size("channels", x.size(1));
     const Tensor& wt = c.tensor("weight", weight);
     if (wt.dim() != 2 || wt.size(0) != C || wt.size(1) < 2 || wt.size(1) > 4)
       c.fail("weight has shape " + str(wt.sizes()) + ", expected [" + std::to_string(C) + ", 2 to 4]");
@@ -288,7 +293,8 @@ PyObject* sconv_step_(PyObject* const* a) {  // x weight bias state slots silu o
   Call c{"sconv_step"};
   const Conv v(c, a[0], a[1], a[2]);
   const Tensor& st = c.tensor("state", a[3]);
-  const int64_t S = st.dim() > 0 ? st.size(0) : 0, state[3] = {S, v.W - 1, v.C}, shape[2] = {v.T, v.C};
+  const int64_t S = c.size("states", st.dim() > 0 ? st.size(0) : 0), state[3] = {S, v.W - 1, v.C}, shape[2] = {v.T, v.C};
+  const int32_t rows = c.size("batch", v.T);
   void* sp = c.dense("state", st, v.type, state);
   const int64_t ldx = v.rows(c, "x", v.x);
   const int32_t* slots = static_cast<const int32_t*>(c.dense("slots", a[4], ScalarType::Int, {v.T}));
@@ -296,7 +302,7 @@ PyObject* sconv_step_(PyObject* const* a) {  // x weight bias state slots silu o
   void* op;
   const Tensor out = c.output("out", a[6], shape, v.type, &op);
   c.run([&] {
-    return sconv_step(v.dt, v.x.data_ptr(), ldx, v.w, v.bias, v.wdt, sp, slots, (int32_t)v.T, (int32_t)S, (int32_t)v.C, v.W,
+    return sconv_step(v.dt, v.x.data_ptr(), ldx, v.w, v.bias, v.wdt, sp, slots, rows, (int32_t)S, (int32_t)v.C, v.W,
                       silu, op, c.stream);
   });
   return wrap(out);
@@ -326,14 +332,14 @@ struct Scan {
     c.on(x);
     if (x.dim() != 3) c.fail("x has shape " + str(x.sizes()) + ", expected [tokens, heads, head dim]");
     T = x.size(0);
-    H = x.size(1);
-    P = x.size(2);
+    H = c.size("heads", x.size(1));
+    P = c.size("head dim", x.size(2));
     ldx = heads(c, "x", x, T);
     ldb = heads(c, "B", B, T);
     ldc = heads(c, "C", C, T);
     if (B.sizes() != C.sizes()) c.fail("B has shape " + str(B.sizes()) + " and C " + str(C.sizes()));
-    G = B.size(1);
-    NS = B.size(2);
+    G = c.size("groups", B.size(1));
+    NS = c.size("state size", B.size(2));
     dt_code = code_of(dt.scalar_type());
     if (dt.dim() != 2 || dt.size(0) != T || dt.size(1) != H || (dt_code != GDR_DTYPE_BF16 && dt_code != GDR_DTYPE_F32) ||
         (H > 1 && dt.stride(1) != 1))
@@ -375,14 +381,15 @@ PyObject* ssm_step_(PyObject* const* a) {  // x dt A B C D dt_bias softplus stat
   const Scan v(c, a);
   const bool softplus = truth(a[7]);
   const Tensor& st = c.tensor("state", a[8]);
-  const int64_t S = st.dim() > 0 ? st.size(0) : 0, state[4] = {S, v.H, v.NS, v.P}, shape[3] = {v.T, v.H, v.P};
+  const int64_t S = c.size("states", st.dim() > 0 ? st.size(0) : 0), state[4] = {S, v.H, v.NS, v.P}, shape[3] = {v.T, v.H, v.P};
+  const int32_t rows = c.size("batch", v.T);
   float* sp = static_cast<float*>(c.dense("state", st, ScalarType::Float, state));
   const int32_t* slots = static_cast<const int32_t*>(c.dense("slots", a[9], ScalarType::Int, {v.T}));
   void* op;
   const Tensor out = c.output("out", a[10], shape, ScalarType::BFloat16, &op);
   c.run([&] {
     return ssm_step(v.bf(v.x), v.ldx, v.dt.data_ptr(), v.dt_code, v.lddt, v.A, v.bf(v.B), v.ldb, v.bf(v.C), v.ldc, v.D, v.bias,
-                    softplus, sp, slots, (int32_t)v.T, (int32_t)S, (int32_t)v.H, (int32_t)v.P, (int32_t)v.G, (int32_t)v.NS,
+                    softplus, sp, slots, rows, (int32_t)S, (int32_t)v.H, (int32_t)v.P, (int32_t)v.G, (int32_t)v.NS,
                     static_cast<gdr_bf16*>(op), c.stream);
   });
   return wrap(out);
@@ -395,7 +402,8 @@ PyObject* delta_step(const char* where, bool kda, PyObject* const* a) {  // q k 
   c.on(q);
   if (q.dim() != 3 || v.dim() != 3 || q.size(2) != 128)
     c.fail("q has shape " + str(q.sizes()) + " and v " + str(v.sizes()) + ", expected [batch, heads, 128]");
-  const int64_t B = q.size(0), Hqk = q.size(1), HV = v.size(1), S = st.dim() > 0 ? st.size(0) : 0;
+  const int64_t B = c.size("batch", q.size(0)), Hqk = c.size("heads", q.size(1)), HV = c.size("heads", v.size(1)),
+                S = c.size("states", st.dim() > 0 ? st.size(0) : 0);
   if (kda && Hqk != HV)
     c.fail("q and k have " + std::to_string(Hqk) + " heads and v has " + std::to_string(HV) + "; KDA needs the same count");
   if (Hqk < 1 || HV % Hqk)
@@ -472,7 +480,7 @@ struct Norm {
     D = x.size(nd - 1);
     const int64_t inner = nd >= 3 ? x.size(nd - 2) : 1;
     R0 = inner ? x.numel() / (inner * D) : 0;
-    R1 = (int)(inner ? inner : 1);
+    R1 = c.size("rows of the inner dimension", inner ? inner : 1);
     const ScalarType wtype = has_weight ? c.tensor("weight", a[1]).scalar_type()
                              : has_post ? c.tensor("post_weight", a[2]).scalar_type()
                                         : type;

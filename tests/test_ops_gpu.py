@@ -714,6 +714,16 @@ def test_refusals(gdr):
     torch.cuda.synchronize()
 
 
+def test_refuses_sizes_past_32_bits(gdr):
+    # (no memory behind them: every row is the same one)
+    x = torch.ones(1, device="cuda", dtype=BF16).expand(1, 2**32 + 4, 1)
+    w = torch.ones(1, device="cuda", dtype=BF16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gdr.norm_fwd(x, post_weight=w)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gdr.norm_bwd(x, post_weight=w, dh=x)
+
+
 def test_binding_holds_nothing(gdr):
     # references and device memory after calls, refused calls included, are what they were before
     import sys
