@@ -10,6 +10,7 @@
 #pragma once
 #include "gdr_ops.cuh"
 #include <algorithm>
+#include <atomic>
 
 #include "gdr_runtime.h"
 
@@ -53,14 +54,21 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, in
 // Most blocks of an SM that a backward on rows of D elements is launched with.
 constexpr int norm_bwd_blocks(int D) { return D <= 2048 ? 8 : 3; }
 
+// What a device holds of a kernel at a time, kept from call to call (and from thread to
+// thread): blocks an SM, or clusters by their size.  0: not known yet.
+struct Held {
+  static constexpr int DEVICES = 16;
+  std::atomic<int> n[DEVICES][MAX_CLUSTER + 1];
+};
+
 // Launches as many row groups (blocks or clusters, each goes through its share of
-// the rows) as the GPU holds at a time, or fewer where there are fewer rows; a
-// shifted row keeps its place within 16 bytes from one of a thread's rows to the
-// next (the step between them is a multiple of V).  held: what the GPU holds, by
-// cluster, kept from call to call.
+// the rows) as the GPU holds at a time, `limit` blocks an SM at most, or fewer where
+// there are fewer rows; a shifted row keeps its place within 16 bytes from one of a
+// thread's rows to the next (the step between them is a multiple of V).  held: the
+// kernel's own; smem is always the same for a kernel.
 template <typename K>
-cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t smem, int limit,
-                        int (&held)[MAX_CLUSTER + 1], int* parts, cudaStream_t st) {
+cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t smem, int limit, Held& held, int* parts,
+                        cudaStream_t st) {
   const int threads = norm_threads(s.TPR), groups = threads / s.TPR, size = s.cluster > 0 ? s.cluster : 1;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -79,20 +87,22 @@ cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t 
   if (s.cluster > 8) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
   }
-  int& most = held[s.cluster];
-  if (most == 0) {
-    int n = 0;
+  int dev = 0, fits = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  std::atomic<int>* known = dev >= 0 && dev < Held::DEVICES ? &held.n[dev][s.cluster] : nullptr;
+  if (known) fits = known->load(std::memory_order_relaxed);
+  if (fits == 0) {
     if (s.cluster > 0) {
       cfg.gridDim = dim3(152 / size * size);
-      if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) return e;
-      n = std::min(n, 152 * limit / size);
-    } else {
-      if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem)) return e;
-      n = 152 * std::min(n, limit);
+      if (cudaError_t e = cudaOccupancyMaxActiveClusters(&fits, kernel, &cfg)) return e;
+    } else if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fits, kernel, threads, smem)) {
+      return e;
     }
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    most = n;
+    if (fits < 1) return cudaErrorInvalidConfiguration;
+    if (known) known->store(fits, std::memory_order_relaxed);
   }
+  // (the limit of this call's width, whatever width came first: the backward's workspace holds no more)
+  const int most = s.cluster > 0 ? std::min(fits, 152 * limit / size) : 152 * std::min(fits, limit);
   int64_t n = std::min<int64_t>((a.rows + groups - 1) / groups, most);
   if (s.shift && s.V > groups) {
     const int64_t unit = s.V / groups;

@@ -364,11 +364,10 @@ __global__ void __launch_bounds__(1024) k_norm_wgrad(const float* __restrict__ p
 
 template <typename T, int V, int TPR, int NV, bool CLUSTER, bool OUT, bool SHIFT>
 cudaError_t launch_one(const NormArgs& a, const NormShape& s, int* parts, cudaStream_t st) {
-  static int held[MAX_CLUSTER + 1];
+  static Held held;
   using F = BwdRows<T, V, TPR, NV, OUT, SHIFT>;
-  size_t smem = F::AHEAD ? F::Rows::BYTES : 0;
-  // (the groups' weight gradients meet in the same bytes)
-  if (TPR <= 32) smem = std::max(smem, (size_t)(128 / TPR) * a.D * sizeof(float));
+  // (the groups' weight gradients meet in the same bytes: at most V NV columns a thread)
+  const size_t smem = std::max((size_t)(F::AHEAD ? F::Rows::BYTES : 0), TPR <= 32 ? 128 * V * NV * sizeof(float) : (size_t)0);
   return norm_launch(k_norm_bwd<T, V, TPR, NV, CLUSTER, OUT, SHIFT>, a, s, smem, norm_bwd_blocks(a.D), held, parts, st);
 }
 

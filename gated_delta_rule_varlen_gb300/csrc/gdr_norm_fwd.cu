@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
 
 template <typename T, int V, int TPR, int NV, bool CLUSTER, bool OUT, bool SHIFT>
 cudaError_t launch_one(const NormArgs& a, const NormShape& s, int* parts, cudaStream_t st) {
-  static int held[MAX_CLUSTER + 1];
+  static Held held;
   using F = FwdRows<T, V, TPR, NV, OUT, SHIFT>;
   const size_t smem = F::AHEAD ? F::Rows::BYTES : 0;
   return norm_launch(k_norm_fwd<T, V, TPR, NV, CLUSTER, OUT, SHIFT>, a, s, smem, 32, held, parts, st);

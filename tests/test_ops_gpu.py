@@ -589,6 +589,24 @@ def test_norm_rows_keep_to_themselves(gdr, D):
     assert torch.isnan(b["dx"][5]).all()
 
 
+@pytest.mark.parametrize("widths", [(2047, 3000), (3000, 2047, 3064), (2045, 2056), (1024, 2048, 2049, 4096), (4099, 9001, 16384)])
+def test_norm_partial_rows_stay_in_the_workspace(gdr, widths):
+    # widths that share a kernel, but not the number of partial rows their workspaces hold, one after another
+    g = gen(35)
+    for D in widths:
+        rows, need = 4000, gdr.norm_workspace_bytes(D)
+        x, r, dy = (randn(g, rows, D, dtype=BF16) for _ in range(3))
+        w = (1 + 0.1 * randn(g, D)).to(BF16)
+        buf = torch.full((need + 4096 * D,), 0x5a, dtype=torch.uint8, device="cuda")
+        got = gdr.norm_bwd(x, weight=w, post_weight=w, residual=r, dy=dy, scratch=buf[:need])
+        assert bool((buf[need:] == 0x5a).all()), D
+        a = [t.double().requires_grad_() for t in (x, w, w, r)]
+        torch.autograd.backward(ref.norms(a[0], a[1], a[2], None, "silu", a[3], 1.0, 1e-6)[1], dy.double())
+        check(got["dx"], a[0].grad, f"dx {D}")
+        check(got["dweight"], a[1].grad, f"dweight {D}")
+        check(got["dpost_weight"], a[2].grad, f"dpost_weight {D}")
+
+
 def test_norm_gradients_by_differences(gdr):
     g, shape = gen(8), (6, 2, 40)
     a = {"x": randn(g, *shape), "gate": randn(g, *shape), "residual": randn(g, *shape), "weight": 1 + 0.3 * randn(g, 40),
