@@ -306,10 +306,11 @@ __device__ __forceinline__ void load_weight(const NormArgs& a, const void* p, in
 
 // sigmoid(z) and z sigmoid(z) of a pair; the latter closes at z = -inf (where
 // the product would be 0 inf).
+template <typename T>
 __device__ __forceinline__ void gate_of(uint64_t z, uint64_t& sg, uint64_t& act, bool sigmoid) {
   float a, b;
   unpack2(z, a, b);
-  const float sa = sigmoid_f(a), sb = sigmoid_f(b);
+  const float sa = sigmoid_f<T>(a), sb = sigmoid_f<T>(b);
   sg = pack2(sa, sb);
   act = sigmoid ? sg : pack2(a == -INFINITY ? 0.f : a * sa, b == -INFINITY ? 0.f : b * sb);
 }

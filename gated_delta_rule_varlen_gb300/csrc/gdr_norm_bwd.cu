@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_bwd_min_blocks(TPR, V 
             get(1, i, raw.z[i], f);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-              gate_of(f[q], sg, act, a.sigmoid);
+              gate_of<T>(f[q], sg, act, a.sigmoid);
               h[i][q] = mul2(h[i][q], act);
             }
           }
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_bwd_min_blocks(TPR, V 
           }
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            gate_of(z[q], sg, act, a.sigmoid);
+            gate_of<T>(z[q], sg, act, a.sigmoid);
             // silu: sg + act (1 - sg); sigmoid: sg (1 - sg)
             const uint64_t rest = fma2(minus, sg, one);
             const uint64_t dact = a.sigmoid ? mul2(sg, rest) : fma2(act, rest, sg);

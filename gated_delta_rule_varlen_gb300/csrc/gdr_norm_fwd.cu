@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_norm_fwd(NormArgs a) {
           get(1, i, raw.z[i], z);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            gate_of(z[q], sg, act, a.sigmoid);
+            gate_of<T>(z[q], sg, act, a.sigmoid);
             u[i][q] = mul2(u[i][q], act);
           }
         }

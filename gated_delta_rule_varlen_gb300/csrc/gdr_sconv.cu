@@ -56,7 +56,8 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const T* x, const
 // Rows of the walks asked for ahead: in shared memory (4 to 16 bytes each a thread),
 // or, single elements of 16 bits, which cannot be copied there, in registers.  (Of
 // single FP32 elements the forward keeps its rows in registers, too: 65536 x 4095
-// takes 391 us against 465; the backward, with two rings, 785 against 918.)
+// took 391 us against 465; the backward, with two rings, 785 against 918.  With the
+// sigmoid of FP32 exact to 6e-7 the kept ones take 408 and 816.)
 constexpr int kDepth = 8;
 template <typename T, int V>
 constexpr bool kRing = V * sizeof(T) >= 4;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(128, 5) k_sconv_fwd(ConvArgs a) {
         if (a.silu) {
           float z0, z1;
           unpack2(z, z0, z1);
-          z = mul2(z, pack2(sigmoid_f(z0), V > 1 ? sigmoid_f(z1) : 0.f));
+          z = mul2(z, pack2(sigmoid_f<T>(z0), V > 1 ? sigmoid_f<T>(z1) : 0.f));
         }
         y[i] = z;
 #pragma unroll
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(128, 5) k_sconv_bwd(ConvBwdArgs a) {
           z = fma2(w[K][i], xv[i], z);
           float z0, z1;
           unpack2(z, z0, z1);
-          const uint64_t s = pack2(sigmoid_f(z0), V > 1 ? sigmoid_f(z1) : 0.f);
+          const uint64_t s = pack2(sigmoid_f<T>(z0), V > 1 ? sigmoid_f<T>(z1) : 0.f);
           // s + z s (1 - s)
           dz = mul2(dz, fma2(mul2(z, s), fma2(minus, s, one), s));
         }
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(128) k_sconv_step(ConvStepArgs a) {
 #pragma unroll
       for (int j = 0; j < W; ++j)
         z = fmaf(load_param<T>(a.weight, a.wf32, (int64_t)(c + v) * W + j), to_f<T>(win[j].e[v]), z);
-      y[v] = a.silu ? z * sigmoid_f(z) : z;
+      y[v] = a.silu ? z * sigmoid_f<T>(z) : z;
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) *reinterpret_cast<Vec<T, V>*>(st + (int64_t)k * a.C) = win[k + 1];

@@ -160,6 +160,31 @@ def test_sconv_step_follows_the_prompt(gdr, B, C, W, dtype, bias, silu, pad, odd
     assert torch.equal(state[rest], before[rest]), "a state of no row was touched"
 
 
+def test_silu_and_sigmoid_keep_their_bits(gdr):
+    # FP32, element by element over the whole range: the exponential (2 ulp), the factor of its argument's rounding
+    # and its product with it, 1 + y and z s (half an ulp each) and the reciprocal (1 ulp) add up to 5 ulp of 2^-23
+    z = torch.cat([torch.linspace(-86, 86, 4001), torch.linspace(-1, 1, 1003)]).cuda()
+    n, zd, W = z.numel(), z.double(), 3
+    w = torch.zeros(n, W, device="cuda")
+    w[:, W - 1] = 1
+    s = torch.exp(-torch.nn.functional.softplus(-zd, threshold=1e9))
+
+    def off(got, want):
+        assert torch.isfinite(got).all()
+        return float(((got.double() - want).abs() / want.abs().clamp_min(1e-300)).max())
+    most = 5 * 2.0 ** -23
+    assert off(gdr.sconv_step(z[None], w, None, torch.zeros(1, W - 1, n, device="cuda"))[0], zd * s) <= most
+    cu = pack([2])
+    assert off(gdr.sconv_fwd(torch.stack([z, z]), w, None, *cu)[0][1], zd * s) <= most
+    one, zero = torch.ones_like(z), torch.zeros_like(z)
+    for act, want in (("silu", zd * s), ("sigmoid", s)):
+        h, _ = gdr.norm_fwd(one[None], gate=z[None], act=act, residual=zero[None])
+        assert off(h[0], want) <= most, act
+    inf = torch.tensor([float("inf"), -float("inf"), NAN], device="cuda")
+    h, _ = gdr.norm_fwd(torch.ones(1, 3, device="cuda"), gate=inf[None], act="sigmoid", residual=torch.zeros(1, 3, device="cuda"))
+    assert h[0, 0] == 1 and h[0, 1] == 0 and torch.isnan(h[0, 2])
+
+
 def test_sconv_infinities_stay_in_their_document(gdr):
     # an inf or NaN before a document's start, or in its neighbour channel, reaches no other output
     g, C, lengths = gen(3), 16, [4, 4, 4]
