@@ -4,7 +4,9 @@ and the operators' Python binding beside it.
 Each translation unit is compiled in parallel with nvcc (the binding with the
 host compiler), then linked as one shared library at
 gated_delta_rule_varlen_gb300/lib/libgdr.so; the binding, which depends on the
-PyTorch it was compiled against, carries that version in its name.
+PyTorch and the Python it was compiled against, carries both in its name.  The
+library needs neither: without PyTorch it is built alone, and an error in the
+binding is raised once the library is there.
 """
 from __future__ import annotations
 
@@ -33,7 +35,7 @@ def nvcc() -> str:
 
 def binding_path() -> str:
     import torch
-    return os.path.join(LIBDIR, f"_gdr_ops-{torch.__version__}.so")
+    return os.path.join(LIBDIR, f"_gdr_ops-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _cxx(source: str, target: str):
@@ -70,26 +72,39 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    binding, source = binding_path(), os.path.join(CSRC, "gdr_binding.cpp")
-    bobj, compile_, link = _cxx(source, binding)
-    compiled = list(procs)
-    if force or _stale(bobj, [source, headers[-1]]):
-        compiled.append(("gdr_binding.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    errors = []
-    for src, p in compiled:
+    bound = None
+    try:
+        binding = binding_path()
+    except ImportError:
+        print("PyTorch is not installed: the library is built without the operators' Python binding", file=sys.stderr)
+        binding = None
+    if binding:
+        source = os.path.join(CSRC, "gdr_binding.cpp")
+        bobj, compile_, link = _cxx(source, binding)
+        if force or _stale(bobj, [source, headers[-1]]):
+            bound = subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+    def finish(src, p):
+        """The compiler's complaint, or None."""
         out, _ = p.communicate()
+        text = out.decode(errors="replace")
         if p.returncode != 0:
-            errors.append(f"{src}:\n{out.decode(errors='replace')}")
-        elif verbose and out:
-            print(out.decode(errors="replace"), file=sys.stderr)
-    if errors:
-        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
-    if force or procs or _stale(LIB, objs):
+            return f"{src}:\n{text}"
+        if verbose and text:
+            print(text, file=sys.stderr)
+        return None
+
+    errors = [e for e in (finish(src, p) for src, p in procs) if e]
+    if not errors and (force or procs or _stale(LIB, objs)):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or _stale(binding, [bobj]):
+    if bound:
+        errors += [e for e in (finish("gdr_binding.cpp", bound),) if e]
+    if errors:
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
+    if binding and (force or _stale(binding, [bobj])):
         subprocess.run(link, check=True)
         os.replace(binding + f".tmp{os.getpid()}", binding)
     return LIB
