@@ -24,8 +24,13 @@
 // they hold another document's values (a NaN there would pass through a zero
 // weight).  Within a document a non-finite value reaches the outputs of its
 // whole chunk.
-#include <algorithm>
 #include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <functional>
+#include <new>
+#include <utility>
+#include <vector>
 
 #include "gdr_ssm.cuh"
 #include "gdr_tc.cuh"
@@ -1143,16 +1148,35 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
   best.scratch = up256((size_t)gate_chunks * H * GATES * sizeof(float));
   // (nothing to gain where whole documents come near to even work)
   if (cost < 1.1 * nc * items / sms) return best;
-  // pieces of the longest document
-  for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
-    const int64_t L = (most + k - 1) / k;
-    int64_t nseg = 0, ends = 0;
+  // pieces of the longest document; only documents longer than the shortest piece are
+  // looked at again, those of one length together
+  const int64_t shortest = std::max<int64_t>(4, (most + 255) / 256);
+  std::vector<std::pair<int64_t, int64_t>> longer;  // (chunks, documents that have as many), longest first
+  try {
+    std::vector<int64_t> chunks;
     for (int i = 0; i < N; ++i) {
       const int64_t ch = (cu[i + 1] - (int64_t)cu[i] + Q - 1) / Q;
-      const int64_t n = ch == 0 ? 1 : (ch + L - 1) / L;
-      nseg += n;
-      ends += std::max<int64_t>(n, 1) - 1;
+      if (ch > shortest) chunks.push_back(ch);
     }
+    std::sort(chunks.begin(), chunks.end(), std::greater<int64_t>());
+    for (int64_t ch : chunks) {
+      if (longer.empty() || longer.back().first != ch) longer.push_back({ch, 0});
+      ++longer.back().second;
+    }
+  } catch (const std::bad_alloc&) {
+    return best;  // (whole documents need no list)
+  }
+  int64_t last = 0;
+  for (int64_t k = 2; k <= 256 && (most + k - 1) / k >= 4; ++k) {
+    const int64_t L = (most + k - 1) / k;
+    if (L == last) continue;
+    last = L;
+    int64_t ends = 0;
+    for (const auto& d : longer) {
+      if (d.first <= L) break;
+      ends += ((d.first + L - 1) / L - 1) * d.second;
+    }
+    const int64_t nseg = N + ends;
     const double waves = (double)nseg * items / sms;
     const double walk = std::max((nc + kStart * nseg) * items / sms, (double)(L + kStart) * (int64_t)(waves + 0.999));
     const double sum = kSum * L * (int64_t)((double)(ends * items >> pairs) / sms + 0.999) + 2 * kStart;
