@@ -60,6 +60,7 @@ __device__ __forceinline__ float load_dt(const SsmArgs& a, int64_t t, int h) {
 struct SsmPlan {
   int lseg;          // chunks of a segment at most
   int64_t nseg;      // segments of all documents (an empty document has one)
+  int64_t states;    // segments of documents that have several
   int64_t chunks;    // chunks of all documents (an empty document has one)
   bool split;        // some document has several
   size_t scratch;    // bytes

@@ -50,8 +50,8 @@ struct TcArgs {
   int pblocks;      // ceil(P / 64)
   int pairs;        // summaries: two neighbours a block
   int lseg;         // chunks of a segment at most
-  float* seg;       // [segments][H][NS][P]: start states of split documents' segments
-  float* gsum;      // [segments][H]: log2 decay over each segment
+  float* seg;       // [split documents' segments][H][NS][P]: their start states
+  float* gsum;      // [split documents' segments][H]: log2 decay over each
   int* err;
 };
 
@@ -59,6 +59,7 @@ struct TcArgs {
 struct Seg {
   int doc, idx, nseg, tok0, len;  // first token and tokens of the segment
   int chunk0;                     // its first chunk; an empty document counts as one
+  int slot;                       // its place among the segments of split documents
 };
 
 // A token's gate dt A (log2).  Below -128 it is -128: ex2 of either is zero (it flushes
@@ -91,7 +92,7 @@ __device__ __forceinline__ Gates gates_of(const TcArgs& t, int chunk, int h) {
 // Finds segment `want` by a scan over the documents (one warp).
 __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int want) {
   const int lane = threadIdx.x & 31;
-  int base = 0, cbase = 0;
+  int base = 0, cbase = 0, whole = 0;  // documents that are not split
 #pragma unroll 1
   for (int d0 = 0; d0 < N; d0 += 32) {
     const int d = d0 + lane;
@@ -113,6 +114,7 @@ __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int wan
       }
     }
     const int total = __shfl_sync(0xffffffffu, pre, 31), ctotal = __shfl_sync(0xffffffffu, cpre, 31);
+    const unsigned ones = __ballot_sync(0xffffffffu, n == 1);
     if (want < base + total) {
       const unsigned hit = __ballot_sync(0xffffffffu, want < base + pre);
       const int l = __ffs(hit) - 1;
@@ -127,12 +129,14 @@ __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int wan
       s.tok0 = ds + c0 * Q;
       s.len = min(dl, c1 * Q) - c0 * Q;
       s.chunk0 = cbase + __shfl_sync(0xffffffffu, cpre - nc, l) + c0;
+      s.slot = want - whole - __popc(ones & ((1u << l) - 1));
       return s;
     }
     base += total;
     cbase += ctotal;
+    whole += __popc(ones);
   }
-  return Seg{0, 0, 1, 0, 0, 0};
+  return Seg{0, 0, 1, 0, 0, 0, 0};
 }
 
 // Waits of the blocks' roles.  Each gives up after kTries tries of at most a
@@ -236,6 +240,7 @@ __device__ __forceinline__ Seg uniform(const Seg& s) {
   u.tok0 = __shfl_sync(0xffffffffu, s.tok0, 0);
   u.len = __shfl_sync(0xffffffffu, s.len, 0);
   u.chunk0 = __shfl_sync(0xffffffffu, s.chunk0, 0);
+  u.slot = __shfl_sync(0xffffffffu, s.slot, 0);
   return u;
 }
 // One arrival for the warp, after all its lanes' work.
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     previous_ended();  // a segment's start state, too
     // Of a split document every start state comes from k_ssm_merge, the first segment's too:
     // ht may be h0, and the block of the last segment writes it whenever it is done.
-    if (sg.nseg > 1) start = ta.seg + (((int64_t)sid * a.H + h) * a.NS + r) * a.P + pc;
+    if (sg.nseg > 1) start = ta.seg + (((int64_t)sg.slot * a.H + h) * a.NS + r) * a.P + pc;
     else if (a.h0) start = a.h0 + (((int64_t)sg.doc * a.H + h) * a.NS + r) * a.P + pc;
 #pragma unroll
     for (int q = 0; q < 16; q += 2) {
@@ -1011,14 +1016,14 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
 #pragma unroll 1
       while (ok && drained * kBatch < nch) ok = drain(drained++);
       if (ok && j < a.NS) {
-        float* to = ta.seg + (((int64_t)sid * a.H + h) * a.NS + j) * a.P;
+        float* to = ta.seg + (((int64_t)sg.slot * a.H + h) * a.NS + j) * a.P;
 #pragma unroll
         for (int q = 0; q < PT / 4; q += 2) {
           const int p = p0 + PT / 2 * half + 2 * q;
           if (p < a.P) *reinterpret_cast<ulonglong2*>(to + p) = make_ulonglong2(S[q], S[q + 1]);
         }
       }
-      if (j == 0 && half == 0 && p0 == 0) ta.gsum[(int64_t)sid * a.H + h] = tail;
+      if (j == 0 && half == 0 && p0 == 0) ta.gsum[(int64_t)sg.slot * a.H + h] = tail;
     }
   }
   tc::tc_fence_before();
@@ -1035,11 +1040,11 @@ __global__ void __launch_bounds__(256) k_ssm_merge(const __grid_constant__ TcArg
   const int eblocks = (int)((elems + 1023) / 1024);
   const int e0 = (blockIdx.x % eblocks) * 1024 + threadIdx.x * 4, h = (blockIdx.x / eblocks) % a.H;
   const int d = blockIdx.x / eblocks / a.H;
-  // the document's first segment: the segments of the documents before it
+  // the document's first segment: the segments of the split documents before it
   int before = 0;
   for (int i = threadIdx.x; i < d; i += 256) {
     const int ch = (a.cu[i + 1] - a.cu[i] + Q - 1) / Q;
-    before += ch == 0 ? 1 : (ch + ta.lseg - 1) / ta.lseg;
+    before += ch > ta.lseg ? (ch + ta.lseg - 1) / ta.lseg : 0;
   }
   __shared__ int sums[8];
 #pragma unroll
@@ -1142,7 +1147,7 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
     gate_chunks += std::max<int64_t>(ch, 1);
     most = std::max(most, ch);
   }
-  SsmPlan best{(int)std::max<int64_t>(most, 1), N, 0, false, 0};
+  SsmPlan best{(int)std::max<int64_t>(most, 1), N, 0, 0, false, 0};
   double cost = std::max((double)(nc + kStart * N) * items / sms, most + kStart);
   best.chunks = gate_chunks;
   best.scratch = up256((size_t)gate_chunks * H * GATES * sizeof(float));
@@ -1171,10 +1176,11 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
     const int64_t L = (most + k - 1) / k;
     if (L == last) continue;
     last = L;
-    int64_t ends = 0;
+    int64_t ends = 0, split = 0;  // segments that another one follows, documents that have such
     for (const auto& d : longer) {
       if (d.first <= L) break;
       ends += ((d.first + L - 1) / L - 1) * d.second;
+      split += d.second;
     }
     const int64_t nseg = N + ends;
     const double waves = (double)nseg * items / sms;
@@ -1184,11 +1190,12 @@ SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
       cost = walk + sum;
       best.lseg = (int)L;
       best.nseg = nseg;
+      best.states = ends + split;
       best.split = true;
     }
   }
   if (best.split)
-    best.scratch += up256((size_t)best.nseg * H * NS * P * sizeof(float)) + up256((size_t)best.nseg * H * sizeof(float));
+    best.scratch += up256((size_t)best.states * H * NS * P * sizeof(float)) + up256((size_t)best.states * H * sizeof(float));
   return best;
 }
 
@@ -1220,7 +1227,7 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, const SsmPlan& plan, void* scratch, 
   static_assert(sm_walk <= 232448 && sm_sum <= 232448, "227 KB of shared memory a block");
   if (plan.split) {
     t.seg = reinterpret_cast<float*>(rest);
-    t.gsum = reinterpret_cast<float*>(rest + up256((size_t)plan.nseg * a.H * a.NS * a.P * sizeof(float)));
+    t.gsum = reinterpret_cast<float*>(rest + up256((size_t)plan.states * a.H * a.NS * a.P * sizeof(float)));
     cudaFuncSetAttribute(k_ssm_sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_sum);
     {
       ProfScope ps("ssm_sum", st, (double)a.T * a.H);

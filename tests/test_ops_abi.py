@@ -166,6 +166,15 @@ def test_workspace_sizes(gdr):
         gdr.ssm_workspace_bytes(100, 4, 64, 1, 128, [0, 99])
 
 
+def test_scan_scratch_holds_states_of_split_documents_only(gdr):
+    # 128k tokens in segments and 1000 documents of 64 tokens, whose states are carried in registers
+    H, state = 8, 8 * 64 * 128 * 4
+    cu_host = [0] + [131072 + 64 * i for i in range(1001)]
+    gates = (1024 + 1000) * H * 352 * 4
+    n = gdr.ssm_workspace_bytes(cu_host[-1], H, 64, 1, 128, cu_host)
+    assert gates + 2 * state < n < gates + 256 * (state + 4 * H) + 1024  # (at most 256 segments a document)
+
+
 def test_scan_plan_is_quick_with_many_documents(gdr):
     # the plan runs twice a call: one long document among 4095 of 16 tokens took it 3.8 ms when it went through
     # all documents for every segment length, and takes some 15 us

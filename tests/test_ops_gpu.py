@@ -330,7 +330,8 @@ def test_ssm_prompt_states_in_place(gdr, lengths):
 
 @pytest.mark.parametrize("lengths,H,P,G,N,states", [
     ([9000, 2500, 70], 3, 64, 1, 128, True), ([20000], 8, 64, 2, 64, True), ([5000, 0, 4999], 2, 80, 1, 96, True),
-    ([7000, 33], 4, 64, 1, 128, False)])
+    ([7000, 33], 4, 64, 1, 128, False), ([40, 9000, 0, 200, 5000, 33, 1, 6000, 129], 2, 64, 1, 64, True),
+    ([5] * 40 + [6000] + [130, 0] * 35 + [5000, 7], 1, 64, 1, 64, True)])
 def test_ssm_prompt_in_segments_in_place(gdr, lengths, H, P, G, N, states):
     # a split document's first segment takes its start state from the merge, whatever its last segment has
     # written over h0 by then: in place, out of place and without h0 but zeros, the same bits
