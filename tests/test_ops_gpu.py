@@ -707,6 +707,66 @@ def test_calls_are_captured_in_a_graph(gdr):
     assert torch.equal(state, eager)
 
 
+def test_calls_of_several_kernels_are_captured_in_a_graph(gdr):
+    # calls whose own kernels overlap by programmatic launches: a prompt in segments and in one, the convolution's and
+    # the norms' gradients; replayed on new inputs they give what the calls give
+    g, lengths, H, P, N, C = gen(15), [3000, 70], 2, 64, 128, 256
+    T = sum(lengths)
+    cu, cuh = pack(lengths)
+    xs, dt, A, B, Cm, D, bias = scan_inputs(g, T, H, P, 1, N, F32)
+    x, dy, w = randn(g, T, C, dtype=BF16), randn(g, T, C, dtype=BF16), randn(g, C, 4, dtype=BF16)
+    nw = (1 + 0.1 * randn(g, C)).to(BF16)
+
+    def calls():
+        out, ht = gdr.ssm_fwd(xs, dt, A, B, Cm, cu, cuh, D=D, dt_bias=bias)
+        conv = gdr.sconv_bwd(x, w, None, cu, cuh, dy)
+        norm = gdr.norm_bwd(x, weight=nw, post_weight=nw, residual=dy, dy=dy)
+        return [out, ht, conv["dx"], conv["dweight"], norm["dx"], norm["dresidual"], norm["dweight"], norm["dpost_weight"]]
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for seed in (16, 17):
+        h = gen(seed)
+        for t in (xs, dt, x, dy):
+            t.copy_(0.5 * randn(h, *t.shape))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(captured, calls())):
+            assert torch.equal(a, b), i
+    gdr.gdr_check_device()
+
+
+def test_calls_from_several_threads(gdr):
+    # the interpreter's lock is released during a call: widths that share kernels, each thread on a stream of its own
+    import threading
+    g = gen(18)
+    inputs = [[randn(g, 700, D, dtype=BF16) for _ in range(2)] + [(1 + 0.1 * randn(g, D)).to(BF16)] for D in (2047, 3000, 2048, 66)]
+    want = [gdr.norm_bwd(x, weight=w, post_weight=w, residual=r, dy=r) for x, r, w in inputs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            x, r, w = inputs[i]
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = gdr.norm_bwd(x, weight=w, post_weight=w, residual=r, dy=r)
+                stream.synchronize()
+                failed.extend((i, k) for k in got if not torch.equal(got[k], want[i][k]))
+        except Exception as e:  # a thread's exception would be lost
+            failed.append((i, repr(e)))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(inputs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
 def test_refusals(gdr):
     g = gen(11)
     x, w = randn(g, 10, 16, dtype=BF16), randn(g, 16, 4, dtype=BF16)
