@@ -192,11 +192,11 @@ __global__ void __launch_bounds__(256) k_ssm_step(SsmArgs a) {
 }
 
 // Whether the documents are short enough to go token by token.  The chunked
-// kernels work on 128 tokens whatever a document has; up to 32 tokens (a tile)
-// each the tokens one by one are faster: 64 documents of 64 heads x 128 x 64 states,
-// with h0 and ht, take 107, 186, 281, 397 us at 2, 16, 32, 48 tokens, in chunks
-// 256-260; of 8 heads x 64 x 64 17, 25, 33, 44 against 41; of 32 heads x 32 x 128 42, 88,
-// 145, 212 against 172-187.
+// kernels work on 128 tokens whatever a document has; documents of up to 32 tokens
+// (a tile) each are faster one by one, or nearly as fast at the end of that range: 64 of
+// 64 heads x 128 x 64 states, with h0 and ht, take 109, 189, 281, 398 us at 2, 16, 32, 48
+// tokens, in chunks 238-242; of 8 heads x 64 x 64 17, 25, 36, 48 against 36; of 32 heads x
+// 32 x 128 46, 91, 148, 212 against 175-187.
 bool short_documents(int N, const int32_t* cu) {
   for (int i = 0; i < N; ++i)
     if (cu[i + 1] - cu[i] > kSeqTok) return false;

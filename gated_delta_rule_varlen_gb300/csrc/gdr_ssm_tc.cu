@@ -1129,11 +1129,11 @@ bool ssm_tc_layout(const SsmArgs& a) {
 static int ssm_pairs(int H, int P, int G) { return H / G * ((P + 63) / 64) % 2 == 0; }
 
 // Whole documents while they keep the SMs evenly busy; else the segment length
-// with the least estimated time, in chunk steps of one walking block: kStart steps
-// (2.2 us) to start a block, kSum for a chunk of a summary (of one (head, 64 columns) or
-// of two).  All kernels one by one, one document of 32768 tokens of 64 heads: 409 us in 9 segments, 581 whole (64
-// blocks); 8192 tokens of 16 heads 67 us against 158; three documents of 65536 together of
-// 16 heads 218 against 394.
+// with the least estimated time, in chunk steps of one walking block (2.5 us): kStart
+// steps to start a block, kSum for a chunk of a summary (of one (head, 64 columns) or of
+// two; 0.7 and 0.48 give the same plans' times).  One document of 32768 tokens of 64 heads:
+// 442 us in 9 segments, 680 whole (64 blocks); 8192 tokens of 16 heads 57 us against 175;
+// three documents of 65536 together of 16 heads 230 against 464.
 SsmPlan ssm_tc_plan(int H, int P, int NS, int G, int N, const int32_t* cu) {
   const int pairs = ssm_pairs(H, P, G);
   const double kStart = 3.0, kSum = pairs ? 0.8 : 0.55;

@@ -6,7 +6,8 @@ type, shape and layout before the library is called, and a check that fails
 raises ``ValueError`` with nothing enqueued.
 
 Outputs and workspaces are allocated on the stream the call runs on: `stream`,
-or the current one.
+or the current one.  Inputs that belong to another stream are the caller's to order
+before the call and to keep until it has run (``Tensor.record_stream``).
 """
 from __future__ import annotations
 
@@ -114,7 +115,11 @@ def ssm_fwd(x, dt, A, B, C, cu_seqlens, cu_seqlens_host, D=None, dt_bias=None, s
     x bf16 [T, H, P]; dt bf16 or fp32 [T, H]; A (negative), D, dt_bias fp32
     [H]; B, C bf16 [T, G, NS], shared by the H / G heads of a group; h0 fp32 [N,
     H, NS, P] or None.  x, B, C and dt may be slices of wider rows.  Returns
-    (out bf16 [T, H, P], ht fp32 [N, H, NS, P] or None)."""
+    (out bf16 [T, H, P], ht fp32 [N, H, NS, P] or None).
+
+    P and NS go up to 256.  Chunks on the tensor cores need P and NS in multiples of
+    8, NS <= 128 and rows on 16-byte boundaries; other sizes go token by token, about
+    25 times slower on a long prompt."""
     if stream is not None:
         return _on(stream, _binding.ssm_fwd, x, dt, A, B, C, D, dt_bias, softplus, cu_seqlens,
                    _host(cu_seqlens_host), h0, out, ht, want_ht, scratch)
