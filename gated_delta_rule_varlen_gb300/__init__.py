@@ -10,8 +10,8 @@ is missing, every call raises.
 Entry points carry the C names (``kda_workspace_bytes``, ``kda_fwd``,
 ``kda_bwd``, ``gdn_workspace_bytes``, ``gdn_fwd``, ``gdn_bwd``,
 ``gdr_status_string``); the operators around the recurrence (``sconv_*``,
-``ssm_*``, ``kda_step``, ``gdn_step``, ``norm_*``) live in ``ops.py`` and are
-reached from here too.  Outputs and workspaces are allocated with torch when
+``ssm_*``, ``kda_step``, ``gdn_step``, ``norm_*``, ``lnorm_*``, ``rope_*``,
+``attn_*``) live in ``ops.py`` and are reached from here too.  Outputs and workspaces are allocated with torch when
 the caller does not pass them.
 """
 from __future__ import annotations
@@ -66,6 +66,13 @@ EXPORTED = (
     "norm_fwd",
     "norm_workspace_bytes",
     "norm_bwd",
+    "lnorm_fwd",
+    "lnorm_workspace_bytes",
+    "lnorm_bwd",
+    "rope_turn",
+    "attn_workspace_bytes",
+    "attn_fwd",
+    "attn_bwd",
 )
 
 _lock = threading.Lock()
@@ -121,6 +128,17 @@ _SIGS = {
                  ctypes.c_int),
     "norm_bwd": ([I32, I64, I32, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, F32, P, P, I32, F32, P, I64, I64, P,
                   I64, I64, P, P, P, P, P, P, SZ, P], ctypes.c_int),
+    "lnorm_workspace_bytes": ([I32, PSZ], ctypes.c_int),
+    "lnorm_fwd": ([I32, I64, I32, I32, P, I64, I64, P, I64, I64, F32, P, P, I32, F32, P, P, P], ctypes.c_int),
+    "lnorm_bwd": ([I32, I64, I32, I32, P, I64, I64, P, I64, I64, F32, P, I32, F32, P, I64, I64, P, I64, I64, P, P, P, P, P,
+                   SZ, P], ctypes.c_int),
+    "rope_turn": ([I32, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, I64, I32, I32, P, P, I32, P, I32, I32,
+                   F32, I32, P], ctypes.c_int),
+    "attn_workspace_bytes": ([I64, I64, I32, I32, I32, I32, P, P, I32, I32, PSZ, PSZ], ctypes.c_int),
+    "attn_fwd": ([P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, P, I32, I64, I64, I32, I32, I32, F32, I32, I32, P, P, P, SZ,
+                  P], ctypes.c_int),
+    "attn_bwd": ([P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P, P, P, P, I32, I64, I64, I32, I32, I32, F32,
+                  I32, I32, P, P, P, P, SZ, P], ctypes.c_int),
 }
 
 
@@ -424,7 +442,8 @@ def gdr_selftest_wait(limit_ns: int, stream=None):
 # The operators around the recurrence (torch is needed from here on; the host-side
 # functions above work without it).
 _OPS = ("sconv_workspace_bytes", "sconv_fwd", "sconv_bwd", "sconv_step", "ssm_workspace_bytes", "ssm_fwd", "ssm_step",
-        "kda_step", "gdn_step", "norm_workspace_bytes", "norm_fwd", "norm_bwd")
+        "kda_step", "gdn_step", "norm_workspace_bytes", "norm_fwd", "norm_bwd", "lnorm_workspace_bytes", "lnorm_fwd",
+        "lnorm_bwd", "rope_frequencies", "rope_fwd", "rope_bwd", "attn_workspace_bytes", "attn_fwd", "attn_bwd")
 
 
 def __getattr__(name):

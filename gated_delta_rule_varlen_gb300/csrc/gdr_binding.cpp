@@ -13,7 +13,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
+#include <memory>
 #include <stdexcept>
 #include <string>
 
@@ -437,6 +439,21 @@ struct RowPtr {
   const void* p = nullptr;
   int64_t s0 = 0, s1 = 0;
 };
+// Address and strides of a tensor shaped like x: [..., D] as [R0, R1, D] with dense rows.
+RowPtr row_ptr(const Call& c, const char* name, PyObject* o, const Tensor& x) {
+  if (o == Py_None) return {};
+  const Tensor& t = c.tensor(name, o);
+  const int64_t nd = t.dim(), D = x.size(x.dim() - 1);
+  if (t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type())
+    c.fail(std::string(name) + " is " + str(t.scalar_type()) + " " + str(t.sizes()) + ", expected " + str(x.scalar_type()) + " " + str(x.sizes()));
+  c.same_device(name, t);
+  if (t.stride(nd - 1) != 1 && D > 1) c.fail(std::string(name) + " must have dense rows");
+  if (nd == 3) return {t.data_ptr(), t.stride(0), t.stride(1)};
+  if (nd == 2) return {t.data_ptr(), t.stride(0), D};
+  if (nd > 3 && !t.is_contiguous())
+    c.fail(std::string(name) + " has " + std::to_string(nd) + " dimensions and must be contiguous");
+  return {t.data_ptr(), nd == 1 ? D : D * t.size(nd - 2), D};
+}
 struct Norm {
   const Tensor& x;
   ScalarType type;
@@ -446,21 +463,7 @@ struct Norm {
   bool has_weight, has_post, has_gate, has_res;
   const void *w, *wp;
   float alpha, eps;
-  // Address and strides of a tensor shaped like x: [..., D] as [R0, R1, D] with dense rows.
-  RowPtr rows(const Call& c, const char* name, PyObject* o) const {
-    if (o == Py_None) return {};
-    const Tensor& t = c.tensor(name, o);
-    if (t.sizes() != x.sizes() || t.scalar_type() != type)
-      c.fail(std::string(name) + " is " + str(t.scalar_type()) + " " + str(t.sizes()) + ", expected " + str(type) + " " + str(x.sizes()));
-    c.same_device(name, t);
-    const int64_t nd = t.dim();
-    if (t.stride(nd - 1) != 1 && D > 1) c.fail(std::string(name) + " must have dense rows");
-    if (nd == 3) return {t.data_ptr(), t.stride(0), t.stride(1)};
-    if (nd == 2) return {t.data_ptr(), t.stride(0), D};
-    if (nd > 3 && !t.is_contiguous())
-      c.fail(std::string(name) + " has " + std::to_string(nd) + " dimensions and must be contiguous");
-    return {t.data_ptr(), nd == 1 ? D : D * t.size(nd - 2), D};
-  }
+  RowPtr rows(const Call& c, const char* name, PyObject* o) const { return row_ptr(c, name, o, x); }
   Norm(Call& c, PyObject* const* a) : x(c.tensor("x", a[0])) {  // x weight post_weight gate act residual res_scale eps
     c.on(x);
     type = x.scalar_type();
@@ -539,6 +542,250 @@ PyObject* norm_bwd_(PyObject* const* a) {  // ... dh dy scratch grads
   return g.release();
 }
 
+// --- layer norm in front of a block ------------------------------------------------------
+struct LayerNorm {
+  const Tensor& x;
+  ScalarType type;
+  int dt, wdt, R1;
+  int64_t R0, D;
+  RowPtr xr, res;
+  bool has_res;
+  const void *w, *b;
+  float alpha, eps;
+  LayerNorm(Call& c, PyObject* const* a) : x(c.tensor("x", a[0])) {  // x weight bias residual res_scale eps
+    c.on(x);
+    type = x.scalar_type();
+    dt = code_of(type);
+    if (dt < 0) c.fail("x is " + str(type) + "; bfloat16, float16 and float32 are supported");
+    const int64_t nd = x.dim();
+    if (nd < 1 || x.size(nd - 1) < 1 || x.size(nd - 1) > GDR_NORM_MAX_D)
+      c.fail("x has shape " + str(x.sizes()) + "; rows of 1 to 16384 elements are supported");
+    D = x.size(nd - 1);
+    const int64_t inner = nd >= 3 ? x.size(nd - 2) : 1;
+    R0 = inner ? x.numel() / (inner * D) : 0;
+    R1 = c.size("rows of the inner dimension", inner ? inner : 1);
+    const ScalarType wtype = a[1] != Py_None   ? c.tensor("weight", a[1]).scalar_type()
+                             : a[2] != Py_None ? c.tensor("bias", a[2]).scalar_type()
+                                               : type;
+    if (wtype != type && wtype != ScalarType::Float) c.fail("weights are " + str(wtype) + ", expected " + str(type) + " or float32");
+    wdt = code_of(wtype);
+    xr = row_ptr(c, "x", a[0], x);
+    res = row_ptr(c, "residual", a[3], x);
+    has_res = a[3] != Py_None;
+    w = c.dense("weight", a[1], wtype, {D});
+    b = c.dense("bias", a[2], wtype, {D});
+    alpha = (float)number(a[4]);
+    eps = (float)number(a[5]);
+  }
+};
+
+PyObject* lnorm_fwd_(PyObject* const* a) {  // ... h y
+  Call c{"lnorm_fwd"};
+  const LayerNorm v(c, a);
+  void *hp = nullptr, *yp;
+  Tensor h;
+  if (a[6] != Py_None || v.has_res) h = c.output("h", a[6], v.x.sizes(), v.type, &hp);
+  const Tensor y = c.output("y", a[7], v.x.sizes(), v.type, &yp);
+  c.run([&] {
+    return lnorm_fwd(v.dt, v.R0, v.R1, (int32_t)v.D, v.xr.p, v.xr.s0, v.xr.s1, v.res.p, v.res.s0, v.res.s1, v.alpha, v.w, v.b,
+                     v.wdt, v.eps, hp, yp, c.stream);
+  });
+  return two(h, y);
+}
+
+PyObject* lnorm_bwd_(PyObject* const* a) {  // ... dh dy scratch grads
+  Call c{"lnorm_bwd"};
+  const LayerNorm v(c, a);
+  if (a[7] == Py_None) c.fail("dy is needed");
+  const RowPtr dh = row_ptr(c, "dh", a[6], v.x), dy = row_ptr(c, "dy", a[7], v.x);
+  // where res_scale = 1, dx and dresidual are one tensor
+  const bool same = v.has_res && v.alpha == 1.f && (a[9] == Py_None || PyDict_Size(a[9]) == 0);
+  Grads g(a[9]);
+  void *dres = nullptr, *dx = g.tensor(c, "dx", v.x.sizes(), v.type);
+  float *dw = nullptr, *db = nullptr;
+  if (same) g.set("dresidual", Py_NewRef(g.get("dx")));
+  else if (v.has_res || g.get("dresidual")) dres = g.tensor(c, "dresidual", v.x.sizes(), v.type);
+  if (v.w || g.get("dweight")) dw = static_cast<float*>(g.tensor(c, "dweight", {v.D}, ScalarType::Float));
+  if (v.b || g.get("dbias")) db = static_cast<float*>(g.tensor(c, "dbias", {v.D}, ScalarType::Float));
+  size_t need = 0, bytes = 0;
+  c.status(lnorm_workspace_bytes((int32_t)v.D, &need));
+  void* sp;
+  const Tensor scratch = c.scratch(a[8], need, &sp, &bytes);
+  c.run([&] {
+    return lnorm_bwd(v.dt, v.R0, v.R1, (int32_t)v.D, v.xr.p, v.xr.s0, v.xr.s1, v.res.p, v.res.s0, v.res.s1, v.alpha, v.w, v.wdt,
+                     v.eps, dh.p, dh.s0, dh.s1, dy.p, dy.s0, dy.s1, dx, dres, dw, db, sp, bytes, c.stream);
+  });
+  return g.release();
+}
+
+// --- [tokens, heads, dim] with dense heads ---------------------------------------------------
+struct Heads {
+  void* p = nullptr;
+  int64_t T = 0, H = 0, D = 0, s0 = 0, s1 = 0;
+  Heads() = default;
+  Heads(const Call& c, const char* name, const Tensor& t, ScalarType type) {
+    if (t.dim() != 3) c.fail(std::string(name) + " has shape " + str(t.sizes()) + ", expected [tokens, heads, dim]");
+    if (t.scalar_type() != type) c.fail(std::string(name) + " is " + str(t.scalar_type()) + ", expected " + str(type));
+    c.same_device(name, t);
+    T = t.size(0);
+    H = t.size(1);
+    D = t.size(2);
+    if (D > 1 && t.stride(2) != 1) c.fail(std::string(name) + " must have dense heads");
+    s1 = H > 1 ? t.stride(1) : D;
+    s0 = T > 1 ? t.stride(0) : H * D;
+    p = t.data_ptr();
+  }
+  const gdr_bf16* bf() const { return static_cast<const gdr_bf16*>(p); }
+};
+
+// --- rotary positions --------------------------------------------------------------------
+PyObject* rope_(PyObject* const* a) {  // q k freqs positions cu interleaved amplitude q_out k_out inverse
+  const bool back = truth(a[9]);
+  Call c{back ? "rope_bwd" : "rope_fwd"};
+  if (a[0] == Py_None && a[1] == Py_None) c.fail("one of q and k is needed");
+  const Tensor& first = c.tensor(a[0] != Py_None ? "q" : "k", a[a[0] != Py_None ? 0 : 1]);
+  c.on(first);
+  const ScalarType type = first.scalar_type();
+  const int dt = code_of(type);
+  if (dt < 0) c.fail("rows are " + str(type) + "; bfloat16, float16 and float32 are supported");
+  Heads in[2], out[2];
+  Tensor res[2];
+  const char* names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
+  int64_t T = 0, D = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (a[i] == Py_None) {
+      if (a[7 + i] != Py_None) c.fail(std::string(names[i][1]) + " without " + names[i][0]);
+      continue;
+    }
+    const Tensor& t = c.tensor(names[i][0], a[i]);
+    in[i] = Heads(c, names[i][0], t, type);
+    if (i == 1 && a[0] != Py_None && (in[1].T != T || in[1].D != D))
+      c.fail("k has shape " + str(t.sizes()) + ", expected [" + std::to_string(T) + ", heads, " + std::to_string(D) + "]");
+    T = in[i].T;
+    D = in[i].D;
+    if (a[7 + i] == Py_None) {
+      res[i] = c.empty(t.sizes(), type);
+    } else {
+      res[i] = c.tensor(names[i][1], a[7 + i]);
+      if (res[i].sizes() != t.sizes()) c.fail(std::string(names[i][1]) + " has shape " + str(res[i].sizes()) + ", expected " + str(t.sizes()));
+    }
+    out[i] = Heads(c, names[i][1], res[i], type);
+  }
+  const Tensor& freqs = c.tensor("freqs", a[2]);
+  const int64_t R = freqs.dim() == 1 ? 2 * freqs.size(0) : -1;
+  if (R < 0 || R > D) c.fail("freqs has shape " + str(freqs.sizes()) + ", expected [pairs] of heads of " + std::to_string(D));
+  const float* fp = static_cast<const float*>(c.dense("freqs", freqs, ScalarType::Float, {R / 2}));
+  const void* pos = nullptr;
+  bool wide = false;
+  const int32_t* cu = nullptr;
+  int32_t N = 0;
+  if (a[3] != Py_None) {
+    const Tensor& p = c.tensor("positions", a[3]);
+    wide = p.scalar_type() == ScalarType::Long;
+    pos = c.dense("positions", p, wide ? ScalarType::Long : ScalarType::Int, {T});
+  } else if (a[4] != Py_None) {
+    const Tensor& u = c.tensor("cu_seqlens", a[4]);
+    if (u.dim() != 1 || u.size(0) < 1) c.fail("cu_seqlens has shape " + str(u.sizes()) + ", expected [documents + 1]");
+    N = c.size("documents", u.size(0) - 1);
+    cu = static_cast<const int32_t*>(c.dense("cu_seqlens", u, ScalarType::Int, {u.size(0)}));
+  } else {
+    c.fail("one of positions and cu_seqlens is needed");
+  }
+  const bool inter = truth(a[5]);
+  const float amp = (float)number(a[6]);
+  const int32_t HQ = c.size("heads", in[0].H), HK = c.size("heads", in[1].H), d = c.size("head dim", D);
+  c.run([&] {
+    return rope_turn(dt, in[0].p, in[0].s0, in[0].s1, HQ, out[0].p, out[0].s0, out[0].s1, in[1].p, in[1].s0, in[1].s1, HK, out[1].p,
+                     out[1].s0, out[1].s1, T, d, (int32_t)R, fp, pos, wide, cu, N, inter, amp, back, c.stream);
+  });
+  return two(res[0], res[1]);
+}
+
+// --- softmax attention ---------------------------------------------------------------------
+struct Attention {
+  Heads q, k, v;
+  Pack pack;
+  std::unique_ptr<Pack> keys;
+  float scale;
+  bool causal;
+  int32_t window;
+  Attention(Call& c, PyObject* const* a)  // q k v cu cuh cu_keys cu_keys_host scale causal window
+      : q((c.on(c.tensor("q", a[0])), Heads(c, "q", c.tensor("q", a[0]), ScalarType::BFloat16))),
+        k(c, "k", c.tensor("k", a[1]), ScalarType::BFloat16), v(c, "v", c.tensor("v", a[2]), ScalarType::BFloat16),
+        pack(c, a[3], a[4]) {
+    if (k.T != v.T || k.H != v.H || k.D != v.D || k.D != q.D)
+      c.fail("q has shape " + str(c.tensor("q", a[0]).sizes()) + ", k " + str(c.tensor("k", a[1]).sizes()) + " and v " +
+             str(c.tensor("v", a[2]).sizes()));
+    if (k.H < 1 || q.H < 1 || q.H % k.H) c.fail(std::to_string(q.H) + " heads do not share " + std::to_string(k.H) + " key heads evenly");
+    if (q.D < 1 || q.D > GDR_ATTN_MAX_D) c.fail("head dim " + std::to_string(q.D) + "; 1 to 256 are supported");
+    c.size("heads", q.H);
+    if ((a[5] == Py_None) != (a[6] == Py_None)) c.fail("cu_keys and cu_keys_host come together");
+    if (a[5] != Py_None) {
+      keys = std::make_unique<Pack>(c, a[5], a[6]);
+      if (keys->n != pack.n) c.fail("cu_keys has " + std::to_string(keys->n) + " documents, cu_seqlens " + std::to_string(pack.n));
+    } else if (k.T != q.T) {
+      c.fail("k has " + std::to_string(k.T) + " tokens and q " + std::to_string(q.T) + "; other keys need cu_keys");
+    }
+    scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)q.D)) : (float)number(a[7]);
+    if (!(scale > 0) || !std::isfinite(scale)) c.fail("scale must be positive and finite");
+    causal = truth(a[8]);
+    const long w = PyLong_AsLong(a[9]);
+    if (w == -1 && PyErr_Occurred()) throw PyError();
+    if (w < 0) c.fail("window must not be negative");
+    if (w > 0 && !causal) c.fail("a window needs causal");
+    window = w > INT32_MAX ? 0 : (int32_t)w;  // (sees everything)
+  }
+  const int32_t* cuk() const { return keys ? keys->cu : nullptr; }
+  const int32_t* cuk_host() const { return keys ? keys->host : nullptr; }
+  void workspace(const Call& c, size_t* fwd, size_t* bwd) const {
+    c.status(attn_workspace_bytes(q.T, k.T, (int32_t)q.H, (int32_t)k.H, (int32_t)q.D, pack.n, pack.host, cuk_host(), causal, window,
+                                  fwd, bwd));
+  }
+};
+
+PyObject* attn_fwd_(PyObject* const* a) {  // ... out lse scratch
+  Call c{"attn_fwd"};
+  const Attention v(c, a);
+  size_t need = 0, bytes = 0;
+  v.workspace(c, &need, nullptr);
+  void *op, *lp, *sp = nullptr;
+  const Tensor out = c.output("out", a[10], {v.q.T, v.q.H, v.q.D}, ScalarType::BFloat16, &op);
+  const Tensor lse = c.output("lse", a[11], {v.q.H, v.q.T}, ScalarType::Float, &lp);
+  const Tensor scratch = a[12] == Py_None && need == 0 ? Tensor() : c.scratch(a[12], need, &sp, &bytes);
+  c.run([&] {
+    return attn_fwd(v.q.bf(), v.q.s0, v.q.s1, v.k.bf(), v.k.s0, v.k.s1, v.v.bf(), v.v.s0, v.v.s1, v.pack.cu, v.pack.host, v.cuk(),
+                    v.cuk_host(), v.pack.n, v.q.T, v.k.T, (int32_t)v.q.H, (int32_t)v.k.H, (int32_t)v.q.D, v.scale, v.causal,
+                    v.window, static_cast<gdr_bf16*>(op), static_cast<float*>(lp), sp, bytes, c.stream);
+  });
+  return two(out, lse);
+}
+
+PyObject* attn_bwd_(PyObject* const* a) {  // ... out lse dout scratch grads
+  Call c{"attn_bwd"};
+  const Attention v(c, a);
+  const auto bf = ScalarType::BFloat16;
+  const int64_t qs[3] = {v.q.T, v.q.H, v.q.D}, ks[3] = {v.k.T, v.k.H, v.k.D};
+  const auto* out = static_cast<const gdr_bf16*>(c.dense("out", c.tensor("out", a[10]), bf, qs));
+  const auto* lse = static_cast<const float*>(c.dense("lse", c.tensor("lse", a[11]), ScalarType::Float, {v.q.H, v.q.T}));
+  const Tensor& dt = c.tensor("dout", a[12]);
+  const Heads dout(c, "dout", dt, bf);
+  if (dt.sizes() != Shape(qs, 3)) c.fail("dout has shape " + str(dt.sizes()) + ", expected " + str(Shape(qs, 3)));
+  size_t need = 0, bytes = 0;
+  v.workspace(c, nullptr, &need);
+  Grads g(a[14]);
+  auto* dq = static_cast<gdr_bf16*>(g.tensor(c, "dq", qs, bf));
+  auto* dk = static_cast<gdr_bf16*>(g.tensor(c, "dk", ks, bf));
+  auto* dv = static_cast<gdr_bf16*>(g.tensor(c, "dv", ks, bf));
+  void* sp;
+  const Tensor scratch = c.scratch(a[13], need, &sp, &bytes);
+  c.run([&] {
+    return attn_bwd(v.q.bf(), v.q.s0, v.q.s1, v.k.bf(), v.k.s0, v.k.s1, v.v.bf(), v.v.s0, v.v.s1, out, lse, dout.bf(), dout.s0, dout.s1,
+                    v.pack.cu, v.pack.host, v.cuk(), v.cuk_host(), v.pack.n, v.q.T, v.k.T, (int32_t)v.q.H, (int32_t)v.k.H,
+                    (int32_t)v.q.D, v.scale, v.causal, v.window, dq, dk, dv, sp, bytes, c.stream);
+  });
+  return g.release();
+}
+
 // --- the module --------------------------------------------------------------------------
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -571,7 +818,8 @@ PyMODINIT_FUNC PyInit__gdr_ops() {
       {"set_check", set_check, METH_O, nullptr},
       GDR_ENTRY(sconv_fwd, 10), GDR_ENTRY(sconv_bwd, 12), GDR_ENTRY(sconv_step, 7), GDR_ENTRY(ssm_fwd, 15),
       GDR_ENTRY(ssm_step, 11), GDR_ENTRY(kda_step, 10), GDR_ENTRY(gdn_step, 10), GDR_ENTRY(norm_fwd, 10),
-      GDR_ENTRY(norm_bwd, 12), {nullptr, nullptr, 0, nullptr}};
+      GDR_ENTRY(norm_bwd, 12), GDR_ENTRY(lnorm_fwd, 8), GDR_ENTRY(lnorm_bwd, 10), GDR_ENTRY(rope, 10), GDR_ENTRY(attn_fwd, 13),
+      GDR_ENTRY(attn_bwd, 15), {nullptr, nullptr, 0, nullptr}};
 #undef GDR_ENTRY
   static PyModuleDef def = {PyModuleDef_HEAD_INIT, "_gdr_ops", nullptr, -1, table, nullptr, nullptr, nullptr, nullptr};
   return PyModule_Create(&def);

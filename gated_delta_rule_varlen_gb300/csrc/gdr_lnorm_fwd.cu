@@ -1,0 +1,119 @@
+// gdr_lnorm_fwd.cu -- forward of the layer norm in front of a block (gdr_lnorm.cuh).
+#include "gdr_lnorm.cuh"
+
+namespace gdr {
+namespace {
+
+// Bound by HBM: each input read and each output written once.
+template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
+__global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {
+  using W = RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 2>;
+  constexpr int P = W::P;
+  __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
+  extern __shared__ __align__(16) unsigned char lnorm_smem[];
+  W w(a, lnorm_smem);
+  const float inv_d = 1.f / (float)a.D;
+  typename W::Weight wk, bk;
+  w.keep(wk, a.w);
+  w.keep(bk, a.w_post);
+  w.in.add(0, a.x);
+  if (a.res.p) w.in.add(1, a.res);
+  if constexpr (W::AHEAD) {
+#pragma unroll
+    for (int i = 0; i < W::DEPTH; ++i) w.ask(i);
+  }
+  const uint64_t alpha = both(a.alpha);
+  int slot = 0;
+#pragma unroll 1
+  for (int64_t r = w.g.first; r - w.g.grp < a.rows; r += w.g.step) {
+    if constexpr (W::AHEAD) cp_async_wait<W::DEPTH - 1>();
+    else w.ask(0);
+    auto on = [&](int i) { return r < a.rows && w.col(i) < a.D; };
+    uint64_t h[NV][P], s2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      zero_pairs<V>(h[i]);
+      if (on(i)) {
+        w.get(slot, 0, i, h[i]);
+        if (a.res.p) {
+          uint64_t f[P];
+          w.get(slot, 1, i, f);
+#pragma unroll
+          for (int q = 0; q < P; ++q) h[i][q] = fma2(alpha, h[i][q], f[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < P; ++q) s2 = add2(s2, h[i][q]);
+      }
+    }
+    w.put(a.h, r, h);
+    if (a.y) {
+      float s[1] = {sum_of(s2)};
+      w.g.sum(s, sm[0]);
+      const float mean = s[0] * inv_d;
+      s2 = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          w.sub(h[i], i, mean);
+#pragma unroll
+          for (int q = 0; q < P; ++q) s2 = fma2(h[i][q], h[i][q], s2);
+        }
+      s[0] = sum_of(s2);
+      w.g.sum(s, sm[1]);
+      const uint64_t rr = both(rsqrtf(fmaf(s[0], inv_d, a.eps)));
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (on(i)) {
+          uint64_t f[P], b[P];
+          if (a.w) {
+            w.weight(wk, i, f);
+#pragma unroll
+            for (int q = 0; q < P; ++q) f[q] = mul2(rr, f[q]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < P; ++q) f[q] = rr;
+          }
+          if (a.w_post) {
+            w.weight(bk, i, b);
+#pragma unroll
+            for (int q = 0; q < P; ++q) h[i][q] = fma2(h[i][q], f[q], b[q]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < P; ++q) h[i][q] = mul2(h[i][q], f[q]);
+          }
+        }
+      w.put(a.y, r, h);
+    }
+    if constexpr (W::AHEAD) {  // (what was read from the slot has been used)
+      w.ask(slot);
+      slot = slot == W::DEPTH - 1 ? 0 : slot + 1;
+    }
+  }
+}
+
+template <typename T>
+struct Launch {
+  const NormArgs& a;
+  const NormShape& s;
+  int* parts;
+  cudaStream_t st;
+  template <int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
+  cudaError_t run() const {
+    static Held held;
+    return norm_launch(k_lnorm_fwd<T, V, TPR, NV, CLUSTER, SHIFT>, a, s, RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 2>::BYTES, 32,
+                       held, parts, st);
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_lnorm_fwd(const NormArgs& a, int dtype, const NormShape& s, cudaStream_t st) {
+  int parts = 0;
+  switch (dtype) {
+    case GDR_DTYPE_BF16: return dispatch_lnorm<8>(s, Launch<__nv_bfloat16>{a, s, &parts, st});
+    case GDR_DTYPE_F16: return dispatch_lnorm<8>(s, Launch<__half>{a, s, &parts, st});
+    default: return dispatch_lnorm<4>(s, Launch<float>{a, s, &parts, st});
+  }
+}
+
+}  // namespace gdr

@@ -51,8 +51,32 @@ cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const NormShape& s, cu
 // *parts: how many partial rows of weight gradients it left
 cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* parts, cudaStream_t st);
 
+// The partial rows added in a fixed order: [parts][2][D] to the first's and the second's sums (or null).
+cudaError_t launch_norm_wgrad(const float* part, int parts, int D, float* dw, float* dw2, cudaStream_t st);
+
+// Rows of D elements: how they can be read.
+struct RowLayout {
+  int64_t R0;
+  int R1, D, V;
+  bool pieces = true, dense = true;  // in pieces of V = 16 bytes; one after another from 16 bytes on
+  void input(const RowTensor& t) {
+    if (!t.p) return;
+    const bool on16 = ((uintptr_t)t.p & 15) == 0;
+    pieces = pieces && on16 && t.s0 % V == 0 && t.s1 % V == 0;
+    dense = dense && on16 && (R1 == 1 || t.s1 == D) && (R0 == 1 || t.s0 == (int64_t)R1 * D);
+  }
+  void output(const void* p) {
+    pieces = pieces && ((uintptr_t)p & 15) == 0;
+    dense = dense && ((uintptr_t)p & 15) == 0;
+  }
+};
+
+NormShape norm_shape(const RowLayout& l);
+
 // Most blocks of an SM that a backward on rows of D elements is launched with.
 constexpr int norm_bwd_blocks(int D) { return D <= 2048 ? 8 : 3; }
+// Most row groups of a backward: the partial rows its workspace has to hold.
+constexpr int max_norm_parts(int D) { return 152 * norm_bwd_blocks(D); }
 
 // What a device holds of a kernel at a time, kept from call to call (and from thread to
 // thread): blocks an SM, or clusters by their size.  0: not known yet.

@@ -409,6 +409,10 @@ cudaError_t launch_t(const NormArgs& a, const NormShape& s, int* parts, cudaStre
 
 }  // namespace
 
+cudaError_t launch_norm_wgrad(const float* part, int parts, int D, float* dw, float* dw2, cudaStream_t st) {
+  return launch_early(k_norm_wgrad, dim3((D + 31) / 32, 2), 1024, 0, st, part, parts, D, dw, dw2);
+}
+
 cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, int* parts, cudaStream_t st) {
   switch (dtype) {
     case GDR_DTYPE_BF16: return launch_t<__nv_bfloat16, 8>(a, s, parts, st);
@@ -416,28 +420,6 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const NormShape& s, in
     default: return launch_t<float, 4>(a, s, parts, st);
   }
 }
-
-namespace {
-
-// Most row groups of a backward: the partial rows its workspace has to hold.
-int max_norm_parts(int D) { return 152 * norm_bwd_blocks(D); }
-
-// Rows of D elements: how they can be read.
-struct RowLayout {
-  int64_t R0;
-  int R1, D, V;
-  bool pieces = true, dense = true;  // in pieces of V = 16 bytes; one after another from 16 bytes on
-  void input(const RowTensor& t) {
-    if (!t.p) return;
-    const bool on16 = ((uintptr_t)t.p & 15) == 0;
-    pieces = pieces && on16 && t.s0 % V == 0 && t.s1 % V == 0;
-    dense = dense && on16 && (R1 == 1 || t.s1 == D) && (R0 == 1 || t.s0 == (int64_t)R1 * D);
-  }
-  void output(const void* p) {
-    pieces = pieces && ((uintptr_t)p & 15) == 0;
-    dense = dense && ((uintptr_t)p & 15) == 0;
-  }
-};
 
 // The threads that hold a row: in pieces of 16 bytes where all rows start on them,
 // or, rows of any length that lie one after another, shifted to the 16 bytes each
@@ -468,6 +450,8 @@ NormShape norm_shape(const RowLayout& l) {
   if (D <= 256) return {1, 32, 8, 0, false};
   return {1, 128, 8, (D + 1023) / 1024, false};
 }
+
+namespace {
 
 gdr_status norm_check(int dtype, int wdtype, int64_t R0, int32_t R1, int32_t D, const void* x, const void* residual,
                       const void* post_weight, const void* weight, int act) {
@@ -572,8 +556,7 @@ gdr_status norm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x,
   }
   if (dweight || dpost_weight) {
     ProfScope ps("norm_wgrad", stream);
-    if (launch_early(k_norm_wgrad, dim3((D + 31) / 32, 2), 1024, 0, stream, a.part, parts, D, dweight, dpost_weight) != cudaSuccess)
-      return GDR_CUDA_ERROR;
+    if (launch_norm_wgrad(a.part, parts, D, dweight, dpost_weight, stream) != cudaSuccess) return GDR_CUDA_ERROR;
   }
   return GDR_OK;
 }

@@ -1,0 +1,251 @@
+// gdr_rope.cu -- rotary positions: the first R elements of every head of q and k in
+// pairs (a, b), turned by the token's position times the pair's frequency,
+//   (a, b) -> amplitude (a cos t - b sin t, b cos t + a sin t),  t = position frequency,
+// the rest copied.  Pairs are elements (i, i + R / 2), or (2 i, 2 i + 1) interleaved.
+// The gradient of the turned rows turns the other way.
+//
+// The angle keeps its accuracy at far positions without 64-bit floating point: the
+// frequency in turns a token is a 64-bit binary fraction, whose product with the
+// position, modulo 2^64, is the angle's fraction of a turn (off by position 2^-65 turns
+// beside the frequency's own rounding), and the top 32 bits of it become sine and cosine.
+//
+// Bound by HBM: each element read once and written once.  A thread keeps the sines and
+// cosines of its columns over several heads of a token.
+#include <algorithm>
+
+#include "gdr_ops.cuh"
+#include "gdr_runtime.h"
+
+namespace gdr {
+namespace {
+
+struct RopeRows {
+  const void* x;
+  int64_t s0, s1;  // element strides of a token and of a head
+  void* y;
+  int64_t y0, y1;
+};
+struct RopeArgs {
+  RopeRows q, k;
+  int HQ, H;           // query heads; with the key heads
+  int D, R;
+  int64_t T;
+  const void* pos;     // or null: counted from each document's start
+  int pos64;
+  const int* cu;
+  int N;
+  const float* freq;   // [R / 2]
+  float amp;
+  int back;
+  int units, turned;   // pieces of a head: all, those that turn
+  int per_thread;      // heads a thread goes through
+};
+
+constexpr int THREADS = 256;
+
+// 2^64 of the fraction of a turn that frequency f (radians) advances: f = m 2^(e - 150)
+// times 1 / (2 pi) = kTurn 2^-66, in integers (64-bit floating point has 1/64 of their rate).
+constexpr unsigned long long kTurn = 0xa2f9836e4e44152aull;
+__device__ __forceinline__ uint64_t turns_of(float f) {
+  const uint32_t bits = __float_as_uint(f) & 0x7fffffffu, ex = bits >> 23;
+  const uint64_t m = ex ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const uint64_t lo = m * kTurn, hi = __umul64hi(m, kTurn);
+  const int sh = 152 - (ex ? (int)ex : 1);  // product 2^-sh
+  uint64_t u;
+  if (sh >= 64) u = sh < 128 ? hi >> (sh - 64) : 0;
+  else if (sh > 0) u = lo >> sh | hi << (64 - sh);
+  else u = sh > -64 ? lo << -sh : 0;
+  return f < 0.f ? 0 - u : u;
+}
+__device__ __forceinline__ void angle(uint64_t turns, uint64_t pos, float amp, bool back, float& c, float& s) {
+  const int top = (int)((turns * pos) >> 32);  // [-1/2, 1/2) turns
+  sincospif((float)top * 4.656612873077393e-10f, &s, &c);
+  c *= amp;
+  s *= back ? -amp : amp;
+}
+
+// A thread's unit of a head: V elements from each half of the turned part (interleaved:
+// V elements of V / 2 pairs), or V elements to copy.  LOOSE: rows on no common boundary,
+// element by element.
+template <typename T, int V, bool LOOSE>
+__device__ __forceinline__ Vec<T, V> load_piece(const T* p, int n) {
+  if constexpr (!LOOSE) return vload<T, V>(p);
+  Vec<T, V> v{};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) v.e[i] = p[i];
+  return v;
+}
+template <typename T, int V, bool LOOSE>
+__device__ __forceinline__ void store_piece(T* p, const Vec<T, V>& v, int n) {
+  if constexpr (!LOOSE) {
+    *reinterpret_cast<Vec<T, V>*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = v.e[i];
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> packed(const float (&f)[V]) {
+  Vec<T, V> v;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v.e[i] = from_f<T>(f[i]);
+  return v;
+}
+
+template <typename T, int V, bool INTER, bool LOOSE>
+__global__ void __launch_bounds__(THREADS) k_rope(const __grid_constant__ RopeArgs a) {
+  const int64_t item = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+  const int64_t t = item / a.units;
+  if (t >= a.T) return;
+  const int u = (int)(item % a.units), h0 = blockIdx.y * a.per_thread, h1 = min(a.H, h0 + a.per_thread);
+  const bool turn = u < a.turned;
+  constexpr int PAIRS = INTER ? V / 2 : V;
+  const int c0 = turn ? u * V : a.R + (u - a.turned) * V;
+  const int n = a.D - c0;  // (elements up to the head's end)
+  float cs[PAIRS], sn[PAIRS];
+  if (turn) {
+    uint64_t pos;
+    if (!a.pos) pos = (uint64_t)(t - a.cu[doc_of(a.cu, a.N, (int)t)]);
+    else if (a.pos64) pos = (uint64_t)static_cast<const int64_t*>(a.pos)[t];
+    else pos = (uint64_t)(int64_t)static_cast<const int*>(a.pos)[t];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+      angle(turns_of(__ldg(a.freq + (INTER ? c0 / 2 : c0) + i)), pos, a.amp, a.back, cs[i], sn[i]);
+  }
+  const bool two = turn && !INTER;
+  auto at = [&](int h, const T*& x, T*& y) {
+    const bool isq = h < a.HQ;
+    const RopeRows& r = isq ? a.q : a.k;
+    const int hh = isq ? h : h - a.HQ;
+    x = static_cast<const T*>(r.x) + t * r.s0 + hh * r.s1 + c0;
+    y = static_cast<T*>(r.y) + t * r.y0 + hh * r.y1 + c0;
+  };
+  constexpr int U = 4;  // heads asked for together
+  for (int h = h0; h < h1; h += U) {
+    Vec<T, V> lo[U], hi[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (h + j < h1) {
+        const T* x;
+        T* y;
+        at(h + j, x, y);
+        lo[j] = load_piece<T, V, LOOSE>(x, n);
+        if (two) hi[j] = load_piece<T, V, LOOSE>(x + a.R / 2, V);
+      }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (h + j < h1) {
+        const T* x;
+        T* y;
+        at(h + j, x, y);
+        if (!turn) {
+          store_piece<T, V, LOOSE>(y, lo[j], n);
+        } else if constexpr (INTER) {
+          float f[V];
+          vunpack<T, V>(lo[j], f);
+#pragma unroll
+          for (int i = 0; i < PAIRS; ++i) {
+            const float p = f[2 * i], q = f[2 * i + 1];
+            f[2 * i] = p * cs[i] - q * sn[i];
+            f[2 * i + 1] = q * cs[i] + p * sn[i];
+          }
+          store_piece<T, V, LOOSE>(y, packed<T, V>(f), V);
+        } else {
+          float f[V], g[V];
+          vunpack<T, V>(lo[j], f);
+          vunpack<T, V>(hi[j], g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float p = f[i], q = g[i];
+            f[i] = p * cs[i] - q * sn[i];
+            g[i] = q * cs[i] + p * sn[i];
+          }
+          store_piece<T, V, LOOSE>(y, packed<T, V>(f), V);
+          store_piece<T, V, LOOSE>(y + a.R / 2, packed<T, V>(g), V);
+        }
+      }
+  }
+}
+
+// The widest pieces that every row allows: up to 16 bytes; 0: pairs side by side on no
+// boundary of a pair.
+int piece_of(const RopeArgs& a, int elem, bool inter) {
+  for (int v = 16 / elem; v > 1; v /= 2) {
+    bool ok = (inter ? a.R : a.R / 2) % v == 0 && (a.D - a.R) % v == 0;
+    for (const RopeRows* r : {&a.q, &a.k}) {
+      if (r == &a.k && a.H == a.HQ) continue;
+      const uintptr_t p = (uintptr_t)r->x | (uintptr_t)r->y;
+      ok = ok && p % (v * elem) == 0 && r->s0 % v == 0 && r->s1 % v == 0 && r->y0 % v == 0 && r->y1 % v == 0;
+    }
+    if (ok) return v;
+  }
+  return inter ? 0 : 1;
+}
+
+template <typename T, int V, bool INTER, bool LOOSE = false>
+cudaError_t launch(RopeArgs a, cudaStream_t st) {
+  a.turned = (INTER ? a.R : a.R / 2) / V;
+  a.units = a.turned + (a.D - a.R + V - 1) / V;
+  // Heads a thread: all of them share the sines, fewer where that leaves SMs without work.
+  const int64_t threads = a.T * a.units, room = 152ll * 2048;
+  int per = a.H;
+  while (per > 4 && threads * ((a.H + per - 1) / per) < 2 * room) per = (per + 1) / 2;
+  per = std::max((per + 3) / 4 * 4, (a.H + 65534) / 65535);
+  a.per_thread = per;
+  const int64_t blocks = (threads + THREADS - 1) / THREADS;
+  k_rope<T, V, INTER, LOOSE><<<dim3((unsigned)blocks, (a.H + per - 1) / per), THREADS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const RopeArgs& a, bool inter, cudaStream_t st) {
+  const int v = piece_of(a, sizeof(T), inter);
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return inter ? launch<T, 8, true>(a, st) : launch<T, 8, false>(a, st);
+  if (v == 4) return inter ? launch<T, 4, true>(a, st) : launch<T, 4, false>(a, st);
+  if (v == 2) return inter ? launch<T, 2, true>(a, st) : launch<T, 2, false>(a, st);
+  return inter ? launch<T, 2, true, true>(a, st) : launch<T, 1, false>(a, st);
+}
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, int32_t HQ, void* q_out,
+                                int64_t qo0, int64_t qo1, const void* k, int64_t ks0, int64_t ks1, int32_t HK, void* k_out,
+                           int64_t ko0, int64_t ko1, int64_t T, int32_t D, int32_t R, const float* freqs,
+                           const void* positions, int positions64, const int32_t* cu_seqlens, int32_t N,
+                           int interleaved, float amplitude, int inverse, cudaStream_t stream) {
+  if (dtype < 0 || dtype > GDR_DTYPE_F32 || T < 0 || T > GDR_OPS_MAX_T || HQ < 0 || HK < 0) return GDR_INVALID_ARG;
+  if (D <= 0 || R < 0 || R > D || R % 2 != 0 || (int64_t)D * ((int64_t)HQ + HK) > INT32_MAX) return GDR_INVALID_ARG;
+  if ((T * D + THREADS - 1) / THREADS > INT32_MAX) return GDR_INVALID_ARG;  // (blocks)
+  if (T == 0 || HQ + HK == 0) return GDR_OK;
+  if ((HQ > 0 && (!q || !q_out)) || (HK > 0 && (!k || !k_out)) || (R > 0 && !freqs)) return GDR_INVALID_ARG;
+  if (R > 0 && !positions && (!cu_seqlens || N <= 0)) return GDR_INVALID_ARG;
+  const gdr_status rc = check_device();
+  if (rc != GDR_OK) return rc;
+  RopeArgs a{};
+  a.q = {q, qs0, qs1, q_out, qo0, qo1};
+  a.k = {k, ks0, ks1, k_out, ko0, ko1};
+  a.HQ = HQ;
+  a.H = HQ + HK;
+  a.D = D;
+  a.R = R;
+  a.T = T;
+  a.pos = positions;
+  a.pos64 = positions64;
+  a.cu = cu_seqlens;
+  a.N = N;
+  a.freq = freqs;
+  a.amp = amplitude;
+  a.back = inverse != 0;
+  ProfScope ps("rope", stream, (double)T * a.H);
+  const bool inter = interleaved != 0;
+  const cudaError_t e = dtype == GDR_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, inter, stream)
+                        : dtype == GDR_DTYPE_F16 ? launch_t<__half>(a, inter, stream)
+                                                 : launch_t<float>(a, inter, stream);
+  return e == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+}

@@ -24,8 +24,6 @@
 // they hold another document's values (a NaN there would pass through a zero
 // weight).  Within a document a non-finite value reaches the outputs of its
 // whole chunk.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <functional>
 #include <new>
@@ -33,14 +31,14 @@
 #include <vector>
 
 #include "gdr_ssm.cuh"
-#include "gdr_tc.cuh"
+#include "gdr_tc_roles.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int Q = 128;        // tokens of a chunk
 constexpr int PT = 64;        // columns of the state that a block works on
-constexpr int BLK = Q * 128;  // bytes of a tile block: 128 rows of 64 BF16
+static_assert(BLK == Q * 128, "a chunk is a tile");
 constexpr int GATES = 2 * Q + 96;  // floats of a chunk's gates
 
 struct TcArgs {
@@ -139,37 +137,6 @@ __device__ Seg find_segment(const int* __restrict__ cu, int N, int lseg, int wan
   return Seg{0, 0, 1, 0, 0, 0, 0};
 }
 
-// Waits of the blocks' roles.  Each gives up after kTries tries of at most a
-// microsecond, or once another role has, and returns false; the block then
-// reports the timeout as it ends.  Few instructions: the roles run straight
-// through long loops that share the instruction cache.
-constexpr int kTries = 1 << 20;
-__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (int tries = 0; !try_phase(bar, parity); ++tries)
-    if (tries > kTries || *abort) {
-      *abort = 1;
-      return false;
-    }
-  return true;
-}
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
-constexpr uint32_t kIdescTransposeA = 1u << 15;
-
-// Byte of the 16-byte piece c (8 BF16) of row r of a 128-byte-swizzled block.
-__device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
 // The two BF16 of a word as a pair of FP32.
 __device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(bf_lo(w), bf_hi(w)); }
 
@@ -197,39 +164,6 @@ __device__ __forceinline__ void split3(uint64_t v, uint32_t& hi, uint32_t& mid, 
   lo = round2(fma2(widen2(mid), minus, v));
 }
 
-// Shared-memory matrix descriptors of 128-byte-swizzled tiles share their upper
-// word (8-row groups 1024 bytes apart, descriptor version 1, the swizzle); the
-// lower word is the address in 16-byte units and, for MN-major tiles, the
-// distance of the 64-element blocks along MN.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(const void* tile) { return tc::smem_u32(tile) >> 4 | (BLK / 16) << 16; }
-
-// MMAs and commits that a whole warp walks through together and one elected
-// thread performs (the same one each time).  Measured: 36 clocks an MMA of 64
-// columns from TMEM and 53 from shared memory, its read time; picked by a
-// comparison of the lane instead, 72 for either.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 db;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 db, {%2, %5};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_u32(bar))
-      : "memory");
-}
 // The same values, known to be the same on every lane: what is computed from
 // them (loop bounds, operand addresses) can live in uniform registers.
 __device__ __forceinline__ Seg uniform(const Seg& s) {
@@ -242,45 +176,6 @@ __device__ __forceinline__ Seg uniform(const Seg& s) {
   u.chunk0 = __shfl_sync(0xffffffffu, s.chunk0, 0);
   u.slot = __shfl_sync(0xffffffffu, s.slot, 0);
   return u;
-}
-// One arrival for the warp, after all its lanes' work.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) arrive(bar);
-}
-// The wait of a whole warp: the same answer on every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (int tries = 0; !__all_sync(0xffffffffu, try_phase(bar, parity)); ++tries)
-    if (__any_sync(0xffffffffu, tries > kTries || *abort)) {
-      *abort = 1;
-      return false;
-    }
-  return true;
-}
-// tcgen05.wait::ld with the loaded registers as operands: nothing that reads
-// them can be scheduled before it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-               :
-               : "memory");
-}
-// Eight consecutive TMEM columns of the warp's lanes to registers (complete
-// after wait_ld).
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) {
-  return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 // ---------------------------------------------------------------------------
 // The gates of every chunk: one block per (chunk, 32 heads).  dt is read with
@@ -1084,18 +979,6 @@ __global__ void __launch_bounds__(256) k_ssm_merge(const __grid_constant__ TcArg
         }
       }
   }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
 }
 
 // [T][heads][dim] BF16, tokens ld elements apart, one head at a time: boxes of

@@ -1,6 +1,7 @@
 """The operators around the gated delta rule: the short causal convolution, the
-selective state space scan, the single-token forms and the norms around a
-block (``include/gdr.h``).  Thin names over the compiled binding
+selective state space scan, the single-token forms, the norms around a block, and
+the softmax attention layer between such layers: layer norm, rotary positions,
+attention over packed documents (``include/gdr.h``).  Thin names over the compiled binding
 (csrc/gdr_binding.cpp), re-exported by the package; all arguments are checked for device,
 type, shape and layout before the library is called, and a check that fails
 raises ``ValueError`` with nothing enqueued.
@@ -22,7 +23,8 @@ import torch
 from . import _check, build, load
 
 __all__ = ("sconv_workspace_bytes", "sconv_fwd", "sconv_bwd", "sconv_step", "ssm_workspace_bytes", "ssm_fwd", "ssm_step",
-           "kda_step", "gdn_step", "norm_workspace_bytes", "norm_fwd", "norm_bwd")
+           "kda_step", "gdn_step", "norm_workspace_bytes", "norm_fwd", "norm_bwd", "lnorm_workspace_bytes", "lnorm_fwd", "lnorm_bwd",
+           "rope_frequencies", "rope_fwd", "rope_bwd", "attn_workspace_bytes", "attn_fwd", "attn_bwd")
 
 
 def _load_binding():
@@ -186,3 +188,127 @@ def norm_bwd(x, weight=None, post_weight=None, gate=None, act="silu", residual=N
         return _on(stream, _binding.norm_bwd, x, weight, post_weight, gate, act, residual, res_scale, eps, dh, dy,
                    scratch, grads)
     return _binding.norm_bwd(x, weight, post_weight, gate, act, residual, res_scale, eps, dh, dy, scratch, grads)
+
+
+def lnorm_workspace_bytes(D: int) -> int:
+    """Scratch bytes of lnorm_bwd for rows of D elements; host only."""
+    n = ctypes.c_size_t(0)
+    _check(load().lnorm_workspace_bytes(D, ctypes.byref(n)), "lnorm_workspace_bytes")
+    return n.value
+
+
+def lnorm_fwd(x, weight=None, bias=None, residual=None, res_scale=1.0, eps=1e-5, h=None, y=None, stream=None):
+    """Layer norm with the scaled residual in front of it, in one pass:
+
+        h = residual + res_scale x, or x;  y = (h - mean) / sqrt(var + eps) weight + bias
+
+    on rows x [..., D] (bf16, fp16 or fp32; two leading dimensions may be strided);
+    residual is shaped like x, weight and bias [D] have x's type or fp32.  Returns
+    (h, y): h is None without a residual."""
+    if stream is not None:
+        return _on(stream, _binding.lnorm_fwd, x, weight, bias, residual, res_scale, eps, h, y)
+    return _binding.lnorm_fwd(x, weight, bias, residual, res_scale, eps, h, y)
+
+
+def lnorm_bwd(x, weight=None, bias=None, residual=None, res_scale=1.0, eps=1e-5, dh=None, dy=None, scratch=None, grads=None,
+              stream=None):
+    """Gradients of lnorm_fwd from dy and dh (the gradient of h, or None).  Returns a
+    dict with dx and, for the arguments given, dresidual, dweight and dbias (fp32);
+    `grads` may bring preallocated tensors.  Where res_scale = 1, dx and dresidual are
+    one tensor."""
+    if stream is not None:
+        return _on(stream, _binding.lnorm_bwd, x, weight, bias, residual, res_scale, eps, dh, dy, scratch, grads)
+    return _binding.lnorm_bwd(x, weight, bias, residual, res_scale, eps, dh, dy, scratch, grads)
+
+
+def rope_frequencies(R: int, base: float = 10000.0, scaling=None, factor: float = 1.0, context: int = 4096, slow: float = 1.0,
+                     fast: float = 32.0, device=None):
+    """Frequencies of rope_fwd's R / 2 pairs (fp32, radians a token): base^(-2 i / R), and
+    for contexts `factor` times as long as the `context` a model was trained on
+
+    * scaling "linear": all of them divided by factor;
+    * "base": those of a base grown by factor^(R / (R - 2)), which leaves the fastest pair
+      and divides the slowest by factor;
+    * "parts": a pair that turns less than `slow` times within the context divided by
+      factor, one that turns more than `fast` times left, linear in the turns between.
+
+    Whether such a model also scales its rows is rope_fwd's `amplitude` (with "parts"
+    often 1 + 0.1 log(factor))."""
+    if R < 0 or R % 2:
+        raise ValueError(f"rope_frequencies: {R} elements are not pairs")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError(f"rope_frequencies: scaling is {scaling!r}; None, 'linear', 'base' and 'parts' are supported")
+    if not (base > 0 and factor > 0 and context > 0 and fast > slow):
+        raise ValueError("rope_frequencies: base, factor and context must be positive, fast above slow")
+    if scaling == "base" and R > 2:
+        base = base * factor ** (R / (R - 2))
+    f = base ** (-np.arange(0, R, 2, dtype=np.float64) / max(R, 1))
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        left = np.clip((f * context / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+        f = f * (left + (1 - left) / factor)
+    return torch.from_numpy(f.astype(np.float32)).to(device if device is not None else "cuda")
+
+
+def rope_fwd(q, k, freqs, positions=None, cu_seqlens=None, interleaved=False, amplitude=1.0, q_out=None, k_out=None,
+             stream=None):
+    """Rotary positions: the first 2 len(freqs) elements of every head of q [T, H, D] and
+    k [T, HK, D] (either may be None; bf16, fp16 or fp32; tokens and heads may be strided)
+    turned in pairs by position times freqs (fp32), times amplitude; the rest copied.
+    Pairs are elements (i, i + R / 2) or, interleaved, (2 i, 2 i + 1).  positions int32 or
+    int64 [T], or None: counted from each document's start (cu_seqlens).  Returns (q, k):
+    new tensors, or q_out and k_out, which may be the inputs themselves."""
+    if stream is not None:
+        return _on(stream, _binding.rope, q, k, freqs, positions, cu_seqlens, interleaved, amplitude, q_out, k_out, False)
+    return _binding.rope(q, k, freqs, positions, cu_seqlens, interleaved, amplitude, q_out, k_out, False)
+
+
+def rope_bwd(dq, dk, freqs, positions=None, cu_seqlens=None, interleaved=False, amplitude=1.0, dq_out=None, dk_out=None,
+             stream=None):
+    """Gradients of rope_fwd: dq and dk turned back.  Returns (dq, dk) as rope_fwd does."""
+    if stream is not None:
+        return _on(stream, _binding.rope, dq, dk, freqs, positions, cu_seqlens, interleaved, amplitude, dq_out, dk_out, True)
+    return _binding.rope(dq, dk, freqs, positions, cu_seqlens, interleaved, amplitude, dq_out, dk_out, True)
+
+
+def attn_workspace_bytes(T: int, TK: int, H: int, HK: int, D: int, cu_seqlens_host, cu_keys_host=None, causal=True, window=0):
+    """(scratch bytes of attn_fwd, of attn_bwd); host only."""
+    host, keys = _host(cu_seqlens_host), None if cu_keys_host is None else _host(cu_keys_host)
+    fwd, bwd = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().attn_workspace_bytes(T, TK, H, HK, D, host.shape[0] - 1, host.ctypes.data,
+                                       None if keys is None else keys.ctypes.data, int(bool(causal)), window,
+                                       ctypes.byref(fwd), ctypes.byref(bwd)), "attn_workspace_bytes")
+    return fwd.value, bwd.value
+
+
+def attn_fwd(q, k, v, cu_seqlens, cu_seqlens_host, scale=None, causal=True, window=0, cu_keys=None, cu_keys_host=None,
+             out=None, lse=None, scratch=None, stream=None):
+    """Softmax attention over packed documents.
+
+    q bf16 [T, H, D]; k, v bf16 [TK, HK, D], shared by H / HK query heads (tokens and heads
+    may be strided); scale: D^-0.5 unless given.  Without cu_keys a document's keys are its
+    own tokens; with it (int32 [N + 1], and its host copy) document n has the keys
+    cu_keys[n] to cu_keys[n + 1], its queries the last of them: a prompt that goes on after
+    cached keys, or one token of each sequence.  causal: a query sees the keys up to its own
+    place, of those the last `window` (0: all).  Returns (out bf16 [T, H, D], lse fp32 [H, T]);
+    a query that sees no key gets 0 and -inf.
+
+    D goes up to 256."""
+    args = (q, k, v, cu_seqlens, _host(cu_seqlens_host), cu_keys, None if cu_keys_host is None else _host(cu_keys_host), scale,
+            causal, window, out, lse, scratch)
+    if stream is not None:
+        return _on(stream, _binding.attn_fwd, *args)
+    return _binding.attn_fwd(*args)
+
+
+def attn_bwd(q, k, v, out, lse, dout, cu_seqlens, cu_seqlens_host, scale=None, causal=True, window=0, cu_keys=None,
+             cu_keys_host=None, scratch=None, grads=None, stream=None):
+    """Gradients of attn_fwd from dout, its out and its lse; the probabilities are formed
+    again.  Returns a dict with dq [T, H, D], dk and dv [TK, HK, D] (bf16); `grads` may bring
+    preallocated tensors."""
+    args = (q, k, v, cu_seqlens, _host(cu_seqlens_host), cu_keys, None if cu_keys_host is None else _host(cu_keys_host), scale,
+            causal, window, out, lse, dout, scratch, grads)
+    if stream is not None:
+        return _on(stream, _binding.attn_bwd, *args)
+    return _binding.attn_bwd(*args)

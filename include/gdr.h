@@ -262,7 +262,8 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * launches run only for split packs, l2norm only with qk_l2norm); the
  * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
  * sconv_step, ssm_gates, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
- * gdn_step, norm_fwd, norm_bwd, norm_wgrad. */
+ * gdn_step, norm_fwd, norm_bwd, norm_wgrad, lnorm_fwd, lnorm_bwd, lnorm_wgrad,
+ * rope, attn_rows, attn_dq_rows, attn_dkv_rows. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
 
@@ -480,6 +481,89 @@ gdr_status norm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const vo
                     float eps, const void* dh, int64_t dhs0, int64_t dhs1, const void* dy, int64_t dys0, int64_t dys1,
                     void* dx, void* dgate, void* dresidual, float* dweight, float* dpost_weight, void* scratch,
                     size_t scratch_bytes, cudaStream_t stream);
+
+/* ===========================================================================
+ * The softmax attention layer of a hybrid stack: the layer norm in front of a
+ * block, rotary positions of q and k, attention over packed documents.
+ * Conventions as for the operators above. */
+
+/* Layer norm with the scaled residual, on rows of D elements (1 <= D <=
+ * GDR_NORM_MAX_D) indexed by (R0, R1) as in norm_fwd:
+ *     h = residual + res_scale x, or x                       (residual null)
+ *     y = (h - mean h) (mean (h - mean h)^2 + eps)^(-1/2) weight + bias
+ * weight, bias [D] (dtype or FP32; null: one, zero).  y is formed from the
+ * unrounded h, its variance from the differences to the mean.  h (may be null)
+ * and y are dense [R0][R1][D]; either may be residual or x itself (the same
+ * rows). */
+gdr_status lnorm_fwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
+                     const void* residual, int64_t rs0, int64_t rs1, float res_scale, const void* weight,
+                     const void* bias, gdr_dtype wdtype, float eps, void* h, void* y, cudaStream_t stream);
+
+/* Bytes of scratch that lnorm_bwd needs (host only). */
+gdr_status lnorm_workspace_bytes(int32_t D, size_t* scratch_bytes);
+
+/* Gradients of lnorm_fwd from dy and dh (the gradient of h; null: zero).
+ * Writes, each when non-null, dx, dresidual (dense rows, the activations'
+ * type) and dweight, dbias [D] FP32, summed over the rows in a fixed order. */
+gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
+                     const void* residual, int64_t rs0, int64_t rs1, float res_scale, const void* weight,
+                     gdr_dtype wdtype, float eps, const void* dh, int64_t dhs0, int64_t dhs1, const void* dy,
+                     int64_t dys0, int64_t dys1, void* dx, void* dresidual, float* dweight, float* dbias,
+                     void* scratch, size_t scratch_bytes, cudaStream_t stream);
+
+/* Rotary positions of q [T][HQ][D] and k [T][HK][D] (either may have no
+ * heads): the first R elements (R even) of every head in pairs (a, b) become
+ *     amplitude (a cos t - b sin t),  amplitude (b cos t + a sin t),
+ *     t = position freqs[pair],
+ * the rest is copied.  Pairs are elements (i, i + R / 2) or, interleaved, (2 i,
+ * 2 i + 1).  inverse: t = -position freqs[pair], the gradient of the forward.
+ * freqs [R / 2] FP32, radians a token; positions int32 or (positions64) int64
+ * [T], any sign, or null: counted from the document's start by cu_seqlens
+ * [N + 1].  The angle modulo a turn is exact to 2^-32 turns at any position up to
+ * 2^31.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
+ * elements apart, a head's elements dense.  An output may be its input (the same
+ * rows). */
+gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, int32_t HQ, void* q_out, int64_t qo0,
+                int64_t qo1, const void* k, int64_t ks0, int64_t ks1, int32_t HK, void* k_out, int64_t ko0,
+                int64_t ko1, int64_t T, int32_t D, int32_t R, const float* freqs, const void* positions,
+                int positions64, const int32_t* cu_seqlens, int32_t N, int interleaved, float amplitude, int inverse,
+                cudaStream_t stream);
+
+/* Softmax attention over packed documents.  Document n has the queries
+ * cu_seqlens[n] .. cu_seqlens[n + 1] and the keys cu_keys[n] .. cu_keys[n + 1]
+ * (cu_keys, cu_keys_host null: the queries' own, TK = T); with lq queries and lk
+ * keys, query i of a document sees its keys
+ *     j < lk;  causal: j <= i + lk - lq;  window > 0: j > i + lk - lq - window
+ * (the last query sees the last key; a window needs causal), and
+ *     s_ij = scale q_i . k_j,  lse_i = log sum_j e^s_ij,
+ *     out_i = sum_j e^(s_ij - lse_i) v_j.
+ * A query that sees no key has out 0 and lse -inf, and takes part in no gradient.
+ * q, dout [T][H][D], k, v [TK][HK][D] BF16, their tokens and heads *s0 and *s1
+ * elements apart; head h reads key head h / (H / HK).  out [T][H][D] BF16 and lse
+ * [H][T] FP32 are dense.  scale > 0; 1 <= D <= GDR_ATTN_MAX_D.  Scores, maxima,
+ * sums and outputs are FP32 until the one rounding.
+ * Values of a document that are not finite reach its own outputs only.
+ * scratch: attn_workspace_bytes, on a 256-byte boundary (null when 0). */
+#define GDR_ATTN_MAX_D 256
+gdr_status attn_workspace_bytes(int64_t T, int64_t TK, int32_t H, int32_t HK, int32_t D, int32_t N,
+                                const int32_t* cu_seqlens_host, const int32_t* cu_keys_host, int causal,
+                                int32_t window, size_t* fwd_scratch_bytes, size_t* bwd_scratch_bytes);
+gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16* k, int64_t ks0, int64_t ks1,
+                    const gdr_bf16* v, int64_t vs0, int64_t vs1, const int32_t* cu_seqlens,
+                    const int32_t* cu_seqlens_host, const int32_t* cu_keys, const int32_t* cu_keys_host, int32_t N,
+                    int64_t T, int64_t TK, int32_t H, int32_t HK, int32_t D, float scale, int causal, int32_t window,
+                    gdr_bf16* out, float* lse, void* scratch, size_t scratch_bytes, cudaStream_t stream);
+
+/* Gradients of attn_fwd from dout, the forward's out and lse; the probabilities
+ * are formed again.  Writes dq [T][H][D], dk, dv [TK][HK][D] BF16, dense, dk and dv
+ * summed in FP32 over the query heads of a key head.  Deterministic. */
+gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16* k, int64_t ks0, int64_t ks1,
+                    const gdr_bf16* v, int64_t vs0, int64_t vs1, const gdr_bf16* out, const float* lse,
+                    const gdr_bf16* dout, int64_t ds0, int64_t ds1, const int32_t* cu_seqlens,
+                    const int32_t* cu_seqlens_host, const int32_t* cu_keys, const int32_t* cu_keys_host, int32_t N,
+                    int64_t T, int64_t TK, int32_t H, int32_t HK, int32_t D, float scale, int causal, int32_t window,
+                    gdr_bf16* dq, gdr_bf16* dk, gdr_bf16* dv, void* scratch, size_t scratch_bytes,
+                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }
