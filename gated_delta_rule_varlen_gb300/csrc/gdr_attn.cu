@@ -214,6 +214,10 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   if (T == 0) return GDR_OK;
   if (!out || !lse) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
+  if (attn_tc_shape(D) && attn_tc_layout(a))
+    return launch_attn_fwd(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_CUDA_ERROR;
   ProfScope ps("attn_rows", stream, (double)T * H);
   k_attn_rows<<<blocks_of(T * H), WARPS * 32, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;

@@ -48,4 +48,48 @@ __device__ __forceinline__ KeyRange keys_of(const AttnArgs& a, int i, int lq, in
   return r;
 }
 
+// Blocks of `per` queries (or keys) of a document, those of later tokens first: what is
+// causal has the most work there.
+struct AttnBlock {
+  int first;           // token within the document
+  int q0, lq, k0, lk;  // the document's queries and keys
+};
+// Finds block `want` of the documents whose lengths cu gives (one warp, the same answer on
+// every lane).
+__device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __restrict__ cu, int per, int want) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+#pragma unroll 1
+  for (int d0 = 0; d0 < a.N; d0 += 32) {
+    const int d = d0 + lane;
+    const int n = d < a.N ? (cu[d + 1] - cu[d] + per - 1) / per : 0;
+    int pre = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, pre, m);
+      if (lane >= m) pre += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, pre, 31);
+    if (want < base + total) {
+      const int l = __ffs(__ballot_sync(0xffffffffu, want < base + pre)) - 1;
+      AttnBlock b;
+      b.first = (base + __shfl_sync(0xffffffffu, pre, l) - 1 - want) * per;
+      const int doc = d0 + l;
+      b.q0 = a.cu[doc];
+      b.lq = a.cu[doc + 1] - b.q0;
+      b.k0 = a.cuk[doc];
+      b.lk = a.cuk[doc + 1] - b.k0;
+      return b;
+    }
+    base += total;
+  }
+  return AttnBlock{0, 0, 0, 0, 0};
+}
+
+// The kernels on the tensor cores (gdr_attn_fwd.cu, gdr_attn_bwd.cu): whether they take
+// the arguments, and their launches.
+bool attn_tc_shape(int D);
+bool attn_tc_layout(const AttnArgs& a);
+cudaError_t launch_attn_fwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st);
+
 }  // namespace gdr

@@ -90,6 +90,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     }
   return true;
 }
+// A wait before a block ends, whatever has happened: some milliseconds at most.
+__device__ __forceinline__ void wait_some(uint64_t* bar, uint32_t parity) {
+  for (int tries = 0; tries < 1 << 14 && !try_phase(bar, parity); ++tries) {
+  }
+}
 // tcgen05.wait::ld with the loaded registers as operands: nothing that reads
 // them can be scheduled before it.
 __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {

@@ -229,7 +229,7 @@ gdr_status gdr_check_device(void);
  * GDR_INVALID_ARG) it records the timeout in the error word and exits.
  * Device error codes: 3 forward walk, 4 backward walk, 5 this self-test,
  * 6 state-side gradient products, 7 chunk-local gradients, 9 the grouped-GDN
- * prep, 10 the selective scan (all reported as GDR_DEVICE_TIMEOUT); 8 a saved-buffer header that
+ * prep, 10 the selective scan, 11 attention (all reported as GDR_DEVICE_TIMEOUT); 8 a saved-buffer header that
  * does not match the backward (reported as GDR_STALE_WORKSPACE). */
 gdr_status gdr_inject_device_error(int code);
 
@@ -263,7 +263,7 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
  * sconv_step, ssm_gates, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
  * gdn_step, norm_fwd, norm_bwd, norm_wgrad, lnorm_fwd, lnorm_bwd, lnorm_wgrad,
- * rope, attn_rows, attn_dq_rows, attn_dkv_rows. */
+ * rope, attn_fwd, attn_rows, attn_dq_rows, attn_dkv_rows. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
 
