@@ -22,7 +22,7 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libgdr.so")
 SOURCES = ["gdr_fwd.cu", "gdr_walk.cu", "gdr_bwd.cu", "gdr_api.cu", "gdr_sconv.cu", "gdr_ssm.cu", "gdr_ssm_tc.cu",
            "gdr_step.cu", "gdr_norm_fwd.cu", "gdr_norm_bwd.cu", "gdr_lnorm_fwd.cu", "gdr_lnorm_bwd.cu", "gdr_rope.cu",
-           "gdr_attn.cu", "gdr_attn_fwd.cu"]
+           "gdr_attn.cu", "gdr_attn_fwd.cu", "gdr_attn_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -3,7 +3,7 @@
 // formulas).
 #include <cmath>
 
-#include "gdr_attn.cuh"
+#include "gdr_attn_tc.cuh"
 
 namespace gdr {
 namespace {
@@ -258,6 +258,10 @@ gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   if (T == 0 && TK == 0) return GDR_OK;
   if ((rc = check_device()) != GDR_OK) return rc;
   a.delta = static_cast<float*>(scratch);
+  if (attn_tc_shape(D) && attn_tc_layout(a))
+    return launch_attn_bwd(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_CUDA_ERROR;
   if (T > 0) {
     ProfScope ps("attn_dq_rows", stream, (double)T * H);
     k_attn_dq_rows<<<blocks_of(T * H), WARPS * 32, 0, stream>>>(a);

@@ -48,14 +48,15 @@ __device__ __forceinline__ KeyRange keys_of(const AttnArgs& a, int i, int lq, in
   return r;
 }
 
-// Blocks of `per` queries (or keys) of a document, those of later tokens first: what is
-// causal has the most work there.
+// Blocks of `per` queries or keys of a document, those with the most work under a causal mask
+// first: the later queries (LAST) or the earlier keys.
 struct AttnBlock {
   int first;           // token within the document
   int q0, lq, k0, lk;  // the document's queries and keys
 };
 // Finds block `want` of the documents whose lengths cu gives (one warp, the same answer on
 // every lane).
+template <bool LAST>
 __device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __restrict__ cu, int per, int want) {
   const int lane = threadIdx.x & 31;
   int base = 0;
@@ -73,7 +74,8 @@ __device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __
     if (want < base + total) {
       const int l = __ffs(__ballot_sync(0xffffffffu, want < base + pre)) - 1;
       AttnBlock b;
-      b.first = (base + __shfl_sync(0xffffffffu, pre, l) - 1 - want) * per;
+      const int end = base + __shfl_sync(0xffffffffu, pre, l);  // of the document's blocks
+      b.first = (LAST ? end - 1 - want : want - end + __shfl_sync(0xffffffffu, n, l)) * per;
       const int doc = d0 + l;
       b.q0 = a.cu[doc];
       b.lq = a.cu[doc + 1] - b.q0;
@@ -86,10 +88,8 @@ __device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __
   return AttnBlock{0, 0, 0, 0, 0};
 }
 
-// The kernels on the tensor cores (gdr_attn_fwd.cu, gdr_attn_bwd.cu): whether they take
-// the arguments, and their launches.
-bool attn_tc_shape(int D);
-bool attn_tc_layout(const AttnArgs& a);
+// The kernels on the tensor cores (gdr_attn_fwd.cu, gdr_attn_bwd.cu); cu, cuk: the host's.
 cudaError_t launch_attn_fwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st);
+cudaError_t launch_attn_bwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st);
 
 }  // namespace gdr

@@ -1,0 +1,644 @@
+// gdr_attn_bwd.cu -- softmax attention's backward on the tensor cores (formulas:
+// gdr_attn.cuh), in two kernels so that every sum has one owner and a fixed order:
+//
+//   k_attn_dq   a tile of 128 queries, its keys 128 at a time:
+//               S = Q K^T, dP = dO V^T, dS = P (dP - delta) over S in tensor memory, dQ += dS K
+//   k_attn_dkv  a tile of 128 keys of one key head, the queries of its heads 128 at a time:
+//               S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+//
+// Scores and probabilities are formed in both (seven products instead of five, but no sums
+// across blocks).  P and dS are the A operands of their products, read from tensor memory in
+// BF16 (2^-9 of each term at most, independently); accumulators, P and dS before that are
+// FP32.
+//
+// delta = dout . out of the rounded out, but for queries whose keys fit one tile: with few
+// keys |out| is like |v|, and 2^-9 of it shows beside the differences dP - delta; there
+// delta is sum p dP, which the tile holds.
+//
+// Rows past a document's end belong to another one: they are cleared where they are summed
+// over (K for dQ, Q and dO for dK and dV).
+#include "gdr_attn_tc.cuh"
+
+namespace gdr {
+namespace {
+
+struct BwdArgs {
+  CUtensorMap q_map, k_map, v_map, do_map;
+  AttnArgs a;
+  int pack;
+  int* err;
+};
+
+constexpr int THREADS = 384;
+
+// One after another through a ring of tiles.
+template <int ST>
+struct Ring {
+  int st = 0, ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == ST) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// A tile of 128 rows to shared memory; the bytes are credited to bar (one lane).
+template <int DB>
+__device__ __forceinline__ void load_tile(unsigned char* to, const CUtensorMap* map, int head, int64_t token, uint64_t* bar) {
+  tc::mbar_arrive_expect_tx(bar, DB * BLK);
+#pragma unroll
+  for (int c = 0; c < DB; ++c) tc::tma_load_3d(to + c * BLK, map, 64 * c, head, (int)token, bar);
+}
+// Rows [rows, 128) of a tile to zero (one warp).
+template <int DB>
+__device__ __forceinline__ void clear_rows(unsigned char* tile, int rows) {
+  for (int e = rows * 8 + (threadIdx.x & 31); e < TILE * 8; e += 32)
+#pragma unroll
+    for (int c = 0; c < DB; ++c) *reinterpret_cast<uint4*>(tile + c * BLK + e * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async();
+}
+// A tile's products over the columns of two tiles in shared memory, D of them.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, int ks) {
+  for (int k = 0; k < ks; ++k) {
+    const uint32_t at = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
+    mma_ss(d, a_lo + at, b_lo + at, id, k > 0);
+  }
+}
+// Products over 128 rows of a tile in shared memory; A in tensor memory, 64 columns of BF16
+// pairs in the first half of each 64 columns.
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t at, uint32_t b_lo, uint32_t id, bool more) {
+#pragma unroll
+  for (int k = 0; k < TILE / 16; ++k)
+    mma_ts(d, at + (k >> 2) * 64 + (k & 3) * 8, b_lo + k * (16 * 128 >> 4), id, more || k > 0);
+}
+__device__ __forceinline__ uint32_t round_pair(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint64_t pair_at(const uint32_t* x) { return pack2(__uint_as_float(x[0]), __uint_as_float(x[1])); }
+__device__ __forceinline__ void load64(uint32_t at, uint32_t (&x)[64]) {
+  tc::tmem_ld32(at, x);
+  tc::tmem_ld32(at + 32, x + 32);
+  tc::tmem_wait_ld();
+  pin(x);
+}
+// 32 accumulator columns of a row, scaled, to 32 (or up to the row's end) elements.
+__device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int D, uint32_t at, float f, bool any, bool live) {
+  uint32_t o[32];
+  if (any) {
+    tc::tmem_ld32(at + c0, o);
+    tc::tmem_wait_ld();
+    pin(o);
+  }
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = any ? round_pair(mul2(pair_at(o + k + 2 * e), pack2(f, f))) : 0u;
+    if (live && c0 + k < D) *reinterpret_cast<uint4*>(row + c0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+template <int DB>
+struct DqSmem {
+  static constexpr int STAGES = DB == 2 ? 5 : 10;
+  unsigned char Q[DB * BLK], dO[DB * BLK];
+  unsigned char KV[STAGES][DB * BLK];  // K and V tiles in turn
+  float part[2][TILE];                 // the warpgroups' halves of delta
+  uint64_t q_full, do_full, full[STAGES], empty[STAGES], cleared;
+  uint64_t s_full[2], dp_full, dp_read, ds_full, part_full, done;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int T_DP = 256, T_DQ = 384;  // (two tiles of S, and over them dS, before)
+
+template <int DB>
+__global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ BwdArgs ba) {
+  using Smem = DqSmem<DB>;
+  constexpr int ST = Smem::STAGES;
+  extern __shared__ unsigned char attn_smem[];
+  Smem& s = *reinterpret_cast<Smem*>(tc::align1024(attn_smem));
+  const AttnArgs& a = ba.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* ab = &s.abort;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.done}) tc::mbar_init(bar, 1);
+      for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full}) tc::mbar_init(bar, 8);
+      for (int i = 0; i < ST; ++i) {
+        tc::mbar_init(&s.full[i], 1);
+        tc::mbar_init(&s.empty[i], 1);
+      }
+      s.abort = 0;
+      tc::mbar_fence_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc(&s.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, groups = a.H >> ba.pack;
+  const AttnBlock b = find_block<true>(a, a.cu, tokens, blockIdx.x / groups);
+  const int h0 = (int)(blockIdx.x % groups) * heads, hk = h0 / (a.H / a.HK);
+  const int i1 = min(b.lq, b.first + tokens);
+  const TileRange r = tiles_of(a, b, b.first, i1);
+  const int n_tiles = r.hi - r.lo;
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    if (warp == 8 && n_tiles > 0) {  // loads
+      if (lane == 0) {
+        load_tile<DB>(s.Q, &ba.q_map, h0, b.q0 + b.first, &s.q_full);
+        load_tile<DB>(s.dO, &ba.do_map, h0, b.q0 + b.first, &s.do_full);
+      }
+      __syncwarp();
+      Ring<ST> w;
+      int i = 0;
+      for (; i < 2 * n_tiles; ++i) {
+        const int j = r.lo + (i >> 1);
+        const bool isk = !(i & 1);
+        if (i >= ST && !warp_wait(&s.empty[w.st], w.ph ^ 1, ab)) break;
+        const int rows = b.lk - j * TILE;
+        const bool clear = isk && rows < TILE;
+        if (lane == 0)
+          load_tile<DB>(s.KV[w.st], isk ? &ba.k_map : &ba.v_map, hk, b.k0 + j * TILE, clear ? &s.cleared : &s.full[w.st]);
+        __syncwarp();
+        if (clear) {
+          if (!warp_wait(&s.cleared, 0, ab)) break;
+          clear_rows<DB>(s.KV[w.st], rows);
+          warp_arrive(&s.full[w.st]);
+        }
+        w.step();
+      }
+      if (i < 2 * n_tiles) {  // given up: the copies in flight land before the block ends
+        for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
+        wait_some(&s.q_full, 0);
+        wait_some(&s.do_full, 0);
+      }
+    } else if (warp == 9 && n_tiles > 0) {  // products
+      const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
+      const int ks = (a.D + 15) / 16;
+      const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
+      const uint32_t q_lo = desc_lo(s.Q), do_lo = desc_lo(s.dO);
+      bool ok = warp_wait(&s.q_full, 0, ab);
+      Ring<ST> w;
+      auto next = [&] {
+        ok = ok && warp_wait(&s.full[w.st], w.ph, ab);
+        const int at = w.st;
+        w.step();
+        return at;
+      };
+      int kst = next(), k2 = 0;
+      if (ok) {
+        mma_rows(tmem, q_lo, desc_lo(s.KV[kst]), id_s, ks);
+        commit(&s.s_full[0]);
+        ok = warp_wait(&s.do_full, 0, ab);
+      }
+      int vst = next();
+      if (ok) {
+        mma_rows(tmem + T_DP, do_lo, desc_lo(s.KV[vst]), id_s, ks);
+        commit(&s.dp_full);
+        commit(&s.empty[vst]);
+      }
+      for (int n = 0; n < n_tiles && ok; ++n) {
+        if (n + 1 < n_tiles) {
+          k2 = next();
+          if (!ok) break;
+          mma_rows(tmem + ((n + 1) & 1) * TILE, q_lo, desc_lo(s.KV[k2]), id_s, ks);
+          commit(&s.s_full[(n + 1) & 1]);
+          vst = next();
+          ok = ok && warp_wait(&s.dp_read, n & 1, ab);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma_rows(tmem + T_DP, do_lo, desc_lo(s.KV[vst]), id_s, ks);
+          commit(&s.dp_full);
+          commit(&s.empty[vst]);
+        }
+        ok = warp_wait(&s.ds_full, n & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.KV[kst]), id_d, n > 0);
+        commit(&s.empty[kst]);
+        kst = k2;
+      }
+      commit(&s.done);
+      wait_some(&s.done, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    // a row a thread, of S and dP the columns 64 half + [0, 64)
+    const int half = warp >> 2, row = tid & 127, c0 = 64 * half;
+    const int token = b.first + (row >> ba.pack), h = h0 + (row & (heads - 1));
+    const int64_t at = b.q0 + token;
+    const bool live = token < b.lq;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const float c = a.scale * LOG2E, lse = live ? a.lse_in[h * a.T + at] : -INFINITY;
+    const float base = lse == -INFINITY ? -INFINITY : -lse * LOG2E;  // (rows that see nothing: p = 0)
+    const uint64_t cc = pack2(c, c), bb = pack2(base, base);
+    const KeyRange kr = keys_of(a, token, b.lq, b.lk);
+    const KeyRange all{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
+    bool ok = true;
+    float delta = 0.f;
+    auto exchange = [&](float mine) {  // delta of both halves
+      s.part[half][row] = mine;
+      warp_arrive(&s.part_full);
+      ok = ok && warp_wait(&s.part_full, 0, ab);
+      delta = s.part[0][row] + s.part[1][row];
+      if (live && half == 0) a.delta[h * a.T + at] = delta;
+    };
+    if (n_tiles > 1) {
+      constexpr int PIECES = DB * 4;  // of 8 elements, half a row's
+      uint4 o[PIECES];
+      const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int d = (half * PIECES + i) * 8;
+        o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
+      }
+      ok = warp_wait(&s.do_full, 0, ab);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int pc = half * PIECES + i;
+        const uint4 g = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
+        const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
+      }
+      exchange(sum);
+    } else if (n_tiles == 0 && live && half == 0) {
+      a.delta[h * a.T + at] = 0.f;
+    }
+#pragma unroll 1
+    for (int n = 0; n < n_tiles; ++n) {
+      const int j = r.lo + n;
+      const uint32_t ts = lanes + (n & 1) * TILE + c0;
+      ok = ok && warp_wait(&s.s_full[n & 1], (n >> 1) & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint64_t p[32];
+      {
+        uint32_t x[64];
+        load64(ts, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float e, f;
+          unpack2(fma2(pair_at(x + 2 * i), cc, bb), e, f);
+          p[i] = pack2(ex2(e), ex2(f));
+        }
+        if (j * TILE < all.lo || (j + 1) * TILE > all.hi) {
+          const int lo = kr.lo - j * TILE - c0, hi = kr.hi - j * TILE - c0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float e, f;
+            unpack2(p[i], e, f);
+            p[i] = pack2(2 * i >= lo && 2 * i < hi ? e : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? f : 0.f);
+          }
+        }
+      }
+      ok = warp_wait(&s.dp_full, n & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint32_t x[64];
+      load64(lanes + T_DP + c0, x);
+      tc::tc_fence_before();
+      warp_arrive(&s.dp_read);
+      if (b.lk - j * TILE < TILE) {  // keys past the document's end: whatever V holds there
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
+      }
+      if (n_tiles == 1) {
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
+        exchange(sum_of(add2(sum[0], sum[1])));
+        if (!ok) break;
+      }
+      const uint64_t minus = pack2(-delta, -delta);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
+      tc::tmem_st32(ts, x);
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      warp_arrive(&s.ds_full);
+    }
+    if (ok && n_tiles > 0) {
+      ok = warp_wait(&s.done, 0, ab);
+      tc::tc_fence_after();
+    }
+    if (ok) {
+      __nv_bfloat16* dq = a.dq + (at * a.H + h) * a.D;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) store32(dq, DB * 32 * half + 32 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s.abort) atomicExch(ba.err, 11);
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// dK, dV
+// ---------------------------------------------------------------------------
+template <int DB>
+struct DkvSmem {
+  static constexpr int STAGES = DB == 2 ? 4 : 8;
+  unsigned char K[DB * BLK], V[DB * BLK];
+  unsigned char QO[STAGES][DB * BLK];  // Q and dO tiles in turn
+  alignas(16) float lse[2][TILE], delta[2][TILE];  // -lse log2 e, -delta
+  uint64_t k_full, v_full, full[STAGES], empty[STAGES], cleared;
+  uint64_t s_full, p_full, dp_full, ds_full, row_full[2], row_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int T_DPT = 128, T_DK = 256, T_DV = 384;  // (S^T, and over it P^T, before)
+
+template <int DB>
+__global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__ BwdArgs ba) {
+  using Smem = DkvSmem<DB>;
+  constexpr int ST = Smem::STAGES;
+  extern __shared__ unsigned char attn_smem[];
+  Smem& s = *reinterpret_cast<Smem*>(tc::align1024(attn_smem));
+  const AttnArgs& a = ba.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* ab = &s.abort;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (uint64_t* bar : {&s.k_full, &s.v_full, &s.cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1], &s.done})
+        tc::mbar_init(bar, 1);
+      for (uint64_t* bar : {&s.p_full, &s.ds_full, &s.row_empty[0], &s.row_empty[1]}) tc::mbar_init(bar, 8);
+      for (int i = 0; i < ST; ++i) {
+        tc::mbar_init(&s.full[i], 1);
+        tc::mbar_init(&s.empty[i], 1);
+      }
+      s.abort = 0;
+      tc::mbar_fence_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc(&s.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, G = a.H / a.HK;
+  const AttnBlock b = find_block<false>(a, a.cuk, TILE, blockIdx.x / a.HK);
+  const int hk = (int)(blockIdx.x % a.HK);
+  // the tiles of queries that see any of the keys [first, last]: each head group's
+  const int off = b.lk - b.lq, last = min(b.lk, b.first + TILE) - 1;
+  const int qlo = a.causal ? max(0, b.first - off) : 0;
+  const int qhi = a.window ? (int)min((int64_t)b.lq, (int64_t)last - off + a.window) : b.lq;
+  const int t0 = qlo / tokens, per = qhi > qlo ? (qhi + tokens - 1) / tokens - t0 : 0;
+  const int n_tiles = per * (G >> ba.pack);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    if (warp == 8 && n_tiles > 0) {  // loads
+      if (lane == 0) {
+        load_tile<DB>(s.K, &ba.k_map, hk, b.k0 + b.first, &s.k_full);
+        load_tile<DB>(s.V, &ba.v_map, hk, b.k0 + b.first, &s.v_full);
+      }
+      __syncwarp();
+      Ring<ST> w;
+      int i = 0, cleared = 0;
+      for (int g = 0, t = 0; i < 2 * n_tiles; ++i) {
+        const bool isq = !(i & 1);
+        if (i >= ST && !warp_wait(&s.empty[w.st], w.ph ^ 1, ab)) break;
+        const int token = (t0 + t) * tokens, rows = (int)min((int64_t)TILE, (int64_t)(b.lq - token) << ba.pack);
+        const bool clear = rows < TILE;
+        if (lane == 0)
+          load_tile<DB>(s.QO[w.st], isq ? &ba.q_map : &ba.do_map, hk * G + g * heads, b.q0 + token, clear ? &s.cleared : &s.full[w.st]);
+        __syncwarp();
+        if (clear) {
+          if (!warp_wait(&s.cleared, cleared++ & 1, ab)) break;
+          clear_rows<DB>(s.QO[w.st], rows);
+          warp_arrive(&s.full[w.st]);
+        }
+        w.step();
+        if (!isq && ++t == per) {
+          t = 0;
+          ++g;
+        }
+      }
+      if (i < 2 * n_tiles) {  // given up: the copies in flight land before the block ends
+        for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
+        wait_some(&s.k_full, 0);
+        wait_some(&s.v_full, 0);
+      }
+    } else if (warp == 9 && n_tiles > 0) {  // products
+      const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
+      const int ks = (a.D + 15) / 16;
+      const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
+      const uint32_t k_lo = desc_lo(s.K), v_lo = desc_lo(s.V);
+      bool ok = warp_wait(&s.k_full, 0, ab);
+      Ring<ST> w;
+      auto next = [&] {
+        ok = ok && warp_wait(&s.full[w.st], w.ph, ab);
+        const int at = w.st;
+        w.step();
+        return at;
+      };
+      int qst = next(), q2 = 0;
+      if (ok) {
+        mma_rows(tmem, k_lo, desc_lo(s.QO[qst]), id_s, ks);
+        commit(&s.s_full);
+        ok = warp_wait(&s.v_full, 0, ab);
+      }
+      int dst = next();
+      if (ok) {
+        mma_rows(tmem + T_DPT, v_lo, desc_lo(s.QO[dst]), id_s, ks);
+        commit(&s.dp_full);
+      }
+      for (int n = 0; n < n_tiles && ok; ++n) {
+        const bool more = n + 1 < n_tiles;
+        ok = warp_wait(&s.p_full, n & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        mma_sum(tmem + T_DV, tmem, desc_lo(s.QO[dst]), id_d, n > 0);
+        if (more) {
+          q2 = next();
+          if (!ok) break;
+          mma_rows(tmem, k_lo, desc_lo(s.QO[q2]), id_s, ks);
+          commit(&s.s_full);
+        }
+        ok = warp_wait(&s.ds_full, n & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.QO[qst]), id_d, n > 0);
+        commit(&s.empty[qst]);
+        commit(&s.empty[dst]);
+        if (more) {
+          dst = next();
+          if (!ok) break;
+          mma_rows(tmem + T_DPT, v_lo, desc_lo(s.QO[dst]), id_s, ks);
+          commit(&s.dp_full);
+        }
+        qst = q2;
+      }
+      commit(&s.done);
+      wait_some(&s.done, 0);
+    } else if (warp == 10 && n_tiles > 0) {  // lse and delta of a tile's queries
+      for (int n = 0, g = 0, t = 0; n < n_tiles; ++n) {
+        float l[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 4 * lane + e, token = (t0 + t) * tokens + (row >> ba.pack);
+          const int64_t at = (int64_t)(hk * G + g * heads + (row & (heads - 1))) * a.T + b.q0 + token;
+          const bool live = token < b.lq;
+          const float x = live ? a.lse_in[at] : -INFINITY;
+          l[e] = x == -INFINITY ? x : -x * LOG2E;  // (queries that see nothing: p = 0)
+          d[e] = live ? -a.delta[at] : 0.f;
+        }
+        if (n >= 2 && !warp_wait(&s.row_empty[n & 1], ((n >> 1) - 1) & 1, ab)) break;
+        *reinterpret_cast<float4*>(&s.lse[n & 1][4 * lane]) = make_float4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<float4*>(&s.delta[n & 1][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+        warp_arrive(&s.row_full[n & 1]);
+        if (++t == per) {
+          t = 0;
+          ++g;
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    // a key a thread, of S^T and dP^T the queries 64 half + [0, 64)
+    const int half = warp >> 2, row = tid & 127, c0 = 64 * half;
+    const int key = b.first + row;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const float c = a.scale * LOG2E;
+    const uint64_t cc = pack2(c, c);
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0, t = 0; n < n_tiles; ++n) {
+      ok = warp_wait(&s.row_full[n & 1], (n >> 1) & 1, ab) && warp_wait(&s.s_full, n & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint64_t p[32];
+      uint32_t x[64];
+      load64(lanes + c0, x);
+      const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(&s.lse[n & 1][c0]);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const ulonglong2 l = ls[i / 2];
+        float e, f;
+        unpack2(fma2(pair_at(x + 2 * i), cc, l.x), e, f);
+        p[i] = pack2(ex2(e), ex2(f));
+        unpack2(fma2(pair_at(x + 2 * i + 2), cc, l.y), e, f);
+        p[i + 1] = pack2(ex2(e), ex2(f));
+      }
+      const int q0 = (t0 + t) * tokens;
+      if (a.causal && (q0 + off < last || (a.window && (int64_t)q0 + tokens > (int64_t)b.first - off + a.window))) {
+        // the queries of this tile that see the key: [lo, hi)
+        const int64_t first = (int64_t)key - off - q0;
+        const int lo = (int)min(max(first, (int64_t)0), (int64_t)tokens) << ba.pack;
+        const int hi = a.window ? (int)min(max(first + a.window, (int64_t)0), (int64_t)tokens) << ba.pack : TILE;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float e, f;
+          unpack2(p[i], e, f);
+          p[i] = pack2(c0 + 2 * i >= lo && c0 + 2 * i < hi ? e : 0.f, c0 + 2 * i + 1 >= lo && c0 + 2 * i + 1 < hi ? f : 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = round_pair(p[i]);
+      tc::tmem_st32(lanes + c0, x);
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      warp_arrive(&s.p_full);
+      ok = warp_wait(&s.dp_full, n & 1, ab);
+      if (!ok) break;
+      tc::tc_fence_after();
+      load64(lanes + T_DPT + c0, x);
+      const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(&s.delta[n & 1][c0]);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const ulonglong2 d = ds[i / 2];
+        x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), d.x)));
+        x[i + 1] = round_pair(mul2(p[i + 1], add2(pair_at(x + 2 * i + 2), d.y)));
+      }
+      tc::tmem_st32(lanes + T_DPT + c0, x);
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      warp_arrive(&s.ds_full);
+      warp_arrive(&s.row_empty[n & 1]);
+      if (++t == per) t = 0;
+    }
+    if (ok && n_tiles > 0) {
+      ok = warp_wait(&s.done, 0, ab);
+      tc::tc_fence_after();
+    }
+    if (ok) {
+      const int64_t at = ((int64_t)(b.k0 + key) * a.HK + hk) * a.D;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+        store32(a.dk + at, DB * 32 * half + 32 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
+        store32(a.dv + at, DB * 32 * half + 32 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s.abort) atomicExch(ba.err, 11);
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+template <typename K>
+cudaError_t go(K kernel, size_t smem, int64_t blocks, const BwdArgs& f, cudaStream_t st) {
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  kernel<<<(unsigned)blocks, THREADS, smem, st>>>(f);
+  return cudaGetLastError();
+}
+template <typename S>
+constexpr size_t bytes_of() {
+  static_assert(sizeof(S) + 1024 <= 232448, "227 KB of shared memory a block");
+  return sizeof(S) + 1024;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st) {
+  BwdArgs f{};
+  f.a = a;
+  f.err = device_error_ptr();
+  if (!f.err) return cudaErrorUnknown;
+  f.pack = attn_pack(a, cu);
+  const int tokens = TILE >> f.pack;
+  int64_t qblocks = 0, kblocks = 0;
+  for (int i = 0; i < a.N; ++i) {
+    qblocks += (cu[i + 1] - cu[i] + tokens - 1) / tokens;
+    kblocks += (cuk[i + 1] - cuk[i] + TILE - 1) / TILE;
+  }
+  if (a.T > 0 && (!attn_map(&f.q_map, a.q, a.T, a.H, a.D, 1 << f.pack, tokens) ||
+                  !attn_map(&f.do_map, a.dout, a.T, a.H, a.D, 1 << f.pack, tokens)))
+    return cudaErrorInvalidValue;
+  if (a.TK > 0 && (!attn_map(&f.k_map, a.k, a.TK, a.HK, a.D, 1, TILE) || !attn_map(&f.v_map, a.v, a.TK, a.HK, a.D, 1, TILE)))
+    return cudaErrorInvalidValue;
+  if (qblocks > 0) {
+    ProfScope ps("attn_dq", st, (double)a.T * a.H);
+    const int64_t blocks = qblocks * (a.H >> f.pack);
+    if (cudaError_t e = a.D <= 64 ? go(k_attn_dq<1>, bytes_of<DqSmem<1>>(), blocks, f, st)
+                                  : go(k_attn_dq<2>, bytes_of<DqSmem<2>>(), blocks, f, st))
+      return e;
+  }
+  if (kblocks > 0) {
+    ProfScope ps("attn_dkv", st, (double)a.TK * a.HK);
+    return a.D <= 64 ? go(k_attn_dkv<1>, bytes_of<DkvSmem<1>>(), kblocks * a.HK, f, st)
+                     : go(k_attn_dkv<2>, bytes_of<DkvSmem<2>>(), kblocks * a.HK, f, st);
+  }
+  return cudaSuccess;
+}
+
+}  // namespace gdr

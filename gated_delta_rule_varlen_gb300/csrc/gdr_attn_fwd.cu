@@ -15,10 +15,7 @@
 //
 // Rows of V past a document's keys are cleared, since they hold another document's values (a
 // NaN there would pass through a zero probability).
-#include <algorithm>
-
-#include "gdr_attn.cuh"
-#include "gdr_tc_roles.cuh"
+#include "gdr_attn_tc.cuh"
 
 namespace gdr {
 namespace {
@@ -30,7 +27,7 @@ struct FwdArgs {
   int* err;
 };
 
-constexpr int TILE = 128, THREADS = 384;
+constexpr int THREADS = 384;
 // Tensor memory: S (and over it P) of the tiles, out of the tiles.
 constexpr int T_S = 0, T_O = 256;
 
@@ -44,23 +41,6 @@ struct FwdSmem {
   uint32_t tmem;
   int abort;
 };
-
-// The key tiles [lo, hi) that tokens [i0, i1) of a document see.
-struct TileRange {
-  int lo, hi;
-};
-__device__ __forceinline__ TileRange tiles_of(const AttnArgs& a, const AttnBlock& b, int i0, int i1) {
-  if (i0 >= i1) return {0, 0};
-  const KeyRange first = keys_of(a, i0, b.lq, b.lk), last = keys_of(a, i1 - 1, b.lq, b.lk);
-  if (last.hi <= first.lo) return {0, 0};
-  return {first.lo / TILE, (last.hi + TILE - 1) / TILE};
-}
-
-template <int N>
-__device__ __forceinline__ void pin(uint32_t (&r)[N]) {  // nothing that reads them moves before this
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
 
 template <int DB>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__ FwdArgs fa) {
@@ -94,7 +74,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
   }
   const int heads = 1 << fa.pack, tokens = TILE >> fa.pack;  // of a tile
   const int groups = a.H >> fa.pack;
-  const AttnBlock b = find_block(a, a.cu, 2 * tokens, blockIdx.x / groups);
+  const AttnBlock b = find_block<true>(a, a.cu, 2 * tokens, blockIdx.x / groups);
   const int h0 = (int)(blockIdx.x % groups) * heads, hk = h0 / (a.H / a.HK);
   TileRange r[2];
 #pragma unroll
@@ -318,40 +298,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
 
 }  // namespace
 
-bool attn_tc_shape(int D) { return D % 8 == 0 && D <= 128; }
-
-bool attn_tc_layout(const AttnArgs& a) {
-  for (const AttnRows* t : {&a.q, &a.k, &a.v, &a.dout})
-    if (t->p && (((uintptr_t)t->p & 15) != 0 || t->s0 <= 0 || t->s1 <= 0 || t->s0 % 8 != 0 || t->s1 % 8 != 0)) return false;
-  for (const void* p : {(const void*)a.out, (const void*)a.o, (const void*)a.dq, (const void*)a.dk, (const void*)a.dv})
-    if (((uintptr_t)p & 15) != 0) return false;
-  return true;
-}
-
-// [T][heads][D] BF16: boxes of 64 elements x `heads` heads x `tokens` tokens, 128-byte
-// swizzle, zero fill outside.
-bool attn_map(CUtensorMap* map, const AttnRows& t, int64_t T, int H, int D, int heads, int tokens) {
-  auto enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
-  cuuint64_t strides[2] = {(cuuint64_t)t.s1 * 2, (cuuint64_t)t.s0 * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(t.p), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t launch_attn_fwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st) {
   FwdArgs f{};
   f.a = a;
   f.err = device_error_ptr();
   if (!f.err) return cudaErrorUnknown;
-  int most = 0;
-  for (int i = 0; i < a.N; ++i) most = std::max(most, cu[i + 1] - cu[i]);
-  // Heads that share their keys lie side by side while the queries alone do not fill a tile.
-  const int G = a.H / a.HK;
-  while (f.pack < 7 && G % (2 << f.pack) == 0 && (most << f.pack) < TILE) ++f.pack;
+  f.pack = attn_pack(a, cu);
   const int per = 2 * (TILE >> f.pack);
   int64_t blocks = 0;
   for (int i = 0; i < a.N; ++i) blocks += (cu[i + 1] - cu[i] + per - 1) / per;
