@@ -29,7 +29,11 @@ struct BwdArgs {
   int* err;
 };
 
-constexpr int THREADS = 384;
+// Sixteen warps on the elements of a tile, four on each quarter of its columns (of two
+// warpgroups with halves each waited on its own loads and barriers), and one warpgroup of
+// roles.
+constexpr int QUARTERS = 4, WORKERS = 4 * QUARTERS, THREADS = 32 * WORKERS + 128;
+constexpr int COLS = TILE / QUARTERS;
 
 // One after another through a ring of tiles.
 template <int ST>
@@ -58,19 +62,21 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int rows) {
     for (int c = 0; c < DB; ++c) *reinterpret_cast<uint4*>(tile + c * BLK + e * 16) = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async();
 }
-// A tile's products over the columns of two tiles in shared memory, D of them.
+// A tile's products over the columns of two tiles in shared memory, ks steps of 16.
+template <int DB>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, int ks) {
-  for (int k = 0; k < ks; ++k) {
+#pragma unroll
+  for (int k = 0; k < 4 * DB; ++k) {
     const uint32_t at = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
-    mma_ss(d, a_lo + at, b_lo + at, id, k > 0);
+    if (k < ks) mma_ss(d, a_lo + at, b_lo + at, id, k > 0);
   }
 }
-// Products over 128 rows of a tile in shared memory; A in tensor memory, 64 columns of BF16
-// pairs in the first half of each 64 columns.
+// Products over 128 rows of a tile in shared memory; A in tensor memory, BF16 pairs in the
+// first half of each quarter's columns.
 __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t at, uint32_t b_lo, uint32_t id, bool more) {
 #pragma unroll
   for (int k = 0; k < TILE / 16; ++k)
-    mma_ts(d, at + (k >> 2) * 64 + (k & 3) * 8, b_lo + k * (16 * 128 >> 4), id, more || k > 0);
+    mma_ts(d, at + (k >> 1) * COLS + (k & 1) * 8, b_lo + k * (16 * 128 >> 4), id, more || k > 0);
 }
 __device__ __forceinline__ uint32_t round_pair(uint64_t v) {
   float a, b;
@@ -79,22 +85,27 @@ __device__ __forceinline__ uint32_t round_pair(uint64_t v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint64_t pair_at(const uint32_t* x) { return pack2(__uint_as_float(x[0]), __uint_as_float(x[1])); }
-__device__ __forceinline__ void load64(uint32_t at, uint32_t (&x)[64]) {
+__device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&x)[COLS]) {
   tc::tmem_ld32(at, x);
-  tc::tmem_ld32(at + 32, x + 32);
   tc::tmem_wait_ld();
   pin(x);
 }
-// 32 accumulator columns of a row, scaled, to 32 (or up to the row's end) elements.
-__device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int D, uint32_t at, float f, bool any, bool live) {
-  uint32_t o[32];
+__device__ __forceinline__ void store_words(uint32_t at, const uint32_t (&x)[COLS]) {  // the first half of x
+  uint32_t w[COLS / 2];
+#pragma unroll
+  for (int i = 0; i < COLS / 2; ++i) w[i] = x[i];
+  tc::tmem_st16(at, w);
+  tc::tmem_wait_st();
+}
+// 16 accumulator columns of a row, scaled, to 16 (or up to the row's end) elements.
+__device__ __forceinline__ void store16(__nv_bfloat16* row, int c0, int D, uint32_t at, float f, bool any, bool live) {
+  uint32_t o[16];
   if (any) {
-    tc::tmem_ld32(at + c0, o);
-    tc::tmem_wait_ld();
-    pin(o);
+    tc::tmem_ld16(at + c0, o);
+    wait_ld(o);
   }
 #pragma unroll
-  for (int k = 0; k < 32; k += 8) {
+  for (int k = 0; k < 16; k += 8) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = any ? round_pair(mul2(pair_at(o + k + 2 * e), pack2(f, f))) : 0u;
@@ -107,11 +118,12 @@ __device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int D, uint3
 // ---------------------------------------------------------------------------
 template <int DB>
 struct DqSmem {
-  static constexpr int STAGES = DB == 2 ? 5 : 10;
+  // a K tile is held from S until its dQ, a step later
+  static constexpr int KS = DB == 2 ? 3 : 6, VS = DB == 2 ? 2 : 4;
   unsigned char Q[DB * BLK], dO[DB * BLK];
-  unsigned char KV[STAGES][DB * BLK];  // K and V tiles in turn
-  float part[2][TILE];                 // the warpgroups' halves of delta
-  uint64_t q_full, do_full, full[STAGES], empty[STAGES], cleared;
+  unsigned char K[KS][DB * BLK], V[VS][DB * BLK];
+  float part[QUARTERS][TILE];          // the quarters' shares of delta
+  uint64_t q_full, do_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], cleared;
   uint64_t s_full[2], dp_full, dp_read, ds_full, part_full, done;
   uint32_t tmem;
   int abort;
@@ -121,19 +133,23 @@ constexpr int T_DP = 256, T_DQ = 384;  // (two tiles of S, and over them dS, bef
 template <int DB>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ BwdArgs ba) {
   using Smem = DqSmem<DB>;
-  constexpr int ST = Smem::STAGES;
-  extern __shared__ unsigned char attn_smem[];
-  Smem& s = *reinterpret_cast<Smem*>(tc::align1024(attn_smem));
+  constexpr int KS = Smem::KS, VS = Smem::VS;
+  extern __shared__ __align__(1024) unsigned char attn_smem[];
+  Smem& s = *reinterpret_cast<Smem*>(attn_smem);
   const AttnArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
   if (warp == 0) {
     if (lane == 0) {
       for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.done}) tc::mbar_init(bar, 1);
-      for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full}) tc::mbar_init(bar, 8);
-      for (int i = 0; i < ST; ++i) {
-        tc::mbar_init(&s.full[i], 1);
-        tc::mbar_init(&s.empty[i], 1);
+      for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full}) tc::mbar_init(bar, WORKERS);
+      for (int i = 0; i < KS; ++i) {
+        tc::mbar_init(&s.k_full[i], 1);
+        tc::mbar_init(&s.k_empty[i], 1);
+      }
+      for (int i = 0; i < VS; ++i) {
+        tc::mbar_init(&s.v_full[i], 1);
+        tc::mbar_init(&s.v_empty[i], 1);
       }
       s.abort = 0;
       tc::mbar_fence_init();
@@ -153,90 +169,92 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    if (warp == 8 && n_tiles > 0) {  // loads
+  if (warp >= WORKERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == WORKERS && n_tiles > 0) {  // loads
       if (lane == 0) {
         load_tile<DB>(s.Q, &ba.q_map, h0, b.q0 + b.first, &s.q_full);
         load_tile<DB>(s.dO, &ba.do_map, h0, b.q0 + b.first, &s.do_full);
       }
       __syncwarp();
-      Ring<ST> w;
-      int i = 0;
-      for (; i < 2 * n_tiles; ++i) {
-        const int j = r.lo + (i >> 1);
-        const bool isk = !(i & 1);
-        if (i >= ST && !warp_wait(&s.empty[w.st], w.ph ^ 1, ab)) break;
-        const int rows = b.lk - j * TILE;
-        const bool clear = isk && rows < TILE;
-        if (lane == 0)
-          load_tile<DB>(s.KV[w.st], isk ? &ba.k_map : &ba.v_map, hk, b.k0 + j * TILE, clear ? &s.cleared : &s.full[w.st]);
+      Ring<KS> kr;
+      Ring<VS> vr;
+      int n = 0;
+      for (; n < n_tiles; ++n) {
+        const int j = r.lo + n, rows = b.lk - j * TILE;
+        const bool clear = rows < TILE;
+        if (n >= KS && !warp_wait(&s.k_empty[kr.st], kr.ph ^ 1, ab)) break;
+        if (lane == 0) load_tile<DB>(s.K[kr.st], &ba.k_map, hk, b.k0 + j * TILE, clear ? &s.cleared : &s.k_full[kr.st]);
         __syncwarp();
         if (clear) {
           if (!warp_wait(&s.cleared, 0, ab)) break;
-          clear_rows<DB>(s.KV[w.st], rows);
-          warp_arrive(&s.full[w.st]);
+          clear_rows<DB>(s.K[kr.st], rows);
+          warp_arrive(&s.k_full[kr.st]);
         }
-        w.step();
+        kr.step();
+        if (n >= VS && !warp_wait(&s.v_empty[vr.st], vr.ph ^ 1, ab)) break;
+        if (lane == 0) load_tile<DB>(s.V[vr.st], &ba.v_map, hk, b.k0 + j * TILE, &s.v_full[vr.st]);
+        __syncwarp();
+        vr.step();
       }
-      if (i < 2 * n_tiles) {  // given up: the copies in flight land before the block ends
-        for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
+      if (n < n_tiles) {  // given up: the copies in flight land before the block ends
+        for (int k = max(0, n + 1 - KS); k <= n; ++k) wait_some(&s.k_full[k % KS], (k / KS) & 1);
+        for (int k = max(0, n - VS); k < n; ++k) wait_some(&s.v_full[k % VS], (k / VS) & 1);
+        wait_some(&s.cleared, 0);
         wait_some(&s.q_full, 0);
         wait_some(&s.do_full, 0);
       }
-    } else if (warp == 9 && n_tiles > 0) {  // products
+    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // products
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const int ks = (a.D + 15) / 16;
       const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
       const uint32_t q_lo = desc_lo(s.Q), do_lo = desc_lo(s.dO);
       bool ok = warp_wait(&s.q_full, 0, ab);
-      Ring<ST> w;
-      auto next = [&] {
-        ok = ok && warp_wait(&s.full[w.st], w.ph, ab);
-        const int at = w.st;
-        w.step();
+      Ring<KS> kr;
+      Ring<VS> vr;
+      auto score = [&](int n) {  // S of the next tile; its K
+        const int at = kr.st;
+        mma_rows<DB>(tmem + (n & 1) * TILE, q_lo, desc_lo(s.K[at]), id_s, ks);
+        commit(&s.s_full[n & 1]);
+        kr.step();
         return at;
       };
-      int kst = next(), k2 = 0;
-      if (ok) {
-        mma_rows(tmem, q_lo, desc_lo(s.KV[kst]), id_s, ks);
-        commit(&s.s_full[0]);
-        ok = warp_wait(&s.do_full, 0, ab);
-      }
-      int vst = next();
-      if (ok) {
-        mma_rows(tmem + T_DP, do_lo, desc_lo(s.KV[vst]), id_s, ks);
+      auto grad = [&] {  // dP of the next tile
+        mma_rows<DB>(tmem + T_DP, do_lo, desc_lo(s.V[vr.st]), id_s, ks);
         commit(&s.dp_full);
-        commit(&s.empty[vst]);
+        commit(&s.v_empty[vr.st]);
+        vr.step();
+      };
+      int kst = 0, k2 = 0;
+      ok = ok && warp_wait(&s.k_full[0], 0, ab);
+      if (ok) {
+        kst = score(0);
+        ok = warp_wait_all(ab, Phase{&s.do_full, 0}, Phase{&s.v_full[0], 0});
       }
+      if (ok) grad();
       for (int n = 0; n < n_tiles && ok; ++n) {
         if (n + 1 < n_tiles) {
-          k2 = next();
-          if (!ok) break;
-          mma_rows(tmem + ((n + 1) & 1) * TILE, q_lo, desc_lo(s.KV[k2]), id_s, ks);
-          commit(&s.s_full[(n + 1) & 1]);
-          vst = next();
-          ok = ok && warp_wait(&s.dp_read, n & 1, ab);
+          ok = warp_wait_all(ab, Phase{&s.k_full[kr.st], (uint32_t)kr.ph}, Phase{&s.v_full[vr.st], (uint32_t)vr.ph},
+                             Phase{&s.dp_read, (uint32_t)n & 1});
           if (!ok) break;
           tc::tc_fence_after();
-          mma_rows(tmem + T_DP, do_lo, desc_lo(s.KV[vst]), id_s, ks);
-          commit(&s.dp_full);
-          commit(&s.empty[vst]);
+          k2 = score(n + 1);
+          grad();
         }
         ok = warp_wait(&s.ds_full, n & 1, ab);
         if (!ok) break;
         tc::tc_fence_after();
-        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.KV[kst]), id_d, n > 0);
-        commit(&s.empty[kst]);
+        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.K[kst]), id_d, n > 0);
+        commit(&s.k_empty[kst]);
         kst = k2;
       }
       commit(&s.done);
       wait_some(&s.done, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-    // a row a thread, of S and dP the columns 64 half + [0, 64)
-    const int half = warp >> 2, row = tid & 127, c0 = 64 * half;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    // a row a thread, of S and dP a quarter's columns
+    const int part = warp >> 2, row = tid & 127, c0 = COLS * part;
     const int token = b.first + (row >> ba.pack), h = h0 + (row & (heads - 1));
     const int64_t at = b.q0 + token;
     const bool live = token < b.lq;
@@ -248,34 +266,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     const KeyRange all{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
     bool ok = true;
     float delta = 0.f;
-    auto exchange = [&](float mine) {  // delta of both halves
-      s.part[half][row] = mine;
+    auto exchange = [&](float mine) {  // delta of all quarters
+      s.part[part][row] = mine;
       warp_arrive(&s.part_full);
       ok = ok && warp_wait(&s.part_full, 0, ab);
-      delta = s.part[0][row] + s.part[1][row];
-      if (live && half == 0) a.delta[h * a.T + at] = delta;
+      delta = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
+      if (live && part == 0) a.delta[h * a.T + at] = delta;
     };
     if (n_tiles > 1) {
-      constexpr int PIECES = DB * 4;  // of 8 elements, half a row's
+      constexpr int PIECES = DB * 8 / QUARTERS;  // of 8 elements of a row
       uint4 o[PIECES];
       const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int d = (half * PIECES + i) * 8;
+        const int d = (part * PIECES + i) * 8;
         o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
       }
       ok = warp_wait(&s.do_full, 0, ab);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int pc = half * PIECES + i;
+        const int pc = part * PIECES + i;
         const uint4 g = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
         const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
       }
       exchange(sum);
-    } else if (n_tiles == 0 && live && half == 0) {
+    } else if (n_tiles == 0 && live && part == 0) {
       a.delta[h * a.T + at] = 0.f;
     }
 #pragma unroll 1
@@ -285,12 +303,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       ok = ok && warp_wait(&s.s_full[n & 1], (n >> 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
-      uint64_t p[32];
+      uint64_t p[COLS / 2];
       {
-        uint32_t x[64];
-        load64(ts, x);
+        uint32_t x[COLS];
+        load_cols(ts, x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < COLS / 2; ++i) {
           float e, f;
           unpack2(fma2(pair_at(x + 2 * i), cc, bb), e, f);
           p[i] = pack2(ex2(e), ex2(f));
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         if (j * TILE < all.lo || (j + 1) * TILE > all.hi) {
           const int lo = kr.lo - j * TILE - c0, hi = kr.hi - j * TILE - c0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < COLS / 2; ++i) {
             float e, f;
             unpack2(p[i], e, f);
             p[i] = pack2(2 * i >= lo && 2 * i < hi ? e : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? f : 0.f);
@@ -308,27 +326,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       ok = warp_wait(&s.dp_full, n & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
-      uint32_t x[64];
-      load64(lanes + T_DP + c0, x);
+      uint32_t x[COLS];
+      load_cols(lanes + T_DP + c0, x);
       tc::tc_fence_before();
       warp_arrive(&s.dp_read);
       if (b.lk - j * TILE < TILE) {  // keys past the document's end: whatever V holds there
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < COLS; ++i)
           if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
       }
       if (n_tiles == 1) {
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
+        for (int i = 0; i < COLS / 2; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
         exchange(sum_of(add2(sum[0], sum[1])));
         if (!ok) break;
       }
       const uint64_t minus = pack2(-delta, -delta);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
-      tc::tmem_st32(ts, x);
-      tc::tmem_wait_st();
+      for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
+      store_words(ts, x);
       tc::tc_fence_before();
       warp_arrive(&s.ds_full);
     }
@@ -339,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     if (ok) {
       __nv_bfloat16* dq = a.dq + (at * a.H + h) * a.D;
 #pragma unroll
-      for (int i = 0; i < DB; ++i) store32(dq, DB * 32 * half + 32 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
+      for (int i = 0; i < DB; ++i) store16(dq, DB * 16 * part + 16 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
     }
   }
   tc::tc_fence_before();
@@ -353,11 +370,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 template <int DB>
 struct DkvSmem {
-  static constexpr int STAGES = DB == 2 ? 4 : 8;
+  // a Q tile is held until its dK, behind its dV
+  static constexpr int QS = DB == 2 ? 3 : 6, OS = DB == 2 ? 2 : 4;
   unsigned char K[DB * BLK], V[DB * BLK];
-  unsigned char QO[STAGES][DB * BLK];  // Q and dO tiles in turn
+  unsigned char Q[QS][DB * BLK], dO[OS][DB * BLK];
   alignas(16) float lse[2][TILE], delta[2][TILE];  // -lse log2 e, -delta
-  uint64_t k_full, v_full, full[STAGES], empty[STAGES], cleared;
+  uint64_t k_full, v_full, q_full[QS], q_empty[QS], o_full[OS], o_empty[OS], q_cleared, o_cleared;
   uint64_t s_full, p_full, dp_full, ds_full, row_full[2], row_empty[2], done;
   uint32_t tmem;
   int abort;
@@ -367,20 +385,24 @@ constexpr int T_DPT = 128, T_DK = 256, T_DV = 384;  // (S^T, and over it P^T, be
 template <int DB>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__ BwdArgs ba) {
   using Smem = DkvSmem<DB>;
-  constexpr int ST = Smem::STAGES;
-  extern __shared__ unsigned char attn_smem[];
-  Smem& s = *reinterpret_cast<Smem*>(tc::align1024(attn_smem));
+  constexpr int QS = Smem::QS, OS = Smem::OS;
+  extern __shared__ __align__(1024) unsigned char attn_smem[];
+  Smem& s = *reinterpret_cast<Smem*>(attn_smem);
   const AttnArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
   if (warp == 0) {
     if (lane == 0) {
-      for (uint64_t* bar : {&s.k_full, &s.v_full, &s.cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1], &s.done})
+      for (uint64_t* bar : {&s.k_full, &s.v_full, &s.q_cleared, &s.o_cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1], &s.done})
         tc::mbar_init(bar, 1);
-      for (uint64_t* bar : {&s.p_full, &s.ds_full, &s.row_empty[0], &s.row_empty[1]}) tc::mbar_init(bar, 8);
-      for (int i = 0; i < ST; ++i) {
-        tc::mbar_init(&s.full[i], 1);
-        tc::mbar_init(&s.empty[i], 1);
+      for (uint64_t* bar : {&s.p_full, &s.ds_full, &s.row_empty[0], &s.row_empty[1]}) tc::mbar_init(bar, WORKERS);
+      for (int i = 0; i < QS; ++i) {
+        tc::mbar_init(&s.q_full[i], 1);
+        tc::mbar_init(&s.q_empty[i], 1);
+      }
+      for (int i = 0; i < OS; ++i) {
+        tc::mbar_init(&s.o_full[i], 1);
+        tc::mbar_init(&s.o_empty[i], 1);
       }
       s.abort = 0;
       tc::mbar_fence_init();
@@ -403,93 +425,107 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    if (warp == 8 && n_tiles > 0) {  // loads
+  if (warp >= WORKERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == WORKERS && n_tiles > 0) {  // loads
       if (lane == 0) {
         load_tile<DB>(s.K, &ba.k_map, hk, b.k0 + b.first, &s.k_full);
         load_tile<DB>(s.V, &ba.v_map, hk, b.k0 + b.first, &s.v_full);
       }
       __syncwarp();
-      Ring<ST> w;
-      int i = 0, cleared = 0;
-      for (int g = 0, t = 0; i < 2 * n_tiles; ++i) {
-        const bool isq = !(i & 1);
-        if (i >= ST && !warp_wait(&s.empty[w.st], w.ph ^ 1, ab)) break;
+      Ring<QS> qr;
+      Ring<OS> orr;
+      int n = 0, cleared = 0;
+      for (int g = 0, t = 0; n < n_tiles; ++n) {
         const int token = (t0 + t) * tokens, rows = (int)min((int64_t)TILE, (int64_t)(b.lq - token) << ba.pack);
         const bool clear = rows < TILE;
-        if (lane == 0)
-          load_tile<DB>(s.QO[w.st], isq ? &ba.q_map : &ba.do_map, hk * G + g * heads, b.q0 + token, clear ? &s.cleared : &s.full[w.st]);
+        const int h = hk * G + g * heads;
+        if (n >= QS && !warp_wait(&s.q_empty[qr.st], qr.ph ^ 1, ab)) break;
+        if (lane == 0) load_tile<DB>(s.Q[qr.st], &ba.q_map, h, b.q0 + token, clear ? &s.q_cleared : &s.q_full[qr.st]);
+        __syncwarp();
+        if (n >= OS && !warp_wait(&s.o_empty[orr.st], orr.ph ^ 1, ab)) break;
+        if (lane == 0) load_tile<DB>(s.dO[orr.st], &ba.do_map, h, b.q0 + token, clear ? &s.o_cleared : &s.o_full[orr.st]);
         __syncwarp();
         if (clear) {
-          if (!warp_wait(&s.cleared, cleared++ & 1, ab)) break;
-          clear_rows<DB>(s.QO[w.st], rows);
-          warp_arrive(&s.full[w.st]);
+          if (!warp_wait(&s.q_cleared, cleared & 1, ab)) break;
+          clear_rows<DB>(s.Q[qr.st], rows);
+          warp_arrive(&s.q_full[qr.st]);
+          if (!warp_wait(&s.o_cleared, cleared & 1, ab)) break;
+          clear_rows<DB>(s.dO[orr.st], rows);
+          warp_arrive(&s.o_full[orr.st]);
+          ++cleared;
         }
-        w.step();
-        if (!isq && ++t == per) {
+        qr.step();
+        orr.step();
+        if (++t == per) {
           t = 0;
           ++g;
         }
       }
-      if (i < 2 * n_tiles) {  // given up: the copies in flight land before the block ends
-        for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
+      if (n < n_tiles) {  // given up: the copies in flight land before the block ends
+        for (int k = max(0, n + 1 - QS); k <= n; ++k) wait_some(&s.q_full[k % QS], (k / QS) & 1);
+        for (int k = max(0, n + 1 - OS); k <= n; ++k) wait_some(&s.o_full[k % OS], (k / OS) & 1);
+        wait_some(&s.q_cleared, cleared & 1);
+        wait_some(&s.o_cleared, cleared & 1);
         wait_some(&s.k_full, 0);
         wait_some(&s.v_full, 0);
       }
-    } else if (warp == 9 && n_tiles > 0) {  // products
+    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // products
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const int ks = (a.D + 15) / 16;
       const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
       const uint32_t k_lo = desc_lo(s.K), v_lo = desc_lo(s.V);
       bool ok = warp_wait(&s.k_full, 0, ab);
-      Ring<ST> w;
-      auto next = [&] {
-        ok = ok && warp_wait(&s.full[w.st], w.ph, ab);
-        const int at = w.st;
-        w.step();
-        return at;
-      };
-      int qst = next(), q2 = 0;
-      if (ok) {
-        mma_rows(tmem, k_lo, desc_lo(s.QO[qst]), id_s, ks);
+      Ring<QS> qr;
+      Ring<OS> orr;
+      int qst = 0, q2 = 0, ost = 0;
+      auto score = [&](int& at) {  // S^T of the next tile
+        at = qr.st;
+        mma_rows<DB>(tmem, k_lo, desc_lo(s.Q[at]), id_s, ks);
         commit(&s.s_full);
-        ok = warp_wait(&s.v_full, 0, ab);
-      }
-      int dst = next();
-      if (ok) {
-        mma_rows(tmem + T_DPT, v_lo, desc_lo(s.QO[dst]), id_s, ks);
+        qr.step();
+      };
+      auto grad = [&] {  // dP^T of the next tile
+        ost = orr.st;
+        mma_rows<DB>(tmem + T_DPT, v_lo, desc_lo(s.dO[ost]), id_s, ks);
         commit(&s.dp_full);
+        orr.step();
+      };
+      ok = ok && warp_wait(&s.q_full[0], 0, ab);
+      if (ok) {
+        score(qst);
+        ok = warp_wait_all(ab, Phase{&s.v_full, 0}, Phase{&s.o_full[0], 0});
       }
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        const bool more = n + 1 < n_tiles;
-        ok = warp_wait(&s.p_full, n & 1, ab);
+      if (ok) grad();
+      for (int n = 0; n + 1 < n_tiles && ok; ++n) {
+        ok = warp_wait_all(ab, Phase{&s.p_full, (uint32_t)n & 1}, Phase{&s.q_full[qr.st], (uint32_t)qr.ph});
         if (!ok) break;
         tc::tc_fence_after();
-        mma_sum(tmem + T_DV, tmem, desc_lo(s.QO[dst]), id_d, n > 0);
-        if (more) {
-          q2 = next();
-          if (!ok) break;
-          mma_rows(tmem, k_lo, desc_lo(s.QO[q2]), id_s, ks);
-          commit(&s.s_full);
-        }
-        ok = warp_wait(&s.ds_full, n & 1, ab);
+        mma_sum(tmem + T_DV, tmem, desc_lo(s.dO[ost]), id_d, n > 0);
+        commit(&s.o_empty[ost]);
+        score(q2);
+        ok = warp_wait_all(ab, Phase{&s.ds_full, (uint32_t)n & 1}, Phase{&s.o_full[orr.st], (uint32_t)orr.ph});
         if (!ok) break;
         tc::tc_fence_after();
-        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.QO[qst]), id_d, n > 0);
-        commit(&s.empty[qst]);
-        commit(&s.empty[dst]);
-        if (more) {
-          dst = next();
-          if (!ok) break;
-          mma_rows(tmem + T_DPT, v_lo, desc_lo(s.QO[dst]), id_s, ks);
-          commit(&s.dp_full);
-        }
+        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.Q[qst]), id_d, n > 0);
+        commit(&s.q_empty[qst]);
+        grad();
         qst = q2;
+      }
+      const int n = n_tiles - 1;  // the last tile
+      ok = ok && warp_wait(&s.p_full, n & 1, ab);
+      if (ok) {
+        tc::tc_fence_after();
+        mma_sum(tmem + T_DV, tmem, desc_lo(s.dO[ost]), id_d, n > 0);
+        ok = warp_wait(&s.ds_full, n & 1, ab);
+      }
+      if (ok) {
+        tc::tc_fence_after();
+        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.Q[qst]), id_d, n > 0);
       }
       commit(&s.done);
       wait_some(&s.done, 0);
-    } else if (warp == 10 && n_tiles > 0) {  // lse and delta of a tile's queries
+    } else if (warp == WORKERS + 2 && n_tiles > 0) {  // lse and delta of a tile's queries
       for (int n = 0, g = 0, t = 0; n < n_tiles; ++n) {
         float l[4], d[4];
 #pragma unroll
@@ -512,9 +548,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-    // a key a thread, of S^T and dP^T the queries 64 half + [0, 64)
-    const int half = warp >> 2, row = tid & 127, c0 = 64 * half;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    // a key a thread, of S^T and dP^T a quarter's queries
+    const int part = warp >> 2, row = tid & 127, c0 = COLS * part;
     const int key = b.first + row;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = a.scale * LOG2E;
@@ -522,15 +558,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
     bool ok = true;
 #pragma unroll 1
     for (int n = 0, t = 0; n < n_tiles; ++n) {
-      ok = warp_wait(&s.row_full[n & 1], (n >> 1) & 1, ab) && warp_wait(&s.s_full, n & 1, ab);
+      ok = warp_wait_all(ab, Phase{&s.row_full[n & 1], (uint32_t)(n >> 1) & 1}, Phase{&s.s_full, (uint32_t)n & 1});
       if (!ok) break;
       tc::tc_fence_after();
-      uint64_t p[32];
-      uint32_t x[64];
-      load64(lanes + c0, x);
+      uint64_t p[COLS / 2];
+      uint32_t x[COLS];
+      load_cols(lanes + c0, x);
       const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(&s.lse[n & 1][c0]);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < COLS / 2; i += 2) {
         const ulonglong2 l = ls[i / 2];
         float e, f;
         unpack2(fma2(pair_at(x + 2 * i), cc, l.x), e, f);
@@ -545,31 +581,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
         const int lo = (int)min(max(first, (int64_t)0), (int64_t)tokens) << ba.pack;
         const int hi = a.window ? (int)min(max(first + a.window, (int64_t)0), (int64_t)tokens) << ba.pack : TILE;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < COLS / 2; ++i) {
           float e, f;
           unpack2(p[i], e, f);
           p[i] = pack2(c0 + 2 * i >= lo && c0 + 2 * i < hi ? e : 0.f, c0 + 2 * i + 1 >= lo && c0 + 2 * i + 1 < hi ? f : 0.f);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = round_pair(p[i]);
-      tc::tmem_st32(lanes + c0, x);
-      tc::tmem_wait_st();
+      for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(p[i]);
+      store_words(lanes + c0, x);
       tc::tc_fence_before();
       warp_arrive(&s.p_full);
       ok = warp_wait(&s.dp_full, n & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
-      load64(lanes + T_DPT + c0, x);
+      load_cols(lanes + T_DPT + c0, x);
       const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(&s.delta[n & 1][c0]);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < COLS / 2; i += 2) {
         const ulonglong2 d = ds[i / 2];
         x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), d.x)));
         x[i + 1] = round_pair(mul2(p[i + 1], add2(pair_at(x + 2 * i + 2), d.y)));
       }
-      tc::tmem_st32(lanes + T_DPT + c0, x);
-      tc::tmem_wait_st();
+      store_words(lanes + T_DPT + c0, x);
       tc::tc_fence_before();
       warp_arrive(&s.ds_full);
       warp_arrive(&s.row_empty[n & 1]);
@@ -583,8 +617,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       const int64_t at = ((int64_t)(b.k0 + key) * a.HK + hk) * a.D;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        store32(a.dk + at, DB * 32 * half + 32 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
-        store32(a.dv + at, DB * 32 * half + 32 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
+        store16(a.dk + at, DB * 16 * part + 16 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
+        store16(a.dv + at, DB * 16 * part + 16 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
       }
     }
   }
@@ -603,8 +637,8 @@ cudaError_t go(K kernel, size_t smem, int64_t blocks, const BwdArgs& f, cudaStre
 }
 template <typename S>
 constexpr size_t bytes_of() {
-  static_assert(sizeof(S) + 1024 <= 232448, "227 KB of shared memory a block");
-  return sizeof(S) + 1024;
+  static_assert(sizeof(S) <= 232448, "227 KB of shared memory a block");
+  return sizeof(S);
 }
 
 }  // namespace

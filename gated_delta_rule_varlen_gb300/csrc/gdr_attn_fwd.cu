@@ -140,51 +140,62 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
       uint32_t q_lo[2] = {desc_lo(s.Q[0]), desc_lo(s.Q[1])};
       auto score = [&](int t, int st) {
         const uint32_t k_lo = desc_lo(s.KV[st]);
-        for (int k = 0; k < ks; ++k) {
+#pragma unroll
+        for (int k = 0; k < 4 * DB; ++k) {
           const uint32_t at = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
-          mma_ss(tmem + T_S + t * TILE, q_lo[t] + at, k_lo + at, id_s, k > 0);
+          if (k < ks) mma_ss(tmem + T_S + t * TILE, q_lo[t] + at, k_lo + at, id_s, k > 0);
         }
         commit(&s.s_full[t]);
       };
       bool ok = true;
       int used[2] = {0, 0};
       int st = 0, ph = 0;  // the next tile of the ring
-      auto next = [&](int& at) {
-        ok = ok && warp_wait(&s.full[st], ph, ab);
-        at = st;
+      auto next = [&] {
+        const Phase p{&s.full[st], (uint32_t)ph};
         if (++st == ST) {
           st = 0;
           ph ^= 1;
         }
+        return p;
       };
-      int kst, vst;
-      next(kst);
+      auto stage = [&](const Phase& p) { return (int)(p.bar - s.full); };
+      Phase kp = next();
+      ok = warp_wait(kp.bar, kp.parity, ab);
       for (int t = 0; t < 2 && ok; ++t)
         if (r[t].lo < r[t].hi) {
           ok = warp_wait(&s.q_full[t], 0, ab);
-          if (ok && r[t].lo == j0) score(t, kst);
+          if (ok && r[t].lo == j0) score(t, stage(kp));
         }
-      if (ok) commit(&s.empty[kst]);
+      if (ok) commit(&s.empty[stage(kp)]);
       for (int j = j0; j < j1 && ok; ++j) {
-        next(vst);
         const bool more = j + 1 < j1;
-        if (more) next(kst);
+        const Phase vp = next();
+        if (more) kp = next();
+        bool loaded = false;  // V of this step, K of the next
         for (int t = 0; t < 2 && ok; ++t) {
-          if (j >= r[t].lo && j < r[t].hi) {
-            ok = warp_wait(&s.p_full[t], used[t] & 1, ab);
-            if (!ok) break;
+          const bool here = j >= r[t].lo && j < r[t].hi;
+          const Phase pp{here ? &s.p_full[t] : kp.bar, here ? (uint32_t)used[t] & 1 : kp.parity};
+          if (!loaded) {
+            ok = more ? warp_wait_all(ab, vp, kp, here ? pp : kp) : warp_wait_all(ab, vp, here ? pp : vp);
+            loaded = true;
+          } else if (here) {
+            ok = warp_wait(pp.bar, pp.parity, ab);
+          }
+          if (!ok) break;
+          if (here) {
             tc::tc_fence_after();
-            const uint32_t v_lo = desc_lo(s.KV[vst]);
+            const uint32_t v_lo = desc_lo(s.KV[stage(vp)]);
+#pragma unroll
             for (int k = 0; k < TILE / 16; ++k)
               mma_ts(tmem + T_O + t * TILE, tmem + T_S + t * TILE + 8 * k, v_lo + k * (16 * 128 >> 4), id_o, used[t] > 0 || k > 0);
             ++used[t];
             if (j + 1 == r[t].hi) commit(&s.o_full[t]);
           }
-          if (more && j + 1 >= r[t].lo && j + 1 < r[t].hi) score(t, kst);
+          if (more && j + 1 >= r[t].lo && j + 1 < r[t].hi) score(t, stage(kp));
         }
         if (!ok) break;
-        commit(&s.empty[vst]);
-        if (more) commit(&s.empty[kst]);
+        commit(&s.empty[stage(vp)]);
+        if (more) commit(&s.empty[stage(kp)]);
       }
       commit(&s.done);
       wait_some(&s.done, 0);

@@ -9,8 +9,8 @@
 // position, modulo 2^64, is the angle's fraction of a turn (off by position 2^-65 turns
 // beside the frequency's own rounding), and the top 32 bits of it become sine and cosine.
 //
-// Bound by HBM: each element read once and written once.  A thread keeps the sines and
-// cosines of its columns over several heads of a token.
+// Bound by HBM: each element read once and written once.  A block turns the heads of some
+// tokens; their sines and cosines are formed once, into shared memory.
 #include <algorithm>
 
 #include "gdr_ops.cuh"
@@ -38,7 +38,7 @@ struct RopeArgs {
   float amp;
   int back;
   int units, turned;   // pieces of a head: all, those that turn
-  int per_thread;      // heads a thread goes through
+  int tokens;          // of a block
 };
 
 constexpr int THREADS = 256;
@@ -64,9 +64,9 @@ __device__ __forceinline__ void angle(uint64_t turns, uint64_t pos, float amp, b
   s *= back ? -amp : amp;
 }
 
-// A thread's unit of a head: V elements from each half of the turned part (interleaved:
-// V elements of V / 2 pairs), or V elements to copy.  LOOSE: rows on no common boundary,
-// element by element.
+// A unit of a head: V elements from each half of the turned part (interleaved: V elements
+// of V / 2 pairs), or V elements to copy.  LOOSE: rows on no common boundary, element by
+// element.
 template <typename T, int V, bool LOOSE>
 __device__ __forceinline__ Vec<T, V> load_piece(const T* p, int n) {
   if constexpr (!LOOSE) return vload<T, V>(p);
@@ -96,76 +96,100 @@ __device__ __forceinline__ Vec<T, V> packed(const float (&f)[V]) {
 
 template <typename T, int V, bool INTER, bool LOOSE>
 __global__ void __launch_bounds__(THREADS) k_rope(const __grid_constant__ RopeArgs a) {
-  const int64_t item = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-  const int64_t t = item / a.units;
-  if (t >= a.T) return;
-  const int u = (int)(item % a.units), h0 = blockIdx.y * a.per_thread, h1 = min(a.H, h0 + a.per_thread);
-  const bool turn = u < a.turned;
-  constexpr int PAIRS = INTER ? V / 2 : V;
-  const int c0 = turn ? u * V : a.R + (u - a.turned) * V;
-  const int n = a.D - c0;  // (elements up to the head's end)
-  float cs[PAIRS], sn[PAIRS];
-  if (turn) {
-    uint64_t pos;
-    if (!a.pos) pos = (uint64_t)(t - a.cu[doc_of(a.cu, a.N, (int)t)]);
-    else if (a.pos64) pos = (uint64_t)static_cast<const int64_t*>(a.pos)[t];
-    else pos = (uint64_t)(int64_t)static_cast<const int*>(a.pos)[t];
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i)
-      angle(turns_of(__ldg(a.freq + (INTER ? c0 / 2 : c0) + i)), pos, a.amp, a.back, cs[i], sn[i]);
-  }
-  const bool two = turn && !INTER;
-  auto at = [&](int h, const T*& x, T*& y) {
-    const bool isq = h < a.HQ;
-    const RopeRows& r = isq ? a.q : a.k;
-    const int hh = isq ? h : h - a.HQ;
-    x = static_cast<const T*>(r.x) + t * r.s0 + hh * r.s1 + c0;
-    y = static_cast<T*>(r.y) + t * r.y0 + hh * r.y1 + c0;
+  constexpr int PAIRS = INTER ? V / 2 : V, U = 4;  // units asked for together
+  extern __shared__ __align__(16) float rope_smem[];
+  const int half = a.R / 2;
+  float *cs = rope_smem, *sn = rope_smem + a.tokens * half;  // [tokens][R / 2]
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int tokens = (int)min((int64_t)a.tokens, a.T - t0);
+  // The next U units of the thread: unit, head and token advance by sums with carries.
+  const int per = a.units * a.H, n = tokens * per;
+  const int du = THREADS % a.units, dh = THREADS / a.units % a.H, dt = THREADS / per;
+  int u = threadIdx.x % a.units, h = threadIdx.x / a.units % a.H, t = threadIdx.x / per;
+  struct Unit {
+    const T* x;
+    T* y;
+    int u, t;
+    Vec<T, V> lo, hi;
   };
-  constexpr int U = 4;  // heads asked for together
-  for (int h = h0; h < h1; h += U) {
-    Vec<T, V> lo[U], hi[U];
+  auto load = [&](Unit& w) {
+    w.u = u;
+    w.t = t;
+    const bool isq = h < a.HQ, turn = u < a.turned;
+    const RopeRows& r = isq ? a.q : a.k;
+    const int hh = isq ? h : h - a.HQ, c0 = turn ? u * V : a.R + (u - a.turned) * V;
+    w.x = static_cast<const T*>(r.x) + (t0 + t) * r.s0 + hh * r.s1 + c0;
+    w.y = static_cast<T*>(r.y) + (t0 + t) * r.y0 + hh * r.y1 + c0;
+    w.lo = load_piece<T, V, LOOSE>(w.x, a.D - c0);
+    if (!INTER && turn) w.hi = load_piece<T, V, LOOSE>(w.x + half, V);
+    u += du;
+    const int cu = u >= a.units;
+    u -= cu ? a.units : 0;
+    h += dh + cu;
+    const int ch = h >= a.H;
+    h -= ch ? a.H : 0;
+    t += dt + ch;
+  };
+  Unit w[U];
+  int i = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+    if (i + j * THREADS < n) load(w[j]);  // (on their way while the angles are formed)
+  for (int e = threadIdx.x; e < tokens * half; e += THREADS) {
+    const int64_t at = t0 + e / half;
+    uint64_t pos;
+    if (!a.pos) pos = (uint64_t)(at - a.cu[doc_of(a.cu, a.N, (int)at)]);
+    else if (a.pos64) pos = (uint64_t)static_cast<const int64_t*>(a.pos)[at];
+    else pos = (uint64_t)(int64_t)static_cast<const int*>(a.pos)[at];
+    angle(turns_of(__ldg(a.freq + e % half)), pos, a.amp, a.back, cs[e], sn[e]);
+  }
+  __syncthreads();
+  while (i < n) {
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if (h + j < h1) {
-        const T* x;
-        T* y;
-        at(h + j, x, y);
-        lo[j] = load_piece<T, V, LOOSE>(x, n);
-        if (two) hi[j] = load_piece<T, V, LOOSE>(x + a.R / 2, V);
-      }
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (h + j < h1) {
-        const T* x;
-        T* y;
-        at(h + j, x, y);
-        if (!turn) {
-          store_piece<T, V, LOOSE>(y, lo[j], n);
-        } else if constexpr (INTER) {
-          float f[V];
-          vunpack<T, V>(lo[j], f);
-#pragma unroll
-          for (int i = 0; i < PAIRS; ++i) {
-            const float p = f[2 * i], q = f[2 * i + 1];
-            f[2 * i] = p * cs[i] - q * sn[i];
-            f[2 * i + 1] = q * cs[i] + p * sn[i];
-          }
-          store_piece<T, V, LOOSE>(y, packed<T, V>(f), V);
-        } else {
-          float f[V], g[V];
-          vunpack<T, V>(lo[j], f);
-          vunpack<T, V>(hi[j], g);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float p = f[i], q = g[i];
-            f[i] = p * cs[i] - q * sn[i];
-            g[i] = q * cs[i] + p * sn[i];
-          }
-          store_piece<T, V, LOOSE>(y, packed<T, V>(f), V);
-          store_piece<T, V, LOOSE>(y + a.R / 2, packed<T, V>(g), V);
+      if (i + j * THREADS < n) {
+        const Unit& k = w[j];
+        if (k.u >= a.turned) {
+          store_piece<T, V, LOOSE>(k.y, k.lo, a.D - (a.R + (k.u - a.turned) * V));
+          continue;
         }
+        float c[PAIRS], s[PAIRS], f[V], g[V];
+        const int at = k.t * half + k.u * PAIRS;
+        if (PAIRS % 4 == 0 && half % 4 == 0) {
+#pragma unroll
+          for (int e = 0; e < PAIRS; e += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(cs + at + e), y = *reinterpret_cast<const float4*>(sn + at + e);
+            c[e] = x.x, c[(e + 1) % PAIRS] = x.y, c[(e + 2) % PAIRS] = x.z, c[(e + 3) % PAIRS] = x.w;
+            s[e] = y.x, s[(e + 1) % PAIRS] = y.y, s[(e + 2) % PAIRS] = y.z, s[(e + 3) % PAIRS] = y.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < PAIRS; ++e) c[e] = cs[at + e], s[e] = sn[at + e];
+        }
+        vunpack<T, V>(k.lo, f);
+        if constexpr (INTER) {
+#pragma unroll
+          for (int e = 0; e < PAIRS; ++e) {
+            const float p = f[2 * e], q = f[2 * e + 1];
+            f[2 * e] = p * c[e] - q * s[e];
+            f[2 * e + 1] = q * c[e] + p * s[e];
+          }
+        } else {
+          vunpack<T, V>(k.hi, g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float p = f[e], q = g[e];
+            f[e] = p * c[e] - q * s[e];
+            g[e] = q * c[e] + p * s[e];
+          }
+          store_piece<T, V, LOOSE>(k.y + half, packed<T, V>(g), V);
+        }
+        store_piece<T, V, LOOSE>(k.y, packed<T, V>(f), V);
       }
+    i += U * THREADS;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (i + j * THREADS < n) load(w[j]);
   }
 }
 
@@ -188,14 +212,14 @@ template <typename T, int V, bool INTER, bool LOOSE = false>
 cudaError_t launch(RopeArgs a, cudaStream_t st) {
   a.turned = (INTER ? a.R : a.R / 2) / V;
   a.units = a.turned + (a.D - a.R + V - 1) / V;
-  // Heads a thread: all of them share the sines, fewer where that leaves SMs without work.
-  const int64_t threads = a.T * a.units, room = 152ll * 2048;
-  int per = a.H;
-  while (per > 4 && threads * ((a.H + per - 1) / per) < 2 * room) per = (per + 1) / 2;
-  per = std::max((per + 3) / 4 * 4, (a.H + 65534) / 65535);
-  a.per_thread = per;
-  const int64_t blocks = (threads + THREADS - 1) / THREADS;
-  k_rope<T, V, INTER, LOOSE><<<dim3((unsigned)blocks, (a.H + per - 1) / per), THREADS, 0, st>>>(a);
+  // Tokens of a block: two rounds of units for its threads, or as many as share the heads'
+  // sines where there are few heads; sines up to 32 KB.
+  const int64_t per = (int64_t)a.units * a.H;
+  int64_t n = std::max<int64_t>(1, 8 * THREADS / per);
+  if (a.R > 0) n = std::min<int64_t>(n, std::max(1, 4096 / (a.R / 2)));
+  a.tokens = (int)std::min(n, a.T);
+  const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
+  k_rope<T, V, INTER, LOOSE><<<(unsigned)blocks, THREADS, (size_t)a.tokens * a.R * sizeof(float), st>>>(a);
   return cudaGetLastError();
 }
 
@@ -220,8 +244,7 @@ extern "C" gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int
                            const void* positions, int positions64, const int32_t* cu_seqlens, int32_t N,
                            int interleaved, float amplitude, int inverse, cudaStream_t stream) {
   if (dtype < 0 || dtype > GDR_DTYPE_F32 || T < 0 || T > GDR_OPS_MAX_T || HQ < 0 || HK < 0) return GDR_INVALID_ARG;
-  if (D <= 0 || R < 0 || R > D || R % 2 != 0 || (int64_t)D * ((int64_t)HQ + HK) > INT32_MAX) return GDR_INVALID_ARG;
-  if ((T * D + THREADS - 1) / THREADS > INT32_MAX) return GDR_INVALID_ARG;  // (blocks)
+  if (D <= 0 || R < 0 || R > D || R > GDR_ROPE_MAX_R || R % 2 != 0 || (int64_t)D * ((int64_t)HQ + HK) > INT32_MAX) return GDR_INVALID_ARG;
   if (T == 0 || HQ + HK == 0) return GDR_OK;
   if ((HQ > 0 && (!q || !q_out)) || (HK > 0 && (!k || !k_out)) || (R > 0 && !freqs)) return GDR_INVALID_ARG;
   if (R > 0 && !positions && (!cu_seqlens || N <= 0)) return GDR_INVALID_ARG;

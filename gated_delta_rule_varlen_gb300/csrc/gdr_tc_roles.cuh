@@ -20,9 +20,9 @@ constexpr int kTries = 1 << 20;
 __device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done)
-      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -84,6 +84,21 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 // The wait of a whole warp: the same answer on every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   for (int tries = 0; !__all_sync(0xffffffffu, try_phase(bar, parity)); ++tries)
+    if (__any_sync(0xffffffffu, tries > kTries || *abort)) {
+      *abort = 1;
+      return false;
+    }
+  return true;
+}
+// The waits for several barriers at once: a wait costs some 200 clocks even where its phase
+// is complete, together they cost that once.
+struct Phase {
+  uint64_t* bar;
+  uint32_t parity;
+};
+template <typename... P>
+__device__ __forceinline__ bool warp_wait_all(volatile int* abort, P... p) {
+  for (int tries = 0; !__all_sync(0xffffffffu, (try_phase(p.bar, p.parity) & ...)); ++tries)
     if (__any_sync(0xffffffffu, tries > kTries || *abort)) {
       *abort = 1;
       return false;
