@@ -155,7 +155,7 @@ gdr_status attn_check(AttnArgs& a, const int32_t* cu_host, const int32_t* cuk_ho
   return GDR_OK;
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+size_t delta_bytes(const AttnArgs& a) { return ((size_t)a.T * a.H * sizeof(float) + 255) / 256 * 256; }
 unsigned blocks_of(int64_t rows) { return (unsigned)((rows + WARPS - 1) / WARPS); }
 
 }  // namespace
@@ -182,8 +182,10 @@ gdr_status attn_workspace_bytes(int64_t T, int64_t TK, int32_t H, int32_t HK, in
   a.cu = reinterpret_cast<const int*>(16);
   a.cuk = cu_keys_host ? a.cu : nullptr;
   if (const gdr_status rc = attn_check(a, cu_seqlens_host, cu_keys_host); rc != GDR_OK) return rc;
-  if (fwd_scratch_bytes) *fwd_scratch_bytes = 0;
-  if (bwd_scratch_bytes) *bwd_scratch_bytes = up256((size_t)T * H * sizeof(float));
+  AttnPlan p{};
+  if (attn_tc_shape(D)) p = attn_plan(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host);
+  if (fwd_scratch_bytes) *fwd_scratch_bytes = p.fwd_bytes;
+  if (bwd_scratch_bytes) *bwd_scratch_bytes = delta_bytes(a) + p.bwd_bytes;
   return GDR_OK;
 }
 
@@ -214,10 +216,12 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   if (T == 0) return GDR_OK;
   if (!out || !lse) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
-  if (attn_tc_shape(D) && attn_tc_layout(a))
-    return launch_attn_fwd(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host, stream) == cudaSuccess
-               ? GDR_OK
-               : GDR_CUDA_ERROR;
+  if (attn_tc_shape(D) && attn_tc_layout(a)) {
+    const AttnPlan p = attn_plan(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host);
+    if (p.fwd_bytes > 0 && (!scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
+    if (scratch_bytes < p.fwd_bytes) return GDR_WORKSPACE_TOO_SMALL;
+    return launch_attn_fwd(a, p, cu_seqlens_host, static_cast<float*>(scratch), stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  }
   ProfScope ps("attn_rows", stream, (double)T * H);
   k_attn_rows<<<blocks_of(T * H), WARPS * 32, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
@@ -252,16 +256,21 @@ gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   a.dv = reinterpret_cast<__nv_bfloat16*>(dv);
   gdr_status rc = attn_check(a, cu_seqlens_host, cu_keys_host);
   if (rc != GDR_OK) return rc;
-  if (T > 0 && (!dout || !out || !lse || !dq || !scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
+  if (T > 0 && (!dout || !out || !lse || !dq)) return GDR_INVALID_ARG;
   if (TK > 0 && (!dk || !dv)) return GDR_INVALID_ARG;
-  if (T > 0 && scratch_bytes < up256((size_t)T * H * sizeof(float))) return GDR_WORKSPACE_TOO_SMALL;
   if (T == 0 && TK == 0) return GDR_OK;
+  const int32_t* keys_host = cu_keys_host ? cu_keys_host : cu_seqlens_host;
+  AttnPlan p{};
+  if (attn_tc_shape(D)) p = attn_plan(a, cu_seqlens_host, keys_host);
+  const size_t need = delta_bytes(a) + p.bwd_bytes;
+  if (need > 0 && (!scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
+  if (scratch_bytes < need) return GDR_WORKSPACE_TOO_SMALL;
   if ((rc = check_device()) != GDR_OK) return rc;
   a.delta = static_cast<float*>(scratch);
-  if (attn_tc_shape(D) && attn_tc_layout(a))
-    return launch_attn_bwd(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host, stream) == cudaSuccess
-               ? GDR_OK
-               : GDR_CUDA_ERROR;
+  if (attn_tc_shape(D) && attn_tc_layout(a)) {
+    float* rest = reinterpret_cast<float*>(static_cast<char*>(scratch) + delta_bytes(a));
+    return launch_attn_bwd(a, p, cu_seqlens_host, keys_host, rest, stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  }
   if (T > 0) {
     ProfScope ps("attn_dq_rows", stream, (double)T * H);
     k_attn_dq_rows<<<blocks_of(T * H), WARPS * 32, 0, stream>>>(a);

@@ -41,10 +41,11 @@ struct AttnArgs {
 struct KeyRange {
   int lo, hi;
 };
-__device__ __forceinline__ KeyRange keys_of(const AttnArgs& a, int i, int lq, int lk) {
+__host__ __device__ __forceinline__ KeyRange keys_of(const AttnArgs& a, int i, int lq, int lk) {
   KeyRange r{0, lk};
-  if (a.causal) r.hi = min(lk, i + lk - lq + 1);
-  if (a.window && i + lk - lq >= a.window) r.lo = i + lk - lq - a.window + 1;
+  const int last = i + lk - lq;  // (its own place)
+  if (a.causal && last < lk) r.hi = last + 1;
+  if (a.window && last >= a.window) r.lo = last - a.window + 1;
   return r;
 }
 
@@ -88,8 +89,18 @@ __device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __
   return AttnBlock{0, 0, 0, 0, 0};
 }
 
-// The kernels on the tensor cores (gdr_attn_fwd.cu, gdr_attn_bwd.cu); cu, cuk: the host's.
-cudaError_t launch_attn_fwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st);
-cudaError_t launch_attn_bwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st);
+// How the kernels on the tensor cores cut the work: heads side by side in a tile of queries
+// (2^pack), and into how many parts the sums of each kernel's blocks, joined by another
+// kernel from scratch.
+struct AttnPlan {
+  int pack, fwd, dq, dkv;
+  size_t fwd_bytes, bwd_bytes;
+};
+bool attn_tc_shape(int D);
+AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk);  // cu, cuk: the host's
+
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, float* scratch, cudaStream_t st);
+cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, const int32_t* cuk, float* scratch,
+                            cudaStream_t st);
 
 }  // namespace gdr

@@ -26,6 +26,8 @@ struct BwdArgs {
   CUtensorMap q_map, k_map, v_map, do_map;
   AttnArgs a;
   int pack;
+  int parts;    // blocks that share a tile's sums
+  float* part;  // their shares: dQ [parts][T][H][D], or dK and dV [2][parts][TK][HK][D]
   int* err;
 };
 
@@ -97,19 +99,29 @@ __device__ __forceinline__ void store_words(uint32_t at, const uint32_t (&x)[COL
   tc::tmem_st16(at, w);
   tc::tmem_wait_st();
 }
-// 16 accumulator columns of a row, scaled, to 16 (or up to the row's end) elements.
-__device__ __forceinline__ void store16(__nv_bfloat16* row, int c0, int D, uint32_t at, float f, bool any, bool live) {
+// 16 accumulator columns of a row, scaled, to 16 (or up to the row's end) elements, or, a
+// share of them, to FP32.
+__device__ __forceinline__ void store16(__nv_bfloat16* row, float* share, int c0, int D, uint32_t at, float f, bool any, bool live) {
   uint32_t o[16];
   if (any) {
     tc::tmem_ld16(at + c0, o);
     wait_ld(o);
   }
 #pragma unroll
+  for (int k = 0; k < 16; ++k) o[k] = any ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
+  if (!live) return;
+  if (share) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      if (c0 + k < D) *reinterpret_cast<uint4*>(share + c0 + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    return;
+  }
+#pragma unroll
   for (int k = 0; k < 16; k += 8) {
     uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = any ? round_pair(mul2(pair_at(o + k + 2 * e), pack2(f, f))) : 0u;
-    if (live && c0 + k < D) *reinterpret_cast<uint4*>(row + c0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int e = 0; e < 4; ++e) w[e] = round_pair(pair_at(o + k + 2 * e));
+    if (c0 + k < D) *reinterpret_cast<uint4*>(row + c0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -159,10 +171,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     tc::tmem_relinquish();
   }
   const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, groups = a.H >> ba.pack;
-  const AttnBlock b = find_block<true>(a, a.cu, tokens, blockIdx.x / groups);
-  const int h0 = (int)(blockIdx.x % groups) * heads, hk = h0 / (a.H / a.HK);
+  const int item = blockIdx.x / ba.parts, part = blockIdx.x % ba.parts;
+  const AttnBlock b = find_block<true>(a, a.cu, tokens, item / groups);
+  const int h0 = item % groups * heads, hk = h0 / (a.H / a.HK);
   const int i1 = min(b.lq, b.first + tokens);
-  const TileRange r = tiles_of(a, b, b.first, i1);
+  const TileRange all = tiles_of(a, b.lq, b.lk, b.first, i1), r = part_of(all, part, ba.parts);
+  const bool one = all.hi - all.lo == 1;  // the queries' keys fit one tile
   const int n_tiles = r.hi - r.lo;
   tc::tc_fence_before();
   __syncthreads();
@@ -170,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   const uint32_t tmem = s.tmem;
 
   if (warp >= WORKERS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (warp == WORKERS && n_tiles > 0) {  // loads
       if (lane == 0) {
         load_tile<DB>(s.Q, &ba.q_map, h0, b.q0 + b.first, &s.q_full);
@@ -252,9 +266,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       wait_some(&s.done, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a row a thread, of S and dP a quarter's columns
-    const int part = warp >> 2, row = tid & 127, c0 = COLS * part;
+    const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const int token = b.first + (row >> ba.pack), h = h0 + (row & (heads - 1));
     const int64_t at = b.q0 + token;
     const bool live = token < b.lq;
@@ -263,37 +277,37 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     const float base = lse == -INFINITY ? -INFINITY : -lse * LOG2E;  // (rows that see nothing: p = 0)
     const uint64_t cc = pack2(c, c), bb = pack2(base, base);
     const KeyRange kr = keys_of(a, token, b.lq, b.lk);
-    const KeyRange all{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
+    const KeyRange seen{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
     bool ok = true;
     float delta = 0.f;
-    auto exchange = [&](float mine) {  // delta of all quarters
-      s.part[part][row] = mine;
+    auto exchange = [&](float mine, bool write) {  // delta of all quarters
+      s.part[quarter][row] = mine;
       warp_arrive(&s.part_full);
       ok = ok && warp_wait(&s.part_full, 0, ab);
       delta = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
-      if (live && part == 0) a.delta[h * a.T + at] = delta;
+      if (live && write && quarter == 0) a.delta[h * a.T + at] = delta;
     };
-    if (n_tiles > 1) {
+    if (n_tiles > 0 && !one) {
       constexpr int PIECES = DB * 8 / QUARTERS;  // of 8 elements of a row
       uint4 o[PIECES];
       const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int d = (part * PIECES + i) * 8;
+        const int d = (quarter * PIECES + i) * 8;
         o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
       }
       ok = warp_wait(&s.do_full, 0, ab);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int pc = part * PIECES + i;
+        const int pc = quarter * PIECES + i;
         const uint4 g = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
         const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
       }
-      exchange(sum);
-    } else if (n_tiles == 0 && live && part == 0) {
+      exchange(sum, r.lo == all.lo);
+    } else if (all.lo == all.hi && part == 0 && live && quarter == 0) {
       a.delta[h * a.T + at] = 0.f;
     }
 #pragma unroll 1
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           unpack2(fma2(pair_at(x + 2 * i), cc, bb), e, f);
           p[i] = pack2(ex2(e), ex2(f));
         }
-        if (j * TILE < all.lo || (j + 1) * TILE > all.hi) {
+        if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
           const int lo = kr.lo - j * TILE - c0, hi = kr.hi - j * TILE - c0;
 #pragma unroll
           for (int i = 0; i < COLS / 2; ++i) {
@@ -335,11 +349,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         for (int i = 0; i < COLS; ++i)
           if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
       }
-      if (n_tiles == 1) {
+      if (one) {
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < COLS / 2; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
-        exchange(sum_of(add2(sum[0], sum[1])));
+        exchange(sum_of(add2(sum[0], sum[1])), true);
         if (!ok) break;
       }
       const uint64_t minus = pack2(-delta, -delta);
@@ -354,9 +368,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       tc::tc_fence_after();
     }
     if (ok) {
-      __nv_bfloat16* dq = a.dq + (at * a.H + h) * a.D;
+      const int64_t to = (at * a.H + h) * a.D;
+      float* share = ba.parts > 1 ? ba.part + part * a.T * a.H * a.D + to : nullptr;
 #pragma unroll
-      for (int i = 0; i < DB; ++i) store16(dq, DB * 16 * part + 16 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
+      for (int i = 0; i < DB; ++i) store16(a.dq + to, share, DB * 16 * quarter + 16 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
     }
   }
   tc::tc_fence_before();
@@ -412,21 +427,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
     tc::tmem_relinquish();
   }
   const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, G = a.H / a.HK;
-  const AttnBlock b = find_block<false>(a, a.cuk, TILE, blockIdx.x / a.HK);
-  const int hk = (int)(blockIdx.x % a.HK);
+  const int item = blockIdx.x / ba.parts, part = blockIdx.x % ba.parts;
+  const AttnBlock b = find_block<false>(a, a.cuk, TILE, item / a.HK);
+  const int hk = item % a.HK;
   // the tiles of queries that see any of the keys [first, last]: each head group's
   const int off = b.lk - b.lq, last = min(b.lk, b.first + TILE) - 1;
-  const int qlo = a.causal ? max(0, b.first - off) : 0;
-  const int qhi = a.window ? (int)min((int64_t)b.lq, (int64_t)last - off + a.window) : b.lq;
-  const int t0 = qlo / tokens, per = qhi > qlo ? (qhi + tokens - 1) / tokens - t0 : 0;
-  const int n_tiles = per * (G >> ba.pack);
+  const TileRange r = query_tiles_of(a, b.lq, b.lk, b.first, last, tokens);
+  const int t0 = r.lo, per = r.hi - r.lo;
+  const TileRange mine = part_of(TileRange{0, per * (G >> ba.pack)}, part, ba.parts);
+  const int n_tiles = mine.hi - mine.lo, g0 = per ? mine.lo / per : 0, tt0 = per ? mine.lo % per : 0;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem;
 
   if (warp >= WORKERS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (warp == WORKERS && n_tiles > 0) {  // loads
       if (lane == 0) {
         load_tile<DB>(s.K, &ba.k_map, hk, b.k0 + b.first, &s.k_full);
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       Ring<QS> qr;
       Ring<OS> orr;
       int n = 0, cleared = 0;
-      for (int g = 0, t = 0; n < n_tiles; ++n) {
+      for (int g = g0, t = tt0; n < n_tiles; ++n) {
         const int token = (t0 + t) * tokens, rows = (int)min((int64_t)TILE, (int64_t)(b.lq - token) << ba.pack);
         const bool clear = rows < TILE;
         const int h = hk * G + g * heads;
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       commit(&s.done);
       wait_some(&s.done, 0);
     } else if (warp == WORKERS + 2 && n_tiles > 0) {  // lse and delta of a tile's queries
-      for (int n = 0, g = 0, t = 0; n < n_tiles; ++n) {
+      for (int n = 0, g = g0, t = tt0; n < n_tiles; ++n) {
         float l[4], d[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -548,16 +564,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a key a thread, of S^T and dP^T a quarter's queries
-    const int part = warp >> 2, row = tid & 127, c0 = COLS * part;
+    const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const int key = b.first + row;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = a.scale * LOG2E;
     const uint64_t cc = pack2(c, c);
     bool ok = true;
 #pragma unroll 1
-    for (int n = 0, t = 0; n < n_tiles; ++n) {
+    for (int n = 0, t = tt0; n < n_tiles; ++n) {
       ok = warp_wait_all(ab, Phase{&s.row_full[n & 1], (uint32_t)(n >> 1) & 1}, Phase{&s.s_full, (uint32_t)n & 1});
       if (!ok) break;
       tc::tc_fence_after();
@@ -614,11 +630,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       tc::tc_fence_after();
     }
     if (ok) {
-      const int64_t at = ((int64_t)(b.k0 + key) * a.HK + hk) * a.D;
+      const int64_t to = ((int64_t)(b.k0 + key) * a.HK + hk) * a.D, all = a.TK * a.HK * a.D;
+      float *dk = nullptr, *dv = nullptr;
+      if (ba.parts > 1) {
+        dk = ba.part + part * all + to;
+        dv = dk + ba.parts * all;
+      }
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        store16(a.dk + at, DB * 16 * part + 16 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
-        store16(a.dv + at, DB * 16 * part + 16 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
+        store16(a.dk + to, dk, DB * 16 * quarter + 16 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
+        store16(a.dv + to, dv, DB * 16 * quarter + 16 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
       }
     }
   }
@@ -626,6 +647,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
   __syncthreads();
   if (tid == 0 && s.abort) atomicExch(ba.err, 11);
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// The shares of a sum, [parts][n], added in their order (blockIdx.y: dK, dV).
+__global__ void __launch_bounds__(256) k_attn_sum(const float* __restrict__ part, int parts, int64_t n, __nv_bfloat16* x, __nv_bfloat16* y) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  previous_ended();
+  if (i >= n) return;
+  part += blockIdx.y * parts * n + i;
+  float s[8] = {};
+  for (int p = 0; p < parts; ++p, part += n) {
+    const float4 u = *reinterpret_cast<const float4*>(part), v = *reinterpret_cast<const float4*>(part + 4);
+    s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w, s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+  }
+  vstore<__nv_bfloat16, 8>((blockIdx.y ? y : x) + i, s);
 }
 
 template <typename K>
@@ -643,12 +678,14 @@ constexpr size_t bytes_of() {
 
 }  // namespace
 
-cudaError_t launch_attn_bwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st) {
+cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, const int32_t* cuk, float* scratch,
+                            cudaStream_t st) {
   BwdArgs f{};
   f.a = a;
   f.err = device_error_ptr();
   if (!f.err) return cudaErrorUnknown;
-  f.pack = attn_pack(a, cu);
+  f.pack = p.pack;
+  f.part = scratch;
   const int tokens = TILE >> f.pack;
   int64_t qblocks = 0, kblocks = 0;
   for (int i = 0; i < a.N; ++i) {
@@ -660,17 +697,34 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const int32_t* cu, const int32_t*
     return cudaErrorInvalidValue;
   if (a.TK > 0 && (!attn_map(&f.k_map, a.k, a.TK, a.HK, a.D, 1, TILE) || !attn_map(&f.v_map, a.v, a.TK, a.HK, a.D, 1, TILE)))
     return cudaErrorInvalidValue;
+  auto sum = [&](int64_t n, __nv_bfloat16* x, __nv_bfloat16* y) {  // (n is a multiple of 8, as D is)
+    const int64_t blocks = (n / 8 + 255) / 256;
+    if (f.parts == 1) return cudaSuccess;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    ProfScope ps("attn_sum", st, (double)n / a.D);
+    return launch_early(k_attn_sum, dim3((unsigned)blocks, y ? 2 : 1), 256, 0, st, f.part, f.parts, n, x, y);
+  };
   if (qblocks > 0) {
-    ProfScope ps("attn_dq", st, (double)a.T * a.H);
-    const int64_t blocks = qblocks * (a.H >> f.pack);
-    if (cudaError_t e = a.D <= 64 ? go(k_attn_dq<1>, bytes_of<DqSmem<1>>(), blocks, f, st)
-                                  : go(k_attn_dq<2>, bytes_of<DqSmem<2>>(), blocks, f, st))
-      return e;
+    f.parts = p.dq;
+    const int64_t blocks = qblocks * (a.H >> f.pack) * f.parts;
+    {
+      ProfScope ps("attn_dq", st, (double)a.T * a.H);
+      if (cudaError_t e = a.D <= 64 ? go(k_attn_dq<1>, bytes_of<DqSmem<1>>(), blocks, f, st)
+                                    : go(k_attn_dq<2>, bytes_of<DqSmem<2>>(), blocks, f, st))
+        return e;
+    }
+    if (cudaError_t e = sum(a.T * a.H * a.D, a.dq, nullptr)) return e;
   }
   if (kblocks > 0) {
-    ProfScope ps("attn_dkv", st, (double)a.TK * a.HK);
-    return a.D <= 64 ? go(k_attn_dkv<1>, bytes_of<DkvSmem<1>>(), kblocks * a.HK, f, st)
-                     : go(k_attn_dkv<2>, bytes_of<DkvSmem<2>>(), kblocks * a.HK, f, st);
+    f.parts = p.dkv;
+    const int64_t blocks = kblocks * a.HK * f.parts;
+    {
+      ProfScope ps("attn_dkv", st, (double)a.TK * a.HK);
+      if (cudaError_t e = a.D <= 64 ? go(k_attn_dkv<1>, bytes_of<DkvSmem<1>>(), blocks, f, st)
+                                    : go(k_attn_dkv<2>, bytes_of<DkvSmem<2>>(), blocks, f, st))
+        return e;
+    }
+    if (cudaError_t e = sum(a.TK * a.HK * a.D, a.dk, a.dv)) return e;
   }
   return cudaSuccess;
 }

@@ -24,6 +24,8 @@ struct FwdArgs {
   CUtensorMap q_map, k_map, v_map;
   AttnArgs a;
   int pack;   // log2 of the heads side by side in a tile: row r is token r >> pack, head r & (2^pack - 1)
+  int parts;  // blocks that share the keys of two tiles
+  float *part_out, *part_lse;  // [parts][T][H][D], [parts][H][T]
   int* err;
 };
 
@@ -37,7 +39,8 @@ struct FwdSmem {
   unsigned char Q[2][DB * BLK];
   unsigned char KV[STAGES][DB * BLK];  // K and V tiles in turn
   uint64_t q_full[2], full[STAGES], empty[STAGES], cleared;
-  uint64_t s_full[2], p_full[2], o_full[2], done;
+  uint64_t s_full[2], p_full[2], o_full[2], merged, done;
+  float m[TILE], l[TILE];
   uint32_t tmem;
   int abort;
 };
@@ -46,8 +49,8 @@ template <int DB>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__ FwdArgs fa) {
   using Smem = FwdSmem<DB>;
   constexpr int ST = Smem::STAGES;
-  extern __shared__ unsigned char attn_smem[];
-  Smem& s = *reinterpret_cast<Smem*>(tc::align1024(attn_smem));
+  extern __shared__ __align__(1024) unsigned char attn_smem[];
+  Smem& s = *reinterpret_cast<Smem*>(attn_smem);
   const AttnArgs& a = fa.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
@@ -64,6 +67,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         tc::mbar_init(&s.empty[i], 1);
       }
       tc::mbar_init(&s.cleared, 1);
+      tc::mbar_init(&s.merged, 4);
       tc::mbar_init(&s.done, 1);
       s.abort = 0;
       tc::mbar_fence_init();
@@ -73,41 +77,51 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
     tc::tmem_relinquish();
   }
   const int heads = 1 << fa.pack, tokens = TILE >> fa.pack;  // of a tile
-  const int groups = a.H >> fa.pack;
-  const AttnBlock b = find_block<true>(a, a.cu, 2 * tokens, blockIdx.x / groups);
-  const int h0 = (int)(blockIdx.x % groups) * heads, hk = h0 / (a.H / a.HK);
+  const int groups = a.H >> fa.pack, item = blockIdx.x / fa.parts, part = blockIdx.x % fa.parts;
+  const AttnBlock b = find_block<true>(a, a.cu, 2 * tokens, item / groups);
+  const int h0 = item % groups * heads, hk = h0 / (a.H / a.HK);
   TileRange r[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int i0 = b.first + t * tokens;
-    r[t] = tiles_of(a, b, i0, min(b.lq, i0 + tokens));
+    r[t] = tiles_of(a, b.lq, b.lk, i0, min(b.lq, i0 + tokens));
   }
-  // (an empty range follows the other one)
-  if (r[0].lo >= r[0].hi) r[0].lo = r[0].hi = r[1].lo;
-  if (r[1].lo >= r[1].hi) r[1].lo = r[1].hi = r[0].hi;
-  const int j0 = min(r[0].lo, r[1].lo), j1 = max(r[0].hi, r[1].hi);
+  TileRange all{min(r[0].lo, r[1].lo), max(r[0].hi, r[1].hi)};
+  if (r[0].lo >= r[0].hi) all = r[1];
+  if (r[1].lo >= r[1].hi) all = r[0];
+  all = part_of(all, part, fa.parts);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    r[t].lo = max(r[t].lo, all.lo);
+    r[t].hi = min(r[t].hi, all.hi);
+  }
+  // Where the second tile has no queries (few, of long keys), it takes every other key tile
+  // of the first's: what waits on one pair of products goes on with the other.
+  const bool dual = b.first + tokens >= b.lq && r[0].hi - r[0].lo > 1;
+  if (dual) r[1] = r[0];
+  const int step = dual ? 2 : 1;
+  auto works = [&](int t, int j) { return dual ? ((j - all.lo) & 1) == t : j >= r[t].lo && j < r[t].hi; };
+  const int j0 = all.lo, j1 = all.hi;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8 && j0 < j1) {  // loads
       if (lane == 0)
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 3 - step; ++t)
           if (r[t].lo < r[t].hi) {
             tc::mbar_arrive_expect_tx(&s.q_full[t], DB * BLK);
             for (int c = 0; c < DB; ++c)
               tc::tma_load_3d(s.Q[t] + c * BLK, &fa.q_map, 64 * c, h0, b.q0 + b.first + t * tokens, &s.q_full[t]);
           }
       __syncwarp();
-      const int n = 2 * (j1 - j0);
-      int i = 0;
-      for (int st = 0, ph = 0; i < n; ++i) {
-        const int j = j0 + (i >> 1);
-        const bool isv = i & 1;
-        if (i >= ST && !warp_wait(&s.empty[st], ph ^ 1, ab)) break;
+      // K of the first `step` tiles, then V of each and K of the one `step` behind it
+      int i = 0, st = 0, ph = 0;
+      auto load = [&](int j, bool isv) {
+        if (i >= ST && !warp_wait(&s.empty[st], ph ^ 1, ab)) return false;
         const int rows = b.lk - j * TILE;
         uint64_t* bar = isv && rows < TILE ? &s.cleared : &s.full[st];
         if (lane == 0) {
@@ -116,8 +130,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
             tc::tma_load_3d(s.KV[st] + c * BLK, isv ? &fa.v_map : &fa.k_map, 64 * c, hk, b.k0 + j * TILE, bar);
         }
         __syncwarp();
+        ++i;
         if (isv && rows < TILE) {  // the document's last tile: clear what lies behind it
-          if (!warp_wait(&s.cleared, 0, ab)) break;
+          if (!warp_wait(&s.cleared, 0, ab)) return false;
           for (int e = rows * 8 + lane; e < TILE * 8; e += 32)
             for (int c = 0; c < DB; ++c) *reinterpret_cast<uint4*>(s.KV[st] + c * BLK + e * 16) = make_uint4(0, 0, 0, 0);
           tc::fence_proxy_async();
@@ -127,17 +142,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           st = 0;
           ph ^= 1;
         }
+        return true;
+      };
+      bool ok = true;
+      for (int j = j0; j < j0 + step && ok; ++j) ok = load(j, false);
+      for (int j = j0; j < j1 && ok; ++j) {
+        ok = load(j, true);
+        if (ok && j + step < j1) ok = load(j + step, false);
       }
-      if (i < n) {  // given up: the copies in flight land before the block ends
+      if (!ok) {  // given up: the copies in flight land before the block ends
         for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
-        for (int t = 0; t < 2; ++t)
+        wait_some(&s.cleared, 0);
+        for (int t = 0; t < 3 - step; ++t)
           if (r[t].lo < r[t].hi) wait_some(&s.q_full[t], 0);
       }
     } else if (warp == 9 && j0 < j1) {  // products
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const uint32_t id_o = tc::idesc_bf16(TILE, (a.D + 15) / 16 * 16) | tc::kIdescTransposeB;
       const int ks = (a.D + 15) / 16;
-      uint32_t q_lo[2] = {desc_lo(s.Q[0]), desc_lo(s.Q[1])};
+      uint32_t q_lo[2] = {desc_lo(s.Q[0]), desc_lo(s.Q[dual ? 0 : 1])};
       auto score = [&](int t, int st) {
         const uint32_t k_lo = desc_lo(s.KV[st]);
 #pragma unroll
@@ -159,21 +182,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         return p;
       };
       auto stage = [&](const Phase& p) { return (int)(p.bar - s.full); };
-      Phase kp = next();
-      ok = warp_wait(kp.bar, kp.parity, ab);
-      for (int t = 0; t < 2 && ok; ++t)
-        if (r[t].lo < r[t].hi) {
-          ok = warp_wait(&s.q_full[t], 0, ab);
-          if (ok && r[t].lo == j0) score(t, stage(kp));
-        }
-      if (ok) commit(&s.empty[stage(kp)]);
+      Phase kp{};
+      for (int t = 0; t < 3 - step && ok; ++t)
+        if (r[t].lo < r[t].hi) ok = warp_wait(&s.q_full[t], 0, ab);
+      for (int j = j0; j < j0 + step && ok; ++j) {
+        kp = next();
+        ok = warp_wait(kp.bar, kp.parity, ab);
+        if (!ok) break;
+        for (int t = 0; t < 2; ++t)
+          if (works(t, j)) score(t, stage(kp));
+        commit(&s.empty[stage(kp)]);
+      }
       for (int j = j0; j < j1 && ok; ++j) {
-        const bool more = j + 1 < j1;
+        const bool more = j + step < j1;
         const Phase vp = next();
         if (more) kp = next();
         bool loaded = false;  // V of this step, K of the next
         for (int t = 0; t < 2 && ok; ++t) {
-          const bool here = j >= r[t].lo && j < r[t].hi;
+          const bool here = works(t, j);
           const Phase pp{here ? &s.p_full[t] : kp.bar, here ? (uint32_t)used[t] & 1 : kp.parity};
           if (!loaded) {
             ok = more ? warp_wait_all(ab, vp, kp, here ? pp : kp) : warp_wait_all(ab, vp, here ? pp : vp);
@@ -189,9 +215,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
             for (int k = 0; k < TILE / 16; ++k)
               mma_ts(tmem + T_O + t * TILE, tmem + T_S + t * TILE + 8 * k, v_lo + k * (16 * 128 >> 4), id_o, used[t] > 0 || k > 0);
             ++used[t];
-            if (j + 1 == r[t].hi) commit(&s.o_full[t]);
+            if (j + step >= r[t].hi) commit(&s.o_full[t]);
           }
-          if (more && j + 1 >= r[t].lo && j + 1 < r[t].hi) score(t, stage(kp));
+          if (more && works(t, j + step)) score(t, stage(kp));
         }
         if (!ok) break;
         commit(&s.empty[stage(vp)]);
@@ -201,19 +227,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
       wait_some(&s.done, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     const int t = warp >> 2, row = tid & 127;
-    const int token = b.first + t * tokens + (row >> fa.pack), h = h0 + (row & (heads - 1));
+    const int i0 = b.first + (dual ? 0 : t * tokens), i1 = min(b.lq, i0 + tokens);
+    const int token = i0 + (row >> fa.pack), h = h0 + (row & (heads - 1));
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + T_S + t * TILE, to = lanes + T_O + t * TILE;
     const bool live = token < b.lq;
     const KeyRange kr = keys_of(a, token, b.lq, b.lk);
     const float c = a.scale * LOG2E;
     float m = -INFINITY, l = 0.f;  // the maximum (of scores before the scale), the sum
-    const int i0 = b.first + t * tokens, i1 = min(b.lq, i0 + tokens);
-    const KeyRange all{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, i0, b.lq, b.lk).hi};  // keys every row sees
+    const KeyRange seen{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, i0, b.lq, b.lk).hi};  // keys every row sees
     bool ok = true;
-    for (int j = r[t].lo, n = 0; j < r[t].hi; ++j, ++n) {
+    for (int j = r[t].lo + (dual ? t : 0), n = 0; j < r[t].hi; j += step, ++n) {
       ok = warp_wait(&s.s_full[t], n & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
@@ -222,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
       for (int i = 0; i < TILE; i += 32) tc::tmem_ld32(ts + i, x + i);
       tc::tmem_wait_ld();
       pin(x);
-      if (j * TILE < all.lo || (j + 1) * TILE > all.hi) {
+      if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
         const int lo = kr.lo - j * TILE, hi = kr.hi - j * TILE;
 #pragma unroll
         for (int i = 0; i < TILE; ++i) x[i] = i >= lo && i < hi ? x[i] : 0xff800000u;
@@ -272,12 +298,45 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
     const int64_t at = (int64_t)(b.q0 + token);
     const bool any = r[t].lo < r[t].hi;
     if (ok && any) {
-      ok = warp_wait(&s.o_full[t], 0, ab);
+      ok = dual ? warp_wait_all(ab, Phase{&s.o_full[0], 0}, Phase{&s.o_full[1], 0}) : warp_wait(&s.o_full[t], 0, ab);
       tc::tc_fence_after();
     }
-    if (ok) {
+    // The halves of a dual tile: the second's sums and out cross shared memory (the key tiles',
+    // which nothing reads any more) to the first.
+    constexpr int PITCH = DB * 64 + 4;
+    static_assert(TILE * PITCH * 4 <= sizeof(s.KV), "a tile of FP32");
+    float* swap = reinterpret_cast<float*>(s.KV) + row * PITCH;
+    float f0 = 1.f, f1 = 0.f;
+    if (dual && t == 1 && ok) {
+      s.m[row] = m;
+      s.l[row] = l;
+      if (__any_sync(0xffffffffu, live)) {
+#pragma unroll 1
+        for (int i = 0; i < DB * 64; i += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(to + i, o);
+          tc::tmem_wait_ld();
+          pin(o);
+          if (live)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(swap + i + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+      warp_arrive(&s.merged);
+    } else if (dual && ok) {
+      ok = warp_wait(&s.merged, 0, ab);
+      const float m1 = s.m[row], top = fmaxf(m, m1);
+      f0 = m == -INFINITY ? 0.f : ex2((m - top) * c);
+      f1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * c);
+      l = fmaf(l, f0, s.l[row] * f1);
+      m = top;
+    }
+    if (ok && !(dual && t == 1) && __any_sync(0xffffffffu, live)) {
       const float f = l == 0.f ? 0.f : 1.f / l;
+      f0 *= f;
+      f1 *= f;
       __nv_bfloat16* out = a.out + (at * a.H + h) * a.D;
+      float* part_out = fa.part_out + ((part * a.T + at) * a.H + h) * a.D;
 #pragma unroll 1
       for (int i = 0; i < DB * 64; i += 32) {
         uint32_t o[32];
@@ -286,19 +345,37 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           tc::tmem_wait_ld();
           pin(o);
         }
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * f0;
+        if (dual && live)
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(swap + i + k);
+            v[k] = fmaf(x.x, f1, v[k]);
+            v[k + 1] = fmaf(x.y, f1, v[k + 1]);
+            v[k + 2] = fmaf(x.z, f1, v[k + 2]);
+            v[k + 3] = fmaf(x.w, f1, v[k + 3]);
+          }
+        if (fa.parts > 1) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            if (live && i + k < a.D) *reinterpret_cast<float4*>(part_out + i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          continue;
+        }
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(l == 0.f ? 0.f : __uint_as_float(o[k + 2 * e]) * f,
-                                                           l == 0.f ? 0.f : __uint_as_float(o[k + 2 * e + 1]) * f);
-            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[k + 2 * e], v[k + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&x);
           }
           if (live && i + k < a.D) *reinterpret_cast<uint4*>(out + i + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (live) a.lse[h * a.T + at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718f;
+      float* lse = fa.parts > 1 ? fa.part_lse + (int64_t)part * a.H * a.T : a.lse;
+      if (live) lse[h * a.T + at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718f;
     }
   }
   tc::tc_fence_before();
@@ -307,30 +384,137 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
+// The parts of a query's keys joined: lse = log sum e^lse_p, out = sum e^(lse_p - lse)
+// out_p.  A warp a query and head.
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ FwdArgs fa) {
+  const AttnArgs& a = fa.a;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  previous_ended();
+  if (row >= a.T * a.H) return;
+  const int64_t t = row / a.H, at = row % a.H * a.T + t, stride = a.T * a.H;
+  float top = -INFINITY;
+  for (int p = 0; p < fa.parts; ++p) top = fmaxf(top, fa.part_lse[p * stride + at]);
+  const bool none = top == -INFINITY;
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < fa.parts && !none; ++p) {
+    const float w = ex2((fa.part_lse[p * stride + at] - top) * LOG2E);
+    sum += w;
+    if (4 * lane < a.D) {
+      const float4 x = *reinterpret_cast<const float4*>(fa.part_out + (p * stride + row) * a.D + 4 * lane);
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+  }
+  const float f = none ? 0.f : 1.f / sum;
+  if (4 * lane < a.D) {
+    const float v[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+    vstore<__nv_bfloat16, 4>(a.out + row * a.D + 4 * lane, v);
+  }
+  if (lane == 0) a.lse[at] = none ? -INFINITY : top + logf(sum);
+}
+
 }  // namespace
 
-cudaError_t launch_attn_fwd(const AttnArgs& a, const int32_t* cu, const int32_t* cuk, cudaStream_t st) {
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, float* scratch, cudaStream_t st) {
   FwdArgs f{};
   f.a = a;
   f.err = device_error_ptr();
   if (!f.err) return cudaErrorUnknown;
-  f.pack = attn_pack(a, cu);
+  f.pack = p.pack;
+  f.parts = p.fwd;
+  f.part_out = scratch;
+  f.part_lse = scratch + (int64_t)p.fwd * a.T * a.H * a.D;
   const int per = 2 * (TILE >> f.pack);
   int64_t blocks = 0;
   for (int i = 0; i < a.N; ++i) blocks += (cu[i + 1] - cu[i] + per - 1) / per;
   if (!attn_map(&f.q_map, a.q, a.T, a.H, a.D, 1 << f.pack, TILE >> f.pack)) return cudaErrorInvalidValue;
   if (a.TK > 0 && (!attn_map(&f.k_map, a.k, a.TK, a.HK, a.D, 1, TILE) || !attn_map(&f.v_map, a.v, a.TK, a.HK, a.D, 1, TILE)))
     return cudaErrorInvalidValue;
-  blocks *= a.H >> f.pack;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  blocks *= (a.H >> f.pack) * f.parts;
+  const int64_t rows = (a.T * a.H + 7) / 8;
+  if (blocks > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
   auto go = [&](auto kernel, size_t smem) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
     kernel<<<(unsigned)blocks, THREADS, smem, st>>>(f);
     return cudaGetLastError();
   };
-  static_assert(sizeof(FwdSmem<1>) + 1024 <= 232448 && sizeof(FwdSmem<2>) + 1024 <= 232448, "227 KB of shared memory a block");
-  ProfScope ps("attn_fwd", st, (double)a.T * a.H);
-  return a.D <= 64 ? go(k_attn_fwd<1>, sizeof(FwdSmem<1>) + 1024) : go(k_attn_fwd<2>, sizeof(FwdSmem<2>) + 1024);
+  static_assert(sizeof(FwdSmem<1>) <= 232448 && sizeof(FwdSmem<2>) <= 232448, "227 KB of shared memory a block");
+  {
+    ProfScope ps("attn_fwd", st, (double)a.T * a.H);
+    if (cudaError_t e = a.D <= 64 ? go(k_attn_fwd<1>, sizeof(FwdSmem<1>)) : go(k_attn_fwd<2>, sizeof(FwdSmem<2>))) return e;
+  }
+  if (f.parts == 1) return cudaSuccess;
+  ProfScope ps("attn_join", st, (double)a.T * a.H);
+  return launch_early(k_attn_join, dim3((unsigned)rows), 256, 0, st, f);
 }
+
+// Heads that share their keys lie side by side while the longest document's queries alone do
+// not fill a tile.
+//
+// Parts: few blocks, or few of them much longer than the rest, leave SMs without work.  The
+// number with the least estimated time is taken, in steps of a block (a pair of tiles): kStart
+// to start and end a block, the join's traffic in steps' worth of bytes.  Only plans of up to
+// four waves of blocks are looked at: more of them are even enough.
+AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
+  AttnPlan p{0, 1, 1, 1, 0, 0};
+  int most = 0;
+  for (int i = 0; i < a.N; ++i) most = std::max(most, cu[i + 1] - cu[i]);
+  const int G = a.H / a.HK;
+  while (p.pack < 7 && G % (2 << p.pack) == 0 && ((int64_t)most << p.pack) < TILE) ++p.pack;
+  const double sms = 152.0, kStart = 3.0, kBytes = 8e6;  // (bytes that HBM moves in a step)
+  const int tokens = TILE >> p.pack;
+  // parts of blocks of `per` rows of `lens`, `heads` a block each, `rows` of FP32 left by a part
+  auto parts = [&](const int32_t* lens, int per, int64_t heads, double row_bytes, auto tiles) {
+    int64_t blocks = 0;
+    for (int i = 0; i < a.N; ++i) blocks += (lens[i + 1] - lens[i] + per - 1) / per;
+    blocks *= heads;
+    if (blocks == 0 || blocks > 4 * 152) return 1;
+    int64_t total = 0, longest = 0;
+    for (int i = 0; i < a.N; ++i)
+      for (int at = 0; at < lens[i + 1] - lens[i]; at += per) {
+        const int64_t n = tiles(cu[i + 1] - cu[i], cuk[i + 1] - cuk[i], at);
+        total += n * heads;
+        longest = std::max(longest, n);
+      }
+    int best = 1;
+    double least = 0;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (s > 1 && s > longest / 2) break;
+      const double one = (double)((longest + s - 1) / s) + kStart, work = (total + kStart * blocks * s) / sms;
+      double time = blocks * s <= 152 ? one : std::max(one, work) + 0.3 * one;
+      if (s > 1) time += 2.0 + 2.0 * s * row_bytes / kBytes;
+      if (s == 1 || time < 0.9 * least) {
+        best = s;
+        least = time;
+      }
+    }
+    return best;
+  };
+  const double out_bytes = 4.0 * a.T * a.H * a.D, key_bytes = 8.0 * a.TK * a.HK * a.D;
+  p.fwd = parts(cu, 2 * tokens, a.H >> p.pack, out_bytes, [&](int lq, int lk, int at) {
+    const TileRange r = tiles_of(a, lq, lk, at, std::min(lq, at + 2 * tokens));
+    const int n = r.hi - r.lo;
+    return at + tokens >= lq ? (n + 1) / 2 : n;  // (two key tiles a step where the second tile has no queries)
+  });
+  p.dq = parts(cu, tokens, a.H >> p.pack, out_bytes, [&](int lq, int lk, int at) {
+    const TileRange r = tiles_of(a, lq, lk, at, std::min(lq, at + tokens));
+    return r.hi - r.lo;
+  });
+  p.dkv = parts(cuk, TILE, a.HK, key_bytes, [&](int lq, int lk, int at) {
+    const TileRange r = query_tiles_of(a, lq, lk, at, std::min(lk, at + TILE) - 1, tokens);
+    return (r.hi - r.lo) * (G >> p.pack);
+  });
+  auto floats = [](int parts, double n) { return parts > 1 ? (size_t)parts * (size_t)n * sizeof(float) : 0; };
+  const size_t rows = (size_t)a.T * a.H;
+  p.fwd_bytes = floats(p.fwd, (double)rows * (a.D + 1));
+  p.bwd_bytes = std::max(floats(p.dq, (double)rows * a.D), floats(p.dkv, 2.0 * a.TK * a.HK * a.D));
+  return p;
+}
+
+bool attn_tc_shape(int D) { return D % 8 == 0 && D <= 128; }
 
 }  // namespace gdr

@@ -9,15 +9,30 @@ namespace gdr {
 
 constexpr int TILE = 128;  // rows of a tile of queries or keys
 
-// The key tiles [lo, hi) that tokens [i0, i1) of a document see.
+// The tiles [lo, hi) that a block goes through.
 struct TileRange {
   int lo, hi;
 };
-__device__ __forceinline__ TileRange tiles_of(const AttnArgs& a, const AttnBlock& b, int i0, int i1) {
+// Of keys: those that queries [i0, i1) of a document see.
+__host__ __device__ __forceinline__ TileRange tiles_of(const AttnArgs& a, int lq, int lk, int i0, int i1) {
   if (i0 >= i1) return {0, 0};
-  const KeyRange first = keys_of(a, i0, b.lq, b.lk), last = keys_of(a, i1 - 1, b.lq, b.lk);
+  const KeyRange first = keys_of(a, i0, lq, lk), last = keys_of(a, i1 - 1, lq, lk);
   if (last.hi <= first.lo) return {0, 0};
   return {first.lo / TILE, (last.hi + TILE - 1) / TILE};
+}
+// Of queries, `tokens` a tile: those that see any of the keys [first, last].
+__host__ __device__ __forceinline__ TileRange query_tiles_of(const AttnArgs& a, int lq, int lk, int first, int last, int tokens) {
+  const int off = lk - lq;
+  const int lo = a.causal && first > off ? first - off : 0;
+  int hi = lq;
+  if (a.window && (int64_t)last - off + a.window < lq) hi = last - off + a.window;
+  if (hi <= lo) return {0, 0};
+  return {lo / tokens, (hi + tokens - 1) / tokens};
+}
+// Part `part` of `parts` of a range.
+__device__ __forceinline__ TileRange part_of(const TileRange& r, int part, int parts) {
+  const int64_t n = r.hi - r.lo;
+  return {r.lo + (int)(n * part / parts), r.lo + (int)(n * (part + 1) / parts)};
 }
 
 template <int N>
@@ -26,9 +41,7 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {  // nothing that reads t
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Whether the kernels take the arguments: what TMA addresses, and tiles of up to 128 columns.
-inline bool attn_tc_shape(int D) { return D % 8 == 0 && D <= 128; }
-
+// Whether TMA addresses the tensors.
 inline bool attn_tc_layout(const AttnArgs& a) {
   for (const AttnRows* t : {&a.q, &a.k, &a.v, &a.dout})
     if (t->p && (((uintptr_t)t->p & 15) != 0 || t->s0 <= 0 || t->s1 <= 0 || t->s0 % 8 != 0 || t->s1 % 8 != 0)) return false;
@@ -49,16 +62,6 @@ inline bool attn_map(CUtensorMap* map, const AttnRows& t, int64_t T, int H, int 
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(t.p), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Heads that share their keys lie side by side in a tile of queries (row r is token r >> pack,
-// head r & (2^pack - 1)) while the longest document's queries alone do not fill it.
-inline int attn_pack(const AttnArgs& a, const int32_t* cu) {
-  int most = 0, pack = 0;
-  for (int i = 0; i < a.N; ++i) most = std::max(most, cu[i + 1] - cu[i]);
-  const int G = a.H / a.HK;
-  while (pack < 7 && G % (2 << pack) == 0 && ((int64_t)most << pack) < TILE) ++pack;
-  return pack;
 }
 
 }  // namespace gdr

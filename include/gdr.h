@@ -263,7 +263,7 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
  * sconv_step, ssm_gates, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
  * gdn_step, norm_fwd, norm_bwd, norm_wgrad, lnorm_fwd, lnorm_bwd, lnorm_wgrad,
- * rope, attn_fwd, attn_dq, attn_dkv, attn_rows, attn_dq_rows, attn_dkv_rows. */
+ * rope, attn_fwd, attn_join, attn_dq, attn_dkv, attn_sum, attn_rows, attn_dq_rows, attn_dkv_rows. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
 
