@@ -136,7 +136,7 @@ struct DqSmem {
   unsigned char K[KS][DB * BLK], V[VS][DB * BLK];
   float part[QUARTERS][TILE];          // the quarters' shares of delta
   uint64_t q_full, do_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], cleared;
-  uint64_t s_full[2], dp_full, dp_read, ds_full, part_full, done;
+  uint64_t s_full[2], dp_full, dp_read, ds_full, dq_done[2], part_full, done;
   uint32_t tmem;
   int abort;
 };
@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   volatile int* ab = &s.abort;
   if (warp == 0) {
     if (lane == 0) {
-      for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.done}) tc::mbar_init(bar, 1);
+      for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.dq_done[0], &s.dq_done[1]}) tc::mbar_init(bar, 1);
       for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full}) tc::mbar_init(bar, WORKERS);
+      tc::mbar_init(&s.done, 2);
       for (int i = 0; i < KS; ++i) {
         tc::mbar_init(&s.k_full[i], 1);
         tc::mbar_init(&s.k_empty[i], 1);
@@ -218,49 +219,44 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         wait_some(&s.q_full, 0);
         wait_some(&s.do_full, 0);
       }
-    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // products
+    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // S and dP
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const int ks = (a.D + 15) / 16;
-      const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
       const uint32_t q_lo = desc_lo(s.Q), do_lo = desc_lo(s.dO);
-      bool ok = warp_wait(&s.q_full, 0, ab);
+      bool ok = warp_wait_all(ab, Phase{&s.q_full, 0}, Phase{&s.do_full, 0});
       Ring<KS> kr;
       Ring<VS> vr;
-      auto score = [&](int n) {  // S of the next tile; its K
-        const int at = kr.st;
-        mma_rows<DB>(tmem + (n & 1) * TILE, q_lo, desc_lo(s.K[at]), id_s, ks);
+      for (int n = 0; n < n_tiles && ok; ++n) {
+        // S(n) takes the place of dS(n - 2), dP(n) that of dP(n - 1)
+        const Phase kp{&s.k_full[kr.st], (uint32_t)kr.ph}, vp{&s.v_full[vr.st], (uint32_t)vr.ph};
+        if (n >= 2) ok = warp_wait_all(ab, kp, Phase{&s.dq_done[n & 1], (uint32_t)(n / 2 - 1) & 1});
+        else ok = warp_wait(kp.bar, kp.parity, ab);
+        if (!ok) break;
+        mma_rows<DB>(tmem + (n & 1) * TILE, q_lo, desc_lo(s.K[kr.st]), id_s, ks);
         commit(&s.s_full[n & 1]);
         kr.step();
-        return at;
-      };
-      auto grad = [&] {  // dP of the next tile
+        if (n >= 1) ok = warp_wait_all(ab, vp, Phase{&s.dp_read, (uint32_t)(n - 1) & 1});
+        else ok = warp_wait(vp.bar, vp.parity, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
         mma_rows<DB>(tmem + T_DP, do_lo, desc_lo(s.V[vr.st]), id_s, ks);
         commit(&s.dp_full);
         commit(&s.v_empty[vr.st]);
         vr.step();
-      };
-      int kst = 0, k2 = 0;
-      ok = ok && warp_wait(&s.k_full[0], 0, ab);
-      if (ok) {
-        kst = score(0);
-        ok = warp_wait_all(ab, Phase{&s.do_full, 0}, Phase{&s.v_full[0], 0});
       }
-      if (ok) grad();
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        if (n + 1 < n_tiles) {
-          ok = warp_wait_all(ab, Phase{&s.k_full[kr.st], (uint32_t)kr.ph}, Phase{&s.v_full[vr.st], (uint32_t)vr.ph},
-                             Phase{&s.dp_read, (uint32_t)n & 1});
-          if (!ok) break;
-          tc::tc_fence_after();
-          k2 = score(n + 1);
-          grad();
-        }
-        ok = warp_wait(&s.ds_full, n & 1, ab);
-        if (!ok) break;
+      commit(&s.done);
+      wait_some(&s.done, 0);
+    } else if (warp == WORKERS + 2 && n_tiles > 0) {  // dQ: its waits cost the others nothing
+      const int ks = (a.D + 15) / 16;
+      const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
+      Ring<KS> kr;
+      for (int n = 0; n < n_tiles; ++n) {
+        if (!warp_wait(&s.ds_full, n & 1, ab)) break;
         tc::tc_fence_after();
-        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.K[kst]), id_d, n > 0);
-        commit(&s.k_empty[kst]);
-        kst = k2;
+        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.K[kr.st]), id_d, n > 0);
+        commit(&s.dq_done[n & 1]);
+        commit(&s.k_empty[kr.st]);
+        kr.step();
       }
       commit(&s.done);
       wait_some(&s.done, 0);
