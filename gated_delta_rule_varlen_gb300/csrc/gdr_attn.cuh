@@ -55,39 +55,53 @@ struct AttnBlock {
   int first;           // token within the document
   int q0, lq, k0, lk;  // the document's queries and keys
 };
-// Finds block `want` of the documents whose lengths cu gives (one warp, the same answer on
-// every lane).
+// Finds blocks of the documents, each `want` at least the one before it (one warp, the same
+// answer on every lane): 32 documents are held in registers.
 template <bool LAST>
-__device__ __forceinline__ AttnBlock find_block(const AttnArgs& a, const int* __restrict__ cu, int per, int want) {
-  const int lane = threadIdx.x & 31;
-  int base = 0;
-#pragma unroll 1
-  for (int d0 = 0; d0 < a.N; d0 += 32) {
-    const int d = d0 + lane;
-    const int n = d < a.N ? (cu[d + 1] - cu[d] + per - 1) / per : 0;
-    int pre = n;
+struct BlockFinder {
+  const AttnArgs& a;
+  const int per;
+  int before = 0;  // the blocks of the documents before d0
+  int d0, q0, lq, k0, lk, n, pre, total;  // documents d0 + lane, their blocks, the sum up to them, of all 32
+
+  __device__ __forceinline__ BlockFinder(const AttnArgs& args, int per_) : a(args), per(per_) { load(0); }
+  __device__ __forceinline__ void load(int first) {
+    const int lane = threadIdx.x & 31, d = first + lane;
+    d0 = first;
+    q0 = lq = k0 = lk = 0;
+    if (d < a.N) {
+      q0 = a.cu[d];
+      lq = a.cu[d + 1] - q0;
+      k0 = a.cuk[d];
+      lk = a.cuk[d + 1] - k0;
+    }
+    n = d < a.N ? ((LAST ? lq : lk) + per - 1) / per : 0;
+    pre = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, pre, m);
       if (lane >= m) pre += v;
     }
-    const int total = __shfl_sync(0xffffffffu, pre, 31);
-    if (want < base + total) {
-      const int l = __ffs(__ballot_sync(0xffffffffu, want < base + pre)) - 1;
-      AttnBlock b;
-      const int end = base + __shfl_sync(0xffffffffu, pre, l);  // of the document's blocks
-      b.first = (LAST ? end - 1 - want : want - end + __shfl_sync(0xffffffffu, n, l)) * per;
-      const int doc = d0 + l;
-      b.q0 = a.cu[doc];
-      b.lq = a.cu[doc + 1] - b.q0;
-      b.k0 = a.cuk[doc];
-      b.lk = a.cuk[doc + 1] - b.k0;
-      return b;
-    }
-    base += total;
+    total = __shfl_sync(0xffffffffu, pre, 31);
   }
-  return AttnBlock{0, 0, 0, 0, 0};
-}
+  __device__ __forceinline__ AttnBlock find(int want) {
+#pragma unroll 1
+    while (want - before >= total && d0 + 32 < a.N) {
+      before += total;
+      load(d0 + 32);
+    }
+    want -= before;
+    const int l = __ffs(__ballot_sync(0xffffffffu, want < pre)) - 1;
+    AttnBlock b;
+    const int end = __shfl_sync(0xffffffffu, pre, l);  // of the document's blocks
+    b.first = (LAST ? end - 1 - want : want - end + __shfl_sync(0xffffffffu, n, l)) * per;
+    b.q0 = __shfl_sync(0xffffffffu, q0, l);
+    b.lq = __shfl_sync(0xffffffffu, lq, l);
+    b.k0 = __shfl_sync(0xffffffffu, k0, l);
+    b.lk = __shfl_sync(0xffffffffu, lk, l);
+    return b;
+  }
+};
 
 // How the kernels on the tensor cores cut the work: heads side by side in a tile of queries
 // (2^pack), and into how many parts the sums of each kernel's blocks, joined by another

@@ -128,6 +128,25 @@ __device__ __forceinline__ void store16(__nv_bfloat16* row, float* share, int c0
 // ---------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------
+// What a block works on at a time: a tile of queries, a part of its keys.
+struct DqWork {
+  AttnBlock b;
+  int h0, hk, part, i1;
+  TileRange all, r;
+  __device__ __forceinline__ void find(const BwdArgs& ba, BlockFinder<true>& finder, int item) {
+    const AttnArgs& a = ba.a;
+    const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, groups = a.H >> ba.pack;
+    part = item % ba.parts;
+    item /= ba.parts;
+    b = finder.find(item / groups);
+    h0 = item % groups * heads;
+    hk = h0 / (a.H / a.HK);
+    i1 = min(b.lq, b.first + tokens);
+    all = tiles_of(a, b.lq, b.lk, b.first, i1);
+    r = part_of(all, part, ba.parts);
+  }
+};
+
 template <int DB>
 struct DqSmem {
   // a K tile is held from S until its dQ, a step later
@@ -135,14 +154,15 @@ struct DqSmem {
   unsigned char Q[DB * BLK], dO[DB * BLK];
   unsigned char K[KS][DB * BLK], V[VS][DB * BLK];
   float part[QUARTERS][TILE];          // the quarters' shares of delta
-  uint64_t q_full, do_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], cleared;
-  uint64_t s_full[2], dp_full, dp_read, ds_full, dq_done[2], part_full, done;
+  WorkQueue<DqWork> queue;
+  uint64_t q_full, do_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], cleared;
+  uint64_t s_full[2], dp_full, dp_read, ds_full, dq_done[2], part_full, acc_full, acc_empty, done;
   uint32_t tmem;
   int abort;
 };
 constexpr int T_DP = 256, T_DQ = 384;  // (two tiles of S, and over them dS, before)
 
-template <int DB>
+template <int DB, bool QUEUE>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ BwdArgs ba) {
   using Smem = DqSmem<DB>;
   constexpr int KS = Smem::KS, VS = Smem::VS;
@@ -153,8 +173,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   volatile int* ab = &s.abort;
   if (warp == 0) {
     if (lane == 0) {
-      for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.dq_done[0], &s.dq_done[1]}) tc::mbar_init(bar, 1);
-      for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full}) tc::mbar_init(bar, WORKERS);
+      for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.dq_done[0], &s.dq_done[1],
+                            &s.acc_full})
+        tc::mbar_init(bar, 1);
+      for (uint64_t* bar : {&s.dp_read, &s.ds_full, &s.part_full, &s.acc_empty}) tc::mbar_init(bar, WORKERS);
+      tc::mbar_init(&s.q_empty, 1 + WORKERS);
       tc::mbar_init(&s.done, 2);
       for (int i = 0; i < KS; ++i) {
         tc::mbar_init(&s.k_full[i], 1);
@@ -164,6 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         tc::mbar_init(&s.v_full[i], 1);
         tc::mbar_init(&s.v_empty[i], 1);
       }
+      s.queue.init(3 + WORKERS);
       s.abort = 0;
       tc::mbar_fence_init();
     }
@@ -171,14 +195,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     tc::tmem_alloc(&s.tmem, 512);
     tc::tmem_relinquish();
   }
-  const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, groups = a.H >> ba.pack;
-  const int item = blockIdx.x / ba.parts, part = blockIdx.x % ba.parts;
-  const AttnBlock b = find_block<true>(a, a.cu, tokens, item / groups);
-  const int h0 = item % groups * heads, hk = h0 / (a.H / a.HK);
-  const int i1 = min(b.lq, b.first + tokens);
-  const TileRange all = tiles_of(a, b.lq, b.lk, b.first, i1), r = part_of(all, part, ba.parts);
-  const bool one = all.hi - all.lo == 1;  // the queries' keys fit one tile
-  const int n_tiles = r.hi - r.lo;
+  const int heads = 1 << ba.pack, tokens = TILE >> ba.pack;
+  DqWork w;
+  if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
+    BlockFinder<true> finder(a, tokens);
+    w.find(ba, finder, (int)blockIdx.x);
+  }
+  int taken = 0;
+  auto next_item = [&](bool ask) {
+    if constexpr (QUEUE) return s.queue.take(taken, w, ab, ask);
+    else return taken++ == 0;
+  };
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -186,188 +213,237 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
 
   if (warp >= WORKERS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
-    if (warp == WORKERS && n_tiles > 0) {  // loads
-      if (lane == 0) {
-        load_tile<DB>(s.Q, &ba.q_map, h0, b.q0 + b.first, &s.q_full);
-        load_tile<DB>(s.dO, &ba.do_map, h0, b.q0 + b.first, &s.do_full);
-      }
-      __syncwarp();
+    if (warp == WORKERS) {  // loads
       Ring<KS> kr;
       Ring<VS> vr;
-      int n = 0;
-      for (; n < n_tiles; ++n) {
-        const int j = r.lo + n, rows = b.lk - j * TILE;
-        const bool clear = rows < TILE;
-        if (n >= KS && !warp_wait(&s.k_empty[kr.st], kr.ph ^ 1, ab)) break;
-        if (lane == 0) load_tile<DB>(s.K[kr.st], &ba.k_map, hk, b.k0 + j * TILE, clear ? &s.cleared : &s.k_full[kr.st]);
-        __syncwarp();
-        if (clear) {
-          if (!warp_wait(&s.cleared, 0, ab)) break;
-          clear_rows<DB>(s.K[kr.st], rows);
-          warp_arrive(&s.k_full[kr.st]);
+      int g = 0, k = 0, cleared = 0;  // tiles, items so far
+      bool ok = true;
+      while (ok && next_item(true)) {
+        const AttnBlock& b = w.b;
+        if (w.r.lo >= w.r.hi) continue;
+        if (k > 0 && !warp_wait(&s.q_empty, (k - 1) & 1, ab)) break;
+        ++k;
+        if (lane == 0) {
+          load_tile<DB>(s.Q, &ba.q_map, w.h0, b.q0 + b.first, &s.q_full);
+          load_tile<DB>(s.dO, &ba.do_map, w.h0, b.q0 + b.first, &s.do_full);
         }
-        kr.step();
-        if (n >= VS && !warp_wait(&s.v_empty[vr.st], vr.ph ^ 1, ab)) break;
-        if (lane == 0) load_tile<DB>(s.V[vr.st], &ba.v_map, hk, b.k0 + j * TILE, &s.v_full[vr.st]);
         __syncwarp();
-        vr.step();
+        for (int j = w.r.lo; j < w.r.hi; ++j, ++g) {
+          const int rows = b.lk - j * TILE;
+          const bool clear = rows < TILE;
+          ok = g < KS || warp_wait(&s.k_empty[kr.st], kr.ph ^ 1, ab);
+          if (!ok) break;
+          if (lane == 0) load_tile<DB>(s.K[kr.st], &ba.k_map, w.hk, b.k0 + j * TILE, clear ? &s.cleared : &s.k_full[kr.st]);
+          __syncwarp();
+          if (clear) {
+            ok = warp_wait(&s.cleared, cleared++ & 1, ab);
+            if (!ok) break;
+            clear_rows<DB>(s.K[kr.st], rows);
+            warp_arrive(&s.k_full[kr.st]);
+          }
+          kr.step();
+          ok = g < VS || warp_wait(&s.v_empty[vr.st], vr.ph ^ 1, ab);
+          if (!ok) break;
+          if (lane == 0) load_tile<DB>(s.V[vr.st], &ba.v_map, w.hk, b.k0 + j * TILE, &s.v_full[vr.st]);
+          __syncwarp();
+          vr.step();
+        }
       }
-      if (n < n_tiles) {  // given up: the copies in flight land before the block ends
-        for (int k = max(0, n + 1 - KS); k <= n; ++k) wait_some(&s.k_full[k % KS], (k / KS) & 1);
-        for (int k = max(0, n - VS); k < n; ++k) wait_some(&s.v_full[k % VS], (k / VS) & 1);
-        wait_some(&s.cleared, 0);
-        wait_some(&s.q_full, 0);
-        wait_some(&s.do_full, 0);
+      if (s.abort) {  // given up: the copies in flight land before the block ends
+        for (int n = max(0, g + 1 - KS); n <= g; ++n) wait_some(&s.k_full[n % KS], (n / KS) & 1);
+        for (int n = max(0, g - VS); n < g; ++n) wait_some(&s.v_full[n % VS], (n / VS) & 1);
+        if (cleared > 0) wait_some(&s.cleared, (cleared - 1) & 1);
+        if (k > 0) {
+          wait_some(&s.q_full, (k - 1) & 1);
+          wait_some(&s.do_full, (k - 1) & 1);
+        }
       }
-    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // S and dP
+    } else if (warp == WORKERS + 1) {  // S and dP
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const int ks = (a.D + 15) / 16;
       const uint32_t q_lo = desc_lo(s.Q), do_lo = desc_lo(s.dO);
-      bool ok = warp_wait_all(ab, Phase{&s.q_full, 0}, Phase{&s.do_full, 0});
       Ring<KS> kr;
       Ring<VS> vr;
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        // S(n) takes the place of dS(n - 2), dP(n) that of dP(n - 1)
-        const Phase kp{&s.k_full[kr.st], (uint32_t)kr.ph}, vp{&s.v_full[vr.st], (uint32_t)vr.ph};
-        if (n >= 2) ok = warp_wait_all(ab, kp, Phase{&s.dq_done[n & 1], (uint32_t)(n / 2 - 1) & 1});
-        else ok = warp_wait(kp.bar, kp.parity, ab);
-        if (!ok) break;
-        mma_rows<DB>(tmem + (n & 1) * TILE, q_lo, desc_lo(s.K[kr.st]), id_s, ks);
-        commit(&s.s_full[n & 1]);
-        kr.step();
-        if (n >= 1) ok = warp_wait_all(ab, vp, Phase{&s.dp_read, (uint32_t)(n - 1) & 1});
-        else ok = warp_wait(vp.bar, vp.parity, ab);
-        if (!ok) break;
-        tc::tc_fence_after();
-        mma_rows<DB>(tmem + T_DP, do_lo, desc_lo(s.V[vr.st]), id_s, ks);
-        commit(&s.dp_full);
-        commit(&s.v_empty[vr.st]);
-        vr.step();
+      int g = 0, k = 0;
+      bool ok = true;
+      while (ok && next_item(false)) {
+        if (w.r.lo >= w.r.hi) continue;
+        ok = warp_wait_all(ab, Phase{&s.q_full, (uint32_t)k & 1}, Phase{&s.do_full, (uint32_t)k & 1});
+        ++k;
+        for (int j = w.r.lo; j < w.r.hi && ok; ++j, ++g) {
+          // S takes the place of dS two tiles ago, dP that of the last dP
+          const Phase kp{&s.k_full[kr.st], (uint32_t)kr.ph}, vp{&s.v_full[vr.st], (uint32_t)vr.ph};
+          ok = warp_wait_all(ab, kp, g >= 2 ? Phase{&s.dq_done[g & 1], (uint32_t)(g / 2 - 1) & 1} : kp);
+          if (!ok) break;
+          mma_rows<DB>(tmem + (g & 1) * TILE, q_lo, desc_lo(s.K[kr.st]), id_s, ks);
+          commit(&s.s_full[g & 1]);
+          kr.step();
+          ok = warp_wait_all(ab, vp, g >= 1 ? Phase{&s.dp_read, (uint32_t)(g - 1) & 1} : vp);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma_rows<DB>(tmem + T_DP, do_lo, desc_lo(s.V[vr.st]), id_s, ks);
+          commit(&s.dp_full);
+          commit(&s.v_empty[vr.st]);
+          vr.step();
+        }
+        commit(&s.q_empty);
       }
       commit(&s.done);
       wait_some(&s.done, 0);
-    } else if (warp == WORKERS + 2 && n_tiles > 0) {  // dQ: its waits cost the others nothing
+    } else if (warp == WORKERS + 2) {  // dQ: its waits cost the others nothing
       const int ks = (a.D + 15) / 16;
       const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
       Ring<KS> kr;
-      for (int n = 0; n < n_tiles; ++n) {
-        if (!warp_wait(&s.ds_full, n & 1, ab)) break;
-        tc::tc_fence_after();
-        mma_sum(tmem + T_DQ, tmem + (n & 1) * TILE, desc_lo(s.K[kr.st]), id_d, n > 0);
-        commit(&s.dq_done[n & 1]);
-        commit(&s.k_empty[kr.st]);
-        kr.step();
+      int g = 0, k = 0;
+      bool ok = true;
+      while (ok && next_item(false)) {
+        if (w.r.lo >= w.r.hi) continue;
+        if (k > 0) ok = warp_wait(&s.acc_empty, (k - 1) & 1, ab);
+        ++k;
+        for (int j = w.r.lo; j < w.r.hi && ok; ++j, ++g) {
+          ok = warp_wait(&s.ds_full, g & 1, ab);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma_sum(tmem + T_DQ, tmem + (g & 1) * TILE, desc_lo(s.K[kr.st]), id_d, j > w.r.lo);
+          commit(&s.dq_done[g & 1]);
+          commit(&s.k_empty[kr.st]);
+          kr.step();
+        }
+        commit(&s.acc_full);
       }
       commit(&s.done);
       wait_some(&s.done, 0);
+    } else {
+      if constexpr (QUEUE) {
+        BlockFinder<true> finder(a, tokens);
+        s.queue.run(ab, [&](int item) {
+          w.find(ba, finder, item);
+          return w;
+        });
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a row a thread, of S and dP a quarter's columns
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
-    const int token = b.first + (row >> ba.pack), h = h0 + (row & (heads - 1));
-    const int64_t at = b.q0 + token;
-    const bool live = token < b.lq;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float c = a.scale * LOG2E, lse = live ? a.lse_in[h * a.T + at] : -INFINITY;
-    const float base = lse == -INFINITY ? -INFINITY : -lse * LOG2E;  // (rows that see nothing: p = 0)
-    const uint64_t cc = pack2(c, c), bb = pack2(base, base);
-    const KeyRange kr = keys_of(a, token, b.lq, b.lk);
-    const KeyRange seen{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
+    const float c = a.scale * LOG2E;
+    const uint64_t cc = pack2(c, c);
     bool ok = true;
-    float delta = 0.f;
-    auto exchange = [&](float mine, bool write) {  // delta of all quarters
-      s.part[quarter][row] = mine;
-      warp_arrive(&s.part_full);
-      ok = ok && warp_wait(&s.part_full, 0, ab);
-      delta = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
-      if (live && write && quarter == 0) a.delta[h * a.T + at] = delta;
-    };
-    if (n_tiles > 0 && !one) {
-      constexpr int PIECES = DB * 8 / QUARTERS;  // of 8 elements of a row
-      uint4 o[PIECES];
-      const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
+    int g = 0, k = 0;
+    while (ok && next_item(false)) {
+      const AttnBlock& b = w.b;
+      const bool one = w.all.hi - w.all.lo == 1, any = w.r.lo < w.r.hi;  // one: the queries' keys fit one tile
+      const int token = b.first + (row >> ba.pack), h = w.h0 + (row & (heads - 1));
+      const int64_t at = b.q0 + token;
+      const bool live = token < b.lq;
+      const float lse = live ? a.lse_in[h * a.T + at] : -INFINITY;
+      const float base = lse == -INFINITY ? -INFINITY : -lse * LOG2E;  // (rows that see nothing: p = 0)
+      const uint64_t bb = pack2(base, base);
+      const KeyRange kr = keys_of(a, token, b.lq, b.lk);
+      const KeyRange seen{keys_of(a, w.i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
+      float delta = 0.f;
+      auto exchange = [&](float mine, bool write) {  // delta of all quarters
+        s.part[quarter][row] = mine;
+        warp_arrive(&s.part_full);
+        ok = ok && warp_wait(&s.part_full, k & 1, ab);
+        delta = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
+        if (live && write && quarter == 0) a.delta[h * a.T + at] = delta;
+      };
+      if (any && !one) {
+        constexpr int PIECES = DB * 8 / QUARTERS;  // of 8 elements of a row
+        uint4 o[PIECES];
+        const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int d = (quarter * PIECES + i) * 8;
-        o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
-      }
-      ok = warp_wait(&s.do_full, 0, ab);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int pc = quarter * PIECES + i;
-        const uint4 g = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
-        const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
-      }
-      exchange(sum, r.lo == all.lo);
-    } else if (all.lo == all.hi && part == 0 && live && quarter == 0) {
-      a.delta[h * a.T + at] = 0.f;
-    }
-#pragma unroll 1
-    for (int n = 0; n < n_tiles; ++n) {
-      const int j = r.lo + n;
-      const uint32_t ts = lanes + (n & 1) * TILE + c0;
-      ok = ok && warp_wait(&s.s_full[n & 1], (n >> 1) & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
-      uint64_t p[COLS / 2];
-      {
-        uint32_t x[COLS];
-        load_cols(ts, x);
-#pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) {
-          float e, f;
-          unpack2(fma2(pair_at(x + 2 * i), cc, bb), e, f);
-          p[i] = pack2(ex2(e), ex2(f));
+        for (int i = 0; i < PIECES; ++i) {
+          const int d = (quarter * PIECES + i) * 8;
+          o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
         }
-        if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
-          const int lo = kr.lo - j * TILE - c0, hi = kr.hi - j * TILE - c0;
+        ok = warp_wait(&s.do_full, k & 1, ab);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int pc = quarter * PIECES + i;
+          const uint4 v = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
+          const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
+        }
+        exchange(sum, w.r.lo == w.all.lo);
+      } else if (w.all.lo == w.all.hi && w.part == 0 && live && quarter == 0) {
+        a.delta[h * a.T + at] = 0.f;
+      }
+      if (any) {  // (not before this item's tiles are there: the last one's place is free)
+        if (one) ok = warp_wait(&s.do_full, k & 1, ab);
+        warp_arrive(&s.q_empty);
+      }
+#pragma unroll 1
+      for (int j = w.r.lo; j < w.r.hi; ++j, ++g) {
+        const uint32_t ts = lanes + (g & 1) * TILE + c0;
+        ok = ok && warp_wait(&s.s_full[g & 1], (g >> 1) & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint64_t p[COLS / 2];
+        {
+          uint32_t x[COLS];
+          load_cols(ts, x);
 #pragma unroll
           for (int i = 0; i < COLS / 2; ++i) {
             float e, f;
-            unpack2(p[i], e, f);
-            p[i] = pack2(2 * i >= lo && 2 * i < hi ? e : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? f : 0.f);
+            unpack2(fma2(pair_at(x + 2 * i), cc, bb), e, f);
+            p[i] = pack2(ex2(e), ex2(f));
+          }
+          if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
+            const int lo = kr.lo - j * TILE - c0, hi = kr.hi - j * TILE - c0;
+#pragma unroll
+            for (int i = 0; i < COLS / 2; ++i) {
+              float e, f;
+              unpack2(p[i], e, f);
+              p[i] = pack2(2 * i >= lo && 2 * i < hi ? e : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? f : 0.f);
+            }
           }
         }
-      }
-      ok = warp_wait(&s.dp_full, n & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
-      uint32_t x[COLS];
-      load_cols(lanes + T_DP + c0, x);
-      tc::tc_fence_before();
-      warp_arrive(&s.dp_read);
-      if (b.lk - j * TILE < TILE) {  // keys past the document's end: whatever V holds there
-#pragma unroll
-        for (int i = 0; i < COLS; ++i)
-          if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
-      }
-      if (one) {
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
-        exchange(sum_of(add2(sum[0], sum[1])), true);
+        ok = warp_wait(&s.dp_full, g & 1, ab);
         if (!ok) break;
+        tc::tc_fence_after();
+        uint32_t x[COLS];
+        load_cols(lanes + T_DP + c0, x);
+        tc::tc_fence_before();
+        warp_arrive(&s.dp_read);
+        if (b.lk - j * TILE < TILE) {  // keys past the document's end: whatever V holds there
+#pragma unroll
+          for (int i = 0; i < COLS; ++i)
+            if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
+        }
+        if (one) {
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < COLS / 2; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
+          exchange(sum_of(add2(sum[0], sum[1])), true);
+          if (!ok) break;
+        }
+        const uint64_t minus = pack2(-delta, -delta);
+#pragma unroll
+        for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
+        store_words(ts, x);
+        tc::tc_fence_before();
+        warp_arrive(&s.ds_full);
       }
-      const uint64_t minus = pack2(-delta, -delta);
-#pragma unroll
-      for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
-      store_words(ts, x);
-      tc::tc_fence_before();
-      warp_arrive(&s.ds_full);
-    }
-    if (ok && n_tiles > 0) {
-      ok = warp_wait(&s.done, 0, ab);
-      tc::tc_fence_after();
-    }
-    if (ok) {
+      if (!ok) break;
+      if (any) {
+        ok = warp_wait(&s.acc_full, k & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        ++k;
+      }
       const int64_t to = (at * a.H + h) * a.D;
-      float* share = ba.parts > 1 ? ba.part + part * a.T * a.H * a.D + to : nullptr;
+      float* share = ba.parts > 1 ? ba.part + w.part * a.T * a.H * a.D + to : nullptr;
 #pragma unroll
-      for (int i = 0; i < DB; ++i) store16(a.dq + to, share, DB * 16 * quarter + 16 * i, a.D, lanes + T_DQ, a.scale, n_tiles > 0, live);
+      for (int i = 0; i < DB; ++i) store16(a.dq + to, share, DB * 16 * quarter + 16 * i, a.D, lanes + T_DQ, a.scale, any, live);
+      if (any) {
+        tc::tc_fence_before();
+        warp_arrive(&s.acc_empty);
+      }
     }
   }
   tc::tc_fence_before();
@@ -379,6 +455,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // dK, dV
 // ---------------------------------------------------------------------------
+// What a block works on at a time: a tile of keys, a part of the tiles of queries (of all its
+// heads, `per` tiles each from t0 on) that see them.
+struct DkvWork {
+  AttnBlock b;
+  int hk, part, off, last, t0, per, n, g0, first;
+  __device__ __forceinline__ void find(const BwdArgs& ba, BlockFinder<false>& finder, int item) {
+    const AttnArgs& a = ba.a;
+    const int G = a.H / a.HK;
+    part = item % ba.parts;
+    item /= ba.parts;
+    b = finder.find(item / a.HK);
+    hk = item % a.HK;
+    off = b.lk - b.lq;
+    last = min(b.lk, b.first + TILE) - 1;
+    const TileRange r = query_tiles_of(a, b.lq, b.lk, b.first, last, TILE >> ba.pack);
+    t0 = r.lo;
+    per = r.hi - r.lo;
+    const TileRange mine = part_of(TileRange{0, per * (G >> ba.pack)}, part, ba.parts);
+    n = mine.hi - mine.lo;
+    g0 = per ? mine.lo / per : 0;
+    first = per ? mine.lo % per : 0;
+  }
+};
+
 template <int DB>
 struct DkvSmem {
   // a Q tile is held until its dK, behind its dV
@@ -386,14 +486,15 @@ struct DkvSmem {
   unsigned char K[DB * BLK], V[DB * BLK];
   unsigned char Q[QS][DB * BLK], dO[OS][DB * BLK];
   alignas(16) float lse[2][TILE], delta[2][TILE];  // -lse log2 e, -delta
-  uint64_t k_full, v_full, q_full[QS], q_empty[QS], o_full[OS], o_empty[OS], q_cleared, o_cleared;
-  uint64_t s_full, p_full, dp_full, ds_full, row_full[2], row_empty[2], done;
+  WorkQueue<DkvWork> queue;
+  uint64_t kv_full, kv_empty, q_full[QS], q_empty[QS], o_full[OS], o_empty[OS], q_cleared, o_cleared;
+  uint64_t s_full, p_full, dp_full, ds_full, row_full[2], row_empty[2], acc_full, acc_empty, done;
   uint32_t tmem;
   int abort;
 };
 constexpr int T_DPT = 128, T_DK = 256, T_DV = 384;  // (S^T, and over it P^T, before)
 
-template <int DB>
+template <int DB, bool QUEUE>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__ BwdArgs ba) {
   using Smem = DkvSmem<DB>;
   constexpr int QS = Smem::QS, OS = Smem::OS;
@@ -404,9 +505,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
   volatile int* ab = &s.abort;
   if (warp == 0) {
     if (lane == 0) {
-      for (uint64_t* bar : {&s.k_full, &s.v_full, &s.q_cleared, &s.o_cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1], &s.done})
+      for (uint64_t* bar : {&s.kv_full, &s.kv_empty, &s.q_cleared, &s.o_cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1],
+                            &s.acc_full, &s.done})
         tc::mbar_init(bar, 1);
-      for (uint64_t* bar : {&s.p_full, &s.ds_full, &s.row_empty[0], &s.row_empty[1]}) tc::mbar_init(bar, WORKERS);
+      for (uint64_t* bar : {&s.p_full, &s.ds_full, &s.row_empty[0], &s.row_empty[1], &s.acc_empty}) tc::mbar_init(bar, WORKERS);
       for (int i = 0; i < QS; ++i) {
         tc::mbar_init(&s.q_full[i], 1);
         tc::mbar_init(&s.q_empty[i], 1);
@@ -415,6 +517,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
         tc::mbar_init(&s.o_full[i], 1);
         tc::mbar_init(&s.o_empty[i], 1);
       }
+      s.queue.init(3 + WORKERS);
       s.abort = 0;
       tc::mbar_fence_init();
     }
@@ -423,15 +526,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
     tc::tmem_relinquish();
   }
   const int heads = 1 << ba.pack, tokens = TILE >> ba.pack, G = a.H / a.HK;
-  const int item = blockIdx.x / ba.parts, part = blockIdx.x % ba.parts;
-  const AttnBlock b = find_block<false>(a, a.cuk, TILE, item / a.HK);
-  const int hk = item % a.HK;
-  // the tiles of queries that see any of the keys [first, last]: each head group's
-  const int off = b.lk - b.lq, last = min(b.lk, b.first + TILE) - 1;
-  const TileRange r = query_tiles_of(a, b.lq, b.lk, b.first, last, tokens);
-  const int t0 = r.lo, per = r.hi - r.lo;
-  const TileRange mine = part_of(TileRange{0, per * (G >> ba.pack)}, part, ba.parts);
-  const int n_tiles = mine.hi - mine.lo, g0 = per ? mine.lo / per : 0, tt0 = per ? mine.lo % per : 0;
+  DkvWork w;
+  if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
+    BlockFinder<false> finder(a, TILE);
+    w.find(ba, finder, (int)blockIdx.x);
+  }
+  int taken = 0;
+  auto next_item = [&](bool ask) {
+    if constexpr (QUEUE) return s.queue.take(taken, w, ab, ask);
+    else return taken++ == 0;
+  };
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -439,58 +543,73 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
 
   if (warp >= WORKERS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
-    if (warp == WORKERS && n_tiles > 0) {  // loads
-      if (lane == 0) {
-        load_tile<DB>(s.K, &ba.k_map, hk, b.k0 + b.first, &s.k_full);
-        load_tile<DB>(s.V, &ba.v_map, hk, b.k0 + b.first, &s.v_full);
-      }
-      __syncwarp();
+    if (warp == WORKERS) {  // loads
       Ring<QS> qr;
       Ring<OS> orr;
-      int n = 0, cleared = 0;
-      for (int g = g0, t = tt0; n < n_tiles; ++n) {
-        const int token = (t0 + t) * tokens, rows = (int)min((int64_t)TILE, (int64_t)(b.lq - token) << ba.pack);
-        const bool clear = rows < TILE;
-        const int h = hk * G + g * heads;
-        if (n >= QS && !warp_wait(&s.q_empty[qr.st], qr.ph ^ 1, ab)) break;
-        if (lane == 0) load_tile<DB>(s.Q[qr.st], &ba.q_map, h, b.q0 + token, clear ? &s.q_cleared : &s.q_full[qr.st]);
-        __syncwarp();
-        if (n >= OS && !warp_wait(&s.o_empty[orr.st], orr.ph ^ 1, ab)) break;
-        if (lane == 0) load_tile<DB>(s.dO[orr.st], &ba.do_map, h, b.q0 + token, clear ? &s.o_cleared : &s.o_full[orr.st]);
-        __syncwarp();
-        if (clear) {
-          if (!warp_wait(&s.q_cleared, cleared & 1, ab)) break;
-          clear_rows<DB>(s.Q[qr.st], rows);
-          warp_arrive(&s.q_full[qr.st]);
-          if (!warp_wait(&s.o_cleared, cleared & 1, ab)) break;
-          clear_rows<DB>(s.dO[orr.st], rows);
-          warp_arrive(&s.o_full[orr.st]);
-          ++cleared;
+      int g = 0, k = 0, cleared = 0;  // tiles, items so far
+      bool ok = true;
+      while (ok && next_item(true)) {
+        const AttnBlock& b = w.b;
+        if (w.n == 0) continue;
+        if (k > 0 && !warp_wait(&s.kv_empty, (k - 1) & 1, ab)) break;
+        ++k;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&s.kv_full, 2 * DB * BLK);
+          for (int c = 0; c < DB; ++c) {
+            tc::tma_load_3d(s.K + c * BLK, &ba.k_map, 64 * c, w.hk, b.k0 + b.first, &s.kv_full);
+            tc::tma_load_3d(s.V + c * BLK, &ba.v_map, 64 * c, w.hk, b.k0 + b.first, &s.kv_full);
+          }
         }
-        qr.step();
-        orr.step();
-        if (++t == per) {
-          t = 0;
-          ++g;
+        __syncwarp();
+        for (int n = 0, hg = w.g0, t = w.first; n < w.n; ++n, ++g) {
+          const int token = (w.t0 + t) * tokens, rows = (int)min((int64_t)TILE, (int64_t)(b.lq - token) << ba.pack);
+          const bool clear = rows < TILE;
+          const int h = w.hk * G + hg * heads;
+          ok = g < QS || warp_wait(&s.q_empty[qr.st], qr.ph ^ 1, ab);
+          if (!ok) break;
+          if (lane == 0) load_tile<DB>(s.Q[qr.st], &ba.q_map, h, b.q0 + token, clear ? &s.q_cleared : &s.q_full[qr.st]);
+          __syncwarp();
+          if (clear) {
+            ok = warp_wait(&s.q_cleared, cleared & 1, ab);
+            if (!ok) break;
+            clear_rows<DB>(s.Q[qr.st], rows);
+            warp_arrive(&s.q_full[qr.st]);
+          }
+          ok = g < OS || warp_wait(&s.o_empty[orr.st], orr.ph ^ 1, ab);
+          if (!ok) break;
+          if (lane == 0) load_tile<DB>(s.dO[orr.st], &ba.do_map, h, b.q0 + token, clear ? &s.o_cleared : &s.o_full[orr.st]);
+          __syncwarp();
+          if (clear) {
+            ok = warp_wait(&s.o_cleared, cleared & 1, ab);
+            if (!ok) break;
+            clear_rows<DB>(s.dO[orr.st], rows);
+            warp_arrive(&s.o_full[orr.st]);
+            ++cleared;
+          }
+          qr.step();
+          orr.step();
+          if (++t == w.per) {
+            t = 0;
+            ++hg;
+          }
         }
       }
-      if (n < n_tiles) {  // given up: the copies in flight land before the block ends
-        for (int k = max(0, n + 1 - QS); k <= n; ++k) wait_some(&s.q_full[k % QS], (k / QS) & 1);
-        for (int k = max(0, n + 1 - OS); k <= n; ++k) wait_some(&s.o_full[k % OS], (k / OS) & 1);
+      if (s.abort) {  // given up: the copies in flight land before the block ends
+        for (int n = max(0, g + 1 - QS); n <= g; ++n) wait_some(&s.q_full[n % QS], (n / QS) & 1);
+        for (int n = max(0, g + 1 - OS); n <= g; ++n) wait_some(&s.o_full[n % OS], (n / OS) & 1);
         wait_some(&s.q_cleared, cleared & 1);
         wait_some(&s.o_cleared, cleared & 1);
-        wait_some(&s.k_full, 0);
-        wait_some(&s.v_full, 0);
+        if (k > 0) wait_some(&s.kv_full, (k - 1) & 1);
       }
-    } else if (warp == WORKERS + 1 && n_tiles > 0) {  // products
+    } else if (warp == WORKERS + 1) {  // products
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const int ks = (a.D + 15) / 16;
       const uint32_t id_d = tc::idesc_bf16(TILE, 16 * ks) | tc::kIdescTransposeB;
       const uint32_t k_lo = desc_lo(s.K), v_lo = desc_lo(s.V);
-      bool ok = warp_wait(&s.k_full, 0, ab);
       Ring<QS> qr;
       Ring<OS> orr;
-      int qst = 0, q2 = 0, ost = 0;
+      int g = 0, k = 0, qst = 0, q2 = 0, ost = 0;
+      bool ok = true;
       auto score = [&](int& at) {  // S^T of the next tile
         at = qr.st;
         mma_rows<DB>(tmem, k_lo, desc_lo(s.Q[at]), id_s, ks);
@@ -503,139 +622,162 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
         commit(&s.dp_full);
         orr.step();
       };
-      ok = ok && warp_wait(&s.q_full[0], 0, ab);
-      if (ok) {
+      while (ok && next_item(false)) {
+        if (w.n == 0) continue;
+        ok = warp_wait_all(ab, Phase{&s.kv_full, (uint32_t)k & 1}, Phase{&s.q_full[qr.st], (uint32_t)qr.ph});
+        if (!ok) break;
         score(qst);
-        ok = warp_wait_all(ab, Phase{&s.v_full, 0}, Phase{&s.o_full[0], 0});
-      }
-      if (ok) grad();
-      for (int n = 0; n + 1 < n_tiles && ok; ++n) {
-        ok = warp_wait_all(ab, Phase{&s.p_full, (uint32_t)n & 1}, Phase{&s.q_full[qr.st], (uint32_t)qr.ph});
+        ok = warp_wait(&s.o_full[orr.st], orr.ph, ab);
         if (!ok) break;
-        tc::tc_fence_after();
-        mma_sum(tmem + T_DV, tmem, desc_lo(s.dO[ost]), id_d, n > 0);
-        commit(&s.o_empty[ost]);
-        score(q2);
-        ok = warp_wait_all(ab, Phase{&s.ds_full, (uint32_t)n & 1}, Phase{&s.o_full[orr.st], (uint32_t)orr.ph});
-        if (!ok) break;
-        tc::tc_fence_after();
-        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.Q[qst]), id_d, n > 0);
-        commit(&s.q_empty[qst]);
         grad();
-        qst = q2;
-      }
-      const int n = n_tiles - 1;  // the last tile
-      ok = ok && warp_wait(&s.p_full, n & 1, ab);
-      if (ok) {
-        tc::tc_fence_after();
-        mma_sum(tmem + T_DV, tmem, desc_lo(s.dO[ost]), id_d, n > 0);
-        ok = warp_wait(&s.ds_full, n & 1, ab);
-      }
-      if (ok) {
-        tc::tc_fence_after();
-        mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.Q[qst]), id_d, n > 0);
+        for (int n = 0; n < w.n && ok; ++n, ++g) {
+          const bool more = n + 1 < w.n;
+          const Phase pp{&s.p_full, (uint32_t)g & 1}, qp{&s.q_full[qr.st], (uint32_t)qr.ph};
+          // (the last item's sums have been read before this one's begin)
+          ok = n == 0 && k > 0 ? warp_wait_all(ab, pp, Phase{&s.acc_empty, (uint32_t)(k - 1) & 1}, more ? qp : pp)
+                               : warp_wait_all(ab, pp, more ? qp : pp);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma_sum(tmem + T_DV, tmem, desc_lo(s.dO[ost]), id_d, n > 0);
+          commit(&s.o_empty[ost]);
+          if (more) score(q2);
+          const Phase dp{&s.ds_full, (uint32_t)g & 1};
+          ok = warp_wait_all(ab, dp, more ? Phase{&s.o_full[orr.st], (uint32_t)orr.ph} : dp);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma_sum(tmem + T_DK, tmem + T_DPT, desc_lo(s.Q[qst]), id_d, n > 0);
+          commit(&s.q_empty[qst]);
+          if (more) grad();
+          else commit(&s.acc_full);
+          if (n + 2 == w.n || w.n == 1) commit(&s.kv_empty);  // (S and dP of the last tile are on their way)
+          qst = q2;
+        }
+        ++k;
       }
       commit(&s.done);
       wait_some(&s.done, 0);
-    } else if (warp == WORKERS + 2 && n_tiles > 0) {  // lse and delta of a tile's queries
-      for (int n = 0, g = g0, t = tt0; n < n_tiles; ++n) {
-        float l[4], d[4];
+    } else if (warp == WORKERS + 2) {  // lse and delta of a tile's queries
+      int g = 0;
+      bool ok = true;
+      while (ok && next_item(false)) {
+        const AttnBlock& b = w.b;
+        for (int n = 0, hg = w.g0, t = w.first; n < w.n; ++n, ++g) {
+          float l[4], d[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 4 * lane + e, token = (t0 + t) * tokens + (row >> ba.pack);
-          const int64_t at = (int64_t)(hk * G + g * heads + (row & (heads - 1))) * a.T + b.q0 + token;
-          const bool live = token < b.lq;
-          const float x = live ? a.lse_in[at] : -INFINITY;
-          l[e] = x == -INFINITY ? x : -x * LOG2E;  // (queries that see nothing: p = 0)
-          d[e] = live ? -a.delta[at] : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const int row = 4 * lane + e, token = (w.t0 + t) * tokens + (row >> ba.pack);
+            const int64_t at = (int64_t)(w.hk * G + hg * heads + (row & (heads - 1))) * a.T + b.q0 + token;
+            const bool live = token < b.lq;
+            const float x = live ? a.lse_in[at] : -INFINITY;
+            l[e] = x == -INFINITY ? x : -x * LOG2E;  // (queries that see nothing: p = 0)
+            d[e] = live ? -a.delta[at] : 0.f;
+          }
+          ok = g < 2 || warp_wait(&s.row_empty[g & 1], ((g >> 1) - 1) & 1, ab);
+          if (!ok) break;
+          *reinterpret_cast<float4*>(&s.lse[g & 1][4 * lane]) = make_float4(l[0], l[1], l[2], l[3]);
+          *reinterpret_cast<float4*>(&s.delta[g & 1][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+          warp_arrive(&s.row_full[g & 1]);
+          if (++t == w.per) {
+            t = 0;
+            ++hg;
+          }
         }
-        if (n >= 2 && !warp_wait(&s.row_empty[n & 1], ((n >> 1) - 1) & 1, ab)) break;
-        *reinterpret_cast<float4*>(&s.lse[n & 1][4 * lane]) = make_float4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<float4*>(&s.delta[n & 1][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
-        warp_arrive(&s.row_full[n & 1]);
-        if (++t == per) {
-          t = 0;
-          ++g;
-        }
+      }
+    } else {
+      if constexpr (QUEUE) {
+        BlockFinder<false> finder(a, TILE);
+        s.queue.run(ab, [&](int item) {
+          w.find(ba, finder, item);
+          return w;
+        });
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a key a thread, of S^T and dP^T a quarter's queries
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
-    const int key = b.first + row;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = a.scale * LOG2E;
     const uint64_t cc = pack2(c, c);
     bool ok = true;
+    int g = 0, k = 0;
+    while (ok && next_item(false)) {
+      const AttnBlock& b = w.b;
+      const int key = b.first + row;
 #pragma unroll 1
-    for (int n = 0, t = tt0; n < n_tiles; ++n) {
-      ok = warp_wait_all(ab, Phase{&s.row_full[n & 1], (uint32_t)(n >> 1) & 1}, Phase{&s.s_full, (uint32_t)n & 1});
-      if (!ok) break;
-      tc::tc_fence_after();
-      uint64_t p[COLS / 2];
-      uint32_t x[COLS];
-      load_cols(lanes + c0, x);
-      const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(&s.lse[n & 1][c0]);
+      for (int n = 0, t = w.first; n < w.n; ++n, ++g) {
+        ok = warp_wait_all(ab, Phase{&s.row_full[g & 1], (uint32_t)(g >> 1) & 1}, Phase{&s.s_full, (uint32_t)g & 1});
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint64_t p[COLS / 2];
+        uint32_t x[COLS];
+        load_cols(lanes + c0, x);
+        const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(&s.lse[g & 1][c0]);
 #pragma unroll
-      for (int i = 0; i < COLS / 2; i += 2) {
-        const ulonglong2 l = ls[i / 2];
-        float e, f;
-        unpack2(fma2(pair_at(x + 2 * i), cc, l.x), e, f);
-        p[i] = pack2(ex2(e), ex2(f));
-        unpack2(fma2(pair_at(x + 2 * i + 2), cc, l.y), e, f);
-        p[i + 1] = pack2(ex2(e), ex2(f));
-      }
-      const int q0 = (t0 + t) * tokens;
-      if (a.causal && (q0 + off < last || (a.window && (int64_t)q0 + tokens > (int64_t)b.first - off + a.window))) {
-        // the queries of this tile that see the key: [lo, hi)
-        const int64_t first = (int64_t)key - off - q0;
-        const int lo = (int)min(max(first, (int64_t)0), (int64_t)tokens) << ba.pack;
-        const int hi = a.window ? (int)min(max(first + a.window, (int64_t)0), (int64_t)tokens) << ba.pack : TILE;
-#pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) {
+        for (int i = 0; i < COLS / 2; i += 2) {
+          const ulonglong2 l = ls[i / 2];
           float e, f;
-          unpack2(p[i], e, f);
-          p[i] = pack2(c0 + 2 * i >= lo && c0 + 2 * i < hi ? e : 0.f, c0 + 2 * i + 1 >= lo && c0 + 2 * i + 1 < hi ? f : 0.f);
+          unpack2(fma2(pair_at(x + 2 * i), cc, l.x), e, f);
+          p[i] = pack2(ex2(e), ex2(f));
+          unpack2(fma2(pair_at(x + 2 * i + 2), cc, l.y), e, f);
+          p[i + 1] = pack2(ex2(e), ex2(f));
         }
-      }
+        const int q0 = (w.t0 + t) * tokens;
+        if (a.causal && (q0 + w.off < w.last || (a.window && (int64_t)q0 + tokens > (int64_t)b.first - w.off + a.window))) {
+          // the queries of this tile that see the key: [lo, hi)
+          const int64_t first = (int64_t)key - w.off - q0;
+          const int lo = (int)min(max(first, (int64_t)0), (int64_t)tokens) << ba.pack;
+          const int hi = a.window ? (int)min(max(first + a.window, (int64_t)0), (int64_t)tokens) << ba.pack : TILE;
 #pragma unroll
-      for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(p[i]);
-      store_words(lanes + c0, x);
-      tc::tc_fence_before();
-      warp_arrive(&s.p_full);
-      ok = warp_wait(&s.dp_full, n & 1, ab);
+          for (int i = 0; i < COLS / 2; ++i) {
+            float e, f;
+            unpack2(p[i], e, f);
+            p[i] = pack2(c0 + 2 * i >= lo && c0 + 2 * i < hi ? e : 0.f, c0 + 2 * i + 1 >= lo && c0 + 2 * i + 1 < hi ? f : 0.f);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(p[i]);
+        store_words(lanes + c0, x);
+        tc::tc_fence_before();
+        warp_arrive(&s.p_full);
+        ok = warp_wait(&s.dp_full, g & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        load_cols(lanes + T_DPT + c0, x);
+        const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(&s.delta[g & 1][c0]);
+#pragma unroll
+        for (int i = 0; i < COLS / 2; i += 2) {
+          const ulonglong2 d = ds[i / 2];
+          x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), d.x)));
+          x[i + 1] = round_pair(mul2(p[i + 1], add2(pair_at(x + 2 * i + 2), d.y)));
+        }
+        store_words(lanes + T_DPT + c0, x);
+        tc::tc_fence_before();
+        warp_arrive(&s.ds_full);
+        warp_arrive(&s.row_empty[g & 1]);
+        if (++t == w.per) t = 0;
+      }
       if (!ok) break;
-      tc::tc_fence_after();
-      load_cols(lanes + T_DPT + c0, x);
-      const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(&s.delta[n & 1][c0]);
-#pragma unroll
-      for (int i = 0; i < COLS / 2; i += 2) {
-        const ulonglong2 d = ds[i / 2];
-        x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), d.x)));
-        x[i + 1] = round_pair(mul2(p[i + 1], add2(pair_at(x + 2 * i + 2), d.y)));
+      const bool any = w.n > 0;
+      if (any) {
+        ok = warp_wait(&s.acc_full, k++ & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
       }
-      store_words(lanes + T_DPT + c0, x);
-      tc::tc_fence_before();
-      warp_arrive(&s.ds_full);
-      warp_arrive(&s.row_empty[n & 1]);
-      if (++t == per) t = 0;
-    }
-    if (ok && n_tiles > 0) {
-      ok = warp_wait(&s.done, 0, ab);
-      tc::tc_fence_after();
-    }
-    if (ok) {
-      const int64_t to = ((int64_t)(b.k0 + key) * a.HK + hk) * a.D, all = a.TK * a.HK * a.D;
+      const int64_t to = ((int64_t)(b.k0 + key) * a.HK + w.hk) * a.D, all = a.TK * a.HK * a.D;
       float *dk = nullptr, *dv = nullptr;
       if (ba.parts > 1) {
-        dk = ba.part + part * all + to;
+        dk = ba.part + w.part * all + to;
         dv = dk + ba.parts * all;
       }
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        store16(a.dk + to, dk, DB * 16 * quarter + 16 * i, a.D, lanes + T_DK, a.scale, n_tiles > 0, key < b.lk);
-        store16(a.dv + to, dv, DB * 16 * quarter + 16 * i, a.D, lanes + T_DV, 1.f, n_tiles > 0, key < b.lk);
+        store16(a.dk + to, dk, DB * 16 * quarter + 16 * i, a.D, lanes + T_DK, a.scale, any, key < b.lk);
+        store16(a.dv + to, dv, DB * 16 * quarter + 16 * i, a.D, lanes + T_DV, 1.f, any, key < b.lk);
+      }
+      if (any) {
+        tc::tc_fence_before();
+        warp_arrive(&s.acc_empty);
       }
     }
   }
@@ -700,13 +842,20 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
     ProfScope ps("attn_sum", st, (double)n / a.D);
     return launch_early(k_attn_sum, dim3((unsigned)blocks, y ? 2 : 1), 256, 0, st, f.part, f.parts, n, x, y);
   };
+  // Blocks that take over others' items where there are enough of them: 16384 tokens of 16 heads
+  // of 64, windows of 128 / 1024 / 4096: dQ 85 / 162 / 372 us against 114 / 185 / 390, dK and dV 77 /
+  // 185 / 495 against 119 / 224 / 528; dK and dV of 8192 tokens of 16 heads of 128 over 4 key heads
+  // (512 blocks) 352 against 340.
   if (qblocks > 0) {
     f.parts = p.dq;
     const int64_t blocks = qblocks * (a.H >> f.pack) * f.parts;
     {
       ProfScope ps("attn_dq", st, (double)a.T * a.H);
-      if (cudaError_t e = a.D <= 64 ? go(k_attn_dq<1>, bytes_of<DqSmem<1>>(), blocks, f, st)
-                                    : go(k_attn_dq<2>, bytes_of<DqSmem<2>>(), blocks, f, st))
+      const bool queue = blocks > sm_count();
+      constexpr size_t b1 = bytes_of<DqSmem<1>>(), b2 = bytes_of<DqSmem<2>>();
+      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dq<1, true>, b1, blocks, f, st) : go(k_attn_dq<1, false>, b1, blocks, f, st)
+                          : queue   ? go(k_attn_dq<2, true>, b2, blocks, f, st)
+                                    : go(k_attn_dq<2, false>, b2, blocks, f, st))
         return e;
     }
     if (cudaError_t e = sum(a.T * a.H * a.D, a.dq, nullptr)) return e;
@@ -716,8 +865,11 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
     const int64_t blocks = kblocks * a.HK * f.parts;
     {
       ProfScope ps("attn_dkv", st, (double)a.TK * a.HK);
-      if (cudaError_t e = a.D <= 64 ? go(k_attn_dkv<1>, bytes_of<DkvSmem<1>>(), blocks, f, st)
-                                    : go(k_attn_dkv<2>, bytes_of<DkvSmem<2>>(), blocks, f, st))
+      const bool queue = blocks > 4 * sm_count();
+      constexpr size_t b1 = bytes_of<DkvSmem<1>>(), b2 = bytes_of<DkvSmem<2>>();
+      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dkv<1, true>, b1, blocks, f, st) : go(k_attn_dkv<1, false>, b1, blocks, f, st)
+                          : queue   ? go(k_attn_dkv<2, true>, b2, blocks, f, st)
+                                    : go(k_attn_dkv<2, false>, b2, blocks, f, st))
         return e;
     }
     if (cudaError_t e = sum(a.TK * a.HK * a.D, a.dk, a.dv)) return e;

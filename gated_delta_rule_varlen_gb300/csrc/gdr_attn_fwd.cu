@@ -33,19 +33,62 @@ constexpr int THREADS = 384;
 // Tensor memory: S (and over it P) of the tiles, out of the tiles.
 constexpr int T_S = 0, T_O = 256;
 
+// What a block works on at a time: two tiles of queries of one head (or of several side by
+// side), and a part of the keys that they see.
+struct FwdWork {
+  AttnBlock b;
+  int h0, hk, part;
+  TileRange r[2], all;
+  bool dual;
+  int step;
+  __device__ __forceinline__ void find(const FwdArgs& fa, BlockFinder<true>& finder, int item) {
+    const AttnArgs& a = fa.a;
+    const int heads = 1 << fa.pack, tokens = TILE >> fa.pack, groups = a.H >> fa.pack;
+    part = item % fa.parts;
+    item /= fa.parts;
+    b = finder.find(item / groups);
+    h0 = item % groups * heads;
+    hk = h0 / (a.H / a.HK);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int i0 = b.first + t * tokens;
+      r[t] = tiles_of(a, b.lq, b.lk, i0, min(b.lq, i0 + tokens));
+    }
+    all = {min(r[0].lo, r[1].lo), max(r[0].hi, r[1].hi)};
+    if (r[0].lo >= r[0].hi) all = r[1];
+    if (r[1].lo >= r[1].hi) all = r[0];
+    all = part_of(all, part, fa.parts);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      r[t].lo = max(r[t].lo, all.lo);
+      r[t].hi = min(r[t].hi, all.hi);
+    }
+    // Where the second tile has no queries (few, of long keys), it takes every other key tile
+    // of the first's: what waits on one pair of products goes on with the other.
+    dual = b.first + tokens >= b.lq && r[0].hi - r[0].lo > 1;
+    if (dual) r[1] = r[0];
+    step = dual ? 2 : 1;
+  }
+  __device__ __forceinline__ bool any(int t) const { return r[t].lo < r[t].hi; }
+  __device__ __forceinline__ bool works(int t, int j) const {
+    return dual ? ((j - all.lo) & 1) == t : j >= r[t].lo && j < r[t].hi;
+  }
+};
+
 template <int DB>  // blocks of 64 columns
 struct FwdSmem {
   static constexpr int STAGES = DB == 2 ? 5 : 10;
   unsigned char Q[2][DB * BLK];
   unsigned char KV[STAGES][DB * BLK];  // K and V tiles in turn
-  uint64_t q_full[2], full[STAGES], empty[STAGES], cleared;
-  uint64_t s_full[2], p_full[2], o_full[2], merged, done;
+  uint64_t q_full[2], q_empty, full[STAGES], empty[STAGES], cleared;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], merged, swapped, done;
+  WorkQueue<FwdWork> queue;
   float m[TILE], l[TILE];
   uint32_t tmem;
   int abort;
 };
 
-template <int DB>
+template <int DB, bool QUEUE>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__ FwdArgs fa) {
   using Smem = FwdSmem<DB>;
   constexpr int ST = Smem::STAGES;
@@ -61,14 +104,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         tc::mbar_init(&s.s_full[i], 1);
         tc::mbar_init(&s.p_full[i], 4);
         tc::mbar_init(&s.o_full[i], 1);
+        tc::mbar_init(&s.o_empty[i], 4);
       }
       for (int i = 0; i < ST; ++i) {
         tc::mbar_init(&s.full[i], 1);
         tc::mbar_init(&s.empty[i], 1);
       }
+      tc::mbar_init(&s.q_empty, 1);
+      tc::mbar_init(&s.swapped, 4);
       tc::mbar_init(&s.cleared, 1);
       tc::mbar_init(&s.merged, 4);
       tc::mbar_init(&s.done, 1);
+      s.queue.init(2 + 8);  // (loads, products, softmax)
       s.abort = 0;
       tc::mbar_fence_init();
     }
@@ -77,31 +124,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
     tc::tmem_relinquish();
   }
   const int heads = 1 << fa.pack, tokens = TILE >> fa.pack;  // of a tile
-  const int groups = a.H >> fa.pack, item = blockIdx.x / fa.parts, part = blockIdx.x % fa.parts;
-  const AttnBlock b = find_block<true>(a, a.cu, 2 * tokens, item / groups);
-  const int h0 = item % groups * heads, hk = h0 / (a.H / a.HK);
-  TileRange r[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int i0 = b.first + t * tokens;
-    r[t] = tiles_of(a, b.lq, b.lk, i0, min(b.lq, i0 + tokens));
+  FwdWork w;
+  if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
+    BlockFinder<true> finder(a, 2 * tokens);
+    w.find(fa, finder, (int)blockIdx.x);
   }
-  TileRange all{min(r[0].lo, r[1].lo), max(r[0].hi, r[1].hi)};
-  if (r[0].lo >= r[0].hi) all = r[1];
-  if (r[1].lo >= r[1].hi) all = r[0];
-  all = part_of(all, part, fa.parts);
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    r[t].lo = max(r[t].lo, all.lo);
-    r[t].hi = min(r[t].hi, all.hi);
-  }
-  // Where the second tile has no queries (few, of long keys), it takes every other key tile
-  // of the first's: what waits on one pair of products goes on with the other.
-  const bool dual = b.first + tokens >= b.lq && r[0].hi - r[0].lo > 1;
-  if (dual) r[1] = r[0];
-  const int step = dual ? 2 : 1;
-  auto works = [&](int t, int j) { return dual ? ((j - all.lo) & 1) == t : j >= r[t].lo && j < r[t].hi; };
-  const int j0 = all.lo, j1 = all.hi;
+  int taken = 0;
+  auto next_item = [&](bool ask) {
+    if constexpr (QUEUE) return s.queue.take(taken, w, ab, ask);
+    else return taken++ == 0;
+  };
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -109,69 +141,70 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (warp == 8 && j0 < j1) {  // loads
-      if (lane == 0)
-        for (int t = 0; t < 3 - step; ++t)
-          if (r[t].lo < r[t].hi) {
-            tc::mbar_arrive_expect_tx(&s.q_full[t], DB * BLK);
-            for (int c = 0; c < DB; ++c)
-              tc::tma_load_3d(s.Q[t] + c * BLK, &fa.q_map, 64 * c, h0, b.q0 + b.first + t * tokens, &s.q_full[t]);
-          }
-      __syncwarp();
-      // K of the first `step` tiles, then V of each and K of the one `step` behind it
-      int i = 0, st = 0, ph = 0;
-      auto load = [&](int j, bool isv) {
-        if (i >= ST && !warp_wait(&s.empty[st], ph ^ 1, ab)) return false;
-        const int rows = b.lk - j * TILE;
-        uint64_t* bar = isv && rows < TILE ? &s.cleared : &s.full[st];
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(bar, DB * BLK);
-          for (int c = 0; c < DB; ++c)
-            tc::tma_load_3d(s.KV[st] + c * BLK, isv ? &fa.v_map : &fa.k_map, 64 * c, hk, b.k0 + j * TILE, bar);
-        }
-        __syncwarp();
-        ++i;
-        if (isv && rows < TILE) {  // the document's last tile: clear what lies behind it
-          if (!warp_wait(&s.cleared, 0, ab)) return false;
-          for (int e = rows * 8 + lane; e < TILE * 8; e += 32)
-            for (int c = 0; c < DB; ++c) *reinterpret_cast<uint4*>(s.KV[st] + c * BLK + e * 16) = make_uint4(0, 0, 0, 0);
-          tc::fence_proxy_async();
-          warp_arrive(&s.full[st]);
-        }
-        if (++st == ST) {
-          st = 0;
-          ph ^= 1;
-        }
-        return true;
-      };
+    if (warp == 8) {  // loads
+      int i = 0, st = 0, ph = 0, cleared = 0, works = 0, duals = 0, q_loads[2] = {0, 0};
       bool ok = true;
-      for (int j = j0; j < j0 + step && ok; ++j) ok = load(j, false);
-      for (int j = j0; j < j1 && ok; ++j) {
-        ok = load(j, true);
-        if (ok && j + step < j1) ok = load(j + step, false);
+      while (ok && next_item(true)) {
+        const AttnBlock& b = w.b;
+        if (w.all.lo >= w.all.hi) continue;
+        if (works > 0) ok = warp_wait(&s.q_empty, (works - 1) & 1, ab);
+        if (ok && duals > 0) ok = warp_wait(&s.swapped, (duals - 1) & 1, ab);
+        if (!ok) break;
+        ++works;
+        duals += w.dual;
+        for (int t = 0; t < 3 - w.step; ++t)
+          if (w.any(t)) {
+            ++q_loads[t];
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(&s.q_full[t], DB * BLK);
+              for (int c = 0; c < DB; ++c)
+                tc::tma_load_3d(s.Q[t] + c * BLK, &fa.q_map, 64 * c, w.h0, b.q0 + b.first + t * tokens, &s.q_full[t]);
+            }
+          }
+        __syncwarp();
+        // K of the first `step` tiles, then V of each and K of the one `step` behind it
+        auto load = [&](int j, bool isv) {
+          if (i >= ST && !warp_wait(&s.empty[st], ph ^ 1, ab)) return false;
+          const int rows = b.lk - j * TILE;
+          uint64_t* bar = isv && rows < TILE ? &s.cleared : &s.full[st];
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(bar, DB * BLK);
+            for (int c = 0; c < DB; ++c)
+              tc::tma_load_3d(s.KV[st] + c * BLK, isv ? &fa.v_map : &fa.k_map, 64 * c, w.hk, b.k0 + j * TILE, bar);
+          }
+          __syncwarp();
+          ++i;
+          if (isv && rows < TILE) {  // the document's last tile: clear what lies behind it
+            if (!warp_wait(&s.cleared, cleared++ & 1, ab)) return false;
+            for (int e = rows * 8 + lane; e < TILE * 8; e += 32)
+              for (int c = 0; c < DB; ++c) *reinterpret_cast<uint4*>(s.KV[st] + c * BLK + e * 16) = make_uint4(0, 0, 0, 0);
+            tc::fence_proxy_async();
+            warp_arrive(&s.full[st]);
+          }
+          if (++st == ST) {
+            st = 0;
+            ph ^= 1;
+          }
+          return true;
+        };
+        for (int j = w.all.lo; j < w.all.lo + w.step && ok; ++j) ok = load(j, false);
+        for (int j = w.all.lo; j < w.all.hi && ok; ++j) {
+          ok = load(j, true);
+          if (ok && j + w.step < w.all.hi) ok = load(j + w.step, false);
+        }
       }
       if (!ok) {  // given up: the copies in flight land before the block ends
         for (int k = max(0, i - ST); k < i; ++k) wait_some(&s.full[k % ST], (k / ST) & 1);
-        wait_some(&s.cleared, 0);
-        for (int t = 0; t < 3 - step; ++t)
-          if (r[t].lo < r[t].hi) wait_some(&s.q_full[t], 0);
+        if (cleared > 0) wait_some(&s.cleared, (cleared - 1) & 1);
+        for (int t = 0; t < 2; ++t)
+          if (q_loads[t] > 0) wait_some(&s.q_full[t], (q_loads[t] - 1) & 1);
       }
-    } else if (warp == 9 && j0 < j1) {  // products
+    } else if (warp == 9) {  // products
       const uint32_t id_s = tc::idesc_bf16(TILE, TILE);
       const uint32_t id_o = tc::idesc_bf16(TILE, (a.D + 15) / 16 * 16) | tc::kIdescTransposeB;
       const int ks = (a.D + 15) / 16;
-      uint32_t q_lo[2] = {desc_lo(s.Q[0]), desc_lo(s.Q[dual ? 0 : 1])};
-      auto score = [&](int t, int st) {
-        const uint32_t k_lo = desc_lo(s.KV[st]);
-#pragma unroll
-        for (int k = 0; k < 4 * DB; ++k) {
-          const uint32_t at = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
-          if (k < ks) mma_ss(tmem + T_S + t * TILE, q_lo[t] + at, k_lo + at, id_s, k > 0);
-        }
-        commit(&s.s_full[t]);
-      };
       bool ok = true;
-      int used[2] = {0, 0};
+      int used[2] = {0, 0}, outs[2] = {0, 0}, q_loads[2] = {0, 0};  // tiles, items, loads of Q so far
       int st = 0, ph = 0;  // the next tile of the ring
       auto next = [&] {
         const Phase p{&s.full[st], (uint32_t)ph};
@@ -182,163 +215,211 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         return p;
       };
       auto stage = [&](const Phase& p) { return (int)(p.bar - s.full); };
-      Phase kp{};
-      for (int t = 0; t < 3 - step && ok; ++t)
-        if (r[t].lo < r[t].hi) ok = warp_wait(&s.q_full[t], 0, ab);
-      for (int j = j0; j < j0 + step && ok; ++j) {
-        kp = next();
-        ok = warp_wait(kp.bar, kp.parity, ab);
-        if (!ok) break;
-        for (int t = 0; t < 2; ++t)
-          if (works(t, j)) score(t, stage(kp));
-        commit(&s.empty[stage(kp)]);
-      }
-      for (int j = j0; j < j1 && ok; ++j) {
-        const bool more = j + step < j1;
-        const Phase vp = next();
-        if (more) kp = next();
-        bool loaded = false;  // V of this step, K of the next
-        for (int t = 0; t < 2 && ok; ++t) {
-          const bool here = works(t, j);
-          const Phase pp{here ? &s.p_full[t] : kp.bar, here ? (uint32_t)used[t] & 1 : kp.parity};
-          if (!loaded) {
-            ok = more ? warp_wait_all(ab, vp, kp, here ? pp : kp) : warp_wait_all(ab, vp, here ? pp : vp);
-            loaded = true;
-          } else if (here) {
-            ok = warp_wait(pp.bar, pp.parity, ab);
+      while (ok && next_item(false)) {
+        const int j0 = w.all.lo, j1 = w.all.hi;
+        if (j0 >= j1) continue;
+        const uint32_t q_lo[2] = {desc_lo(s.Q[0]), desc_lo(s.Q[w.dual ? 0 : 1])};
+        auto score = [&](int t, int at) {
+          const uint32_t k_lo = desc_lo(s.KV[at]);
+#pragma unroll
+          for (int k = 0; k < 4 * DB; ++k) {
+            const uint32_t o = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
+            if (k < ks) mma_ss(tmem + T_S + t * TILE, q_lo[t] + o, k_lo + o, id_s, k > 0);
+          }
+          commit(&s.s_full[t]);
+        };
+        Phase kp{};
+        for (int t = 0; t < 3 - w.step && ok; ++t)
+          if (w.any(t)) ok = warp_wait(&s.q_full[t], q_loads[t]++ & 1, ab);
+        for (int j = j0; j < j0 + w.step && ok; ++j) {
+          kp = next();
+          ok = warp_wait(kp.bar, kp.parity, ab);
+          if (!ok) break;
+          for (int t = 0; t < 2; ++t)
+            if (w.works(t, j)) score(t, stage(kp));
+          commit(&s.empty[stage(kp)]);
+          if (j == j1 - 1) commit(&s.q_empty);
+        }
+        bool first[2] = {true, true};
+        for (int j = j0; j < j1 && ok; ++j) {
+          const bool more = j + w.step < j1;
+          const Phase vp = next();
+          if (more) kp = next();
+          bool loaded = false;  // V of this step, K of the next
+          for (int t = 0; t < 2 && ok; ++t) {
+            const bool here = w.works(t, j);
+            const Phase pp{here ? &s.p_full[t] : vp.bar, here ? (uint32_t)used[t] & 1 : vp.parity};
+            if (here && first[t] && outs[t] > 0) ok = warp_wait(&s.o_empty[t], (outs[t] - 1) & 1, ab);
+            if (!ok) break;
+            if (!loaded) {
+              ok = more ? warp_wait_all(ab, vp, kp, pp) : warp_wait_all(ab, vp, pp);
+              loaded = true;
+            } else if (here) {
+              ok = warp_wait(pp.bar, pp.parity, ab);
+            }
+            if (!ok) break;
+            if (here) {
+              tc::tc_fence_after();
+              const uint32_t v_lo = desc_lo(s.KV[stage(vp)]);
+#pragma unroll
+              for (int k = 0; k < TILE / 16; ++k)
+                mma_ts(tmem + T_O + t * TILE, tmem + T_S + t * TILE + 8 * k, v_lo + k * (16 * 128 >> 4), id_o, !first[t] || k > 0);
+              ++used[t];
+              first[t] = false;
+              if (j + w.step >= w.r[t].hi) {
+                commit(&s.o_full[t]);
+                ++outs[t];
+              }
+            }
+            if (more && w.works(t, j + w.step)) score(t, stage(kp));
           }
           if (!ok) break;
-          if (here) {
-            tc::tc_fence_after();
-            const uint32_t v_lo = desc_lo(s.KV[stage(vp)]);
-#pragma unroll
-            for (int k = 0; k < TILE / 16; ++k)
-              mma_ts(tmem + T_O + t * TILE, tmem + T_S + t * TILE + 8 * k, v_lo + k * (16 * 128 >> 4), id_o, used[t] > 0 || k > 0);
-            ++used[t];
-            if (j + step >= r[t].hi) commit(&s.o_full[t]);
-          }
-          if (more && works(t, j + step)) score(t, stage(kp));
+          commit(&s.empty[stage(vp)]);
+          if (more) commit(&s.empty[stage(kp)]);
+          if (j + w.step == j1 - 1) commit(&s.q_empty);  // (the last scores)
         }
-        if (!ok) break;
-        commit(&s.empty[stage(vp)]);
-        if (more) commit(&s.empty[stage(kp)]);
       }
       commit(&s.done);
       wait_some(&s.done, 0);
+    } else if (warp == 10) {
+      if constexpr (QUEUE) {
+        BlockFinder<true> finder(a, 2 * tokens);
+        s.queue.run(ab, [&](int item) {
+          w.find(fa, finder, item);
+          return w;
+        });
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     const int t = warp >> 2, row = tid & 127;
-    const int i0 = b.first + (dual ? 0 : t * tokens), i1 = min(b.lq, i0 + tokens);
-    const int token = i0 + (row >> fa.pack), h = h0 + (row & (heads - 1));
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + T_S + t * TILE, to = lanes + T_O + t * TILE;
-    const bool live = token < b.lq;
-    const KeyRange kr = keys_of(a, token, b.lq, b.lk);
     const float c = a.scale * LOG2E;
-    float m = -INFINITY, l = 0.f;  // the maximum (of scores before the scale), the sum
-    const KeyRange seen{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, i0, b.lq, b.lk).hi};  // keys every row sees
     bool ok = true;
-    for (int j = r[t].lo + (dual ? t : 0), n = 0; j < r[t].hi; j += step, ++n) {
-      ok = warp_wait(&s.s_full[t], n & 1, ab);
-      if (!ok) break;
-      tc::tc_fence_after();
-      uint32_t x[TILE];
+    int tiles = 0, outs[2] = {0, 0}, merges = 0;
+    while (ok && next_item(false)) {
+      const AttnBlock& b = w.b;
+      const bool dual = w.dual, other = dual && t == 1;
+      const int i0 = b.first + (dual ? 0 : t * tokens), i1 = min(b.lq, i0 + tokens);
+      const int token = i0 + (row >> fa.pack), h = w.h0 + (row & (heads - 1));
+      const bool live = token < b.lq;
+      const KeyRange kr = keys_of(a, token, b.lq, b.lk);
+      float m = -INFINITY, l = 0.f;  // the maximum (of scores before the scale), the sum
+      const KeyRange seen{keys_of(a, i1 - 1, b.lq, b.lk).lo, keys_of(a, i0, b.lq, b.lk).hi};  // keys every row sees
+      bool first = true;
+      for (int j = w.r[t].lo + (other ? 1 : 0); j < w.r[t].hi; j += w.step) {
+        ok = warp_wait(&s.s_full[t], tiles++ & 1, ab);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint32_t x[TILE];
 #pragma unroll
-      for (int i = 0; i < TILE; i += 32) tc::tmem_ld32(ts + i, x + i);
-      tc::tmem_wait_ld();
-      pin(x);
-      if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
-        const int lo = kr.lo - j * TILE, hi = kr.hi - j * TILE;
+        for (int i = 0; i < TILE; i += 32) tc::tmem_ld32(ts + i, x + i);
+        tc::tmem_wait_ld();
+        pin(x);
+        if (j * TILE < seen.lo || (j + 1) * TILE > seen.hi) {
+          const int lo = kr.lo - j * TILE, hi = kr.hi - j * TILE;
 #pragma unroll
-        for (int i = 0; i < TILE; ++i) x[i] = i >= lo && i < hi ? x[i] : 0xff800000u;
+          for (int i = 0; i < TILE; ++i) x[i] = i >= lo && i < hi ? x[i] : 0xff800000u;
+        }
+        float top[4] = {m, m, m, m};
+#pragma unroll
+        for (int i = 0; i < TILE; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(x[i]));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {  // (and of -inf: the first keys a row sees)
+          const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
+          m = mx;
+          l *= f;
+          if (!first) {  // the products before this tile's scores are complete
+#pragma unroll 1
+            for (int i = 0; i < DB * 64; i += 32) {
+              uint32_t o[32];
+              tc::tmem_ld32(to + i, o);
+              tc::tmem_wait_ld();
+              pin(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tc::tmem_st32(to + i, o);
+            }
+          }
+        }
+        first = false;
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t cc = pack2(c, c), bb = pack2(base, base);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < TILE; i += 2) {
+          const uint64_t e = fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cc, bb);
+          float p, q;
+          unpack2(e, p, q);
+          p = ex2(p);
+          q = ex2(q);
+          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p, q));
+          const __nv_bfloat162 v = __floats2bfloat162_rn(p, q);
+          x[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        tc::tmem_st32(ts, x);
+        tc::tmem_st32(ts + 32, x + 32);
+        l += sum_of(add2(sum[0], sum[1]));
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        warp_arrive(&s.p_full[t]);
       }
-      float top[4] = {m, m, m, m};
-#pragma unroll
-      for (int i = 0; i < TILE; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(x[i]));
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {  // (and of -inf: the first keys a row sees)
-        const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
-        m = mx;
-        l *= f;
-        if (n > 0) {  // the products before this tile's scores are complete
+      if (!ok) break;
+      const int64_t at = (int64_t)(b.q0 + token);
+      const bool any = w.any(t);
+      if (dual) {
+        ok = warp_wait_all(ab, Phase{&s.o_full[0], (uint32_t)outs[0] & 1}, Phase{&s.o_full[1], (uint32_t)outs[1] & 1});
+      } else if (any) {
+        ok = warp_wait(&s.o_full[t], (t ? outs[1] : outs[0]) & 1, ab);
+      }
+      if (!ok) break;
+      outs[0] += w.any(0);
+      outs[1] += w.any(1);
+      tc::tc_fence_after();
+      // The halves of a dual tile: the second's sums and out cross shared memory (both places of
+      // Q, which the products have read) to the first.
+      static_assert(TILE * DB * 64 * 4 <= sizeof(s.Q), "a tile of FP32");
+      float* swap = reinterpret_cast<float*>(s.Q) + row * DB * 64;
+      auto place = [&](int i) { return (i / 4 ^ (row & 15)) * 4; };  // (rows are a multiple of 32 banks apart)
+      const bool rows = __any_sync(0xffffffffu, live);
+      float f0 = 1.f, f1 = 0.f;
+      if (other) {
+        s.m[row] = m;
+        s.l[row] = l;
+        if (rows) {
 #pragma unroll 1
           for (int i = 0; i < DB * 64; i += 32) {
             uint32_t o[32];
             tc::tmem_ld32(to + i, o);
             tc::tmem_wait_ld();
             pin(o);
+            if (live)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tc::tmem_st32(to + i, o);
+              for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(swap + place(i + k)) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           }
         }
+        tc::tc_fence_before();
+        warp_arrive(&s.o_empty[1]);
+        warp_arrive(&s.merged);
+        continue;
       }
-      const float base = m == -INFINITY ? 0.f : -m * c;
-      const uint64_t cc = pack2(c, c), bb = pack2(base, base);
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < TILE; i += 2) {
-        const uint64_t e = fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cc, bb);
-        float p, q;
-        unpack2(e, p, q);
-        p = ex2(p);
-        q = ex2(q);
-        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p, q));
-        const __nv_bfloat162 w = __floats2bfloat162_rn(p, q);
-        x[i / 2] = *reinterpret_cast<const uint32_t*>(&w);
+      if (dual) {
+        ok = warp_wait(&s.merged, merges++ & 1, ab);
+        if (!ok) break;
+        const float m1 = s.m[row], top = fmaxf(m, m1);
+        f0 = m == -INFINITY ? 0.f : ex2((m - top) * c);
+        f1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * c);
+        l = fmaf(l, f0, s.l[row] * f1);
+        m = top;
       }
-      tc::tmem_st32(ts, x);
-      tc::tmem_st32(ts + 32, x + 32);
-      l += sum_of(add2(sum[0], sum[1]));
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      warp_arrive(&s.p_full[t]);
-    }
-    const int64_t at = (int64_t)(b.q0 + token);
-    const bool any = r[t].lo < r[t].hi;
-    if (ok && any) {
-      ok = dual ? warp_wait_all(ab, Phase{&s.o_full[0], 0}, Phase{&s.o_full[1], 0}) : warp_wait(&s.o_full[t], 0, ab);
-      tc::tc_fence_after();
-    }
-    // The halves of a dual tile: the second's sums and out cross shared memory (the key tiles',
-    // which nothing reads any more) to the first.
-    constexpr int PITCH = DB * 64 + 4;
-    static_assert(TILE * PITCH * 4 <= sizeof(s.KV), "a tile of FP32");
-    float* swap = reinterpret_cast<float*>(s.KV) + row * PITCH;
-    float f0 = 1.f, f1 = 0.f;
-    if (dual && t == 1 && ok) {
-      s.m[row] = m;
-      s.l[row] = l;
-      if (__any_sync(0xffffffffu, live)) {
-#pragma unroll 1
-        for (int i = 0; i < DB * 64; i += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32(to + i, o);
-          tc::tmem_wait_ld();
-          pin(o);
-          if (live)
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(swap + i + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
-      }
-      warp_arrive(&s.merged);
-    } else if (dual && ok) {
-      ok = warp_wait(&s.merged, 0, ab);
-      const float m1 = s.m[row], top = fmaxf(m, m1);
-      f0 = m == -INFINITY ? 0.f : ex2((m - top) * c);
-      f1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * c);
-      l = fmaf(l, f0, s.l[row] * f1);
-      m = top;
-    }
-    if (ok && !(dual && t == 1) && __any_sync(0xffffffffu, live)) {
       const float f = l == 0.f ? 0.f : 1.f / l;
       f0 *= f;
       f1 *= f;
       __nv_bfloat16* out = a.out + (at * a.H + h) * a.D;
-      float* part_out = fa.part_out + ((part * a.T + at) * a.H + h) * a.D;
+      float* part_out = fa.part_out + ((w.part * a.T + at) * a.H + h) * a.D;
 #pragma unroll 1
-      for (int i = 0; i < DB * 64; i += 32) {
+      for (int i = 0; i < DB * 64 && rows; i += 32) {
         uint32_t o[32];
         if (any) {
           tc::tmem_ld32(to + i, o);
@@ -351,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         if (dual && live)
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(swap + i + k);
+            const float4 x = *reinterpret_cast<const float4*>(swap + place(i + k));
             v[k] = fmaf(x.x, f1, v[k]);
             v[k + 1] = fmaf(x.y, f1, v[k + 1]);
             v[k + 2] = fmaf(x.z, f1, v[k + 2]);
@@ -365,16 +446,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
         }
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
-          uint32_t w[4];
+          uint32_t u[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const __nv_bfloat162 x = __floats2bfloat162_rn(v[k + 2 * e], v[k + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&x);
+            u[e] = *reinterpret_cast<const uint32_t*>(&x);
           }
-          if (live && i + k < a.D) *reinterpret_cast<uint4*>(out + i + k) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (live && i + k < a.D) *reinterpret_cast<uint4*>(out + i + k) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
-      float* lse = fa.parts > 1 ? fa.part_lse + (int64_t)part * a.H * a.T : a.lse;
+      if (any) {
+        tc::tc_fence_before();
+        warp_arrive(&s.o_empty[t]);
+      }
+      if (dual) {
+        tc::fence_proxy_async();  // (Q comes by asynchronous copies again)
+        warp_arrive(&s.swapped);
+      }
+      float* lse = fa.parts > 1 ? fa.part_lse + (int64_t)w.part * a.H * a.T : a.lse;
       if (live) lse[h * a.T + at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718f;
     }
   }
@@ -443,9 +532,15 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
     return cudaGetLastError();
   };
   static_assert(sizeof(FwdSmem<1>) <= 232448 && sizeof(FwdSmem<2>) <= 232448, "227 KB of shared memory a block");
+  // Blocks that take over others' items gain on short ones of up to 64 columns, whose start and end
+  // they hide: 16384 tokens of 16 heads, windows of 128 / 1024 / 4096: 71 / 135 / 316 us against 82 /
+  // 142 / 319; of 128 columns they lose (98 / 175 / 403 against 98 / 169 / 385).
   {
     ProfScope ps("attn_fwd", st, (double)a.T * a.H);
-    if (cudaError_t e = a.D <= 64 ? go(k_attn_fwd<1>, sizeof(FwdSmem<1>)) : go(k_attn_fwd<2>, sizeof(FwdSmem<2>))) return e;
+    if (cudaError_t e = a.D > 64                 ? go(k_attn_fwd<2, false>, sizeof(FwdSmem<2>))
+                        : blocks <= sm_count() ? go(k_attn_fwd<1, false>, sizeof(FwdSmem<1>))
+                                               : go(k_attn_fwd<1, true>, sizeof(FwdSmem<1>)))
+      return e;
   }
   if (f.parts == 1) return cudaSuccess;
   ProfScope ps("attn_join", st, (double)a.T * a.H);
@@ -456,16 +551,20 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
 // not fill a tile.
 //
 // Parts: few blocks, or few of them much longer than the rest, leave SMs without work.  The
-// number with the least estimated time is taken, in steps of a block (a pair of tiles): kStart
-// to start and end a block, the join's traffic in steps' worth of bytes.  Only plans of up to
-// four waves of blocks are looked at: more of them are even enough.
+// number with the least estimated time is taken, in steps of a block (two tiles' products,
+// some 1.4 us): a block's start and end, with the share that it leaves where there are
+// several, and the join's traffic.  Measured in 1 / 2 / 3 / 4 / 8 parts, the join's time
+// included: one token of 65536 keys, 8 key heads 520 / 272 / 190 / 146 / 88 us, 16 parts 73; a
+// prompt of 24576 tokens of one head 319 / 180 / 137 / 156 / 181; dK and dV of 4096 tokens, 16
+// heads over 4 key heads 178 / 109 / 129 / 132 / 179.  Only up to four blocks an SM are
+// looked at: more of them are even enough.
 AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
   AttnPlan p{0, 1, 1, 1, 0, 0};
   int most = 0;
   for (int i = 0; i < a.N; ++i) most = std::max(most, cu[i + 1] - cu[i]);
   const int G = a.H / a.HK;
   while (p.pack < 7 && G % (2 << p.pack) == 0 && ((int64_t)most << p.pack) < TILE) ++p.pack;
-  const double sms = 152.0, kStart = 3.0, kBytes = 8e6;  // (bytes that HBM moves in a step)
+  const double sms = 152.0, kStart = 4.0, kShare = 4.0, kJoin = 2.0, kBytes = 8e6;  // (bytes that HBM moves in a step)
   const int tokens = TILE >> p.pack;
   // parts of blocks of `per` rows of `lens`, `heads` a block each, `rows` of FP32 left by a part
   auto parts = [&](const int32_t* lens, int per, int64_t heads, double row_bytes, auto tiles) {
@@ -484,9 +583,9 @@ AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
     double least = 0;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (s > 1 && s > longest / 2) break;
-      const double one = (double)((longest + s - 1) / s) + kStart, work = (total + kStart * blocks * s) / sms;
-      double time = blocks * s <= 152 ? one : std::max(one, work) + 0.3 * one;
-      if (s > 1) time += 2.0 + 2.0 * s * row_bytes / kBytes;
+      const double start = kStart + (s > 1 ? kShare : 0.0);
+      double time = std::max((double)((longest + s - 1) / s) + start, (total + start * blocks * s) / sms);
+      if (s > 1) time += kJoin + 2.0 * s * row_bytes / kBytes;
       if (s == 1 || time < 0.9 * least) {
         best = s;
         least = time;
