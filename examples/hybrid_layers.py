@@ -1,4 +1,4 @@
-"""Two token mixers built from the library's operators, in training, on prompts
+"""Three token mixers built from the library's operators, in training, on prompts
 and token by token:
 
 * a grouped GDN layer: norm -> projections -> short convolution (+ SiLU) on q, k
@@ -6,8 +6,10 @@ and token by token:
   gate -> output projection;
 * a scan layer: norm -> projections -> short convolution on x, B and C -> selective
   state space scan -> norm and gate -> output projection;
+* a softmax attention layer: layer norm -> projections -> rotary positions on q and k ->
+  attention over the document's tokens and the cached keys before them -> output projection;
 
-between them the residual, its scale and the next norm in one pass.  Run as a
+between the first two the residual, its scale and the next norm in one pass.  Run as a
 program it checks that serving continues a prompt (the same text as one prompt,
 and as a prompt followed by single tokens from the cached states) and that a
 training step's gradients agree with differences, and prints what each form took:
@@ -126,6 +128,48 @@ class ScanMixer:
         return o @ self.w_out
 
 
+class AttentionMixer:
+    """Softmax attention of H query heads over HK key heads of D; the state is each
+    document's keys and values so far, packed as `lengths` says."""
+
+    def __init__(self, g, width, H, HK, D):
+        self.H, self.HK, self.D = H, HK, D
+        self.norm_weight, self.norm_bias = torch.ones(width, device="cuda"), randn(g, width, scale=0.1, dtype=F32)
+        self.w_in = randn(g, width, (H + 2 * HK) * D, scale=width ** -0.5)
+        self.w_out = randn(g, H * D, width, scale=(H * D) ** -0.5)
+        self.freqs = gdr.rope_frequencies(D, scaling="parts", factor=4.0)
+
+    def _project(self, x, positions):
+        _, y = gdr.lnorm_fwd(x, self.norm_weight, self.norm_bias)
+        a, b = self.H * self.D, (self.H + self.HK) * self.D
+        p = y @ self.w_in
+        q, k, v = (s.unflatten(1, (-1, self.D)) for s in (p[:, :a], p[:, a:b], p[:, b:]))  # slices, as they are
+        return *gdr.rope_fwd(q, k, self.freqs, positions=positions), v
+
+    def prompt(self, x, cu, cu_host, state=None):
+        new = [b - a for a, b in zip(cu_host, cu_host[1:])]
+        old, keys, values = state if state is not None else ([0] * len(new), None, None)
+        positions = torch.cat([torch.arange(a, a + n) for a, n in zip(old, new)]).to("cuda", torch.int32)
+        q, k, v = self._project(x, positions)
+        lengths, args = [a + n for a, n in zip(old, new)], {}
+        if state is not None:
+            k, v = (torch.cat([t for pair in zip(c.split(old), n.split(new)) for t in pair]) for c, n in ((keys, k), (values, v)))
+            args = dict(zip(("cu_keys", "cu_keys_host"), pack(lengths)))
+        o, _ = gdr.attn_fwd(q, k, v, cu, cu_host, **args)
+        return o.flatten(1) @ self.w_out, (lengths, k, v)
+
+    def train(self, x, cu, cu_host, dout):
+        """Forward, and the gradients of sum(out * dout) with respect to the norm's weight and bias."""
+        q, k, v = self._project(x, torch.cat([torch.arange(b - a) for a, b in zip(cu_host, cu_host[1:])]).to("cuda", torch.int32))
+        o, lse = gdr.attn_fwd(q, k, v, cu, cu_host)
+        out = o.flatten(1) @ self.w_out
+        ga = gdr.attn_bwd(q, k, v, o, lse, (dout @ self.w_out.t()).unflatten(1, (self.H, self.D)), cu, cu_host)
+        dq, dk = gdr.rope_bwd(ga["dq"], ga["dk"], self.freqs, cu_seqlens=cu)
+        dy = torch.cat([dq.flatten(1), dk.flatten(1), ga["dv"].flatten(1)], 1) @ self.w_in.t()
+        gn = gdr.lnorm_bwd(x, self.norm_weight, self.norm_bias, dy=dy)
+        return out, {"norm_weight": gn["dweight"], "norm_bias": gn["dbias"]}
+
+
 class Model:
     def __init__(self, seed, width=512, Hqk=2, HV=4, H=8, P=64, G=1, N=128, depth=2):
         g = torch.Generator(device="cuda")
@@ -176,15 +220,30 @@ def serve(model, lengths, more, width=512, seed=1):
     return rel(got, torch.stack(want))
 
 
-def train(model, lengths, width=512, seed=2):
+def attend(mixer, lengths, more, width=512, seed=3):
+    """The same of an attention layer alone: prompt, the keys it leaves, and single tokens after them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    texts = [randn(g, n + more, width) for n in lengths]
+    whole, _ = mixer.prompt(torch.cat(texts), *pack([n + more for n in lengths]))
+    want = [t[-more:] for t in whole.split([n + more for n in lengths])]
+    _, state = mixer.prompt(torch.cat([t[:-more] for t in texts]), *pack(lengths))
+    got, each = [], pack([1] * len(lengths))
+    for i in range(more):
+        out, state = mixer.prompt(torch.stack([t[n + i] for t, n in zip(texts, lengths)]), *each, state)
+        got.append(out)
+    return rel(torch.stack(got, 1), torch.stack(want))
+
+
+def train(m, names, lengths, width=512, seed=2):
     """(relative difference of the directional derivative by differences from the gradients', for each parameter)"""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
-    m, T = model.mixers[0], sum(lengths)
+    T = sum(lengths)
     x, dout, cu = randn(g, T, width), randn(g, T, width), pack(lengths)
     _, grads = m.train(x, *cu, dout)
     got = {}
-    for name in ("conv", "out_norm"):
+    for name in names:
         p = getattr(m, name)
         v, eps = grads[name] / grads[name].norm(), 0.25 if name == "conv" else 0.5
         loss = []
@@ -207,18 +266,25 @@ def main(argv=None):
     model = Model(0)
     serve(model, lengths, 2)  # warm-up
     d = serve(model, lengths, a.more)
-    t = train(model, lengths)
+    t = train(model.mixers[0], ("conv", "out_norm"), lengths)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    mixer = AttentionMixer(g, 512, 8, 2, 64)
+    da = attend(mixer, lengths, a.more)
+    t.update(train(mixer, ("norm_weight", "norm_bias"), lengths))
     gdr.gdr_check_device()
-    print(f"serving: outputs of {a.more} single tokens after the prompts differ by {d:.2e} from one prompt of all")
+    print(f"serving: outputs of {a.more} single tokens after the prompts differ by {d:.2e} from one prompt of all, {da:.2e} of attention")
     print("training: gradients and differences apart by " + ", ".join(f"{k} {v:.2e}" for k, v in t.items()))
     gdr.gdr_profile_enable(True)
     serve(model, lengths, a.more)
-    train(model, lengths)
+    train(model.mixers[0], ("conv", "out_norm"), lengths)
+    attend(mixer, lengths, a.more)
+    train(mixer, ("norm_weight", "norm_bias"), lengths)
     torch.cuda.synchronize()
     gdr.gdr_profile_enable(False)
     for name, (n, ms, _) in sorted(gdr.gdr_profile_report().items(), key=lambda kv: -kv[1][1]):
         print(f"  {name:14s} {n:5d} launches {1e3 * ms / n:9.2f} us each")
-    return d, t
+    return max(d, da), t
 
 
 if __name__ == "__main__":

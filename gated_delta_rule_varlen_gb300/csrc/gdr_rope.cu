@@ -42,6 +42,9 @@ struct RopeArgs {
 };
 
 constexpr int THREADS = 256;
+// Units a thread asks for together: of eight elements (two pieces of 16 bytes each) two, so
+// that an SM holds four blocks (64 registers a thread); with four of them it held two.
+constexpr int rope_ahead(int V, bool inter) { return V == 8 && !inter ? 2 : 4; }
 
 // 2^64 of the fraction of a turn that frequency f (radians) advances: f = m 2^(e - 150)
 // times 1 / (2 pi) = kTurn 2^-66, in integers (64-bit floating point has 1/64 of their rate).
@@ -95,8 +98,8 @@ __device__ __forceinline__ Vec<T, V> packed(const float (&f)[V]) {
 }
 
 template <typename T, int V, bool INTER, bool LOOSE>
-__global__ void __launch_bounds__(THREADS) k_rope(const __grid_constant__ RopeArgs a) {
-  constexpr int PAIRS = INTER ? V / 2 : V, U = 4;  // units asked for together
+__global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ RopeArgs a) {
+  constexpr int PAIRS = INTER ? V / 2 : V, U = rope_ahead(V, INTER);  // units asked for together
   extern __shared__ __align__(16) float rope_smem[];
   const int half = a.R / 2;
   float *cs = rope_smem, *sn = rope_smem + a.tokens * half;  // [tokens][R / 2]

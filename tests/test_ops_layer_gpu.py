@@ -480,3 +480,133 @@ def test_the_layer_captured_and_on_another_stream(gdr):
     torch.cuda.synchronize()
     for a, o, n, c in zip(want, other, new, held):
         assert torch.equal(a, o) and torch.equal(n, c) and not torch.equal(a, c)
+
+
+# ---------------------------------------------------------------------------
+# Attention: the kernels' other paths
+# ---------------------------------------------------------------------------
+MANY = [
+    # many documents (found 32 at a time), many short blocks (taken over), few long ones (in
+    # parts), every other key tile of a block with few queries
+    ([200, 0, 1, 65] * 40, None, 4, 2, 128, True, 0), ([300] * 50, None, 8, 8, 64, True, 100), ([128] * 200, None, 2, 1, 64, False, 0),
+    ([2100], None, 1, 1, 128, True, 0), ([1500], None, 8, 1, 64, True, 0), ([3000], None, 2, 2, 64, True, 700),
+    ([129, 1], [2500, 300], 1, 1, 128, True, 0), ([3] * 40, [700 + 13 * i for i in range(40)], 8, 2, 128, True, 0),
+    ([100, 30], [1800, 2300], 4, 4, 80, True, 0), ([1] * 3, [6000, 257, 384], 16, 16, 64, True, 300), ([40], [3000], 6, 3, 128, False, 0),
+]
+
+
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", MANY)
+def test_attention_of_many_and_of_long_documents(gdr, lq, lk, H, HK, D, causal, window):
+    test_attention_forward_and_gradients(gdr, lq, lk, H, HK, D, causal, window, "dense")
+
+
+def test_attention_reads_nothing_of_its_scratch_before_writing_it(gdr):
+    g, T, H, HK, D = gen(21), 2600, 2, 1, 128
+    q, k, v = heads(g, T, H, HK, D, "dense", T)
+    dout = randn(g, T, H, D, dtype=BF16)
+    cu, cuh = pack([2590, 10])
+    fwd, bwd = gdr.attn_workspace_bytes(T, T, H, HK, D, cuh)
+    assert fwd > 0 and bwd > T * H * 4 + 256  # in parts
+    dirty = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in (fwd, bwd)]  # (NaN in every type)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh)
+    got = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh)
+    out2, lse2 = gdr.attn_fwd(q, k, v, cu, cuh, scratch=dirty[0])
+    got2 = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, scratch=dirty[1])
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and all(torch.equal(got[n], got2[n]) for n in got)
+
+
+def test_attention_on_two_streams_at_once_and_captured(gdr):
+    g, H, HK, D = gen(22), 2, 1, 64
+    cases = []
+    for lens in ([2300], [300] * 30):  # in parts; blocks that take over others' items
+        T = sum(lens)
+        cases.append((heads(g, T, H, HK, D, "dense", T), randn(g, T, H, D, dtype=BF16), pack(lens)))
+
+    def run(case):
+        (q, k, v), dout, pk = case
+        out, lse = gdr.attn_fwd(q, k, v, *pk)
+        return out, lse, *gdr.attn_bwd(q, k, v, out, lse, dout, *pk).values()
+
+    want = [run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(3):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(run(c))
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2])), i
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [run(c) for c in cases]
+    for c in cases:
+        c[0][0].copy_(c[0][0].flip(0))
+    new = [run(c) for c in cases]
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(held, new):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    gdr.gdr_check_device()
+
+
+def test_attention_leaves_what_lies_around_its_outputs(gdr):
+    # outputs as parts of larger tensors: rows before and behind keep their values
+    g, lens, H, HK, D = gen(23), [70, 200, 1], 3, 1, 96
+    T = sum(lens)
+    cu, cuh = pack(lens)
+    q, k, v = heads(g, T, H, HK, D, "dense", T)
+    dout = randn(g, T, H, D, dtype=BF16)
+
+    def room(n, h):
+        t = torch.full((n + 6, h, D), 3.0, dtype=BF16, device="cuda")
+        return t, t[3:-3]
+    wide_out, out = room(T, H)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, out=out)
+    wides, grads = {}, {}
+    for n, h in (("dq", H), ("dk", HK), ("dv", HK)):
+        wides[n], grads[n] = room(T, h)
+    gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, grads=grads)
+    plain, _ = gdr.attn_fwd(q, k, v, cu, cuh)
+    assert torch.equal(out, plain)
+    for t in (wide_out, *wides.values()):
+        assert (t[:3] == 3).all() and (t[-3:] == 3).all()
+
+
+def test_calls_on_a_stream_argument(gdr):
+    g, T = gen(24), 300
+    q, k, v = heads(g, T, 2, 2, 64, "dense", T)
+    cu, cuh = pack([T])
+    x, w = randn(g, T, 512, dtype=BF16), randn(g, 512, dtype=BF16)
+    f = gdr.rope_frequencies(64)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, stream=s)
+    grads = gdr.attn_bwd(q, k, v, out, lse, q, cu, cuh, stream=s)
+    _, y = gdr.lnorm_fwd(x, w, stream=s)
+    dx = gdr.lnorm_bwd(x, w, dy=x, stream=s)["dx"]
+    turned, _ = gdr.rope_fwd(q, None, f, cu_seqlens=cu, stream=s)
+    back, _ = gdr.rope_bwd(turned, None, f, cu_seqlens=cu, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    out2, lse2 = gdr.attn_fwd(q, k, v, cu, cuh)
+    assert torch.equal(out, out2) and torch.equal(grads["dk"], gdr.attn_bwd(q, k, v, out2, lse2, q, cu, cuh)["dk"])
+    assert torch.equal(y, gdr.lnorm_fwd(x, w)[1]) and torch.equal(dx, gdr.lnorm_bwd(x, w, dy=x)["dx"])
+    # there and back: two bf16 roundings
+    assert rel(back, q) <= 2 * 2.5e-3
+
+
+def test_single_tokens_follow_the_prompt(gdr):
+    # the last token of each document alone against its keys, and the document's last row
+    g, lens, H, HK, D = gen(25), [1, 130, 1000, 257, 64], 8, 2, 128
+    T = sum(lens)
+    q, k, v = heads(g, T, H, HK, D, "dense", T)
+    cu, cuh = pack(lens)
+    for window in (0, 100):
+        whole, lse = gdr.attn_fwd(q, k, v, cu, cuh, window=window)
+        last = torch.tensor(cuh[1:], device="cuda") - 1
+        one, ocu = pack([1] * len(lens))
+        out, ol = gdr.attn_fwd(q[last], k, v, one, ocu, window=window, cu_keys=cu, cu_keys_host=cuh)
+        assert rel(out, whole[last]) <= 2 * TOL_OUT and rel(ol, lse[:, last]) <= TOL_LSE
