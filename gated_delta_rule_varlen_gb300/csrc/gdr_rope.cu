@@ -39,12 +39,13 @@ struct RopeArgs {
   int back;
   int units, turned;   // pieces of a head: all, those that turn
   int tokens;          // of a block
+  int copy;            // where the second piece of a unit to copy lies (0: it has none)
 };
 
 constexpr int THREADS = 256;
 // Units a thread asks for together: of eight elements (two pieces of 16 bytes each) two, so
 // that an SM holds four blocks (64 registers a thread); with four of them it held two.
-constexpr int rope_ahead(int V, bool inter) { return V == 8 && !inter ? 2 : 4; }
+constexpr int rope_ahead(int V) { return V == 8 ? 2 : 4; }
 
 // 2^64 of the fraction of a turn that frequency f (radians) advances: f = m 2^(e - 150)
 // times 1 / (2 pi) = kTurn 2^-66, in integers (64-bit floating point has 1/64 of their rate).
@@ -67,9 +68,9 @@ __device__ __forceinline__ void angle(uint64_t turns, uint64_t pos, float amp, b
   s *= back ? -amp : amp;
 }
 
-// A unit of a head: V elements from each half of the turned part (interleaved: V elements
-// of V / 2 pairs), or V elements to copy.  LOOSE: rows on no common boundary, element by
-// element.
+// A unit of a head: V elements from each half of the turned part (interleaved: of V / 2 pairs
+// each), or V elements of the rest to copy (from each half of it where its size allows).
+// LOOSE: rows on no common boundary, element by element; interleaved one pair a unit.
 template <typename T, int V, bool LOOSE>
 __device__ __forceinline__ Vec<T, V> load_piece(const T* p, int n) {
   if constexpr (!LOOSE) return vload<T, V>(p);
@@ -99,7 +100,8 @@ __device__ __forceinline__ Vec<T, V> packed(const float (&f)[V]) {
 
 template <typename T, int V, bool INTER, bool LOOSE>
 __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ RopeArgs a) {
-  constexpr int PAIRS = INTER ? V / 2 : V, U = rope_ahead(V, INTER);  // units asked for together
+  constexpr bool TWO = !(INTER && LOOSE);  // pieces of a turned unit
+  constexpr int PAIRS = INTER ? V / 2 : V, U = rope_ahead(V);  // units asked for together
   extern __shared__ __align__(16) float rope_smem[];
   const int half = a.R / 2;
   float *cs = rope_smem, *sn = rope_smem + a.tokens * half;  // [tokens][R / 2]
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
     w.x = static_cast<const T*>(r.x) + (t0 + t) * r.s0 + hh * r.s1 + c0;
     w.y = static_cast<T*>(r.y) + (t0 + t) * r.y0 + hh * r.y1 + c0;
     w.lo = load_piece<T, V, LOOSE>(w.x, a.D - c0);
-    if (!INTER && turn) w.hi = load_piece<T, V, LOOSE>(w.x + half, V);
+    if (turn ? TWO : a.copy > 0) w.hi = load_piece<T, V, LOOSE>(w.x + (turn ? half : a.copy), V);
     u += du;
     const int cu = u >= a.units;
     u -= cu ? a.units : 0;
@@ -154,28 +156,43 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
         const Unit& k = w[j];
         if (k.u >= a.turned) {
           store_piece<T, V, LOOSE>(k.y, k.lo, a.D - (a.R + (k.u - a.turned) * V));
+          if (a.copy > 0) store_piece<T, V, LOOSE>(k.y + a.copy, k.hi, V);
           continue;
         }
+        // PAIRS sines and cosines from pair `at` on
+        auto angles = [&](int at, float (&c)[PAIRS], float (&s)[PAIRS]) {
+          if (PAIRS % 4 == 0 && half % 8 == 0) {
+#pragma unroll
+            for (int e = 0; e < PAIRS; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(cs + at + e), y = *reinterpret_cast<const float4*>(sn + at + e);
+              c[e] = x.x, c[(e + 1) % PAIRS] = x.y, c[(e + 2) % PAIRS] = x.z, c[(e + 3) % PAIRS] = x.w;
+              s[e] = y.x, s[(e + 1) % PAIRS] = y.y, s[(e + 2) % PAIRS] = y.z, s[(e + 3) % PAIRS] = y.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) c[e] = cs[at + e], s[e] = sn[at + e];
+          }
+        };
         float c[PAIRS], s[PAIRS], f[V], g[V];
         const int at = k.t * half + k.u * PAIRS;
-        if (PAIRS % 4 == 0 && half % 4 == 0) {
-#pragma unroll
-          for (int e = 0; e < PAIRS; e += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(cs + at + e), y = *reinterpret_cast<const float4*>(sn + at + e);
-            c[e] = x.x, c[(e + 1) % PAIRS] = x.y, c[(e + 2) % PAIRS] = x.z, c[(e + 3) % PAIRS] = x.w;
-            s[e] = y.x, s[(e + 1) % PAIRS] = y.y, s[(e + 2) % PAIRS] = y.z, s[(e + 3) % PAIRS] = y.w;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < PAIRS; ++e) c[e] = cs[at + e], s[e] = sn[at + e];
-        }
+        angles(at, c, s);
         vunpack<T, V>(k.lo, f);
         if constexpr (INTER) {
+          auto turn = [&](float (&v)[V]) {
 #pragma unroll
-          for (int e = 0; e < PAIRS; ++e) {
-            const float p = f[2 * e], q = f[2 * e + 1];
-            f[2 * e] = p * c[e] - q * s[e];
-            f[2 * e + 1] = q * c[e] + p * s[e];
+            for (int e = 0; e < PAIRS; ++e) {
+              const float p = v[2 * e], q = v[2 * e + 1];
+              v[2 * e] = p * c[e] - q * s[e];
+              v[2 * e + 1] = q * c[e] + p * s[e];
+            }
+          };
+          turn(f);
+          store_piece<T, V, LOOSE>(k.y, packed<T, V>(f), V);
+          if constexpr (TWO) {
+            angles(at + half / 2, c, s);
+            vunpack<T, V>(k.hi, g);
+            turn(g);
+            store_piece<T, V, LOOSE>(k.y + half, packed<T, V>(g), V);
           }
         } else {
           vunpack<T, V>(k.hi, g);
@@ -185,9 +202,9 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
             f[e] = p * c[e] - q * s[e];
             g[e] = q * c[e] + p * s[e];
           }
+          store_piece<T, V, LOOSE>(k.y, packed<T, V>(f), V);
           store_piece<T, V, LOOSE>(k.y + half, packed<T, V>(g), V);
         }
-        store_piece<T, V, LOOSE>(k.y, packed<T, V>(f), V);
       }
     i += U * THREADS;
 #pragma unroll
@@ -196,11 +213,11 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
   }
 }
 
-// The widest pieces that every row allows: up to 16 bytes; 0: pairs side by side on no
-// boundary of a pair.
+// The widest pieces that every row allows: up to 16 bytes; 0: pairs side by side whose halves
+// are no whole pieces of pairs.
 int piece_of(const RopeArgs& a, int elem, bool inter) {
   for (int v = 16 / elem; v > 1; v /= 2) {
-    bool ok = (inter ? a.R : a.R / 2) % v == 0 && (a.D - a.R) % v == 0;
+    bool ok = a.R / 2 % v == 0 && (a.D - a.R) % v == 0;
     for (const RopeRows* r : {&a.q, &a.k}) {
       if (r == &a.k && a.H == a.HQ) continue;
       const uintptr_t p = (uintptr_t)r->x | (uintptr_t)r->y;
@@ -213,8 +230,10 @@ int piece_of(const RopeArgs& a, int elem, bool inter) {
 
 template <typename T, int V, bool INTER, bool LOOSE = false>
 cudaError_t launch(RopeArgs a, cudaStream_t st) {
-  a.turned = (INTER ? a.R : a.R / 2) / V;
-  a.units = a.turned + (a.D - a.R + V - 1) / V;
+  const int rest = a.D - a.R;
+  a.turned = (INTER && LOOSE ? a.R : a.R / 2) / V;
+  a.copy = rest > 0 && rest / 2 % V == 0 && rest % 2 == 0 ? rest / 2 : 0;
+  a.units = a.turned + ((a.copy ? a.copy : rest) + V - 1) / V;
   // Tokens of a block: two rounds of units for its threads, or as many as share the heads'
   // sines where there are few heads; sines up to 32 KB.
   const int64_t per = (int64_t)a.units * a.H;
