@@ -18,10 +18,11 @@ constexpr int lnorm_bwd_min_blocks(int TPR, int elements) {
 }
 
 // Bound by HBM.  A block keeps its columns' weight gradients in registers over all its rows
-// and leaves one partial row of each.
-template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
+// and leaves one partial row of each.  RES: with a residual or dh; without them, rows are
+// asked for twice as far ahead.
+template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>
 __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V * NV)) k_lnorm_bwd(NormArgs a) {
-  using W = RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 4>;
+  using W = RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 4 : 2>;
   constexpr int P = W::P;
   __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
   extern __shared__ __align__(16) unsigned char lnorm_smem[];
@@ -31,9 +32,11 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
   typename W::Weight wk;
   w.keep(wk, a.w);
   w.in.add(0, a.x);
-  if (a.res.p) w.in.add(1, a.res);
-  w.in.add(2, a.dy);
-  if (a.dh.p) w.in.add(3, a.dh);
+  w.in.add(1, a.dy);
+  if constexpr (RES) {
+    if (a.res.p) w.in.add(2, a.res);
+    if (a.dh.p) w.in.add(3, a.dh);
+  }
   uint64_t dw[NV][P], db[NV][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -52,7 +55,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
     else w.ask(0);
     auto on = [&](int i) { return r < a.rows && w.col(i) < a.D; };
     auto dn_of = [&](int i, uint64_t (&f)[P]) {  // dy w
-      w.get(slot, 2, i, f);
+      w.get(slot, 1, i, f);
       if (a.w) {
         uint64_t c[P];
         w.weight(wk, i, c);
@@ -67,8 +70,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
       if (on(i)) {
         uint64_t f[P];
         w.get(slot, 0, i, h[i]);
-        if (a.res.p) {
-          w.get(slot, 1, i, f);
+        if (RES && a.res.p) {
+          w.get(slot, RES ? 2 : 0, i, f);
 #pragma unroll
           for (int q = 0; q < P; ++q) h[i][q] = fma2(alpha, h[i][q], f[q]);
         }
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
     for (int i = 0; i < NV; ++i)
       if (on(i)) {
         uint64_t f[P], y[P];
-        w.get(slot, 2, i, y);
+        w.get(slot, 1, i, y);
         dn_of(i, f);
         const uint64_t mdn = both(-mean_dn);
 #pragma unroll
@@ -116,13 +119,13 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
           db[i][q] = add2(db[i][q], y[q]);
           h[i][q] = fma2(pa, add2(f[q], mdn), mul2(pb, h[i][q]));
         }
-        if (a.dh.p) {
-          w.get(slot, 3, i, f);
+        if (RES && a.dh.p) {
+          w.get(slot, RES ? 3 : 0, i, f);
 #pragma unroll
           for (int q = 0; q < P; ++q) h[i][q] = add2(h[i][q], f[q]);
         }
       }
-    w.put(a.dres, r, h);
+    if (RES) w.put(a.dres, r, h);
     if (a.dx) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -175,11 +178,15 @@ struct Launch {
   cudaStream_t st;
   template <int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
   cudaError_t run() const {
+    return a.res.p || a.dh.p ? go<V, TPR, NV, CLUSTER, SHIFT, true>() : go<V, TPR, NV, CLUSTER, SHIFT, false>();
+  }
+  template <int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>
+  cudaError_t go() const {
     static Held held;
     // (the groups' weight gradients meet in the same bytes: at most V NV columns a thread)
-    const size_t smem = std::max((size_t)RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 4>::BYTES,
+    const size_t smem = std::max((size_t)RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 4 : 2>::BYTES,
                                  TPR <= 32 ? 128 * V * NV * sizeof(float) : (size_t)0);
-    return norm_launch(k_lnorm_bwd<T, V, TPR, NV, CLUSTER, SHIFT>, a, s, smem, norm_bwd_blocks(a.D), held, parts, st);
+    return norm_launch(k_lnorm_bwd<T, V, TPR, NV, CLUSTER, SHIFT, RES>, a, s, smem, norm_bwd_blocks(a.D), held, parts, st);
   }
 };
 

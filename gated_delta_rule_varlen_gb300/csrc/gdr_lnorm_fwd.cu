@@ -4,10 +4,11 @@
 namespace gdr {
 namespace {
 
-// Bound by HBM: each input read and each output written once.
-template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
+// Bound by HBM: each input read and each output written once.  RES: with a residual; without
+// one, rows are asked for twice as far ahead (gdr_norm.cuh).
+template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {
-  using W = RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 2>;
+  using W = RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 2 : 1>;
   constexpr int P = W::P;
   __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
   extern __shared__ __align__(16) unsigned char lnorm_smem[];
@@ -17,7 +18,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {
   w.keep(wk, a.w);
   w.keep(bk, a.w_post);
   w.in.add(0, a.x);
-  if (a.res.p) w.in.add(1, a.res);
+  if constexpr (RES) w.in.add(1, a.res);
   if constexpr (W::AHEAD) {
 #pragma unroll
     for (int i = 0; i < W::DEPTH; ++i) w.ask(i);
@@ -35,7 +36,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {
       zero_pairs<V>(h[i]);
       if (on(i)) {
         w.get(slot, 0, i, h[i]);
-        if (a.res.p) {
+        if constexpr (RES) {
           uint64_t f[P];
           w.get(slot, 1, i, f);
 #pragma unroll
@@ -99,9 +100,13 @@ struct Launch {
   cudaStream_t st;
   template <int V, int TPR, int NV, bool CLUSTER, bool SHIFT>
   cudaError_t run() const {
+    return a.res.p ? go<V, TPR, NV, CLUSTER, SHIFT, true>() : go<V, TPR, NV, CLUSTER, SHIFT, false>();
+  }
+  template <int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>
+  cudaError_t go() const {
     static Held held;
-    return norm_launch(k_lnorm_fwd<T, V, TPR, NV, CLUSTER, SHIFT>, a, s, RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, 2>::BYTES, 32,
-                       held, parts, st);
+    return norm_launch(k_lnorm_fwd<T, V, TPR, NV, CLUSTER, SHIFT, RES>, a, s,
+                       RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 2 : 1>::BYTES, 32, held, parts, st);
   }
 };
 
