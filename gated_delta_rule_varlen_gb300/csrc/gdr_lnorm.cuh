@@ -107,10 +107,21 @@ struct RowWorker {
   }
 };
 
+// The threads of a row: those of the other norms (norm_shape), but that wide rows of 16 bits
+// have two pieces a thread: what a row costs beside its elements, the instructions of two
+// sums, is shared by 16 of them.
+inline NormShape lnorm_shape(const RowLayout& l) {
+  const NormShape s = norm_shape(l);
+  const int n = s.shift ? (l.D + 2 * l.V - 2) / l.V : l.D / l.V;
+  if (s.V == 8 && n > 256)
+    for (int tpr : {256, 384, 512, 768, 1024})
+      if (n <= 2 * tpr) return {8, tpr, 2, 0, s.shift};
+  return s;
+}
+
 // launch.run<V, TPR, NV, CLUSTER, SHIFT>() of a shape.
 template <int VT, typename L>
 cudaError_t dispatch_lnorm(const NormShape& s, L launch) {
-  constexpr int N = 8 / VT;  // vectors of 8 elements
 #define GDR_LNORM_CASE(v, tpr, nv, cl, sh)                                                \
   if (s.V == v && s.TPR == tpr && s.NV == nv && (s.cluster > 0) == cl && s.shift == sh)   \
     return launch.template run<v, tpr, nv, cl, sh>();
@@ -126,14 +137,14 @@ cudaError_t dispatch_lnorm(const NormShape& s, L launch) {
   GDR_LNORM_CASES(64, 2, false)
   GDR_LNORM_CASES(96, 2, false)
   GDR_LNORM_CASES(128, 2, false)
-  if constexpr (VT == 4) {  // (of 16 bits 128 threads with two vectors hold as much)
-    GDR_LNORM_CASES(256, N, false)
+  GDR_LNORM_CASES(256, 2, false)
+  GDR_LNORM_CASES(384, 2, false)
+  GDR_LNORM_CASES(512, 2, false)
+  if constexpr (VT == 4) {
+    GDR_LNORM_CASES(640, 2, false)
   }
-  GDR_LNORM_CASES(384, N, false)
-  GDR_LNORM_CASES(512, N, false)
-  GDR_LNORM_CASES(640, N, false)
-  GDR_LNORM_CASES(768, N, false)
-  GDR_LNORM_CASES(1024, N, false)
+  GDR_LNORM_CASES(768, 2, false)
+  GDR_LNORM_CASES(1024, 2, false)
   GDR_LNORM_CASES(128, 2, true)
   GDR_LNORM_CASE(1, 32, 8, false, false)
   GDR_LNORM_CASE(1, 128, 8, true, false)

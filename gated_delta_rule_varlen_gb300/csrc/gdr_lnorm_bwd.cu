@@ -242,7 +242,7 @@ gdr_status lnorm_fwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x
   for (const RowTensor& t : {a.x, a.res}) l.input(t);
   for (const void* p : {h, y}) l.output(p);
   ProfScope ps("lnorm_fwd", stream, (double)a.rows * D);
-  return launch_lnorm_fwd(a, dtype, norm_shape(l), stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+  return launch_lnorm_fwd(a, dtype, lnorm_shape(l), stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
 }
 
 gdr_status lnorm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
@@ -271,7 +271,7 @@ gdr_status lnorm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x
   int parts = 0;
   if (a.rows > 0) {
     ProfScope ps("lnorm_bwd", stream, (double)a.rows * D);
-    if (launch_lnorm_bwd(a, dtype, norm_shape(l), &parts, stream) != cudaSuccess) return GDR_CUDA_ERROR;
+    if (launch_lnorm_bwd(a, dtype, lnorm_shape(l), &parts, stream) != cudaSuccess) return GDR_CUDA_ERROR;
   }
   if (dweight || dbias) {
     ProfScope ps("lnorm_wgrad", stream);
