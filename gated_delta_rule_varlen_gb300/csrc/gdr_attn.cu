@@ -214,7 +214,7 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   gdr_status rc = attn_check(a, cu_seqlens_host, cu_keys_host);
   if (rc != GDR_OK) return rc;
   if (T == 0) return GDR_OK;
-  if (!out || !lse) return GDR_INVALID_ARG;
+  if (!out || !lse || out == q || out == k || out == v) return GDR_INVALID_ARG;
   const bool tiles = attn_tc_shape(D) && attn_tc_layout(a);
   AttnPlan p{};
   if (tiles) {
@@ -261,6 +261,10 @@ gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   if (rc != GDR_OK) return rc;
   if (T > 0 && (!dout || !out || !lse || !dq)) return GDR_INVALID_ARG;
   if (TK > 0 && (!dk || !dv)) return GDR_INVALID_ARG;
+  for (const void* g : {(const void*)dq, (const void*)dk, (const void*)dv})
+    for (const void* x : {(const void*)q, (const void*)k, (const void*)v, (const void*)out, (const void*)dout})
+      if (g && g == x) return GDR_INVALID_ARG;
+  if ((dq && (dq == dk || dq == dv)) || (dk && dk == dv)) return GDR_INVALID_ARG;
   if (T == 0 && TK == 0) return GDR_OK;
   const int32_t* keys_host = cu_keys_host ? cu_keys_host : cu_seqlens_host;
   AttnPlan p{};

@@ -92,6 +92,7 @@ struct BlockFinder {
     }
     want -= before;
     const int l = __ffs(__ballot_sync(0xffffffffu, want < pre)) - 1;
+    if (l < 0) return AttnBlock{0, 0, 0, 0, 0};  // (no document has it)
     AttnBlock b;
     const int end = __shfl_sync(0xffffffffu, pre, l);  // of the document's blocks
     b.first = (LAST ? end - 1 - want : want - end + __shfl_sync(0xffffffffu, n, l)) * per;

@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   const uint32_t tmem = s.tmem;
 
   if (warp >= WORKERS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (warp == WORKERS) {  // loads
       Ring<KS> kr;
       Ring<VS> vr;
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           commit(&s.v_empty[vr.st]);
           vr.step();
         }
-        commit(&s.q_empty);
+        if (QUEUE) commit(&s.q_empty);
       }
       commit(&s.done);
       wait_some(&s.done, 0);
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       bool ok = true;
       while (ok && next_item(false)) {
         if (w.r.lo >= w.r.hi) continue;
-        if (k > 0) ok = warp_wait(&s.acc_empty, (k - 1) & 1, ab);
+        if (QUEUE && k > 0) ok = warp_wait(&s.acc_empty, (k - 1) & 1, ab);
         ++k;
         for (int j = w.r.lo; j < w.r.hi && ok; ++j, ++g) {
           ok = warp_wait(&s.ds_full, g & 1, ab);
@@ -323,7 +322,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a row a thread, of S and dP a quarter's columns
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -373,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       } else if (w.all.lo == w.all.hi && w.part == 0 && live && quarter == 0) {
         a.delta[h * a.T + at] = 0.f;
       }
-      if (any) {  // (not before this item's tiles are there: the last one's place is free)
+      if (QUEUE && any) {  // (not before this item's tiles are there: the last one's place is free)
         if (one) ok = warp_wait(&s.do_full, k & 1, ab);
         warp_arrive(&s.q_empty);
       }
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       float* share = ba.parts > 1 ? ba.part + w.part * a.T * a.H * a.D + to : nullptr;
 #pragma unroll
       for (int i = 0; i < DB; ++i) store16(a.dq + to, share, DB * 16 * quarter + 16 * i, a.D, lanes + T_DQ, a.scale, any, live);
-      if (any) {
+      if (QUEUE && any) {
         tc::tc_fence_before();
         warp_arrive(&s.acc_empty);
       }
@@ -542,7 +540,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
   const uint32_t tmem = s.tmem;
 
   if (warp >= WORKERS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (warp == WORKERS) {  // loads
       Ring<QS> qr;
       Ring<OS> orr;
@@ -634,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
           const bool more = n + 1 < w.n;
           const Phase pp{&s.p_full, (uint32_t)g & 1}, qp{&s.q_full[qr.st], (uint32_t)qr.ph};
           // (the last item's sums have been read before this one's begin)
-          ok = n == 0 && k > 0 ? warp_wait_all(ab, pp, Phase{&s.acc_empty, (uint32_t)(k - 1) & 1}, more ? qp : pp)
+          ok = QUEUE && n == 0 && k > 0 ? warp_wait_all(ab, pp, Phase{&s.acc_empty, (uint32_t)(k - 1) & 1}, more ? qp : pp)
                                : warp_wait_all(ab, pp, more ? qp : pp);
           if (!ok) break;
           tc::tc_fence_after();
@@ -649,7 +646,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
           commit(&s.q_empty[qst]);
           if (more) grad();
           else commit(&s.acc_full);
-          if (n + 2 == w.n || w.n == 1) commit(&s.kv_empty);  // (S and dP of the last tile are on their way)
+          if (QUEUE && (n + 2 == w.n || w.n == 1)) commit(&s.kv_empty);  // (S and dP of the last tile are on their way)
           qst = q2;
         }
         ++k;
@@ -693,7 +690,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // a key a thread, of S^T and dP^T a quarter's queries
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -775,7 +771,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
         store16(a.dk + to, dk, DB * 16 * quarter + 16 * i, a.D, lanes + T_DK, a.scale, any, key < b.lk);
         store16(a.dv + to, dv, DB * 16 * quarter + 16 * i, a.D, lanes + T_DV, 1.f, any, key < b.lk);
       }
-      if (any) {
+      if (QUEUE && any) {
         tc::tc_fence_before();
         warp_arrive(&s.acc_empty);
       }

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           for (int t = 0; t < 2; ++t)
             if (w.works(t, j)) score(t, stage(kp));
           commit(&s.empty[stage(kp)]);
-          if (j == j1 - 1) commit(&s.q_empty);
+          if (QUEUE && j == j1 - 1) commit(&s.q_empty);
         }
         bool first[2] = {true, true};
         for (int j = j0; j < j1 && ok; ++j) {
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           for (int t = 0; t < 2 && ok; ++t) {
             const bool here = w.works(t, j);
             const Phase pp{here ? &s.p_full[t] : vp.bar, here ? (uint32_t)used[t] & 1 : vp.parity};
-            if (here && first[t] && outs[t] > 0) ok = warp_wait(&s.o_empty[t], (outs[t] - 1) & 1, ab);
+            if (QUEUE && here && first[t] && outs[t] > 0) ok = warp_wait(&s.o_empty[t], (outs[t] - 1) & 1, ab);
             if (!ok) break;
             if (!loaded) {
               ok = more ? warp_wait_all(ab, vp, kp, pp) : warp_wait_all(ab, vp, pp);
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           if (!ok) break;
           commit(&s.empty[stage(vp)]);
           if (more) commit(&s.empty[stage(kp)]);
-          if (j + w.step == j1 - 1) commit(&s.q_empty);  // (the last scores)
+          if (QUEUE && j + w.step == j1 - 1) commit(&s.q_empty);  // (the last scores)
         }
       }
       commit(&s.done);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           }
         }
         tc::tc_fence_before();
-        warp_arrive(&s.o_empty[1]);
+        if (QUEUE) warp_arrive(&s.o_empty[1]);
         warp_arrive(&s.merged);
         continue;
       }
@@ -455,11 +455,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
           if (live && i + k < a.D) *reinterpret_cast<uint4*>(out + i + k) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
-      if (any) {
+      if (QUEUE && any) {
         tc::tc_fence_before();
         warp_arrive(&s.o_empty[t]);
       }
-      if (dual) {
+      if (QUEUE && dual) {
         tc::fence_proxy_async();  // (Q comes by asynchronous copies again)
         warp_arrive(&s.swapped);
       }

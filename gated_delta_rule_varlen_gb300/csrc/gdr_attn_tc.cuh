@@ -120,7 +120,9 @@ struct WorkQueue {
 // Whether TMA addresses the tensors.
 inline bool attn_tc_layout(const AttnArgs& a) {
   for (const AttnRows* t : {&a.q, &a.k, &a.v, &a.dout})
-    if (t->p && (((uintptr_t)t->p & 15) != 0 || t->s0 <= 0 || t->s1 <= 0 || t->s0 % 8 != 0 || t->s1 % 8 != 0)) return false;
+    if (t->p && (((uintptr_t)t->p & 15) != 0 || t->s0 <= 0 || t->s1 <= 0 || t->s0 % 8 != 0 || t->s1 % 8 != 0 ||
+                 std::max(t->s0, t->s1) >= (int64_t)1 << 39))
+      return false;
   for (const void* p : {(const void*)a.out, (const void*)a.o, (const void*)a.dq, (const void*)a.dk, (const void*)a.dv})
     if (((uintptr_t)p & 15) != 0) return false;
   return true;

@@ -82,13 +82,13 @@ def test_rope_frequencies(gdr):
 def test_attention_refusals(gdr):
     lib, bad, (k, c), (k2, c2) = gdr.load(), gdr.GDR_INVALID_ARG, cu(0, 5, 11), cu(0, 40, 100)
 
-    def fwd(q=P(), kk=P(), v=P(), d=P(9), host=c, dk=None, hk=None, N=2, T=11, TK=11, H=4, HK=2, D=64, scale=1.0, causal=1, window=0, out=P(),
-            lse=P(), scratch=None, nbytes=0):
+    def fwd(q=P(), kk=P(), v=P(), d=P(9), host=c, dk=None, hk=None, N=2, T=11, TK=11, H=4, HK=2, D=64, scale=1.0, causal=1, window=0, out=P(2),
+            lse=P(3), scratch=None, nbytes=0):
         return lib.attn_fwd(q, H * 64, 64, kk, HK * 64, 64, v, HK * 64, 64, d, host, dk, hk, N, T, TK, H, HK, D, scale, causal, window,
                             out, lse, scratch, nbytes, None)
     for call in (dict(q=None), dict(kk=None), dict(v=None), dict(d=None), dict(out=None), dict(lse=None), dict(H=3), dict(HK=0), dict(H=0),
                  dict(D=0), dict(D=257), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
-                 dict(causal=0, window=3), dict(TK=12), dict(dk=P()), dict(hk=c2, TK=100), dict(N=-1), dict(host=None)):
+                 dict(causal=0, window=3), dict(out=P()), dict(TK=12), dict(dk=P()), dict(hk=c2, TK=100), dict(N=-1), dict(host=None)):
         assert fwd(**call) == bad, call
     assert fwd(T=12, TK=12) == gdr.GDR_BAD_CU_SEQLENS and fwd(dk=P(), hk=c2, TK=99) == gdr.GDR_BAD_CU_SEQLENS
     kd, cd = cu(0, 7, 5, 11)
@@ -102,11 +102,11 @@ def test_attention_refusals(gdr):
     assert fwd(**long) == bad and fwd(scratch=P() + 8, nbytes=1 << 30, **long) == bad
     assert fwd(scratch=P(), nbytes=256, **long) == gdr.GDR_WORKSPACE_TOO_SMALL
 
-    def bwd(out=P(), lse=P(), dout=P(), dq=P(), dk=P(), dv=P(), scratch=P(), nbytes=1 << 30):
+    def bwd(out=P(2), lse=P(3), dout=P(4), dq=P(5), dk=P(6), dv=P(7), scratch=P(), nbytes=1 << 30):
         return lib.attn_bwd(P(), 256, 64, P(), 128, 64, P(), 128, 64, out, lse, dout, 256, 64, P(9), c, None, None, 2, 11, 11, 4, 2, 64, 1.0, 1,
                             0, dq, dk, dv, scratch, nbytes, None)
     for call in (dict(out=None), dict(lse=None), dict(dout=None), dict(dq=None), dict(dk=None), dict(dv=None), dict(scratch=None),
-                 dict(scratch=P() + 16)):
+                 dict(scratch=P() + 16), dict(dq=P()), dict(dq=P(4)), dict(dk=P(2)), dict(dv=P(6)), dict(dq=P(7))):
         assert bwd(**call) == bad, call
     assert bwd(nbytes=16) == gdr.GDR_WORKSPACE_TOO_SMALL
     kt, ct = cu(0, 2**31 - 1)

@@ -405,7 +405,8 @@ def test_attention_refusals(gdr):
                 lambda: gdr.attn_fwd(q.cpu(), k, v, cu, cuh), lambda: gdr.attn_fwd(q.transpose(1, 2), k, v, cu, cuh),
                 lambda: gdr.attn_bwd(q, k, v, out, lse.t(), dout, cu, cuh), lambda: gdr.attn_bwd(q, k, v, out, lse, dout[:9], cu, cuh),
                 lambda: gdr.attn_bwd(q, k, v, out[:, :2], lse, dout, cu, cuh), lambda: gdr.attn_fwd(q, k, v, cu, cuh, out=out[:5]),
-                lambda: gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, grads={"dk": q})):
+                lambda: gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, grads={"dk": q}), lambda: gdr.attn_fwd(q, k, v, cu, cuh, out=q),
+                lambda: gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, grads={"dq": dout}), lambda: gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, grads={"dk": v})):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises((ValueError, RuntimeError)):
@@ -498,6 +499,38 @@ MANY = [
 @pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", MANY)
 def test_attention_of_many_and_of_long_documents(gdr, lq, lk, H, HK, D, causal, window):
     test_attention_forward_and_gradients(gdr, lq, lk, H, HK, D, causal, window, "dense")
+
+
+@pytest.mark.parametrize("D", [128, 64, 20])
+def test_attention_without_queries_or_keys(gdr, D):
+    g = gen(D)
+    (cu, cuh), (none, noneh) = pack([130, 1]), pack([0, 0])
+    x, e = randn(g, 131, 4, D, dtype=BF16), torch.empty(0, 2, D, dtype=BF16, device="cuda")
+    out, lse = gdr.attn_fwd(x, e, e, cu, cuh, cu_keys=none, cu_keys_host=noneh)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    got = gdr.attn_bwd(x, e, e, out, lse, x, cu, cuh, cu_keys=none, cu_keys_host=noneh)
+    assert (got["dq"] == 0).all() and got["dk"].shape == e.shape
+    k, eq = x[:, :2].contiguous(), torch.empty(0, 4, D, dtype=BF16, device="cuda")
+    out, lse = gdr.attn_fwd(eq, k, k, none, noneh, cu_keys=cu, cu_keys_host=cuh)
+    got = gdr.attn_bwd(eq, k, k, out, lse, eq, none, noneh, cu_keys=cu, cu_keys_host=cuh)
+    assert out.shape == eq.shape and (got["dk"] == 0).all() and (got["dv"] == 0).all()
+
+
+@pytest.mark.parametrize("H,HK", [(128, 1), (256, 2), (48, 3), (7, 7)])
+def test_attention_of_many_heads_a_key_head(gdr, H, HK):
+    # one token of each document: up to 128 heads side by side in a tile
+    g, keys, D = gen(H), [5, 400, 131], 64
+    q, k, v = randn(g, 3, H, D, dtype=BF16), *(randn(g, sum(keys), HK, D, dtype=BF16) for _ in range(2))
+    dout = randn(g, 3, H, D, dtype=BF16)
+    (cu, cuh), (cuk, cukh) = pack([1, 1, 1]), pack(keys)
+    leaves = [t.double().requires_grad_() for t in (q, k, v)]
+    ro, rl = ref.attention(*leaves, [1, 1, 1], keys, D ** -0.5, True, 0)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+    compare(out, ro.detach(), TOL_OUT, "out")
+    compare(lse, rl.detach(), TOL_LSE, "lse")
+    got = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+    for n, r in zip(("dq", "dk", "dv"), torch.autograd.grad((ro * dout.double()).sum(), leaves)):
+        compare(got[n], r, TOL_GRAD, n)
 
 
 def test_attention_reads_nothing_of_its_scratch_before_writing_it(gdr):
