@@ -8,12 +8,21 @@
 //
 // Scores and probabilities are formed in both (seven products instead of five, but no sums
 // across blocks).  P and dS are the A operands of their products, read from tensor memory in
-// BF16 (2^-9 of each term at most, independently); accumulators, P and dS before that are
-// FP32.
+// BF16 (2^-8 of each term at most, independently: where the keys share a large part, which
+// cancels in dQ since a row of dS sums to zero, that part times the roundings stays);
+// accumulators, P and dS before that are FP32.
 //
 // delta = dout . out of the rounded out, but for queries whose keys fit one tile: with few
-// keys |out| is like |v|, and 2^-9 of it shows beside the differences dP - delta; there
+// keys |out| is like |v|, and 2^-8 of it shows beside the differences dP - delta; there
 // delta is sum p dP, which the tile holds.
+//
+// Bound by the products and their operands' way from shared memory: of 8192 tokens of 16
+// heads over 4 of 128 columns dQ takes 276 us (three products, 1.5 PFLOP/s), dK and dV 350
+// (four, 1.6 PFLOP/s; cuBLAS's measured rate is 1.9).  Measured and not kept: tiles three
+// deep in dQ and two in dK and dV, so that elements and products of different tiles overlap
+// (345 and 423 us: the elements' tensor memory traffic slows the products), the products of
+// dK and dV from two warps (408), eight warps on the elements (323 and 417), every warp
+// finding its items for itself (300 and 375).
 //
 // Rows past a document's end belong to another one: they are cleared where they are summed
 // over (K for dQ, Q and dO for dK and dV).

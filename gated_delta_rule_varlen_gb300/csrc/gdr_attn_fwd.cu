@@ -11,7 +11,15 @@
 // two): until then probabilities are up to 2^8 times what they are in the end, which FP32
 // sums and BF16's exponent hold as well, and out needs no rescaling.  Sums of probabilities
 // are of the unrounded ones in FP32.  P is rounded to BF16 (v's type, which the product
-// needs): 2^-9 of each term at most, independently.
+// needs): 2^-8 of each term at most, independently.
+//
+// Bound by the products' operand reads from shared memory (S takes both operands from there,
+// 128 bytes a clock) and by what its one issuing warp waits: a step of a block's two tiles
+// takes some 2700 clocks, its products 2048; one prompt of 32768 tokens of 16 heads over 4
+// of 128 columns 2.9 ms, 1540 TFLOP/s (81% of cuBLAS's measured rate).  The exponentials
+// cost nothing beside that (without them the same time).  Measured and not kept: products
+// from a warp a tile (3.2 ms: the two streams of products slow each other), P handed over
+// in halves (3.15).
 //
 // Rows of V past a document's keys are cleared, since they hold another document's values (a
 // NaN there would pass through a zero probability).

@@ -17,7 +17,9 @@ constexpr int lnorm_bwd_min_blocks(int TPR, int elements) {
   return elements <= 8 ? 5 : 3;
 }
 
-// Bound by HBM.  A block keeps its columns' weight gradients in registers over all its rows
+// Bound by HBM.  Fractions of the copy rate for 2^27 elements of BF16, with residual and dh /
+// without: 128 columns 0.89 / 0.84, 2048 0.93 / 0.61, 4096 0.93 / 0.58, 8192 0.81 / 0.48, 16384
+// 0.48 / 0.31, 1021 0.39 / 0.27; FP32 2048 0.89 / 0.80.  A block keeps its columns' weight gradients in registers over all its rows
 // and leaves one partial row of each.  RES: with a residual or dh; without them, rows are
 // asked for twice as far ahead.
 template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>

@@ -4,7 +4,10 @@
 namespace gdr {
 namespace {
 
-// Bound by HBM: each input read and each output written once.  RES: with a residual; without
+// Bound by HBM: each input read and each output written once.  Fractions of the copy rate for
+// 2^27 elements of BF16, with / without a residual: 128 columns 0.84 / 0.80, 2048 0.80 / 0.80,
+// 4096 0.92 / 0.73, 8192 0.84 / 0.51, 16384 0.72 / 0.45 (the two sums of a row, one after the
+// other), 1021 0.47 / 0.33 (rows shifted to 16-byte pieces); FP32 2048 0.83 / 0.85.  RES: with a residual; without
 // one, rows are asked for twice as far ahead (gdr_norm.cuh).
 template <typename T, int V, int TPR, int NV, bool CLUSTER, bool SHIFT, bool RES>
 __global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {

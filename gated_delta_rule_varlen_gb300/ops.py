@@ -294,7 +294,9 @@ def attn_fwd(q, k, v, cu_seqlens, cu_seqlens_host, scale=None, causal=True, wind
     place, of those the last `window` (0: all).  Returns (out bf16 [T, H, D], lse fp32 [H, T]);
     a query that sees no key gets 0 and -inf.
 
-    D goes up to 256."""
+    D goes up to 256.  The tensor cores take D up to 128 in multiples of 8, tensors on 16-byte
+    boundaries and strides in multiples of 8; others go one query a warp, some 400 times
+    slower on a long prompt."""
     args = (q, k, v, cu_seqlens, _host(cu_seqlens_host), cu_keys, None if cu_keys_host is None else _host(cu_keys_host), scale,
             causal, window, out, lse, scratch)
     if stream is not None:

@@ -541,8 +541,12 @@ gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, i
  * A query that sees no key has out 0 and lse -inf, and takes part in no gradient.
  * q, dout [T][H][D], k, v [TK][HK][D] BF16, their tokens and heads *s0 and *s1
  * elements apart; head h reads key head h / (H / HK).  out [T][H][D] BF16 and lse
- * [H][T] FP32 are dense.  scale > 0; 1 <= D <= GDR_ATTN_MAX_D.  Scores, maxima,
- * sums and outputs are FP32 until the one rounding.
+ * [H][T] FP32 are dense and none of the inputs.  scale > 0; 1 <= D <= GDR_ATTN_MAX_D.
+ * D of at most 128 in multiples of 8, with tensors on 16-byte boundaries and strides
+ * in multiples of 8, runs on the tensor cores, any other one query a warp, some 400
+ * times slower on a long prompt.  Scores, maxima, sums and outputs are FP32 until the
+ * one rounding; the tensor cores take probabilities in BF16 (2^-8 of each term at
+ * most, independently).
  * Values of a document that are not finite reach its own outputs only.
  * scratch: attn_workspace_bytes, on a 256-byte boundary (null when 0). */
 #define GDR_ATTN_MAX_D 256
@@ -557,7 +561,9 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
 
 /* Gradients of attn_fwd from dout, the forward's out and lse; the probabilities
  * are formed again.  Writes dq [T][H][D], dk, dv [TK][HK][D] BF16, dense, dk and dv
- * summed in FP32 over the query heads of a key head.  Deterministic. */
+ * summed in FP32 over the query heads of a key head; none of them is an input.
+ * Deterministic.  On the tensor cores dS is rounded to BF16 as the probabilities
+ * are. */
 gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16* k, int64_t ks0, int64_t ks1,
                     const gdr_bf16* v, int64_t vs0, int64_t vs1, const gdr_bf16* out, const float* lse,
                     const gdr_bf16* dout, int64_t ds0, int64_t ds1, const int32_t* cu_seqlens,
