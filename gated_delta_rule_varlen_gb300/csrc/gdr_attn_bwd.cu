@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     tc::tmem_relinquish();
   }
   const int heads = 1 << ba.pack, tokens = TILE >> ba.pack;
+  previous_ended();
+  if constexpr (!QUEUE) next_may_start();  // (all that came before this kernel has ended)
   DqWork w;
   if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
     BlockFinder<true> finder(a, tokens);
@@ -663,6 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
       commit(&s.done);
       wait_some(&s.done, 0);
     } else if (warp == WORKERS + 2) {  // lse and delta of a tile's queries
+      previous_ended();  // (delta comes from k_attn_dq, beside whose last blocks this kernel begins)
       int g = 0;
       bool ok = true;
       while (ok && next_item(false)) {
@@ -810,8 +813,7 @@ template <typename K>
 cudaError_t go(K kernel, size_t smem, int64_t blocks, const BwdArgs& f, cudaStream_t st) {
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-  kernel<<<(unsigned)blocks, THREADS, smem, st>>>(f);
-  return cudaGetLastError();
+  return launch_early(kernel, dim3((unsigned)blocks), THREADS, smem, st, f);
 }
 template <typename S>
 constexpr size_t bytes_of() {

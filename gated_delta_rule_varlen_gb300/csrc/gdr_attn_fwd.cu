@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
     tc::tmem_relinquish();
   }
   const int heads = 1 << fa.pack, tokens = TILE >> fa.pack;  // of a tile
+  previous_ended();
+  if constexpr (!QUEUE) next_may_start();
   FwdWork w;
   if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
     BlockFinder<true> finder(a, 2 * tokens);
@@ -536,8 +538,7 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
   if (blocks > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
   auto go = [&](auto kernel, size_t smem) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    kernel<<<(unsigned)blocks, THREADS, smem, st>>>(f);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3((unsigned)blocks), THREADS, smem, st, f);
   };
   static_assert(sizeof(FwdSmem<1>) <= 232448 && sizeof(FwdSmem<2>) <= 232448, "227 KB of shared memory a block");
   // Blocks that take over others' items gain on short ones of up to 64 columns, whose start and end
