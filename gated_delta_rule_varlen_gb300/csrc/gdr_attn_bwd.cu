@@ -180,6 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   const AttnArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
+  if (warp == 1 && lane == 0)
+    for (const CUtensorMap* map : {&ba.q_map, &ba.do_map, &ba.k_map, &ba.v_map}) prefetch_map(map);
   if (warp == 0) {
     if (lane == 0) {
       for (uint64_t* bar : {&s.q_full, &s.do_full, &s.cleared, &s.s_full[0], &s.s_full[1], &s.dp_full, &s.dq_done[0], &s.dq_done[1],
@@ -512,6 +514,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
   const AttnArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
+  if (warp == 1 && lane == 0)
+    for (const CUtensorMap* map : {&ba.q_map, &ba.do_map, &ba.k_map, &ba.v_map}) prefetch_map(map);
   if (warp == 0) {
     if (lane == 0) {
       for (uint64_t* bar : {&s.kv_full, &s.kv_empty, &s.q_cleared, &s.o_cleared, &s.s_full, &s.dp_full, &s.row_full[0], &s.row_full[1],

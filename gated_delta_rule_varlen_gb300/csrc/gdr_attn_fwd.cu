@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
   const AttnArgs& a = fa.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* ab = &s.abort;
+  if (warp == 1 && lane == 0)
+    for (const CUtensorMap* map : {&fa.q_map, &fa.k_map, &fa.v_map}) prefetch_map(map);
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {

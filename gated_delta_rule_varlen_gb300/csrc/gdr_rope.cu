@@ -236,12 +236,13 @@ cudaError_t launch(RopeArgs a, cudaStream_t st) {
   a.turned = (INTER && LOOSE ? a.R : a.R / 2) / V;
   a.copy = rest > 0 && rest / 2 % V == 0 && rest % 2 == 0 ? rest / 2 : 0;
   a.units = a.turned + ((a.copy ? a.copy : rest) + V - 1) / V;
-  // Tokens of a block: two rounds of units for its threads, or as many as share the heads'
-  // sines where there are few heads; sines up to 32 KB.
+  // Tokens of a block: eight units a thread, which share the sines; sines up to 32 KB; fewer
+  // where that leaves SMs without blocks (957 tokens of 8 heads of 64: 12.4 us with 15 blocks).
   const int64_t per = (int64_t)a.units * a.H;
   int64_t n = std::max<int64_t>(1, 8 * THREADS / per);
   if (a.R > 0) n = std::min<int64_t>(n, std::max(1, 4096 / (a.R / 2)));
-  a.tokens = (int)std::min(n, a.T);
+  n = std::min<int64_t>(n, (a.T + 4 * sm_count() - 1) / (4 * sm_count()));
+  a.tokens = (int)n;
   const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
   k_rope<T, V, INTER, LOOSE><<<(unsigned)blocks, THREADS, (size_t)a.tokens * a.R * sizeof(float), st>>>(a);
   return cudaGetLastError();

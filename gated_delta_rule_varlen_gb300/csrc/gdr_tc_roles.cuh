@@ -88,6 +88,10 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_u32(bar))
       : "memory");
 }
+// Asks for a tensor map, which the first copy would wait for.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // One arrival for the warp, after all its lanes' work.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
