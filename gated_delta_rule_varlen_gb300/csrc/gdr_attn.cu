@@ -218,14 +218,16 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
   if (!out || !lse || out == q || out == k || out == v) return GDR_INVALID_ARG;
   const bool tiles = attn_tc_shape(D) && attn_tc_layout(a);
   AttnPlan p{};
+  const int32_t* keys_host = cu_keys_host ? cu_keys_host : cu_seqlens_host;
   if (tiles) {
-    p = attn_plan(a, cu_seqlens_host, cu_keys_host ? cu_keys_host : cu_seqlens_host);
+    p = attn_plan(a, cu_seqlens_host, keys_host);
     if (p.fwd_bytes > 0 && (!scratch || ((uintptr_t)scratch & 255) != 0)) return GDR_INVALID_ARG;
     if (scratch_bytes < p.fwd_bytes) return GDR_WORKSPACE_TOO_SMALL;
   }
   if ((rc = check_device()) != GDR_OK) return rc;
   if (tiles)
-    return launch_attn_fwd(a, p, cu_seqlens_host, static_cast<float*>(scratch), stream) == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;
+    return launch_attn_fwd(a, p, cu_seqlens_host, keys_host, static_cast<float*>(scratch), stream) == cudaSuccess ? GDR_OK
+                                                                                                                 : GDR_CUDA_ERROR;
   ProfScope ps("attn_rows", stream, (double)T * H);
   k_attn_rows<<<blocks_of(T * H), WARPS * 32, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_CUDA_ERROR;

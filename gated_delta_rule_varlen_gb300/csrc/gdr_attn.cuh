@@ -22,6 +22,7 @@ struct AttnRows {
   __device__ __forceinline__ const __nv_bfloat16* row(int64_t t, int h) const { return p + t * s0 + h * s1; }
 };
 
+constexpr int ATTN_ORDERED = 256;
 struct AttnArgs {
   AttnRows q, k, v, dout;
   const int *cu, *cuk;       // documents' queries and keys
@@ -35,6 +36,10 @@ struct AttnArgs {
   const float* lse_in;
   float* delta;              // [H][T]
   __nv_bfloat16 *dq, *dk, *dv;
+  // The documents, those with the most keys first (their blocks are the longest), where there
+  // are few enough of them.
+  int ordered;
+  uint8_t order[ATTN_ORDERED];
 };
 
 // The keys [lo, hi) that a query sees.
@@ -66,16 +71,19 @@ struct BlockFinder {
 
   __device__ __forceinline__ BlockFinder(const AttnArgs& args, int per_) : a(args), per(per_) { load(0); }
   __device__ __forceinline__ void load(int first) {
-    const int lane = threadIdx.x & 31, d = first + lane;
+    const int lane = threadIdx.x & 31;
+    int d = first + lane;
     d0 = first;
     q0 = lq = k0 = lk = 0;
-    if (d < a.N) {
+    const bool is = d < a.N;
+    if (is) {
+      if (a.ordered) d = a.order[d];
       q0 = a.cu[d];
       lq = a.cu[d + 1] - q0;
       k0 = a.cuk[d];
       lk = a.cuk[d + 1] - k0;
     }
-    n = d < a.N ? ((LAST ? lq : lk) + per - 1) / per : 0;
+    n = is ? ((LAST ? lq : lk) + per - 1) / per : 0;
     pre = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -114,7 +122,8 @@ struct AttnPlan {
 bool attn_tc_shape(int D);
 AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk);  // cu, cuk: the host's
 
-cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, float* scratch, cudaStream_t st);
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, const int32_t* cuk, float* scratch,
+                            cudaStream_t st);
 cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, const int32_t* cuk, float* scratch,
                             cudaStream_t st);
 

@@ -846,6 +846,7 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
     return cudaErrorInvalidValue;
   if (a.TK > 0 && (!attn_map(&f.k_map, a.k, a.TK, a.HK, a.D, 1, TILE) || !attn_map(&f.v_map, a.v, a.TK, a.HK, a.D, 1, TILE)))
     return cudaErrorInvalidValue;
+  if (std::max(qblocks * (a.H >> f.pack) * p.dq, kblocks * a.HK * p.dkv) > sm_count()) attn_order(f.a, cuk);
   auto sum = [&](int64_t n, __nv_bfloat16* x, __nv_bfloat16* y) {  // (n is a multiple of 8, as D is)
     const int64_t blocks = (n / 8 + 255) / 256;
     if (f.parts == 1) return cudaSuccess;

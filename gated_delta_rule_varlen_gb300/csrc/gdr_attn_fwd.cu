@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ FwdAr
 
 }  // namespace
 
-cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, float* scratch, cudaStream_t st) {
+cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t* cu, const int32_t* cuk, float* scratch,
+                            cudaStream_t st) {
   FwdArgs f{};
   f.a = a;
   f.err = device_error_ptr();
@@ -538,6 +539,7 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
   blocks *= (a.H >> f.pack) * f.parts;
   const int64_t rows = (a.T * a.H + 7) / 8;
   if (blocks > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
+  if (blocks > sm_count()) attn_order(f.a, cuk);
   auto go = [&](auto kernel, size_t smem) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
     return launch_early(kernel, dim3((unsigned)blocks), THREADS, smem, st, f);

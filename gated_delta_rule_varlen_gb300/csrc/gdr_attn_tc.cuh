@@ -128,6 +128,15 @@ inline bool attn_tc_layout(const AttnArgs& a) {
   return true;
 }
 
+// Orders the documents for blocks that do not all run at a time.
+inline void attn_order(AttnArgs& a, const int32_t* cuk) {
+  a.ordered = a.N > 1 && a.N <= ATTN_ORDERED;
+  if (!a.ordered) return;
+  for (int i = 0; i < a.N; ++i) a.order[i] = (uint8_t)i;
+  auto keys = [&](int i) { return cuk[i + 1] - cuk[i]; };
+  std::sort(a.order, a.order + a.N, [&](int x, int y) { return keys(x) != keys(y) ? keys(x) > keys(y) : x < y; });
+}
+
 // [T][heads][D] BF16: boxes of 64 elements x `heads` heads x `tokens` tokens, 128-byte
 // swizzle, zero fill outside.
 inline bool attn_map(CUtensorMap* map, const AttnRows& t, int64_t T, int H, int D, int heads, int tokens) {
