@@ -495,8 +495,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ FwdAr
   if (row >= a.T * a.H) return;
   const int64_t t = row / a.H, at = row % a.H * a.T + t, stride = a.T * a.H;
   float top = -INFINITY;
-  for (int p = 0; p < fa.parts; ++p) top = fmaxf(top, fa.part_lse[p * stride + at]);
-  const bool none = top == -INFINITY;
+  bool none = true;  // (a part of nothing but NaN has seen keys)
+  for (int p = 0; p < fa.parts; ++p) {
+    const float l = fa.part_lse[p * stride + at];
+    top = fmaxf(top, l);
+    none = none && l == -INFINITY;
+  }
   float sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p = 0; p < fa.parts && !none; ++p) {

@@ -373,6 +373,21 @@ def test_attention_keeps_documents_apart(gdr, bad):
             assert torch.equal(grads[n][rows], cleang[n][rows]), n
 
 
+def test_attention_of_scores_that_are_not_numbers(gdr):
+    # a query of NaN sees keys: its row is NaN, in one part or several, and nobody else's
+    g, D = gen(31), 64
+    for lens, keys in (([5], [90]), ([3], [5000]), ([700], [700])):
+        T, TK = sum(lens), sum(keys)
+        q, k, v = heads(g, T, 2, 1, D, "dense", TK)[:1] + heads(g, TK, 2, 1, D, "dense", TK)[1:]
+        (cu, cuh), (cuk, cukh) = pack(lens), pack(keys)
+        clean, cl = gdr.attn_fwd(q, k, v, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+        q[1] = NAN
+        out, lse = gdr.attn_fwd(q, k, v, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+        assert out[1].isnan().all() and lse[:, 1].isnan().all()
+        rest = [i for i in range(T) if i != 1]
+        assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[:, rest], cl[:, rest])
+
+
 def test_attention_over_a_long_cache(gdr):
     # keys 2^20 elements apart: their offsets pass 32 bits
     g, n, D = gen(6), 4200, 128
