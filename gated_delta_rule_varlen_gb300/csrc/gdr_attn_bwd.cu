@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dkv(const __grid_constant__
         if (!ok) break;
         tc::tc_fence_after();
       }
+      previous_ended();  // (nothing is written before; where there are queries delta has waited for it already)
       const int64_t to = ((int64_t)(b.k0 + key) * a.HK + w.hk) * a.D, all = a.TK * a.HK * a.D;
       float *dk = nullptr, *dv = nullptr;
       if (ba.parts > 1) {

@@ -507,6 +507,8 @@ MANY = [
     ([200, 0, 1, 65] * 40, None, 4, 2, 128, True, 0), ([300] * 50, None, 8, 8, 64, True, 100), ([128] * 200, None, 2, 1, 64, False, 0),
     ([2100], None, 1, 1, 128, True, 0), ([1500], None, 8, 1, 64, True, 0), ([3000], None, 2, 2, 64, True, 700),
     ([129, 1], [2500, 300], 1, 1, 128, True, 0), ([3] * 40, [700 + 13 * i for i in range(40)], 8, 2, 128, True, 0),
+    ([1] * 200, [1 + (37 * i) % 700 for i in range(200)], 8, 2, 64, True, 0), ([2] * 90, [300 + i for i in range(90)], 3, 3, 64, True, 100),
+    ([1] * 300, [150] * 300, 2, 1, 32, False, 0),
     ([100, 30], [1800, 2300], 4, 4, 80, True, 0), ([1] * 3, [6000, 257, 384], 16, 16, 64, True, 300), ([40], [3000], 6, 3, 128, False, 0),
 ]
 
