@@ -28,8 +28,9 @@ __global__ void __launch_bounds__(norm_threads(TPR), lnorm_bwd_min_blocks(TPR, V
   constexpr int P = W::P;
   __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
   extern __shared__ __align__(16) unsigned char lnorm_smem[];
-  next_may_start();  // (the sum of the partial rows)
   W w(a, lnorm_smem);
+  previous_ended();
+  next_may_start();  // (the sum of the partial rows)
   const float inv_d = 1.f / (float)a.D;
   typename W::Weight wk;
   w.keep(wk, a.w);
@@ -188,7 +189,7 @@ struct Launch {
     // (the groups' weight gradients meet in the same bytes: at most V NV columns a thread)
     const size_t smem = std::max((size_t)RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 4 : 2>::BYTES,
                                  TPR <= 32 ? 128 * V * NV * sizeof(float) : (size_t)0);
-    return norm_launch(k_lnorm_bwd<T, V, TPR, NV, CLUSTER, SHIFT, RES>, a, s, smem, norm_bwd_blocks(a.D), held, parts, st);
+    return norm_launch(k_lnorm_bwd<T, V, TPR, NV, CLUSTER, SHIFT, RES>, a, s, smem, norm_bwd_blocks(a.D), held, parts, st, true);
   }
 };
 

@@ -16,6 +16,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) k_lnorm_fwd(NormArgs a) {
   __shared__ float2 sm[2][RowGroup<TPR, CLUSTER>::SUMS];
   extern __shared__ __align__(16) unsigned char lnorm_smem[];
   W w(a, lnorm_smem);
+  previous_ended();
   const float inv_d = 1.f / (float)a.D;
   typename W::Weight wk, bk;
   w.keep(wk, a.w);
@@ -109,7 +110,7 @@ struct Launch {
   cudaError_t go() const {
     static Held held;
     return norm_launch(k_lnorm_fwd<T, V, TPR, NV, CLUSTER, SHIFT, RES>, a, s,
-                       RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 2 : 1>::BYTES, 32, held, parts, st);
+                       RowWorker<T, V, TPR, NV, CLUSTER, SHIFT, RES ? 2 : 1>::BYTES, 32, held, parts, st, true);
   }
 };
 

@@ -89,21 +89,27 @@ struct Held {
 // the rows) as the GPU holds at a time, `limit` blocks an SM at most, or fewer where
 // there are fewer rows; a shifted row keeps its place within 16 bytes from one of a
 // thread's rows to the next (the step between them is a multiple of V).  held: the
-// kernel's own; smem is always the same for a kernel.
+// kernel's own; smem is always the same for a kernel.  early: the kernel begins with
+// previous_ended(), and its blocks beside the last ones of the kernel before.
 template <typename K>
 cudaError_t norm_launch(K kernel, const NormArgs& a, const NormShape& s, size_t smem, int limit, Held& held, int* parts,
-                        cudaStream_t st) {
+                        cudaStream_t st, bool early = false) {
   const int threads = norm_threads(s.TPR), groups = threads / s.TPR, size = s.cluster > 0 ? s.cluster : 1;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  if (s.cluster > 0) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  } else {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
-  cfg.numAttrs = s.cluster > 0 ? 1 : 0;
+  cfg.numAttrs = s.cluster > 0 || early ? 1 : 0;
   // (a device's own setting, so not kept from call to call)
   if (smem > 40 << 10) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;

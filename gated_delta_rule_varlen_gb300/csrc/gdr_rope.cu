@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
   };
   Unit w[U];
   int i = threadIdx.x;
+  previous_ended();
 #pragma unroll
   for (int j = 0; j < U; ++j)
     if (i + j * THREADS < n) load(w[j]);  // (on their way while the angles are formed)
@@ -244,8 +245,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t st) {
   n = std::min<int64_t>(n, (a.T + 4 * sm_count() - 1) / (4 * sm_count()));
   a.tokens = (int)n;
   const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
-  k_rope<T, V, INTER, LOOSE><<<(unsigned)blocks, THREADS, (size_t)a.tokens * a.R * sizeof(float), st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_rope<T, V, INTER, LOOSE>, dim3((unsigned)blocks), THREADS, (size_t)a.tokens * a.R * sizeof(float), st, a);
 }
 
 template <typename T>
