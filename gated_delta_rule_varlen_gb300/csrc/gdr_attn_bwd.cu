@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           const Phase kp{&s.k_full[kr.st], (uint32_t)kr.ph}, vp{&s.v_full[vr.st], (uint32_t)vr.ph};
           ok = warp_wait_all(ab, kp, g >= 2 ? Phase{&s.dq_done[g & 1], (uint32_t)(g / 2 - 1) & 1} : kp);
           if (!ok) break;
+          tc::tc_fence_after();  // (another warp issued the products that read dS)
           mma_rows<DB>(tmem + (g & 1) * TILE, q_lo, desc_lo(s.K[kr.st]), id_s, ks);
           commit(&s.s_full[g & 1]);
           kr.step();

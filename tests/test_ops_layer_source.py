@@ -1,0 +1,30 @@
+"""What the attention kernels' source has to hold for their hand-overs between threads, where a
+mistake would show only by chance on a GPU."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gated_delta_rule_varlen_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+# Barriers by which tensor memory changes hands, between the threads that issue products and those
+# that read and write it.
+HANDOVER = re.compile(r"warp_wait(?:_all)?\([^;]*&s\.(s_full|p_full|o_full|o_empty|dp_full|dp_read|ds_full|dq_done|acc_full|acc_empty)\b[^;]*;")
+USES = re.compile(r"tc_fence_after\(\)|\bmma_(?:ss|ts|rows|sum)\b|\bscore\(|\bgrad\(\)|\bload_cols\(|\btmem_ld\d+\(|\bstore16\(")
+
+
+@pytest.mark.parametrize("name", ["gdr_attn_fwd.cu", "gdr_attn_bwd.cu"])
+def test_tensor_memory_is_used_after_a_fence(name):
+    # tcgen05 operations of different threads are ordered by a barrier and the fence behind its wait
+    text, found = source(name), []
+    for m in HANDOVER.finditer(text):
+        use = USES.search(text, m.end())
+        found.append(m.group(1))
+        assert use and use.group(0).startswith("tc_fence_after"), (m.group(0), use and use.group(0))
+    assert len(found) >= 4
