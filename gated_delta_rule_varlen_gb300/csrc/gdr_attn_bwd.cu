@@ -815,11 +815,14 @@ __global__ void __launch_bounds__(256) k_attn_sum(const float* __restrict__ part
   vstore<__nv_bfloat16, 8>((blockIdx.y ? y : x) + i, s);
 }
 
+// early: begins beside the last blocks of the kernel before.
 template <typename K>
-cudaError_t go(K kernel, size_t smem, int64_t blocks, const BwdArgs& f, cudaStream_t st) {
+cudaError_t go(K kernel, size_t smem, int64_t blocks, const BwdArgs& f, cudaStream_t st, bool early) {
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-  return launch_early(kernel, dim3((unsigned)blocks), THREADS, smem, st, f);
+  if (early) return launch_early(kernel, dim3((unsigned)blocks), THREADS, smem, st, f);
+  kernel<<<dim3((unsigned)blocks), THREADS, smem, st>>>(f);
+  return cudaGetLastError();
 }
 template <typename S>
 constexpr size_t bytes_of() {
@@ -867,9 +870,9 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
       ProfScope ps("attn_dq", st, (double)a.T * a.H);
       const bool queue = blocks > sm_count();
       constexpr size_t b1 = bytes_of<DqSmem<1>>(), b2 = bytes_of<DqSmem<2>>();
-      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dq<1, true>, b1, blocks, f, st) : go(k_attn_dq<1, false>, b1, blocks, f, st)
-                          : queue   ? go(k_attn_dq<2, true>, b2, blocks, f, st)
-                                    : go(k_attn_dq<2, false>, b2, blocks, f, st))
+      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dq<1, true>, b1, blocks, f, st, true) : go(k_attn_dq<1, false>, b1, blocks, f, st, true)
+                          : queue   ? go(k_attn_dq<2, true>, b2, blocks, f, st, true)
+                                    : go(k_attn_dq<2, false>, b2, blocks, f, st, true))
         return e;
     }
     if (cudaError_t e = sum(a.T * a.H * a.D, a.dq, nullptr)) return e;
@@ -881,9 +884,12 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
       ProfScope ps("attn_dkv", st, (double)a.TK * a.HK);
       const bool queue = blocks > 4 * sm_count();
       constexpr size_t b1 = bytes_of<DkvSmem<1>>(), b2 = bytes_of<DkvSmem<2>>();
-      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dkv<1, true>, b1, blocks, f, st) : go(k_attn_dkv<1, false>, b1, blocks, f, st)
-                          : queue   ? go(k_attn_dkv<2, true>, b2, blocks, f, st)
-                                    : go(k_attn_dkv<2, false>, b2, blocks, f, st))
+      // What it reads before it waits (the documents, q, k, v, dout) is there because dQ's kernel began
+      // after all that came before; without queries there is no such kernel.
+      const bool early = qblocks > 0;
+      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dkv<1, true>, b1, blocks, f, st, early) : go(k_attn_dkv<1, false>, b1, blocks, f, st, early)
+                          : queue   ? go(k_attn_dkv<2, true>, b2, blocks, f, st, early)
+                                    : go(k_attn_dkv<2, false>, b2, blocks, f, st, early))
         return e;
     }
     if (cudaError_t e = sum(a.TK * a.HK * a.D, a.dk, a.dv)) return e;

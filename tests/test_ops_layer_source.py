@@ -29,3 +29,14 @@ def test_tensor_memory_is_used_after_a_fence(name):
         found.append(m.group(1))
         assert use and use.group(0).startswith("tc_fence_after"), (m.group(0), use and use.group(0))
     assert len(found) >= 4
+
+
+def test_dkv_begins_early_only_behind_dq():
+    # k_attn_dkv reads the documents' bounds and starts its loads before it waits for the kernel before:
+    # only where that is k_attn_dq (or follows it), all of whose threads wait for what came before first
+    text = source("gdr_attn_bwd.cu")
+    launches = re.findall(r"go\(k_attn_dkv<[^>]*>, b\d, blocks, f, st(?:, (\w+))?\)", text)
+    assert len(launches) == 4 and set(launches) == {"early"}
+    assert re.search(r"const bool early = qblocks > 0;", text)
+    dq = text[text.index("k_attn_dq(const"):text.index("k_attn_dkv(const")]
+    assert dq.index("previous_ended();") < min(dq.index("next_may_start();"), dq.index("BlockFinder"), dq.index("if (warp >= WORKERS)"))
