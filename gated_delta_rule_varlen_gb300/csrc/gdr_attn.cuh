@@ -60,8 +60,9 @@ struct AttnBlock {
   int first;           // token within the document
   int q0, lq, k0, lk;  // the document's queries and keys
 };
-// Finds blocks of the documents, each `want` at least the one before it (one warp, the same
-// answer on every lane): 32 documents are held in registers.
+// Finds blocks of the documents (one warp, the same answer on every lane): 32 documents are held
+// in registers, and the search goes on from them, or from the first ones for a block before them
+// (blocks taken over come in no order that the hardware promises).
 template <bool LAST>
 struct BlockFinder {
   const AttnArgs& a;
@@ -93,6 +94,10 @@ struct BlockFinder {
     total = __shfl_sync(0xffffffffu, pre, 31);
   }
   __device__ __forceinline__ AttnBlock find(int want) {
+    if (want < before) {
+      before = 0;
+      load(0);
+    }
 #pragma unroll 1
     while (want - before >= total && d0 + 32 < a.N) {
       before += total;

@@ -40,3 +40,11 @@ def test_dkv_begins_early_only_behind_dq():
     assert re.search(r"const bool early = qblocks > 0;", text)
     dq = text[text.index("k_attn_dq(const"):text.index("k_attn_dkv(const")]
     assert dq.index("previous_ended();") < min(dq.index("next_may_start();"), dq.index("BlockFinder"), dq.index("if (warp >= WORKERS)"))
+
+
+def test_blocks_are_found_in_any_order():
+    # clusterlaunchcontrol.try_cancel answers with any block that has not begun; a search that only
+    # went on would compute a place before its documents
+    text = source("gdr_attn.cuh")
+    find = text[text.index("AttnBlock find(int want)"):]
+    assert re.match(r"AttnBlock find\(int want\) \{\s*if \(want < before\) \{\s*before = 0;\s*load\(0\);\s*\}", find)
