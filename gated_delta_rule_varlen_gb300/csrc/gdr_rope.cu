@@ -45,6 +45,8 @@ struct RopeArgs {
 };
 
 constexpr int THREADS = 256;
+// Most elements of a token: a thread's count of units passes their number by a step of the loop.
+constexpr int64_t ROPE_MAX_ROW = INT32_MAX - 16 * THREADS;
 // Units a thread asks for together: of eight elements (two pieces of 16 bytes each) two, so
 // that an SM holds four blocks (64 registers a thread); with four of them it held two.
 constexpr int rope_ahead(int V) { return V == 8 ? 2 : 4; }
@@ -269,7 +271,7 @@ extern "C" gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int
                            const void* positions, int positions64, const int32_t* cu_seqlens, int32_t N,
                            int interleaved, float amplitude, int inverse, cudaStream_t stream) {
   if (dtype < 0 || dtype > GDR_DTYPE_F32 || T < 0 || T > GDR_OPS_MAX_T || HQ < 0 || HK < 0) return GDR_INVALID_ARG;
-  if (D <= 0 || R < 0 || R > D || R > GDR_ROPE_MAX_R || R % 2 != 0 || (int64_t)D * ((int64_t)HQ + HK) > INT32_MAX) return GDR_INVALID_ARG;
+  if (D <= 0 || R < 0 || R > D || R > GDR_ROPE_MAX_R || R % 2 != 0 || (int64_t)D * ((int64_t)HQ + HK) > ROPE_MAX_ROW) return GDR_INVALID_ARG;
   if (T == 0 || HQ + HK == 0) return GDR_OK;
   if ((HQ > 0 && (!q || !q_out)) || (HK > 0 && (!k || !k_out)) || (R > 0 && !freqs)) return GDR_INVALID_ARG;
   if (R > 0 && !positions && (!cu_seqlens || N <= 0)) return GDR_INVALID_ARG;

@@ -522,7 +522,7 @@ gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const v
  * [N + 1].  The angle modulo a turn is exact to 2^-32 turns at any position up to
  * 2^31.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
  * elements apart, a head's elements dense.  An output may be its input (the same
- * rows).  R goes up to GDR_ROPE_MAX_R, D (HQ + HK) stays below 2^31. */
+ * rows).  R goes up to GDR_ROPE_MAX_R, D (HQ + HK) to 2^31 - 4097. */
 #define GDR_ROPE_MAX_R 8192
 gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, int32_t HQ, void* q_out, int64_t qo0,
                 int64_t qo1, const void* k, int64_t ks0, int64_t ks1, int32_t HK, void* k_out, int64_t ko0,

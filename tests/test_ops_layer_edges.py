@@ -1,0 +1,11 @@
+"""The attention layer's refusals and host arithmetic at the ends of their ranges; no GPU."""
+import pytest
+
+from test_ops_layer_abi import P, gdr  # noqa: F401
+
+
+@pytest.mark.parametrize("D,HQ,HK", [(2**31 - 1, 1, 0), (2**16, 2**15 - 1, 1), (2**31 - 4096, 0, 1), (1, 2**31 - 2, 1)])
+def test_rope_refuses_tokens_whose_count_of_units_passes_32_bits(gdr, D, HQ, HK):
+    # a thread's next unit is up to 2048 past the last one
+    status = gdr.load().rope_turn(0, P(), D, D, HQ, P(2), D, D, P(3), D, D, HK, P(4), D, D, 1, D, 0, P(5), P(6), 0, None, 0, 0, 1.0, 0, None)
+    assert status == gdr.GDR_INVALID_ARG
