@@ -59,6 +59,12 @@ def _host(cu_seqlens_host):
     return np.ascontiguousarray(h, dtype=np.int32)
 
 
+def _int32(name: str, n: int) -> int:
+    if not -2**31 <= n < 2**31:
+        raise ValueError(f"{name} {n} is past 32 bits")
+    return n
+
+
 def sconv_workspace_bytes(T: int, C: int, W: int) -> int:
     """Scratch bytes of sconv_bwd; host only."""
     n = ctypes.c_size_t(0)
@@ -193,7 +199,7 @@ def norm_bwd(x, weight=None, post_weight=None, gate=None, act="silu", residual=N
 def lnorm_workspace_bytes(D: int) -> int:
     """Scratch bytes of lnorm_bwd for rows of D elements; host only."""
     n = ctypes.c_size_t(0)
-    _check(load().lnorm_workspace_bytes(D, ctypes.byref(n)), "lnorm_workspace_bytes")
+    _check(load().lnorm_workspace_bytes(_int32("lnorm_workspace_bytes: D", D), ctypes.byref(n)), "lnorm_workspace_bytes")
     return n.value
 
 
@@ -276,6 +282,8 @@ def attn_workspace_bytes(T: int, TK: int, H: int, HK: int, D: int, cu_seqlens_ho
     """(scratch bytes of attn_fwd, of attn_bwd); host only."""
     host, keys = _host(cu_seqlens_host), None if cu_keys_host is None else _host(cu_keys_host)
     fwd, bwd = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    H, HK, D = (_int32(f"attn_workspace_bytes: {n}", i) for n, i in (("H", H), ("HK", HK), ("D", D)))
+    window = max(-1, min(window, 2**31 - 1))  # (a longer one sees no more)
     _check(load().attn_workspace_bytes(T, TK, H, HK, D, host.shape[0] - 1, host.ctypes.data,
                                        None if keys is None else keys.ctypes.data, int(bool(causal)), window,
                                        ctypes.byref(fwd), ctypes.byref(bwd)), "attn_workspace_bytes")

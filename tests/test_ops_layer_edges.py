@@ -9,3 +9,15 @@ def test_rope_refuses_tokens_whose_count_of_units_passes_32_bits(gdr, D, HQ, HK)
     # a thread's next unit is up to 2048 past the last one
     status = gdr.load().rope_turn(0, P(), D, D, HQ, P(2), D, D, P(3), D, D, HK, P(4), D, D, 1, D, 0, P(5), P(6), 0, None, 0, 0, 1.0, 0, None)
     assert status == gdr.GDR_INVALID_ARG
+
+
+def test_workspace_sizes_past_32_bits(gdr):
+    # as attn_fwd takes them: a window past 2^31 sees everything, other sizes are refused, none is cut to 32 bits
+    want = gdr.attn_workspace_bytes(1, 65536, 32, 8, 128, [0, 1], [0, 65536])
+    for window in (2**31 - 1, 2**31, 2**32 + 5, 2**40):
+        assert gdr.attn_workspace_bytes(1, 65536, 32, 8, 128, [0, 1], [0, 65536], window=window) == want, window
+    for call in (lambda: gdr.attn_workspace_bytes(11, 11, 2, 2, 64, [0, 11], window=-2**32 + 5), lambda: gdr.attn_workspace_bytes(11, 11, 2**32 + 2, 2, 64, [0, 11]),
+                 lambda: gdr.attn_workspace_bytes(11, 11, 2, 2**32 + 2, 64, [0, 11]), lambda: gdr.attn_workspace_bytes(11, 11, 2, 2, 2**32 + 64, [0, 11]),
+                 lambda: gdr.lnorm_workspace_bytes(2**32 + 64)):
+        with pytest.raises(ValueError):
+            call()
