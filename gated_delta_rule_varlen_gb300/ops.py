@@ -282,6 +282,11 @@ def attn_workspace_bytes(T: int, TK: int, H: int, HK: int, D: int, cu_seqlens_ho
     """(scratch bytes of attn_fwd, of attn_bwd); host only."""
     host, keys = _host(cu_seqlens_host), None if cu_keys_host is None else _host(cu_keys_host)
     fwd, bwd = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    for name, a in (("cu_seqlens_host", host), ("cu_keys_host", keys)):
+        if a is not None and (a.ndim != 1 or a.shape[0] < 1):
+            raise ValueError(f"attn_workspace_bytes: {name} must be one-dimensional with at least one entry")
+    if keys is not None and keys.shape != host.shape:
+        raise ValueError(f"attn_workspace_bytes: cu_keys_host has {keys.shape[0] - 1} documents, cu_seqlens_host {host.shape[0] - 1}")
     H, HK, D = (_int32(f"attn_workspace_bytes: {n}", i) for n, i in (("H", H), ("HK", HK), ("D", D)))
     window = max(-1, min(window, 2**31 - 1))  # (a longer one sees no more)
     _check(load().attn_workspace_bytes(T, TK, H, HK, D, host.shape[0] - 1, host.ctypes.data,

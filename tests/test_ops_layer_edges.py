@@ -21,3 +21,10 @@ def test_workspace_sizes_past_32_bits(gdr):
                  lambda: gdr.lnorm_workspace_bytes(2**32 + 64)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_workspace_sizes_of_other_documents(gdr):
+    # host arrays of another length would be read past their end
+    for cu, keys in (([0, 5, 11], [0, 11]), ([0, 11], [0, 5, 11]), ([0, 11], [[0, 11]]), ([], None)):
+        with pytest.raises(ValueError, match="cu_"):
+            gdr.attn_workspace_bytes(11, 11, 2, 2, 64, cu, keys)
