@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = 0; c < nch; ++c) {
       const uint32_t b = c & 1;
       // Yo = C S0, the first terms
-      ok = warp_wait(&s.s_full, c & 1, ab) && warp_wait(&s.bc_full[b], (c >> 1) & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.s_full, c & 1, ab) && warp_wait<ByTries>(&s.bc_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait<ByTries>(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         if (k < ksteps) mma_ss(tmem + T_YO, d_c + b * stage2 + kmaj(k), d_s + k * step, i_yo, k > 0);
       commit(&s.yo_full);
       // U = B^T (w x)
-      ok = warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.u_empty, (c - 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait<ByTries>(&s.u_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = 0; c < nch; ++c) {
       const uint32_t b = c & 1;
       // CB = C B^T, once Yd has read the M in its columns
-      ok = warp_wait(&s.bc_full[b], (c >> 1) & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.y_full, (c - 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.bc_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait<ByTries>(&s.y_full, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
         if (k < ksteps) mma_ss(tmem + T_CB, d_c + b * stage2 + kmaj(k), d_b + b * stage2 + kmaj(k), i_cb, k > 0);
       commit(&s.cb_full);
       // Yo += C S0, the second terms (written once the first terms' products are there)
-      if (!warp_wait(&s.s2_full, c & 1, ab)) break;
+      if (!warp_wait<ByTries>(&s.s2_full, c & 1, ab)) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       commit(&s.yo2_full);
       commit(&s.bc_empty[b]);
       // Yd = M x (M waited for x; the rows past the end are cleared with w x)
-      ok = warp_wait(&s.m_full, c & 1, ab);
-      if (sg.len - c * Q < Q) ok = ok && warp_wait(&s.xw_full[b], (c >> 1) & 1, ab);
-      if (c > 0) ok = ok && warp_wait(&s.y_empty, (c - 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.m_full, c & 1, ab);
+      if (sg.len - c * Q < Q) ok = ok && warp_wait<ByTries>(&s.xw_full[b], (c >> 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait<ByTries>(&s.y_empty, (c - 1) & 1, ab);
       if (!ok) break;
       tc::tc_fence_after();
 #pragma unroll
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
         const int b = c & 1, row = sg.tok0 + c * Q;
-        if (c >= 2 && !wait_or_abort(&s.bc_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        if (c >= 2 && !wait_or_abort<ByTries>(&s.bc_empty[b], ((c >> 1) - 1) & 1, ab)) break;
         tc::mbar_arrive_expect_tx(&s.bc_full[b], (uint32_t)(2 * nblk * BLK));
 #pragma unroll 1
         for (int k = 0; k < nblk; ++k) {
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
           tc::tma_load_3d(s.B[b] + k * BLK, &ta.b_map, 64 * k, grp, row, &s.bc_full[b]);
         }
         bc = c + 1;
-        if (c >= 2 && !wait_or_abort(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
+        if (c >= 2 && !wait_or_abort<ByTries>(&s.x_empty[b], ((c >> 1) - 1) & 1, ab)) break;
         tc::mbar_arrive_expect_tx(&s.x_full[b], (uint32_t)(BLK + sizeof(s.gates[0])));
         tc::tma_load_3d(s.X[b], &ta.x_map, p0, h, row, &s.x_full[b]);
         if (c == 0) previous_ended();  // the gates come from the kernel before
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll 1
     for (int c = 0; c < nch && ok; ++c) {
       const int b = c & 1;
-      ok = warp_wait(&s.staged[b], (c >> 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.staged[b], (c >> 1) & 1, ab);
       if (ok && lane == 0) {
         if (sg.len - c * Q >= Q) {  // a whole chunk; a partial one was stored row by row
           asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
       const Gates g{s.gates[st]};
-      if (!warp_wait(&s.x_full[st], (c >> 1) & 1, ab) || !warp_wait(&s.cb_full, c & 1, ab)) break;
+      if (!warp_wait<ByTries>(&s.x_full[st], (c >> 1) & 1, ab) || !warp_wait<ByTries>(&s.cb_full, c & 1, ab)) break;
       tc::tc_fence_after();
       const float sr = g.ss()[r];
       const uint32_t cb = trow + T_CB + j0;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
     float gam = 0.f;
     bool ok = true;
     auto advance = [&](int c) {  // S = gam S + U of chunk c
-      ok = warp_wait(&s.u_full, c & 1, ab);
+      ok = warp_wait<ByTries>(&s.u_full, c & 1, ab);
       if (!ok) return;
       tc::tc_fence_after();
       const uint64_t gg = pack2(gam, gam), one = pack2(1.f, 1.f);
@@ -605,9 +605,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[q] = make_uint4(round2(S[4 * q]), round2(S[4 * q + 1]), round2(S[4 * q + 2]), round2(S[4 * q + 3]));
-      ok = warp_wait(&s.x_full[c & 1], (c >> 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.x_full[c & 1], (c >> 1) & 1, ab);
       // the previous chunk's Yo has read the operand
-      if (c > 0) ok = ok && warp_wait(&s.yo2_full, (c - 1) & 1, ab);
+      if (c > 0) ok = ok && warp_wait<ByTries>(&s.yo2_full, (c - 1) & 1, ab);
       if (!ok) break;
       gam = ex2(Gates{s.gates[c & 1]}.total(A));
       warp_arrive(&s.x_empty[c & 1]);
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[q] = make_uint4(rest2(S[4 * q]), rest2(S[4 * q + 1]), rest2(S[4 * q + 2]), rest2(S[4 * q + 3]));
-      ok = warp_wait(&s.yo_full, c & 1, ab);
+      ok = warp_wait<ByTries>(&s.yo_full, c & 1, ab);
       if (!ok) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(s.S + piece(r, 4 * half + q)) = v[q];
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       if (c >= 0) {
         const int len = sg.len - c * Q;
         __nv_bfloat16* out = a.out + ((int64_t)(sg.tok0 + c * Q + r) * a.H + h) * a.P + pc;
-        ok = warp_wait(&s.y_full, c & 1, ab);
+        ok = warp_wait<ByTries>(&s.y_full, c & 1, ab);
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
@@ -672,9 +672,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_ssm_walk(const __grid_const
       if (c + 1 < nch) {  // w x of the next chunk, once U has read this one's
         const int n = (c + 1) & 1, len = sg.len - (c + 1) * Q;
         const Gates g{s.gates[n]};
-        ok = warp_wait(&s.x_full[n], ((c + 1) >> 1) & 1, ab);
-        if (c >= 0) ok = ok && warp_wait(&s.u_full, c & 1, ab);
-        if (len < Q) ok = ok && warp_wait(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
+        ok = warp_wait<ByTries>(&s.x_full[n], ((c + 1) >> 1) & 1, ab);
+        if (c >= 0) ok = ok && warp_wait<ByTries>(&s.u_full, c & 1, ab);
+        if (len < Q) ok = ok && warp_wait<ByTries>(&s.bc_full[n], ((c + 1) >> 1) & 1, ab);
         if (!ok) break;
         if (r >= len) {
           clear_pieces<4>(s.X[n], r, 4 * half);
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
 #pragma unroll 1
       for (int k = 0, b = 0, ph = 1; k < nch; ++k) {
         const int row = sg.tok0 + (nch - 1 - k) * Q;
-        if (k >= SUM_STAGES && !wait_or_abort(&empty[b], ph, ab)) break;
+        if (k >= SUM_STAGES && !wait_or_abort<ByTries>(&empty[b], ph, ab)) break;
         tc::mbar_arrive_expect_tx(&full[b], (uint32_t)((is_x ? 1 + two : nblk) * BLK));
         if (is_x) {
 #pragma unroll 1
@@ -821,11 +821,11 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       const int batch = k / kBatch, first = k % kBatch == 0;
       const uint32_t m = two ? 0 : k & 1, acc = tmem + (batch & 1) * 256;
       const uint32_t bb = d_b + b * 2 * blk, ww = d_w + m * 3 * blk;
-      ok = warp_wait(&s.b_full[b], (k / SUM_STAGES) & 1, ab);
-      if (first && batch >= 2) ok = ok && warp_wait(&s.acc_empty[batch & 1], ((batch >> 1) - 1) & 1, ab);
+      ok = warp_wait<ByTries>(&s.b_full[b], (k / SUM_STAGES) & 1, ab);
+      if (first && batch >= 2) ok = ok && warp_wait<ByTries>(&s.acc_empty[batch & 1], ((batch >> 1) - 1) & 1, ab);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        ok = ok && warp_wait(&s.xw_full[m][half], (two ? k : k >> 1) & 1, ab);
+        ok = ok && warp_wait<ByTries>(&s.xw_full[m][half], (two ? k : k >> 1) & 1, ab);
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
 #pragma unroll
     for (int q = 0; q < PT / 4; ++q) S[q] = 0;
     auto drain = [&](int batch) {
-      if (!warp_wait(&s.acc_full[batch & 1], (batch >> 1) & 1, ab)) return false;
+      if (!warp_wait<ByTries>(&s.acc_full[batch & 1], (batch >> 1) & 1, ab)) return false;
       tc::tc_fence_after();
 #pragma unroll
       for (int p = 0; p < PT / 2; p += 8) {
@@ -885,13 +885,13 @@ __global__ void __launch_bounds__(SUM_THREADS, 1) k_ssm_sum(const __grid_constan
       gates(min(k + 1, nch - 1));
       if (two || (k & 1) == g >> 1) {
         const int m = two ? 0 : k & 1, use = two ? k : k >> 1;
-        ok = warp_wait(&s.x_full[b], ph, ab);
+        ok = warp_wait<ByTries>(&s.x_full[b], ph, ab);
         if (!ok) break;
         uint4 x[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(s.X[b][n] + piece(r, c0 + c));
         warp_arrive(&s.x_empty[b]);
-        ok = use < 1 || warp_wait(&s.xw_empty[m][half], (use - 1) & 1, ab);
+        ok = use < 1 || warp_wait<ByTries>(&s.xw_empty[m][half], (use - 1) & 1, ab);
         if (!ok) break;
         build_xw<4>(x, s.xw[3 * m + n], BLK << two, r, c0, w);
         tc::fence_proxy_async();

@@ -12,23 +12,15 @@ namespace gdr {
 
 constexpr int BLK = 128 * 128;  // bytes of a tile block: 128 rows of 64 BF16
 
-// Waits of the blocks' roles.  Each gives up after kWaitNs, or once another role has, and
-// returns false; the block then reports the timeout as it ends.  Few instructions: the roles
-// run straight through long loops that share the instruction cache.  A try is suspended
-// until the phase completes or the hardware's own limit passes (with a limit of a
-// microsecond asked for, the attention kernels took 3 to 4% longer); the clock is read every
-// sixteenth of them.
+// Waits of the blocks' roles.  Each gives up when its limit is over, or once another role has,
+// and returns false; the block then reports the timeout as it ends.  Few instructions: the
+// roles run straight through long loops that share the instruction cache.
 constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(tc::smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-struct WaitLimit {
+// kWaitNs by the clock, read every sixteenth try; a try is suspended until the phase completes or
+// the hardware's own limit passes (with a limit of a microsecond asked for, the attention kernels
+// took 3 to 4% longer).
+struct ByClock {
+  static constexpr uint32_t SUSPEND = 0;
   uint64_t start = 0;
   __device__ __forceinline__ bool over(int tries) {
     if ((tries & 15) != 15) return false;
@@ -37,9 +29,33 @@ struct WaitLimit {
     return now - start > kWaitNs;
   }
 };
+// 2^20 tries of at most a microsecond: the fewest instructions (the scan of 32768 tokens takes
+// 441 us, with the clock 466).
+struct ByTries {
+  static constexpr uint32_t SUSPEND = 1000;
+  __device__ __forceinline__ bool over(int tries) { return tries > 1 << 20; }
+};
+template <typename Limit>
+__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  if constexpr (Limit::SUSPEND > 0)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(Limit::SUSPEND)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+  return done != 0;
+}
+template <typename Limit>
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  WaitLimit limit;
-  for (int tries = 0; !try_phase(bar, parity); ++tries)
+  Limit limit;
+  for (int tries = 0; !try_phase<Limit>(bar, parity); ++tries)
     if (limit.over(tries) || *abort) {
       *abort = 1;
       return false;
@@ -103,25 +119,26 @@ struct Phase {
   uint64_t* bar;
   uint32_t parity;
 };
-template <typename... P>
+template <typename Limit = ByClock, typename... P>
 __device__ __forceinline__ bool warp_wait_all(volatile int* abort, P... p) {
-  WaitLimit limit;
-  for (int tries = 0; !__all_sync(0xffffffffu, (try_phase(p.bar, p.parity) & ...)); ++tries)
+  Limit limit;
+  for (int tries = 0; !__all_sync(0xffffffffu, (try_phase<Limit>(p.bar, p.parity) & ...)); ++tries)
     if (__any_sync(0xffffffffu, limit.over(tries) || *abort)) {
       *abort = 1;
       return false;
     }
   return true;
 }
+template <typename Limit = ByClock>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return warp_wait_all(abort, Phase{bar, parity});
+  return warp_wait_all<Limit>(abort, Phase{bar, parity});
 }
 // A wait before a block ends, whatever has happened: 20 ms at most, and what a try is
 // suspended for.
 __device__ __forceinline__ void wait_some(uint64_t* bar, uint32_t parity) {
-  if (try_phase(bar, parity)) return;
+  if (try_phase<ByClock>(bar, parity)) return;
   const uint64_t start = tc::global_ns();
-  while (!try_phase(bar, parity) && tc::global_ns() - start < 20000000ull) {
+  while (!try_phase<ByClock>(bar, parity) && tc::global_ns() - start < 20000000ull) {
   }
 }
 // tcgen05.wait::ld with the loaded registers as operands: nothing that reads

@@ -48,3 +48,10 @@ def test_blocks_are_found_in_any_order():
     text = source("gdr_attn.cuh")
     find = text[text.index("AttnBlock find(int want)"):]
     assert re.match(r"AttnBlock find\(int want\) \{\s*if \(want < before\) \{\s*before = 0;\s*load\(0\);\s*\}", find)
+
+
+def test_the_scan_waits_by_tries():
+    # the clock's instructions in its loops cost the scan 5% (32768 tokens 441 -> 466 us)
+    text = source("gdr_ssm_tc.cu")
+    waits = re.findall(r"\b(?:warp_wait(?:_all)?|wait_or_abort|try_phase)\b(<\w+>)?\(", text)
+    assert len(waits) > 20 and set(waits) == {"<ByTries>"}
