@@ -154,6 +154,7 @@ struct DqWork {
     all = tiles_of(a, b.lq, b.lk, b.first, i1);
     r = part_of(all, part, ba.parts);
   }
+  __device__ __forceinline__ int steps() const { return max(0, r.hi - r.lo); }
 };
 
 template <int DB>
@@ -489,6 +490,7 @@ struct DkvWork {
     g0 = per ? mine.lo / per : 0;
     first = per ? mine.lo % per : 0;
   }
+  __device__ __forceinline__ int steps() const { return n; }
 };
 
 template <int DB>

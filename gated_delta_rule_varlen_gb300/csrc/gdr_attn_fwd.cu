@@ -77,6 +77,7 @@ struct FwdWork {
     if (dual) r[1] = r[0];
     step = dual ? 2 : 1;
   }
+  __device__ __forceinline__ int steps() const { return max(0, all.hi - all.lo); }
   __device__ __forceinline__ bool any(int t) const { return r[t].lo < r[t].hi; }
   __device__ __forceinline__ bool works(int t, int j) const {
     return dual ? ((j - all.lo) & 1) == t : j >= r[t].lo && j < r[t].hi;

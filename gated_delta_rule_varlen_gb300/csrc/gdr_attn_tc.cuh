@@ -61,22 +61,25 @@ struct WorkQueue {
     tc::mbar_init(&wanted, 1);
     tc::mbar_init(&asked, 1);
   }
-  // The warp that asks: make(item) -> Work.
+  // The warp that asks: make(item) -> Work.  The others ask for the next item when they have
+  // gone through all steps of the last, each of which has waits of its own limit.
   template <typename F>
   __device__ __forceinline__ void run(volatile int* abort, F make) {
     const int lane = threadIdx.x & 31;
     int item = (int)blockIdx.x;
     bool have = true;
+    ByClock limit;
     for (int k = 0;; ++k) {
       const int e = k & 1;
       if (k >= 2 && !warp_wait(&empty[e], ((k >> 1) - 1) & 1, abort)) return;
       if (have) {
         const Work w = make(item);
+        limit.ns = kWaitNs * (1 + (uint64_t)w.steps());
         if (lane == 0) work[e] = w;
       }
       if (lane == 0) more[e] = have;
       warp_arrive(&full[e]);
-      if (!have || !warp_wait(&wanted, e, abort)) return;
+      if (!have || !warp_wait_within(limit, abort, Phase{&wanted, (uint32_t)e})) return;
       if (lane == 0) {
         tc::fence_proxy_async();  // (the last answer has been read)
         tc::mbar_arrive_expect_tx(&asked, 16);

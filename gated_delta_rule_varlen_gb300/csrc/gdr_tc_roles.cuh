@@ -16,17 +16,17 @@ constexpr int BLK = 128 * 128;  // bytes of a tile block: 128 rows of 64 BF16
 // and returns false; the block then reports the timeout as it ends.  Few instructions: the
 // roles run straight through long loops that share the instruction cache.
 constexpr uint64_t kWaitNs = 2000000000ull;
-// kWaitNs by the clock, read every sixteenth try; a try is suspended until the phase completes or
+// A limit by the clock, read every sixteenth try; a try is suspended until the phase completes or
 // the hardware's own limit passes (with a limit of a microsecond asked for, the attention kernels
 // took 3 to 4% longer).
 struct ByClock {
   static constexpr uint32_t SUSPEND = 0;
-  uint64_t start = 0;
+  uint64_t ns = kWaitNs, start = 0;
   __device__ __forceinline__ bool over(int tries) {
     if ((tries & 15) != 15) return false;
     const uint64_t now = tc::global_ns();
     if (start == 0) start = now;
-    return now - start > kWaitNs;
+    return now - start > ns;
   }
 };
 // 2^20 tries of at most a microsecond: the fewest instructions (the scan of 32768 tokens takes
@@ -119,15 +119,18 @@ struct Phase {
   uint64_t* bar;
   uint32_t parity;
 };
-template <typename Limit = ByClock, typename... P>
-__device__ __forceinline__ bool warp_wait_all(volatile int* abort, P... p) {
-  Limit limit;
+template <typename Limit, typename... P>
+__device__ __forceinline__ bool warp_wait_within(Limit limit, volatile int* abort, P... p) {
   for (int tries = 0; !__all_sync(0xffffffffu, (try_phase<Limit>(p.bar, p.parity) & ...)); ++tries)
     if (__any_sync(0xffffffffu, limit.over(tries) || *abort)) {
       *abort = 1;
       return false;
     }
   return true;
+}
+template <typename Limit = ByClock, typename... P>
+__device__ __forceinline__ bool warp_wait_all(volatile int* abort, P... p) {
+  return warp_wait_within(Limit{}, abort, p...);
 }
 template <typename Limit = ByClock>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {

@@ -55,3 +55,12 @@ def test_the_scan_waits_by_tries():
     text = source("gdr_ssm_tc.cu")
     waits = re.findall(r"\b(?:warp_wait(?:_all)?|wait_or_abort|try_phase)\b(<\w+>)?\(", text)
     assert len(waits) > 20 and set(waits) == {"<ByTries>"}
+
+
+def test_the_wait_for_an_items_end_grows_with_the_item():
+    # an item's steps are waited for each within the limit; the warp that asks for items waits for all
+    # of them together, of which a document of some 10^7 tokens has more than fit in it
+    text = source("gdr_attn_tc.cuh")
+    run = text[text.index("void run("):text.index("bool take(")]
+    assert "kWaitNs * (1 + (uint64_t)w.steps())" in run and re.search(r"warp_wait_within\(limit, abort, Phase\{&wanted,", run)
+    assert len(re.findall(r"int steps\(\) const", source("gdr_attn_fwd.cu") + source("gdr_attn_bwd.cu"))) == 3
