@@ -6,8 +6,9 @@
 //
 // The angle keeps its accuracy at far positions without 64-bit floating point: the
 // frequency in turns a token is a 64-bit binary fraction, whose product with the
-// position, modulo 2^64, is the angle's fraction of a turn (off by position 2^-65 turns
-// beside the frequency's own rounding), and the top 32 bits of it become sine and cosine.
+// position, modulo 2^64, is the angle's fraction of a turn, and the top 32 bits of it become
+// sine and cosine.  The fraction of a token is off by (1 + f / 260) 2^-64 turns: what is cut off,
+// and the rounding of 2^66 / (2 pi) to 64 bits.  Frequencies that are not finite turn to NaN.
 //
 // Bound by HBM: each element read once and written once; 32768 tokens of 40 heads of 128 in
 // BF16 take 121 us, 82% of the copy rate (FP32 96%).  A block turns the heads of some
@@ -65,9 +66,10 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   else u = sh > -64 ? lo << -sh : 0;
   return f < 0.f ? 0 - u : u;
 }
-__device__ __forceinline__ void angle(uint64_t turns, uint64_t pos, float amp, bool back, float& c, float& s) {
-  const int top = (int)((turns * pos) >> 32);  // [-1/2, 1/2) turns
+__device__ __forceinline__ void angle(float f, uint64_t pos, float amp, bool back, float& c, float& s) {
+  const int top = (int)((turns_of(f) * pos) >> 32);  // [-1/2, 1/2) turns
   sincospif((float)top * 4.656612873077393e-10f, &s, &c);
+  if (!(fabsf(f) < INFINITY)) c = s = NAN;
   c *= amp;
   s *= back ? -amp : amp;
 }
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_rope(const __grid_constant__ Rop
     if (!a.pos) pos = (uint64_t)(at - a.cu[doc_of(a.cu, a.N, (int)at)]);
     else if (a.pos64) pos = (uint64_t)static_cast<const int64_t*>(a.pos)[at];
     else pos = (uint64_t)(int64_t)static_cast<const int*>(a.pos)[at];
-    angle(turns_of(__ldg(a.freq + e % half)), pos, a.amp, a.back, cs[e], sn[e]);
+    angle(__ldg(a.freq + e % half), pos, a.amp, a.back, cs[e], sn[e]);
   }
   __syncthreads();
   while (i < n) {

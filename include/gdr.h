@@ -519,8 +519,9 @@ gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const v
  * 2 i + 1).  inverse: t = -position freqs[pair], the gradient of the forward.
  * freqs [R / 2] FP32, radians a token; positions int32 or (positions64) int64
  * [T], any sign, or null: counted from the document's start by cu_seqlens
- * [N + 1].  The angle modulo a turn is exact to 2^-32 turns at any position up to
- * 2^31.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
+ * [N + 1].  At any position up to 2^31 the angle modulo a turn is exact to 2^-32
+ * turns for frequencies up to 256, to 2^-40 of the frequency beyond; a frequency that is
+ * not finite turns its pair to NaN.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
  * elements apart, a head's elements dense.  An output may be its input (the same
  * rows).  R goes up to GDR_ROPE_MAX_R, D (HQ + HK) to 2^31 - 4097. */
 #define GDR_ROPE_MAX_R 8192
