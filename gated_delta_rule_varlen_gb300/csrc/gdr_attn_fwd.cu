@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_fwd(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < TILE; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(x[i]));
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {  // (and of -inf: the first keys a row sees)
+        // (and of -inf: the first keys a row sees; rows of the next document do not ask)
+        if (__any_sync(0xffffffffu, live && (mx - m) * c > 8.f)) {
           const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
           m = mx;
           l *= f;

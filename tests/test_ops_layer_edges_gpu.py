@@ -34,6 +34,31 @@ def test_documents_written_by_the_kernel_before(gdr, D):
         assert cuk.tolist() == cuh
 
 
+@pytest.mark.parametrize("D,H,HK", [(128, 2, 1), (64, 2, 2)])
+def test_a_document_does_not_depend_on_its_neighbours(gdr, D, H, HK):
+    # a tile reaches into the next document, whose queries must not move anything of this one's, not
+    # even a rounding: queries 1000 times as large behind it, whose scores grow along its keys
+    g, lens = gen(D + H), [228, 100, 290, 60, 1, 130]
+    T = sum(lens)
+    cu, cuh = pack(lens)
+    q, k, v = heads(g, T, H, HK, D, "dense", T)
+    dout = randn(g, T, H, D, dtype=BF16)
+    k = (k.float() * torch.linspace(0.5, 2, T, device="cuda")[:, None, None]).to(BF16)
+    base = gdr.attn_fwd(q, k, v, cu, cuh)
+    grads = gdr.attn_bwd(q, k, v, *base, dout, cu, cuh)
+    q2, d2 = q.clone(), dout.clone()
+    for n in (1, 3, 5):
+        q2[cuh[n]:cuh[n + 1]] *= 1000
+        d2[cuh[n]:cuh[n + 1]] *= 1000
+    out = gdr.attn_fwd(q2, k, v, cu, cuh)
+    got = gdr.attn_bwd(q2, k, v, *out, d2, cu, cuh)
+    for n in (0, 2, 4):
+        rows = slice(cuh[n], cuh[n + 1])
+        assert torch.equal(out[0][rows], base[0][rows]) and torch.equal(out[1][:, rows], base[1][:, rows]), n
+        for name in got:
+            assert torch.equal(got[name][rows], grads[name][rows]), (n, name)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_frequencies_that_are_not_finite(gdr, interleaved):
     # cos and sin of what is no number, or has no end, are no numbers: at every position, 0 among them
