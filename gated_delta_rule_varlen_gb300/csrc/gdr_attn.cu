@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_attn_rows(AttnArgs a) {
 __device__ __forceinline__ float prob(float s, float c, float lse) { return lse == -INFINITY ? 0.f : ex2(fmaf(s, c, -lse * LOG2E)); }
 
 // sum_j p (dp - delta) k_j as sum_j p dp k_j - delta sum_j p k_j: delta, the sum of p dp
-// itself, is known after the one pass.  (dout . out would bring the rounding of out along:
+// itself (over that of p, which is off 1 by lse's rounding), is known after the one pass.  (dout . out would bring the rounding of out along:
 // where few keys are seen, 2^-8 of dp beside differences of dp.)
 __global__ void __launch_bounds__(WARPS * 32) k_attn_dq_rows(AttnArgs a) {
   const int64_t item = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
@@ -93,15 +93,17 @@ __global__ void __launch_bounds__(WARPS * 32) k_attn_dq_rows(AttnArgs a) {
   g.load(a.dout.row(t, h), a.D);
   pk.zero();
   dk.zero();
-  float delta = 0.f;
+  float delta = 0.f, all = 0.f;
   for (int j = r.lo; j < r.hi; ++j) {
     k.load(a.k.row(k0 + j, hk), a.D);
     v.load(a.v.row(k0 + j, hk), a.D);
     const float p = prob(dot(q, k), c, lse), pd = p * dot(g, v);
     delta += pd;
+    all += p;
     pk.add(p, k);
     dk.add(pd, k);
   }
+  if (all != 0.f) delta /= all;
   dk.add(-delta, pk);
   dk.store(a.dq + item * a.D, a.D, a.scale);
   if ((threadIdx.x & 31) == 0) a.delta[(int64_t)h * a.T + t] = delta;

@@ -12,13 +12,18 @@
 // cancels in dQ since a row of dS sums to zero, that part times the roundings stays);
 // accumulators, P and dS before that are FP32.
 //
-// delta = dout . out of the rounded out, but for queries whose keys fit one tile: with few
-// keys |out| is like |v|, and 2^-8 of it shows beside the differences dP - delta; there
-// delta is sum p dP, which the tile holds.
+// delta = dout . out of the rounded out is off by up to 2^-8 of |dout| |out|, which is nothing
+// beside dS of probabilities spread over many keys, and all of it where one key has nearly all:
+// dP - delta is small there.  What it is off by is sum dS, which comes with the tiles of dS: delta is
+// put right for dK and dV, and a tile of dQ with a row that it matters to (put_right) is formed again by
+// a second launch.  Of 8192 tokens of 16 heads of 128 the sums take 10 us of dQ, the second launch 8 where
+// there is nothing to do, 19 for the 4 tiles of 1024 that scores of unit inputs leave it, and 298 for all of
+// them (scores 4 times as large).  Where a tile of keys holds all that the queries see, delta is
+// sum p dP from the start: with few keys |out| is like |v|.
 //
 // Bound by the products and their operands' way from shared memory: of 8192 tokens of 16
-// heads over 4 of 128 columns dQ takes 276 us (three products, 1.5 PFLOP/s), dK and dV 350
-// (four, 1.6 PFLOP/s; cuBLAS's measured rate is 1.9).  Measured and not kept: tiles three
+// heads over 4 of 128 columns dQ takes 293 us (three products, 1.4 PFLOP/s), dK and dV 354
+// (four, 1.55 PFLOP/s; cuBLAS's measured rate is 1.9).  Measured and not kept: tiles three
 // deep in dQ and two in dK and dV, so that elements and products of different tiles overlap
 // (345 and 423 us: the elements' tensor memory traffic slows the products), the products of
 // dK and dV from two warps (408), eight warps on the elements (323 and 417), every warp
@@ -37,6 +42,8 @@ struct BwdArgs {
   int pack;
   int parts;    // blocks that share a tile's sums
   float* part;  // their shares: dQ [parts][T][H][D], or dK and dV [2][parts][TK][HK][D]
+  float4* sums; // of dQ's parts, [parts][H][T]: sum dS, sum P^2, sum dS^2, the delta that dS was formed with
+  int items;    // dQ's tiles
   int* err;
 };
 
@@ -163,7 +170,8 @@ struct DqSmem {
   static constexpr int KS = DB == 2 ? 3 : 6, VS = DB == 2 ? 2 : 4;
   unsigned char Q[DB * BLK], dO[DB * BLK];
   unsigned char K[KS][DB * BLK], V[VS][DB * BLK];
-  float part[QUARTERS][TILE];          // the quarters' shares of delta
+  float part[QUARTERS][TILE];          // the quarters' shares of delta, or of what it is off by
+  uint8_t squares_ds[TILE][QUARTERS];  // exponents
   WorkQueue<DqWork> queue;
   uint64_t q_full, do_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], cleared;
   uint64_t s_full[2], dp_full, dp_read, ds_full, dq_done[2], part_full, acc_full, acc_empty, done;
@@ -172,8 +180,26 @@ struct DqSmem {
 };
 constexpr int T_DP = 256, T_DQ = 384;  // (two tiles of S, and over them dS, before)
 
-template <int DB, bool QUEUE>
+// The lowest bit of delta says that dQ has to be formed again with it.
+__device__ __forceinline__ float marked(float delta, bool again) {
+  return __uint_as_float((__float_as_uint(delta) & ~1u) | (again ? 1u : 0u));
+}
+__device__ __forceinline__ bool is_marked(float delta) { return (__float_as_uint(delta) & 1u) != 0; }
+// delta put right by e = sum dS, which it was off by.  A row of dQ is then off by e |sum P k|, some e |k|
+// times the root of x = sum P^2, and is some |k| times the root of sum dS^2, of which y has a fourth of the
+// terms: it is formed again where the first is more than 2^-9 of the second (2^-8 where one of the
+// fourth's terms is the row; dS' own rounding is up to 2^-8 a term).
+__device__ __forceinline__ float put_right(float delta, float e, float x, float y) {
+  return marked(delta + e, fabsf(e) * sqrtf(x) > sqrtf(y) * (2.f / 512.f) || y > 1e38f);
+}
+// What a block works on: one tile; one tile, for whose delta it goes through the keys once before;
+// its own and those that it takes over; of every gridDim-th the marked ones, formed again.
+enum Form { ONE_TILE, TWICE, TAKE_OVER, AGAIN };
+
+template <int DB, int FORM>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ BwdArgs ba) {
+  constexpr bool QUEUE = FORM == TAKE_OVER || FORM == AGAIN;  // several tiles, from the queue
+  constexpr bool ROUGH = FORM == ONE_TILE || FORM == TAKE_OVER;  // delta of the rounded out, put right behind the keys
   using Smem = DqSmem<DB>;
   constexpr int KS = Smem::KS, VS = Smem::VS;
   extern __shared__ __align__(1024) unsigned char attn_smem[];
@@ -208,24 +234,54 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     tc::tmem_relinquish();
   }
   const int heads = 1 << ba.pack, tokens = TILE >> ba.pack;
-  previous_ended();
-  if constexpr (!QUEUE) next_may_start();  // (all that came before this kernel has ended)
   DqWork w;
+  if constexpr (FORM != AGAIN) previous_ended();
+  // All that came before this kernel has ended.  (Blocks of several tiles do not let the next kernel
+  // in: its waits for delta would count their time.)
+  if constexpr (!QUEUE) next_may_start();
   if constexpr (!QUEUE) {  // (one item, which every warp finds for itself)
     BlockFinder<true> finder(a, tokens);
     w.find(ba, finder, (int)blockIdx.x);
+  }
+  // Whether a row of the tile is marked (a warp).
+  auto to_do = [&](const DqWork& t) {
+    bool any = false;
+    if (t.r.lo < t.r.hi)
+      for (int row = lane; row < TILE; row += 32) {
+        const int token = t.b.first + (row >> ba.pack);
+        if (token < t.b.lq) any = any || is_marked(a.delta[(int64_t)(t.h0 + (row & (heads - 1))) * a.T + t.b.q0 + token]);
+      }
+    return __any_sync(0xffffffffu, any) != 0;
+  };
+  // Those of the block's first tiles, which its warps look at side by side (in the quarters' places).
+  constexpr int KNOWN = FORM == AGAIN ? (int)sizeof(s.part) : 0;
+  uint8_t* known = reinterpret_cast<uint8_t*>(s.part);
+  if constexpr (FORM == AGAIN) {
+    BlockFinder<true> finder(a, tokens);
+    bool waited = false;
+    for (int i = warp; i < KNOWN; i += THREADS / 32) {
+      const int64_t item = blockIdx.x + (int64_t)i * gridDim.x;
+      if (item >= ba.items) break;
+      w.find(ba, finder, (int)item);
+      if (!waited) previous_ended();  // (delta is there)
+      waited = true;
+      known[i] = to_do(w);
+    }
+    if (!waited) previous_ended();
   }
   int taken = 0;
   auto next_item = [&](bool ask) {
     if constexpr (QUEUE) return s.queue.take(taken, w, ab, ask);
     else return taken++ == 0;
   };
+  auto steps = [&] { return (w.r.hi - w.r.lo) * (FORM == TWICE && w.r.hi - w.r.lo > 1 ? 2 : 1); };  // tiles of keys
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem;
 
   if (warp >= WORKERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     if (warp == WORKERS) {  // loads
       Ring<KS> kr;
       Ring<VS> vr;
@@ -241,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           load_tile<DB>(s.dO, &ba.do_map, w.h0, b.q0 + b.first, &s.do_full);
         }
         __syncwarp();
-        for (int j = w.r.lo; j < w.r.hi; ++j, ++g) {
+        for (int j = w.r.lo, left = steps(); left > 0; --left, j = j + 1 < w.r.hi ? j + 1 : w.r.lo, ++g) {
           const int rows = b.lk - j * TILE;
           const bool clear = rows < TILE;
           ok = g < KS || warp_wait(&s.k_empty[kr.st], kr.ph ^ 1, ab);
@@ -283,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         if (w.r.lo >= w.r.hi) continue;
         ok = warp_wait_all(ab, Phase{&s.q_full, (uint32_t)k & 1}, Phase{&s.do_full, (uint32_t)k & 1});
         ++k;
-        for (int j = w.r.lo; j < w.r.hi && ok; ++j, ++g) {
+        for (int left = steps(); left > 0 && ok; --left, ++g) {
           // S takes the place of dS two tiles ago, dP that of the last dP
           const Phase kp{&s.k_full[kr.st], (uint32_t)kr.ph}, vp{&s.v_full[vr.st], (uint32_t)vr.ph};
           ok = warp_wait_all(ab, kp, g >= 2 ? Phase{&s.dq_done[g & 1], (uint32_t)(g / 2 - 1) & 1} : kp);
@@ -314,11 +370,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         if (w.r.lo >= w.r.hi) continue;
         if (QUEUE && k > 0) ok = warp_wait(&s.acc_empty, (k - 1) & 1, ab);
         ++k;
-        for (int j = w.r.lo; j < w.r.hi && ok; ++j, ++g) {
+        for (int left = steps(); left > 0 && ok; --left, ++g) {
           ok = warp_wait(&s.ds_full, g & 1, ab);
           if (!ok) break;
           tc::tc_fence_after();
-          mma_sum(tmem + T_DQ, tmem + (g & 1) * TILE, desc_lo(s.K[kr.st]), id_d, j > w.r.lo);
+          const int n = w.r.hi - w.r.lo;  // (of the steps for delta alone only the barriers go on)
+          if (left <= n) mma_sum(tmem + T_DQ, tmem + (g & 1) * TILE, desc_lo(s.K[kr.st]), id_d, left < n);
           commit(&s.dq_done[g & 1]);
           commit(&s.k_empty[kr.st]);
           kr.step();
@@ -330,18 +387,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
     } else {
       if constexpr (QUEUE) {
         BlockFinder<true> finder(a, tokens);
-        s.queue.run(ab, [&](int item) {
+        auto make = [&](int item) {
           w.find(ba, finder, item);
           return w;
-        });
+        };
+        if constexpr (FORM == AGAIN)
+          s.queue.run_those(ab, ba.items, make, known, KNOWN, to_do);
+        else
+          s.queue.run(ab, make);
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
     // a row a thread, of S and dP a quarter's columns
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float c = a.scale * LOG2E;
     const uint64_t cc = pack2(c, c);
+    auto squares_p = reinterpret_cast<uint8_t(*)[QUARTERS]>(s.part[0]);  // (the first quarter's own sum stays in registers)
     bool ok = true;
     int g = 0, k = 0;
     while (ok && next_item(false)) {
@@ -355,43 +418,66 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       const uint64_t bb = pack2(base, base);
       const KeyRange kr = keys_of(a, token, b.lq, b.lk);
       const KeyRange seen{keys_of(a, w.i1 - 1, b.lq, b.lk).lo, keys_of(a, b.first, b.lq, b.lk).hi};  // keys every row sees
-      float delta = 0.f;
-      auto exchange = [&](float mine, bool write) {  // delta of all quarters
+      float delta = FORM == AGAIN && live ? a.delta[h * a.T + at] : 0.f;
+      auto exchange = [&](float mine) {  // delta of all quarters
         s.part[quarter][row] = mine;
         warp_arrive(&s.part_full);
-        ok = ok && warp_wait(&s.part_full, k & 1, ab);
+        ok = ok && warp_wait(&s.part_full, 0, ab);  // (two exchanges a tile of queries)
         delta = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
-        if (live && write && quarter == 0) a.delta[h * a.T + at] = delta;
       };
-      if (any && !one) {
+      // delta = sum p dP / sum p of all quarters, through the tensor memory that dQ comes to later.
+      auto settle = [&](uint64_t pd, uint64_t ps) {
+        uint32_t x[16] = {__float_as_uint(sum_of(pd)), __float_as_uint(sum_of(ps))};
+        tc::tmem_st16(lanes + T_DQ + 16 * quarter, x);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        warp_arrive(&s.part_full);
+        ok = ok && warp_wait(&s.part_full, 0, ab);
+        tc::tc_fence_after();
+        float d = 0.f, all = 0.f;
+#pragma unroll
+        for (int i = 0; i < QUARTERS; ++i) {
+          uint32_t y[8];
+          tmem_ld8(lanes + T_DQ + 16 * i, y);
+          wait_ld(y);
+          d += __uint_as_float(y[0]);
+          all += __uint_as_float(y[1]);
+        }
+        delta = all == 0.f ? 0.f : d / all;
+      };
+      if (any) {
         constexpr int PIECES = DB * 8 / QUARTERS;  // of 8 elements of a row
         uint4 o[PIECES];
+        const bool given = !ROUGH || one;  // no delta of out
         const __nv_bfloat16* out = a.o + (at * a.H + h) * a.D;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
           const int d = (quarter * PIECES + i) * 8;
-          o[i] = live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
+          o[i] = !given && live && d < a.D ? *reinterpret_cast<const uint4*>(out + d) : make_uint4(0, 0, 0, 0);
         }
-        ok = warp_wait(&s.do_full, k & 1, ab);
-        float sum = 0.f;
+        // this tile's dO (the last one's place is free); nobody reads the last one's sums any more
+        const Phase there{&s.do_full, (uint32_t)k & 1};
+        ok = warp_wait_all(ab, there, QUEUE && k > 0 ? Phase{&s.acc_empty, (uint32_t)(k - 1) & 1} : there);
+        if (!given) {
+          float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const int pc = quarter * PIECES + i;
-          const uint4 v = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
-          const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < PIECES; ++i) {
+            const int pc = quarter * PIECES + i;
+            const uint4 v = *reinterpret_cast<const uint4*>(s.dO + (pc >> 3) * BLK + piece(row, pc & 7));
+            const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
+            for (int e = 0; e < 4; ++e) sum = fmaf(bf_lo(x[e]), bf_lo(y[e]), fmaf(bf_hi(x[e]), bf_hi(y[e]), sum));
+          }
+          exchange(sum);
         }
-        exchange(sum, w.r.lo == w.all.lo);
-      } else if (w.all.lo == w.all.hi && w.part == 0 && live && quarter == 0) {
-        a.delta[h * a.T + at] = 0.f;
+        if (QUEUE) warp_arrive(&s.q_empty);
       }
-      if (QUEUE && any) {  // (not before this item's tiles are there: the last one's place is free)
-        if (one) ok = warp_wait(&s.do_full, k & 1, ab);
-        warp_arrive(&s.q_empty);
-      }
+      uint64_t off = 0;          // sum dS: what delta is off by
+      uint64_t pp = 0, dd = 0;   // sum P^2, sum dS^2
+      uint64_t pd = 0, ps = 0;   // sum P dP, sum P
 #pragma unroll 1
-      for (int j = w.r.lo; j < w.r.hi; ++j, ++g) {
+      for (int j = w.r.lo, left = steps(); left > 0; --left, j = j + 1 < w.r.hi ? j + 1 : w.r.lo, ++g) {
+        const bool ahead = FORM == TWICE && left > w.r.hi - w.r.lo;  // for delta alone
         const uint32_t ts = lanes + (g & 1) * TILE + c0;
         ok = ok && warp_wait(&s.s_full[g & 1], (g >> 1) & 1, ab);
         if (!ok) break;
@@ -415,6 +501,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
               p[i] = pack2(2 * i >= lo && 2 * i < hi ? e : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? f : 0.f);
             }
           }
+          if constexpr (ROUGH) {
+#pragma unroll
+            for (int i = 0; i < COLS / 2; ++i) pp = fma2(p[i], p[i], pp);
+          }
         }
         ok = warp_wait(&s.dp_full, g & 1, ab);
         if (!ok) break;
@@ -428,16 +518,36 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           for (int i = 0; i < COLS; ++i)
             if (c0 + i >= b.lk - j * TILE) x[i] = 0u;
         }
-        if (one) {
+        if (FORM == TWICE && (one || ahead)) {
+#pragma unroll
+          for (int i = 0; i < COLS / 2; ++i) {
+            pd = fma2(p[i], pair_at(x + 2 * i), pd);
+            ps = add2(ps, p[i]);
+          }
+          if (one || left - 1 == w.r.hi - w.r.lo) settle(pd, ps);
+          if (!ok) break;
+          if (ahead) {
+            tc::tc_fence_before();
+            warp_arrive(&s.ds_full);
+            continue;
+          }
+        } else if (ROUGH && one) {
           uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < COLS / 2; ++i) sum[i & 1] = fma2(p[i], pair_at(x + 2 * i), sum[i & 1]);
-          exchange(sum_of(add2(sum[0], sum[1])), true);
+          exchange(sum_of(add2(sum[0], sum[1])));
           if (!ok) break;
         }
         const uint64_t minus = pack2(-delta, -delta);
 #pragma unroll
-        for (int i = 0; i < COLS / 2; ++i) x[i] = round_pair(mul2(p[i], add2(pair_at(x + 2 * i), minus)));
+        for (int i = 0; i < COLS / 2; ++i) {
+          const uint64_t ds = mul2(p[i], add2(pair_at(x + 2 * i), minus));
+          if constexpr (ROUGH) {
+            off = add2(off, ds);
+            if (i % 4 == 0) dd = fma2(ds, ds, dd);  // (of every fourth pair: all of them took dQ 4% longer)
+          }
+          x[i] = round_pair(ds);
+        }
         store_words(ts, x);
         tc::tc_fence_before();
         warp_arrive(&s.ds_full);
@@ -449,10 +559,43 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         tc::tc_fence_after();
         ++k;
       }
+      // The other quarters' sums reach the first: sum dS in their places, of the sums of squares the
+      // exponents, a byte each.  (All dS of the tile were there, and delta's shares read, for acc_full.)
+      const float my_off = sum_of(off), my_pp = sum_of(pp), my_dd = sum_of(dd);
+      if (ROUGH && any) {
+        if (quarter > 0) {
+          s.part[quarter][row] = my_off;
+          squares_p[row][quarter] = (uint8_t)(__float_as_uint(my_pp) >> 23);
+          s.squares_ds[row][quarter] = (uint8_t)(__float_as_uint(my_dd) >> 23);
+        }
+        warp_arrive(&s.part_full);
+      }
       const int64_t to = (at * a.H + h) * a.D;
       float* share = ba.parts > 1 ? ba.part + w.part * a.T * a.H * a.D + to : nullptr;
 #pragma unroll
       for (int i = 0; i < DB; ++i) store16(a.dq + to, share, DB * 16 * quarter + 16 * i, a.D, lanes + T_DQ, a.scale, any, live);
+      if (ROUGH && any) {
+        if (quarter == 0) {
+          ok = warp_wait(&s.part_full, 1, ab);
+          if (!ok) break;
+          float e = my_off, x = my_pp, y = my_dd;
+#pragma unroll
+          for (int i = 1; i < QUARTERS; ++i) {
+            e += s.part[i][row];
+            x += __uint_as_float((uint32_t)squares_p[row][i] << 23 | 0x400000u);
+            y += __uint_as_float((uint32_t)s.squares_ds[row][i] << 23);
+          }
+          if (live) {
+            if (ba.parts > 1) ba.sums[(w.part * a.H + h) * a.T + at] = make_float4(e, x, y, delta);
+            else a.delta[h * a.T + at] = put_right(delta, e, x, y);
+          }
+        }
+      } else if (FORM == TWICE && any) {
+        if (live && quarter == 0) a.delta[h * a.T + at] = delta;
+      } else if (FORM != AGAIN && live && quarter == 0) {  // no keys, or none of this part
+        if (ba.parts > 1) ba.sums[(w.part * a.H + h) * a.T + at] = make_float4(0.f, 0.f, 0.f, 0.f);
+        else a.delta[h * a.T + at] = 0.f;
+      }
       if (QUEUE && any) {
         tc::tc_fence_before();
         warp_arrive(&s.acc_empty);
@@ -463,6 +606,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
   __syncthreads();
   if (tid == 0 && s.abort) atomicExch(ba.err, 11);
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// delta of a query whose keys are in parts, from the parts' sums.
+__global__ void __launch_bounds__(256) k_attn_delta(const float4* __restrict__ sums, int parts, int64_t n, float* delta) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  previous_ended();
+  if (i >= n) return;
+  float e = 0.f, x = 0.f, y = 0.f, d = 0.f;
+  for (int p = 0; p < parts; ++p) {
+    const float4 s = sums[p * n + i];
+    e += s.x;
+    x += s.y;
+    y += s.z;
+    if (s.w != 0.f) d = s.w;  // (the same of all parts that have keys; zero of the others)
+  }
+  delta[i] = put_right(d, e, x, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -867,15 +1026,48 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
   // (512 blocks) 352 against 340.
   if (qblocks > 0) {
     f.parts = p.dq;
+    f.sums = reinterpret_cast<float4*>(scratch + p.dq * a.T * a.H * a.D);
     const int64_t blocks = qblocks * (a.H >> f.pack) * f.parts;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    f.items = (int)blocks;
+    constexpr size_t b1 = bytes_of<DqSmem<1>>(), b2 = bytes_of<DqSmem<2>>();
+    bool twice = false;
+    int longest = 0;  // tiles of keys
     {
       ProfScope ps("attn_dq", st, (double)a.T * a.H);
-      const bool queue = blocks > sm_count();
-      constexpr size_t b1 = bytes_of<DqSmem<1>>(), b2 = bytes_of<DqSmem<2>>();
-      if (cudaError_t e = a.D <= 64 ? queue ? go(k_attn_dq<1, true>, b1, blocks, f, st, true) : go(k_attn_dq<1, false>, b1, blocks, f, st, true)
-                          : queue   ? go(k_attn_dq<2, true>, b2, blocks, f, st, true)
-                                    : go(k_attn_dq<2, false>, b2, blocks, f, st, true))
+      const int64_t sms = sm_count();
+      auto pick = [&](auto form) {
+        return a.D <= 64 ? go(k_attn_dq<1, decltype(form)::value>, b1, blocks, f, st, true)
+                         : go(k_attn_dq<2, decltype(form)::value>, b2, blocks, f, st, true);
+      };
+      using std::integral_constant;
+      // Where every block has one tile of few keys, going through them twice is quicker than the second
+      // launch that the rounded out asks for: 4 heads of 64 / 128, documents of 300, 200, 157, 100 and 200
+      // tokens 20 / 24 us against 28 / 32, one of 640 tokens (5 tiles of keys) 23.0 / 29.1 against 24.5 /
+      // 30.5, of 900 (8 tiles) 32.7 / 40.5 against 31.5 / 38.7.
+      if (blocks <= sms && f.parts == 1) {
+        for (int i = 0; i < a.N; ++i)
+          for (int lq = cu[i + 1] - cu[i], lk = cuk[i + 1] - cuk[i], at = 0; at < lq; at += tokens) {
+            const TileRange r = tiles_of(a, lq, lk, at, std::min(lq, at + tokens));
+            longest = std::max(longest, r.hi - r.lo);
+          }
+        twice = longest <= 6;
+      }
+      if (cudaError_t e = twice            ? pick(integral_constant<int, TWICE>{})
+                          : blocks <= sms ? pick(integral_constant<int, ONE_TILE>{})
+                                          : pick(integral_constant<int, TAKE_OVER>{}))
         return e;
+    }
+    if (f.parts > 1) {
+      ProfScope ps("attn_delta", st, (double)a.T * a.H);
+      const int64_t n = a.T * a.H, grid = (n + 255) / 256;
+      if (grid > INT32_MAX) return cudaErrorInvalidValue;
+      if (cudaError_t e = launch_early(k_attn_delta, dim3((unsigned)grid), 256, 0, st, f.sums, f.parts, n, a.delta)) return e;
+    }
+    if (!twice) {
+      ProfScope ps("attn_dq_again", st);
+      const int64_t grid = std::min<int64_t>(blocks, sm_count());
+      if (cudaError_t e = a.D <= 64 ? go(k_attn_dq<1, AGAIN>, b1, grid, f, st, true) : go(k_attn_dq<2, AGAIN>, b2, grid, f, st, true)) return e;
     }
     if (cudaError_t e = sum(a.T * a.H * a.D, a.dq, nullptr)) return e;
   }

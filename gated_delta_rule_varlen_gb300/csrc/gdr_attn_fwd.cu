@@ -629,7 +629,7 @@ AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
   auto floats = [](int parts, double n) { return parts > 1 ? (size_t)parts * (size_t)n * sizeof(float) : 0; };
   const size_t rows = (size_t)a.T * a.H;
   p.fwd_bytes = floats(p.fwd, (double)rows * (a.D + 1));
-  p.bwd_bytes = std::max(floats(p.dq, (double)rows * a.D), floats(p.dkv, 2.0 * a.TK * a.HK * a.D));
+  p.bwd_bytes = std::max(floats(p.dq, (double)rows * (a.D + 4)), floats(p.dkv, 2.0 * a.TK * a.HK * a.D));
   return p;
 }
 

@@ -105,6 +105,35 @@ struct WorkQueue {
       item = (int)__shfl_sync(0xffffffffu, next, 0);
     }
   }
+  // The same of those of every gridDim-th item that are to be done: of the first n as known[] has
+  // it, of the others as pick(work) answers.
+  template <typename F, typename P>
+  __device__ __forceinline__ void run_those(volatile int* abort, int items, F make, const uint8_t* known, int n, P pick) {
+    const int lane = threadIdx.x & 31;
+    ByClock limit;
+    int k = 0;
+    for (int64_t i = 0;; ++i) {
+      const int64_t item = blockIdx.x + i * gridDim.x;
+      const bool have = item < items;
+      Work w;
+      if (have) {
+        if (i < n && !known[i]) continue;
+        w = make((int)item);
+        if (i >= n && !pick(w)) continue;
+      }
+      const int e = k & 1;
+      if (k >= 1 && !warp_wait_within(limit, abort, Phase{&wanted, (uint32_t)e ^ 1})) return;
+      if (k >= 2 && !warp_wait(&empty[e], ((k >> 1) - 1) & 1, abort)) return;
+      if (lane == 0) {
+        if (have) work[e] = w;
+        more[e] = have;
+      }
+      warp_arrive(&full[e]);
+      if (!have) return;
+      limit.ns = kWaitNs * (1 + (uint64_t)w.steps());
+      ++k;
+    }
+  }
   // A taking warp's next item, its k-th; false: there is none.  The warp that loads asks for
   // it, when all loads of the last one are on their way: a block that asked sooner would hold
   // items that others have nothing to do for.

@@ -263,7 +263,7 @@ gdr_status gdr_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
  * operators around the recurrence: sconv_fwd, sconv_bwd, sconv_wgrad,
  * sconv_step, ssm_gates, ssm_sum, ssm_merge, ssm_walk, ssm_seq, ssm_step, kda_step,
  * gdn_step, norm_fwd, norm_bwd, norm_wgrad, lnorm_fwd, lnorm_bwd, lnorm_wgrad,
- * rope, attn_fwd, attn_join, attn_dq, attn_dkv, attn_sum, attn_rows, attn_dq_rows, attn_dkv_rows. */
+ * rope, attn_fwd, attn_join, attn_dq, attn_delta, attn_dq_again, attn_dkv, attn_sum, attn_rows, attn_dq_rows, attn_dkv_rows. */
 int gdr_profile_enable(int on);
 gdr_status gdr_profile_report(char* buf, size_t buf_bytes);
 
@@ -519,7 +519,7 @@ gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const v
  * 2 i + 1).  inverse: t = -position freqs[pair], the gradient of the forward.
  * freqs [R / 2] FP32, radians a token; positions int32 or (positions64) int64
  * [T], any sign, or null: counted from the document's start by cu_seqlens
- * [N + 1].  At any position up to 2^31 the angle modulo a turn is exact to 2^-32
+ * [N + 1].  At any position up to 2^31 the angle modulo a turn is exact to 2^-31
  * turns for frequencies up to 256, to 2^-40 of the frequency beyond; a frequency that is
  * not finite turns its pair to NaN.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
  * elements apart, a head's elements dense.  An output may be its input (the same
@@ -564,7 +564,10 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
  * are formed again.  Writes dq [T][H][D], dk, dv [TK][HK][D] BF16, dense, dk and dv
  * summed in FP32 over the query heads of a key head; none of them is an input.
  * Deterministic.  On the tensor cores dS is rounded to BF16 as the probabilities
- * are. */
+ * are (2^-8 of each term at most); sum_j p_ij dout_i . v_j, which dS takes off, is exact to
+ * FP32 for dk and dv, and leaves dq off by up to 2^-8 beside its own terms'
+ * roundings, however peaked the probabilities (the more of them are, the longer dq takes, up to
+ * twice as long: it is formed again). */
 gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16* k, int64_t ks0, int64_t ks1,
                     const gdr_bf16* v, int64_t vs0, int64_t vs1, const gdr_bf16* out, const float* lse,
                     const gdr_bf16* dout, int64_t ds0, int64_t ds1, const int32_t* cu_seqlens,

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import layer_ref as ref
 from test_ops_layer_gpu import BF16, F32, full, gdr, gen, heads, pack, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +93,92 @@ def test_angles_of_fast_frequencies(gdr, f, turns):
         fraction = (p * num * digits // den) % 2 ** 200 / 2 ** 200
         off = 2 * np.pi * (turns + 2.0 ** -25) + 2 * 2.0 ** -24
         assert abs(row[0] - np.cos(2 * np.pi * fraction)) <= off and abs(row[1] - np.sin(2 * np.pi * fraction)) <= off, (f, p)
+
+
+def gradients(q, k, v, dout, lq, lk, scale, causal, window):
+    """FP64 gradients from the formulas, and for every row of each the size of its terms (the root of the
+    sum of their squares) and of what FP32's products leave of it where dP - delta cancels."""
+    G, a, b = q.shape[1] // k.shape[1], 0, 0
+    grads, sizes, floors = ([torch.zeros_like(t) for t in (q, k, v)], [torch.zeros(t.shape[:2], dtype=t.dtype, device=t.device) for t in (q, k, v)],
+                            [torch.zeros(t.shape[:2], dtype=t.dtype, device=t.device) for t in (q, k, v)])
+    for n, m in zip(lq, lk):
+        for h in range(q.shape[1]):
+            Q, K, V, dO = q[a:a + n, h], k[b:b + m, h // G], v[b:b + m, h // G], dout[a:a + n, h]
+            s = scale * Q @ K.T
+            if causal:
+                gap = torch.arange(n, device=q.device)[:, None] + (m - n) - torch.arange(m, device=q.device)
+                s = s.masked_fill((gap < 0) | (gap >= window) if window else gap < 0, -float("inf"))
+            p = torch.where((s == -float("inf")).all(-1, keepdim=True), 0.0, torch.softmax(s, -1)) if m else s
+            dp = dO @ V.T
+            ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+            # dP and delta are off by 2^-20 of |dout| |v| at most: sums of up to 128 products in FP32
+            off = p * (dO.norm(dim=-1)[:, None] * V.norm(dim=-1).max() * 2.0 ** -20) if m else p
+            squares = lambda x, y: x.square() @ y.square().sum(-1)  # noqa: E731
+            for i, (rows, hh, g, size, floor) in enumerate((
+                    (slice(a, a + n), h, scale * ds @ K, scale ** 2 * squares(ds, K), scale ** 2 * squares(off, K)),
+                    (slice(b, b + m), h // G, scale * ds.T @ Q, scale ** 2 * squares(ds.T, Q), scale ** 2 * squares(off.T, Q)),
+                    (slice(b, b + m), h // G, p.T @ dO, squares(p.T, dO), 0 * squares(p.T, dO)))):
+                grads[i][rows, hh] += g
+                sizes[i][rows, hh] += size
+                floors[i][rows, hh] += floor
+        a, b = a + n, b + m
+    return grads, [t.sqrt() for t in sizes], [t.sqrt() for t in floors]
+
+
+PEAKED = [
+    # in parts; taken over; few keys a block, gone through twice; keys of one tile; heads side by side; one query a warp
+    ([2000], None, 2, 1, 128, True, 0), ([300] * 40, None, 4, 4, 64, True, 0), ([700, 20, 1, 129], None, 4, 2, 128, True, 200),
+    ([257, 300], None, 4, 4, 128, False, 0), ([100, 128, 7, 2, 1], None, 2, 2, 128, True, 0), ([1] * 3, [5000, 3, 129], 8, 2, 64, True, 0),
+    ([3] * 60, [300 + 7 * i for i in range(60)], 4, 2, 80, True, 0), ([300, 157, 1, 300], None, 4, 4, 64, True, 0),
+    ([900], None, 1, 1, 128, False, 0), ([640, 129], None, 8, 8, 128, True, 0), ([400, 140], None, 2, 1, 33, True, 0),
+]
+
+
+@pytest.mark.parametrize("sharp", [1, 4, 8, 32])
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", PEAKED)
+def test_gradients_of_peaked_probabilities(gdr, lq, lk, H, HK, D, causal, window, sharp):
+    # scores `sharp` times those of unit inputs: where one key has nearly all, dP - delta is a small
+    # difference.  Every row of a gradient by itself: BF16 leaves each term of it within 2^-8 (P, dS) and
+    # the row within 2^-8 (its rounding), and what delta may be off by leaves dq within 2^-8: 3 2^-8 of the terms'
+    # size together at worst, if all errors lay one way.  Probabilities and dS below the smallest normal
+    # number, 2^-126, are zero: 2^-126 of |dP| |q| scale < 2^12 in each of at most 2^13 terms, below 2^-100
+    g, keys = gen(sum(lq) + sharp), lk or lq
+    T, TK = sum(lq), sum(keys)
+    q, k, v = heads(g, T, H, HK, D, "dense", TK)
+    dout = randn(g, T, H, D, dtype=BF16)
+    (cu, cuh), (cuk, cukh) = pack(lq), pack(keys) if lk else (None, None)
+    args = dict(causal=causal, window=window, cu_keys=cuk, cu_keys_host=cukh, scale=sharp * D ** -0.5)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, **args)
+    got = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, **args)
+    want, sizes, floors = gradients(q.double(), k.double(), v.double(), dout.double(), lq, keys, float(np.float32(sharp * D ** -0.5)), causal, window)
+    for name, r, size, floor in zip(("dq", "dk", "dv"), want, sizes, floors):
+        t = got[name].double()
+        assert torch.isfinite(t).all(), name
+        off = (t - r).norm(dim=-1)
+        # of the whole: what layer_ref.py derives for independent roundings
+        assert off.norm() <= ref.TOL_GRAD * r.norm() + floor.norm(), f"{name}: {float(off.norm() / r.norm()):.3e}"
+        floor = floor + 2.0 ** -100
+        worst = (off - floor - 3 * 2 ** -8 * size).argmax()
+        assert (off <= 3 * 2 ** -8 * size + floor).all(), (name, int(worst), float(off.flatten()[worst]), float(size.flatten()[worst]), float(floor.flatten()[worst]))
+    again = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, **args)
+    for name in got:
+        assert torch.equal(got[name], again[name]), name
+
+
+def test_gradients_of_many_tiles_formed_again(gdr):
+    # 320000 tiles, every one of peaked scores; the last tokens by themselves, which see 128 keys
+    g, T, H, D, window, last = gen(17), 640000, 64, 8, 128, 300
+    q, k, v = heads(g, T, H, 1, D, "dense", T)
+    dout = randn(g, T, H, D, dtype=BF16)
+    cu, cuh = pack([T])
+    scale = 24 * D ** -0.5
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, scale=scale, window=window)
+    dq = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, scale=scale, window=window)["dq"]
+    gdr.gdr_check_device()
+    for end in (T, T // 2, window + last):
+        a, b = end - last, end - last - window
+        want, sizes, floors = gradients(*(t[s:end].double() for t, s in ((q, a), (k, b), (v, b), (dout, a))), [last], [last + window],
+                                        float(np.float32(scale)), True, window)
+        off = (dq[a:end].double() - want[0]).norm(dim=-1)
+        assert off.norm() <= ref.TOL_GRAD * want[0].norm() + floors[0].norm(), end
+        assert (off <= 3 * 2 ** -8 * sizes[0] + floors[0] + 2.0 ** -100).all(), end
