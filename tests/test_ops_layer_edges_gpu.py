@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import layer_ref as ref
-from test_ops_layer_gpu import BF16, F32, full, gdr, gen, heads, pack, randn  # noqa: F401
+from test_ops_layer_gpu import ATTN, BF16, F32, MANY, full, gdr, gen, heads, pack, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +182,45 @@ def test_gradients_of_many_tiles_formed_again(gdr):
         off = (dq[a:end].double() - want[0]).norm(dim=-1)
         assert off.norm() <= ref.TOL_GRAD * want[0].norm() + floors[0].norm(), end
         assert (off <= 3 * 2 ** -8 * sizes[0] + floors[0] + 2.0 ** -100).all(), end
+
+
+def rows_of_gradients(gdr, lq, lk, H, HK, D, causal, window, layout="dense", scale=None):
+    """Every row of dq, dk and dv by itself against FP64, within BF16's roundings of its own terms."""
+    g, keys = gen(sum(lq) + 7 * D), lk or lq
+    T, TK = sum(lq), sum(keys)
+    q, k, v = heads(g, T, H, HK, D, layout, TK)
+    dout = randn(g, T, H, D, dtype=BF16)
+    (cu, cuh), (cuk, cukh) = pack(lq), pack(lk) if lk else (None, None)
+    args = dict(causal=causal, window=window, cu_keys=cuk, cu_keys_host=cukh)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, **args)
+    got = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, **args)
+    want, sizes, floors = gradients(q.double(), k.double(), v.double(), dout.double(), lq, keys, float(np.float32(D ** -0.5)), causal, window)
+    for name, r, size, floor in zip(("dq", "dk", "dv"), want, sizes, floors):
+        off = (got[name].double() - r).norm(dim=-1)
+        assert (off <= 3 * 2 ** -8 * size + floor + 2.0 ** -100).all(), (name, float((off - floor - 3 * 2 ** -8 * size).max()))
+        # and each document's: what layer_ref.py derives for independent roundings of the terms
+        for a, b in zip(*((cuh, cuh[1:]) if name == "dq" else (cukh or cuh, (cukh or cuh)[1:]))):
+            assert off[a:b].norm() <= ref.TOL_GRAD * size[a:b].norm() + floor[a:b].norm(), (name, a, b)
+
+
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window,layout", ATTN)
+def test_every_row_of_the_gradients(gdr, lq, lk, H, HK, D, causal, window, layout):
+    rows_of_gradients(gdr, lq, lk, H, HK, D, causal, window, layout)
+
+
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", MANY)
+def test_every_row_of_the_gradients_of_many_and_of_long_documents(gdr, lq, lk, H, HK, D, causal, window):
+    rows_of_gradients(gdr, lq, lk, H, HK, D, causal, window)
+
+
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", [
+    ([700, 129], None, 4, 2, 192, True, 0), ([513], None, 2, 1, 256, True, 100), ([300], [900], 2, 2, 256, True, 0),
+    ([1, 3], [1500, 260], 4, 1, 136, True, 0), ([400], None, 3, 3, 250, False, 0)])
+def test_wide_heads_of_longer_documents(gdr, lq, lk, H, HK, D, causal, window):
+    g, keys = gen(D), lk or lq
+    q, k, v = heads(g, sum(lq), H, HK, D, "dense", sum(keys))
+    (cu, cuh), (cuk, cukh) = pack(lq), pack(lk) if lk else (None, None)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, causal=causal, window=window, cu_keys=cuk, cu_keys_host=cukh)
+    ro, rl = ref.attention(q.double(), k.double(), v.double(), lq, keys, D ** -0.5, causal, window)
+    assert (out.double() - ro).norm() <= ref.TOL_OUT * ro.norm() and (lse.double() - rl).norm() <= ref.TOL_LSE * rl.norm()
+    rows_of_gradients(gdr, lq, lk, H, HK, D, causal, window)
