@@ -575,8 +575,11 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, const int32_t*
 // several, and the join's traffic.  Measured in 1 / 2 / 3 / 4 / 8 parts, the join's time
 // included: one token of 65536 keys, 8 key heads 520 / 272 / 190 / 146 / 88 us, 16 parts 73; a
 // prompt of 24576 tokens of one head 319 / 180 / 137 / 156 / 181; dK and dV of 4096 tokens, 16
-// heads over 4 key heads 178 / 109 / 129 / 132 / 179.  Only up to four blocks an SM are
-// looked at: more of them are even enough.
+// heads over 4 key heads 178 / 109 / 129 / 132 / 179; 80 to 160 single tokens of 8 key heads, one of 65536 keys,
+// the others of 1000, 528 / 272.  The number is one for the call: cutting the short documents as well costs
+// their blocks' starts, which of 256 such tokens is as much as it gains (537 us in one part).  Packs of more
+// than 1024 tiles of rows are not looked at, for the host's time (up to there 20 us).  152 SMs: the
+// sizes of workspaces are the same without a GPU.
 AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
   AttnPlan p{0, 1, 1, 1, 0, 0};
   int most = 0;
@@ -589,8 +592,8 @@ AttnPlan attn_plan(const AttnArgs& a, const int32_t* cu, const int32_t* cuk) {
   auto parts = [&](const int32_t* lens, int per, int64_t heads, double row_bytes, auto tiles) {
     int64_t blocks = 0;
     for (int i = 0; i < a.N; ++i) blocks += (lens[i + 1] - lens[i] + per - 1) / per;
+    if (blocks == 0 || blocks > 1024) return 1;
     blocks *= heads;
-    if (blocks == 0 || blocks > 4 * 152) return 1;
     int64_t total = 0, longest = 0;
     for (int i = 0; i < a.N; ++i)
       for (int at = 0; at < lens[i + 1] - lens[i]; at += per) {

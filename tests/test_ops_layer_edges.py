@@ -28,3 +28,16 @@ def test_workspace_sizes_of_other_documents(gdr):
     for cu, keys in (([0, 5, 11], [0, 11]), ([0, 11], [0, 5, 11]), ([0, 11], [[0, 11]]), ([], None)):
         with pytest.raises(ValueError, match="cu_"):
             gdr.attn_workspace_bytes(11, 11, 2, 2, 64, cu, keys)
+
+
+def test_one_long_document_among_many_short_ones_is_cut(gdr):
+    # 80 single tokens of 8 key heads are 640 blocks, of which those of one sequence of 65536 keys are
+    # as long as 60 of the others: the plan goes by the longest block against an even share, not by
+    # the number of blocks
+    keys = [0, 65536]
+    for _ in range(79):
+        keys.append(keys[-1] + 1000)
+    fwd, _ = gdr.attn_workspace_bytes(80, keys[-1], 32, 8, 128, list(range(81)), keys)
+    assert fwd >= 2 * 80 * 32 * 129 * 4
+    even = [1000 * i for i in range(81)]
+    assert gdr.attn_workspace_bytes(80, 80000, 32, 8, 128, list(range(81)), even)[0] == 0
