@@ -237,7 +237,7 @@ gdr_status lnorm_fwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x
   gdr_status rc = lnorm_args(a, dtype, wdtype, R0, R1, D, x, xs0, xs1, residual, rs0, rs1, res_scale, weight, bias, eps);
   if (rc != GDR_OK) return rc;
   if (R0 == 0) return GDR_OK;
-  if (!y) return GDR_INVALID_ARG;
+  if (!y || y == h) return GDR_INVALID_ARG;
   if ((rc = check_device()) != GDR_OK) return rc;
   a.h = h;
   a.y = y;
@@ -258,6 +258,7 @@ gdr_status lnorm_bwd(int dtype, int64_t R0, int32_t R1, int32_t D, const void* x
       lnorm_args(a, dtype, wdtype, R0, R1, D, x, xs0, xs1, residual, rs0, rs1, res_scale, weight, nullptr, eps);
   if (rc != GDR_OK) return rc;
   if ((R0 > 0 && !dy) || (dresidual && !residual)) return GDR_INVALID_ARG;
+  if (R0 > 0 && dx && dx == dresidual && res_scale != 1.f) return GDR_INVALID_ARG;
   if (!scratch || ((uintptr_t)scratch & 255) != 0) return GDR_INVALID_ARG;
   size_t need = 0;
   norm_workspace_bytes(D, &need);

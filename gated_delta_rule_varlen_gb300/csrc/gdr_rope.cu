@@ -277,6 +277,7 @@ extern "C" gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int
   if (T == 0 || HQ + HK == 0) return GDR_OK;
   if ((HQ > 0 && (!q || !q_out)) || (HK > 0 && (!k || !k_out)) || (R > 0 && !freqs)) return GDR_INVALID_ARG;
   if (R > 0 && !positions && (!cu_seqlens || N <= 0)) return GDR_INVALID_ARG;
+  if (HQ > 0 && HK > 0 && (q_out == k_out || q_out == k || k_out == q)) return GDR_INVALID_ARG;
   const gdr_status rc = check_device();
   if (rc != GDR_OK) return rc;
   RopeArgs a{};

@@ -493,8 +493,8 @@ gdr_status norm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const vo
  *     y = (h - mean h) (mean (h - mean h)^2 + eps)^(-1/2) weight + bias
  * weight, bias [D] (dtype or FP32; null: one, zero).  y is formed from the
  * unrounded h, its variance from the differences to the mean.  h (may be null)
- * and y are dense [R0][R1][D]; either may be residual or x itself (the same
- * rows). */
+ * and y are dense [R0][R1][D] and not one tensor; either may be residual or x itself
+ * (the same rows). */
 gdr_status lnorm_fwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
                      const void* residual, int64_t rs0, int64_t rs1, float res_scale, const void* weight,
                      const void* bias, gdr_dtype wdtype, float eps, void* h, void* y, cudaStream_t stream);
@@ -504,7 +504,8 @@ gdr_status lnorm_workspace_bytes(int32_t D, size_t* scratch_bytes);
 
 /* Gradients of lnorm_fwd from dy and dh (the gradient of h; null: zero).
  * Writes, each when non-null, dx, dresidual (dense rows, the activations'
- * type) and dweight, dbias [D] FP32, summed over the rows in a fixed order. */
+ * type; one tensor only where res_scale is 1 and they are the same) and dweight, dbias
+ * [D] FP32, summed over the rows in a fixed order. */
 gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const void* x, int64_t xs0, int64_t xs1,
                      const void* residual, int64_t rs0, int64_t rs1, float res_scale, const void* weight,
                      gdr_dtype wdtype, float eps, const void* dh, int64_t dhs0, int64_t dhs1, const void* dy,
@@ -522,8 +523,8 @@ gdr_status lnorm_bwd(gdr_dtype dtype, int64_t R0, int32_t R1, int32_t D, const v
  * [N + 1].  At any position up to 2^31 the angle modulo a turn is exact to 2^-31
  * turns for frequencies up to 256, to 2^-40 of the frequency beyond; a frequency that is
  * not finite turns its pair to NaN.  Each tensor's tokens and heads are *s0 and *s1 (outputs *o0, *o1)
- * elements apart, a head's elements dense.  An output may be its input (the same
- * rows).  R goes up to GDR_ROPE_MAX_R, D (HQ + HK) to 2^31 - 4097. */
+ * elements apart, a head's elements dense.  An output may be its own input (the
+ * same rows), not the other's.  R goes up to GDR_ROPE_MAX_R, D (HQ + HK) to 2^31 - 4097. */
 #define GDR_ROPE_MAX_R 8192
 gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, int32_t HQ, void* q_out, int64_t qo0,
                 int64_t qo1, const void* k, int64_t ks0, int64_t ks1, int32_t HK, void* k_out, int64_t ko0,

@@ -41,3 +41,13 @@ def test_one_long_document_among_many_short_ones_is_cut(gdr):
     assert fwd >= 2 * 80 * 32 * 129 * 4
     even = [1000 * i for i in range(81)]
     assert gdr.attn_workspace_bytes(80, 80000, 32, 8, 128, list(range(81)), even)[0] == 0
+
+
+def test_outputs_that_are_one_tensor(gdr):
+    # one would be written over the other
+    lib, bad = gdr.load(), gdr.GDR_INVALID_ARG
+    assert lib.lnorm_fwd(0, 3, 1, 64, P(), 64, 64, P(2), 64, 64, 0.5, P(3), None, 0, 1e-5, P(4), P(4), None) == bad
+    assert lib.lnorm_bwd(0, 3, 1, 64, P(), 64, 64, P(2), 64, 64, 0.5, P(3), 0, 1e-5, None, 0, 0, P(4), 64, 64, P(5), P(5), None, None, P(6), 1 << 30, None) == bad
+    for q, qo, k, ko in ((1, 3, 2, 3), (1, 2, 2, 4), (1, 3, 2, 1), (1, 2, 2, 1)):
+        status = lib.rope_turn(0, P(q), 128, 64, 2, P(qo), 128, 64, P(k), 64, 64, 1, P(ko), 64, 64, 4, 64, 64, P(7), P(8), 0, None, 0, 0, 1.0, 0, None)
+        assert status == bad, (q, qo, k, ko)
