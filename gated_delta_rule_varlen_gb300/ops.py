@@ -305,7 +305,8 @@ def attn_fwd(q, k, v, cu_seqlens, cu_seqlens_host, scale=None, causal=True, wind
     cu_keys[n] to cu_keys[n + 1], its queries the last of them: a prompt that goes on after
     cached keys, or one token of each sequence.  causal: a query sees the keys up to its own
     place, of those the last `window` (0: all).  Returns (out bf16 [T, H, D], lse fp32 [H, T]);
-    a query that sees no key gets 0 and -inf.
+    a query that sees no key gets 0 and -inf.  A document without queries is room that nobody
+    reads: with one behind each sequence's keys a cache grows in place.
 
     D goes up to 256.  The tensor cores take D up to 128 in multiples of 8, tensors on 16-byte
     boundaries and strides in multiples of 8; others go one query a warp, some 400 times

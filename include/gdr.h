@@ -549,7 +549,9 @@ gdr_status rope_turn(gdr_dtype dtype, const void* q, int64_t qs0, int64_t qs1, i
  * times slower on a long prompt.  Scores, maxima, sums and outputs are FP32 until the
  * one rounding; the tensor cores take probabilities in BF16 (2^-8 of each term at
  * most, independently).
- * Values of a document that are not finite reach its own outputs only.
+ * Values of a document that are not finite reach its own outputs only.  A document without
+ * queries is room that nobody reads: with one behind each sequence a cache of keys
+ * grows in place, and only the bounds move.
  * scratch: attn_workspace_bytes, on a 256-byte boundary (null when 0). */
 #define GDR_ATTN_MAX_D 256
 gdr_status attn_workspace_bytes(int64_t T, int64_t TK, int32_t H, int32_t HK, int32_t D, int32_t N,

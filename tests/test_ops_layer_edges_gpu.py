@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import layer_ref as ref
-from test_ops_layer_gpu import ATTN, BF16, F32, MANY, full, gdr, gen, heads, pack, randn  # noqa: F401
+from test_ops_layer_gpu import ATTN, BF16, F32, MANY, NAN, full, gdr, gen, heads, pack, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -224,3 +224,32 @@ def test_wide_heads_of_longer_documents(gdr, lq, lk, H, HK, D, causal, window):
     ro, rl = ref.attention(q.double(), k.double(), v.double(), lq, keys, D ** -0.5, causal, window)
     assert (out.double() - ro).norm() <= ref.TOL_OUT * ro.norm() and (lse.double() - rl).norm() <= ref.TOL_LSE * rl.norm()
     rows_of_gradients(gdr, lq, lk, H, HK, D, causal, window)
+
+
+@pytest.mark.parametrize("D", [128, 33])
+def test_documents_of_no_queries_are_room_for_others(gdr, D):
+    # a cache that grows in place: between the sequences' keys lie documents without queries, which hold
+    # what nobody reads (NaN here); a token appended moves the bounds, not the keys
+    g, H, HK, room = gen(D), 4, 2, 400
+    used = [300, 1, 257, 128]
+    cache = torch.full((2, len(used), room, HK, D), NAN, dtype=BF16, device="cuda")
+    for i, n in enumerate(used):
+        cache[:, i, :n] = randn(g, 2, n, HK, D, dtype=BF16)
+    k, v = cache[0].flatten(0, 1), cache[1].flatten(0, 1)
+    q = randn(g, len(used), H, D, dtype=BF16)
+    for step in range(2):
+        cu, cuh = pack([1, 0] * len(used))
+        cuk, cukh = pack([n for u in used for n in (u, room - u)])
+        out, lse = gdr.attn_fwd(q, k, v, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+        grads = gdr.attn_bwd(q, k, v, out, lse, q, cu, cuh, cu_keys=cuk, cu_keys_host=cukh)
+        pk, pv = (torch.cat([t[i, :n] for i, n in enumerate(used)]) for t in cache)
+        ro, rl = ref.attention(q.double(), pk.double(), pv.double(), [1] * len(used), used, D ** -0.5, True, 0)
+        assert (out.double() - ro).norm() <= ref.TOL_OUT * ro.norm() and (lse.double() - rl).norm() <= ref.TOL_LSE * rl.norm()
+        assert torch.isfinite(grads["dq"].float()).all()
+        for i, n in enumerate(used):
+            for name in ("dk", "dv"):
+                rows = grads[name][i * room:(i + 1) * room]
+                assert torch.isfinite(rows.float()).all() and (rows[n:] == 0).all(), (name, i)
+        for i in range(len(used)):  # one token more each
+            cache[:, i, used[i]] = randn(g, 2, HK, D, dtype=BF16)
+            used[i] += 1
