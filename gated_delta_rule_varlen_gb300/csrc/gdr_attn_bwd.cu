@@ -16,13 +16,12 @@
 // beside dS of probabilities spread over many keys, and all of it where one key has nearly all:
 // dP - delta is small there.  What it is off by is sum dS, which comes with the tiles of dS: delta is
 // put right for dK and dV, and a tile of dQ with a row that it matters to (put_right) is formed again by
-// a second launch.  Of 8192 tokens of 16 heads of 128 the sums take 10 us of dQ, the second launch 8 where
-// there is nothing to do, 19 for the 4 tiles of 1024 that scores of unit inputs leave it, and 298 for all of
-// them (scores 4 times as large).  Where a tile of keys holds all that the queries see, delta is
+// a second launch.  Of 8192 tokens of 16 heads of 128 the sums take 15 us of dQ, the second launch 19 for
+// the few tiles that unit inputs leave it, and 298 for all of them (scores 4 times as large).  Where a tile of keys holds all that the queries see, delta is
 // sum p dP from the start: with few keys |out| is like |v|.
 //
 // Bound by the products and their operands' way from shared memory: of 8192 tokens of 16
-// heads over 4 of 128 columns dQ takes 293 us (three products, 1.4 PFLOP/s), dK and dV 354
+// heads over 4 of 128 columns dQ takes 298 us (three products, 1.4 PFLOP/s), dK and dV 354
 // (four, 1.55 PFLOP/s; cuBLAS's measured rate is 1.9).  Measured and not kept: tiles three
 // deep in dQ and two in dK and dV, so that elements and products of different tiles overlap
 // (345 and 423 us: the elements' tensor memory traffic slows the products), the products of
@@ -42,7 +41,7 @@ struct BwdArgs {
   int pack;
   int parts;    // blocks that share a tile's sums
   float* part;  // their shares: dQ [parts][T][H][D], or dK and dV [2][parts][TK][HK][D]
-  float4* sums; // of dQ's parts, [parts][H][T]: sum dS, sum P^2, sum dS^2, the delta that dS was formed with
+  float4* sums; // of dQ's parts, [parts][H][T]: sum dS, sum P^2, half of sum dS^2, the delta that dS was formed with
   int items;    // dQ's tiles
   int* err;
 };
@@ -185,12 +184,16 @@ __device__ __forceinline__ float marked(float delta, bool again) {
   return __uint_as_float((__float_as_uint(delta) & ~1u) | (again ? 1u : 0u));
 }
 __device__ __forceinline__ bool is_marked(float delta) { return (__float_as_uint(delta) & 1u) != 0; }
-// delta put right by e = sum dS, which it was off by.  A row of dQ is then off by e |sum P k|, some e |k|
-// times the root of x = sum P^2, and is some |k| times the root of sum dS^2, of which y has a fourth of the
-// terms: it is formed again where the first is more than 2^-9 of the second (2^-8 where one of the
-// fourth's terms is the row; dS' own rounding is up to 2^-8 a term).
+// delta put right by e = sum dS, which it was off by.  A row of dQ is then off by e |sum P k|: some |k| times
+// the root of x = sum P^2 where the keys point in all directions, up to |k| where they share a part (which
+// cancels in dQ, but not in this), so that an eighth of |k| is reckoned with at least.  The row is some |k|
+// times the root of sum dS^2, of which y has half of the terms.  It is formed again where the first is more
+// than 2^-9 of the second.  What stays is within 2^-9 of its terms' size, within 2^-6 where the keys are
+// nearly one, and the root of two times that where the half's terms are the row (dS' own rounding: 2^-8 of
+// each term).  Of unit inputs e is 2^-9 of the root in the mean: with a fourth of |k| reckoned with, one of 130
+// rows was formed again; with an eighth, one of 40000.
 __device__ __forceinline__ float put_right(float delta, float e, float x, float y) {
-  return marked(delta + e, fabsf(e) * sqrtf(x) > sqrtf(y) * (2.f / 512.f) || y > 1e38f);
+  return marked(delta + e, fabsf(e) * fmaxf(sqrtf(x), 0.125f) > sqrtf(2.f * y) * (1.f / 512.f) || y > 1e38f);
 }
 // What a block works on: one tile; one tile, for whose delta it goes through the keys once before;
 // its own and those that it takes over; of every gridDim-th the marked ones, formed again.
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");  // (512 x 104 + 128 x 64 = 640 x 96; with 96 the sums spill)
     // a row a thread, of S and dP a quarter's columns
     const int quarter = warp >> 2, row = tid & 127, c0 = COLS * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
         if (QUEUE) warp_arrive(&s.q_empty);
       }
       uint64_t off = 0;          // sum dS: what delta is off by
-      uint64_t pp = 0, dd = 0;   // sum P^2, sum dS^2
+      uint64_t pp = 0, dd = 0;   // sum P^2, of every other pair sum dS^2
       uint64_t pd = 0, ps = 0;   // sum P dP, sum P
 #pragma unroll 1
       for (int j = w.r.lo, left = steps(); left > 0; --left, j = j + 1 < w.r.hi ? j + 1 : w.r.lo, ++g) {
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_dq(const __grid_constant__ 
           const uint64_t ds = mul2(p[i], add2(pair_at(x + 2 * i), minus));
           if constexpr (ROUGH) {
             off = add2(off, ds);
-            if (i % 4 == 0) dd = fma2(ds, ds, dd);  // (of every fourth pair: all of them took dQ 4% longer)
+            if (i % 2 == 0) dd = fma2(ds, ds, dd);  // (of all pairs: 312 us instead of 298)
           }
           x[i] = round_pair(ds);
         }

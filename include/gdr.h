@@ -567,10 +567,11 @@ gdr_status attn_fwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16*
  * are formed again.  Writes dq [T][H][D], dk, dv [TK][HK][D] BF16, dense, dk and dv
  * summed in FP32 over the query heads of a key head; none of them is an input.
  * Deterministic.  On the tensor cores dS is rounded to BF16 as the probabilities
- * are (2^-8 of each term at most); sum_j p_ij dout_i . v_j, which dS takes off, is exact to
- * FP32 for dk and dv, and leaves dq off by up to 2^-8 beside its own terms'
- * roundings, however peaked the probabilities (the more of them are, the longer dq takes, up to
- * twice as long: it is formed again). */
+ * are (2^-8 of each term at most).  sum_j p_ij dout_i . v_j, which dS takes off, is exact to
+ * FP32 for dk and dv however peaked the probabilities are; of its rounding (that of out)
+ * a row of dq keeps 2^-8 of the size of its terms scale dS k, or 2^-5 where the keys are
+ * nearly one vector (most of the terms, which cancel).  Rows that would keep more
+ * are formed again: dq takes up to twice as long where they are many. */
 gdr_status attn_bwd(const gdr_bf16* q, int64_t qs0, int64_t qs1, const gdr_bf16* k, int64_t ks0, int64_t ks1,
                     const gdr_bf16* v, int64_t vs0, int64_t vs1, const gdr_bf16* out, const float* lse,
                     const gdr_bf16* dout, int64_t ds0, int64_t ds1, const int32_t* cu_seqlens,

@@ -253,3 +253,27 @@ def test_documents_of_no_queries_are_room_for_others(gdr, D):
         for i in range(len(used)):  # one token more each
             cache[:, i, used[i]] = randn(g, 2, HK, D, dtype=BF16)
             used[i] += 1
+
+
+@pytest.mark.parametrize("lq,lk,H,HK,D,causal,window", [
+    ([1] * 4, [1500, 4000, 22, 3223], 8, 1, 24, True, 0), ([2] * 20, [4000, 3000] * 10, 8, 2, 64, True, 0), ([900], None, 2, 2, 128, True, 0), ([300] * 30, None, 4, 2, 64, True, 0),
+    ([99, 135, 290, 106], None, 32, 4, 128, True, 300), ([500], None, 4, 4, 64, False, 0)])
+@pytest.mark.parametrize("kpart,vpart", [(16.0, 0.5), (4.0, 4.0), (16.0, 16.0), (16.0, 0.0)])
+def test_gradients_of_keys_and_values_that_share_a_part(gdr, lq, lk, H, HK, D, causal, window, kpart, vpart):
+    # all keys near one vector, all values near another: the first cancels in dq, since a row of dS sums to
+    # zero, but not in what dS is off by together; the second makes delta large beside dP - delta.  Terms' size
+    # |dS| |k| includes the shared part: P, dS and dq are rounded (3 2^-8), delta leaves 2^-5.5
+    g, keys = gen(D + int(kpart + vpart)), lk or lq
+    T, TK = sum(lq), sum(keys)
+    q, k, v = heads(g, T, H, HK, D, "dense", TK)
+    k, v = ((t.float() + part * randn(g, HK, D)).to(BF16) for t, part in ((k, kpart), (v, vpart)))
+    dout = randn(g, T, H, D, dtype=BF16)
+    (cu, cuh), (cuk, cukh) = pack(lq), pack(lk) if lk else (None, None)
+    args = dict(causal=causal, window=window, cu_keys=cuk, cu_keys_host=cukh)
+    out, lse = gdr.attn_fwd(q, k, v, cu, cuh, **args)
+    got = gdr.attn_bwd(q, k, v, out, lse, dout, cu, cuh, **args)
+    want, sizes, floors = gradients(q.double(), k.double(), v.double(), dout.double(), lq, keys, float(np.float32(D ** -0.5)), causal, window)
+    for name, r, size, floor in zip(("dq", "dk", "dv"), want, sizes, floors):
+        off = (got[name].double() - r).norm(dim=-1)
+        limit = (3 * 2 ** -8 + (2 ** -5.5 if name == "dq" else 0.0)) * size + floor + 2.0 ** -100
+        assert (off <= limit).all(), (name, float((off / limit).max()))
